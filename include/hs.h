@@ -36,7 +36,9 @@
  *   Hq / Hkv query / kv heads, g = Hq / Hkv query heads per kv head,
  *   N_b = ceil(seq_lens[b] / B) blocks of request b.
  *   k_pages, v_pages  [num_pages][B][D]   f32 | bf16 | e4m3 (one byte)
- *   k_scales,v_scales [num_pages][B][D/32] f32 (e4m3 only, else NULL)
+ *   k_scales,v_scales [num_pages][B][D/32] f32 (e4m3 with grouped scales),
+ *                     [num_pages] f32 (e4m3 with a scale per page: positive,
+ *                     finite numbers), else NULL
  *   page_table        [batch][Hkv][max_blocks] int32: physical page of block j
  *                     of (b, kvh); only entries j < N_b are read.
  *   seq_lens          [batch] int32 tokens of each request, including the
@@ -85,12 +87,17 @@ typedef enum hs_status {
 #define HS_EBIT_CAPACITY 0x2u    /* count > capacity, or > hot-buffer slots */
 #define HS_EBIT_TIMEOUT 0x4u     /* a bounded device wait expired */
 #define HS_EBIT_BLOCK_RANGE 0x8u /* selected block index outside [0, N_b) */
+#define HS_EBIT_POSITION 0x10u   /* rotation position outside [0, table_rows) */
 
 typedef enum hs_kv_dtype {
   HS_KV_F32 = 0,         /* fp32 K/V, fp32 q, fp32 summaries */
   HS_KV_BF16 = 1,        /* bf16 K/V, bf16 q, bf16 summaries */
-  HS_KV_FP8E4M3_G32 = 2  /* e4m3 K/V + one fp32 scale per 32 channels per token;
-                            bf16 q; bf16 summaries rounded outward */
+  HS_KV_FP8E4M3_G32 = 2,  /* e4m3 K/V + one fp32 scale per 32 channels per token;
+                             bf16 q; bf16 summaries rounded outward */
+  HS_KV_FP8E4M3_BLOCK = 3 /* e4m3 K/V + one fp32 scale per page (a block of
+                             tokens of one kv head): k_scales, v_scales
+                             [num_pages]; bf16 q; bf16 summaries rounded
+                             outward.  1/9 fewer bytes than G32 */
 } hs_kv_dtype;
 
 /* Attention geometry.  head_dim in {64, 128}; num_q_heads / num_kv_heads in
@@ -184,7 +191,13 @@ typedef struct hs_select_params {
  * whose chunks fall into several runs is merged in place as above.  The
  * library takes them when its cost estimate favours them over equal splits
  * per pair; HS_ATTN_RANGES takes them whenever they apply, HS_ATTN_NO_RANGES
- * never (hs_attn_geometry reports the choice). */
+ * never (hs_attn_geometry reports the choice).
+ * A cache with a scale per page (HS_KV_FP8E4M3_BLOCK) has a tensor-core kernel of
+ * its own, for every block_size: it always cuts balanced ranges, from the
+ * actual selection counts, whatever blocks_per_split and these flags say; it
+ * waits for nothing but its own copies, so wait_limit_ns does not concern it;
+ * max_ctas limits it to n SMs; without split_counters it merges in a second
+ * launch. */
 #define HS_ATTN_EARLY_SUMMARIES 1u
 #define HS_ATTN_RANGES 2u
 #define HS_ATTN_NO_RANGES 4u
@@ -210,7 +223,8 @@ typedef struct hs_attn_params {
  *   k_slot_scales,v_slot_scales device [..][B][D/32] (e4m3 only)
  *   host_k, host_v        pinned, mapped host memory [batch][Hkv][max_blocks][B][D]
  *   host_k_scales, host_v_scales  pinned host [..][B][D/32] (e4m3 only)
- * Start state: page_table, slot_owner and last_used all -1. */
+ * Start state: page_table, slot_owner and last_used all -1.
+ * Not for HS_KV_FP8E4M3_BLOCK: the swap-in calls answer HS_ERR_UNSUPPORTED. */
 typedef struct hs_hot_buffer {
   int32_t* page_table;
   int32_t* slot_owner;
@@ -257,7 +271,8 @@ HS_API int32_t hs_attn_geometry(const hs_attn_shape* shape, int32_t batch, int32
 /* Per-block key summaries, [KVS] §5 Quest: for every request b, kv head kvh and
  * block j with first_block <= j < N_b, smin/smax[b][kvh][j][d] = min/max over
  * the block's valid tokens t in [jB, min((j+1)B, L_b)) of K[t][d].  e4m3 K is
- * dequantised (code * scale in fp32) first and the results rounded outward to
+ * dequantised (code * scale in fp32; with a scale per page the min and max are
+ * taken over the codes and then scaled, which is the same) first and the results rounded outward to
  * bf16 (min toward -inf, max toward +inf).  Other entries are not written.
  * Reading a page id outside [0, num_pages) sets HS_EBIT_PAGE_RANGE and skips
  * that block. */
@@ -275,14 +290,76 @@ HS_API hs_status hs_build_block_summaries(const hs_attn_shape* shape, const hs_p
  * current.  The caller updates seq_lens (to include the new token) and
  * page_table (a page for a new block) before the call.
  *   new_k, new_v  [batch][Hkv][D]  f32 for f32 K/V, bf16 otherwise; an e4m3
- *                 cache stores them quantised as hs_quantize_e4m3_g32 does
- *                 (codes into k_pages/v_pages, scales into k_scales/v_scales).
+ *                 cache with grouped scales stores them quantised as
+ *                 hs_quantize_e4m3_g32 does (codes into k_pages/v_pages, scales
+ *                 into k_scales/v_scales), one with a scale per page as
+ *                 hs_append_tokens does.
  *   The call WRITES through kv->k_pages, v_pages, k_scales and v_scales: they
  *   must point to writable device memory.
  * A block index >= max_blocks sets HS_EBIT_BLOCK_RANGE, a page id outside
  * [0, num_pages) sets HS_EBIT_PAGE_RANGE; that stream is left unchanged. */
 HS_API hs_status hs_append_token(const hs_attn_shape* shape, const hs_paged_kv* kv, const void* new_k,
                                  const void* new_v, void* smin, void* smax, hs_stream_t stream);
+
+/* What hs_append_tokens is told besides the rows.
+ *   new_offsets  nullable device [batch + 1] int32, ascending: rows
+ *                new_offsets[b] .. new_offsets[b+1] - 1 are request b's new
+ *                tokens, in order (none when the two are equal).  NULL: one
+ *                new token per request, row b is request b's (rows = batch).
+ *   positions    nullable device [rows] int32: the position whose angles turn a
+ *                row; NULL: its position in the cache.
+ *   cos_sin      device [table_rows][rotary_dim] f32, 16-byte aligned: for each
+ *                position the rotary_dim/2 cosines of the pairs' angles, then
+ *                their sines.  May be NULL when rotary_dim is 0.
+ *   rotary_dim   channels of each head that are rotated, from channel 0 on: a
+ *                multiple of 16 up to head_dim; 0 = no rotation.
+ *   interleaved  0: pair i is (i, i + rotary_dim/2); else (2i, 2i + 1). */
+typedef struct hs_append_params {
+  const int32_t* new_offsets;
+  const int32_t* positions;
+  const float* cos_sin;
+  int32_t table_rows;
+  int32_t rotary_dim;
+  int32_t interleaved;
+} hs_append_params;
+
+/* Append of any number of new tokens per request, rotated by position on the
+ * way: request b's n_b rows take the cache positions seq_lens[b] - n_b ..
+ * seq_lens[b] - 1 (the caller has advanced seq_lens and given new blocks their
+ * pages).  For every new row and head, with (a, b) a pair of channels and t its
+ * angle at the row's position, a' = a cos t - b sin t, b' = b cos t + a sin t in
+ * fp32: for K before it is stored, for Q into q_out; V is stored as it is.
+ * Stored as the cache holds it: f32; bf16, rounded once; e4m3 with grouped
+ * scales as hs_quantize_e4m3_g32 does; e4m3 with a scale per page (below).  The
+ * summaries of the touched blocks ([KVS] §5) are widened to the new tokens
+ * (started afresh where the block's row 0 is new), so that they equal what
+ * hs_build_block_summaries computes, as with hs_append_token.
+ * Scale of a page: the smallest power of two s >= 2^-117 such that the page's
+ * finite new values are within 448 s.  A page whose earlier rows stay keeps its
+ * scale when that is at least s; else it takes s, the codes of the earlier rows
+ * are multiplied by old/new (exact but for values under the smallest e4m3
+ * step, when the old scale is a power of two) and its summary is taken anew.
+ * Values are stored nearest-even; infinities as +-448 s, NaN as the NaN code.
+ *   q, q_out     [rows][Hq][D], rows q_stride, q_out_stride elements apart; both
+ *                NULL: no Q.  q_out may be q itself (same stride), else they do
+ *                not overlap.
+ *   k, v         [rows][Hkv][D], rows k_stride, v_stride elements apart (views
+ *                of a fused projection will do).
+ *                All in the source precision (bf16, or f32 for an f32 cache),
+ *                16-byte aligned, strides a multiple of 16 bytes.
+ *   rows         rows of q, k and v.  Rows at and past new_offsets[batch] (a
+ *                padded batch) are neither read nor written.
+ *   smin, smax   the summaries, or both NULL.
+ * A request with more new rows than tokens, or offsets that do not ascend within
+ * [0, rows], set HS_EBIT_BLOCK_RANGE and leave the request's cache as it was; so
+ * does a block index >= max_blocks, for that block.  A page id outside [0,
+ * num_pages) sets HS_EBIT_PAGE_RANGE and skips the block; a position outside
+ * [0, table_rows) sets HS_EBIT_POSITION and leaves the row's K and Q unwritten.
+ * Two requests must not share a page that the call writes to. */
+HS_API hs_status hs_append_tokens(const hs_attn_shape* shape, const hs_paged_kv* kv, const hs_append_params* params,
+                                  int64_t rows, const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                                  const void* k, int64_t k_stride, const void* v, int64_t v_stride, void* smin,
+                                  void* smax, hs_stream_t stream);
 
 /* Bytes of workspace hs_score_select_topk needs when scores_opt is NULL: one
  * fp32 score per block, [batch][Hkv][max_blocks].  0 on invalid input. */
@@ -520,7 +597,7 @@ HS_API hs_status hs_sparse_paged_decode_attn_noalloc(const hs_attn_shape* shape,
 
 /* Synchronises `stream`, then reads and clears the current device's error
  * word.  Returns HS_OK when no bit was set, else, in this order of priority:
- * HS_ERR_OUT_OF_RANGE (PAGE_RANGE or BLOCK_RANGE), HS_ERR_CAPACITY,
+ * HS_ERR_OUT_OF_RANGE (PAGE_RANGE, BLOCK_RANGE or POSITION), HS_ERR_CAPACITY,
  * HS_ERR_TIMEOUT.  bits_opt (nullable) receives the raw bits.  A failed
  * synchronisation (an earlier kernel fault) returns HS_ERR_CUDA. */
 HS_API hs_status hs_get_device_error(hs_stream_t stream, uint32_t* bits_opt);

@@ -52,7 +52,7 @@ hs_status check_shape(const hs_attn_shape* s) {
   if (g != 1 && g != 2 && g != 4 && g != 8 && g != 16) return HS_ERR_UNSUPPORTED;
   if (s->head_dim != 64 && s->head_dim != 128) return HS_ERR_UNSUPPORTED;
   if (s->block_size < 1 || s->block_size > 256) return HS_ERR_UNSUPPORTED;
-  if (s->kv_dtype < HS_KV_F32 || s->kv_dtype > HS_KV_FP8E4M3_G32) return HS_ERR_INVALID_ARG;
+  if (s->kv_dtype < HS_KV_F32 || s->kv_dtype > HS_KV_FP8E4M3_BLOCK) return HS_ERR_INVALID_ARG;
   return HS_OK;
 }
 
@@ -61,7 +61,8 @@ int elem_bytes(int kv_dtype) { return kv_dtype == HS_KV_F32 ? 4 : (kv_dtype == H
 hs_status check_kv(const hs_attn_shape* s, const hs_paged_kv* kv, bool need_v) {
   if (!kv || !kv->k_pages || !kv->page_table || !kv->seq_lens) return HS_ERR_INVALID_ARG;
   if (need_v && !kv->v_pages) return HS_ERR_INVALID_ARG;
-  if (s->kv_dtype == HS_KV_FP8E4M3_G32 && (!kv->k_scales || (need_v && !kv->v_scales)))
+  if (s->kv_dtype >= HS_KV_FP8E4M3_G32 &&
+      (!kv->k_scales || !aligned(kv->k_scales, 4) || (need_v && (!kv->v_scales || !aligned(kv->v_scales, 4)))))
     return HS_ERR_INVALID_ARG;
   if (kv->batch < 0 || kv->max_blocks < 1 || kv->num_pages < 0 || kv->num_pages > INT32_MAX)
     return HS_ERR_INVALID_ARG;
@@ -168,6 +169,13 @@ size_t workspace_for(const hs_attn_shape* s, int batch, int splits) {
   return (bytes + 255) & ~static_cast<size_t>(255);
 }
 
+// The same for the kernel of block-scaled e4m3, which cuts ranges from the
+// actual counts: two partial results per CTA.
+size_t block_workspace(const hs_attn_shape* s, int sms) {
+  const size_t bytes = block_attn_workspace(block_attn_ctas(sms), s->num_q_heads / s->num_kv_heads, s->head_dim);
+  return (bytes + 255) & ~static_cast<size_t>(255);
+}
+
 // Partial workspace an attention call may need: the larger of the uniform
 // splits and the tensor-core kernels' geometry (which kernel runs depends on
 // the pointers given at call time).
@@ -177,7 +185,8 @@ size_t attn_workspace_need(const hs_attn_shape* s, int batch, int capacity, cons
   const size_t uniform = workspace_for(s, batch, splits);
   AttnArgs t;
   split_geometry(s, batch, capacity, p, ctas, &bps, &splits, &t);
-  const size_t tc = workspace_for(s, batch, splits);
+  size_t tc = workspace_for(s, batch, splits);
+  if (s->kv_dtype == HS_KV_FP8E4M3_BLOCK) tc = block_workspace(s, ctas);
   return uniform > tc ? uniform : tc;
 }
 
@@ -265,6 +274,8 @@ hs_status prepare_attn(const hs_attn_shape* shape, const hs_paged_kv* kv, const 
   const int ctas = attn_ctas(d.sms, params);
   if (params->algo == 1) {
     *use_tc = false;
+  } else if (shape->kv_dtype == HS_KV_FP8E4M3_BLOCK) {
+    *use_tc = true;
   } else if (params->algo == 2) {
     if (!attn_tc_supported(v)) return HS_ERR_UNSUPPORTED;
     *use_tc = true;
@@ -272,8 +283,10 @@ hs_status prepare_attn(const hs_attn_shape* shape, const hs_paged_kv* kv, const 
     *use_tc = attn_tc_supported(v);
   }
   AttnArgs& a = *out_args;
+  const bool ranges = *use_tc && shape->kv_dtype == HS_KV_FP8E4M3_BLOCK;
+  if (ranges && static_cast<int64_t>(kv->batch) * shape->num_kv_heads > INT32_MAX) return HS_ERR_UNSUPPORTED;
   split_geometry(shape, kv->batch, capacity, params, ctas, &a.blocks_per_split, &a.splits, *use_tc ? &a : nullptr);
-  const size_t need = workspace_for(shape, kv->batch, a.splits);
+  const size_t need = ranges ? block_workspace(shape, ctas) : workspace_for(shape, kv->batch, a.splits);
   if (need > 0 && (!workspace || ws_bytes < need || !aligned(workspace, 16))) return HS_ERR_WORKSPACE;
   a.sms = ctas;
   if (params->split_counters && !aligned(params->split_counters, 4)) return HS_ERR_INVALID_ARG;
@@ -289,8 +302,19 @@ hs_status prepare_attn(const hs_attn_shape* shape, const hs_paged_kv* kv, const 
   a.out = out;
   a.lse = lse_opt;
   a.ws_o = static_cast<float*>(workspace);
-  a.ws_lse = a.ws_o + static_cast<size_t>(kv->batch) * shape->num_q_heads * a.splits * shape->head_dim;
+  a.ws_lse = a.ws_o + (ranges ? static_cast<size_t>(block_attn_ctas(ctas)) * 2 * v.group
+                              : static_cast<size_t>(kv->batch) * shape->num_q_heads * a.splits) *
+                          shape->head_dim;
   return HS_OK;
+}
+
+// The attention's launches, the merge of its splits among them.
+hs_status run_attn(const KvView& v, AttnArgs& a, bool use_tc, unsigned* err, cudaStream_t s) {
+  if (use_tc && v.kv_dtype == HS_KV_FP8E4M3_BLOCK) return from_cuda(launch_block_attn(v, a, err, s));
+  const cudaError_t e = use_tc ? launch_attn_tc(v, a, err, s) : launch_attn_simt(v, a, err, s);
+  if (e != cudaSuccess) return HS_ERR_CUDA;
+  if (a.merged) return HS_OK;
+  return from_cuda(launch_merge(v, a, s));
 }
 
 }  // namespace
@@ -370,6 +394,53 @@ hs_status hs_append_token(const hs_attn_shape* shape, const hs_paged_kv* kv, con
   return from_cuda(launch_append(v, new_k, new_v, smin, smax, d.err, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+hs_status hs_append_tokens(const hs_attn_shape* shape, const hs_paged_kv* kv, const hs_append_params* params,
+                           int64_t rows, const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                           const void* k, int64_t k_stride, const void* v, int64_t v_stride, void* smin, void* smax,
+                           hs_stream_t stream) {
+  hs_status st = check_shape(shape);
+  if (st != HS_OK) return st;
+  if ((st = check_kv(shape, kv, true)) != HS_OK) return st;
+  if (!params || rows < 0 || rows > INT32_MAX || !k || !v || !q != !q_out || !smin != !smax) return HS_ERR_INVALID_ARG;
+  if (!params->new_offsets && rows != kv->batch) return HS_ERR_INVALID_ARG;
+  const int D = shape->head_dim, lane16 = shape->kv_dtype == HS_KV_F32 ? 4 : 8;  // values in 16 bytes
+  const auto rows_ok = [&](const void* p, int64_t stride, int heads) {
+    return aligned(p, 16) && stride % lane16 == 0 && stride >= static_cast<int64_t>(heads) * D;
+  };
+  if (!rows_ok(k, k_stride, shape->num_kv_heads) || !rows_ok(v, v_stride, shape->num_kv_heads)) return HS_ERR_INVALID_ARG;
+  if (q && (!rows_ok(q, q_stride, shape->num_q_heads) || !rows_ok(q_out, q_out_stride, shape->num_q_heads)))
+    return HS_ERR_INVALID_ARG;
+  if (q && q == q_out && q_stride != q_out_stride) return HS_ERR_INVALID_ARG;
+  if (!aligned(smin, 16) || !aligned(smax, 16) || !aligned(params->new_offsets, 4) || !aligned(params->positions, 4))
+    return HS_ERR_INVALID_ARG;
+  if (params->rotary_dim < 0 || params->rotary_dim > D || params->table_rows < 0) return HS_ERR_INVALID_ARG;
+  if (params->rotary_dim % 16 != 0) return HS_ERR_UNSUPPORTED;
+  if (params->rotary_dim > 0 && (!params->cos_sin || !aligned(params->cos_sin, 16))) return HS_ERR_INVALID_ARG;
+  AppendTokensArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_out = q_out;
+  a.q_stride = q_stride;
+  a.q_out_stride = q_out_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.rows = rows;
+  a.offsets = params->new_offsets;
+  a.positions = params->positions;
+  a.cos_sin = params->cos_sin;
+  a.rotary = params->rotary_dim;
+  a.table_rows = params->table_rows;
+  a.interleaved = params->interleaved != 0;
+  a.smin = smin;
+  a.smax = smax;
+  const KvView view = make_view(shape, kv);
+  if (!append_tokens_fits(view, a)) return HS_ERR_UNSUPPORTED;
+  Device d;
+  if ((st = current_device(&d)) != HS_OK) return st;
+  return from_cuda(launch_append_tokens(view, a, d.err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 hs_status hs_score_select_topk(const hs_attn_shape* shape, const hs_paged_kv* kv, const void* q,
                                const void* smin, const void* smax,
                                const hs_select_params* params, int32_t* sel,
@@ -403,11 +474,7 @@ hs_status hs_sparse_paged_decode_attn(const hs_attn_shape* shape, const hs_paged
                     &use_tc);
   if (st != HS_OK) return st;
   const KvView v = make_view(shape, kv);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = use_tc ? launch_attn_tc(v, a, d.err, s) : launch_attn_simt(v, a, d.err, s);
-  if (e != cudaSuccess) return HS_ERR_CUDA;
-  if (a.merged) return HS_OK;
-  return from_cuda(launch_merge(v, a, s));
+  return run_attn(v, a, use_tc, d.err, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t hs_score_select_attend_workspace_bytes(const hs_attn_shape* shape, int32_t batch, int32_t max_blocks,
@@ -475,8 +542,7 @@ hs_status select_attend(const hs_attn_shape* shape, const hs_paged_kv* kv, const
                      cudaSuccess)
       return HS_ERR_CUDA;
     if ((st = run_select(v, sa, d, workspace, sw, s)) != HS_OK) return st;
-    cudaError_t e = use_tc ? launch_attn_tc(v, a, d.err, s) : launch_attn_simt(v, a, d.err, s);
-    if (e != cudaSuccess) return HS_ERR_CUDA;
+    return run_attn(v, a, use_tc, d.err, s);
   }
   if (a.merged) return HS_OK;
   return from_cuda(launch_merge(v, a, s));
@@ -538,8 +604,7 @@ hs_status hs_decode_step_reuse(const hs_attn_shape* shape, const hs_paged_kv* kv
     if (launch_score_select_attn(v, smin, smax, sa, a, d.err, s, new_k, new_v, true) != cudaSuccess) return HS_ERR_CUDA;
   } else {
     if (launch_append(v, new_k, new_v, smin, smax, d.err, s) != cudaSuccess) return HS_ERR_CUDA;
-    cudaError_t e = use_tc ? launch_attn_tc(v, a, d.err, s) : launch_attn_simt(v, a, d.err, s);
-    if (e != cudaSuccess) return HS_ERR_CUDA;
+    return run_attn(v, a, use_tc, d.err, s);
   }
   if (a.merged) return HS_OK;
   return from_cuda(launch_merge(v, a, s));
@@ -572,6 +637,7 @@ static hs_status hot_view(const hs_attn_shape* shape, const hs_hot_buffer* hb, H
   if (!hb->page_table || !hb->slot_owner || !hb->last_used || !hb->k_slots || !hb->v_slots ||
       !hb->host_k || !hb->host_v)
     return HS_ERR_INVALID_ARG;
+  if (shape->kv_dtype == HS_KV_FP8E4M3_BLOCK) return HS_ERR_UNSUPPORTED;  // no copy of a page's scale
   const bool fp8 = shape->kv_dtype == HS_KV_FP8E4M3_G32;
   if (fp8 && (!hb->k_slot_scales || !hb->v_slot_scales || !hb->host_k_scales || !hb->host_v_scales))
     return HS_ERR_INVALID_ARG;
@@ -756,7 +822,7 @@ hs_status hs_get_device_error_detail(hs_stream_t stream, uint32_t* bits_opt, uin
   if (bits_opt) *bits_opt = bits;
   if (timeout_opt)
     for (int i = 1; i < kErrorWords; ++i) timeout_opt[i - 1] = word[i];
-  if (bits & (HS_EBIT_PAGE_RANGE | HS_EBIT_BLOCK_RANGE)) return HS_ERR_OUT_OF_RANGE;
+  if (bits & (HS_EBIT_PAGE_RANGE | HS_EBIT_BLOCK_RANGE | HS_EBIT_POSITION)) return HS_ERR_OUT_OF_RANGE;
   if (bits & HS_EBIT_CAPACITY) return HS_ERR_CAPACITY;
   if (bits & HS_EBIT_TIMEOUT) return HS_ERR_TIMEOUT;
   return HS_OK;

@@ -60,6 +60,24 @@ struct HotView {
 // Newest token of every stream into its page + widening of its block's summary.
 cudaError_t launch_append(const KvView& kv, const void* new_k, const void* new_v, void* smin, void* smax,
                           unsigned* err, cudaStream_t st);
+// New rows of every request into their pages, rotated by position; Q rotated.
+struct AppendTokensArgs {
+  const void* q;  // nullable
+  const void* k;
+  const void* v;
+  void* q_out;
+  int64_t q_stride, q_out_stride, k_stride, v_stride;  // elements from row to row
+  int64_t rows;
+  const int32_t* offsets;    // nullable: row b is request b's one new token
+  const int32_t* positions;  // nullable: the cache positions
+  const float* cos_sin;      // [table_rows][rotary]: cos of every pair, then sin
+  int32_t rotary, table_rows;
+  bool interleaved;
+  void* smin;  // both or neither
+  void* smax;
+};
+bool append_tokens_fits(const KvView& kv, const AppendTokensArgs& a);
+cudaError_t launch_append_tokens(const KvView& kv, const AppendTokensArgs& a, unsigned* err, cudaStream_t st);
 cudaError_t launch_summaries(const KvView& kv, int first_block, void* smin, void* smax,
                              unsigned* err, int sms, cudaStream_t st);
 cudaError_t launch_score_select(const KvView& kv, const SelectArgs& a, unsigned* err,
@@ -75,6 +93,14 @@ cudaError_t launch_select_only(const KvView& kv, const SelectArgs& a, const floa
 cudaError_t launch_attn_simt(const KvView& kv, const AttnArgs& a, unsigned* err, cudaStream_t st);
 cudaError_t launch_attn_tc(const KvView& kv, AttnArgs& a, unsigned* err, cudaStream_t st);
 bool attn_tc_supported(const KvView& kv);
+// Block-scaled e4m3: its own tensor-core kernel, which cuts balanced ranges from
+// the actual counts; a.ws_o / a.ws_lse hold two rows of `group`
+// heads for each of its CTAs.  Merges in place with a.counters, else in a second launch.
+int block_attn_ctas(int sms);
+inline size_t block_attn_workspace(int ctas, int group, int head_dim) {
+  return static_cast<size_t>(ctas) * 2 * group * (head_dim + 1) * sizeof(float);
+}
+cudaError_t launch_block_attn(const KvView& kv, const AttnArgs& a, unsigned* err, cudaStream_t st);
 // Bound scoring, selection and tensor-core attention in one cluster launch
 // (bf16, head_dim 128, g <= 8, every pair in one wave of at most 8 CTAs).
 bool score_select_attn_supported(const KvView& kv, const AttnArgs& a, int sms);

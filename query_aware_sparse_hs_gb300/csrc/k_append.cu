@@ -147,6 +147,16 @@ cudaError_t launch_c(const KvView& kv, const void* new_k, const void* new_v, voi
 cudaError_t launch_append(const KvView& kv, const void* new_k, const void* new_v, void* smin, void* smax,
                           unsigned* err, cudaStream_t st) {
   if (kv.batch == 0) return cudaSuccess;
+  if (kv.kv_dtype == HS_KV_FP8E4M3_BLOCK) {  // the scale of a page concerns all its rows
+    AppendTokensArgs a{};
+    a.k = new_k;
+    a.v = new_v;
+    a.k_stride = a.v_stride = static_cast<int64_t>(kv.hkv) * kv.head_dim;
+    a.rows = kv.batch;
+    a.smin = smin;
+    a.smax = smax;
+    return launch_append_tokens(kv, a, err, st);
+  }
   return kv.head_dim == 128 ? launch_c<4>(kv, new_k, new_v, smin, smax, err, st)
                             : launch_c<2>(kv, new_k, new_v, smin, smax, err, st);
 }

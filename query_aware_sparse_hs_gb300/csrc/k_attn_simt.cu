@@ -17,7 +17,7 @@ namespace {
 constexpr int kWarps = 4;
 
 template <int C, int KIND>
-__device__ __forceinline__ void load_row(const void* pages, const float* scales, int64_t row,
+__device__ __forceinline__ void load_row(const void* pages, const float* scales, int page, int64_t row,
                                          int D, int d0, float (&x)[C]) {
   if constexpr (KIND == HS_KV_F32) {
     const float* p = static_cast<const float*>(pages) + row * D + d0;
@@ -29,7 +29,7 @@ __device__ __forceinline__ void load_row(const void* pages, const float* scales,
     for (int c = 0; c < C; ++c) x[c] = bf16_bits_to_float(__ldg(reinterpret_cast<const unsigned short*>(p + c)));
   } else {
     const uint8_t* p = static_cast<const uint8_t*>(pages) + row * D + d0;
-    const float s = __ldg(scales + row * (D / kQuantGroup) + d0 / kQuantGroup);
+    const float s = __ldg(KIND == HS_KV_FP8E4M3_BLOCK ? scales + page : scales + row * (D / kQuantGroup) + d0 / kQuantGroup);
 #pragma unroll
     for (int c = 0; c < C; c += 2) {
       const uint16_t two = static_cast<uint16_t>(__ldg(p + c)) | (static_cast<uint16_t>(__ldg(p + c + 1)) << 8);
@@ -93,8 +93,8 @@ __global__ __launch_bounds__(kWarps * 32) void attn_simt_kernel(KvView kv, AttnA
     const int64_t row0 = static_cast<int64_t>(page) * B;
     for (int t = warp; t < valid; t += kWarps) {
       float kx[C], vx[C];
-      load_row<C, KIND>(kv.k_pages, kv.k_scales, row0 + t, D, lane * C, kx);
-      load_row<C, KIND>(kv.v_pages, kv.v_scales, row0 + t, D, lane * C, vx);
+      load_row<C, KIND>(kv.k_pages, kv.k_scales, page, row0 + t, D, lane * C, kx);
+      load_row<C, KIND>(kv.v_pages, kv.v_scales, page, row0 + t, D, lane * C, vx);
 #pragma unroll
       for (int h = 0; h < G; ++h) {
         float dot = 0.0f;
@@ -166,7 +166,8 @@ cudaError_t launch_c(const KvView& kv, const AttnArgs& a, unsigned* err, cudaStr
   switch (kv.kv_dtype) {
     case HS_KV_F32: return launch_g<C, HS_KV_F32>(kv, a, err, st);
     case HS_KV_BF16: return launch_g<C, HS_KV_BF16>(kv, a, err, st);
-    default: return launch_g<C, HS_KV_FP8E4M3_G32>(kv, a, err, st);
+    case HS_KV_FP8E4M3_G32: return launch_g<C, HS_KV_FP8E4M3_G32>(kv, a, err, st);
+    default: return launch_g<C, HS_KV_FP8E4M3_BLOCK>(kv, a, err, st);
   }
 }
 

@@ -18,6 +18,8 @@ template <>
 struct Elem<HS_KV_BF16> { static constexpr int kBytes = 2; };
 template <>
 struct Elem<HS_KV_FP8E4M3_G32> { static constexpr int kBytes = 1; };
+template <>
+struct Elem<HS_KV_FP8E4M3_BLOCK> { static constexpr int kBytes = 1; };
 
 // 16 bytes of one row -> min/max of its V channels into mn/mx
 template <int KIND, int V>
@@ -112,6 +114,8 @@ __global__ __launch_bounds__(kWarps * 32) void summaries_kernel(KvView kv, int f
             raw[u] = __ldg(reinterpret_cast<const uint4*>(base + row * (D * E)));
             if constexpr (KIND == HS_KV_FP8E4M3_G32)
               sc[u] = __ldg(kv.k_scales + row * (D / kQuantGroup) + d0 / kQuantGroup);
+            else if constexpr (KIND == HS_KV_FP8E4M3_BLOCK)
+              sc[u] = __ldg(kv.k_scales + page);
             else
               sc[u] = 1.0f;
           }
@@ -192,7 +196,8 @@ cudaError_t launch_d(const KvView& kv, int first_block, int nblocks, void* smin,
   switch (kv.kv_dtype) {
     case HS_KV_F32: return launch_k<D, HS_KV_F32>(kv, first_block, nblocks, smin, smax, err, sms, st);
     case HS_KV_BF16: return launch_k<D, HS_KV_BF16>(kv, first_block, nblocks, smin, smax, err, sms, st);
-    default: return launch_k<D, HS_KV_FP8E4M3_G32>(kv, first_block, nblocks, smin, smax, err, sms, st);
+    case HS_KV_FP8E4M3_G32: return launch_k<D, HS_KV_FP8E4M3_G32>(kv, first_block, nblocks, smin, smax, err, sms, st);
+    default: return launch_k<D, HS_KV_FP8E4M3_BLOCK>(kv, first_block, nblocks, smin, smax, err, sms, st);
   }
 }
 

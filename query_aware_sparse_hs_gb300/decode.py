@@ -12,8 +12,9 @@ import torch
 
 from . import hs
 
-_SUMMARY_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8": torch.bfloat16}
-_Q_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8": torch.bfloat16}
+_SUMMARY_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8": torch.bfloat16,
+                  "fp8_block": torch.bfloat16}
+_Q_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8": torch.bfloat16, "fp8_block": torch.bfloat16}
 
 
 class SparseDecode:
@@ -87,6 +88,13 @@ class SparseDecode:
         """Writes the newest token's K/V ([batch][Hkv][D]) at seq_lens - 1 and
         widens its block's summaries (the caller has advanced seq_lens)."""
         hs.hs_append_token(self.shape, kv, new_k, new_v, self.smin, self.smax, stream)
+
+    def append_tokens(self, kv: hs.PagedKV, params: hs.AppendParams, new_k: torch.Tensor, new_v: torch.Tensor,
+                      q: torch.Tensor | None = None, q_out: torch.Tensor | None = None, stream=None):
+        """Writes any number of new tokens per request (``params.new_offsets``; one each without it) at the end of
+        their requests, K and Q rotated by position, and keeps the summaries of the touched blocks current (the
+        caller has advanced seq_lens).  new_k, new_v [rows][Hkv][D], q, q_out [rows][Hq][D]."""
+        hs.hs_append_tokens(self.shape, kv, params, new_k, new_v, q, q_out, self.smin, self.smax, stream)
 
     def select(self, kv: hs.PagedKV, q: torch.Tensor, keep_scores: bool = True, stream=None):
         hs.hs_score_select_topk(self.shape, kv, q, self.smin, self.smax, self.sel_params, self.sel,

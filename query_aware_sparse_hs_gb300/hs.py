@@ -25,7 +25,8 @@ HS_ATTN_EARLY_SUMMARIES = 1
 HS_ATTN_RANGES = 2
 HS_ATTN_NO_RANGES = 4
 HS_EBIT_PAGE_RANGE, HS_EBIT_CAPACITY, HS_EBIT_TIMEOUT, HS_EBIT_BLOCK_RANGE = 0x1, 0x2, 0x4, 0x8
-KV_DTYPES = {"f32": 0, "bf16": 1, "fp8": 2}
+HS_EBIT_POSITION = 0x10
+KV_DTYPES = {"f32": 0, "bf16": 1, "fp8": 2, "fp8_block": 3}
 ALGO = {"auto": 0, "simt": 1, "tcgen05": 2}
 
 
@@ -49,6 +50,11 @@ class PagedKV(ctypes.Structure):
 class SelectParams(ctypes.Structure):
     _fields_ = [("sink_tokens", c_int32), ("window_tokens", c_int32), ("k_scored", c_int32),
                 ("capacity", c_int32), ("history_weight", c_float), ("score_history", c_void_p)]
+
+
+class AppendParams(ctypes.Structure):
+    _fields_ = [("new_offsets", c_void_p), ("positions", c_void_p), ("cos_sin", c_void_p),
+                ("table_rows", c_int32), ("rotary_dim", c_int32), ("interleaved", c_int32)]
 
 
 class AttnParams(ctypes.Structure):
@@ -81,6 +87,9 @@ SYMBOLS = {
                                            c_void_p, c_void_p]),
     "hs_append_token": (c_int32, [POINTER(AttnShape), POINTER(PagedKV), c_void_p, c_void_p, c_void_p,
                                   c_void_p, c_void_p]),
+    "hs_append_tokens": (c_int32, [POINTER(AttnShape), POINTER(PagedKV), POINTER(AppendParams), c_int64,
+                                   c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                   c_void_p, c_void_p, c_void_p]),
     "hs_score_select_topk": (c_int32, [POINTER(AttnShape), POINTER(PagedKV), c_void_p, c_void_p,
                                        c_void_p, POINTER(SelectParams), c_void_p, c_void_p, c_void_p,
                                        c_void_p, c_size_t, c_void_p]),
@@ -236,6 +245,61 @@ def hs_append_token(shape, kv, new_k, new_v, smin, smax, stream=None):
     _check(_lib.hs_append_token(ctypes.byref(shape), ctypes.byref(kv), _ptr(new_k), _ptr(new_v), _ptr(smin),
                                 _ptr(smax), _stream(stream)),
            "hs_append_token")
+
+
+def append_params(cos_sin=None, interleaved=False, new_offsets=None, positions=None, rotary_dim=None) -> AppendParams:
+    """What hs_append_tokens is told besides the rows.  cos_sin: [positions][rotary_dim] f32, the cosines of a
+    position's rotary_dim/2 angles, then their sines (None: no rotation).  interleaved: pairs (2i, 2i+1) instead of
+    (i, i + rotary_dim/2).  new_offsets: [batch + 1] int32, the rows of each request (None: one row each).
+    positions: [rows] int32 (None: each row's position in the cache)."""
+    if rotary_dim is None:
+        rotary_dim = int(cos_sin.shape[1]) if cos_sin is not None else 0
+    elif cos_sin is not None and cos_sin.shape[1] != rotary_dim:
+        raise ValueError("cos_sin must be [positions][rotary_dim]")
+    for t, dt in ((cos_sin, torch.float32), (new_offsets, torch.int32), (positions, torch.int32)):
+        if t is not None and t.dtype != dt:
+            raise ValueError(f"expected {dt}, got {t.dtype}")
+    p = AppendParams(_ptr(new_offsets), _ptr(positions), _ptr(cos_sin),
+                     0 if cos_sin is None else int(cos_sin.shape[0]), int(rotary_dim), 1 if interleaved else 0)
+    p._keep = (cos_sin, new_offsets, positions)
+    return p
+
+
+def _rows(t, what):
+    """Address and row stride of a [rows][heads][head_dim] tensor whose rows are contiguous."""
+    if t is None:
+        return None, 0
+    st = t.stride()
+    if len(st) != 3 or (t.shape[0] > 0 and (st[2] != 1 or (st[1] != t.shape[2] and t.shape[1] > 1))):
+        raise ValueError(f"{what} must be [rows][heads][head_dim] with contiguous rows")
+    return t.data_ptr(), st[0]
+
+
+def hs_append_tokens(shape, kv, params, new_k, new_v, q=None, q_out=None, smin=None, smax=None, stream=None):
+    """Any number of new tokens per request into the paged cache, K and Q rotated on the way (see hs.h).  new_k,
+    new_v [rows][Hkv][D], q, q_out [rows][Hq][D]; the rows may be strided views (of a fused projection)."""
+    kp, ks = _rows(new_k, "new_k")
+    vp, vs = _rows(new_v, "new_v")
+    qp, qs = _rows(q, "q")
+    op, os_ = _rows(q_out, "q_out")
+    rows = new_k.shape[0]
+    if new_v.shape != new_k.shape or new_k.shape[1:] != (shape.num_kv_heads, shape.head_dim):
+        raise ValueError("new_k and new_v must be [rows][num_kv_heads][head_dim]")
+    if q is not None and (q_out is None or q.shape != q_out.shape
+                          or q.shape != (rows, shape.num_q_heads, shape.head_dim)):
+        raise ValueError("q and q_out must be [rows][num_q_heads][head_dim]")
+    want = torch.float32 if shape.kv_dtype == 0 else torch.bfloat16
+    for t in (new_k, new_v, q, q_out):
+        if t is not None and t.dtype != want:
+            raise ValueError(f"rows must be {want} for this cache, got {t.dtype}")
+    off = params._keep[1]
+    if off is not None and off.numel() != kv.batch + 1:
+        raise ValueError("new_offsets must have batch + 1 entries")
+    if params._keep[2] is not None and params._keep[2].numel() < rows:
+        raise ValueError("positions must have an entry for every row")
+    _check(_lib.hs_append_tokens(ctypes.byref(shape), ctypes.byref(kv), ctypes.byref(params), rows, qp, qs, op, os_,
+                                 kp, ks, vp, vs, _ptr(smin), _ptr(smax), _stream(stream)),
+           "hs_append_tokens")
 
 
 def hs_score_select_topk(shape, kv, q, smin, smax, params, sel, sel_count, scores=None,

@@ -1,0 +1,428 @@
+"""The e4m3 cache with one scale per page: attention over it (tensor-core and CUDA-core), its block summaries, and whole
+decode steps on it, against plain 64-bit loops.  GPU only."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -23  # a rounding of an fp32 sum on the matrix units (truncation counted)
+
+
+class Cache:
+    def __init__(self, lens, hkv, d, block, seed=0, kscale=(-9, -5), vscale=(-9, -5), poison=True, spare=2):
+        rng = np.random.default_rng(seed)
+        self.rng, self.lens, self.hkv, self.d, self.block = rng, list(lens), hkv, d, block
+        self.nb = [-(-n // block) for n in lens]
+        self.mb = max(1, max(self.nb)) + 1
+        self.pages = sum(self.nb) * hkv + spare
+        order = rng.permutation(self.pages)
+        self.table = np.full((len(lens), hkv, self.mb), -1, np.int32)
+        at = 0
+        for b, n in enumerate(self.nb):
+            for h in range(hkv):
+                self.table[b, h, :n] = order[at:at + n]
+                at += n
+        shape = (self.pages, block, d)
+        self.codes = {w: O.e4m3_encode(rng.standard_normal(shape) * 90) for w in "kv"}
+        self.scales = {w: np.exp2(rng.uniform(*e, self.pages)).astype(np.float32) for w, e in (("k", kscale), ("v", vscale))}
+        if poison:  # rows behind the last token, and pages of nobody, hold NaN
+            for b, L in enumerate(lens):
+                if L % block:
+                    for h in range(hkv):
+                        for w in "kv":
+                            self.codes[w][self.table[b, h, L // block], L % block:] = 0x7F
+            for p in order[at:]:
+                for w in "kv":
+                    self.codes[w][p] = 0xFF
+                    self.scales[w][p] = np.nan
+        self.up()
+
+    def up(self):
+        from query_aware_sparse_hs_gb300 import hs
+        c = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+        self.g = {w: c(self.codes[w]) for w in "kv"}
+        self.gs = {w: c(self.scales[w]) for w in "kv"}
+        self.gt, self.gl = c(self.table), torch.tensor(self.lens, dtype=torch.int32).cuda()
+        self.kv = hs.paged_kv(self.g["k"], self.g["v"], self.gt, self.gl, self.gs["k"], self.gs["v"])
+
+    def rows(self, w, b, h, blocks):
+        """64-bit values of the valid tokens of `blocks`."""
+        out = [np.zeros((0, self.d))]
+        for j in blocks:
+            n = min(self.block, self.lens[b] - j * self.block)
+            p = self.table[b, h, j]
+            out.append(O.e4m3_decode(self.codes[w][p, :n]) * float(self.scales[w][p]))
+        return np.concatenate(out)
+
+
+def chosen(c, capacity, keep, shuffle=False):
+    """sel and sel_count: `keep` blocks of each (request, kv head) (None: all)."""
+    sel = np.full((len(c.lens), c.hkv, capacity), -1, np.int32)
+    cnt = np.zeros((len(c.lens), c.hkv), np.int32)
+    for b, n in enumerate(c.nb):
+        for h in range(c.hkv):
+            k = n if keep is None else min(n, keep if isinstance(keep, int) else keep[b])
+            got = c.rng.permutation(n)[:k]
+            sel[b, h, :k] = got if shuffle else np.sort(got)
+            cnt[b, h] = k
+    return sel, cnt
+
+
+def attend(c, q, sel, cnt, f32=True, counters=True, algo="auto", max_ctas=0, scale=None, bps=0, lse=True):
+    from query_aware_sparse_hs_gb300 import hs
+    hq = q.shape[1]
+    shape = hs.attn_shape(hq, c.hkv, c.d, c.block, "fp8_block")
+    ctr = torch.zeros(len(c.lens) * c.hkv, dtype=torch.int32, device="cuda") if counters else None
+    p = hs.attn_params(c.d ** -0.5 if scale is None else scale, f32, bps, algo, max_ctas, split_counters=ctr)
+    ws = torch.full((max(256, hs.hs_workspace_bytes(shape, len(c.lens), sel.shape[2], p)),), 0xFF, dtype=torch.uint8, device="cuda")
+    out = torch.full(q.shape, 3.0, dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
+    ls = torch.full(q.shape[:2], 3.0, device="cuda") if lse else None
+    hs.hs_sparse_paged_decode_attn(shape, c.kv, q, torch.from_numpy(sel).cuda(), torch.from_numpy(cnt).cuda(), sel.shape[2], p,
+                                   out, ls, ws)
+    if ctr is not None:
+        assert (ctr == 0).all()
+    return out, ls
+
+
+def check_attention(c, q, sel, cnt, out, lse, scale=None, simt=False):
+    """Against the definition.  Bounds: a logit is a sum of D fp32-rounded terms (D U of the sum of magnitudes, and the
+    query's entries exact to 2^-33 of the largest), times two factors; P's two f16 terms hold 2^-21 of it, or 2^-39 of
+    the largest V scale met; an output is a sum of T such terms."""
+    scale = c.d ** -0.5 if scale is None else scale
+    qn, group = q.double().cpu().numpy(), q.shape[1] // c.hkv
+    half = 0.0 if out.dtype == torch.float32 else 2.0 ** -8
+    got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b in range(len(c.lens)):
+        for h in range(c.hkv):
+            blocks = sel[b, h, :cnt[b, h]]
+            K, V = c.rows("k", b, h, blocks), c.rows("v", b, h, blocks)
+            T = len(K)
+            for i in range(h * group, (h + 1) * group):
+                if T == 0:
+                    assert (got[b, i] == 0).all() and gl[b, i] == -np.inf
+                    continue
+                s = K @ qn[b, i] * scale
+                mags = (np.abs(K) @ np.abs(qn[b, i]) + np.abs(K).sum(1) * np.abs(qn[b, i]).max() * 2.0 ** -33) * abs(scale)
+                ds = (mags * (c.d * U + 4 * U)).max() + 4 * U * np.abs(s).max()
+                m = s.max()
+                p = np.exp(s - m)
+                want, l = (p[:, None] * V).sum(0) / p.sum(), m + math.log(p.sum())
+                assert abs(gl[b, i] - l) <= ds + (T + 40) * U + 4 * U * abs(l), (b, i, gl[b, i], l)
+                weight = (p[:, None] * np.abs(V)).sum(0) / p.sum()
+                rel = 2 * math.expm1(ds) + (T + 60) * U + 2.0 ** -20
+                tiny = 0.0 if simt else 448 * 2.0 ** -38 * float(np.max([c.scales["v"][c.table[b, h, j]] for j in blocks]))
+                bound = half * np.abs(want) + (1 + half) * (rel * weight + tiny * T / p.sum())
+                assert (np.abs(got[b, i] - want) <= bound).all(), (b, i, np.abs(got[b, i] - want).max(), bound.min())
+
+
+def query(c, hq, seed=1, spread=0.0):
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn((len(c.lens), hq, c.d), generator=g) * torch.exp2(spread * torch.randn((len(c.lens), hq, 1), generator=g))
+    return q.to(torch.bfloat16).cuda()
+
+
+CASES = {
+    # request lengths, kv heads, group, d, block, blocks kept (None: all), order
+    "one_token": ([1], 1, 8, 128, 64, None, False),
+    "around_a_tile": ([31, 32, 33, 63, 64, 65], 2, 8, 128, 64, None, False),
+    "pages_of_16": ([1, 17, 500, 1000], 2, 4, 128, 16, None, False),
+    "pages_of_16_selected": ([900, 30, 2000], 1, 8, 128, 16, 7, False),
+    "any_order": ([900, 30, 2000], 2, 8, 128, 32, 9, True),
+    "pages_of_one": ([5, 40], 1, 2, 128, 1, None, False),
+    "pages_of_five": ([3, 44, 201], 2, 1, 128, 5, None, False),
+    "pages_of_48": ([48, 47, 700], 1, 16, 128, 48, None, False),
+    "pages_of_256": ([255, 257, 1024], 1, 8, 128, 256, None, False),
+    "group_16": ([700, 3, 65], 2, 16, 128, 64, None, False),
+    "d64": ([700, 3, 65], 2, 8, 64, 64, None, False),
+    "d64_group_16": ([333, 1, 64], 1, 16, 64, 16, None, False),
+    "d64_group_1_pages_of_7": ([333, 6, 64], 3, 1, 64, 7, None, True),
+    "empty_requests": ([0, 100, 0, 0, 5, 0], 2, 8, 128, 16, None, False),
+    "nothing_selected": ([100, 200], 2, 8, 128, 16, 0, False),
+    "one_long_among_short": ([20000] + [3] * 20, 1, 8, 128, 64, None, False),
+    "many_requests": ([1 + 7 * i % 90 for i in range(400)], 2, 2, 64, 16, None, False),
+    "one_kv_head_long": ([30011], 1, 8, 128, 32, None, False),
+}
+
+
+@pytest.mark.parametrize("name", list(CASES))
+@pytest.mark.parametrize("form", ["merge_in_place", "merge_launch", "bf16_out", "simt"])
+def test_attention_matches_the_definition(name, form):
+    lens, hkv, group, d, block, keep, shuffle = CASES[name]
+    c = Cache(lens, hkv, d, block, seed=len(name))
+    q = query(c, hkv * group, spread=1.0)
+    sel, cnt = chosen(c, max(1, max(c.nb)) if keep is None else max(1, keep), keep, shuffle)
+    simt = form == "simt"
+    out, lse = attend(c, q, sel, cnt, f32=form != "bf16_out", counters=form != "merge_launch", algo="simt" if simt else "auto")
+    from query_aware_sparse_hs_gb300 import hs
+    assert hs.hs_get_device_error() == (hs.HS_OK, 0)
+    check_attention(c, q, sel, cnt, out, lse, simt=simt)
+
+
+def test_results_do_not_depend_on_the_arrival_order_or_the_number_of_ctas():
+    c = Cache([9000, 100, 5000], 2, 128, 64, seed=3)
+    q = query(c, 16)
+    sel, cnt = chosen(c, max(c.nb), None)
+    a, la = attend(c, q, sel, cnt)
+    for _ in range(20):
+        b, lb = attend(c, q, sel, cnt)
+        assert torch.equal(a, b) and torch.equal(la, lb)
+    m, lm = attend(c, q, sel, cnt, counters=False)
+    assert torch.equal(a, m) and torch.equal(la, lm)
+    for n in (1, 2, 7):
+        b, lb = attend(c, q, sel, cnt, max_ctas=n)
+        check_attention(c, q, sel, cnt, b, lb)
+    b, _ = attend(c, q, sel, cnt, lse=False, bps=5)
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("vscale", [(-30, 4), (-60, -55), (10, 14)])
+def test_v_scales_of_very_different_sizes(vscale):
+    c = Cache([700, 64, 2000], 1, 128, 16, seed=4, vscale=vscale)
+    q = query(c, 8)
+    sel, cnt = chosen(c, max(c.nb), None)
+    out, lse = attend(c, q, sel, cnt)
+    check_attention(c, q, sel, cnt, out, lse)
+
+
+def test_pages_of_zeros_and_large_or_tiny_queries():
+    c = Cache([300, 64], 1, 128, 16, seed=4, poison=False)
+    for p in c.table[0, 0, 3:9]:  # as the append leaves a page of zeros
+        c.codes["v"][p] = 0
+        c.scales["v"][p] = 2.0 ** -117
+    c.codes["k"][c.table[1, 0, :4]] = 0
+    c.scales["k"][c.table[1, 0, :4]] = 2.0 ** -117
+    c.up()
+    sel, cnt = chosen(c, max(c.nb), None)
+    for f in (1.0, 2.0 ** 60, 2.0 ** -60, 2.0 ** -126, 0.0):
+        q = query(c, 8) * f
+        # logits of ordinary size whatever the query's
+        scale = 0.0 if f == 0 else 128 ** -0.5 / f if f > 2.0 ** -100 else 128 ** -0.5
+        out, lse = attend(c, q, sel, cnt, scale=scale)
+        check_attention(c, q, sel, cnt, out, lse, scale=scale)
+
+
+def test_large_logits_of_either_sign():
+    c = Cache([500], 1, 128, 64, seed=5, kscale=(-2, 0))
+    q = query(c, 8)
+    sel, cnt = chosen(c, max(c.nb), None)
+    for scale in (1.0, -1.0):
+        out, lse = attend(c, q, sel, cnt, scale=scale)
+        assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+        check_attention(c, q, sel, cnt, out, lse, scale=scale)
+
+
+def test_not_a_number_in_a_selected_row_reaches_only_its_own_outputs():
+    c = Cache([100, 100], 2, 128, 16, seed=6)
+    c.codes["v"][c.table[0, 1, 2], 5, 7] = 0x7F
+    c.up()
+    q = query(c, 4)
+    sel, cnt = chosen(c, max(c.nb), None)
+    for algo in ("auto", "simt"):
+        out, lse = attend(c, q, sel, cnt, algo=algo)
+        bad = torch.isnan(out)
+        assert bad[0, 2:, 7].all() and bad.sum() == 2 and torch.isfinite(lse).all()
+    c.codes["k"][c.table[0, 1, 2], 5, 7] = 0xFF
+    c.up()
+    out, lse = attend(c, q, sel, cnt)
+    assert torch.isnan(out[0, 2:]).all() and torch.isfinite(out[0, :2]).all() and torch.isfinite(out[1]).all()
+
+
+def test_bad_selections_and_pages_are_reported_and_skipped():
+    from query_aware_sparse_hs_gb300 import hs
+    for algo in ("auto", "simt"):
+        c = Cache([100, 100], 1, 128, 16, seed=7)
+        q = query(c, 8)
+        sel, cnt = chosen(c, max(c.nb), None)
+        good, lse = attend(c, q, sel, cnt, algo=algo)
+        bad = sel.copy()
+        bad[0, 0, 3] = c.nb[0]  # past the request
+        bad[0, 0, 4] = -7
+        out, _ = attend(c, q, bad, cnt, algo=algo)
+        assert hs.hs_get_device_error() == (hs.HS_ERR_OUT_OF_RANGE, hs.HS_EBIT_BLOCK_RANGE)
+        assert torch.equal(out[1], good[1])
+        left = np.delete(sel[0, 0], [3, 4])
+        part, pl = sel.copy(), cnt.copy()
+        part[0, 0, :len(left)] = left
+        pl[0, 0] = len(left)
+        check_attention(c, q, part, pl, out, attend(c, q, part, pl, algo=algo)[1])
+        c.gt[0, 0, 3], c.gt[0, 0, 4] = -1, c.pages
+        out2, _ = attend(c, q, sel, cnt, algo=algo)
+        assert hs.hs_get_device_error() == (hs.HS_ERR_OUT_OF_RANGE, hs.HS_EBIT_PAGE_RANGE)
+        assert torch.equal(out2[1], good[1])
+        big = cnt.copy()
+        big[1, 0] = sel.shape[2] + 9  # counted past the capacity: cut off there
+        out3, _ = attend(c, q, sel, big, algo=algo)
+        bits = hs.hs_get_device_error()[1]
+        assert bits & hs.HS_EBIT_CAPACITY
+        assert torch.equal(out3[1], good[1])
+
+
+def test_no_allocation_call_and_workspace_checks():
+    from query_aware_sparse_hs_gb300 import hs
+    c = Cache([300, 200], 2, 128, 64, seed=8)
+    q = query(c, 16)
+    sel, cnt = chosen(c, max(c.nb), None)
+    want, wl = attend(c, q, sel, cnt)
+    shape = hs.attn_shape(16, 2, 128, 64, "fp8_block")
+    p = hs.attn_params(128 ** -0.5, True)
+    out, lse = torch.empty_like(want), torch.empty_like(wl)
+    gs, gc = torch.from_numpy(sel).cuda(), torch.from_numpy(cnt).cuda()
+    hs.hs_sparse_paged_decode_attn_noalloc(shape, c.kv, q, gs, gc, sel.shape[2], p, out, lse)
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+    need = hs.hs_workspace_bytes(shape, 2, sel.shape[2], p)
+    for ws in (None, torch.empty(need // 8, dtype=torch.uint8, device="cuda")):
+        with pytest.raises(hs.HSError) as e:
+            hs.hs_sparse_paged_decode_attn(shape, c.kv, q, gs, gc, sel.shape[2], p, out, lse, ws)
+        assert e.value.status == hs.HS_ERR_WORKSPACE
+
+
+def test_captured_and_replayed_with_other_lengths_and_on_another_stream():
+    from query_aware_sparse_hs_gb300 import hs
+    c = Cache([900, 70], 2, 128, 16, seed=9)
+    q = query(c, 16)
+    sel, cnt = chosen(c, max(c.nb), None)
+    shape = hs.attn_shape(16, 2, 128, 16, "fp8_block")
+    ctr = torch.zeros(4, dtype=torch.int32, device="cuda")
+    p = hs.attn_params(128 ** -0.5, True, split_counters=ctr)
+    ws = torch.empty(hs.hs_workspace_bytes(shape, 2, sel.shape[2], p), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty(q.shape, device="cuda"), torch.empty(q.shape[:2], device="cuda")
+    gs, gc = torch.from_numpy(sel).cuda(), torch.from_numpy(cnt).cuda()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hs.hs_sparse_paged_decode_attn(shape, c.kv, q, gs, gc, sel.shape[2], p, out, lse, ws)
+    for lens in ([900, 70], [890, 1], [1, 65]):
+        c.lens = lens
+        c.gl.copy_(torch.tensor(lens, dtype=torch.int32))
+        for b in range(2):
+            n = -(-lens[b] // 16)
+            cnt[b] = n
+            sel[b, :, :n] = np.arange(n)
+        gs.copy_(torch.from_numpy(sel))
+        gc.copy_(torch.from_numpy(cnt))
+        for b in range(2):  # rows behind the shorter request are others' from now on
+            pass
+        graph.replay()
+        check_attention(c, q, sel, cnt, out, lse)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    again = torch.empty_like(out)
+    with torch.cuda.stream(side):
+        hs.hs_sparse_paged_decode_attn(shape, c.kv, q, gs, gc, sel.shape[2], p, again, lse, ws)
+    side.synchronize()
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("block", [1, 5, 16, 48, 64, 256])
+def test_summaries_match_the_definition(d, block):
+    from query_aware_sparse_hs_gb300 import hs
+    c = Cache([0, 1, block, block + 1, 5 * block - 1, 777], 2, d, block, seed=block + d)
+    shape = hs.attn_shape(4, 2, d, block, "fp8_block")
+    for first in (0, 2):
+        lo = torch.full((len(c.lens), 2, c.mb, d), 9.0, dtype=torch.bfloat16, device="cuda")
+        hi = lo.clone()
+        hs.hs_build_block_summaries(shape, c.kv, first, lo, hi)
+        for b, n in enumerate(c.nb):
+            for h in range(2):
+                for j in range(c.mb):
+                    got = lo[b, h, j].double().cpu().numpy(), hi[b, h, j].double().cpu().numpy()
+                    if j < first or j >= n:
+                        assert (got[0] == 9).all() and (got[1] == 9).all()
+                        continue
+                    x = c.rows("k", b, h, [j])
+                    # code times scale in fp32, then outward
+                    x32 = x.astype(np.float32)
+                    assert np.array_equal(got[0], O.bf16_round_down(x32.min(0))) and np.array_equal(got[1], O.bf16_round_up(x32.max(0)))
+
+
+def test_summaries_of_extreme_codes_and_scales():
+    """Every code that is a number, -0 among them, at scales from 2^-117 to 2^100."""
+    from query_aware_sparse_hs_gb300 import hs
+    codes = np.array([x for x in range(256) if x & 0x7F != 0x7F], np.uint8)
+    c = Cache([64 * 40], 1, 64, 64, seed=2, poison=False)
+    c.codes["k"] = codes[c.rng.integers(0, len(codes), c.codes["k"].shape)]
+    c.scales["k"] = np.exp2(c.rng.integers(-117, 100, c.pages)).astype(np.float32)
+    c.scales["k"][:10] *= 1.37
+    c.up()
+    lo = torch.zeros((1, 1, c.mb, 64), dtype=torch.bfloat16, device="cuda")
+    hi = lo.clone()
+    hs.hs_build_block_summaries(hs.attn_shape(1, 1, 64, 64, "fp8_block"), c.kv, 0, lo, hi)
+    for j in range(40):
+        x = c.rows("k", 0, 0, [j]).astype(np.float32)
+        assert np.array_equal(lo[0, 0, j].double().cpu().numpy(), O.bf16_round_down(x.min(0)))
+        assert np.array_equal(hi[0, 0, j].double().cpu().numpy(), O.bf16_round_up(x.max(0)))
+
+
+@pytest.mark.parametrize("d,block", [(128, 64), (128, 16), (64, 32)])
+@pytest.mark.parametrize("fuse", [True, False])
+def test_prompts_then_decode_steps(d, block, fuse):
+    """Prompts appended with rotation, then tokens: append -> selection -> attention, every step against the definition on
+    the cache as the append left it."""
+    from query_aware_sparse_hs_gb300 import hs
+    from query_aware_sparse_hs_gb300.decode import SparseDecode
+    hq, hkv, prompts, steps = 16, 2, [5 * block + 3, 20, 9 * block], 5
+    batch, dev = len(prompts), "cuda"
+    mb = -(-(max(prompts) + steps) // block) + 1
+    g = torch.Generator(device=dev).manual_seed(d + block)
+    pages = batch * hkv * mb
+    k = torch.full((pages, block, d), 0x7F, dtype=torch.uint8, device=dev)
+    v = k.clone()
+    ks, vs = torch.full((pages,), float("nan"), device=dev), torch.full((pages,), float("nan"), device=dev)
+    table = torch.randperm(pages, generator=g, device=dev).to(torch.int32).view(batch, hkv, mb)
+    lens = torch.tensor(prompts, dtype=torch.int32, device=dev)
+    kv = hs.paged_kv(k, v, table, lens, ks, vs)
+    dec = SparseDecode(num_q_heads=hq, num_kv_heads=hkv, head_dim=d, block_size=block, kv_dtype="fp8_block", batch=batch,
+                       max_blocks=mb, sink_tokens=4, window_tokens=block + 1, k_scored=2, out_is_fp32=True, fuse_step=fuse)
+    ang = torch.arange(mb * block, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(d // 2, dtype=torch.float64) / (d // 2))
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float().to(dev)
+    off = torch.tensor([0] + list(np.cumsum(prompts)), dtype=torch.int32, device=dev)
+    rows = torch.randn((sum(prompts), hq + 2 * hkv, d), generator=g, device=dev).to(torch.bfloat16)
+    q_out = torch.empty((sum(prompts), hq, d), dtype=torch.bfloat16, device=dev)
+    dec.append_tokens(kv, hs.append_params(cs, new_offsets=off), rows[:, hq:hq + hkv], rows[:, hq + hkv:], rows[:, :hq], q_out)
+    one = hs.append_params(cs)
+    q1 = torch.empty((batch, hq, d), dtype=torch.bfloat16, device=dev)
+    c = Cache.__new__(Cache)
+    c.hkv, c.d, c.block, c.table = hkv, d, block, table.cpu().numpy()
+    for _ in range(steps):
+        lens += 1
+        rows = torch.randn((batch, hq + 2 * hkv, d), generator=g, device=dev).to(torch.bfloat16)
+        dec.append_tokens(kv, one, rows[:, hq:hq + hkv], rows[:, hq + hkv:], rows[:, :hq], q1)
+        dec.step(kv, q1)
+        assert hs.hs_get_device_error() == (hs.HS_OK, 0)
+        c.lens = lens.tolist()
+        c.nb = [-(-n // block) for n in c.lens]
+        c.codes, c.scales = {"k": k.cpu().numpy(), "v": v.cpu().numpy()}, {"k": ks.cpu().numpy(), "v": vs.cpu().numpy()}
+        sel, cnt = dec.sel.cpu().numpy(), dec.sel_count.cpu().numpy()
+        for b in range(batch):
+            forced = O.forced_blocks(c.lens[b], block, 4, block + 1)
+            for h in range(hkv):
+                K = c.rows("k", b, h, range(c.nb[b]))
+                smin, smax = O.stored_summaries(*O.block_summaries(K, block), "fp8")
+                n = c.nb[b]
+                assert np.array_equal(dec.smin[b, h, :n].double().cpu().numpy(), smin)
+                assert np.array_equal(dec.smax[b, h, :n].double().cpu().numpy(), smax)
+                score = O.bound_scores(q1[b, h * hq // hkv:(h + 1) * hq // hkv].double().cpu().numpy(), smin, smax)[-1]
+                assert sel[b, h, :cnt[b, h]].tolist() == O.select_blocks(score, forced, 2)
+        check_attention(c, q1, sel, cnt, dec.out, dec.lse)
+    # the other step calls: the token appended inside the call
+    lens += 1
+    new = torch.randn((2, batch, hkv, d), generator=g, device=dev).to(torch.bfloat16)
+    a = [t.clone() for t in (k, v, ks, vs, dec.smin, dec.smax)]
+    out, lse = (t.clone() for t in dec.step(kv, q1, new_kv=(new[0], new[1])))
+    after = [t.clone() for t in (k, v, ks, vs, dec.smin, dec.smax)]
+    for dst, src in zip((k, v, ks, vs, dec.smin, dec.smax), a):
+        dst.copy_(src)
+    dec.append(kv, new[0], new[1])
+    dec.select(kv, q1)
+    dec.attend(kv, q1)
+    for x, y in zip(after + [out, lse], (k, v, ks, vs, dec.smin, dec.smax, dec.out, dec.lse)):
+        assert torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))
+    for dst, src in zip((k, v, ks, vs, dec.smin, dec.smax), a):
+        dst.copy_(src)
+    out2, lse2 = dec.step(kv, q1, new_kv=(new[0], new[1]), reuse=dec)
+    assert torch.equal(out2, out) and torch.equal(lse2, lse)
