@@ -284,7 +284,10 @@ hs_status prepare_attn(const hs_attn_shape* shape, const hs_paged_kv* kv, const 
   }
   AttnArgs& a = *out_args;
   const bool ranges = *use_tc && shape->kv_dtype == HS_KV_FP8E4M3_BLOCK;
-  if (ranges && static_cast<int64_t>(kv->batch) * shape->num_kv_heads > INT32_MAX) return HS_ERR_UNSUPPORTED;
+  if (ranges && (static_cast<int64_t>(kv->batch) * shape->num_kv_heads > INT32_MAX ||
+                 kv->num_pages * shape->block_size > UINT32_MAX ||  // rows are numbered in 32 bits
+                 static_cast<int64_t>(capacity) * shape->block_size > INT32_MAX))
+    return HS_ERR_UNSUPPORTED;
   split_geometry(shape, kv->batch, capacity, params, ctas, &a.blocks_per_split, &a.splits, *use_tc ? &a : nullptr);
   const size_t need = ranges ? block_workspace(shape, ctas) : workspace_for(shape, kv->batch, a.splits);
   if (need > 0 && (!workspace || ws_bytes < need || !aligned(workspace, 16))) return HS_ERR_WORKSPACE;

@@ -30,8 +30,12 @@
 // Precision: q times a power of two per head (largest entry into [128, 256)) is
 // exact in f16 for entries within 2^-21 of the largest, and absolutely within
 // 2^-33 of it below.  P * vscale, in units of 2^-14 times the largest V scale
-// met so far (a power of two), enters as two f16 terms (22 bits).  Sums,
-// maxima and outputs are fp32.
+// met so far (a power of two), enters as two f16 terms (22 bits) for fp32
+// outputs; for bf16 outputs as one (rounded by 2^-11 at most, an eighth of the
+// output's own rounding, and differently for each token).  Sums, maxima and
+// partial outputs are fp32.
+#include <limits.h>
+
 #include "hs_internal.h"
 
 namespace hs {
@@ -42,7 +46,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kCtasPerSm = 2;
 constexpr int kTile = 32;       // tokens a warp handles at a time
 constexpr int kStages = 3;      // tiles in a warp's ring
-constexpr int kMinTiles = 4;    // tiles of a range at least: one per warp
+constexpr int kMinTiles = 8;    // tiles of a part at least: two per warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinRef = 7.888609052210118e-31f;  // 2^-100
 constexpr float kLn2 = 0.6931471805599453f;
@@ -50,8 +54,12 @@ constexpr float kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
-// 16 bytes to shared memory; zeros, and nothing read, unless `live`
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+// 16 bytes to shared memory
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// the same; zeros, and nothing read, unless `live`
+__device__ __forceinline__ void copy16_if(uint32_t dst, const void* src, bool live) {
   const int n = live ? 16 : 0;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
@@ -76,13 +84,17 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-// two e4m3 codes (the low or the high half of w) to two f16, exactly
-__device__ __forceinline__ uint32_t half2_of(uint16_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// four e4m3 codes to two pairs of f16, exactly
+__device__ __forceinline__ void halves_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
-__device__ __forceinline__ uint32_t lo2(uint32_t w) { return half2_of(static_cast<uint16_t>(w)); }
-__device__ __forceinline__ uint32_t hi2(uint32_t w) { return half2_of(static_cast<uint16_t>(w >> 16)); }
+__device__ __forceinline__ float exp2_fast(float x) {  // 2 ulp; results under 2^-126 are 0
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -130,21 +142,24 @@ __device__ __forceinline__ int64_t tiles_of(const KvView& kv, int count) {
   return (static_cast<int64_t>(count) * kv.block + kTile - 1) / kTile;
 }
 
-// Lays the pairs' tiles end to end.  Every thread of the CTA calls it with the
-// same `at`; afterwards *pair / *start are the pair that holds tile `at` and its
-// first tile, and the total is returned.  `each(p, count)` sees every pair once.
+// How the tiles are cut.
+//   parts: at most as many pairs as CTAs.  Every pair is cut into equal parts of
+//     at most `per` tiles, one CTA each: no CTA pays the start and the end of
+//     two pairs, and short pairs are not cut (nothing to merge).
+//   ranges: more pairs.  The tiles laid end to end, `per` to a CTA.
+struct Cut {
+  int64_t per;
+  int64_t total;
+  bool parts;
+};
+__device__ __forceinline__ int parts_of(int64_t tiles, int64_t per) { return static_cast<int>((tiles + per - 1) / per); }
+
 struct Scan {
   int64_t sums[kWarps];
-  int64_t start;
-  int pair;
 };
-template <typename F>
-__device__ int64_t sum_tiles(const KvView& kv, const BlockArgs& a, Scan& sc, F&& begin, int* pair, int64_t* start) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int pairs = kv.batch * kv.hkv, per = (pairs + kThreads - 1) / kThreads;
-  const int p0 = min(pairs, tid * per), p1 = min(pairs, p0 + per);
-  int64_t mine = 0;
-  for (int p = p0; p < p1; ++p) mine += tiles_of(kv, pair_count(kv, a, p));
+// Sum over the CTA's threads before this one, and over all of them.
+__device__ __forceinline__ int64_t scan_before(int64_t mine, Scan& sc, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -153,33 +168,73 @@ __device__ int64_t sum_tiles(const KvView& kv, const BlockArgs& a, Scan& sc, F&&
   }
   if (lane == 31) sc.sums[warp] = incl;
   __syncthreads();
-  int64_t total = 0, before = 0;
+  int64_t all = 0, before = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w == warp) before = total;
-    total += sc.sums[w];
+    if (w == warp) before = all;
+    all += sc.sums[w];
   }
-  const int64_t at = begin(total);
-  int64_t t = before + incl - mine;
-  if (at >= t && at < t + mine)
-    for (int p = p0; p < p1; ++p) {
-      const int64_t n = tiles_of(kv, pair_count(kv, a, p));
-      if (at < t + n) {
-        sc.pair = p;
-        sc.start = t;
-        break;
-      }
-      t += n;
-    }
   __syncthreads();
-  *pair = sc.pair;
-  *start = sc.start;
-  return total;
+  *total = all;
+  return before + incl - mine;
 }
 
-__device__ __forceinline__ int64_t range_length(int64_t total, int ctas) {
-  const int64_t per = (total + ctas - 1) / ctas;
-  return per > kMinTiles ? per : kMinTiles;
+// The cut for this call's counts; every thread of a CTA calls it.  `each(cut, p,
+// tiles, first tile, first part)` sees every pair once, in one of the threads;
+// the CTA's threads meet before it returns.
+template <typename F>
+__device__ Cut cut_work(const KvView& kv, const BlockArgs& a, int ctas, Scan& sc, F&& each) {
+  const int pairs = kv.batch * kv.hkv, mine_n = (pairs + kThreads - 1) / kThreads;
+  const int p0 = min(pairs, static_cast<int>(threadIdx.x) * mine_n), p1 = min(pairs, p0 + mine_n);
+  Cut cut;
+  int64_t tiles = 0;
+  for (int p = p0; p < p1; ++p) tiles += tiles_of(kv, pair_count(kv, a, p));
+  int64_t at = scan_before(tiles, sc, &cut.total);
+  cut.parts = pairs <= ctas;
+  int64_t part = 0;
+  if (cut.parts) {
+    // sum of ceil(n / per) <= total / per + pairs <= ctas
+    cut.per = pairs < ctas ? max((cut.total + ctas - pairs - 1) / (ctas - pairs), static_cast<int64_t>(kMinTiles)) : INT64_MAX / 2;
+    int64_t parts = 0, all;
+    for (int p = p0; p < p1; ++p) parts += parts_of(tiles_of(kv, pair_count(kv, a, p)), cut.per);
+    part = scan_before(parts, sc, &all);
+  } else {
+    cut.per = max((cut.total + ctas - 1) / ctas, static_cast<int64_t>(1));
+  }
+  for (int p = p0; p < p1; ++p) {
+    const int64_t n = tiles_of(kv, pair_count(kv, a, p));
+    each(cut, p, n, at, part);
+    at += n;
+    if (cut.parts) part += parts_of(n, cut.per);
+  }
+  __syncthreads();
+  return cut;
+}
+
+// The rows of the workspace that hold a pair's partial results, in the order of
+// its tiles: row(0) = first, row(i) = second + (i - 1) * step.
+//   parts: CTA c writes row c.
+//   ranges: range c writes row 2c for a pair that is under way at the range's
+//   start or begins there, else row 2c + 1.
+struct Partials {
+  int first, second, step, count;
+  __device__ __forceinline__ int64_t row(int i) const { return i == 0 ? first : second + static_cast<int64_t>(i - 1) * step; }
+};
+__device__ __forceinline__ Partials partials_of(const Cut& cut, int64_t tiles, int64_t start, int64_t part) {
+  Partials r;
+  if (cut.parts) {
+    r.first = static_cast<int>(part);
+    r.second = r.first + 1;
+    r.step = 1;
+    r.count = parts_of(tiles, cut.per);
+  } else {
+    const int c0 = static_cast<int>(start / cut.per), c1 = static_cast<int>((start + tiles - 1) / cut.per);
+    r.first = 2 * c0 + (c0 * cut.per == start ? 0 : 1);
+    r.second = 2 * (c0 + 1);
+    r.step = 2;
+    r.count = c1 - c0 + 1;
+  }
+  return r;
 }
 
 __device__ __forceinline__ void store_out(const BlockArgs& a, int64_t at, float4 v) {
@@ -192,38 +247,50 @@ __device__ __forceinline__ void store_out(const BlockArgs& a, int64_t at, float4
   }
 }
 
-// Joins the partial results of a pair (ranges c0 .. c1, in that order) into
-// out / lse.  Range c's partial of the pair is row 2c when the pair was already
-// under way at the range's start or begins there, else row 2c + 1.
+// Joins the partial results of a pair, in the order of its tiles, into out /
+// lse.  w: shared memory for G * (count + 2) floats.
 template <int D>
-__device__ void merge_pair(const KvView& kv, const BlockArgs& a, int64_t pair, int64_t start, int64_t per, int c0, int c1) {
-  const int G = kv.group;
-  const int first_row = 2 * c0 + (static_cast<int64_t>(c0) * per >= start ? 0 : 1);
-  const int64_t b = pair / kv.hkv, kvh = pair - b * kv.hkv;
-  for (int idx = threadIdx.x; idx < G * (D / 4); idx += kThreads) {
-    const int h = idx / (D / 4), d = (idx - h * (D / 4)) * 4;
-    float M = -INFINITY;
-    for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(a.ws_lse + static_cast<int64_t>(c == c0 ? first_row : 2 * c) * G + h));
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float tot = 0.0f;
-    if (M != -INFINITY) {
-#pragma unroll 4
-      for (int c = c0; c <= c1; ++c) {
-        const int64_t row = static_cast<int64_t>(c == c0 ? first_row : 2 * c) * G + h;
-        const float w = expf(__ldcg(a.ws_lse + row) - M);
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.ws_o + row * D + d));
-        tot += w;
-        acc.x = fmaf(w, v.x, acc.x);
-        acc.y = fmaf(w, v.y, acc.y);
-        acc.z = fmaf(w, v.z, acc.z);
-        acc.w = fmaf(w, v.w, acc.w);
-      }
-      acc = make_float4(acc.x / tot, acc.y / tot, acc.z / tot, acc.w / tot);
+__device__ void merge_pair(const KvView& kv, const BlockArgs& a, int64_t pair, const Partials& r, float* w) {
+  const int G = kv.group, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* norm = w + G * r.count;  // per head: 1 / sum of the weights
+  float* lses = norm + G;
+  for (int i = threadIdx.x; i < G * r.count; i += kThreads) w[i] = __ldcg(a.ws_lse + r.row(i / G) * G + i % G);
+  __syncthreads();
+  for (int h = warp; h < G; h += kWarps) {
+    float M = -INFINITY, tot = 0.0f;
+    for (int i = lane; i < r.count; i += 32) M = fmaxf(M, w[i * G + h]);
+    M = warp_max(M);
+    if (M == -INFINITY) M = 0.0f;  // no token, or only results that are not numbers: those stay so
+    for (int i = lane; i < r.count; i += 32) {
+      const float e = expf(w[i * G + h] - M);
+      w[i * G + h] = e;
+      tot += e;
     }
-    const int64_t row = b * kv.hq + kvh * G + h;
-    store_out(a, row * D + d, acc);
-    if (d == 0 && a.lse) a.lse[row] = M == -INFINITY ? M : M + logf(tot);
+    tot = warp_sum(tot);
+    if (lane == 0) {
+      norm[h] = tot == 0.0f ? 0.0f : 1.0f / tot;
+      lses[h] = tot == 0.0f ? -INFINITY : M + logf(tot);
+    }
   }
+  __syncthreads();
+  const int64_t b = pair / kv.hkv, out_row = b * kv.hq + (pair - b * kv.hkv) * G;
+  for (int idx = threadIdx.x; idx < G * (D / 4); idx += kThreads) {
+    const int h = idx / (D / 4);
+    const float* src = a.ws_o + 4 * idx;  // a partial result is G * D floats
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int i = 0; i < r.count; ++i) {
+      const float e = w[i * G + h];
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(src + r.row(i) * G * D));
+      acc.x = fmaf(e, v.x, acc.x);
+      acc.y = fmaf(e, v.y, acc.y);
+      acc.z = fmaf(e, v.z, acc.z);
+      acc.w = fmaf(e, v.w, acc.w);
+    }
+    const float n = norm[h];
+    store_out(a, out_row * D + 4 * idx, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n));
+  }
+  if (a.lse && threadIdx.x < G) a.lse[out_row + threadIdx.x] = lses[threadIdx.x];
 }
 
 template <int D>
@@ -231,7 +298,7 @@ constexpr int ring_bytes() {
   return kWarps * kStages * 2 * kTile * D;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool F32>
 __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView kv, BlockArgs a, unsigned* err) {
   constexpr int kStageBytes = 2 * kTile * D;
   constexpr int kPieces = D / 16;        // 16-byte pieces of a row
@@ -242,73 +309,178 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
   __shared__ uint32_t s_live[kWarps][kStages];
   __shared__ float s_m[kWarps][8 * NT], s_l[kWarps][8 * NT];
   __shared__ Scan s_scan;
-  __shared__ int s_last;
+  __shared__ int s_last, s_pair, s_empty;
+  __shared__ int64_t s_at;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {  // (cut_work's barriers come before anyone writes them again)
+    s_pair = -1;
+    s_empty = 0;
+  }
   const int g = lane >> 2, c4 = lane & 3;
   const int G = kv.group, B = kv.block;
   const int pairs = kv.batch * kv.hkv, ctas = gridDim.x;
 
-  int64_t per = 0, start = 0;
-  int pair = 0;
-  const int64_t total = sum_tiles(kv, a, s_scan, [&](int64_t all) {
-    per = range_length(all, ctas);
-    return static_cast<int64_t>(blockIdx.x) * per;
-  }, &pair, &start);
-  // pairs with nothing selected, and counts past the capacity
-  for (int p = blockIdx.x; p < pairs; p += ctas) {
-    const int raw = a.sel_count[p];
-    if (raw > a.capacity && tid == 0) set_error(err, HS_EBIT_CAPACITY);
-    if (raw > 0) continue;
-    const int64_t b = p / kv.hkv, row = b * kv.hq + static_cast<int64_t>(p - b * kv.hkv) * G;
-    for (int i = tid; i < G * D / 4; i += kThreads) store_out(a, row * D + 4 * i, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
-    if (a.lse && tid < G) a.lse[row + tid] = -INFINITY;
+  const Cut cut = cut_work(kv, a, ctas, s_scan, [&](const Cut& c, int p, int64_t n, int64_t at, int64_t part) {
+    if (c.parts) {
+      if (blockIdx.x >= part && blockIdx.x < part + parts_of(n, c.per)) {
+        s_pair = p;
+        s_at = part;
+      }
+    } else {
+      const int64_t t = blockIdx.x * c.per;
+      if (t >= at && t < at + n) {
+        s_pair = p;
+        s_at = at;
+      }
+    }
+    // the CTA numbered like a pair mod the grid answers for it when it is empty
+    if (n == 0 && p % ctas == static_cast<int>(blockIdx.x)) s_empty = 1;
+    if (p % ctas == static_cast<int>(blockIdx.x) && a.sel_count[p] > a.capacity) set_error(err, HS_EBIT_CAPACITY);
+  });
+  if (s_empty) {  // nothing selected: out = 0, lse = -inf
+    for (int p = blockIdx.x; p < pairs; p += ctas) {
+      if (pair_count(kv, a, p) > 0) continue;
+      const int64_t b = p / kv.hkv, row = b * kv.hq + static_cast<int64_t>(p - b * kv.hkv) * G;
+      for (int i = tid; i < G * D / 4; i += kThreads) store_out(a, row * D + 4 * i, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+      if (a.lse && tid < G) a.lse[row + tid] = -INFINITY;
+    }
   }
-  const int64_t t_begin = static_cast<int64_t>(blockIdx.x) * per;
-  const int64_t t_end = min(total, t_begin + per);
+  int pair = s_pair;
+  if (pair < 0) return;  // no tiles for this CTA
+  int64_t start = s_at;  // parts: the pair's first part; ranges: its first tile
+  int64_t t = cut.parts ? 0 : blockIdx.x * cut.per;  // (ranges) the next tile
+  const int64_t t_end = cut.parts ? 0 : min(cut.total, t + cut.per);
 
+  // this lane's 16-byte piece of the first rows a copy instruction covers
+  const uint8_t* k_piece = static_cast<const uint8_t*>(kv.k_pages) + (lane / kPieces) * D + 16 * (lane % kPieces);
+  const uint8_t* v_piece = static_cast<const uint8_t*>(kv.v_pages) + (lane / kPieces) * D + 16 * (lane % kPieces);
   uint8_t* my_ring = ring + warp * (kStages * kStageBytes);
   const uint32_t my_ring_addr = smem_addr(my_ring);
 
-  for (int64_t t = t_begin; t < t_end;) {
+  for (;;) {
     // ---- the segment: tiles [seg0, seg1) of `pair` ----
     const int cnt = pair_count(kv, a, pair);
     const int64_t pair_tiles = tiles_of(kv, cnt);
-    if (pair_tiles == 0) {
+    if (pair_tiles == 0) {  // (ranges)
       ++pair;
       continue;
     }
-    const int seg0 = static_cast<int>(t - start);
-    const int seg1 = static_cast<int>(min(pair_tiles, t_end - start));
+    const Partials parts = partials_of(cut, pair_tiles, start, start);
+    int seg0, seg1, ws_row;
+    if (cut.parts) {
+      const int64_t i = blockIdx.x - start;
+      seg0 = static_cast<int>(i * pair_tiles / parts.count);
+      seg1 = static_cast<int>((i + 1) * pair_tiles / parts.count);
+      ws_row = blockIdx.x * G;
+    } else {
+      seg0 = static_cast<int>(t - start);
+      seg1 = static_cast<int>(min(pair_tiles, t_end - start));
+      ws_row = (2 * static_cast<int>(blockIdx.x) + (blockIdx.x * cut.per >= start ? 0 : 1)) * G;
+    }
     const int b = pair / kv.hkv, kvh = pair - b * kv.hkv;
     const int L = kv.seq_lens[b];
     const int nb = min(ceil_div(max(L, 0), B), kv.max_blocks);
     const int32_t* sel = a.sel + static_cast<int64_t>(pair) * a.capacity;
     const int32_t* table = kv.page_table + static_cast<int64_t>(pair) * kv.max_blocks;
 
-    // this lane's row of the warp's next tile to look up: selection entry, row in the block
-    const int64_t u = static_cast<int64_t>(seg0 + warp) * kTile + lane;
-    int ei = static_cast<int>(u / B), er = static_cast<int>(u - static_cast<int64_t>(ei) * B);
-    const int step_i = kWarps * kTile / B, step_r = kWarps * kTile - step_i * B;
-    const int tiles = seg0 + warp < seg1 ? (seg1 - seg0 - warp + kWarps - 1) / kWarps : 0;
-    // lookups run ahead of the copies: the selected block one tile, its page another
-    int left = tiles;               // tiles whose selection entry is still to be read
-    int j1 = -1, r1 = 0;            // selected block (-1: none)
-    int pg = -1, r2 = 0;            // page (-1: no row)
-    auto look_sel = [&]() {
-      j1 = -1;
-      r1 = er;
-      if (left > 0) {
-        if (ei < cnt) {
-          j1 = __ldg(sel + ei);
-          if (j1 < 0 || j1 >= nb) {
-            set_error(err, HS_EBIT_BLOCK_RANGE);
-            j1 = -1;
+    // The warp's tiles: a run of the segment.
+    const int run0 = seg0 + static_cast<int>(static_cast<int64_t>(seg1 - seg0) * warp / kWarps);
+    const int tiles = seg0 + static_cast<int>(static_cast<int64_t>(seg1 - seg0) * (warp + 1) / kWarps) - run0;
+    // Selected blocks are looked up 32 at a time, one to a lane, the pages one
+    // window ahead of the copies and the selection two, so that neither load is
+    // waited for.  A window holds the entries from that of its first tile on;
+    // a tile that does not fit opens the next.
+    const uint32_t u0 = static_cast<uint32_t>(run0) * kTile, u_stop = u0 + static_cast<uint32_t>(tiles) * kTile;
+    const uint32_t Bu = B;
+    const auto window_end = [&](uint32_t u, uint32_t e) {  // first token past the window's whole tiles
+      return u + ((e + 32) * Bu - u) / kTile * kTile;
+    };
+    const auto load_sel = [&](uint32_t u, uint32_t e) {  // INT_MIN: no such entry
+      return u < u_stop && e + lane < static_cast<uint32_t>(cnt) ? __ldg(sel + e + lane) : INT_MIN;
+    };
+    const auto load_page = [&](int j, int& page, int& lim) {  // lim: valid rows of the page
+      page = lim = 0;
+      if (j == INT_MIN) return;
+      if (j < 0 || j >= nb) {
+        set_error(err, HS_EBIT_BLOCK_RANGE);
+        return;
+      }
+      page = __ldg(table + j);
+      if (page < 0 || page >= kv.num_pages) {
+        set_error(err, HS_EBIT_PAGE_RANGE);
+        page = 0;
+        return;
+      }
+      lim = min(B, L - j * B);
+    };
+    uint32_t w_end, w_end1, w_end2;  // of the window in use, the next, the one after
+    uint32_t e_base = u0 / Bu, e1, e2;
+    int page, lim, page1, lim1, j2;
+    {
+      const int j0 = load_sel(u0, e_base);
+      w_end = window_end(u0, e_base);
+      e1 = w_end / Bu;
+      const int j1 = load_sel(w_end, e1);
+      w_end1 = window_end(w_end, e1);
+      e2 = w_end1 / Bu;
+      j2 = load_sel(w_end1, e2);
+      w_end2 = window_end(w_end1, e2);
+      load_page(j0, page, lim);
+      load_page(j1, page1, lim1);
+    }
+    // this lane's row of the next tile: its entry and its row in the block
+    uint32_t u = u0;
+    int ei = static_cast<int>((u0 + lane) / Bu), er = static_cast<int>(u0 + lane - ei * Bu);
+    const int step_i = kTile / B, step_r = kTile - step_i * B;
+    int stage_in = 0;
+    const auto issue = [&]() {  // the copies of the next tile
+      if (u >= w_end) {
+        e_base = e1;
+        w_end = w_end1;
+        page = page1;
+        lim = lim1;
+        e1 = e2;
+        w_end1 = w_end2;
+        load_page(j2, page1, lim1);
+        e2 = w_end2 / Bu;
+        j2 = load_sel(w_end2, e2);
+        w_end2 = window_end(w_end2, e2);
+      }
+      const int pg = __shfl_sync(0xffffffffu, page, ei - static_cast<int>(e_base));
+      const bool ok = er < __shfl_sync(0xffffffffu, lim, ei - static_cast<int>(e_base));
+      const uint32_t live = __ballot_sync(0xffffffffu, ok);
+      const uint32_t row = ok ? static_cast<uint32_t>(pg) * B + er : 0u;
+      const uint32_t dst = my_ring_addr + stage_in * kStageBytes;
+      if (live == 0xffffffffu && (B & 15) == 0) {  // 16 rows in a row of one page, twice
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint64_t at = static_cast<uint64_t>(__shfl_sync(0xffffffffu, row, 16 * h)) * D;
+          const uint8_t* ks = k_piece + at;
+          const uint8_t* vs = v_piece + at;
+#pragma unroll
+          for (int i = 0; i < 16 / kRowsPer; ++i) {
+            const int r = 16 * h + i * kRowsPer + lane / kPieces;
+            copy16(dst + piece_at<D>(r, lane % kPieces), ks + i * kRowsPer * D);
+            copy16(dst + kTile * D + piece_at<D>(r, lane % kPieces), vs + i * kRowsPer * D);
           }
         }
-        --left;
+      } else {  // any rows; those that are not there are zeros
+#pragma unroll
+        for (int i = 0; i < kTile / kRowsPer; ++i) {
+          const int r = i * kRowsPer + lane / kPieces;
+          const uint64_t at = static_cast<uint64_t>(__shfl_sync(0xffffffffu, row, r)) * D - (lane / kPieces) * D;
+          const bool there = (live >> r) & 1u;
+          copy16_if(dst + piece_at<D>(r, lane % kPieces), k_piece + at, there);
+          copy16_if(dst + kTile * D + piece_at<D>(r, lane % kPieces), v_piece + at, there);
+        }
       }
+      copy4(smem_addr(&s_ks[warp][stage_in][lane]), kv.k_scales + pg, ok);
+      copy4(smem_addr(&s_vs[warp][stage_in][lane]), kv.v_scales + pg, ok);
+      if (lane == 0) s_live[warp][stage_in] = live;
+      stage_in = stage_in + 1 == kStages ? 0 : stage_in + 1;
+      u += kTile;
       ei += step_i;
       er += step_r;
       if (er >= B) {
@@ -316,39 +488,6 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
         ++ei;
       }
     };
-    auto look_page = [&]() {
-      pg = -1;
-      r2 = r1;
-      if (j1 >= 0 && r1 < L - j1 * B) {
-        pg = __ldg(table + j1);
-        if (pg < 0 || pg >= kv.num_pages) {
-          set_error(err, HS_EBIT_PAGE_RANGE);
-          pg = -1;
-        }
-      }
-    };
-    int stage_in = 0;
-    auto issue = [&]() {  // copies of the tile whose pages are known
-      const uint32_t dst = my_ring_addr + stage_in * kStageBytes;
-      const uint32_t live = __ballot_sync(0xffffffffu, pg >= 0);
-      const int64_t row = pg >= 0 ? static_cast<int64_t>(pg) * B + r2 : 0;
-#pragma unroll
-      for (int i = 0; i < kTile / kRowsPer; ++i) {
-        const int r = i * kRowsPer + lane / kPieces, c = lane % kPieces;
-        const int64_t at = __shfl_sync(0xffffffffu, row, r) * D + 16 * c;
-        const bool ok = (live >> r) & 1u;
-        copy16(dst + piece_at<D>(r, c), static_cast<const uint8_t*>(kv.k_pages) + at, ok);
-        copy16(dst + kTile * D + piece_at<D>(r, c), static_cast<const uint8_t*>(kv.v_pages) + at, ok);
-      }
-      const int pp = pg >= 0 ? pg : 0;
-      copy4(smem_addr(&s_ks[warp][stage_in][lane]), kv.k_scales + pp, pg >= 0);
-      copy4(smem_addr(&s_vs[warp][stage_in][lane]), kv.v_scales + pp, pg >= 0);
-      if (lane == 0) s_live[warp][stage_in] = live;
-      stage_in = stage_in + 1 == kStages ? 0 : stage_in + 1;
-    };
-    look_sel();
-    look_page();
-    look_sel();
     int issued = 0;
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
@@ -357,8 +496,6 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
         ++issued;
       }
       copies_commit();
-      look_page();
-      look_sel();
     }
 
     // ---- the query, as the S product's second operand ----
@@ -391,14 +528,15 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       float f = 1.0f;  // 2^(7 - exponent of amax)
       if (amax > 0.0f && amax < INFINITY) f = __uint_as_float(static_cast<uint32_t>(min(254, 261 - static_cast<int>(__float_as_uint(amax) >> 23))) << 23);
+      const float fs = a.scale < 0.0f ? -f : f;  // the factors of the logits are not negative
 #pragma unroll
       for (int k = 0; k < kChunks; ++k)
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          qf[nt][4 * k + w][0] = pack_half2(x[k][4 * w] * f, x[k][4 * w + 1] * f);
-          qf[nt][4 * k + w][1] = pack_half2(x[k][4 * w + 2] * f, x[k][4 * w + 3] * f);
+          qf[nt][4 * k + w][0] = pack_half2(x[k][4 * w] * fs, x[k][4 * w + 1] * fs);
+          qf[nt][4 * k + w][1] = pack_half2(x[k][4 * w + 2] * fs, x[k][4 * w + 3] * fs);
         }
-      const float s = a.scale * kLog2e / f;
+      const float s = fmaxf(fabsf(a.scale) * kLog2e / f, 1e-37f);  // (times -inf is -inf, for a scale of 0 too)
       qs[nt][0] = __shfl_sync(0xffffffffu, s, 8 * c4);
       qs[nt][1] = __shfl_sync(0xffffffffu, s, 8 * c4 + 4);
     }
@@ -424,8 +562,6 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
         ++issued;
       }
       copies_commit();
-      look_page();
-      look_sel();
       copies_wait<kStages - 1>();
       __syncwarp();
       const uint8_t* kt = my_ring + stage * kStageBytes;
@@ -450,7 +586,9 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
           const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            const uint32_t a0 = lo2(wa[w]), a1 = lo2(wb[w]), a2 = hi2(wa[w]), a3 = hi2(wb[w]);
+            uint32_t a0, a1, a2, a3;
+            halves_of(wa[w], a0, a2);
+            halves_of(wb[w], a1, a3);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma(s[st][nt], a0, a1, a2, a3, qf[nt][4 * k + w][0], qf[nt][4 * k + w][1]);
           }
@@ -477,13 +615,13 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float& x = s[i >> 1][nt][2 * (i & 1) + e];
-            x = ok[i] ? x * (kr[i] * qs[nt][e]) : -INFINITY;
+            x = ok[i] ? x * kr[i] : -INFINITY;  // (times qs: the logit)
             top = fmaxf(top, x);
           }
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          mn[nt][e] = fmaxf(m[nt][e], top);
+          mn[nt][e] = fmaxf(m[nt][e], top * qs[nt][e]);
           raised |= mn[nt][e] > m[nt][e];
         }
       const uint32_t vmax = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(vs[lane])));
@@ -522,14 +660,16 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float base = m[nt][e] == -INFINITY ? 0.0f : m[nt][e];
-              p[e] = exp2f(s[st][nt][2 * i + e] - base);
+              p[e] = exp2_fast(fmaf(s[st][nt][2 * i + e], qs[nt][e], -base));
               l[nt][e] += p[e];
               p[e] *= vr[2 * st + i];
             }
             const uint32_t hi = pack_half2(p[0], p[1]);
-            const float2 back = unpack_half2(hi);
             ph[nt][i] = transpose8x8(hi);
-            pl[nt][i] = transpose8x8(pack_half2(p[0] - back.x, p[1] - back.y));
+            if constexpr (F32) {
+              const float2 back = unpack_half2(hi);
+              pl[nt][i] = transpose8x8(pack_half2(p[0] - back.x, p[1] - back.y));
+            }
           }
         const int t0 = 16 * st + token_of<D>(2 * c4), t1 = 16 * st + token_of<D>(2 * c4 + 1);
         constexpr int kWords = D / 32;  // words of a lane's channels: D / 8 of them
@@ -551,11 +691,13 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
         for (int i = 0; i < D / 16; ++i) {
           const uint32_t pick = (i & 1) ? 0x7362u : 0x5140u;  // (byte of token 2k, byte of token 2k + 1) twice
           const uint32_t y0 = __byte_perm(x[0][i >> 1], x[1][i >> 1], pick), y1 = __byte_perm(x[2][i >> 1], x[3][i >> 1], pick);
-          const uint32_t a0 = lo2(y0), a1 = hi2(y0), a2 = lo2(y1), a3 = hi2(y1);
+          uint32_t a0, a1, a2, a3;
+          halves_of(y0, a0, a1);
+          halves_of(y1, a2, a3);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma(o[nt][i], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-            mma(o[nt][i], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+            if constexpr (F32) mma(o[nt][i], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
           }
         }
       }
@@ -587,28 +729,27 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
               make_float4(o[nt][i][e] * back, o[nt][i][2 + e] * back, o[nt][i + 1][e] * back, o[nt][i + 1][2 + e] * back);
       }
     __syncthreads();
-    const int c0 = static_cast<int>(start / per), c1 = static_cast<int>((start + pair_tiles - 1) / per);
-    const bool whole = c0 == c1;
-    const int64_t ws_row = (2 * static_cast<int64_t>(blockIdx.x) + (t_begin >= start ? 0 : 1)) * G;
+    const bool whole = parts.count == 1;
     for (int idx = tid; idx < G * (D / 4); idx += kThreads) {
       const int h = idx / (D / 4), d = (idx - h * (D / 4)) * 4;
       float M = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][h]);
+      if (M == -INFINITY) M = 0.0f;  // no token, or only logits that are not numbers
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      float lse = -INFINITY;
-      if (M != -INFINITY) {
-        float tot = 0.0f;
+      float tot = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float f = exp2f(s_m[w][h] - M);
-          const float4 v = *reinterpret_cast<const float4*>(so + (w * 8 * NT + h) * D + d);
-          tot = fmaf(s_l[w][h], f, tot);
-          acc.x = fmaf(v.x, f, acc.x);
-          acc.y = fmaf(v.y, f, acc.y);
-          acc.z = fmaf(v.z, f, acc.z);
-          acc.w = fmaf(v.w, f, acc.w);
-        }
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = exp2f(s_m[w][h] - M);
+        const float4 v = *reinterpret_cast<const float4*>(so + (w * 8 * NT + h) * D + d);
+        tot = fmaf(s_l[w][h], f, tot);
+        acc.x = fmaf(v.x, f, acc.x);
+        acc.y = fmaf(v.y, f, acc.y);
+        acc.z = fmaf(v.z, f, acc.z);
+        acc.w = fmaf(v.w, f, acc.w);
+      }
+      float lse = -INFINITY;
+      if (tot != 0.0f) {
         acc = make_float4(acc.x / tot, acc.y / tot, acc.z / tot, acc.w / tot);
         lse = M * kLn2 + logf(tot);
       }
@@ -617,7 +758,7 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
         store_out(a, row * D + d, acc);
         if (d == 0 && a.lse) a.lse[row] = lse;
       } else {
-        *reinterpret_cast<float4*>(a.ws_o + (ws_row + h) * D + d) = acc;
+        *reinterpret_cast<float4*>(a.ws_o + static_cast<int64_t>(ws_row + h) * D + d) = acc;
         if (d == 0) a.ws_lse[ws_row + h] = lse;
       }
     }
@@ -626,13 +767,14 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
       __syncthreads();
       if (tid == 0) {
         const uint32_t there = atomicAdd(a.counters + pair, 1u);
-        s_last = there == static_cast<uint32_t>(c1 - c0);
+        s_last = there == static_cast<uint32_t>(parts.count - 1);
         if (s_last) a.counters[pair] = 0u;
         __threadfence();
       }
       __syncthreads();
-      if (s_last) merge_pair<D>(kv, a, pair, start, per, c0, c1);
+      if (s_last) merge_pair<D>(kv, a, pair, parts, reinterpret_cast<float*>(ring));
     }
+    if (cut.parts || start + seg1 >= t_end) return;
     __syncthreads();  // the ring and s_m are free again
     t = start + seg1;
     if (seg1 == pair_tiles) {
@@ -646,42 +788,39 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
 // pair.
 template <int D>
 __global__ __launch_bounds__(kThreads) void attn_block_merge_kernel(KvView kv, BlockArgs a, int ctas) {
+  extern __shared__ float weights[];
   __shared__ Scan s_scan;
+  __shared__ int64_t s_tiles, s_start, s_part;
   pdl_trigger();
   pdl_wait();
   const int pair = blockIdx.x;
-  const int64_t n = tiles_of(kv, pair_count(kv, a, pair));
-  // the pair's first tile: the tiles of the pairs before it
-  int64_t mine = 0;
-  for (int p = threadIdx.x; p < kv.batch * kv.hkv; p += kThreads) {
-    const int64_t k = tiles_of(kv, pair_count(kv, a, p));
-    if (p < pair) mine += k;
-  }
-  mine = warp_sum(mine);
-  if ((threadIdx.x & 31) == 0) s_scan.sums[threadIdx.x >> 5] = mine;
-  __syncthreads();
-  int64_t start = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) start += s_scan.sums[w];
-  __syncthreads();
-  int unused_pair;
-  int64_t unused_start, per = 0;
-  sum_tiles(kv, a, s_scan, [&](int64_t all) {
-    per = range_length(all, ctas);
-    return int64_t(0);
-  }, &unused_pair, &unused_start);
-  if (n == 0) return;
-  const int c0 = static_cast<int>(start / per), c1 = static_cast<int>((start + n - 1) / per);
-  if (c0 != c1) merge_pair<D>(kv, a, pair, start, per, c0, c1);
+  const Cut cut = cut_work(kv, a, ctas, s_scan, [&](const Cut&, int p, int64_t n, int64_t at, int64_t part) {
+    if (p == pair) {
+      s_tiles = n;
+      s_start = at;
+      s_part = part;
+    }
+  });
+  if (s_tiles == 0) return;
+  const Partials r = partials_of(cut, s_tiles, s_start, s_part);
+  if (r.count > 1) merge_pair<D>(kv, a, pair, r, weights);
+}
+
+template <int D, int NT, bool F32>
+cudaError_t launch_o(const KvView& kv, const BlockArgs& b, int ctas, unsigned* err, cudaStream_t st) {
+  auto kern = attn_block_kernel<D, NT, F32>;
+  if (cudaError_t e = allow_dynamic_smem(kern, ring_bytes<D>()); e != cudaSuccess) return e;
+  cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(kThreads), ring_bytes<D>(), st, kv, b, err);
+  if (e != cudaSuccess || b.counters) return e;
+  const size_t smem = static_cast<size_t>(ctas + 2) * kv.group * sizeof(float);
+  auto merge = attn_block_merge_kernel<D>;
+  if ((e = allow_dynamic_smem(merge, smem)) != cudaSuccess) return e;
+  return launch_pdl(merge, dim3(kv.batch * kv.hkv), dim3(kThreads), smem, st, kv, b, ctas);
 }
 
 template <int D, int NT>
 cudaError_t launch_n(const KvView& kv, const BlockArgs& b, int ctas, unsigned* err, cudaStream_t st) {
-  auto kern = attn_block_kernel<D, NT>;
-  if (cudaError_t e = allow_dynamic_smem(kern, ring_bytes<D>()); e != cudaSuccess) return e;
-  cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(kThreads), ring_bytes<D>(), st, kv, b, err);
-  if (e != cudaSuccess || b.counters) return e;
-  return launch_pdl(attn_block_merge_kernel<D>, dim3(kv.batch * kv.hkv), dim3(kThreads), 0, st, kv, b, ctas);
+  return b.out_f32 ? launch_o<D, NT, true>(kv, b, ctas, err, st) : launch_o<D, NT, false>(kv, b, ctas, err, st);
 }
 
 }  // namespace

@@ -92,7 +92,7 @@ def attend(c, q, sel, cnt, f32=True, counters=True, algo="auto", max_ctas=0, sca
 def check_attention(c, q, sel, cnt, out, lse, scale=None, simt=False):
     """Against the definition.  Bounds: a logit is a sum of D fp32-rounded terms (D U of the sum of magnitudes, and the
     query's entries exact to 2^-33 of the largest), times two factors; P's two f16 terms hold 2^-21 of it, or 2^-39 of
-    the largest V scale met; an output is a sum of T such terms."""
+    the largest V scale met (one term, 2^-11 or 2^-39, for bf16 outputs); an output is a sum of T such terms."""
     scale = c.d ** -0.5 if scale is None else scale
     qn, group = q.double().cpu().numpy(), q.shape[1] // c.hkv
     half = 0.0 if out.dtype == torch.float32 else 2.0 ** -8
@@ -114,7 +114,7 @@ def check_attention(c, q, sel, cnt, out, lse, scale=None, simt=False):
                 want, l = (p[:, None] * V).sum(0) / p.sum(), m + math.log(p.sum())
                 assert abs(gl[b, i] - l) <= ds + (T + 40) * U + 4 * U * abs(l), (b, i, gl[b, i], l)
                 weight = (p[:, None] * np.abs(V)).sum(0) / p.sum()
-                rel = 2 * math.expm1(ds) + (T + 60) * U + 2.0 ** -20
+                rel = 2 * math.expm1(ds) + (T + 60) * U + (2.0 ** -20 if half == 0 or simt else 2.0 ** -11)
                 tiny = 0.0 if simt else 448 * 2.0 ** -38 * float(np.max([c.scales["v"][c.table[b, h, j]] for j in blocks]))
                 bound = half * np.abs(want) + (1 + half) * (rel * weight + tiny * T / p.sum())
                 assert (np.abs(got[b, i] - want) <= bound).all(), (b, i, np.abs(got[b, i] - want).max(), bound.min())
@@ -230,6 +230,19 @@ def test_not_a_number_in_a_selected_row_reaches_only_its_own_outputs():
     c.up()
     out, lse = attend(c, q, sel, cnt)
     assert torch.isnan(out[0, 2:]).all() and torch.isfinite(out[0, :2]).all() and torch.isfinite(out[1]).all()
+
+
+def test_requests_of_nothing_but_not_a_number():
+    for lens in ([1, 40], [9000, 40]):  # one CTA, and several merged
+        c = Cache(lens, 1, 128, 16, seed=6)
+        n = -(-lens[0] // 16)
+        c.codes["k"][c.table[0, 0, :n]] = 0x7F
+        c.up()
+        q = query(c, 4)
+        sel, cnt = chosen(c, max(c.nb), None)
+        for counters in (True, False):
+            out, lse = attend(c, q, sel, cnt, counters=counters)
+            assert torch.isnan(out[0]).all() and torch.isnan(lse[0]).all() and torch.isfinite(out[1]).all()
 
 
 def test_bad_selections_and_pages_are_reported_and_skipped():
