@@ -193,11 +193,12 @@ typedef struct hs_select_params {
  * per pair; HS_ATTN_RANGES takes them whenever they apply, HS_ATTN_NO_RANGES
  * never (hs_attn_geometry reports the choice).
  * A cache with a scale per page (HS_KV_FP8E4M3_BLOCK) has a tensor-core kernel of
- * its own, for every block_size: it always cuts balanced ranges, from the
- * actual selection counts, whatever blocks_per_split and these flags say; it
- * waits for nothing but its own copies, so wait_limit_ns does not concern it;
- * max_ctas limits it to n SMs; without split_counters it merges in a second
- * launch. */
+ * its own, for every block_size: it cuts the work by the actual selection
+ * counts, whatever blocks_per_split and these flags say, and needs no more
+ * workspace for more requests; it waits for nothing but its own copies, so
+ * wait_limit_ns does not concern it; max_ctas as above; without split_counters
+ * it merges in a second launch.  Pools of 2^32 token rows and selections of 2^31
+ * tokens are not supported. */
 #define HS_ATTN_EARLY_SUMMARIES 1u
 #define HS_ATTN_RANGES 2u
 #define HS_ATTN_NO_RANGES 4u

@@ -169,10 +169,14 @@ size_t workspace_for(const hs_attn_shape* s, int batch, int splits) {
   return (bytes + 255) & ~static_cast<size_t>(255);
 }
 
-// The same for the kernel of block-scaled e4m3, which cuts ranges from the
-// actual counts: two partial results per CTA.
-size_t block_workspace(const hs_attn_shape* s, int sms) {
-  const size_t bytes = block_attn_workspace(block_attn_ctas(sms), s->num_q_heads / s->num_kv_heads, s->head_dim);
+// The same for the kernel of block-scaled e4m3, which cuts the work by the
+// actual counts: its CTAs (as many as fit the GPU, or max_ctas), and two partial
+// results for each.
+int block_ctas(int sms, const hs_attn_params* p) {
+  return p && p->max_ctas > 0 && p->max_ctas <= sms ? p->max_ctas : block_attn_ctas(sms);
+}
+size_t block_workspace(const hs_attn_shape* s, int ctas) {
+  const size_t bytes = block_attn_workspace(ctas, s->num_q_heads / s->num_kv_heads, s->head_dim);
   return (bytes + 255) & ~static_cast<size_t>(255);
 }
 
@@ -186,7 +190,7 @@ size_t attn_workspace_need(const hs_attn_shape* s, int batch, int capacity, cons
   AttnArgs t;
   split_geometry(s, batch, capacity, p, ctas, &bps, &splits, &t);
   size_t tc = workspace_for(s, batch, splits);
-  if (s->kv_dtype == HS_KV_FP8E4M3_BLOCK) tc = block_workspace(s, ctas);
+  if (s->kv_dtype == HS_KV_FP8E4M3_BLOCK) tc = block_workspace(s, block_ctas(ctas, p));
   return uniform > tc ? uniform : tc;
 }
 
@@ -289,9 +293,10 @@ hs_status prepare_attn(const hs_attn_shape* shape, const hs_paged_kv* kv, const 
                  static_cast<int64_t>(capacity) * shape->block_size > INT32_MAX))
     return HS_ERR_UNSUPPORTED;
   split_geometry(shape, kv->batch, capacity, params, ctas, &a.blocks_per_split, &a.splits, *use_tc ? &a : nullptr);
-  const size_t need = ranges ? block_workspace(shape, ctas) : workspace_for(shape, kv->batch, a.splits);
+  const int bctas = block_ctas(ctas, params);
+  const size_t need = ranges ? block_workspace(shape, bctas) : workspace_for(shape, kv->batch, a.splits);
   if (need > 0 && (!workspace || ws_bytes < need || !aligned(workspace, 16))) return HS_ERR_WORKSPACE;
-  a.sms = ctas;
+  a.sms = ranges ? bctas : ctas;
   if (params->split_counters && !aligned(params->split_counters, 4)) return HS_ERR_INVALID_ARG;
   a.counters = params->split_counters;
   a.wait_ns = static_cast<uint64_t>(params->wait_limit_ns);
@@ -305,7 +310,7 @@ hs_status prepare_attn(const hs_attn_shape* shape, const hs_paged_kv* kv, const 
   a.out = out;
   a.lse = lse_opt;
   a.ws_o = static_cast<float*>(workspace);
-  a.ws_lse = a.ws_o + (ranges ? static_cast<size_t>(block_attn_ctas(ctas)) * 2 * v.group
+  a.ws_lse = a.ws_o + (ranges ? static_cast<size_t>(bctas) * 2 * v.group
                               : static_cast<size_t>(kv->batch) * shape->num_q_heads * a.splits) *
                           shape->head_dim;
   return HS_OK;

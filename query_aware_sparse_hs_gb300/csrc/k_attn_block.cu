@@ -8,14 +8,14 @@
 // token, vscale its probability, so the codes enter the matrix units as they
 // are (as f16, which holds every e4m3 number exactly).
 //
-// Work: the 32-token tiles of every (request, kv head)'s selection are laid end
-// to end (from the actual counts, summed by every CTA) and cut into equal
-// ranges, one per CTA; a range that ends inside a pair leaves a partial result,
-// and the CTA that arrives last at the pair merges them in range order (the
-// same result whichever CTA that is).  The warps of a CTA take the tiles of a
-// segment in turn, each with its own running maximum, sum and output, its own
-// ring of tiles in shared memory filled by asynchronous 16-byte copies, and no
-// barrier with the others until the segment ends.
+// Work: the 32-token tiles of every (request, kv head)'s selection, from the
+// actual counts, which every CTA sums; pairs are cut into equal parts (cut_work
+// below), and of a pair that is cut the CTA that arrives last merges the partial
+// results in the parts' order (the same result whichever CTA that is).  The
+// warps of a CTA take a run of the part's tiles each, with their own running
+// maximum, sum and output, their own ring of tiles in shared memory filled by
+// asynchronous 16-byte copies, and no barrier with the others until the part
+// ends.
 //
 // Products on the warp-level matrix instruction m16n8k16 (f16 in, fp32 sums):
 //   S[token][head] = K . Q^T: 16 tokens by 8 heads, so that the group of query
@@ -46,7 +46,8 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kCtasPerSm = 2;
 constexpr int kTile = 32;       // tokens a warp handles at a time
 constexpr int kStages = 3;      // tiles in a warp's ring
-constexpr int kMinTiles = 8;    // tiles of a part at least: two per warp
+constexpr int kMinTiles = 8;    // tiles of a part of a cut pair at least: two per warp
+constexpr int kWholeTiles = 32;  // pairs of up to so many tiles are not cut
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinRef = 7.888609052210118e-31f;  // 2^-100
 constexpr float kLn2 = 0.6931471805599453f;
@@ -142,17 +143,28 @@ __device__ __forceinline__ int64_t tiles_of(const KvView& kv, int count) {
   return (static_cast<int64_t>(count) * kv.block + kTile - 1) / kTile;
 }
 
-// How the tiles are cut.
-//   parts: at most as many pairs as CTAs.  Every pair is cut into equal parts of
-//     at most `per` tiles, one CTA each: no CTA pays the start and the end of
-//     two pairs, and short pairs are not cut (nothing to merge).
-//   ranges: more pairs.  The tiles laid end to end, `per` to a CTA.
-struct Cut {
-  int64_t per;
-  int64_t total;
-  bool parts;
+// Every pair is cut into equal parts of at most `per` tiles; the parts of all
+// pairs are numbered through, and CTA c takes parts c, c + ctas, ...  With
+// per = total / max(ctas - pairs, ctas / 2) there are no more parts than CTAs
+// where the pairs leave room for that (sum of ceil(n / per) <= total / per +
+// pairs), and a long pair among many short ones is
+// still spread over half the CTAs.  Short pairs are not cut: they have nothing
+// to merge.  A pair that is cut has a row of the workspace for each part: at
+// most 2 total / per <= 2 ctas rows in all.
+struct Part {
+  int pair;
+  int index, count;  // which of the pair's parts
+  int row;           // workspace row of the pair's first part
 };
-__device__ __forceinline__ int parts_of(int64_t tiles, int64_t per) { return static_cast<int>((tiles + per - 1) / per); }
+struct Pairs {  // one pair's numbers
+  int64_t tiles;
+  int part, count, row;  // its first part, how many, workspace row of the first
+};
+constexpr int kListed = 32;  // parts a CTA notes at a time
+
+__device__ __forceinline__ int parts_of(int64_t tiles, int64_t per) {
+  return tiles <= kWholeTiles ? (tiles > 0 ? 1 : 0) : static_cast<int>((tiles + per - 1) / per);
+}
 
 struct Scan {
   int64_t sums[kWarps];
@@ -179,62 +191,35 @@ __device__ __forceinline__ int64_t scan_before(int64_t mine, Scan& sc, int64_t* 
   return before + incl - mine;
 }
 
-// The cut for this call's counts; every thread of a CTA calls it.  `each(cut, p,
-// tiles, first tile, first part)` sees every pair once, in one of the threads;
-// the CTA's threads meet before it returns.
+// Cuts this call's pairs; every thread of a CTA calls it.  each(p, numbers) sees
+// every pair once, in one of the threads; the CTA's threads meet before it
+// returns the number of parts.
 template <typename F>
-__device__ Cut cut_work(const KvView& kv, const BlockArgs& a, int ctas, Scan& sc, F&& each) {
+__device__ int cut_work(const KvView& kv, const BlockArgs& a, int ctas, Scan& sc, F&& each) {
   const int pairs = kv.batch * kv.hkv, mine_n = (pairs + kThreads - 1) / kThreads;
   const int p0 = min(pairs, static_cast<int>(threadIdx.x) * mine_n), p1 = min(pairs, p0 + mine_n);
-  Cut cut;
-  int64_t tiles = 0;
+  int64_t tiles = 0, total, all;
   for (int p = p0; p < p1; ++p) tiles += tiles_of(kv, pair_count(kv, a, p));
-  int64_t at = scan_before(tiles, sc, &cut.total);
-  cut.parts = pairs <= ctas;
-  int64_t part = 0;
-  if (cut.parts) {
-    // sum of ceil(n / per) <= total / per + pairs <= ctas
-    cut.per = pairs < ctas ? max((cut.total + ctas - pairs - 1) / (ctas - pairs), static_cast<int64_t>(kMinTiles)) : INT64_MAX / 2;
-    int64_t parts = 0, all;
-    for (int p = p0; p < p1; ++p) parts += parts_of(tiles_of(kv, pair_count(kv, a, p)), cut.per);
-    part = scan_before(parts, sc, &all);
-  } else {
-    cut.per = max((cut.total + ctas - 1) / ctas, static_cast<int64_t>(1));
-  }
+  scan_before(tiles, sc, &total);
+  const int room = max(max(ctas - pairs, ctas / 2), 1);
+  const int64_t per = max((total + room - 1) / room, static_cast<int64_t>(kMinTiles));
+  int64_t both = 0;  // parts, and rows of the workspace in the upper half
   for (int p = p0; p < p1; ++p) {
-    const int64_t n = tiles_of(kv, pair_count(kv, a, p));
-    each(cut, p, n, at, part);
-    at += n;
-    if (cut.parts) part += parts_of(n, cut.per);
+    const int k = parts_of(tiles_of(kv, pair_count(kv, a, p)), per);
+    both += k + (k > 1 ? static_cast<int64_t>(k) << 32 : 0);
+  }
+  both = scan_before(both, sc, &all);
+  for (int p = p0; p < p1; ++p) {
+    Pairs n;
+    n.tiles = tiles_of(kv, pair_count(kv, a, p));
+    n.count = parts_of(n.tiles, per);
+    n.part = static_cast<int>(both & 0xffffffff);
+    n.row = static_cast<int>(both >> 32);
+    each(p, n);
+    both += n.count + (n.count > 1 ? static_cast<int64_t>(n.count) << 32 : 0);
   }
   __syncthreads();
-  return cut;
-}
-
-// The rows of the workspace that hold a pair's partial results, in the order of
-// its tiles: row(0) = first, row(i) = second + (i - 1) * step.
-//   parts: CTA c writes row c.
-//   ranges: range c writes row 2c for a pair that is under way at the range's
-//   start or begins there, else row 2c + 1.
-struct Partials {
-  int first, second, step, count;
-  __device__ __forceinline__ int64_t row(int i) const { return i == 0 ? first : second + static_cast<int64_t>(i - 1) * step; }
-};
-__device__ __forceinline__ Partials partials_of(const Cut& cut, int64_t tiles, int64_t start, int64_t part) {
-  Partials r;
-  if (cut.parts) {
-    r.first = static_cast<int>(part);
-    r.second = r.first + 1;
-    r.step = 1;
-    r.count = parts_of(tiles, cut.per);
-  } else {
-    const int c0 = static_cast<int>(start / cut.per), c1 = static_cast<int>((start + tiles - 1) / cut.per);
-    r.first = 2 * c0 + (c0 * cut.per == start ? 0 : 1);
-    r.second = 2 * (c0 + 1);
-    r.step = 2;
-    r.count = c1 - c0 + 1;
-  }
-  return r;
+  return static_cast<int>(all & 0xffffffff);
 }
 
 __device__ __forceinline__ void store_out(const BlockArgs& a, int64_t at, float4 v) {
@@ -250,18 +235,20 @@ __device__ __forceinline__ void store_out(const BlockArgs& a, int64_t at, float4
 // Joins the partial results of a pair, in the order of its tiles, into out /
 // lse.  w: shared memory for G * (count + 2) floats.
 template <int D>
-__device__ void merge_pair(const KvView& kv, const BlockArgs& a, int64_t pair, const Partials& r, float* w) {
+__device__ void merge_pair(const KvView& kv, const BlockArgs& a, int64_t pair, int row0, int count, float* w) {
   const int G = kv.group, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* norm = w + G * r.count;  // per head: 1 / sum of the weights
+  float* norm = w + G * count;  // per head: 1 / sum of the weights
   float* lses = norm + G;
-  for (int i = threadIdx.x; i < G * r.count; i += kThreads) w[i] = __ldcg(a.ws_lse + r.row(i / G) * G + i % G);
+  const float* ws_lse = a.ws_lse + static_cast<int64_t>(row0) * G;
+  const float* ws_o = a.ws_o + static_cast<int64_t>(row0) * G * D;
+  for (int i = threadIdx.x; i < G * count; i += kThreads) w[i] = __ldcg(ws_lse + i);
   __syncthreads();
   for (int h = warp; h < G; h += kWarps) {
     float M = -INFINITY, tot = 0.0f;
-    for (int i = lane; i < r.count; i += 32) M = fmaxf(M, w[i * G + h]);
+    for (int i = lane; i < count; i += 32) M = fmaxf(M, w[i * G + h]);
     M = warp_max(M);
     if (M == -INFINITY) M = 0.0f;  // no token, or only results that are not numbers: those stay so
-    for (int i = lane; i < r.count; i += 32) {
+    for (int i = lane; i < count; i += 32) {
       const float e = expf(w[i * G + h] - M);
       w[i * G + h] = e;
       tot += e;
@@ -276,12 +263,12 @@ __device__ void merge_pair(const KvView& kv, const BlockArgs& a, int64_t pair, c
   const int64_t b = pair / kv.hkv, out_row = b * kv.hq + (pair - b * kv.hkv) * G;
   for (int idx = threadIdx.x; idx < G * (D / 4); idx += kThreads) {
     const int h = idx / (D / 4);
-    const float* src = a.ws_o + 4 * idx;  // a partial result is G * D floats
+    const float* src = ws_o + 4 * idx;  // a partial result is G * D floats
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
-    for (int i = 0; i < r.count; ++i) {
+    for (int i = 0; i < count; ++i) {
       const float e = w[i * G + h];
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(src + r.row(i) * G * D));
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(src + static_cast<int64_t>(i) * G * D));
       acc.x = fmaf(e, v.x, acc.x);
       acc.y = fmaf(e, v.y, acc.y);
       acc.z = fmaf(e, v.z, acc.z);
@@ -309,35 +296,31 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
   __shared__ uint32_t s_live[kWarps][kStages];
   __shared__ float s_m[kWarps][8 * NT], s_l[kWarps][8 * NT];
   __shared__ Scan s_scan;
-  __shared__ int s_last, s_pair, s_empty;
-  __shared__ int64_t s_at;
+  __shared__ Part s_parts[kListed];
+  __shared__ int s_last, s_empty;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {  // (cut_work's barriers come before anyone writes them again)
-    s_pair = -1;
-    s_empty = 0;
-  }
+  if (tid == 0) s_empty = 0;  // (cut_work has barriers before it is set)
   const int g = lane >> 2, c4 = lane & 3;
   const int G = kv.group, B = kv.block;
   const int pairs = kv.batch * kv.hkv, ctas = gridDim.x;
 
-  const Cut cut = cut_work(kv, a, ctas, s_scan, [&](const Cut& c, int p, int64_t n, int64_t at, int64_t part) {
-    if (c.parts) {
-      if (blockIdx.x >= part && blockIdx.x < part + parts_of(n, c.per)) {
-        s_pair = p;
-        s_at = part;
-      }
-    } else {
-      const int64_t t = blockIdx.x * c.per;
-      if (t >= at && t < at + n) {
-        s_pair = p;
-        s_at = at;
-      }
+  int listed = 0;  // parts of this CTA noted so far
+  const auto note = [&](int p, const Pairs& n) {
+    // this CTA's parts among the pair's, the next kListed of them
+    const int me = blockIdx.x;
+    for (int j = n.part + (me + ctas - n.part % ctas) % ctas; j < n.part + n.count; j += ctas) {
+      const int slot = j / ctas - listed;
+      if (slot >= 0 && slot < kListed) s_parts[slot] = Part{p, j - n.part, n.count, n.row};
     }
-    // the CTA numbered like a pair mod the grid answers for it when it is empty
-    if (n == 0 && p % ctas == static_cast<int>(blockIdx.x)) s_empty = 1;
-    if (p % ctas == static_cast<int>(blockIdx.x) && a.sel_count[p] > a.capacity) set_error(err, HS_EBIT_CAPACITY);
+  };
+  const int all_parts = cut_work(kv, a, ctas, s_scan, [&](int p, const Pairs& n) {
+    note(p, n);
+    if (p % ctas == static_cast<int>(blockIdx.x)) {  // the CTA that answers for the pair's count
+      if (n.count == 0) s_empty = 1;
+      if (a.sel_count[p] > a.capacity) set_error(err, HS_EBIT_CAPACITY);
+    }
   });
   if (s_empty) {  // nothing selected: out = 0, lse = -inf
     for (int p = blockIdx.x; p < pairs; p += ctas) {
@@ -347,11 +330,6 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
       if (a.lse && tid < G) a.lse[row + tid] = -INFINITY;
     }
   }
-  int pair = s_pair;
-  if (pair < 0) return;  // no tiles for this CTA
-  int64_t start = s_at;  // parts: the pair's first part; ranges: its first tile
-  int64_t t = cut.parts ? 0 : blockIdx.x * cut.per;  // (ranges) the next tile
-  const int64_t t_end = cut.parts ? 0 : min(cut.total, t + cut.per);
 
   // this lane's 16-byte piece of the first rows a copy instruction covers
   const uint8_t* k_piece = static_cast<const uint8_t*>(kv.k_pages) + (lane / kPieces) * D + 16 * (lane % kPieces);
@@ -359,33 +337,27 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
   uint8_t* my_ring = ring + warp * (kStages * kStageBytes);
   const uint32_t my_ring_addr = smem_addr(my_ring);
 
-  for (;;) {
-    // ---- the segment: tiles [seg0, seg1) of `pair` ----
+  const int my_parts = (all_parts - static_cast<int>(blockIdx.x) + ctas - 1) / ctas;
+  for (int n_part = 0; n_part < my_parts; ++n_part) {
+    if (n_part == listed + kListed) {
+      listed = n_part;
+      cut_work(kv, a, ctas, s_scan, note);
+    }
+    // ---- the part: tiles [seg0, seg1) of `pair` ----
+    const Part part = s_parts[n_part - listed];
+    const int pair = part.pair;
     const int cnt = pair_count(kv, a, pair);
     const int64_t pair_tiles = tiles_of(kv, cnt);
-    if (pair_tiles == 0) {  // (ranges)
-      ++pair;
-      continue;
-    }
-    const Partials parts = partials_of(cut, pair_tiles, start, start);
-    int seg0, seg1, ws_row;
-    if (cut.parts) {
-      const int64_t i = blockIdx.x - start;
-      seg0 = static_cast<int>(i * pair_tiles / parts.count);
-      seg1 = static_cast<int>((i + 1) * pair_tiles / parts.count);
-      ws_row = blockIdx.x * G;
-    } else {
-      seg0 = static_cast<int>(t - start);
-      seg1 = static_cast<int>(min(pair_tiles, t_end - start));
-      ws_row = (2 * static_cast<int>(blockIdx.x) + (blockIdx.x * cut.per >= start ? 0 : 1)) * G;
-    }
+    const int seg0 = static_cast<int>(part.index * pair_tiles / part.count);
+    const int seg1 = static_cast<int>((part.index + 1) * pair_tiles / part.count);
+    const int ws_row = (part.row + part.index) * G;
     const int b = pair / kv.hkv, kvh = pair - b * kv.hkv;
     const int L = kv.seq_lens[b];
     const int nb = min(ceil_div(max(L, 0), B), kv.max_blocks);
     const int32_t* sel = a.sel + static_cast<int64_t>(pair) * a.capacity;
     const int32_t* table = kv.page_table + static_cast<int64_t>(pair) * kv.max_blocks;
 
-    // The warp's tiles: a run of the segment.
+    // The warp's tiles: a run of the part.
     const int run0 = seg0 + static_cast<int>(static_cast<int64_t>(seg1 - seg0) * warp / kWarps);
     const int tiles = seg0 + static_cast<int>(static_cast<int64_t>(seg1 - seg0) * (warp + 1) / kWarps) - run0;
     // Selected blocks are looked up 32 at a time, one to a lane, the pages one
@@ -729,7 +701,7 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
               make_float4(o[nt][i][e] * back, o[nt][i][2 + e] * back, o[nt][i + 1][e] * back, o[nt][i + 1][2 + e] * back);
       }
     __syncthreads();
-    const bool whole = parts.count == 1;
+    const bool whole = part.count == 1;
     for (int idx = tid; idx < G * (D / 4); idx += kThreads) {
       const int h = idx / (D / 4), d = (idx - h * (D / 4)) * 4;
       float M = -INFINITY;
@@ -763,24 +735,18 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
       }
     }
     if (!whole && a.counters) {
-      __threadfence();
       __syncthreads();
       if (tid == 0) {
-        const uint32_t there = atomicAdd(a.counters + pair, 1u);
-        s_last = there == static_cast<uint32_t>(parts.count - 1);
+        // releases what the CTA wrote before the barrier, acquires what the others released
+        uint32_t there;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(there) : "l"(a.counters + pair) : "memory");
+        s_last = there == static_cast<uint32_t>(part.count - 1);
         if (s_last) a.counters[pair] = 0u;
-        __threadfence();
       }
       __syncthreads();
-      if (s_last) merge_pair<D>(kv, a, pair, parts, reinterpret_cast<float*>(ring));
+      if (s_last) merge_pair<D>(kv, a, pair, part.row, part.count, reinterpret_cast<float*>(ring));
     }
-    if (cut.parts || start + seg1 >= t_end) return;
     __syncthreads();  // the ring and s_m are free again
-    t = start + seg1;
-    if (seg1 == pair_tiles) {
-      start += pair_tiles;
-      ++pair;
-    }
   }
 }
 
@@ -790,20 +756,14 @@ template <int D>
 __global__ __launch_bounds__(kThreads) void attn_block_merge_kernel(KvView kv, BlockArgs a, int ctas) {
   extern __shared__ float weights[];
   __shared__ Scan s_scan;
-  __shared__ int64_t s_tiles, s_start, s_part;
+  __shared__ Pairs s_pair;
   pdl_trigger();
   pdl_wait();
   const int pair = blockIdx.x;
-  const Cut cut = cut_work(kv, a, ctas, s_scan, [&](const Cut&, int p, int64_t n, int64_t at, int64_t part) {
-    if (p == pair) {
-      s_tiles = n;
-      s_start = at;
-      s_part = part;
-    }
+  cut_work(kv, a, ctas, s_scan, [&](int p, const Pairs& n) {
+    if (p == pair) s_pair = n;
   });
-  if (s_tiles == 0) return;
-  const Partials r = partials_of(cut, s_tiles, s_start, s_part);
-  if (r.count > 1) merge_pair<D>(kv, a, pair, r, weights);
+  if (s_pair.count > 1) merge_pair<D>(kv, a, pair, s_pair.row, s_pair.count, weights);
 }
 
 template <int D, int NT, bool F32>
@@ -841,7 +801,7 @@ cudaError_t launch_block_attn(const KvView& kv, const AttnArgs& a, unsigned* err
   b.capacity = a.capacity;
   b.out_f32 = a.out_is_fp32;
   b.scale = a.scale;
-  const int ctas = block_attn_ctas(a.sms);
+  const int ctas = a.sms;
   if (kv.head_dim == 128)
     return kv.group <= 8 ? launch_n<128, 1>(kv, b, ctas, err, st) : launch_n<128, 2>(kv, b, ctas, err, st);
   return kv.group <= 8 ? launch_n<64, 1>(kv, b, ctas, err, st) : launch_n<64, 2>(kv, b, ctas, err, st);

@@ -178,6 +178,14 @@ def test_results_do_not_depend_on_the_arrival_order_or_the_number_of_ctas():
         check_attention(c, q, sel, cnt, b, lb)
     b, _ = attend(c, q, sel, cnt, lse=False, bps=5)
     assert torch.equal(a, b)
+    # hundreds of pairs to a CTA, a long one among them
+    c = Cache([1 + 7 * i % 90 for i in range(150)] + [3000], 2, 64, 16, seed=3)
+    q = query(c, 4)
+    sel, cnt = chosen(c, max(c.nb), None)
+    for n in (1, 3, 0):
+        for counters in (True, False):
+            b, lb = attend(c, q, sel, cnt, max_ctas=n, counters=counters)
+            check_attention(c, q, sel, cnt, b, lb)
 
 
 @pytest.mark.parametrize("vscale", [(-30, 4), (-60, -55), (10, 14)])
