@@ -176,6 +176,8 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
+        if torch.cuda.is_initialized():  # the current device's current stream, without building a Stream object
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
     if isinstance(stream, int):
         return stream
@@ -265,37 +267,42 @@ def append_params(cos_sin=None, interleaved=False, new_offsets=None, positions=N
     return p
 
 
-def _rows(t, what):
-    """Address and row stride of a [rows][heads][head_dim] tensor whose rows are contiguous."""
-    if t is None:
-        return None, 0
-    st = t.stride()
-    if len(st) != 3 or (t.shape[0] > 0 and (st[2] != 1 or (st[1] != t.shape[2] and t.shape[1] > 1))):
-        raise ValueError(f"{what} must be [rows][heads][head_dim] with contiguous rows")
-    return t.data_ptr(), st[0]
+_BF16, _F32, _NEW_ROWS = torch.bfloat16, torch.float32, "{} must be [rows][{}][{}] of {} with contiguous rows, on the current device"
+
+
+def _rows(t, heads, dim, dtype, device, what):
+    """Rows, address and row stride of a [rows][heads][dim] tensor whose rows are contiguous."""
+    sh, st = t.shape, t.stride()
+    if (len(sh) != 3 or sh[1] != heads or sh[2] != dim or st[2] != 1 or (st[1] != dim and heads != 1)
+            or t.dtype is not dtype or t.get_device() != device):
+        raise ValueError(_NEW_ROWS.format(what, heads, dim, dtype))
+    return sh[0], t.data_ptr(), st[0] if sh[0] > 1 else heads * dim
 
 
 def hs_append_tokens(shape, kv, params, new_k, new_v, q=None, q_out=None, smin=None, smax=None, stream=None):
     """Any number of new tokens per request into the paged cache, K and Q rotated on the way (see hs.h).  new_k,
     new_v [rows][Hkv][D], q, q_out [rows][Hq][D]; the rows may be strided views (of a fused projection)."""
-    kp, ks = _rows(new_k, "new_k")
-    vp, vs = _rows(new_v, "new_v")
-    qp, qs = _rows(q, "q")
-    op, os_ = _rows(q_out, "q_out")
-    rows = new_k.shape[0]
-    if new_v.shape != new_k.shape or new_k.shape[1:] != (shape.num_kv_heads, shape.head_dim):
-        raise ValueError("new_k and new_v must be [rows][num_kv_heads][head_dim]")
-    if q is not None and (q_out is None or q.shape != q_out.shape
-                          or q.shape != (rows, shape.num_q_heads, shape.head_dim)):
-        raise ValueError("q and q_out must be [rows][num_q_heads][head_dim]")
-    want = torch.float32 if shape.kv_dtype == 0 else torch.bfloat16
-    for t in (new_k, new_v, q, q_out):
-        if t is not None and t.dtype != want:
-            raise ValueError(f"rows must be {want} for this cache, got {t.dtype}")
-    off = params._keep[1]
-    if off is not None and off.numel() != kv.batch + 1:
+    dim, hkv = shape.head_dim, shape.num_kv_heads
+    dtype = _F32 if shape.kv_dtype == 0 else _BF16
+    device = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+    rows, kp, ks = _rows(new_k, hkv, dim, dtype, device, "new_k")
+    v_rows, vp, vs = _rows(new_v, hkv, dim, dtype, device, "new_v")
+    qp = op = None
+    qs = os_ = q_rows = 0
+    if q is not None or q_out is not None:
+        if q is None or q_out is None:
+            raise ValueError("q and q_out are given together")
+        hq = shape.num_q_heads
+        q_rows, qp, qs = _rows(q, hq, dim, dtype, device, "q")
+        o_rows, op, os_ = _rows(q_out, hq, dim, dtype, device, "q_out")
+        if q_rows != rows or o_rows != rows:
+            raise ValueError("q and q_out must have the rows of new_k")
+    if v_rows != rows:
+        raise ValueError("new_v must have the rows of new_k")
+    _, offsets, positions = params._keep
+    if offsets is not None and offsets.numel() != kv.batch + 1:
         raise ValueError("new_offsets must have batch + 1 entries")
-    if params._keep[2] is not None and params._keep[2].numel() < rows:
+    if positions is not None and positions.numel() < rows:
         raise ValueError("positions must have an entry for every row")
     _check(_lib.hs_append_tokens(ctypes.byref(shape), ctypes.byref(kv), ctypes.byref(params), rows, qp, qs, op, os_,
                                  kp, ks, vp, vs, _ptr(smin), _ptr(smax), _stream(stream)),
