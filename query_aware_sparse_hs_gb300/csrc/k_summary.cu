@@ -18,8 +18,6 @@ template <>
 struct Elem<HS_KV_BF16> { static constexpr int kBytes = 2; };
 template <>
 struct Elem<HS_KV_FP8E4M3_G32> { static constexpr int kBytes = 1; };
-template <>
-struct Elem<HS_KV_FP8E4M3_BLOCK> { static constexpr int kBytes = 1; };
 
 // 16 bytes of one row -> min/max of its V channels into mn/mx
 template <int KIND, int V>
@@ -114,8 +112,6 @@ __global__ __launch_bounds__(kWarps * 32) void summaries_kernel(KvView kv, int f
             raw[u] = __ldg(reinterpret_cast<const uint4*>(base + row * (D * E)));
             if constexpr (KIND == HS_KV_FP8E4M3_G32)
               sc[u] = __ldg(kv.k_scales + row * (D / kQuantGroup) + d0 / kQuantGroup);
-            else if constexpr (KIND == HS_KV_FP8E4M3_BLOCK)
-              sc[u] = __ldg(kv.k_scales + page);
             else
               sc[u] = 1.0f;
           }
@@ -190,6 +186,185 @@ cudaError_t launch_k(const KvView& kv, int first_block, int nblocks, void* smin,
   }
 }
 
+// ---- e4m3 with one scale per page ----
+// The scale is the same for the whole block, so min and max are taken over the
+// codes, as f16 pairs (which hold every e4m3 number), and only the two results
+// are scaled: 2 conversions and 4 two-wide comparisons for 4 codes, where the
+// grouped kind needs 4 products and 8 comparisons more.  A lane owns 4
+// neighbouring channels of every row it loads, so the block needs no exchange
+// between lanes (64 channels: one with the other half of the warp), and a warp
+// none with other warps.  The blocks of all requests and kv heads are laid end to
+// end and cut into equal runs, one per warp (every warp sums the requests' block
+// counts); a warp looks up 32 blocks of its run together and loads the next 16
+// rows (64 channels: 32) while it folds the last.
+__device__ __forceinline__ void codes_to_half2(uint32_t w, __half2& a, __half2& b) {
+  uint32_t x, y;
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+      : "=r"(x), "=r"(y)
+      : "r"(w));
+  a = *reinterpret_cast<__half2*>(&x);
+  b = *reinterpret_cast<__half2*>(&y);
+}
+__device__ __forceinline__ __half2 shfl_half2(__half2 v, int off) {
+  const uint32_t x = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<uint32_t*>(&v), off);
+  return *reinterpret_cast<const __half2*>(&x);
+}
+
+constexpr int kBlockCtas = 3;  // CTAs of the kernel per SM
+constexpr int kRows = 16;      // loads in flight
+
+template <int D>
+__global__ __launch_bounds__(kWarps * 32, kBlockCtas) void summaries_block_kernel(KvView kv, int first_block, void* smin,
+                                                                                 void* smax, unsigned* err) {
+  constexpr int RPL = 128 / D;  // rows of one warp load
+  constexpr int kStep = kRows * RPL;
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int rs = lane / (D / 4), d0 = lane % (D / 4) * 4;
+  const int B = kv.block, batch = kv.batch;
+  const auto blocks_of = [&](int b) { return max(min(ceil_div(max(__ldg(kv.seq_lens + b), 0), B), kv.max_blocks) - first_block, 0); };
+
+  // ---- this warp's run [g, g_end) of all blocks, and where it begins ----
+  const int mine_n = (batch + 31) / 32, b0 = min(batch, lane * mine_n), b1 = min(batch, b0 + mine_n);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += blocks_of(b);
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  const int64_t total = __shfl_sync(0xffffffffu, incl, 31) * kv.hkv;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps, w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t per = (total + warps - 1) / warps;
+  int64_t g = w * per;
+  const int64_t g_end = min(total, g + per);
+  if (g >= g_end) return;
+  int req = 0;
+  int64_t before = 0;  // blocks of the requests before req, all kv heads
+  {
+    const unsigned has = __ballot_sync(0xffffffffu, incl * kv.hkv > g);
+    const int owner = __ffs(has) - 1;
+    if (lane == owner) {
+      before = (incl - mine) * kv.hkv;
+      for (req = b0; req < b1 - 1; ++req) {
+        const int64_t n = static_cast<int64_t>(blocks_of(req)) * kv.hkv;
+        if (g < before + n) break;
+        before += n;
+      }
+    }
+    req = __shfl_sync(0xffffffffu, req, owner);
+    before = __shfl_sync(0xffffffffu, before, owner);
+  }
+  int n_req = blocks_of(req);
+  int64_t pair = static_cast<int64_t>(req) * kv.hkv + (g - before) / n_req;
+  int j = first_block + static_cast<int>((g - before) % n_req);
+
+  while (g < g_end) {
+    // ---- up to 32 blocks of one pair ----
+    const int n = static_cast<int>(min(static_cast<int64_t>(min(32, first_block + n_req - j)), g_end - g));
+    const int L = __ldg(kv.seq_lens + req);
+    int my_page = -1;
+    float my_scale = 0.0f;
+    if (lane < n) {
+      my_page = __ldg(kv.page_table + pair * kv.max_blocks + j + lane);
+      if (my_page < 0 || my_page >= kv.num_pages) {
+        set_error(err, HS_EBIT_PAGE_RANGE);
+        my_page = -1;
+      } else {
+        my_scale = __ldg(kv.k_scales + my_page);
+      }
+    }
+    unsigned left = __ballot_sync(0xffffffffu, my_page >= 0);
+    uint32_t raw[kRows], next[kRows];
+    const auto load = [&](uint32_t (&r)[kRows], int i, int t0) {
+      const int page = __shfl_sync(0xffffffffu, my_page, i);
+      const int last = min(B, L - (j + i) * B) - 1;
+      const uint8_t* base = static_cast<const uint8_t*>(kv.k_pages) + static_cast<int64_t>(page) * B * D + d0;
+#pragma unroll
+      for (int u = 0; u < kRows; ++u)  // clamp: a repeated valid row changes nothing
+        r[u] = __ldg(reinterpret_cast<const uint32_t*>(base + min(t0 + u * RPL + rs, last) * D));
+    };
+    __half2 mn[2], mx[2];
+    mn[0] = mn[1] = __half2half2(__ushort_as_half(0x7c00));  // inf
+    mx[0] = mx[1] = __half2half2(__ushort_as_half(0xfc00));
+    int i = left ? __ffs(left) - 1 : 32, t0 = 0;
+    if (left) load(next, i, 0);
+    while (left) {
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) raw[u] = next[u];
+      const int now = i;
+      const bool ends = t0 + kStep >= min(B, L - (j + i) * B);
+      if (ends) {
+        left &= left - 1;
+        i = left ? __ffs(left) - 1 : 32;
+        t0 = 0;
+      } else {
+        t0 += kStep;
+      }
+      if (left) load(next, i, t0);
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        __half2 x, y;
+        codes_to_half2(raw[u], x, y);
+        mn[0] = __hmin2(mn[0], x);
+        mn[1] = __hmin2(mn[1], y);
+        mx[0] = __hmax2(mx[0], x);
+        mx[1] = __hmax2(mx[1], y);
+      }
+      if (ends) {
+        const float scale = __shfl_sync(0xffffffffu, my_scale, now);
+        if constexpr (RPL > 1)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            mn[c] = __hmin2(mn[c], shfl_half2(mn[c], 16));
+            mx[c] = __hmax2(mx[c], shfl_half2(mx[c], 16));
+          }
+        if (rs == 0) {
+          const int64_t o = (pair * kv.max_blocks + j + now) * D + d0;
+          __nv_bfloat162 lo[2], hi[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {  // outward: the stored box still contains every dequantised key
+            const float2 x = __half22float2(mn[c]), y = __half22float2(mx[c]);
+            lo[c].x = __float2bfloat16_rd(x.x * scale);
+            lo[c].y = __float2bfloat16_rd(x.y * scale);
+            hi[c].x = __float2bfloat16_ru(y.x * scale);
+            hi[c].y = __float2bfloat16_ru(y.y * scale);
+          }
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(smin) + o) = *reinterpret_cast<const uint2*>(lo);
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(smax) + o) = *reinterpret_cast<const uint2*>(hi);
+        }
+        mn[0] = mn[1] = __half2half2(__ushort_as_half(0x7c00));
+        mx[0] = mx[1] = __half2half2(__ushort_as_half(0xfc00));
+      }
+    }
+    // ---- on ----
+    g += n;
+    j += n;
+    if (j == first_block + n_req) {
+      j = first_block;
+      ++pair;
+      if (pair == static_cast<int64_t>(req + 1) * kv.hkv && g < g_end) {
+        do {  // the next request with blocks: there is one before g_end
+          ++req;
+          n_req = blocks_of(req);
+        } while (n_req == 0);
+        pair = static_cast<int64_t>(req) * kv.hkv;
+      }
+    }
+  }
+}
+
+template <int D>
+cudaError_t launch_block(const KvView& kv, int first_block, int nblocks, void* smin, void* smax, unsigned* err,
+                         int sms, cudaStream_t st) {
+  // a warp for each block at most
+  const int64_t most = (static_cast<int64_t>(kv.batch) * kv.hkv * nblocks + kWarps - 1) / kWarps;
+  const unsigned grid = static_cast<unsigned>(most < sms * kBlockCtas ? most : sms * kBlockCtas);
+  return launch_pdl(summaries_block_kernel<D>, dim3(grid), dim3(kWarps * 32), 0, st, kv, first_block, smin, smax, err);
+}
+
 template <int D>
 cudaError_t launch_d(const KvView& kv, int first_block, int nblocks, void* smin, void* smax,
                      unsigned* err, int sms, cudaStream_t st) {
@@ -197,7 +372,7 @@ cudaError_t launch_d(const KvView& kv, int first_block, int nblocks, void* smin,
     case HS_KV_F32: return launch_k<D, HS_KV_F32>(kv, first_block, nblocks, smin, smax, err, sms, st);
     case HS_KV_BF16: return launch_k<D, HS_KV_BF16>(kv, first_block, nblocks, smin, smax, err, sms, st);
     case HS_KV_FP8E4M3_G32: return launch_k<D, HS_KV_FP8E4M3_G32>(kv, first_block, nblocks, smin, smax, err, sms, st);
-    default: return launch_k<D, HS_KV_FP8E4M3_BLOCK>(kv, first_block, nblocks, smin, smax, err, sms, st);
+    default: return launch_block<D>(kv, first_block, nblocks, smin, smax, err, sms, st);
   }
 }
 
