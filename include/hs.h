@@ -349,11 +349,12 @@ typedef struct hs_append_params {
  *                All in the source precision (bf16, or f32 for an f32 cache),
  *                16-byte aligned, strides a multiple of 16 bytes.
  *   rows         rows of q, k and v.  Rows at and past new_offsets[batch] (a
- *                padded batch) are neither read nor written.
+ *                padded batch) are not written, and what they hold does not
+ *                matter.
  *   smin, smax   the summaries, or both NULL.
- * A request with more new rows than tokens, or offsets that do not ascend within
- * [0, rows], set HS_EBIT_BLOCK_RANGE and leave the request's cache as it was; so
- * does a block index >= max_blocks, for that block.  A page id outside [0,
+ * Without new_offsets a request of seq_lens 0 has no new token.  A request with
+ * more new rows than tokens, or offsets that do not ascend within [0, rows], set
+ * HS_EBIT_BLOCK_RANGE and leave the request's cache as it was; so does a block index >= max_blocks, for that block.  A page id outside [0,
  * num_pages) sets HS_EBIT_PAGE_RANGE and skips the block; a position outside
  * [0, table_rows) sets HS_EBIT_POSITION and leaves the row's K and Q unwritten.
  * Two requests must not share a page that the call writes to. */

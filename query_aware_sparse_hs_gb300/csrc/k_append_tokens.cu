@@ -14,12 +14,18 @@
 // its relative precision.  Quantisation with one scale is monotone, so the
 // summary of the stored values is the stored image of the rows' min and max.
 //
-// One launch.  A CTA takes one (touched block, kv head, K or V): it owns the
-// page and its scale, so nothing is exchanged between CTAs and there are no
-// atomics.  The other CTAs rotate Q, one warp per row and 16 heads, so that the
-// row's cos and sin are read once for 16 heads.  A thread holds 16 channels of a
-// row as two vectors of 8 chosen so that both members of every rotated pair are
-// its own.  Memory-bound (prompts) or latency-bound (single tokens).
+// A thread holds 16 channels of a row as two vectors of 8 chosen so that both
+// members of every rotated pair are its own.  One launch either way:
+//   any number of rows per request: a CTA takes one (touched block, kv head, K or
+//     V).  It owns the page and its scale, so CTAs exchange nothing and there are
+//     no atomics; the rows of pages up to 64 tokens are read once and held in
+//     registers while the scale is found.  Other CTAs, mixed in evenly, rotate Q:
+//     a warp takes 16 heads of a few consecutive rows, and reads a row's cos and
+//     sin once for the 16.  Memory-bound.
+//   one row per request: the D / 16 threads of a row take its K and V, so a warp
+//     holds several (request, kv head) pairs; the row's thread holds the channels
+//     of the summary too, and nothing is exchanged but the row's largest value.
+//     Latency-bound: seq_lens, page table, then everything else at once.
 #include <float.h>
 
 #include "hs_internal.h"
@@ -46,15 +52,17 @@ __device__ __forceinline__ int last_not_above(int n, int64_t x, int lane, F key)
   return lo;
 }
 
-template <bool F32>
+// Eight f32 or bf16 values.  INPUT: nothing in the kernel writes them.
+template <bool F32, bool INPUT = true>
 __device__ __forceinline__ void load8(const void* p, int64_t at, float (&x)[8]) {
   if constexpr (F32) {
     const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-    const float4 u = __ldg(s), w = __ldg(s + 1);
+    const float4 u = INPUT ? __ldg(s) : s[0], w = INPUT ? __ldg(s + 1) : s[1];
     x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
     x[4] = w.x; x[5] = w.y; x[6] = w.z; x[7] = w.w;
   } else {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at));
+    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+    const uint4 u = INPUT ? __ldg(s) : *s;
     const uint32_t r[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -150,51 +158,178 @@ __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const Angle
   }
 }
 
-template <int D, bool F32>
-__device__ void rotate_q(const KvView& kv, const AppendTokensArgs& a, int64_t unit, int lane, unsigned* err) {
-  constexpr int TPR = D / 16, HPP = 32 / TPR;  // threads per head, heads per step
-  const int chunks = ceil_div(kv.hq, kQHeads);
-  const int64_t row = unit / chunks;
-  if (row >= a.rows) return;
-  const int h0 = static_cast<int>(unit - row * chunks) * kQHeads;
-  int b = static_cast<int>(row);
+// CTAs for the touched blocks: with offsets, request b's blocks have the slots
+// from offsets[b] / B + 2 b on.
+int64_t kv_units_of(const KvView& kv, const AppendTokensArgs& a) {
+  return (a.rows / kv.block + 2 * static_cast<int64_t>(kv.batch)) * kv.hkv * 2;
+}
+// Rows a warp rotates 16 heads of: more than one only where there are warps
+// enough without that.
+int q_rows_of(const KvView& kv, const AppendTokensArgs& a) {
+  return a.offsets && a.rows * ceil_div(kv.hq, kQHeads) >= 32768 ? 4 : 1;
+}
+int64_t q_units_of(const KvView& kv, const AppendTokensArgs& a) {
+  const int n = q_rows_of(kv, a);
+  return a.q ? (a.rows + n - 1) / n * ceil_div(kv.hq, kQHeads) : 0;
+}
+
+// Request of new row `row` and its position in the cache; false: no such row.
+__device__ __forceinline__ bool place_of_row(const KvView& kv, const AppendTokensArgs& a, int64_t row, int b, int64_t* p) {
   int64_t behind = 1;  // tokens from this row's to the end of its request
   if (a.offsets) {
-    b = last_not_above(kv.batch, row, lane, [&](int i) { return static_cast<int64_t>(__ldg(a.offsets + i)); });
-    const int64_t o0 = a.offsets[b], o1 = a.offsets[b + 1];
-    if (row < o0 || row >= o1 || o1 > a.rows) return;  // behind the last request, or offsets reported by the K and V units
-    if (o1 - o0 > kv.seq_lens[b]) return;
+    const int64_t o0 = __ldg(a.offsets + b), o1 = __ldg(a.offsets + b + 1);
+    // behind the last request, or offsets that the K and V units report
+    if (row < o0 || row >= o1 || o1 > a.rows || o1 - o0 > __ldg(kv.seq_lens + b)) return false;
     behind = o1 - row;
   }
-  const int64_t p = static_cast<int64_t>(kv.seq_lens[b]) - behind;
-  if (p < 0) return;
-  const int64_t pos = a.positions ? a.positions[row] : p;
-  if (a.rotary > 0 && (pos < 0 || pos >= a.table_rows)) {
-    if (lane == 0) set_error(err, HS_EBIT_POSITION);
-    return;
-  }
+  *p = static_cast<int64_t>(__ldg(kv.seq_lens + b)) - behind;
+  return *p >= 0;
+}
+
+// kQHeads heads of rows [row, row_end).
+template <int D, bool F32>
+__device__ void rotate_q(const KvView& kv, const AppendTokensArgs& a, int h0, int64_t row, int64_t row_end, int lane,
+                         unsigned* err) {
+  constexpr int TPR = D / 16, HPP = 32 / TPR, N = kQHeads / HPP;  // threads per head, heads per step, steps
   const int s = lane % TPR;
   const Slot t = slot_of(s, a.rotary, a.interleaved);
-  Angles ang;
-  if (t.rotated) load_angles(a.cos_sin, a.rotary, pos, s, ang);
-  const int64_t in = row * a.q_stride, out = row * a.q_out_stride;
+  int b = static_cast<int>(row);
+  bool found = a.offsets == nullptr;
+  for (; row < row_end; ++row) {
+    float x[N][8], y[N][8];
+    const int64_t in = row * a.q_stride, out = row * a.q_out_stride;
 #pragma unroll
-  for (int i = 0; i < kQHeads / HPP; ++i) {
-    const int h = h0 + i * HPP + lane / TPR;
-    if (h < kv.hq) {
-      float x[8], y[8];
-      load8<F32>(a.q, in + h * D + t.ca, x);
-      load8<F32>(a.q, in + h * D + t.cb, y);
-      if (t.rotated) rotate(x, y, ang, a.interleaved);
-      store8<F32>(a.q_out, out + h * D + t.ca, x);
-      store8<F32>(a.q_out, out + h * D + t.cb, y);
+    for (int i = 0; i < N; ++i) {  // read ahead of everything that takes lookups
+      const int h = min(h0 + i * HPP + lane / TPR, kv.hq - 1);
+      load8<F32>(a.q, in + h * D + t.ca, x[i]);
+      load8<F32>(a.q, in + h * D + t.cb, y[i]);
+    }
+    if (!found) {
+      b = last_not_above(kv.batch, row, lane, [&](int i) { return static_cast<int64_t>(__ldg(a.offsets + i)); });
+      found = true;
+    } else if (a.offsets) {
+      while (b + 1 < kv.batch && row >= __ldg(a.offsets + b + 1)) ++b;
+    } else {
+      b = static_cast<int>(row);
+    }
+    int64_t p;
+    if (!place_of_row(kv, a, row, b, &p)) continue;
+    const int64_t pos = a.positions ? __ldg(a.positions + row) : p;
+    if (a.rotary > 0 && (pos < 0 || pos >= a.table_rows)) {
+      if (lane == 0) set_error(err, HS_EBIT_POSITION);
+      continue;
+    }
+    Angles ang;
+    if (t.rotated) load_angles(a.cos_sin, a.rotary, pos, s, ang);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int h = h0 + i * HPP + lane / TPR;
+      if (t.rotated) rotate(x[i], y[i], ang, a.interleaved);
+      if (h < kv.hq) {
+        store8<F32>(a.q_out, out + h * D + t.ca, x[i]);
+        store8<F32>(a.q_out, out + h * D + t.cb, y[i]);
+      }
     }
   }
 }
 
+// 16 codes of a row, as both formats of e4m3 store them: the encoded values and
+// (box) the values they stand for.
+__device__ __forceinline__ void decode8(uint2 c, float s, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = e4m3x2_to_float2(static_cast<uint16_t>((i < 2 ? c.x : c.y) >> (16 * (i & 1))));
+    x[2 * i] = f.x * s;
+    x[2 * i + 1] = f.y * s;
+  }
+}
+
+// The grouped format: every 32-channel group its own scale (amax / 448).  A row's
+// TPR neighbouring threads call it together; `part` is their D / 32 words of
+// shared memory.  Stores the codes and scales and leaves in u, w what they stand
+// for.
+template <int D>
+__device__ __forceinline__ void store_grouped(void* pages, float* scales, int64_t row, int s, const Slot& t, bool live,
+                                              unsigned* part, float (&u)[8], float (&w)[8]) {
+  if (s < D / kQuantGroup) part[s] = 0u;
+  __syncwarp();
+  if (live) {
+    float p = 0.0f, q = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      p = fmaxf(p, fabsf(u[c]));
+      q = fmaxf(q, fabsf(w[c]));
+    }
+    atomicMax(&part[t.ca / kQuantGroup], __float_as_uint(p));  // a maximum: the order does not matter
+    atomicMax(&part[t.cb / kQuantGroup], __float_as_uint(q));
+  }
+  __syncwarp();
+  if (live) {
+    const float ga = __uint_as_float(part[t.ca / kQuantGroup]), gb = __uint_as_float(part[t.cb / kQuantGroup]);
+    const float sa = ga > 0.0f ? ga / 448.0f : 1.0f, sb = gb > 0.0f ? gb / 448.0f : 1.0f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {  // IEEE division, as the quantiser of whole rows does
+      u[c] = u[c] / sa;
+      w[c] = w[c] / sb;
+    }
+    uint8_t* dst = static_cast<uint8_t*>(pages) + row * D;
+    const uint2 cu = encode8(u, 1.0f), cw = encode8(w, 1.0f);
+    *reinterpret_cast<uint2*>(dst + t.ca) = cu;
+    *reinterpret_cast<uint2*>(dst + t.cb) = cw;
+    if (s < D / kQuantGroup) {
+      const float g = __uint_as_float(part[s]);
+      scales[row * (D / kQuantGroup) + s] = g > 0.0f ? g / 448.0f : 1.0f;
+    }
+    decode8(cu, sa, u);
+    decode8(cw, sb, w);
+  }
+  __syncwarp();
+}
+
+// Stores a row of an f32 or bf16 cache and leaves in u, w what it holds.
 template <int D, int KIND>
-__global__ __launch_bounds__(kThreads) void append_tokens_kernel(KvView kv, AppendTokensArgs a, int64_t kv_units,
-                                                                 unsigned* err) {
+__device__ __forceinline__ void store_plain(void* pages, int64_t row, const Slot& t, float (&u)[8], float (&w)[8]) {
+  store8<KIND == HS_KV_F32>(pages, row * D + t.ca, u);
+  store8<KIND == HS_KV_F32>(pages, row * D + t.cb, w);
+  if constexpr (KIND == HS_KV_BF16) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      u[c] = __bfloat162float(__float2bfloat16_rn(u[c]));
+      w[c] = __bfloat162float(__float2bfloat16_rn(w[c]));
+    }
+  }
+}
+
+// Largest finite magnitude among the values, and m.
+__device__ __forceinline__ float widen_finite(float m, const float (&u)[8], const float (&w)[8]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const float p = fabsf(u[c]), q = fabsf(w[c]);
+    m = fmaxf(m, p <= FLT_MAX ? p : 0.0f);
+    m = fmaxf(m, q <= FLT_MAX ? q : 0.0f);
+  }
+  return m;
+}
+
+// 16 codes times f (a page whose scale grows)
+__device__ __forceinline__ uint4 rescaled(uint4 v, float f) {
+  const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+  uint32_t out[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const float2 lo = e4m3x2_to_float2(static_cast<uint16_t>(in[c])), hi = e4m3x2_to_float2(static_cast<uint16_t>(in[c] >> 16));
+    out[c] = __nv_cvt_float2_to_fp8x2(make_float2(lo.x * f, lo.y * f), __NV_SATFINITE, __NV_E4M3) |
+             static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(hi.x * f, hi.y * f), __NV_SATFINITE, __NV_E4M3)) << 16;
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// ---- any number of rows per request ----
+// P: passes of the CTA over its rows that are read together (and, block-scaled,
+// held until the scale is known).
+template <int D, int KIND, int P>
+__global__ __launch_bounds__(kThreads) void append_rows_kernel(KvView kv, AppendTokensArgs a, int64_t kv_units,
+                                                               int64_t q_units, int q_rows, unsigned* err) {
   constexpr bool F32 = KIND == HS_KV_F32;
   constexpr int TPR = D / 16, RPP = kThreads / TPR;  // threads per row, rows per pass
   __shared__ float s_mn[kWarps][D], s_mx[kWarps][D];
@@ -204,41 +339,35 @@ __global__ __launch_bounds__(kThreads) void append_tokens_kernel(KvView kv, Appe
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (static_cast<int64_t>(blockIdx.x) >= kv_units) {
-    rotate_q<D, F32>(kv, a, (blockIdx.x - kv_units) * kWarps + warp, lane, err);
+  // ---- K and V units and Q units, mixed evenly over the grid ----
+  const int64_t ctas = gridDim.x, unit = static_cast<int64_t>(blockIdx.x) * kv_units / ctas;
+  if ((static_cast<int64_t>(blockIdx.x) + 1) * kv_units / ctas == unit) {
+    const int64_t q = (blockIdx.x - unit) * kWarps + warp;
+    if (q >= q_units) return;
+    const int chunks = ceil_div(kv.hq, kQHeads);
+    const int64_t r = q / chunks;
+    rotate_q<D, F32>(kv, a, static_cast<int>(q - r * chunks) * kQHeads, r * q_rows, min(a.rows, (r + 1) * q_rows), lane, err);
     return;
   }
   // ---- which block ----
-  const bool is_k = (blockIdx.x & 1) == 0;
-  const int64_t rest = blockIdx.x >> 1;
-  const int64_t slot = rest / kv.hkv;
-  const int kvh = static_cast<int>(rest - slot * kv.hkv);
+  const bool is_k = (unit & 1) == 0;
+  const int64_t slot = (unit >> 1) / kv.hkv;
+  const int kvh = static_cast<int>((unit >> 1) - slot * kv.hkv);
   const int B = kv.block;
-  int b = static_cast<int>(slot);
-  int64_t o0 = slot;
-  int n = 1, x = 0;
-  if (a.offsets) {
-    // request b has the slots from offsets[b] / B + 2 b on: enough for every
-    // block its rows can touch, wherever in a block they begin
-    b = last_not_above(kv.batch, slot, lane, [&](int i) { return static_cast<int64_t>(__ldg(a.offsets + i)) / B + 2 * i; });
-    o0 = a.offsets[b];
-    const int64_t o1 = a.offsets[b + 1];
-    if (o0 < 0 || o1 < o0 || o1 > a.rows) {
-      if (tid == 0) set_error(err, HS_EBIT_BLOCK_RANGE);
-      return;
-    }
-    n = static_cast<int>(o1 - o0);
-    x = static_cast<int>(slot - (o0 / B + 2 * static_cast<int64_t>(b)));
-    if (x < 0) return;
-  }
-  const int L = kv.seq_lens[b];
-  if (n <= 0 || L <= 0) return;
-  if (n > L) {
+  // request b has the slots from offsets[b] / B + 2 b on: enough for every block
+  // its rows can touch, wherever in a block they begin
+  const int b = last_not_above(kv.batch, slot, lane, [&](int i) { return static_cast<int64_t>(__ldg(a.offsets + i)) / B + 2 * i; });
+  const int64_t o0 = __ldg(a.offsets + b), o1 = __ldg(a.offsets + b + 1);
+  const int L = __ldg(kv.seq_lens + b);
+  if (o0 < 0 || o1 < o0 || o1 > a.rows || o1 - o0 > max(L, 0)) {
     if (tid == 0) set_error(err, HS_EBIT_BLOCK_RANGE);
     return;
   }
+  const int n = static_cast<int>(o1 - o0);
+  const int64_t x = slot - (o0 / B + 2 * static_cast<int64_t>(b));
+  if (x < 0 || n == 0) return;
   const int first = L - n;  // cache position of the request's first new row
-  const int64_t j64 = static_cast<int64_t>(first / B) + x;
+  const int64_t j64 = first / B + x;
   if (j64 > (L - 1) / B) return;
   const int j = static_cast<int>(j64);
   const int64_t pair = static_cast<int64_t>(b) * kv.hkv + kvh;
@@ -261,29 +390,37 @@ __global__ __launch_bounds__(kThreads) void append_tokens_kernel(KvView kv, Appe
   const int rotary = is_k ? a.rotary : 0;
   const bool box = is_k && a.smin != nullptr;
   const int s = tid % TPR, rs = tid / TPR;
-  const Slot t = slot_of(s, rotary, a.interleaved);
+  const Slot t = slot_of(s, a.rotary, a.interleaved);
 
-  // the rotated channels of page row r; false where the position has no table row
-  auto fetch = [&](int r, float (&u)[8], float (&w)[8]) {
-    const int64_t sr = src0 + r;
-    if (rotary > 0) {
-      const int64_t pos = a.positions ? a.positions[sr] : static_cast<int64_t>(j) * B + r;
-      if (pos < 0 || pos >= a.table_rows) {
-        set_error(err, HS_EBIT_POSITION);
-        return false;
-      }
-      load8<F32>(src, sr * stride + kvh * D + t.ca, u);
-      load8<F32>(src, sr * stride + kvh * D + t.cb, w);
-      if (t.rotated) {
-        Angles ang;
-        load_angles(a.cos_sin, rotary, pos, s, ang);
-        rotate(u, w, ang, a.interleaved);
-      }
-    } else {
-      load8<F32>(src, sr * stride + kvh * D + t.ca, u);
-      load8<F32>(src, sr * stride + kvh * D + t.cb, w);
+  float u[P][8], w[P][8];
+  // The rotated channels of page rows r0 + i RPP + rs; bit i of the answer: the
+  // row is there and its position has angles.
+  const auto fetch = [&](int r0) {
+    unsigned live = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {  // every load before the first use; rows past the end repeat the last
+      const int64_t sr = src0 + min(r0 + i * RPP + rs, rb - 1);
+      load8<F32>(src, sr * stride + kvh * D + t.ca, u[i]);
+      load8<F32>(src, sr * stride + kvh * D + t.cb, w[i]);
     }
-    return true;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int r = min(r0 + i * RPP + rs, rb - 1);
+      bool ok = r0 + i * RPP + rs < rb;
+      if (rotary > 0) {
+        const int64_t pos = a.positions ? __ldg(a.positions + src0 + r) : static_cast<int64_t>(j) * B + r;
+        if (pos < 0 || pos >= a.table_rows) {
+          if (ok) set_error(err, HS_EBIT_POSITION);
+          ok = false;
+        } else if (t.rotated) {
+          Angles ang;
+          load_angles(a.cos_sin, rotary, pos, s, ang);
+          rotate(u[i], w[i], ang, a.interleaved);
+        }
+      }
+      live |= static_cast<unsigned>(ok) << i;
+    }
+    return live;
   };
 
   float mn[16], mx[16];
@@ -292,85 +429,32 @@ __global__ __launch_bounds__(kThreads) void append_tokens_kernel(KvView kv, Appe
     mn[c] = INFINITY;
     mx[c] = -INFINITY;
   }
-  auto widen = [&](const float (&u)[8], const float (&w)[8]) {
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      mn[c] = fminf(mn[c], u[c]);
-      mx[c] = fmaxf(mx[c], u[c]);
-      mn[8 + c] = fminf(mn[8 + c], w[c]);
-      mx[8 + c] = fmaxf(mx[8 + c], w[c]);
-    }
-  };
   bool any = false;
   float amax = 0.0f;
-  const int passes = ceil_div(rb - ra, RPP);
-  for (int i = 0; i < passes; ++i) {
-    const int r = ra + i * RPP + rs;
-    float u[8], w[8];
-    const bool live = r < rb && fetch(r, u, w);
-    any |= live;
-    if constexpr (KIND == HS_KV_FP8E4M3_G32) {
-      // the row's threads are neighbours in one warp
-      if (s < D / kQuantGroup) s_group[rs][s] = 0u;
-      __syncwarp();
-      if (live) {
-        float p = 0.0f, q = 0.0f;
+  unsigned live = 0;
+  for (int r0 = ra; r0 < rb; r0 += P * RPP) {
+    live = fetch(r0);
+    any |= live != 0;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          p = fmaxf(p, fabsf(u[c]));
-          q = fmaxf(q, fabsf(w[c]));
-        }
-        atomicMax(&s_group[rs][t.ca / kQuantGroup], __float_as_uint(p));
-        atomicMax(&s_group[rs][t.cb / kQuantGroup], __float_as_uint(q));
-      }
-      __syncwarp();
-      if (live) {
-        const float ga = __uint_as_float(s_group[rs][t.ca / kQuantGroup]);
-        const float gb = __uint_as_float(s_group[rs][t.cb / kQuantGroup]);
-        const float sa = ga > 0.0f ? ga / 448.0f : 1.0f, sb = gb > 0.0f ? gb / 448.0f : 1.0f;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {  // IEEE division, as the quantiser of whole rows does
-          u[c] = u[c] / sa;
-          w[c] = w[c] / sb;
-        }
-        uint8_t* dst = static_cast<uint8_t*>(pages) + (row0 + r) * D;
-        const uint2 cu = encode8(u, 1.0f), cw = encode8(w, 1.0f);
-        *reinterpret_cast<uint2*>(dst + t.ca) = cu;
-        *reinterpret_cast<uint2*>(dst + t.cb) = cw;
-        if (s < D / kQuantGroup) {
-          const float g = __uint_as_float(s_group[rs][s]);
-          scales[(row0 + r) * (D / kQuantGroup) + s] = g > 0.0f ? g / 448.0f : 1.0f;
-        }
-        if (box) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            u[c] = decode1((c < 4 ? cu.x : cu.y) >> (8 * (c & 3)) & 0xffu) * sa;
-            w[c] = decode1((c < 4 ? cw.x : cw.y) >> (8 * (c & 3)) & 0xffu) * sb;
-          }
-          widen(u, w);
-        }
-      }
-      __syncwarp();
-    } else if (live) {
-      if constexpr (KIND == HS_KV_FP8E4M3_BLOCK) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const float p = fabsf(u[c]), q = fabsf(w[c]);
-          amax = fmaxf(amax, p <= FLT_MAX ? p : 0.0f);
-          amax = fmaxf(amax, q <= FLT_MAX ? q : 0.0f);
-        }
+    for (int i = 0; i < P; ++i) {
+      const int64_t row = row0 + r0 + i * RPP + rs;
+      const bool on = (live >> i) & 1u;
+      if constexpr (KIND == HS_KV_FP8E4M3_G32) {
+        store_grouped<D>(pages, scales, row, s, t, on, s_group[rs], u[i], w[i]);
+      } else if constexpr (KIND == HS_KV_FP8E4M3_BLOCK) {
+        if (on) amax = widen_finite(amax, u[i], w[i]);
       } else {
-        store8<F32>(pages, (row0 + r) * D + t.ca, u);
-        store8<F32>(pages, (row0 + r) * D + t.cb, w);
-        if constexpr (KIND == HS_KV_BF16) {
+        if (on) store_plain<D, KIND>(pages, row, t, u[i], w[i]);
+      }
+      if (box && on) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            u[c] = __bfloat162float(__float2bfloat16_rn(u[c]));
-            w[c] = __bfloat162float(__float2bfloat16_rn(w[c]));
-          }
+        for (int c = 0; c < 8; ++c) {
+          mn[c] = fminf(mn[c], u[i][c]);
+          mx[c] = fmaxf(mx[c], u[i][c]);
+          mn[8 + c] = fminf(mn[8 + c], w[i][c]);
+          mx[8 + c] = fmaxf(mx[8 + c], w[i][c]);
         }
       }
-      if (box) widen(u, w);
     }
   }
 
@@ -389,31 +473,24 @@ __global__ __launch_bounds__(kThreads) void append_tokens_kernel(KvView kv, Appe
       if (!grown) scale = held;
     }
     inv = 1.0f / scale;
-    if (grown) {
-      // the rows already there, at the new scale
+    if (grown) {  // the rows already there, at the new scale
       const float f = held > 0.0f ? held * inv : 0.0f;
       for (int r = rs; r < ra; r += RPP) {
         uint4* p = reinterpret_cast<uint4*>(static_cast<uint8_t*>(pages) + (row0 + r) * D + 16 * s);
-        const uint4 old = *p;
-        const uint32_t in[4] = {old.x, old.y, old.z, old.w};
-        uint32_t out[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float2 lo = e4m3x2_to_float2(static_cast<uint16_t>(in[c])), hi = e4m3x2_to_float2(static_cast<uint16_t>(in[c] >> 16));
-          out[c] = __nv_cvt_float2_to_fp8x2(make_float2(lo.x * f, lo.y * f), __NV_SATFINITE, __NV_E4M3) |
-                   static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(hi.x * f, hi.y * f), __NV_SATFINITE, __NV_E4M3)) << 16;
-        }
-        *p = make_uint4(out[0], out[1], out[2], out[3]);
+        *p = rescaled(*p, f);
       }
     }
     if (tid == 0 && (ra == 0 || grown)) scales[page] = scale;
-    for (int i = 0; i < passes; ++i) {  // the rows again (from the caches), as codes
-      const int r = ra + i * RPP + rs;
-      float u[8], w[8];
-      if (r < rb && fetch(r, u, w)) {
-        uint8_t* dst = static_cast<uint8_t*>(pages) + (row0 + r) * D;
-        *reinterpret_cast<uint2*>(dst + t.ca) = encode8(u, inv);
-        *reinterpret_cast<uint2*>(dst + t.cb) = encode8(w, inv);
+    const bool again = rb - ra > P * RPP;  // more rows than are held: read once more, from the caches
+    for (int r0 = ra; r0 < rb; r0 += P * RPP) {
+      if (again) live = fetch(r0);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        if ((live >> i) & 1u) {
+          uint8_t* dst = static_cast<uint8_t*>(pages) + (row0 + r0 + i * RPP + rs) * D;
+          *reinterpret_cast<uint2*>(dst + t.ca) = encode8(u[i], inv);
+          *reinterpret_cast<uint2*>(dst + t.cb) = encode8(w[i], inv);
+        }
       }
     }
   }
@@ -479,39 +556,224 @@ __global__ __launch_bounds__(kThreads) void append_tokens_kernel(KvView kv, Appe
   }
 }
 
-template <int D>
-cudaError_t launch_d(const KvView& kv, const AppendTokensArgs& a, int64_t kv_units, unsigned grid, unsigned* err,
-                     cudaStream_t st) {
-  const dim3 g(grid), t(kThreads);
-  switch (kv.kv_dtype) {
-    case HS_KV_F32: return launch_pdl(append_tokens_kernel<D, HS_KV_F32>, g, t, 0, st, kv, a, kv_units, err);
-    case HS_KV_BF16: return launch_pdl(append_tokens_kernel<D, HS_KV_BF16>, g, t, 0, st, kv, a, kv_units, err);
-    case HS_KV_FP8E4M3_G32: return launch_pdl(append_tokens_kernel<D, HS_KV_FP8E4M3_G32>, g, t, 0, st, kv, a, kv_units, err);
-    default: return launch_pdl(append_tokens_kernel<D, HS_KV_FP8E4M3_BLOCK>, g, t, 0, st, kv, a, kv_units, err);
+// ---- one row per request ----
+// Eight channels of a summary row, widened to lo / hi (or started afresh).
+template <bool F32>
+__device__ __forceinline__ void widen_box(void* smin, void* smax, int64_t at, bool keep, float (&lo)[8], float (&hi)[8]) {
+  if (keep) {
+    float p[8], q[8];
+    load8<F32, false>(smin, at, p);
+    load8<F32, false>(smax, at, q);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      lo[c] = fminf(p[c], lo[c]);
+      hi[c] = fmaxf(q[c], hi[c]);
+    }
+  }
+  store8<F32>(smin, at, lo);
+  store8<F32>(smax, at, hi);
+}
+
+template <int D, int KIND>
+__global__ __launch_bounds__(kThreads) void append_one_kernel(KvView kv, AppendTokensArgs a, int kv_ctas, unsigned* err) {
+  constexpr bool F32 = KIND == HS_KV_F32;
+  constexpr int TPR = D / 16, RPC = kThreads / TPR;  // threads per row, rows per CTA
+  __shared__ unsigned s_group[RPC][D / kQuantGroup];
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (static_cast<int>(blockIdx.x) >= kv_ctas) {
+    const int64_t q = static_cast<int64_t>(blockIdx.x - kv_ctas) * kWarps + warp;
+    const int chunks = ceil_div(kv.hq, kQHeads);
+    const int64_t row = q / chunks;
+    if (row < a.rows) rotate_q<D, F32>(kv, a, static_cast<int>(q - row * chunks) * kQHeads, row, row + 1, lane, err);
+    return;
+  }
+  const int s = tid % TPR, rs = tid / TPR;
+  const int pairs = kv.batch * kv.hkv;
+  const int pair = static_cast<int>(blockIdx.x) * RPC + rs;
+  const int b = min(pair, pairs - 1) / kv.hkv, kvh = min(pair, pairs - 1) - b * kv.hkv;
+  const Slot t = slot_of(s, a.rotary, a.interleaved);
+  // the row itself needs no lookup
+  float ku[8], kw[8], vu[8], vw[8];
+  load8<F32>(a.k, b * a.k_stride + kvh * D + t.ca, ku);
+  load8<F32>(a.k, b * a.k_stride + kvh * D + t.cb, kw);
+  load8<F32>(a.v, b * a.v_stride + kvh * D + t.ca, vu);
+  load8<F32>(a.v, b * a.v_stride + kvh * D + t.cb, vw);
+  const int B = kv.block, L = __ldg(kv.seq_lens + b);
+  const int p = L - 1, j = p / B, r = p - j * B;
+  bool live = pair < pairs && L > 0, live_k = false;
+  int page = 0;
+  if (live) {
+    if (j >= kv.max_blocks) {
+      set_error(err, HS_EBIT_BLOCK_RANGE);
+      live = false;
+    } else {
+      page = __ldg(kv.page_table + static_cast<int64_t>(pair) * kv.max_blocks + j);
+      if (page < 0 || page >= kv.num_pages) {
+        set_error(err, HS_EBIT_PAGE_RANGE);
+        live = false;
+      }
+    }
+  }
+  if (live) {
+    live_k = true;
+    if (a.rotary > 0) {
+      const int64_t pos = a.positions ? __ldg(a.positions + b) : p;
+      if (pos < 0 || pos >= a.table_rows) {
+        set_error(err, HS_EBIT_POSITION);
+        live_k = false;
+      } else if (t.rotated) {
+        Angles ang;
+        load_angles(a.cos_sin, a.rotary, pos, s, ang);
+        rotate(ku, kw, ang, a.interleaved);
+      }
+    }
+  }
+  const int64_t row0 = static_cast<int64_t>(page) * B, row = row0 + r;
+  void* kp = const_cast<void*>(kv.k_pages);
+  void* vp = const_cast<void*>(kv.v_pages);
+  float* ks = const_cast<float*>(kv.k_scales);
+  float* vs = const_cast<float*>(kv.v_scales);
+  const bool box = a.smin != nullptr;
+
+  if constexpr (KIND == HS_KV_FP8E4M3_G32) {
+    store_grouped<D>(kp, ks, row, s, t, live_k, s_group[rs], ku, kw);
+    store_grouped<D>(vp, vs, row, s, t, live, s_group[rs], vu, vw);
+  } else if constexpr (KIND == HS_KV_FP8E4M3_BLOCK) {
+    float lo[16], hi[16];  // box of the earlier rows, channels 16 s and up, where their codes change
+    // The page's scale, the codes and the earlier rows' codes where the scale
+    // grows (false); afterwards u, w are what is held.
+    const auto store_block = [&](void* pages, float* scales, bool on, bool boxes, float (&u)[8], float (&w)[8]) {
+      float amax = on ? widen_finite(0.0f, u, w) : 0.0f;
+#pragma unroll
+      for (int o = TPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      bool kept = true;
+      if (on) {
+        const float held = r > 0 ? scales[page] : 0.0f;
+        float scale = block_scale(amax);
+        const bool grown = r > 0 && !(held >= scale);  // (a scale that is not a number is replaced)
+        if (r > 0 && !grown) scale = held;
+        const float inv = 1.0f / scale;
+        if (grown) {
+          const float f = held > 0.0f ? held * inv : 0.0f;
+          kept = false;
+#pragma unroll 4
+          for (int i = 0; i < r; ++i) {
+            uint4* at = reinterpret_cast<uint4*>(static_cast<uint8_t*>(pages) + (row0 + i) * D + 16 * s);
+            const uint4 c = rescaled(*at, f);
+            *at = c;
+            if (boxes) {
+              float x[8], y[8];
+              decode8(make_uint2(c.x, c.y), scale, x);
+              decode8(make_uint2(c.z, c.w), scale, y);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                lo[e] = fminf(lo[e], x[e]);
+                hi[e] = fmaxf(hi[e], x[e]);
+                lo[8 + e] = fminf(lo[8 + e], y[e]);
+                hi[8 + e] = fmaxf(hi[8 + e], y[e]);
+              }
+            }
+          }
+        }
+        uint8_t* dst = static_cast<uint8_t*>(pages) + row * D;
+        const uint2 cu = encode8(u, inv), cw = encode8(w, inv);
+        *reinterpret_cast<uint2*>(dst + t.ca) = cu;
+        *reinterpret_cast<uint2*>(dst + t.cb) = cw;
+        decode8(cu, scale, u);
+        decode8(cw, scale, w);
+        __syncwarp(((1u << TPR) - 1u) << (lane / TPR * TPR));  // every thread of the row has read the old scale
+        if (s == 0 && (r == 0 || grown)) scales[page] = scale;
+      }
+      return kept;
+    };
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      lo[c] = INFINITY;
+      hi[c] = -INFINITY;
+    }
+    const bool kept = store_block(kp, ks, live_k, box, ku, kw);
+    store_block(vp, vs, live, false, vu, vw);
+    if (live_k && box && !kept) {
+      // the earlier rows' box lies by 16 neighbouring channels to a thread: it
+      // goes down first, and the row widens it like any other
+      const int64_t at = (static_cast<int64_t>(pair) * kv.max_blocks + j) * D + 16 * s;
+      float x[8], y[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          x[c] = __bfloat162float(__float2bfloat16_rd(lo[8 * h + c]));
+          y[c] = __bfloat162float(__float2bfloat16_ru(hi[8 * h + c]));
+        }
+        widen_box<false>(a.smin, a.smax, at + 8 * h, false, x, y);
+      }
+    }
+    __syncwarp();
+  } else {
+    if (live_k) store_plain<D, KIND>(kp, row, t, ku, kw);
+    if (live) store_plain<D, KIND>(vp, row, t, vu, vw);
+  }
+  if (!box || !live_k) return;
+  const int64_t at = (static_cast<int64_t>(pair) * kv.max_blocks + j) * D;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float x[8], y[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float v = h ? kw[c] : ku[c];
+      // NaN: nothing to widen.  bf16: outward, exact for values that are bf16 already
+      x[c] = isnan(v) ? INFINITY : F32 ? v : __bfloat162float(__float2bfloat16_rd(v));
+      y[c] = isnan(v) ? -INFINITY : F32 ? v : __bfloat162float(__float2bfloat16_ru(v));
+    }
+    widen_box<F32>(a.smin, a.smax, at + (h ? t.cb : t.ca), r > 0, x, y);
   }
 }
 
-// CTAs for the touched blocks: with offsets, request b's blocks have the slots
-// from offsets[b] / B + 2 b on.
-int64_t append_units(const KvView& kv, const AppendTokensArgs& a) {
-  const int64_t slots = a.offsets ? a.rows / kv.block + 2 * static_cast<int64_t>(kv.batch) : kv.batch;
-  return slots * kv.hkv * 2;
+template <int D, int KIND, int P>
+cudaError_t launch_rows(const KvView& kv, const AppendTokensArgs& a, int64_t kv_units, unsigned* err, cudaStream_t st) {
+  const int64_t q_units = q_units_of(kv, a);
+  const int64_t ctas = kv_units + (q_units + kWarps - 1) / kWarps;
+  return launch_pdl(append_rows_kernel<D, KIND, P>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, st, kv, a,
+                    kv_units, q_units, q_rows_of(kv, a), err);
 }
-int64_t append_q_ctas(const KvView& kv, const AppendTokensArgs& a) {
-  return a.q ? (a.rows * ceil_div(kv.hq, kQHeads) + kWarps - 1) / kWarps : 0;
+
+template <int D, int KIND>
+cudaError_t launch_k(const KvView& kv, const AppendTokensArgs& a, unsigned* err, cudaStream_t st) {
+  if (!a.offsets) {
+    const int kv_ctas = static_cast<int>((static_cast<int64_t>(kv.batch) * kv.hkv + kThreads / (D / 16) - 1) / (kThreads / (D / 16)));
+    const int64_t ctas = kv_ctas + (q_units_of(kv, a) + kWarps - 1) / kWarps;
+    return launch_pdl(append_one_kernel<D, KIND>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, st, kv, a, kv_ctas,
+                      err);
+  }
+  constexpr int RPP = kThreads / (D / 16);
+  const int64_t units = kv_units_of(kv, a);
+  if (kv.block <= RPP) return launch_rows<D, KIND, 1>(kv, a, units, err, st);
+  if (kv.block <= 2 * RPP) return launch_rows<D, KIND, 2>(kv, a, units, err, st);
+  return launch_rows<D, KIND, 4>(kv, a, units, err, st);
+}
+
+template <int D>
+cudaError_t launch_d(const KvView& kv, const AppendTokensArgs& a, unsigned* err, cudaStream_t st) {
+  switch (kv.kv_dtype) {
+    case HS_KV_F32: return launch_k<D, HS_KV_F32>(kv, a, err, st);
+    case HS_KV_BF16: return launch_k<D, HS_KV_BF16>(kv, a, err, st);
+    case HS_KV_FP8E4M3_G32: return launch_k<D, HS_KV_FP8E4M3_G32>(kv, a, err, st);
+    default: return launch_k<D, HS_KV_FP8E4M3_BLOCK>(kv, a, err, st);
+  }
 }
 
 }  // namespace
 
 bool append_tokens_fits(const KvView& kv, const AppendTokensArgs& a) {
-  return append_units(kv, a) + append_q_ctas(kv, a) <= INT32_MAX;
+  return static_cast<int64_t>(kv.batch) * kv.hkv <= INT32_MAX &&
+         (a.offsets ? kv_units_of(kv, a) : 0) + a.rows * ceil_div(kv.hq, kQHeads) <= INT32_MAX;
 }
 
 cudaError_t launch_append_tokens(const KvView& kv, const AppendTokensArgs& a, unsigned* err, cudaStream_t st) {
-  const int64_t units = append_units(kv, a), ctas = units + append_q_ctas(kv, a);
   if (kv.batch == 0 || a.rows == 0) return cudaSuccess;
-  return kv.head_dim == 128 ? launch_d<128>(kv, a, units, static_cast<unsigned>(ctas), err, st)
-                            : launch_d<64>(kv, a, units, static_cast<unsigned>(ctas), err, st);
+  return kv.head_dim == 128 ? launch_d<128>(kv, a, err, st) : launch_d<64>(kv, a, err, st);
 }
 
 }  // namespace hs
