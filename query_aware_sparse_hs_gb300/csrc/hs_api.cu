@@ -446,7 +446,7 @@ hs_status hs_append_tokens(const hs_attn_shape* shape, const hs_paged_kv* kv, co
   if (!append_tokens_fits(view, a)) return HS_ERR_UNSUPPORTED;
   Device d;
   if ((st = current_device(&d)) != HS_OK) return st;
-  return from_cuda(launch_append_tokens(view, a, d.err, reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_append_tokens(view, a, d.sms, d.err, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 hs_status hs_score_select_topk(const hs_attn_shape* shape, const hs_paged_kv* kv, const void* q,

@@ -77,7 +77,8 @@ struct AppendTokensArgs {
   void* smax;
 };
 bool append_tokens_fits(const KvView& kv, const AppendTokensArgs& a);
-cudaError_t launch_append_tokens(const KvView& kv, const AppendTokensArgs& a, unsigned* err, cudaStream_t st);
+cudaError_t launch_append_tokens(const KvView& kv, const AppendTokensArgs& a, int sms, unsigned* err,
+                                 cudaStream_t st);
 cudaError_t launch_summaries(const KvView& kv, int first_block, void* smin, void* smax,
                              unsigned* err, int sms, cudaStream_t st);
 cudaError_t launch_score_select(const KvView& kv, const SelectArgs& a, unsigned* err,

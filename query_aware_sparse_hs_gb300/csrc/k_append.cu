@@ -155,7 +155,7 @@ cudaError_t launch_append(const KvView& kv, const void* new_k, const void* new_v
     a.rows = kv.batch;
     a.smin = smin;
     a.smax = smax;
-    return launch_append_tokens(kv, a, err, st);
+    return launch_append_tokens(kv, a, 0, err, st);  // (one row per request: the SM count is not asked for)
   }
   return kv.head_dim == 128 ? launch_c<4>(kv, new_k, new_v, smin, smax, err, st)
                             : launch_c<2>(kv, new_k, new_v, smin, smax, err, st);

@@ -36,6 +36,8 @@
 // partial outputs are fp32.
 #include <limits.h>
 
+#include <atomic>
+
 #include "hs_internal.h"
 
 namespace hs {
@@ -769,7 +771,15 @@ __global__ __launch_bounds__(kThreads) void attn_block_merge_kernel(KvView kv, B
 template <int D, int NT, bool F32>
 cudaError_t launch_o(const KvView& kv, const BlockArgs& b, int ctas, unsigned* err, cudaStream_t st) {
   auto kern = attn_block_kernel<D, NT, F32>;
-  if (cudaError_t e = allow_dynamic_smem(kern, ring_bytes<D>()); e != cudaSuccess) return e;
+  // the attribute stays with the device: asked for once
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+    if (cudaError_t e = allow_dynamic_smem(kern, ring_bytes<D>()); e != cudaSuccess) return e;
+    allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(kThreads), ring_bytes<D>(), st, kv, b, err);
   if (e != cudaSuccess || b.counters) return e;
   const size_t smem = static_cast<size_t>(ctas + 2) * kv.group * sizeof(float);

@@ -167,7 +167,7 @@ def _check(status: int, where: str):
 
 
 def _ptr(t) -> int | None:
-    if t is None or isinstance(t, int):  # None, or an address already
+    if t is None or t.__class__ is int:  # None, or an address already
         return t
     if not t.is_contiguous():
         raise ValueError("tensor arguments must be contiguous")
@@ -264,49 +264,53 @@ def append_params(cos_sin=None, interleaved=False, new_offsets=None, positions=N
     p = AppendParams(_ptr(new_offsets), _ptr(positions), _ptr(cos_sin),
                      0 if cos_sin is None else int(cos_sin.shape[0]), int(rotary_dim), 1 if interleaved else 0)
     p._keep = (cos_sin, new_offsets, positions)
+    p._requests = None if new_offsets is None else new_offsets.numel() - 1
+    p._rows = None if positions is None else positions.numel()
     return p
 
 
-_BF16, _F32, _NEW_ROWS = torch.bfloat16, torch.float32, "{} must be [rows][{}][{}] of {} with contiguous rows, on the current device"
+_NEW_ROWS = "{} must be [{}][{}][{}] of {} with contiguous rows, on the current device"
 
 
-def _rows(t, heads, dim, dtype, device, what):
-    """Rows, address and row stride of a [rows][heads][dim] tensor whose rows are contiguous."""
-    sh, st = t.shape, t.stride()
-    if (len(sh) != 3 or sh[1] != heads or sh[2] != dim or st[2] != 1 or (st[1] != dim and heads != 1)
-            or t.dtype is not dtype or t.get_device() != device):
-        raise ValueError(_NEW_ROWS.format(what, heads, dim, dtype))
-    return sh[0], t.data_ptr(), st[0] if sh[0] > 1 else heads * dim
+def _new_rows(t, rows, heads, dim, dtype, device, what):
+    """Address and row stride of a [rows][heads][dim] tensor whose rows are contiguous."""
+    n, h, d = t.shape
+    s, sh, sd = t.stride()
+    if (n != rows or h != heads or d != dim or sd != 1 or (sh != dim and heads != 1) or t.dtype is not dtype
+            or t.get_device() != device):
+        raise ValueError(_NEW_ROWS.format(what, rows, heads, dim, dtype))
+    return t.data_ptr(), s if n > 1 else heads * dim
 
 
 def hs_append_tokens(shape, kv, params, new_k, new_v, q=None, q_out=None, smin=None, smax=None, stream=None):
     """Any number of new tokens per request into the paged cache, K and Q rotated on the way (see hs.h).  new_k,
     new_v [rows][Hkv][D], q, q_out [rows][Hq][D]; the rows may be strided views (of a fused projection)."""
-    dim, hkv = shape.head_dim, shape.num_kv_heads
-    dtype = _F32 if shape.kv_dtype == 0 else _BF16
-    device = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
-    rows, kp, ks = _rows(new_k, hkv, dim, dtype, device, "new_k")
-    v_rows, vp, vs = _rows(new_v, hkv, dim, dtype, device, "new_v")
-    qp = op = None
-    qs = os_ = q_rows = 0
-    if q is not None or q_out is not None:
-        if q is None or q_out is None:
-            raise ValueError("q and q_out are given together")
+    dim, hkv, rows = shape.head_dim, shape.num_kv_heads, new_k.shape[0]
+    dtype = torch.float32 if shape.kv_dtype == 0 else torch.bfloat16
+    device = torch._C._cuda_getDevice() if new_k.is_cuda else -2
+    kp, ks = _new_rows(new_k, rows, hkv, dim, dtype, device, "new_k")
+    vp, vs = _new_rows(new_v, rows, hkv, dim, dtype, device, "new_v")
+    if q is not None and q_out is not None:
         hq = shape.num_q_heads
-        q_rows, qp, qs = _rows(q, hq, dim, dtype, device, "q")
-        o_rows, op, os_ = _rows(q_out, hq, dim, dtype, device, "q_out")
-        if q_rows != rows or o_rows != rows:
-            raise ValueError("q and q_out must have the rows of new_k")
-    if v_rows != rows:
-        raise ValueError("new_v must have the rows of new_k")
-    _, offsets, positions = params._keep
-    if offsets is not None and offsets.numel() != kv.batch + 1:
+        qp, qs = _new_rows(q, rows, hq, dim, dtype, device, "q")
+        op, os_ = _new_rows(q_out, rows, hq, dim, dtype, device, "q_out")
+    elif q is None and q_out is None:
+        qp = op = None
+        qs = os_ = 0
+    else:
+        raise ValueError("q and q_out are given together")
+    if params._requests is not None and params._requests != kv.batch:
         raise ValueError("new_offsets must have batch + 1 entries")
-    if positions is not None and positions.numel() < rows:
+    if params._rows is not None and params._rows < rows:
         raise ValueError("positions must have an entry for every row")
-    _check(_lib.hs_append_tokens(ctypes.byref(shape), ctypes.byref(kv), ctypes.byref(params), rows, qp, qs, op, os_,
-                                 kp, ks, vp, vs, _ptr(smin), _ptr(smax), _stream(stream)),
-           "hs_append_tokens")
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif stream.__class__ is not int:
+        stream = stream.cuda_stream
+    st = _lib.hs_append_tokens(ctypes.byref(shape), ctypes.byref(kv), ctypes.byref(params), rows, qp, qs, op, os_, kp, ks,
+                               vp, vs, _ptr(smin), _ptr(smax), stream)
+    if st:
+        raise HSError(st, "hs_append_tokens")
 
 
 def hs_score_select_topk(shape, kv, q, smin, smax, params, sel, sel_count, scores=None,
