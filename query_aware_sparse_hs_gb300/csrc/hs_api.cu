@@ -290,7 +290,9 @@ hs_status prepare_attn(const hs_attn_shape* shape, const hs_paged_kv* kv, const 
   const bool ranges = *use_tc && shape->kv_dtype == HS_KV_FP8E4M3_BLOCK;
   if (ranges && (static_cast<int64_t>(kv->batch) * shape->num_kv_heads > INT32_MAX ||
                  kv->num_pages * shape->block_size > UINT32_MAX ||  // rows are numbered in 32 bits
-                 static_cast<int64_t>(capacity) * shape->block_size > INT32_MAX))
+                 static_cast<int64_t>(capacity) * shape->block_size > INT32_MAX ||
+                 // (a pair's 32-token tiles, and all pairs' together)
+                 (static_cast<int64_t>(capacity) * shape->block_size / 32 + 1) * kv->batch * shape->num_kv_heads > INT32_MAX))
     return HS_ERR_UNSUPPORTED;
   split_geometry(shape, kv->batch, capacity, params, ctas, &a.blocks_per_split, &a.splits, *use_tc ? &a : nullptr);
   const int bctas = block_ctas(ctas, params);

@@ -141,8 +141,8 @@ __device__ __forceinline__ int pair_count(const KvView& kv, const BlockArgs& a, 
   const int c = __ldg(a.sel_count + p);
   return min(max(c, 0), a.capacity);
 }
-__device__ __forceinline__ int64_t tiles_of(const KvView& kv, int count) {
-  return (static_cast<int64_t>(count) * kv.block + kTile - 1) / kTile;
+__device__ __forceinline__ int tiles_of(const KvView& kv, int count) {  // (the host saw that all of them fit)
+  return static_cast<int>((static_cast<uint32_t>(count) * kv.block + kTile - 1) / kTile);
 }
 
 // Every pair is cut into equal parts of at most `per` tiles; the parts of all
@@ -159,17 +159,18 @@ struct Part {
   int row;           // workspace row of the pair's first part
 };
 struct Pairs {  // one pair's numbers
-  int64_t tiles;
+  int tiles;
   int part, count, row;  // its first part, how many, workspace row of the first
 };
 constexpr int kListed = 32;  // parts a CTA notes at a time
 
-__device__ __forceinline__ int parts_of(int64_t tiles, int64_t per) {
-  return tiles <= kWholeTiles ? (tiles > 0 ? 1 : 0) : static_cast<int>((tiles + per - 1) / per);
+__device__ __forceinline__ int parts_of(int tiles, int per) {
+  return tiles <= kWholeTiles ? (tiles > 0 ? 1 : 0) : (tiles + per - 1) / per;
 }
 
 struct Scan {
   int64_t sums[kWarps];
+  int tiles[kWarps];
 };
 // Sum over the CTA's threads before this one, and over all of them.
 __device__ __forceinline__ int64_t scan_before(int64_t mine, Scan& sc, int64_t* total) {
@@ -188,9 +189,17 @@ __device__ __forceinline__ int64_t scan_before(int64_t mine, Scan& sc, int64_t* 
     if (w == warp) before = all;
     all += sc.sums[w];
   }
-  __syncthreads();
   *total = all;
   return before + incl - mine;
+}
+__device__ __forceinline__ int sum_over_cta(int mine, Scan& sc) {
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if ((threadIdx.x & 31) == 0) sc.tiles[threadIdx.x >> 5] = mine;
+  __syncthreads();
+  int all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) all += sc.tiles[w];
+  return all;
 }
 
 // Cuts this call's pairs; every thread of a CTA calls it.  each(p, numbers) sees
@@ -200,12 +209,12 @@ template <typename F>
 __device__ int cut_work(const KvView& kv, const BlockArgs& a, int ctas, Scan& sc, F&& each) {
   const int pairs = kv.batch * kv.hkv, mine_n = (pairs + kThreads - 1) / kThreads;
   const int p0 = min(pairs, static_cast<int>(threadIdx.x) * mine_n), p1 = min(pairs, p0 + mine_n);
-  int64_t tiles = 0, total, all;
+  int tiles = 0;
   for (int p = p0; p < p1; ++p) tiles += tiles_of(kv, pair_count(kv, a, p));
-  scan_before(tiles, sc, &total);
+  const int total = sum_over_cta(tiles, sc);
   const int room = max(max(ctas - pairs, ctas / 2), 1);
-  const int64_t per = max((total + room - 1) / room, static_cast<int64_t>(kMinTiles));
-  int64_t both = 0;  // parts, and rows of the workspace in the upper half
+  const int per = max((total - 1) / room + 1, kMinTiles);
+  int64_t both = 0, all;  // parts, and rows of the workspace in the upper half
   for (int p = p0; p < p1; ++p) {
     const int k = parts_of(tiles_of(kv, pair_count(kv, a, p)), per);
     both += k + (k > 1 ? static_cast<int64_t>(k) << 32 : 0);
@@ -235,14 +244,30 @@ __device__ __forceinline__ void store_out(const BlockArgs& a, int64_t at, float4
 }
 
 // Joins the partial results of a pair, in the order of its tiles, into out /
-// lse.  w: shared memory for G * (count + 2) floats.
-template <int D>
+// lse.  w: shared memory for G * (count + 2) floats.  The first results are on
+// their way while their weights are found.
+template <int D, int NT>
 __device__ void merge_pair(const KvView& kv, const BlockArgs& a, int64_t pair, int row0, int count, float* w) {
+  constexpr int NI = NT * 8 * D / 4 / kThreads;  // 16-byte pieces of a result per thread, at most
+  constexpr int U = 8 / NI;                      // results in flight
   const int G = kv.group, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* norm = w + G * count;  // per head: 1 / sum of the weights
   float* lses = norm + G;
   const float* ws_lse = a.ws_lse + static_cast<int64_t>(row0) * G;
-  const float* ws_o = a.ws_o + static_cast<int64_t>(row0) * G * D;
+  const float4* ws_o = reinterpret_cast<const float4*>(a.ws_o + static_cast<int64_t>(row0) * G * D);
+  const int pieces = G * (D / 4);
+  float4 next[U][NI];
+  const auto load = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+#pragma unroll
+      for (int n = 0; n < NI; ++n) {
+        const int idx = threadIdx.x + n * kThreads;
+        next[k][n] = i0 + k < count && idx < pieces ? __ldcg(ws_o + static_cast<int64_t>(i0 + k) * pieces + idx)
+                                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+  };
+  load(0);
   for (int i = threadIdx.x; i < G * count; i += kThreads) w[i] = __ldcg(ws_lse + i);
   __syncthreads();
   for (int h = warp; h < G; h += kWarps) {
@@ -262,22 +287,35 @@ __device__ void merge_pair(const KvView& kv, const BlockArgs& a, int64_t pair, i
     }
   }
   __syncthreads();
+  float4 acc[NI];
+#pragma unroll
+  for (int n = 0; n < NI; ++n) acc[n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int i0 = 0; i0 < count; i0 += U) {
+    float4 now[U][NI];
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+#pragma unroll
+      for (int n = 0; n < NI; ++n) now[k][n] = next[k][n];
+    if (i0 + U < count) load(i0 + U);
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+#pragma unroll
+      for (int n = 0; n < NI; ++n) {
+        const int idx = threadIdx.x + n * kThreads;
+        const float e = i0 + k < count && idx < pieces ? w[(i0 + k) * G + idx / (D / 4)] : 0.0f;
+        acc[n].x = fmaf(e, now[k][n].x, acc[n].x);
+        acc[n].y = fmaf(e, now[k][n].y, acc[n].y);
+        acc[n].z = fmaf(e, now[k][n].z, acc[n].z);
+        acc[n].w = fmaf(e, now[k][n].w, acc[n].w);
+      }
+  }
   const int64_t b = pair / kv.hkv, out_row = b * kv.hq + (pair - b * kv.hkv) * G;
-  for (int idx = threadIdx.x; idx < G * (D / 4); idx += kThreads) {
-    const int h = idx / (D / 4);
-    const float* src = ws_o + 4 * idx;  // a partial result is G * D floats
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-    for (int i = 0; i < count; ++i) {
-      const float e = w[i * G + h];
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(src + static_cast<int64_t>(i) * G * D));
-      acc.x = fmaf(e, v.x, acc.x);
-      acc.y = fmaf(e, v.y, acc.y);
-      acc.z = fmaf(e, v.z, acc.z);
-      acc.w = fmaf(e, v.w, acc.w);
-    }
-    const float n = norm[h];
-    store_out(a, out_row * D + 4 * idx, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n));
+#pragma unroll
+  for (int n = 0; n < NI; ++n) {
+    const int idx = threadIdx.x + n * kThreads;
+    if (idx >= pieces) continue;
+    const float s = norm[idx / (D / 4)];
+    store_out(a, out_row * D + 4 * idx, make_float4(acc[n].x * s, acc[n].y * s, acc[n].z * s, acc[n].w * s));
   }
   if (a.lse && threadIdx.x < G) a.lse[out_row + threadIdx.x] = lses[threadIdx.x];
 }
@@ -349,19 +387,31 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
     const Part part = s_parts[n_part - listed];
     const int pair = part.pair;
     const int cnt = pair_count(kv, a, pair);
-    const int64_t pair_tiles = tiles_of(kv, cnt);
-    const int seg0 = static_cast<int>(part.index * pair_tiles / part.count);
-    const int seg1 = static_cast<int>((part.index + 1) * pair_tiles / part.count);
+    const int pair_tiles = tiles_of(kv, cnt), each = pair_tiles / part.count, more = pair_tiles - each * part.count;
+    const int seg0 = part.index * each + min(part.index, more), seg_tiles = each + (part.index < more ? 1 : 0);
     const int ws_row = (part.row + part.index) * G;
     const int b = pair / kv.hkv, kvh = pair - b * kv.hkv;
     const int L = kv.seq_lens[b];
     const int nb = min(ceil_div(max(L, 0), B), kv.max_blocks);
+    // the query's loads go out ahead of the rows'
+    uint4 q_raw[NT][kChunks][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) {
+        q_raw[nt][k][0] = q_raw[nt][k][1] = make_uint4(0u, 0u, 0u, 0u);
+        if (nt * 8 + g < G) {
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                            (static_cast<int64_t>(b) * kv.hq + kvh * G + nt * 8 + g) * D + 64 * k + 16 * c4);
+          q_raw[nt][k][0] = __ldg(src);
+          q_raw[nt][k][1] = __ldg(src + 1);
+        }
+      }
     const int32_t* sel = a.sel + static_cast<int64_t>(pair) * a.capacity;
     const int32_t* table = kv.page_table + static_cast<int64_t>(pair) * kv.max_blocks;
 
     // The warp's tiles: a run of the part.
-    const int run0 = seg0 + static_cast<int>(static_cast<int64_t>(seg1 - seg0) * warp / kWarps);
-    const int tiles = seg0 + static_cast<int>(static_cast<int64_t>(seg1 - seg0) * (warp + 1) / kWarps) - run0;
+    const int run0 = seg0 + seg_tiles * warp / kWarps, tiles = seg0 + seg_tiles * (warp + 1) / kWarps - run0;
     // Selected blocks are looked up 32 at a time, one to a lane, the pages one
     // window ahead of the copies and the selection two, so that neither load is
     // waited for.  A window holds the entries from that of its first tile on;
@@ -477,25 +527,17 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
     float qs[NT][2];  // logit factor of heads 2 c4, 2 c4 + 1 (log2 units)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int h = nt * 8 + g;
       float x[kChunks][16];
       float amax = 0.0f;
 #pragma unroll
       for (int k = 0; k < kChunks; ++k) {
-        if (h < G) {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                                            (static_cast<int64_t>(b) * kv.hq + kvh * G + h) * D + 64 * k + 16 * c4);
-          const uint4 v0 = __ldg(src), v1 = __ldg(src + 1);
-          const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        const uint4 v0 = q_raw[nt][k][0], v1 = q_raw[nt][k][1];
+        const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[k][2 * i] = __uint_as_float(w[i] << 16);
-            x[k][2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            amax = fmaxf(amax, fmaxf(fabsf(x[k][2 * i]), fabsf(x[k][2 * i + 1])));
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[k][i] = 0.0f;
+        for (int i = 0; i < 8; ++i) {
+          x[k][2 * i] = __uint_as_float(w[i] << 16);
+          x[k][2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+          amax = fmaxf(amax, fmaxf(fabsf(x[k][2 * i]), fabsf(x[k][2 * i + 1])));
         }
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
@@ -571,13 +613,24 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
 
       // logits (log2 units), their maximum over the tile
       float kr[4], vr[4];
-      bool ok[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = 8 * i + token_of<D>(g);
         kr[i] = ks[r];
         vr[i] = vs[r];
-        ok[i] = (live >> r) & 1u;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          s[i >> 1][nt][2 * (i & 1)] *= kr[i];  // (times qs: the logit)
+          s[i >> 1][nt][2 * (i & 1) + 1] *= kr[i];
+        }
+      }
+      if (live != 0xffffffffu) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!((live >> (8 * i + token_of<D>(g))) & 1u)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) s[i >> 1][nt][2 * (i & 1)] = s[i >> 1][nt][2 * (i & 1) + 1] = -INFINITY;
+          }
       }
       bool raised = false;
       float mn[NT][2];
@@ -587,11 +640,7 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
         for (int e = 0; e < 2; ++e) {
           float top = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float& x = s[i >> 1][nt][2 * (i & 1) + e];
-            x = ok[i] ? x * kr[i] : -INFINITY;  // (times qs: the logit)
-            top = fmaxf(top, x);
-          }
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, s[i >> 1][nt][2 * (i & 1) + e]);
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -746,7 +795,7 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
         if (s_last) a.counters[pair] = 0u;
       }
       __syncthreads();
-      if (s_last) merge_pair<D>(kv, a, pair, part.row, part.count, reinterpret_cast<float*>(ring));
+      if (s_last) merge_pair<D, NT>(kv, a, pair, part.row, part.count, reinterpret_cast<float*>(ring));
     }
     __syncthreads();  // the ring and s_m are free again
   }
@@ -754,7 +803,7 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
 
 // The merge as a launch of its own, for callers without split counters.  CTA =
 // pair.
-template <int D>
+template <int D, int NT>
 __global__ __launch_bounds__(kThreads) void attn_block_merge_kernel(KvView kv, BlockArgs a, int ctas) {
   extern __shared__ float weights[];
   __shared__ Scan s_scan;
@@ -765,7 +814,7 @@ __global__ __launch_bounds__(kThreads) void attn_block_merge_kernel(KvView kv, B
   cut_work(kv, a, ctas, s_scan, [&](int p, const Pairs& n) {
     if (p == pair) s_pair = n;
   });
-  if (s_pair.count > 1) merge_pair<D>(kv, a, pair, s_pair.row, s_pair.count, weights);
+  if (s_pair.count > 1) merge_pair<D, NT>(kv, a, pair, s_pair.row, s_pair.count, weights);
 }
 
 template <int D, int NT, bool F32>
@@ -783,7 +832,7 @@ cudaError_t launch_o(const KvView& kv, const BlockArgs& b, int ctas, unsigned* e
   cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(kThreads), ring_bytes<D>(), st, kv, b, err);
   if (e != cudaSuccess || b.counters) return e;
   const size_t smem = static_cast<size_t>(ctas + 2) * kv.group * sizeof(float);
-  auto merge = attn_block_merge_kernel<D>;
+  auto merge = attn_block_merge_kernel<D, NT>;
   if ((e = allow_dynamic_smem(merge, smem)) != cudaSuccess) return e;
   return launch_pdl(merge, dim3(kv.batch * kv.hkv), dim3(kThreads), smem, st, kv, b, ctas);
 }
