@@ -170,14 +170,10 @@ size_t workspace_for(const hs_attn_shape* s, int batch, int splits) {
 }
 
 // The same for the kernel of block-scaled e4m3, which cuts the work by the
-// actual counts: its CTAs (as many as fit the GPU, or max_ctas), and two partial
-// results for each.
-int block_ctas(int sms, const hs_attn_params* p) {
-  return p && p->max_ctas > 0 && p->max_ctas <= sms ? p->max_ctas : block_attn_ctas(sms);
-}
+// actual counts.
 size_t block_workspace(const hs_attn_shape* s, int ctas) {
-  const size_t bytes = block_attn_workspace(ctas, s->num_q_heads / s->num_kv_heads, s->head_dim);
-  return (bytes + 255) & ~static_cast<size_t>(255);
+  const size_t rows = static_cast<size_t>(block_attn_rows(ctas, s->head_dim)) * (s->num_q_heads / s->num_kv_heads);
+  return (rows * (s->head_dim + 1) * sizeof(float) + 255) & ~static_cast<size_t>(255);
 }
 
 // Partial workspace an attention call may need: the larger of the uniform
@@ -190,7 +186,7 @@ size_t attn_workspace_need(const hs_attn_shape* s, int batch, int capacity, cons
   AttnArgs t;
   split_geometry(s, batch, capacity, p, ctas, &bps, &splits, &t);
   size_t tc = workspace_for(s, batch, splits);
-  if (s->kv_dtype == HS_KV_FP8E4M3_BLOCK) tc = block_workspace(s, block_ctas(ctas, p));
+  if (s->kv_dtype == HS_KV_FP8E4M3_BLOCK) tc = block_workspace(s, ctas);
   return uniform > tc ? uniform : tc;
 }
 
@@ -287,18 +283,17 @@ hs_status prepare_attn(const hs_attn_shape* shape, const hs_paged_kv* kv, const 
     *use_tc = attn_tc_supported(v);
   }
   AttnArgs& a = *out_args;
-  const bool ranges = *use_tc && shape->kv_dtype == HS_KV_FP8E4M3_BLOCK;
-  if (ranges && (static_cast<int64_t>(kv->batch) * shape->num_kv_heads > INT32_MAX ||
+  const bool by_counts = *use_tc && shape->kv_dtype == HS_KV_FP8E4M3_BLOCK;
+  if (by_counts && (static_cast<int64_t>(kv->batch) * shape->num_kv_heads > INT32_MAX ||
                  kv->num_pages * shape->block_size > UINT32_MAX ||  // rows are numbered in 32 bits
                  static_cast<int64_t>(capacity) * shape->block_size > INT32_MAX ||
                  // (a pair's 32-token tiles, and all pairs' together)
                  (static_cast<int64_t>(capacity) * shape->block_size / 32 + 1) * kv->batch * shape->num_kv_heads > INT32_MAX))
     return HS_ERR_UNSUPPORTED;
   split_geometry(shape, kv->batch, capacity, params, ctas, &a.blocks_per_split, &a.splits, *use_tc ? &a : nullptr);
-  const int bctas = block_ctas(ctas, params);
-  const size_t need = ranges ? block_workspace(shape, bctas) : workspace_for(shape, kv->batch, a.splits);
+  const size_t need = by_counts ? block_workspace(shape, ctas) : workspace_for(shape, kv->batch, a.splits);
   if (need > 0 && (!workspace || ws_bytes < need || !aligned(workspace, 16))) return HS_ERR_WORKSPACE;
-  a.sms = ranges ? bctas : ctas;
+  a.sms = ctas;
   if (params->split_counters && !aligned(params->split_counters, 4)) return HS_ERR_INVALID_ARG;
   a.counters = params->split_counters;
   a.wait_ns = static_cast<uint64_t>(params->wait_limit_ns);
@@ -312,7 +307,7 @@ hs_status prepare_attn(const hs_attn_shape* shape, const hs_paged_kv* kv, const 
   a.out = out;
   a.lse = lse_opt;
   a.ws_o = static_cast<float*>(workspace);
-  a.ws_lse = a.ws_o + (ranges ? static_cast<size_t>(bctas) * 2 * v.group
+  a.ws_lse = a.ws_o + (by_counts ? static_cast<size_t>(block_attn_rows(ctas, v.head_dim)) * v.group
                               : static_cast<size_t>(kv->batch) * shape->num_q_heads * a.splits) *
                           shape->head_dim;
   return HS_OK;

@@ -95,13 +95,10 @@ cudaError_t launch_attn_simt(const KvView& kv, const AttnArgs& a, unsigned* err,
 cudaError_t launch_attn_tc(const KvView& kv, AttnArgs& a, unsigned* err, cudaStream_t st);
 bool attn_tc_supported(const KvView& kv);
 // Block-scaled e4m3: its own tensor-core kernel, which cuts the work by the
-// actual counts.  a.sms is its number of CTAs (block_attn_ctas at most); a.ws_o /
-// a.ws_lse hold two rows of `group` heads for each of them.  Merges in place
-// with a.counters, else in a second launch.
-int block_attn_ctas(int sms);
-inline size_t block_attn_workspace(int ctas, int group, int head_dim) {
-  return static_cast<size_t>(ctas) * 2 * group * (head_dim + 1) * sizeof(float);
-}
+// actual counts.  a.sms is its number of CTAs (each takes an SM); a.ws_o /
+// a.ws_lse hold block_attn_rows rows of `group` heads.  Merges in place with
+// a.counters, else in a second launch.
+int block_attn_rows(int ctas, int head_dim);
 cudaError_t launch_block_attn(const KvView& kv, const AttnArgs& a, unsigned* err, cudaStream_t st);
 // Bound scoring, selection and tensor-core attention in one cluster launch
 // (bf16, head_dim 128, g <= 8, every pair in one wave of at most 8 CTAs).

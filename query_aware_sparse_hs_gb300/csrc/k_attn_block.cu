@@ -9,13 +9,13 @@
 // are (as f16, which holds every e4m3 number exactly).
 //
 // Work: the 32-token tiles of every (request, kv head)'s selection, from the
-// actual counts, which every CTA sums; pairs are cut into equal parts (cut_work
-// below), and of a pair that is cut the CTA that arrives last merges the partial
-// results in the parts' order (the same result whichever CTA that is).  The
-// warps of a CTA take a run of the part's tiles each, with their own running
-// maximum, sum and output, their own ring of tiles in shared memory filled by
-// asynchronous 16-byte copies, and no barrier with the others until the part
-// ends.
+// actual counts, which every CTA sums; pairs are cut into equal parts for teams
+// of warps (choose_cut below), and of a pair that is cut the team that arrives
+// last merges the partial results in the parts' order (the same result whichever
+// team that is).  The warps of a team take a run of the part's tiles each, with
+// their own running maximum, sum and output, their own ring of tiles in shared
+// memory filled by asynchronous 16-byte copies, and no barrier with the others
+// until the part ends.
 //
 // Products on the warp-level matrix instruction m16n8k16 (f16 in, fp32 sums):
 //   S[token][head] = K . Q^T: 16 tokens by 8 heads, so that the group of query
@@ -43,13 +43,17 @@
 namespace hs {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kCtasPerSm = 2;
+constexpr int kTeamWarps = 4;
+// Teams of a CTA, and with them the warps of an SM (one CTA on each): as many as
+// the registers (128 channels: up to 255 a thread, 64 channels: 168) and the
+// rings of tiles allow.
+__host__ __device__ constexpr int teams_of(int head_dim) { return head_dim == 128 ? 2 : 3; }
+constexpr int kMaxWarps = 3 * kTeamWarps;
 constexpr int kTile = 32;       // tokens a warp handles at a time
 constexpr int kStages = 3;      // tiles in a warp's ring
-constexpr int kMinTiles = 8;    // tiles of a part of a cut pair at least: two per warp
+constexpr int kMinTiles = 8;    // tiles of a part of a cut pair at least
 constexpr int kWholeTiles = 32;  // pairs of up to so many tiles are not cut
+constexpr int kMergeTiles = 2;  // what a merge costs, in tiles per warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinRef = 7.888609052210118e-31f;  // 2^-100
 constexpr float kLn2 = 0.6931471805599453f;
@@ -145,91 +149,146 @@ __device__ __forceinline__ int tiles_of(const KvView& kv, int count) {  // (the 
   return static_cast<int>((static_cast<uint32_t>(count) * kv.block + kTile - 1) / kTile);
 }
 
+// Warps that take parts together.  bar: 0 for the whole CTA, else the number of
+// the hardware barrier.
+struct Team {
+  int rank, warps, bar;  // the thread's number in the team, the team's warps
+  __device__ __forceinline__ int threads() const { return warps * 32; }
+  __device__ __forceinline__ void sync() const {
+    if (bar == 0)
+      __syncthreads();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(kTeamWarps * 32) : "memory");
+  }
+};
+
 // Every pair is cut into equal parts of at most `per` tiles; the parts of all
-// pairs are numbered through, and CTA c takes parts c, c + ctas, ...  With
-// per = total / max(ctas - pairs, ctas / 2) there are no more parts than CTAs
+// pairs are numbered through and dealt to the slots in turn.  A slot is a team
+// of kTeamWarps warps, or (joint) all warps of a CTA.  With
+// per = total / max(slots - pairs, slots / 2) there are no more parts than slots
 // where the pairs leave room for that (sum of ceil(n / per) <= total / per +
-// pairs), and a long pair among many short ones is
-// still spread over half the CTAs.  Short pairs are not cut: they have nothing
-// to merge.  A pair that is cut has a row of the workspace for each part: at
-// most 2 total / per <= 2 ctas rows in all.
+// pairs), and a long pair among many short ones is still spread over half the
+// slots.  Short pairs are not cut: they have nothing to merge.  A pair that is cut
+// has a row of the workspace for each part: at most 2 total / per <= 2 slots rows
+// in all.
+//   Joint parts halve (64 channels: third) the parts, and so the merges, and the
+//   time of a short part; with more pairs than CTAs, or pairs so uneven that CTAs
+//   are left idle, teams balance better.  Taken where every CTA has one part at
+//   most and the longest, in tiles per warp, is not longer than the teams' by more
+//   than a merge.  32 requests x 4 heads x 4096 selected tokens: joint 28 us, teams
+//   31.5; 24 uneven requests x 4 heads: 55 and 48; 64 x 4 heads x 4096: 52 and 48.
+struct Cut {
+  int per, slots;
+  bool joint;
+};
 struct Part {
   int pair;
   int index, count;  // which of the pair's parts
   int row;           // workspace row of the pair's first part
 };
 struct Pairs {  // one pair's numbers
-  int tiles;
   int part, count, row;  // its first part, how many, workspace row of the first
 };
-constexpr int kListed = 32;  // parts a CTA notes at a time
+constexpr int kListed = 32;  // parts a team notes at a time
 
 __device__ __forceinline__ int parts_of(int tiles, int per) {
   return tiles <= kWholeTiles ? (tiles > 0 ? 1 : 0) : (tiles + per - 1) / per;
 }
+__device__ __forceinline__ int per_of(int total, int pairs, int slots) {
+  return max((total - 1) / max(max(slots - pairs, slots / 2), 1) + 1, kMinTiles);
+}
 
-struct Scan {
-  int64_t sums[kWarps];
-  int tiles[kWarps];
+struct Scratch {
+  int64_t sums[kMaxWarps];
+  int tiles[kMaxWarps], parts[kMaxWarps], longest[2][kMaxWarps];
 };
-// Sum over the CTA's threads before this one, and over all of them.
-__device__ __forceinline__ int64_t scan_before(int64_t mine, Scan& sc, int64_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t incl = mine;
+
+// The cut for this call's counts, by all threads of a CTA (`cta`).  seen(p, count)
+// sees every pair once, in one of the threads.
+template <typename F>
+__device__ Cut choose_cut(const KvView& kv, const BlockArgs& a, int ctas, int teams, const Team& cta, Scratch& sc, F&& seen) {
+  const int warp = cta.rank >> 5, lane = cta.rank & 31;
+  const int pairs = kv.batch * kv.hkv, mine_n = (pairs + cta.threads() - 1) / cta.threads();
+  const int p0 = min(pairs, cta.rank * mine_n), p1 = min(pairs, p0 + mine_n);
+  int tiles = 0;
+  for (int p = p0; p < p1; ++p) {
+    const int c = pair_count(kv, a, p);
+    seen(p, c);
+    tiles += tiles_of(kv, c);
+  }
+  tiles = __reduce_add_sync(0xffffffffu, tiles);
+  if (lane == 0) sc.tiles[warp] = tiles;
+  cta.sync();
+  int total = 0;
+  for (int w = 0; w < cta.warps; ++w) total += sc.tiles[w];
+  const int per_joint = per_of(total, pairs, ctas), per_team = per_of(total, pairs, ctas * teams);
+  int parts = 0, joint = 0, team = 0;  // parts of joint cutting; the longest part either way
+  for (int p = p0; p < p1; ++p) {
+    const int n = tiles_of(kv, pair_count(kv, a, p)), k = parts_of(n, per_joint);
+    parts += k;
+    if (k > 0) {
+      const int kt = parts_of(n, per_team);
+      joint = max(joint, (n + k - 1) / k);
+      team = max(team, (n + kt - 1) / kt);
+    }
+  }
+  parts = __reduce_add_sync(0xffffffffu, parts);
+  joint = __reduce_max_sync(0xffffffffu, joint);
+  team = __reduce_max_sync(0xffffffffu, team);
+  if (lane == 0) {
+    sc.parts[warp] = parts;
+    sc.longest[0][warp] = joint;
+    sc.longest[1][warp] = team;
+  }
+  cta.sync();
+  parts = 0;
+  for (int w = 0; w < cta.warps; ++w) {
+    parts += sc.parts[w];
+    joint = max(joint, sc.longest[0][w]);
+    team = max(team, sc.longest[1][w]);
+  }
+  Cut cut;
+  cut.joint = parts <= ctas && joint <= (team / kTeamWarps + kMergeTiles) * kTeamWarps * teams;
+  cut.slots = cut.joint ? ctas : ctas * teams;
+  cut.per = cut.joint ? per_joint : per_team;
+  return cut;
+}
+
+// each(p, numbers) sees every pair once, in one of the team's threads; the team
+// meets before the number of parts is returned.
+template <typename F>
+__device__ int number_parts(const KvView& kv, const BlockArgs& a, const Cut& cut, const Team& team, Scratch& sc, F&& each) {
+  const int warp = team.rank >> 5, lane = team.rank & 31;
+  const int pairs = kv.batch * kv.hkv, mine_n = (pairs + team.threads() - 1) / team.threads();
+  const int p0 = min(pairs, team.rank * mine_n), p1 = min(pairs, p0 + mine_n);
+  int64_t mine = 0;  // parts, and rows of the workspace in the upper half
+  for (int p = p0; p < p1; ++p) {
+    const int k = parts_of(tiles_of(kv, pair_count(kv, a, p)), cut.per);
+    mine += k + (k > 1 ? static_cast<int64_t>(k) << 32 : 0);
+  }
+  int64_t at = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+    const int64_t v = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += v;
   }
-  if (lane == 31) sc.sums[warp] = incl;
-  __syncthreads();
-  int64_t all = 0, before = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w == warp) before = all;
+  if (lane == 31) sc.sums[warp] = at;
+  at -= mine;
+  team.sync();
+  int64_t all = 0;
+  for (int w = 0; w < team.warps; ++w) {
+    if (w == warp) at += all;
     all += sc.sums[w];
   }
-  *total = all;
-  return before + incl - mine;
-}
-__device__ __forceinline__ int sum_over_cta(int mine, Scan& sc) {
-  mine = __reduce_add_sync(0xffffffffu, mine);
-  if ((threadIdx.x & 31) == 0) sc.tiles[threadIdx.x >> 5] = mine;
-  __syncthreads();
-  int all = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) all += sc.tiles[w];
-  return all;
-}
-
-// Cuts this call's pairs; every thread of a CTA calls it.  each(p, numbers) sees
-// every pair once, in one of the threads; the CTA's threads meet before it
-// returns the number of parts.
-template <typename F>
-__device__ int cut_work(const KvView& kv, const BlockArgs& a, int ctas, Scan& sc, F&& each) {
-  const int pairs = kv.batch * kv.hkv, mine_n = (pairs + kThreads - 1) / kThreads;
-  const int p0 = min(pairs, static_cast<int>(threadIdx.x) * mine_n), p1 = min(pairs, p0 + mine_n);
-  int tiles = 0;
-  for (int p = p0; p < p1; ++p) tiles += tiles_of(kv, pair_count(kv, a, p));
-  const int total = sum_over_cta(tiles, sc);
-  const int room = max(max(ctas - pairs, ctas / 2), 1);
-  const int per = max((total - 1) / room + 1, kMinTiles);
-  int64_t both = 0, all;  // parts, and rows of the workspace in the upper half
-  for (int p = p0; p < p1; ++p) {
-    const int k = parts_of(tiles_of(kv, pair_count(kv, a, p)), per);
-    both += k + (k > 1 ? static_cast<int64_t>(k) << 32 : 0);
-  }
-  both = scan_before(both, sc, &all);
   for (int p = p0; p < p1; ++p) {
     Pairs n;
-    n.tiles = tiles_of(kv, pair_count(kv, a, p));
-    n.count = parts_of(n.tiles, per);
-    n.part = static_cast<int>(both & 0xffffffff);
-    n.row = static_cast<int>(both >> 32);
+    n.count = parts_of(tiles_of(kv, pair_count(kv, a, p)), cut.per);
+    n.part = static_cast<int>(at & 0xffffffff);
+    n.row = static_cast<int>(at >> 32);
     each(p, n);
-    both += n.count + (n.count > 1 ? static_cast<int64_t>(n.count) << 32 : 0);
+    at += n.count + (n.count > 1 ? static_cast<int64_t>(n.count) << 32 : 0);
   }
-  __syncthreads();
+  team.sync();
   return static_cast<int>(all & 0xffffffff);
 }
 
@@ -243,34 +302,40 @@ __device__ __forceinline__ void store_out(const BlockArgs& a, int64_t at, float4
   }
 }
 
-// Joins the partial results of a pair, in the order of its tiles, into out /
-// lse.  w: shared memory for G * (count + 2) floats.  The first results are on
-// their way while their weights are found.
+// Joins the partial results of a pair into out / lse, every kTeamWarps warps of
+// the team those of every groups-th part, and then the groups.  The order goes by
+// the parts' numbers alone.  w: shared memory for G * (count + 2) floats and
+// groups - 1 results.  The first results are on their way while their weights are
+// found.
 template <int D, int NT>
-__device__ void merge_pair(const KvView& kv, const BlockArgs& a, int64_t pair, int row0, int count, float* w) {
-  constexpr int NI = NT * 8 * D / 4 / kThreads;  // 16-byte pieces of a result per thread, at most
-  constexpr int U = 8 / NI;                      // results in flight
-  const int G = kv.group, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ void merge_pair(const KvView& kv, const BlockArgs& a, const Team& team, int64_t pair, int row0, int count,
+                           float* w) {
+  constexpr int kGroup = kTeamWarps * 32;
+  constexpr int NI = NT * 8 * D / 4 / kGroup;  // 16-byte pieces of a result per thread, at most
+  constexpr int U = 16 / NI;                   // results in flight
+  const int G = kv.group, lane = team.rank & 31, warp = team.rank >> 5, threads = team.threads();
+  const int groups = team.warps / kTeamWarps, grp = team.rank / kGroup, rank = team.rank - grp * kGroup;
   float* norm = w + G * count;  // per head: 1 / sum of the weights
   float* lses = norm + G;
+  float4* sums = reinterpret_cast<float4*>(w + (G * (count + 2) + 3) / 4 * 4);
   const float* ws_lse = a.ws_lse + static_cast<int64_t>(row0) * G;
   const float4* ws_o = reinterpret_cast<const float4*>(a.ws_o + static_cast<int64_t>(row0) * G * D);
   const int pieces = G * (D / 4);
-  float4 next[U][NI];
+  float4 got[U][NI];
   const auto load = [&](int i0) {
 #pragma unroll
     for (int k = 0; k < U; ++k)
 #pragma unroll
       for (int n = 0; n < NI; ++n) {
-        const int idx = threadIdx.x + n * kThreads;
-        next[k][n] = i0 + k < count && idx < pieces ? __ldcg(ws_o + static_cast<int64_t>(i0 + k) * pieces + idx)
-                                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int i = i0 + k * groups, idx = rank + n * kGroup;
+        got[k][n] = i < count && idx < pieces ? __ldcg(ws_o + static_cast<int64_t>(i) * pieces + idx)
+                                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
   };
-  load(0);
-  for (int i = threadIdx.x; i < G * count; i += kThreads) w[i] = __ldcg(ws_lse + i);
-  __syncthreads();
-  for (int h = warp; h < G; h += kWarps) {
+  load(grp);
+  for (int i = team.rank; i < G * count; i += threads) w[i] = __ldcg(ws_lse + i);
+  team.sync();
+  for (int h = warp; h < G; h += team.warps) {
     float M = -INFINITY, tot = 0.0f;
     for (int i = lane; i < count; i += 32) M = fmaxf(M, w[i * G + h]);
     M = warp_max(M);
@@ -286,47 +351,54 @@ __device__ void merge_pair(const KvView& kv, const BlockArgs& a, int64_t pair, i
       lses[h] = tot == 0.0f ? -INFINITY : M + logf(tot);
     }
   }
-  __syncthreads();
+  team.sync();
   float4 acc[NI];
 #pragma unroll
   for (int n = 0; n < NI; ++n) acc[n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int i0 = 0; i0 < count; i0 += U) {
-    float4 now[U][NI];
-#pragma unroll
-    for (int k = 0; k < U; ++k)
-#pragma unroll
-      for (int n = 0; n < NI; ++n) now[k][n] = next[k][n];
-    if (i0 + U < count) load(i0 + U);
+  for (int i0 = grp; i0 < count;) {
 #pragma unroll
     for (int k = 0; k < U; ++k)
 #pragma unroll
       for (int n = 0; n < NI; ++n) {
-        const int idx = threadIdx.x + n * kThreads;
-        const float e = i0 + k < count && idx < pieces ? w[(i0 + k) * G + idx / (D / 4)] : 0.0f;
-        acc[n].x = fmaf(e, now[k][n].x, acc[n].x);
-        acc[n].y = fmaf(e, now[k][n].y, acc[n].y);
-        acc[n].z = fmaf(e, now[k][n].z, acc[n].z);
-        acc[n].w = fmaf(e, now[k][n].w, acc[n].w);
+        const int i = i0 + k * groups, idx = rank + n * kGroup;
+        const float e = i < count && idx < pieces ? w[i * G + idx / (D / 4)] : 0.0f;
+        acc[n].x = fmaf(e, got[k][n].x, acc[n].x);
+        acc[n].y = fmaf(e, got[k][n].y, acc[n].y);
+        acc[n].z = fmaf(e, got[k][n].z, acc[n].z);
+        acc[n].w = fmaf(e, got[k][n].w, acc[n].w);
       }
+    i0 += U * groups;
+    if (i0 < count) load(i0);
+  }
+  if (groups > 1) {
+#pragma unroll
+    for (int n = 0; n < NI; ++n)
+      if (grp > 0 && rank + n * kGroup < pieces) sums[(grp - 1) * pieces + rank + n * kGroup] = acc[n];
+    team.sync();
   }
   const int64_t b = pair / kv.hkv, out_row = b * kv.hq + (pair - b * kv.hkv) * G;
 #pragma unroll
   for (int n = 0; n < NI; ++n) {
-    const int idx = threadIdx.x + n * kThreads;
-    if (idx >= pieces) continue;
+    const int idx = rank + n * kGroup;
+    if (grp > 0 || idx >= pieces) continue;
+    for (int j = 0; j < groups - 1; ++j) {
+      const float4 v = sums[j * pieces + idx];
+      acc[n] = make_float4(acc[n].x + v.x, acc[n].y + v.y, acc[n].z + v.z, acc[n].w + v.w);
+    }
     const float s = norm[idx / (D / 4)];
     store_out(a, out_row * D + 4 * idx, make_float4(acc[n].x * s, acc[n].y * s, acc[n].z * s, acc[n].w * s));
   }
-  if (a.lse && threadIdx.x < G) a.lse[out_row + threadIdx.x] = lses[threadIdx.x];
+  if (a.lse && team.rank < G) a.lse[out_row + team.rank] = lses[team.rank];
 }
 
 template <int D>
 constexpr int ring_bytes() {
-  return kWarps * kStages * 2 * kTile * D;
+  return teams_of(D) * kTeamWarps * kStages * 2 * kTile * D;
 }
 
 template <int D, int NT, bool F32>
-__global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView kv, BlockArgs a, unsigned* err) {
+__global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_kernel(KvView kv, BlockArgs a, unsigned* err) {
+  constexpr int kTeams = teams_of(D), kWarps = kTeams * kTeamWarps;
   constexpr int kStageBytes = 2 * kTile * D;
   constexpr int kPieces = D / 16;        // 16-byte pieces of a row
   constexpr int kRowsPer = 32 / kPieces; // rows one copy instruction of a warp covers
@@ -335,30 +407,22 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
   __shared__ float s_ks[kWarps][kStages][kTile], s_vs[kWarps][kStages][kTile];
   __shared__ uint32_t s_live[kWarps][kStages];
   __shared__ float s_m[kWarps][8 * NT], s_l[kWarps][8 * NT];
-  __shared__ Scan s_scan;
-  __shared__ Part s_parts[kListed];
-  __shared__ int s_last, s_empty;
+  __shared__ Scratch s_scratch[kTeams];
+  __shared__ Part s_parts[kTeams][kListed];
+  __shared__ int s_last[kTeams], s_empty;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) s_empty = 0;  // (cut_work has barriers before it is set)
+  if (tid == 0) s_empty = 0;
+  __syncthreads();
   const int g = lane >> 2, c4 = lane & 3;
   const int G = kv.group, B = kv.block;
   const int pairs = kv.batch * kv.hkv, ctas = gridDim.x;
 
-  int listed = 0;  // parts of this CTA noted so far
-  const auto note = [&](int p, const Pairs& n) {
-    // this CTA's parts among the pair's, the next kListed of them
-    const int me = blockIdx.x;
-    for (int j = n.part + (me + ctas - n.part % ctas) % ctas; j < n.part + n.count; j += ctas) {
-      const int slot = j / ctas - listed;
-      if (slot >= 0 && slot < kListed) s_parts[slot] = Part{p, j - n.part, n.count, n.row};
-    }
-  };
-  const int all_parts = cut_work(kv, a, ctas, s_scan, [&](int p, const Pairs& n) {
-    note(p, n);
+  const Team cta{tid, kWarps, 0};
+  const Cut cut = choose_cut(kv, a, ctas, kTeams, cta, s_scratch[0], [&](int p, int count) {
     if (p % ctas == static_cast<int>(blockIdx.x)) {  // the CTA that answers for the pair's count
-      if (n.count == 0) s_empty = 1;
+      if (count == 0) s_empty = 1;
       if (a.sel_count[p] > a.capacity) set_error(err, HS_EBIT_CAPACITY);
     }
   });
@@ -366,10 +430,23 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
     for (int p = blockIdx.x; p < pairs; p += ctas) {
       if (pair_count(kv, a, p) > 0) continue;
       const int64_t b = p / kv.hkv, row = b * kv.hq + static_cast<int64_t>(p - b * kv.hkv) * G;
-      for (int i = tid; i < G * D / 4; i += kThreads) store_out(a, row * D + 4 * i, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+      for (int i = tid; i < G * D / 4; i += kWarps * 32)
+        store_out(a, row * D + 4 * i, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
       if (a.lse && tid < G) a.lse[row + tid] = -INFINITY;
     }
   }
+  const int tm = cut.joint ? 0 : warp / kTeamWarps, first_warp = tm * kTeamWarps, team_warp = warp - first_warp;
+  const Team team = cut.joint ? cta : Team{tid - tm * kTeamWarps * 32, kTeamWarps, 1 + tm};
+  const int slot = tm * ctas + blockIdx.x;  // (the first slots are on different SMs)
+  int listed = 0;                           // parts of this team noted so far
+  const auto note = [&](int p, const Pairs& n) {
+    // this team's parts among the pair's, the next kListed of them
+    for (int j = n.part + (slot + cut.slots - n.part % cut.slots) % cut.slots; j < n.part + n.count; j += cut.slots) {
+      const int at = j / cut.slots - listed;
+      if (at >= 0 && at < kListed) s_parts[tm][at] = Part{p, j - n.part, n.count, n.row};
+    }
+  };
+  const int all_parts = number_parts(kv, a, cut, team, s_scratch[tm], note);
 
   // this lane's 16-byte piece of the first rows a copy instruction covers
   const uint8_t* k_piece = static_cast<const uint8_t*>(kv.k_pages) + (lane / kPieces) * D + 16 * (lane % kPieces);
@@ -377,14 +454,14 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
   uint8_t* my_ring = ring + warp * (kStages * kStageBytes);
   const uint32_t my_ring_addr = smem_addr(my_ring);
 
-  const int my_parts = (all_parts - static_cast<int>(blockIdx.x) + ctas - 1) / ctas;
+  const int my_parts = (all_parts - slot + cut.slots - 1) / cut.slots;
   for (int n_part = 0; n_part < my_parts; ++n_part) {
     if (n_part == listed + kListed) {
       listed = n_part;
-      cut_work(kv, a, ctas, s_scan, note);
+      number_parts(kv, a, cut, team, s_scratch[tm], note);
     }
-    // ---- the part: tiles [seg0, seg1) of `pair` ----
-    const Part part = s_parts[n_part - listed];
+    // ---- the part: seg_tiles tiles of `pair` from seg0 on ----
+    const Part part = s_parts[tm][n_part - listed];
     const int pair = part.pair;
     const int cnt = pair_count(kv, a, pair);
     const int pair_tiles = tiles_of(kv, cnt), each = pair_tiles / part.count, more = pair_tiles - each * part.count;
@@ -411,7 +488,8 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
     const int32_t* table = kv.page_table + static_cast<int64_t>(pair) * kv.max_blocks;
 
     // The warp's tiles: a run of the part.
-    const int run0 = seg0 + seg_tiles * warp / kWarps, tiles = seg0 + seg_tiles * (warp + 1) / kWarps - run0;
+    const int run0 = seg0 + seg_tiles * team_warp / team.warps;
+    const int tiles = seg0 + seg_tiles * (team_warp + 1) / team.warps - run0;
     // Selected blocks are looked up 32 at a time, one to a lane, the pages one
     // window ahead of the copies and the selection two, so that neither load is
     // waited for.  A window holds the entries from that of its first tile on;
@@ -586,29 +664,35 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
       const float* vs = s_vs[warp][stage];
       const uint32_t live = s_live[warp][stage];
 
-      // S = K Q^T
+      // S = K Q^T, the two 16-token halves in turn so that no product waits for the last
       float s[2][NT][4];
 #pragma unroll
-      for (int st = 0; st < 2; ++st) {
+      for (int st = 0; st < 2; ++st)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[st][nt][e] = 0.0f;
-        const int ra = 16 * st + token_of<D>(g), rb = ra + 8;
 #pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
+      for (int k = 0; k < kChunks; ++k) {
+        uint32_t wa[2][4], wb[2][4];
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          const int ra = 16 * st + token_of<D>(g);
           const uint4 xa = *reinterpret_cast<const uint4*>(kt + piece_at<D>(ra, 4 * k + c4));
-          const uint4 xb = *reinterpret_cast<const uint4*>(kt + piece_at<D>(rb, 4 * k + c4));
-          const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
+          const uint4 xb = *reinterpret_cast<const uint4*>(kt + piece_at<D>(ra + 8, 4 * k + c4));
+          wa[st][0] = xa.x; wa[st][1] = xa.y; wa[st][2] = xa.z; wa[st][3] = xa.w;
+          wb[st][0] = xb.x; wb[st][1] = xb.y; wb[st][2] = xb.z; wb[st][3] = xb.w;
+        }
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < 4; ++w)
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
             uint32_t a0, a1, a2, a3;
-            halves_of(wa[w], a0, a2);
-            halves_of(wb[w], a1, a3);
+            halves_of(wa[st][w], a0, a2);
+            halves_of(wb[st][w], a1, a3);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma(s[st][nt], a0, a1, a2, a3, qf[nt][4 * k + w][0], qf[nt][4 * k + w][1]);
           }
-        }
       }
 
       // logits (log2 units), their maximum over the tile
@@ -729,8 +813,8 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
     copies_wait<0>();
 
     // ---- the warps' states joined ----
-    __syncthreads();  // every warp is done with its ring: it now holds the outputs
-    float* so = reinterpret_cast<float*>(ring);  // [warp][8 NT][D]
+    team.sync();  // every warp is done with its ring: the team's rings now hold the outputs
+    float* so = reinterpret_cast<float*>(ring + first_warp * (kStages * kStageBytes));  // [team warp][8 NT][D]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -745,27 +829,26 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
           s_l[warp][h] = sum;
         }
         const float back = vref * 6.103515625e-05f;  // 2^-14
-        float* dst = so + (warp * 8 * NT + h) * D + g * (D / 8);
+        float* dst = so + (team_warp * 8 * NT + h) * D + g * (D / 8);
 #pragma unroll
         for (int i = 0; i < D / 16; i += 2)
           *reinterpret_cast<float4*>(dst + 2 * i) =
               make_float4(o[nt][i][e] * back, o[nt][i][2 + e] * back, o[nt][i + 1][e] * back, o[nt][i + 1][2 + e] * back);
       }
-    __syncthreads();
+    team.sync();
     const bool whole = part.count == 1;
-    for (int idx = tid; idx < G * (D / 4); idx += kThreads) {
+    for (int idx = team.rank; idx < G * (D / 4); idx += team.threads()) {
       const int h = idx / (D / 4), d = (idx - h * (D / 4)) * 4;
       float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][h]);
+      for (int w = 0; w < team.warps; ++w) M = fmaxf(M, s_m[first_warp + w][h]);
       if (M == -INFINITY) M = 0.0f;  // no token, or only logits that are not numbers
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       float tot = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2f(s_m[w][h] - M);
+#pragma unroll 4
+      for (int w = 0; w < team.warps; ++w) {
+        const float f = exp2f(s_m[first_warp + w][h] - M);
         const float4 v = *reinterpret_cast<const float4*>(so + (w * 8 * NT + h) * D + d);
-        tot = fmaf(s_l[w][h], f, tot);
+        tot = fmaf(s_l[first_warp + w][h], f, tot);
         acc.x = fmaf(v.x, f, acc.x);
         acc.y = fmaf(v.y, f, acc.y);
         acc.z = fmaf(v.z, f, acc.z);
@@ -786,35 +869,39 @@ __global__ __launch_bounds__(kThreads, kCtasPerSm) void attn_block_kernel(KvView
       }
     }
     if (!whole && a.counters) {
-      __syncthreads();
-      if (tid == 0) {
-        // releases what the CTA wrote before the barrier, acquires what the others released
+      team.sync();
+      if (team.rank == 0) {
+        // releases what the team wrote before the barrier, acquires what the others released
         uint32_t there;
         asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(there) : "l"(a.counters + pair) : "memory");
-        s_last = there == static_cast<uint32_t>(part.count - 1);
-        if (s_last) a.counters[pair] = 0u;
+        s_last[tm] = there == static_cast<uint32_t>(part.count - 1);
+        if (s_last[tm]) a.counters[pair] = 0u;
       }
-      __syncthreads();
-      if (s_last) merge_pair<D, NT>(kv, a, pair, part.row, part.count, reinterpret_cast<float*>(ring));
+      team.sync();
+      if (s_last[tm]) merge_pair<D, NT>(kv, a, team, pair, part.row, part.count, so);
     }
-    __syncthreads();  // the ring and s_m are free again
+    team.sync();  // the rings and s_m are free again
   }
 }
 
 // The merge as a launch of its own, for callers without split counters.  CTA =
-// pair.
+// pair; as many warps as merge in place, so that the results are the same.
 template <int D, int NT>
-__global__ __launch_bounds__(kThreads) void attn_block_merge_kernel(KvView kv, BlockArgs a, int ctas) {
-  extern __shared__ float weights[];
-  __shared__ Scan s_scan;
+__global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32) void attn_block_merge_kernel(KvView kv, BlockArgs a, int ctas) {
+  extern __shared__ __align__(16) float weights[];
+  __shared__ Scratch s_scratch;
   __shared__ Pairs s_pair;
   pdl_trigger();
   pdl_wait();
-  const int pair = blockIdx.x;
-  cut_work(kv, a, ctas, s_scan, [&](int p, const Pairs& n) {
+  const int pair = blockIdx.x, tid = threadIdx.x;
+  const Team cta{tid, teams_of(D) * kTeamWarps, 0};
+  const Cut cut = choose_cut(kv, a, ctas, teams_of(D), cta, s_scratch, [](int, int) {});
+  if (!cut.joint && tid >= kTeamWarps * 32) return;
+  const Team team = cut.joint ? cta : Team{tid, kTeamWarps, 1};
+  number_parts(kv, a, cut, team, s_scratch, [&](int p, const Pairs& n) {
     if (p == pair) s_pair = n;
   });
-  if (s_pair.count > 1) merge_pair<D, NT>(kv, a, pair, s_pair.row, s_pair.count, weights);
+  if (s_pair.count > 1) merge_pair<D, NT>(kv, a, team, pair, s_pair.row, s_pair.count, weights);
 }
 
 template <int D, int NT, bool F32>
@@ -829,12 +916,13 @@ cudaError_t launch_o(const KvView& kv, const BlockArgs& b, int ctas, unsigned* e
     if (cudaError_t e = allow_dynamic_smem(kern, ring_bytes<D>()); e != cudaSuccess) return e;
     allowed.fetch_or(bit, std::memory_order_relaxed);
   }
-  cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(kThreads), ring_bytes<D>(), st, kv, b, err);
+  cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(teams_of(D) * kTeamWarps * 32), ring_bytes<D>(), st, kv, b, err);
   if (e != cudaSuccess || b.counters) return e;
-  const size_t smem = static_cast<size_t>(ctas + 2) * kv.group * sizeof(float);
+  const size_t smem = (static_cast<size_t>(ctas * teams_of(D) + 2) * kv.group + 4 +
+                       static_cast<size_t>(teams_of(D) - 1) * kv.group * D) * sizeof(float);
   auto merge = attn_block_merge_kernel<D, NT>;
   if ((e = allow_dynamic_smem(merge, smem)) != cudaSuccess) return e;
-  return launch_pdl(merge, dim3(kv.batch * kv.hkv), dim3(kThreads), smem, st, kv, b, ctas);
+  return launch_pdl(merge, dim3(kv.batch * kv.hkv), dim3(teams_of(D) * kTeamWarps * 32), smem, st, kv, b, ctas);
 }
 
 template <int D, int NT>
@@ -844,7 +932,7 @@ cudaError_t launch_n(const KvView& kv, const BlockArgs& b, int ctas, unsigned* e
 
 }  // namespace
 
-int block_attn_ctas(int sms) { return sms * kCtasPerSm; }
+int block_attn_rows(int ctas, int head_dim) { return 2 * ctas * teams_of(head_dim); }
 
 cudaError_t launch_block_attn(const KvView& kv, const AttnArgs& a, unsigned* err, cudaStream_t st) {
   if (kv.batch == 0) return cudaSuccess;
