@@ -369,26 +369,32 @@ __device__ __forceinline__ uint4 rescaled(uint4 v, float f) {
 }
 
 // ---- any number of rows per request ----
-// P: passes of the CTA over its rows that are read together (and, block-scaled,
-// held, as read, until the scale is known).
-template <int D, int KIND, int THREADS, int P>
-__global__ __launch_bounds__(THREADS, (KIND == HS_KV_F32 ? 384 : 512) / THREADS) void append_rows_kernel(KvView kv, AppendTokensArgs a, int64_t kv_units,
+// A unit is one touched block of one kv head, K or V, taken by UW warps: as many
+// as let the page's rows be read in P = 4 passes (pages of more than 8 warps'
+// rows are taken in turns).  The rows of the passes are read together and,
+// block-scaled, held, as read, until the scale is known.
+constexpr int P = 4;
+constexpr int threads_of(int unit_warps) { return unit_warps > 4 ? 32 * unit_warps : 128; }
+
+template <int D, int KIND, int UW>
+__global__ __launch_bounds__(threads_of(UW), (KIND == HS_KV_F32 ? 384 : 512) / threads_of(UW)) void append_rows_kernel(KvView kv, AppendTokensArgs a, int64_t kv_units,
                                                                int64_t span, int64_t q_units, int q_rows,
                                                                unsigned* err) {
   constexpr bool F32 = KIND == HS_KV_F32;
-  constexpr int TPR = D / 16, RPP = THREADS / TPR;  // threads per row, rows per pass
-  constexpr int kWarps = THREADS / 32;
+  constexpr int kWarps = threads_of(UW) / 32, kUnits = kWarps / UW;  // of a CTA
+  constexpr int TPR = D / 16, RPP = UW * 32 / TPR;  // threads per row, rows per pass of a unit
   __shared__ float s_mn[kWarps][D], s_mx[kWarps][D];
   __shared__ float s_amax[kWarps];
   __shared__ int s_any[kWarps];
-  __shared__ unsigned s_group[RPP][D / kQuantGroup];
+  __shared__ unsigned s_group[kWarps * 32 / TPR][D / kQuantGroup];
   pdl_trigger();
   pdl_wait();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // ---- K and V units are spread over the first `span` CTAs, the others rotate Q ----
-  const int64_t unit = min(static_cast<int64_t>(blockIdx.x) * kv_units / span, kv_units);
-  if (min((static_cast<int64_t>(blockIdx.x) + 1) * kv_units / span, kv_units) == unit) {
-    const int64_t q = (blockIdx.x - unit) * kWarps + warp;
+  const int64_t kv_ctas = (kv_units + kUnits - 1) / kUnits;
+  const int64_t cta = min(static_cast<int64_t>(blockIdx.x) * kv_ctas / span, kv_ctas);
+  if (min((static_cast<int64_t>(blockIdx.x) + 1) * kv_ctas / span, kv_ctas) == cta) {
+    const int64_t q = (blockIdx.x - cta) * kWarps + warp;
     if (q >= q_units) return;
     const int chunks = ceil_div(kv.hq, kQHeads);
     const int64_t r = q / chunks;
@@ -396,6 +402,17 @@ __global__ __launch_bounds__(THREADS, (KIND == HS_KV_F32 ? 384 : 512) / THREADS)
     return;
   }
   // ---- which block ----
+  const int first_warp = warp / UW * UW, tid = threadIdx.x - first_warp * 32;  // the unit's first warp, the thread in it
+  const auto unit_sync = [&]() {
+    if constexpr (UW == 1)
+      __syncwarp();
+    else if constexpr (kUnits == 1)
+      __syncthreads();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + first_warp / UW), "n"(UW * 32) : "memory");
+  };
+  const int64_t unit = cta * kUnits + first_warp / UW;
+  if (unit >= kv_units) return;
   const bool is_k = (unit & 1) == 0;
   const int64_t slot = (unit >> 1) / kv.hkv;
   const int kvh = static_cast<int>((unit >> 1) - slot * kv.hkv);
@@ -490,7 +507,7 @@ __global__ __launch_bounds__(THREADS, (KIND == HS_KV_F32 ? 384 : 512) / THREADS)
       const bool on = turned(r, xa[i], xb[i], u, w);
       any |= on;
       if constexpr (KIND == HS_KV_FP8E4M3_G32) {
-        store_grouped<D>(pages, scales, row0 + r, s, t, on, s_group[rs], u, w);
+        store_grouped<D>(pages, scales, row0 + r, s, t, on, s_group[threadIdx.x / TPR], u, w);
       } else if constexpr (KIND == HS_KV_FP8E4M3_BLOCK) {
         if (on && !box) amax = widen_any(amax, u, w);
       } else {
@@ -511,20 +528,22 @@ __global__ __launch_bounds__(THREADS, (KIND == HS_KV_F32 ? 384 : 512) / THREADS)
   float scale = 1.0f, inv = 1.0f;
   bool grown = false;
   if constexpr (KIND == HS_KV_FP8E4M3_BLOCK) {
-    const float held = ra > 0 ? scales[page] : 0.0f;  // read by every thread before one of them writes it
+    const float held = ra > 0 ? scales[page] : 0.0f;  // read by every thread before one of them writes it (below)
     if (box && any) {  // the box has the largest magnitude in it
 #pragma unroll
       for (int c = 0; c < 16; ++c) amax = fmaxf(amax, mn[c] <= mx[c] ? fmaxf(-mn[c], mx[c]) : 0.0f);
     }
-    const auto over_cta = [&](float m) {
+    const auto over_unit = [&](float m) {
       m = warp_max(m);
-      if (lane == 0) s_amax[warp] = m;
-      __syncthreads();
+      if constexpr (UW > 1) {
+        if (lane == 0) s_amax[warp] = m;
+        unit_sync();
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) m = fmaxf(m, s_amax[i]);
+        for (int i = 0; i < UW; ++i) m = fmaxf(m, s_amax[first_warp + i]);
+      }
       return m;
     };
-    amax = over_cta(amax);
+    amax = over_unit(amax);
     const bool again = rb - ra > P * RPP;  // more rows than are held: read once more, from the caches
     if (amax == INFINITY) {  // the scale goes by the finite values
       amax = 0.0f;
@@ -536,8 +555,8 @@ __global__ __launch_bounds__(THREADS, (KIND == HS_KV_F32 ? 384 : 512) / THREADS)
           if (turned(r0 + i * RPP + rs, xa[i], xb[i], u, w)) amax = widen_finite(amax, u, w);
         }
       }
-      __syncthreads();
-      amax = over_cta(amax);
+      unit_sync();
+      amax = over_unit(amax);
     }
     scale = block_scale(amax);
     if (ra > 0) {
@@ -552,6 +571,7 @@ __global__ __launch_bounds__(THREADS, (KIND == HS_KV_F32 ? 384 : 512) / THREADS)
         *p = rescaled(*p, f);
       }
     }
+    if constexpr (UW == 1) __syncwarp();
     if (tid == 0 && (ra == 0 || grown)) scales[page] = scale;
     for (int r0 = ra; r0 < rb; r0 += P * RPP) {
       if (again) read(r0);
@@ -587,45 +607,46 @@ __global__ __launch_bounds__(THREADS, (KIND == HS_KV_F32 ? 384 : 512) / THREADS)
   }
   any = __any_sync(0xffffffffu, any);
   if (lane == 0) s_any[warp] = any ? 1 : 0;
-  __syncthreads();  // (also: the page's rows are written)
+  unit_sync();  // (also: the page's rows are written)
   int rows_written = 0;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) rows_written |= s_any[i];
+  for (int i = 0; i < UW; ++i) rows_written |= s_any[first_warp + i];
   if (!rows_written) return;  // every row's position was out of range
-  const int d = tid;
-  if (d >= D) return;
-  float lo = s_mn[0][d], hi = s_mx[0][d];
 #pragma unroll
-  for (int i = 1; i < kWarps; ++i) {
-    lo = fminf(lo, s_mn[i][d]);
-    hi = fmaxf(hi, s_mx[i][d]);
-  }
-  if constexpr (KIND == HS_KV_FP8E4M3_BLOCK) {
-    if (lo <= hi) {  // (else only NaN)
-      lo = as_stored(lo, inv, scale);
-      hi = as_stored(hi, inv, scale);
+  for (int d = tid; d < D; d += UW * 32) {
+    float lo = s_mn[first_warp][d], hi = s_mx[first_warp][d];
+#pragma unroll
+    for (int i = 1; i < UW; ++i) {
+      lo = fminf(lo, s_mn[first_warp + i][d]);
+      hi = fmaxf(hi, s_mx[first_warp + i][d]);
     }
-    if (grown)  // the earlier rows' codes may have been rounded: their box is taken anew
-      for (int r = 0; r < ra; ++r) {
-        const float v = decode1(static_cast<const uint8_t*>(pages)[(row0 + r) * D + d]) * scale;
-        lo = fminf(lo, v);
-        hi = fmaxf(hi, v);
+    if constexpr (KIND == HS_KV_FP8E4M3_BLOCK) {
+      if (lo <= hi) {  // (else only NaN)
+        lo = as_stored(lo, inv, scale);
+        hi = as_stored(hi, inv, scale);
       }
-  }
-  const int64_t o = (pair * kv.max_blocks + j) * D + d;
-  const bool keep = ra > 0 && !grown;
-  if constexpr (F32) {
-    float* pn = static_cast<float*>(a.smin) + o;
-    float* px = static_cast<float*>(a.smax) + o;
-    *pn = keep ? fminf(*pn, lo) : lo;
-    *px = keep ? fmaxf(*px, hi) : hi;
-  } else {
-    __nv_bfloat16* pn = static_cast<__nv_bfloat16*>(a.smin) + o;
-    __nv_bfloat16* px = static_cast<__nv_bfloat16*>(a.smax) + o;
-    lo = __bfloat162float(__float2bfloat16_rd(lo));  // outward; exact for values that are bf16 already
-    hi = __bfloat162float(__float2bfloat16_ru(hi));
-    *pn = __float2bfloat16_rn(keep ? fminf(__bfloat162float(*pn), lo) : lo);
-    *px = __float2bfloat16_rn(keep ? fmaxf(__bfloat162float(*px), hi) : hi);
+      if (grown)  // the earlier rows' codes may have been rounded: their box is taken anew
+        for (int r = 0; r < ra; ++r) {
+          const float v = decode1(static_cast<const uint8_t*>(pages)[(row0 + r) * D + d]) * scale;
+          lo = fminf(lo, v);
+          hi = fmaxf(hi, v);
+        }
+    }
+    const int64_t o = (pair * kv.max_blocks + j) * D + d;
+    const bool keep = ra > 0 && !grown;
+    if constexpr (F32) {
+      float* pn = static_cast<float*>(a.smin) + o;
+      float* px = static_cast<float*>(a.smax) + o;
+      *pn = keep ? fminf(*pn, lo) : lo;
+      *px = keep ? fmaxf(*px, hi) : hi;
+    } else {
+      __nv_bfloat16* pn = static_cast<__nv_bfloat16*>(a.smin) + o;
+      __nv_bfloat16* px = static_cast<__nv_bfloat16*>(a.smax) + o;
+      lo = __bfloat162float(__float2bfloat16_rd(lo));  // outward; exact for values that are bf16 already
+      hi = __bfloat162float(__float2bfloat16_ru(hi));
+      *pn = __float2bfloat16_rn(keep ? fminf(__bfloat162float(*pn), lo) : lo);
+      *px = __float2bfloat16_rn(keep ? fmaxf(__bfloat162float(*px), hi) : hi);
+    }
   }
 }
 
@@ -804,19 +825,18 @@ __global__ __launch_bounds__(kThreads) void append_one_kernel(KvView kv, AppendT
   }
 }
 
-template <int D, int KIND, int THREADS, int P>
-cudaError_t launch_rows(const KvView& kv, const AppendTokensArgs& a, int64_t kv_units, int sms, unsigned* err,
-                        cudaStream_t st) {
-  constexpr int kQWarps = THREADS / 32;
-  const int64_t q_units = q_units_of(kv, a);
-  const int64_t ctas = kv_units + (q_units + kQWarps - 1) / kQWarps;
+template <int D, int KIND, int UW>
+cudaError_t launch_rows(const KvView& kv, const AppendTokensArgs& a, int sms, unsigned* err, cudaStream_t st) {
+  constexpr int kThreads = threads_of(UW), kWarps = kThreads / 32, kUnits = kWarps / UW;
+  const int64_t kv_units = kv_units_of(kv, a), kv_ctas = (kv_units + kUnits - 1) / kUnits;
+  const int64_t q_units = q_units_of(kv, a), ctas = kv_ctas + (q_units + kWarps - 1) / kWarps;
   // K and V units that all run at once go first: they take longest (a chunk of
   // 2000 tokens 12.0 us, mixed evenly 15.7).  More than that are mixed evenly
   // with the Q units, which keep the memory busy while they look up and reduce
   // (prompts of 16 requests 143 us, K and V first 155).
-  const int64_t span = kv_units <= static_cast<int64_t>(sms) * (512 / THREADS) ? kv_units : ctas;
-  return launch_pdl(append_rows_kernel<D, KIND, THREADS, P>, dim3(static_cast<unsigned>(ctas)), dim3(THREADS), 0, st, kv,
-                    a, kv_units, span, q_units, q_rows_of(kv, a), err);
+  const int64_t span = kv_ctas <= static_cast<int64_t>(sms) * (512 / kThreads) ? kv_ctas : ctas;
+  return launch_pdl(append_rows_kernel<D, KIND, UW>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, st, kv, a,
+                    kv_units, span, q_units, q_rows_of(kv, a), err);
 }
 
 template <int D, int KIND>
@@ -827,12 +847,11 @@ cudaError_t launch_k(const KvView& kv, const AppendTokensArgs& a, int sms, unsig
     return launch_pdl(append_one_kernel<D, KIND>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, st, kv, a, kv_ctas,
                       err);
   }
-  constexpr int RPP = 128 / (D / 16);
-  const int64_t units = kv_units_of(kv, a);
-  if (kv.block <= RPP) return launch_rows<D, KIND, 128, 1>(kv, a, units, sms, err, st);
-  if (kv.block <= 2 * RPP) return launch_rows<D, KIND, 128, 2>(kv, a, units, sms, err, st);
-  if (kv.block <= 4 * RPP) return launch_rows<D, KIND, 128, 4>(kv, a, units, sms, err, st);
-  return launch_rows<D, KIND, 256, 4>(kv, a, units, sms, err, st);
+  constexpr int kWarpRows = P * 32 / (D / 16);  // rows of a page that a warp reads at once
+  if (kv.block <= kWarpRows) return launch_rows<D, KIND, 1>(kv, a, sms, err, st);
+  if (kv.block <= 2 * kWarpRows) return launch_rows<D, KIND, 2>(kv, a, sms, err, st);
+  if (kv.block <= 4 * kWarpRows) return launch_rows<D, KIND, 4>(kv, a, sms, err, st);
+  return launch_rows<D, KIND, 8>(kv, a, sms, err, st);
 }
 
 template <int D>
