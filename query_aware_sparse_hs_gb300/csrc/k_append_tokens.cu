@@ -40,7 +40,7 @@ constexpr int kQHeads = 16;  // heads of one row that a warp rotates
 // Largest i in [0, n) with key(i) <= x, for nondecreasing keys with key(0) <= x
 // (0 if there is none): 32 probes a round.  All 32 lanes must call it.
 template <typename F>
-__device__ __forceinline__ int last_not_above(int n, int64_t x, int lane, F key) {
+__device__ __forceinline__ int last_not_above(int n, int x, int lane, F key) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32;
@@ -165,8 +165,9 @@ __device__ __forceinline__ void load_angles(const float* cos_sin, int rotary, in
   load8<true>(row, 0, t.c);
   load8<true>(row, rotary / 2, t.s);
 }
-__device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const Angles& t, bool interleaved) {
-  if (interleaved) {
+template <bool INTERLEAVED>  // (at run time both forms would be computed and one kept)
+__device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const Angles& t) {
+  if constexpr (INTERLEAVED) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float x = a[2 * i], y = a[2 * i + 1], z = b[2 * i], w = b[2 * i + 1];
@@ -214,13 +215,13 @@ __device__ __forceinline__ bool place_of_row(const KvView& kv, const AppendToken
 }
 
 // kQHeads heads of rows [row, row_end).
-template <int D, bool F32>
+template <int D, bool F32, bool INTERLEAVED>
 __device__ void rotate_q(const KvView& kv, const AppendTokensArgs& a, int h0, int64_t row, int64_t row_end, int lane,
                          unsigned* err) {
   constexpr int TPR = D / 16, HPP = 32 / TPR, N = kQHeads / HPP;  // threads per head, heads per step, steps
   constexpr int E = F32 ? 4 : 2;
   const int s = lane % TPR, h = h0 + lane / TPR;
-  const Slot t = slot_of(s, a.rotary, a.interleaved);
+  const Slot t = slot_of(s, a.rotary, INTERLEAVED);
   const uint8_t* q = static_cast<const uint8_t*>(a.q) + (row * a.q_stride + h * D) * E;
   uint8_t* out = static_cast<uint8_t*>(a.q_out) + (row * a.q_out_stride + h * D) * E;
   Raw8<F32> x[N], y[N];
@@ -234,7 +235,7 @@ __device__ void rotate_q(const KvView& kv, const AppendTokensArgs& a, int h0, in
   };
   read();  // ahead of everything that takes lookups
   int b = static_cast<int>(row);
-  if (a.offsets) b = last_not_above(kv.batch, row, lane, [&](int i) { return static_cast<int64_t>(__ldg(a.offsets + i)); });
+  if (a.offsets) b = last_not_above(kv.batch, static_cast<int>(row), lane, [&](int i) { return __ldg(a.offsets + i); });
   for (;;) {
     int64_t p, pos = 0;
     bool ok = place_of_row(kv, a, row, b, &p);
@@ -253,7 +254,7 @@ __device__ void rotate_q(const KvView& kv, const AppendTokensArgs& a, int h0, in
         float u[8], w[8];
         x[i].get(u);
         y[i].get(w);
-        if (t.rotated) rotate(u, w, ang, a.interleaved);
+        if (t.rotated) rotate<INTERLEAVED>(u, w, ang);
         if (h + i * HPP < kv.hq) {
           store8<F32>(out + (i * HPP * D + t.ca) * E, 0, u);
           store8<F32>(out + (i * HPP * D + t.cb) * E, 0, w);
@@ -376,10 +377,8 @@ __device__ __forceinline__ uint4 rescaled(uint4 v, float f) {
 constexpr int P = 4;
 constexpr int threads_of(int unit_warps) { return unit_warps > 4 ? 32 * unit_warps : 128; }
 
-template <int D, int KIND, int UW>
-__global__ __launch_bounds__(threads_of(UW), (KIND == HS_KV_F32 ? 384 : 512) / threads_of(UW)) void append_rows_kernel(KvView kv, AppendTokensArgs a, int64_t kv_units,
-                                                               int64_t span, int64_t q_units, int q_rows,
-                                                               unsigned* err) {
+template <int D, int KIND, bool INTERLEAVED, int UW>
+__global__ __launch_bounds__(threads_of(UW), (KIND == HS_KV_F32 ? 384 : 512) / threads_of(UW)) void append_rows_kernel(KvView kv, AppendTokensArgs a, int kv_units, uint64_t mix, int q_units, int q_rows, unsigned* err) {
   constexpr bool F32 = KIND == HS_KV_F32;
   constexpr int kWarps = threads_of(UW) / 32, kUnits = kWarps / UW;  // of a CTA
   constexpr int TPR = D / 16, RPP = UW * 32 / TPR;  // threads per row, rows per pass of a unit
@@ -391,14 +390,16 @@ __global__ __launch_bounds__(threads_of(UW), (KIND == HS_KV_F32 ? 384 : 512) / t
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // ---- K and V units are spread over the first `span` CTAs, the others rotate Q ----
-  const int64_t kv_ctas = (kv_units + kUnits - 1) / kUnits;
-  const int64_t cta = min(static_cast<int64_t>(blockIdx.x) * kv_ctas / span, kv_ctas);
-  if (min((static_cast<int64_t>(blockIdx.x) + 1) * kv_ctas / span, kv_ctas) == cta) {
-    const int64_t q = (blockIdx.x - cta) * kWarps + warp;
+  // (mix: K and V CTAs per CTA, in 2^-32; divisions are in 32 bits: they are most
+  // of a unit's fixed work)
+  const int kv_ctas = (kv_units + kUnits - 1) / kUnits;
+  const int cta = static_cast<int>(min((blockIdx.x * mix) >> 32, static_cast<uint64_t>(kv_ctas)));
+  if (static_cast<int>(min(((blockIdx.x + uint64_t(1)) * mix) >> 32, static_cast<uint64_t>(kv_ctas))) == cta) {
+    const int q = static_cast<int>(blockIdx.x - cta) * kWarps + warp;
     if (q >= q_units) return;
-    const int chunks = ceil_div(kv.hq, kQHeads);
-    const int64_t r = q / chunks;
-    rotate_q<D, F32>(kv, a, static_cast<int>(q - r * chunks) * kQHeads, r * q_rows, min(a.rows, (r + 1) * q_rows), lane, err);
+    const int chunks = ceil_div(kv.hq, kQHeads), r = q / chunks;
+    rotate_q<D, F32, INTERLEAVED>(kv, a, (q - r * chunks) * kQHeads, static_cast<int64_t>(r) * q_rows,
+                     min(a.rows, (r + int64_t(1)) * q_rows), lane, err);
     return;
   }
   // ---- which block ----
@@ -411,28 +412,25 @@ __global__ __launch_bounds__(threads_of(UW), (KIND == HS_KV_F32 ? 384 : 512) / t
     else
       asm volatile("bar.sync %0, %1;" ::"r"(1 + first_warp / UW), "n"(UW * 32) : "memory");
   };
-  const int64_t unit = cta * kUnits + first_warp / UW;
+  const int unit = cta * kUnits + first_warp / UW;
   if (unit >= kv_units) return;
   const bool is_k = (unit & 1) == 0;
-  const int64_t slot = (unit >> 1) / kv.hkv;
-  const int kvh = static_cast<int>((unit >> 1) - slot * kv.hkv);
+  const int slot = (unit >> 1) / kv.hkv, kvh = (unit >> 1) - slot * kv.hkv;
   const int B = kv.block;
   // request b has the slots from offsets[b] / B + 2 b on: enough for every block
   // its rows can touch, wherever in a block they begin
-  const int b = last_not_above(kv.batch, slot, lane, [&](int i) { return static_cast<int64_t>(__ldg(a.offsets + i)) / B + 2 * i; });
-  const int64_t o0 = __ldg(a.offsets + b), o1 = __ldg(a.offsets + b + 1);
+  const int b = last_not_above(kv.batch, slot, lane, [&](int i) { return __ldg(a.offsets + i) / B + 2 * i; });
+  const int o0 = __ldg(a.offsets + b), o1 = __ldg(a.offsets + b + 1);
   const int L = __ldg(kv.seq_lens + b);
   if (o0 < 0 || o1 < o0 || o1 > a.rows || o1 - o0 > max(L, 0)) {
     if (tid == 0) set_error(err, HS_EBIT_BLOCK_RANGE);
     return;
   }
-  const int n = static_cast<int>(o1 - o0);
-  const int64_t x = slot - (o0 / B + 2 * static_cast<int64_t>(b));
+  const int n = o1 - o0, x = slot - (o0 / B + 2 * b);
   if (x < 0 || n == 0) return;
   const int first = L - n;  // cache position of the request's first new row
-  const int64_t j64 = first / B + x;
-  if (j64 > (L - 1) / B) return;
-  const int j = static_cast<int>(j64);
+  const int j = first / B + x;
+  if (j > (L - 1) / B) return;
   const int64_t pair = static_cast<int64_t>(b) * kv.hkv + kvh;
   if (j >= kv.max_blocks) {
     if (tid == 0) set_error(err, HS_EBIT_BLOCK_RANGE);
@@ -441,13 +439,13 @@ __global__ __launch_bounds__(threads_of(UW), (KIND == HS_KV_F32 ? 384 : 512) / t
   const int ra = max(0, first - j * B), rb = min(B, L - j * B);  // rows of the page that are new
   const void* src = is_k ? a.k : a.v;
   const int64_t stride = is_k ? a.k_stride : a.v_stride;
-  const int64_t src0 = o0 + (static_cast<int64_t>(j) * B - first);  // + page row = source row
+  const int64_t src0 = o0 + (j * B - first);  // + page row = source row
   void* pages = const_cast<void*>(is_k ? kv.k_pages : kv.v_pages);
   float* scales = const_cast<float*>(is_k ? kv.k_scales : kv.v_scales);
   const int rotary = is_k ? a.rotary : 0;
   const bool box = is_k && a.smin != nullptr;
   const int s = tid % TPR, rs = tid / TPR;
-  const Slot t = slot_of(s, a.rotary, a.interleaved);
+  const Slot t = slot_of(s, a.rotary, INTERLEAVED);
 
   // Page rows r0 + i RPP + rs, as they lie in memory: every load before the first
   // use; rows past the end repeat the last.
@@ -484,7 +482,7 @@ __global__ __launch_bounds__(threads_of(UW), (KIND == HS_KV_F32 ? 384 : 512) / t
       if (t.rotated) {
         Angles ang;
         load_angles(a.cos_sin, rotary, pos, s, ang);
-        rotate(u, w, ang, a.interleaved);
+        rotate<INTERLEAVED>(u, w, ang);
       }
     }
     return true;
@@ -668,7 +666,7 @@ __device__ __forceinline__ void widen_box(void* smin, void* smax, int64_t at, bo
   store8<F32>(smax, at, hi);
 }
 
-template <int D, int KIND>
+template <int D, int KIND, bool INTERLEAVED>
 __global__ __launch_bounds__(kThreads) void append_one_kernel(KvView kv, AppendTokensArgs a, int kv_ctas, unsigned* err) {
   constexpr bool F32 = KIND == HS_KV_F32;
   constexpr int TPR = D / 16, RPC = kThreads / TPR;  // threads per row, rows per CTA
@@ -680,14 +678,14 @@ __global__ __launch_bounds__(kThreads) void append_one_kernel(KvView kv, AppendT
     const int64_t q = static_cast<int64_t>(blockIdx.x - kv_ctas) * kWarps + warp;
     const int chunks = ceil_div(kv.hq, kQHeads);
     const int64_t row = q / chunks;
-    if (row < a.rows) rotate_q<D, F32>(kv, a, static_cast<int>(q - row * chunks) * kQHeads, row, row + 1, lane, err);
+    if (row < a.rows) rotate_q<D, F32, INTERLEAVED>(kv, a, static_cast<int>(q - row * chunks) * kQHeads, row, row + 1, lane, err);
     return;
   }
   const int s = tid % TPR, rs = tid / TPR;
   const int pairs = kv.batch * kv.hkv;
   const int pair = static_cast<int>(blockIdx.x) * RPC + rs;
   const int b = min(pair, pairs - 1) / kv.hkv, kvh = min(pair, pairs - 1) - b * kv.hkv;
-  const Slot t = slot_of(s, a.rotary, a.interleaved);
+  const Slot t = slot_of(s, a.rotary, INTERLEAVED);
   // the row itself needs no lookup
   float ku[8], kw[8], vu[8], vw[8];
   load8<F32>(a.k, b * a.k_stride + kvh * D + t.ca, ku);
@@ -720,7 +718,7 @@ __global__ __launch_bounds__(kThreads) void append_one_kernel(KvView kv, AppendT
       } else if (t.rotated) {
         Angles ang;
         load_angles(a.cos_sin, a.rotary, pos, s, ang);
-        rotate(ku, kw, ang, a.interleaved);
+        rotate<INTERLEAVED>(ku, kw, ang);
       }
     }
   }
@@ -825,7 +823,7 @@ __global__ __launch_bounds__(kThreads) void append_one_kernel(KvView kv, AppendT
   }
 }
 
-template <int D, int KIND, int UW>
+template <int D, int KIND, bool INTERLEAVED, int UW>
 cudaError_t launch_rows(const KvView& kv, const AppendTokensArgs& a, int sms, unsigned* err, cudaStream_t st) {
   constexpr int kThreads = threads_of(UW), kWarps = kThreads / 32, kUnits = kWarps / UW;
   const int64_t kv_units = kv_units_of(kv, a), kv_ctas = (kv_units + kUnits - 1) / kUnits;
@@ -835,23 +833,29 @@ cudaError_t launch_rows(const KvView& kv, const AppendTokensArgs& a, int sms, un
   // with the Q units, which keep the memory busy while they look up and reduce
   // (prompts of 16 requests 143 us, K and V first 155).
   const int64_t span = kv_ctas <= static_cast<int64_t>(sms) * (512 / kThreads) ? kv_ctas : ctas;
-  return launch_pdl(append_rows_kernel<D, KIND, UW>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, st, kv, a,
-                    kv_units, span, q_units, q_rows_of(kv, a), err);
+  const uint64_t mix = ((static_cast<uint64_t>(kv_ctas) << 32) + span - 1) / span;
+  return launch_pdl(append_rows_kernel<D, KIND, INTERLEAVED, UW>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, st, kv, a,
+                    static_cast<int>(kv_units), mix, static_cast<int>(q_units), q_rows_of(kv, a), err);
+}
+
+template <int D, int KIND, bool INTERLEAVED>
+cudaError_t launch_i(const KvView& kv, const AppendTokensArgs& a, int sms, unsigned* err, cudaStream_t st) {
+  if (!a.offsets) {
+    const int kv_ctas = static_cast<int>((static_cast<int64_t>(kv.batch) * kv.hkv + kThreads / (D / 16) - 1) / (kThreads / (D / 16)));
+    const int64_t ctas = kv_ctas + (q_units_of(kv, a) + kWarps - 1) / kWarps;
+    return launch_pdl(append_one_kernel<D, KIND, INTERLEAVED>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, st, kv, a, kv_ctas,
+                      err);
+  }
+  constexpr int kWarpRows = P * 32 / (D / 16);  // rows of a page that a warp reads at once
+  if (kv.block <= kWarpRows) return launch_rows<D, KIND, INTERLEAVED, 1>(kv, a, sms, err, st);
+  if (kv.block <= 2 * kWarpRows) return launch_rows<D, KIND, INTERLEAVED, 2>(kv, a, sms, err, st);
+  if (kv.block <= 4 * kWarpRows) return launch_rows<D, KIND, INTERLEAVED, 4>(kv, a, sms, err, st);
+  return launch_rows<D, KIND, INTERLEAVED, 8>(kv, a, sms, err, st);
 }
 
 template <int D, int KIND>
 cudaError_t launch_k(const KvView& kv, const AppendTokensArgs& a, int sms, unsigned* err, cudaStream_t st) {
-  if (!a.offsets) {
-    const int kv_ctas = static_cast<int>((static_cast<int64_t>(kv.batch) * kv.hkv + kThreads / (D / 16) - 1) / (kThreads / (D / 16)));
-    const int64_t ctas = kv_ctas + (q_units_of(kv, a) + kWarps - 1) / kWarps;
-    return launch_pdl(append_one_kernel<D, KIND>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, st, kv, a, kv_ctas,
-                      err);
-  }
-  constexpr int kWarpRows = P * 32 / (D / 16);  // rows of a page that a warp reads at once
-  if (kv.block <= kWarpRows) return launch_rows<D, KIND, 1>(kv, a, sms, err, st);
-  if (kv.block <= 2 * kWarpRows) return launch_rows<D, KIND, 2>(kv, a, sms, err, st);
-  if (kv.block <= 4 * kWarpRows) return launch_rows<D, KIND, 4>(kv, a, sms, err, st);
-  return launch_rows<D, KIND, 8>(kv, a, sms, err, st);
+  return a.interleaved ? launch_i<D, KIND, true>(kv, a, sms, err, st) : launch_i<D, KIND, false>(kv, a, sms, err, st);
 }
 
 template <int D>
