@@ -1,7 +1,8 @@
 /*
  * hs.h - C ABI of a GB300 (sm_103a) library for one decode step of query-aware
  * block-sparse attention over a paged KV cache, with a HiSparse-style hot
- * device buffer.
+ * device buffer, and for filling that cache (prompts and tokens, rotated by
+ * position on the way).
  *
  * The operations follow these pages:
  *   [KVS] "KV 稀疏化" (KV-cache sparsity wiki): §2 attention sink + sliding
@@ -197,8 +198,10 @@ typedef struct hs_select_params {
  * counts, whatever blocks_per_split and these flags say, and needs no more
  * workspace for more requests; it waits for nothing but its own copies, so
  * wait_limit_ns does not concern it; max_ctas as above; without split_counters
- * it merges in a second launch.  Pools of 2^32 token rows and selections of 2^31
- * tokens are not supported. */
+ * it merges in a second launch.  Pools of 2^32 token rows, and selections of 2^31
+ * tokens or (over all requests and kv heads) 2^36, are not supported.
+ * Calls that may overlap on the GPU (other streams, graphs replayed side by side)
+ * need a workspace and split_counters each. */
 #define HS_ATTN_EARLY_SUMMARIES 1u
 #define HS_ATTN_RANGES 2u
 #define HS_ATTN_NO_RANGES 4u
@@ -265,7 +268,8 @@ HS_API size_t hs_workspace_bytes(const hs_attn_shape* shape, int32_t batch, int3
  * *chunks_per_cta = the length of a balanced chunk range (0 = equal splits
  * per pair instead).  Returns 0, or -1 on invalid input (outputs untouched).
  * Without a device it assumes 148 SMs, as hs_workspace_bytes does.  The
- * CUDA-core kernel always uses equal splits. */
+ * CUDA-core kernel always uses equal splits.  Both are 0 for a cache with a
+ * scale per page, whose kernel divides by the counts it finds on the device. */
 HS_API int32_t hs_attn_geometry(const hs_attn_shape* shape, int32_t batch, int32_t capacity,
                                 const hs_attn_params* params, int32_t* splits, int32_t* chunks_per_cta);
 

@@ -6,7 +6,8 @@ loudly when the library has not been built) and ``.decode`` a small decode-step
 driver.  ``python -m query_aware_sparse_hs_gb300.build`` compiles the library.
 """
 
-_BINDING = ("HSError", "attn_params", "attn_shape", "hot_buffer", "hs_build_block_summaries",
+_BINDING = ("HSError", "append_params", "attn_params", "attn_shape", "hot_buffer", "hs_append_tokens",
+            "hs_build_block_summaries",
             "hs_get_device_error", "hs_quantize_e4m3_g32", "hs_score_select_topk",
             "hs_sparse_paged_decode_attn", "hs_status_string", "hs_swapin_misses", "hs_version",
             "hs_workspace_bytes", "paged_kv", "select_params")

@@ -269,6 +269,9 @@ def append_params(cos_sin=None, interleaved=False, new_offsets=None, positions=N
     return p
 
 
+_append_tokens, _byref = _lib.hs_append_tokens, ctypes.byref
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+_BF16, _F32 = torch.bfloat16, torch.float32
 _NEW_ROWS = "{} must be [{}][{}][{}] of {} with contiguous rows, on the current device"
 
 
@@ -285,9 +288,10 @@ def _new_rows(t, rows, heads, dim, dtype, device, what):
 def hs_append_tokens(shape, kv, params, new_k, new_v, q=None, q_out=None, smin=None, smax=None, stream=None):
     """Any number of new tokens per request into the paged cache, K and Q rotated on the way (see hs.h).  new_k,
     new_v [rows][Hkv][D], q, q_out [rows][Hq][D]; the rows may be strided views (of a fused projection)."""
-    dim, hkv, rows = shape.head_dim, shape.num_kv_heads, new_k.shape[0]
-    dtype = torch.float32 if shape.kv_dtype == 0 else torch.bfloat16
-    device = torch._C._cuda_getDevice() if new_k.is_cuda else -2
+    dim, hkv = shape.head_dim, shape.num_kv_heads
+    rows = new_k.shape[0]
+    dtype = _BF16 if shape.kv_dtype else _F32
+    device = _current_device() if new_k.is_cuda else -2
     kp, ks = _new_rows(new_k, rows, hkv, dim, dtype, device, "new_k")
     vp, vs = _new_rows(new_v, rows, hkv, dim, dtype, device, "new_v")
     if q is not None and q_out is not None:
@@ -303,12 +307,8 @@ def hs_append_tokens(shape, kv, params, new_k, new_v, q=None, q_out=None, smin=N
         raise ValueError("new_offsets must have batch + 1 entries")
     if params._rows is not None and params._rows < rows:
         raise ValueError("positions must have an entry for every row")
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device)
-    elif stream.__class__ is not int:
-        stream = stream.cuda_stream
-    st = _lib.hs_append_tokens(ctypes.byref(shape), ctypes.byref(kv), ctypes.byref(params), rows, qp, qs, op, os_, kp, ks,
-                               vp, vs, _ptr(smin), _ptr(smax), stream)
+    st = _append_tokens(_byref(shape), _byref(kv), _byref(params), rows, qp, qs, op, os_, kp, ks, vp, vs, _ptr(smin),
+                        _ptr(smax), _raw_stream(device) if stream is None else _stream(stream))
     if st:
         raise HSError(st, "hs_append_tokens")
 

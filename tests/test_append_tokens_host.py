@@ -97,6 +97,15 @@ def test_workspace_of_the_block_scaled_attention_does_not_grow_with_the_batch():
     assert hs.hs_workspace_bytes(hs.attn_shape(32, 4, 128, 64, "fp8_block"), 8, 2048, p) == small
 
 
+def test_geometry_queries_of_the_block_scaled_cache():
+    from query_aware_sparse_hs_gb300 import hs
+    shape, p = hs.attn_shape(32, 4, 128, 64, "fp8_block"), hs.attn_params(0.1)
+    assert hs.hs_attn_geometry(shape, 8, 64, p) == (0, 0)
+    assert hs.hs_score_select_attend_fused(shape, 8, 512, 64, p) in (0, -1)  # (-1: no device here)
+    assert hs.hs_score_select_attend_workspace_bytes(shape, 8, 512, 64, p) == \
+        hs.hs_select_workspace_bytes(shape, 8, 512) + hs.hs_workspace_bytes(shape, 8, 64, p)
+
+
 def test_the_binding_checks_shapes_and_types():
     from query_aware_sparse_hs_gb300 import hs
     shape = hs.attn_shape(8, 2, 64, 16, "bf16")

@@ -338,6 +338,66 @@ def test_captured_and_replayed_with_other_lengths_and_on_another_stream():
     assert torch.equal(again, out)
 
 
+def test_two_calls_at_once_with_their_own_workspaces():
+    a, b = Cache([5000, 70], 2, 128, 16, seed=9), Cache([20, 9000, 3], 1, 64, 64, seed=10)
+    qa, qb = query(a, 16), query(b, 16)
+    want = [attend(a, qa, *chosen(a, max(a.nb), None)), attend(b, qb, *chosen(b, max(b.nb), None))]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = []
+        for s, c, q in zip(streams, (a, b), (qa, qb)):
+            with torch.cuda.stream(s):
+                got.append(attend(c, q, *chosen(c, max(c.nb), None)))
+        torch.cuda.synchronize()
+        for (o, l), (wo, wl) in zip(got, want):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+def test_pages_past_4_gib_of_the_pool():
+    """Append, summaries and attention on pages whose byte offsets pass 32 bits."""
+    from query_aware_sparse_hs_gb300 import hs
+    d, block, lens = 128, 64, [130, 64]
+    pages = (1 << 32) // (d * block) + 40
+    k = torch.empty((pages, block, d), dtype=torch.uint8, device="cuda")
+    v = torch.empty((pages, block, d), dtype=torch.uint8, device="cuda")
+    ks, vs = torch.empty(pages, device="cuda"), torch.empty(pages, device="cuda")
+    table = (pages - 1 - 3 * torch.arange(2 * 3, dtype=torch.int32).view(2, 1, 3)).cuda()
+    gl = torch.tensor(lens, dtype=torch.int32).cuda()
+    kv = hs.paged_kv(k, v, table, gl, ks, vs)
+    shape = hs.attn_shape(4, 1, d, block, "fp8_block")
+    rows = torch.randn((sum(lens), 2, d), device="cuda").to(torch.bfloat16)
+    off = torch.tensor([0, 130, 194], dtype=torch.int32).cuda()
+    smin = torch.zeros((2, 1, 3, d), dtype=torch.bfloat16, device="cuda")
+    smax = smin.clone()
+    hs.hs_append_tokens(shape, kv, hs.append_params(new_offsets=off), rows[:, :1], rows[:, 1:], None, None, smin, smax)
+    gl += 1
+    one = torch.randn((2, 2, d), device="cuda").to(torch.bfloat16)
+    hs.hs_append_tokens(shape, kv, hs.append_params(), one[:, :1], one[:, 1:], None, None, smin, smax)
+    assert hs.hs_get_device_error() == (hs.HS_OK, 0)
+    c = Cache.__new__(Cache)
+    c.lens, c.hkv, c.d, c.block, c.nb, c.kv, c.rng = [131, 65], 1, d, block, [3, 2], kv, np.random.default_rng(1)
+    used = table.flatten().long()
+    at = {int(p): i for i, p in enumerate(used)}
+    c.table = np.array([[[at[int(table[b, 0, j])] for j in range(3)]] for b in range(2)], np.int32)
+    c.codes, c.scales = {"k": k[used].cpu().numpy(), "v": v[used].cpu().numpy()}, {"k": ks[used].cpu().numpy(), "v": vs[used].cpu().numpy()}
+    for b, L in enumerate(lens):  # what was appended is there
+        src = torch.cat([rows[130 * b:130 * b + L], one[b:b + 1]]).double().cpu().numpy()
+        for w, i in (("k", 0), ("v", 1)):
+            x = c.rows(w, b, 0, range(c.nb[b]))
+            s = np.repeat(c.scales[w][c.table[b, 0, :c.nb[b]]], block)[:L + 1, None]
+            # half a step of the code, twice where the page's scale grew
+            assert (np.abs(x - src[:, i]) <= np.maximum(2.0 ** -4 * np.abs(src[:, i]), 2 * 2.0 ** -10 * s)).all()
+    lo, hi = torch.zeros_like(smin), torch.zeros_like(smax)
+    hs.hs_build_block_summaries(shape, kv, 0, lo, hi)
+    assert torch.equal(lo, smin) and torch.equal(hi, smax)
+    q = query(c, 4)
+    sel, cnt = chosen(c, 3, None)
+    for algo in ("auto", "simt"):
+        out, lse = attend(c, q, sel, cnt, algo=algo)
+        check_attention(c, q, sel, cnt, out, lse, simt=algo == "simt")
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("block", [1, 5, 16, 48, 64, 256])
 def test_summaries_match_the_definition(d, block):
