@@ -52,7 +52,9 @@ constexpr int kMaxWarps = 3 * kTeamWarps;
 constexpr int kTile = 32;       // tokens a warp handles at a time
 constexpr int kStages = 3;      // tiles in a warp's ring
 constexpr int kMinTiles = 8;    // tiles of a part of a cut pair at least
-constexpr int kWholeTiles = 32;  // pairs of up to so many tiles are not cut
+// Pairs of up to so many tiles are not cut: two for each warp of a CTA (4 pairs of
+// 1000 tokens, 128 channels, 32 tiles: 9.6 us cut, 11.0 whole; 16 tiles: 8.2 whole).
+__host__ __device__ constexpr int whole_tiles(int teams) { return 2 * teams * kTeamWarps; }
 constexpr int kMergeTiles = 2;  // what a merge costs, in tiles per warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinRef = 7.888609052210118e-31f;  // 2^-100
@@ -178,7 +180,7 @@ struct Team {
 //   than a merge.  32 requests x 4 heads x 4096 selected tokens: joint 28 us, teams
 //   31.5; 24 uneven requests x 4 heads: 55 and 48; 64 x 4 heads x 4096: 52 and 48.
 struct Cut {
-  int per, slots;
+  int per, slots, whole;
   bool joint;
 };
 struct Part {
@@ -191,8 +193,8 @@ struct Pairs {  // one pair's numbers
 };
 constexpr int kListed = 32;  // parts a team notes at a time
 
-__device__ __forceinline__ int parts_of(int tiles, int per) {
-  return tiles <= kWholeTiles ? (tiles > 0 ? 1 : 0) : (tiles + per - 1) / per;
+__device__ __forceinline__ int parts_of(int tiles, int per, int whole) {
+  return tiles <= whole ? (tiles > 0 ? 1 : 0) : (tiles + per - 1) / per;
 }
 __device__ __forceinline__ int per_of(int total, int pairs, int slots) {
   return max((total - 1) / max(max(slots - pairs, slots / 2), 1) + 1, kMinTiles);
@@ -222,12 +224,13 @@ __device__ Cut choose_cut(const KvView& kv, const BlockArgs& a, int ctas, int te
   int total = 0;
   for (int w = 0; w < cta.warps; ++w) total += sc.tiles[w];
   const int per_joint = per_of(total, pairs, ctas), per_team = per_of(total, pairs, ctas * teams);
+  const int whole = whole_tiles(teams);
   int parts = 0, joint = 0, team = 0;  // parts of joint cutting; the longest part either way
   for (int p = p0; p < p1; ++p) {
-    const int n = tiles_of(kv, pair_count(kv, a, p)), k = parts_of(n, per_joint);
+    const int n = tiles_of(kv, pair_count(kv, a, p)), k = parts_of(n, per_joint, whole);
     parts += k;
     if (k > 0) {
-      const int kt = parts_of(n, per_team);
+      const int kt = parts_of(n, per_team, whole);
       joint = max(joint, (n + k - 1) / k);
       team = max(team, (n + kt - 1) / kt);
     }
@@ -248,6 +251,7 @@ __device__ Cut choose_cut(const KvView& kv, const BlockArgs& a, int ctas, int te
     team = max(team, sc.longest[1][w]);
   }
   Cut cut;
+  cut.whole = whole;
   cut.joint = parts <= ctas && joint <= (team / kTeamWarps + kMergeTiles) * kTeamWarps * teams;
   cut.slots = cut.joint ? ctas : ctas * teams;
   cut.per = cut.joint ? per_joint : per_team;
@@ -263,7 +267,7 @@ __device__ int number_parts(const KvView& kv, const BlockArgs& a, const Cut& cut
   const int p0 = min(pairs, team.rank * mine_n), p1 = min(pairs, p0 + mine_n);
   int64_t mine = 0;  // parts, and rows of the workspace in the upper half
   for (int p = p0; p < p1; ++p) {
-    const int k = parts_of(tiles_of(kv, pair_count(kv, a, p)), cut.per);
+    const int k = parts_of(tiles_of(kv, pair_count(kv, a, p)), cut.per, cut.whole);
     mine += k + (k > 1 ? static_cast<int64_t>(k) << 32 : 0);
   }
   int64_t at = mine;
@@ -282,7 +286,7 @@ __device__ int number_parts(const KvView& kv, const BlockArgs& a, const Cut& cut
   }
   for (int p = p0; p < p1; ++p) {
     Pairs n;
-    n.count = parts_of(tiles_of(kv, pair_count(kv, a, p)), cut.per);
+    n.count = parts_of(tiles_of(kv, pair_count(kv, a, p)), cut.per, cut.whole);
     n.part = static_cast<int>(at & 0xffffffff);
     n.row = static_cast<int>(at >> 32);
     each(p, n);
