@@ -196,7 +196,7 @@ cudaError_t launch_k(const KvView& kv, int first_block, int nblocks, void* smin,
 // none with other warps.  The blocks of all requests and kv heads are laid end to
 // end and cut into equal runs, one per warp (every warp sums the requests' block
 // counts); a warp looks up 32 blocks of its run together and loads the next 16
-// rows (64 channels: 32) while it folds the last.
+// rows (64 channels: 32; half as many for short blocks) while it folds the last.
 __device__ __forceinline__ void codes_to_half2(uint32_t w, __half2& a, __half2& b) {
   uint32_t x, y;
   asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
@@ -210,11 +210,12 @@ __device__ __forceinline__ __half2 shfl_half2(__half2 v, int off) {
   return *reinterpret_cast<const __half2*>(&x);
 }
 
-constexpr int kBlockCtas = 3;  // CTAs of the kernel per SM
-constexpr int kRows = 16;      // loads in flight
+// Loads in flight: 16, or 8 where those are a whole block.  CTAs per SM: as the
+// registers allow.
+constexpr int block_ctas(int rows) { return rows == 16 ? 3 : 5; }
 
-template <int D>
-__global__ __launch_bounds__(kWarps * 32, kBlockCtas) void summaries_block_kernel(KvView kv, int first_block, void* smin,
+template <int D, int kRows>
+__global__ __launch_bounds__(kWarps * 32, block_ctas(kRows)) void summaries_block_kernel(KvView kv, int first_block, void* smin,
                                                                                  void* smax, unsigned* err) {
   constexpr int RPL = 128 / D;  // rows of one warp load
   constexpr int kStep = kRows * RPL;
@@ -356,13 +357,22 @@ __global__ __launch_bounds__(kWarps * 32, kBlockCtas) void summaries_block_kerne
   }
 }
 
+template <int D, int kRows>
+cudaError_t launch_block_rows(const KvView& kv, int first_block, int nblocks, void* smin, void* smax, unsigned* err,
+                              int sms, cudaStream_t st) {
+  // a warp for each block at most
+  const int64_t most = (static_cast<int64_t>(kv.batch) * kv.hkv * nblocks + kWarps - 1) / kWarps;
+  const int resident = sms * block_ctas(kRows);
+  const unsigned grid = static_cast<unsigned>(most < resident ? most : resident);
+  return launch_pdl(summaries_block_kernel<D, kRows>, dim3(grid), dim3(kWarps * 32), 0, st, kv, first_block, smin, smax,
+                    err);
+}
+
 template <int D>
 cudaError_t launch_block(const KvView& kv, int first_block, int nblocks, void* smin, void* smax, unsigned* err,
                          int sms, cudaStream_t st) {
-  // a warp for each block at most
-  const int64_t most = (static_cast<int64_t>(kv.batch) * kv.hkv * nblocks + kWarps - 1) / kWarps;
-  const unsigned grid = static_cast<unsigned>(most < sms * kBlockCtas ? most : sms * kBlockCtas);
-  return launch_pdl(summaries_block_kernel<D>, dim3(grid), dim3(kWarps * 32), 0, st, kv, first_block, smin, smax, err);
+  return kv.block <= 8 * (128 / D) ? launch_block_rows<D, 8>(kv, first_block, nblocks, smin, smax, err, sms, st)
+                                   : launch_block_rows<D, 16>(kv, first_block, nblocks, smin, smax, err, sms, st);
 }
 
 template <int D>
