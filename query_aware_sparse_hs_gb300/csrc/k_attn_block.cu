@@ -21,11 +21,24 @@
 //   S[token][head] = K . Q^T: 16 tokens by 8 heads, so that the group of query
 //     heads that shares the kv head fills the instruction's narrow side;
 //   O^T[channel][head] += V^T . P^T: 16 channels by 8 heads over 16 tokens.
+// (tcgen05 would take K's codes as they are, but P and V through shared and tensor
+// memory: that chain, not the products, bounds the kernel of grouped scales at
+// half the copy rate; here the matrix pipe is 6% busy, and its e4m3 form of this
+// instruction, which converts inside, was slower by an eighth.)
 // Order of the contracted channels and of the output's channels is free, so a
 // lane's operands are whole 16-byte pieces of a row as it lies in memory; V's
 // transposition is one byte permutation per two operands.  Rows lie in shared
 // memory with their 16-byte pieces XOR-permuted, so that neither reading order
 // has bank conflicts.
+//
+// What bounds it: memory, for long work (16 requests x 4 heads x 131072 tokens, 2.15
+// GB: 322 us, 1.0 of the copy rate; 64 channels 0.83).  Before it streams, a part
+// waits for a chain of lookups (counts, selection, pages, rows: 4 us), after it
+// for the join of its warps and the merge (3 to 4 us): 32 requests x 4096 selected
+// tokens, 134 MB: 29 us, 0.69.  With 16 query heads and 64 channels a 32-token
+// tile takes an SM about 240 cycles whatever the number of warps: conversions
+// (120 cycles: the instruction retires 17 code pairs a cycle) and the other
+// arithmetic of 16 heads' softmax.
 //
 // Precision: q times a power of two per head (largest entry into [128, 256)) is
 // exact in f16 for entries within 2^-21 of the largest, and absolutely within
@@ -46,7 +59,8 @@ namespace {
 constexpr int kTeamWarps = 4;
 // Teams of a CTA, and with them the warps of an SM (one CTA on each): as many as
 // the registers (128 channels: up to 255 a thread, 64 channels: 168) and the
-// rings of tiles allow.
+// rings of tiles allow.  64 channels, 32 x 4 heads x 65536 tokens: 12 warps 195 us, 8
+// warps 222, 16 warps (128 registers) 192 but slower for short requests.
 __host__ __device__ constexpr int teams_of(int head_dim) { return head_dim == 128 ? 2 : 3; }
 constexpr int kMaxWarps = 3 * kTeamWarps;
 constexpr int kTile = 32;       // tokens a warp handles at a time
@@ -55,7 +69,7 @@ constexpr int kMinTiles = 8;    // tiles of a part of a cut pair at least
 // Pairs of up to so many tiles are not cut: two for each warp of a CTA (4 pairs of
 // 1000 tokens, 128 channels, 32 tiles: 9.6 us cut, 11.0 whole; 16 tiles: 8.2 whole).
 __host__ __device__ constexpr int whole_tiles(int teams) { return 2 * teams * kTeamWarps; }
-constexpr int kMergeTiles = 2;  // what a merge costs, in tiles per warp
+constexpr int kMergeTiles = 3;  // what a merge costs, in tiles per warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinRef = 7.888609052210118e-31f;  // 2^-100
 constexpr float kLn2 = 0.6931471805599453f;
@@ -177,8 +191,8 @@ struct Team {
 //   time of a short part; with more pairs than CTAs, or pairs so uneven that CTAs
 //   are left idle, teams balance better.  Taken where every CTA has one part at
 //   most and the longest, in tiles per warp, is not longer than the teams' by more
-//   than a merge.  32 requests x 4 heads x 4096 selected tokens: joint 28 us, teams
-//   31.5; 24 uneven requests x 4 heads: 55 and 48; 64 x 4 heads x 4096: 52 and 48.
+//   than a merge.  32 requests x 4 heads x 4096 selected tokens: joint 29 us, teams
+//   32; 24 uneven requests x 4 heads: 56 and 48; 64 x 4 heads x 4096: 54 and 49.
 struct Cut {
   int per, slots, whole;
   bool joint;
@@ -496,7 +510,8 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
     const int tiles = seg0 + seg_tiles * (team_warp + 1) / team.warps - run0;
     // Selected blocks are looked up 32 at a time, one to a lane, the pages one
     // window ahead of the copies and the selection two, so that neither load is
-    // waited for.  A window holds the entries from that of its first tile on;
+    // waited for (looked up tile by tile, one tile ahead, 16-token pages took 458 us
+    // where they now take 328).  A window holds the entries from that of its first tile on;
     // a tile that does not fit opens the next.
     const uint32_t u0 = static_cast<uint32_t>(run0) * kTile, u_stop = u0 + static_cast<uint32_t>(tiles) * kTile;
     const uint32_t Bu = B;

@@ -197,6 +197,8 @@ cudaError_t launch_k(const KvView& kv, int first_block, int nblocks, void* smin,
 // end and cut into equal runs, one per warp (every warp sums the requests' block
 // counts); a warp looks up 32 blocks of its run together and loads the next 16
 // rows (64 channels: 32; half as many for short blocks) while it folds the last.
+// Memory-bound: 32 requests x 4 heads of 4K to 64K tokens, 16-token pages of 128
+// channels, 770 MB: 128 us, 0.90 of the copy rate (the common kernel above: 400).
 __device__ __forceinline__ void codes_to_half2(uint32_t w, __half2& a, __half2& b) {
   uint32_t x, y;
   asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
@@ -210,7 +212,8 @@ __device__ __forceinline__ __half2 shfl_half2(__half2 v, int off) {
   return *reinterpret_cast<const __half2*>(&x);
 }
 
-// Loads in flight: 16, or 8 where those are a whole block.  CTAs per SM: as the
+// Loads in flight: 16, or 8 where those are a whole block (64 channels, 16-token
+// pages: 78 us, with 16 loads, half of them repeats, 112).  CTAs per SM: as the
 // registers allow.
 constexpr int block_ctas(int rows) { return rows == 16 ? 3 : 5; }
 
