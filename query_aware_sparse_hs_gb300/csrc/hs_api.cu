@@ -410,7 +410,8 @@ hs_status hs_append_tokens(const hs_attn_shape* shape, const hs_paged_kv* kv, co
   hs_status st = check_shape(shape);
   if (st != HS_OK) return st;
   if ((st = check_kv(shape, kv, true)) != HS_OK) return st;
-  if (!params || rows < 0 || rows > INT32_MAX || !k || !v || !q != !q_out || !smin != !smax) return HS_ERR_INVALID_ARG;
+  if (!params || rows < 0 || rows > INT32_MAX || !q != !q_out || !smin != !smax) return HS_ERR_INVALID_ARG;
+  if (rows > 0 && (!k || !v)) return HS_ERR_INVALID_ARG;
   if (!params->new_offsets && rows != kv->batch) return HS_ERR_INVALID_ARG;
   const int D = shape->head_dim, lane16 = shape->kv_dtype == HS_KV_F32 ? 4 : 8;  // values in 16 bytes
   const auto rows_ok = [&](const void* p, int64_t stride, int heads) {

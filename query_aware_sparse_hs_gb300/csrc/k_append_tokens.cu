@@ -61,9 +61,10 @@ __device__ __forceinline__ int last_not_above(int n, int x, int lane, F key) {
 template <bool F32>
 struct Raw8 {
   uint4 v[F32 ? 2 : 1];
+  // (plain loads: Q may be rotated in place, next to K and V in the same rows)
   __device__ __forceinline__ void load(const uint8_t* p) {
-    v[0] = __ldg(reinterpret_cast<const uint4*>(p));
-    if constexpr (F32) v[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    v[0] = reinterpret_cast<const uint4*>(p)[0];
+    if constexpr (F32) v[1] = reinterpret_cast<const uint4*>(p)[1];
   }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     const uint32_t r[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
@@ -84,7 +85,8 @@ struct Raw8 {
   }
 };
 
-// Eight f32 or bf16 values.  INPUT: nothing in the kernel writes them.
+// Eight f32 or bf16 values.  INPUT: nothing in the kernel writes them or next to
+// them.
 template <bool F32, bool INPUT = true>
 __device__ __forceinline__ void load8(const void* p, int64_t at, float (&x)[8]) {
   if constexpr (F32) {
@@ -379,13 +381,15 @@ __device__ __forceinline__ uint4 rescaled(uint4 v, float f) {
 // A unit is one touched block of one kv head, K or V, taken by UW warps: as many
 // as let the page's rows be read in P = 4 passes (pages of more than 8 warps'
 // rows are taken in turns; with four warps for every page size, prompts into
-// 16-token bf16 pages took 179 us where one warp takes 140).  The rows of the passes are read together and,
-// block-scaled, held, as read, until the scale is known.
+// 16-token bf16 pages took 179 us where one warp takes 140).  The rows of the
+// passes are read together and, block-scaled, held, as read, until the scale is
+// known.
 constexpr int P = 4;
 constexpr int threads_of(int unit_warps) { return unit_warps > 4 ? 32 * unit_warps : 128; }
 
 template <int D, int KIND, bool INTERLEAVED, int UW>
-__global__ __launch_bounds__(threads_of(UW), (KIND == HS_KV_F32 ? 384 : 512) / threads_of(UW)) void append_rows_kernel(KvView kv, AppendTokensArgs a, int kv_units, uint64_t mix, int q_units, int q_rows, unsigned* err) {
+__global__ __launch_bounds__(threads_of(UW), (KIND == HS_KV_F32 ? 384 : 512) / threads_of(UW)) void append_rows_kernel(
+    KvView kv, AppendTokensArgs a, int kv_units, uint64_t mix, int q_units, int q_rows, unsigned* err) {
   constexpr bool F32 = KIND == HS_KV_F32;
   constexpr int kWarps = threads_of(UW) / 32, kUnits = kWarps / UW;  // of a CTA
   constexpr int TPR = D / 16, RPP = UW * 32 / TPR;  // threads per row, rows per pass of a unit
@@ -406,7 +410,7 @@ __global__ __launch_bounds__(threads_of(UW), (KIND == HS_KV_F32 ? 384 : 512) / t
     if (q >= q_units) return;
     const int chunks = ceil_div(kv.hq, kQHeads), r = q / chunks;
     rotate_q<D, F32, INTERLEAVED>(kv, a, (q - r * chunks) * kQHeads, static_cast<int64_t>(r) * q_rows,
-                     min(a.rows, (r + int64_t(1)) * q_rows), lane, err);
+                                  min(a.rows, (r + int64_t(1)) * q_rows), lane, err);
     return;
   }
   // ---- which block ----
@@ -695,10 +699,10 @@ __global__ __launch_bounds__(kThreads) void append_one_kernel(KvView kv, AppendT
   const Slot t = slot_of(s, a.rotary, INTERLEAVED);
   // the row itself needs no lookup
   float ku[8], kw[8], vu[8], vw[8];
-  load8<F32>(a.k, b * a.k_stride + kvh * D + t.ca, ku);
-  load8<F32>(a.k, b * a.k_stride + kvh * D + t.cb, kw);
-  load8<F32>(a.v, b * a.v_stride + kvh * D + t.ca, vu);
-  load8<F32>(a.v, b * a.v_stride + kvh * D + t.cb, vw);
+  load8<F32, false>(a.k, b * a.k_stride + kvh * D + t.ca, ku);
+  load8<F32, false>(a.k, b * a.k_stride + kvh * D + t.cb, kw);
+  load8<F32, false>(a.v, b * a.v_stride + kvh * D + t.ca, vu);
+  load8<F32, false>(a.v, b * a.v_stride + kvh * D + t.cb, vw);
   const int B = kv.block, L = __ldg(kv.seq_lens + b);
   const int p = L - 1, j = p / B, r = p - j * B;
   bool live = pair < pairs && L > 0, live_k = false;

@@ -256,6 +256,33 @@ def test_without_query_and_without_summaries(kind):
     check(w)
 
 
+def test_no_rows_at_all():
+    """Nothing to append: an empty batch of rows is not an error, and nothing changes."""
+    w = World("fp8_block", 64, 16, 4, 2, [5, 20], [0, 0], 64, pad=0, seed=2)
+    keep = [t.clone() for t in (w.g["k"], w.gs["k"], w.smin)]
+    assert w.kn.shape[0] == 0 and w.params._requests == 2
+    w.append()
+    assert w.hs.hs_get_device_error() == (w.hs.HS_OK, 0)
+    for a, b in zip(keep, (w.g["k"], w.gs["k"], w.smin)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "fp8_block"])
+@pytest.mark.parametrize("n", [1, 20])
+def test_channels_of_nothing_but_not_a_number(kind, n):
+    """Their summary is what the builder gives (no bound at all), and does not spoil what later rows give."""
+    w = World(kind, 64, 16, 2, 1, [0], [n], 0, seed=3)
+    w.kn[:, :, 5] = float("nan")
+    w.append()
+    check_summaries(w)
+    w.gl += 1
+    w.offsets = None
+    row = torch.ones((1, 1, 64), dtype=w.wide, device="cuda")
+    w.hs.hs_append_tokens(w.shape, w.kv, w.hs.append_params(), row, row, None, None, w.smin, w.smax)
+    check_summaries(w)
+    assert torch.isfinite(w.smin[0, 0, n // 16]).all()
+
+
 def test_query_in_place():
     w = World("bf16", 128, 16, 4, 2, [20, 0], [30, 3], 128, seed=6)
     w.append()

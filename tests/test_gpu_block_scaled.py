@@ -283,6 +283,16 @@ def test_bad_selections_and_pages_are_reported_and_skipped():
         assert torch.equal(out3[1], good[1])
 
 
+def test_a_block_selected_twice_counts_twice():
+    c = Cache([500], 1, 128, 16, seed=7)
+    q = query(c, 8)
+    sel = np.array([[[3, 3, 31, 0, 31, 31]]], np.int32)
+    cnt = np.array([[6]], np.int32)
+    for algo in ("auto", "simt"):
+        out, lse = attend(c, q, sel, cnt, algo=algo)
+        check_attention(c, q, sel, cnt, out, lse, simt=algo == "simt")
+
+
 def test_no_allocation_call_and_workspace_checks():
     from query_aware_sparse_hs_gb300 import hs
     c = Cache([300, 200], 2, 128, 64, seed=8)
