@@ -190,8 +190,8 @@ struct Team {
 //   Joint parts halve (64 channels: third) the parts, and so the merges, and the
 //   time of a short part; with more pairs than CTAs, or pairs so uneven that CTAs
 //   are left idle, teams balance better.  Taken where every CTA has one part at
-//   most and the longest, in tiles per warp, is not longer than the teams' by more
-//   than a merge.  32 requests x 4 heads x 4096 selected tokens: joint 29 us, teams
+//   most and the longest pair's, in tiles per warp, is not longer than the teams' by
+//   more than a merge.  32 requests x 4 heads x 4096 selected tokens: joint 29 us, teams
 //   32; 24 uneven requests x 4 heads: 56 and 48; 64 x 4 heads x 4096: 54 and 49.
 struct Cut {
   int per, slots, whole;
@@ -210,13 +210,17 @@ constexpr int kListed = 32;  // parts a team notes at a time
 __device__ __forceinline__ int parts_of(int tiles, int per, int whole) {
   return tiles <= whole ? (tiles > 0 ? 1 : 0) : (tiles + per - 1) / per;
 }
+__device__ __forceinline__ int part_of(int tiles, int per) {  // the longest part of a pair that is cut
+  const int k = max((tiles + per - 1) / per, 1);
+  return (tiles + k - 1) / k;
+}
 __device__ __forceinline__ int per_of(int total, int pairs, int slots) {
   return max((total - 1) / max(max(slots - pairs, slots / 2), 1) + 1, kMinTiles);
 }
 
 struct Scratch {
   int64_t sums[kMaxWarps];
-  int tiles[kMaxWarps], parts[kMaxWarps], longest[2][kMaxWarps];
+  int tiles[kMaxWarps], longest[kMaxWarps];
 };
 
 // The cut for this call's counts, by all threads of a CTA (`cta`).  seen(p, count)
@@ -226,47 +230,32 @@ __device__ Cut choose_cut(const KvView& kv, const BlockArgs& a, int ctas, int te
   const int warp = cta.rank >> 5, lane = cta.rank & 31;
   const int pairs = kv.batch * kv.hkv, mine_n = (pairs + cta.threads() - 1) / cta.threads();
   const int p0 = min(pairs, cta.rank * mine_n), p1 = min(pairs, p0 + mine_n);
-  int tiles = 0;
+  int total = 0, longest = 0;  // tiles
   for (int p = p0; p < p1; ++p) {
-    const int c = pair_count(kv, a, p);
+    const int c = pair_count(kv, a, p), n = tiles_of(kv, c);
     seen(p, c);
-    tiles += tiles_of(kv, c);
+    total += n;
+    longest = max(longest, n);
   }
-  tiles = __reduce_add_sync(0xffffffffu, tiles);
-  if (lane == 0) sc.tiles[warp] = tiles;
-  cta.sync();
-  int total = 0;
-  for (int w = 0; w < cta.warps; ++w) total += sc.tiles[w];
-  const int per_joint = per_of(total, pairs, ctas), per_team = per_of(total, pairs, ctas * teams);
-  const int whole = whole_tiles(teams);
-  int parts = 0, joint = 0, team = 0;  // parts of joint cutting; the longest part either way
-  for (int p = p0; p < p1; ++p) {
-    const int n = tiles_of(kv, pair_count(kv, a, p)), k = parts_of(n, per_joint, whole);
-    parts += k;
-    if (k > 0) {
-      const int kt = parts_of(n, per_team, whole);
-      joint = max(joint, (n + k - 1) / k);
-      team = max(team, (n + kt - 1) / kt);
-    }
-  }
-  parts = __reduce_add_sync(0xffffffffu, parts);
-  joint = __reduce_max_sync(0xffffffffu, joint);
-  team = __reduce_max_sync(0xffffffffu, team);
+  total = __reduce_add_sync(0xffffffffu, total);
+  longest = __reduce_max_sync(0xffffffffu, longest);
   if (lane == 0) {
-    sc.parts[warp] = parts;
-    sc.longest[0][warp] = joint;
-    sc.longest[1][warp] = team;
+    sc.tiles[warp] = total;
+    sc.longest[warp] = longest;
   }
   cta.sync();
-  parts = 0;
+  total = longest = 0;
   for (int w = 0; w < cta.warps; ++w) {
-    parts += sc.parts[w];
-    joint = max(joint, sc.longest[0][w]);
-    team = max(team, sc.longest[1][w]);
+    total += sc.tiles[w];
+    longest = max(longest, sc.longest[w]);
   }
+  const int per_joint = per_of(total, pairs, ctas), per_team = per_of(total, pairs, ctas * teams);
   Cut cut;
-  cut.whole = whole;
-  cut.joint = parts <= ctas && joint <= (team / kTeamWarps + kMergeTiles) * kTeamWarps * teams;
+  cut.whole = whole_tiles(teams);
+  // no more joint parts than CTAs: the pairs leave room for the cuts, or none is cut
+  const bool one_each = pairs <= ctas / 2 || (pairs <= ctas && longest <= max(per_joint, cut.whole));
+  const int joint = part_of(longest, per_joint), team = part_of(longest, per_team);
+  cut.joint = one_each && joint <= (team / kTeamWarps + kMergeTiles) * kTeamWarps * teams;
   cut.slots = cut.joint ? ctas : ctas * teams;
   cut.per = cut.joint ? per_joint : per_team;
   return cut;
