@@ -72,6 +72,12 @@ __host__ __device__ constexpr int whole_tiles(int teams) { return 2 * teams * kT
 constexpr int kMergeTiles = 3;  // what a merge costs, in tiles per warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinRef = 7.888609052210118e-31f;  // 2^-100
+constexpr uint32_t kMaxRef = 0x7f000000u;          // 2^127, as bits
+// A logit passes the running maximum by 2^kRoom before the state is rescaled to a
+// new one, and P enters in units of 2^-kUnit: 2^(kRoom + kUnit) at most, twice that
+// for a V scale above 2^127, which f16 holds.
+constexpr float kRoom = 6.0f;
+constexpr int kUnit = 8;
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -644,11 +650,13 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
     }
 
     float m[NT][2], l[NT][2];
+    float base[NT][2];  // the maximum, 0 as long as there is none
     float o[NT][D / 16][4];
-    float vref = kMinRef;  // power of two >= every V scale met
+    float vref = kMinRef;  // power of two, not below the V scales met
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = -INFINITY;
+      base[nt][0] = base[nt][1] = 0.0f;
       l[nt][0] = l[nt][1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
@@ -737,10 +745,10 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
           mn[nt][e] = fmaxf(m[nt][e], top * qs[nt][e]);
-          raised |= mn[nt][e] > m[nt][e];
+          raised |= mn[nt][e] > m[nt][e] + kRoom;
         }
       const uint32_t vmax = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(vs[lane])));
-      const uint32_t vcap = max(__float_as_uint(vref), (vmax + 0x7fffffu) & 0x7f800000u);
+      const uint32_t vcap = max(__float_as_uint(vref), min((vmax + 0x7fffffu) & 0x7f800000u, kMaxRef));
       if (__any_sync(0xffffffffu, raised) || vcap != __float_as_uint(vref)) {
         const float vnew = __uint_as_float(vcap);
         const float down = vref / vnew;
@@ -752,6 +760,7 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
             const float f = m[nt][e] == -INFINITY ? 0.0f : exp2f(m[nt][e] - mn[nt][e]);
             l[nt][e] *= f;
             m[nt][e] = mn[nt][e];
+            base[nt][e] = mn[nt][e] == -INFINITY ? 0.0f : mn[nt][e];
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
               o[nt][i][e] *= f * down;
@@ -759,7 +768,7 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
             }
           }
       }
-      const float unit = 16384.0f / vref;
+      const float unit = __uint_as_float((static_cast<uint32_t>(254 + kUnit) << 23) - __float_as_uint(vref));  // 2^kUnit / vref
 #pragma unroll
       for (int i = 0; i < 4; ++i) vr[i] *= unit;
 
@@ -774,8 +783,7 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
             float p[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float base = m[nt][e] == -INFINITY ? 0.0f : m[nt][e];
-              p[e] = exp2_fast(fmaf(s[st][nt][2 * i + e], qs[nt][e], -base));
+              p[e] = exp2_fast(fmaf(s[st][nt][2 * i + e], qs[nt][e], -base[nt][e]));
               l[nt][e] += p[e];
               p[e] *= vr[2 * st + i];
             }
@@ -836,7 +844,7 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
           s_m[warp][h] = m[nt][e];
           s_l[warp][h] = sum;
         }
-        const float back = vref * 6.103515625e-05f;  // 2^-14
+        const float back = vref * (1.0f / (1 << kUnit));
         float* dst = so + (team_warp * 8 * NT + h) * D + g * (D / 8);
 #pragma unroll
         for (int i = 0; i < D / 16; i += 2)
