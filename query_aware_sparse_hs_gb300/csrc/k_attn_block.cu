@@ -32,21 +32,25 @@
 // has bank conflicts.
 //
 // What bounds it: memory, for long work (16 requests x 4 heads x 131072 tokens, 2.15
-// GB: 322 us, 1.0 of the copy rate; 64 channels 0.83).  Before it streams, a part
+// GB: 318 us, 1.0 of the copy rate; 64 channels 0.83).  Before it streams, a part
 // waits for a chain of lookups (counts, selection, pages, rows: 4 us), after it
-// for the join of its warps and the merge (3 to 4 us): 32 requests x 4096 selected
-// tokens, 134 MB: 29 us, 0.69.  With 16 query heads and 64 channels a 32-token
-// tile takes an SM about 240 cycles whatever the number of warps: conversions
-// (120 cycles: the instruction retires 17 code pairs a cycle) and the other
-// arithmetic of 16 heads' softmax.
+// for the join of its warps and, where pairs are cut, the merge (2 and 2 us): 32
+// requests x 4096 selected tokens, 134 MB, no pair cut: 28 us, 0.71.  (Asking the L2
+// ahead for selections and pages did not shorten the chain.)  With 16 query heads
+// and 64 channels a 32-token tile takes an SM about 240 cycles whatever the number
+// of warps: instructions, some 440 a tile.  (Codes converted by shifts on the
+// integer pipe instead of the converting instruction, which retires 17 pairs a
+// cycle: 29.4 us where it takes 28.6; 64 tokens at a time: long runs 5% faster, 30.1
+// for 27.7 us where a warp has few tiles.)
 //
 // Precision: q times a power of two per head (largest entry into [128, 256)) is
 // exact in f16 for entries within 2^-21 of the largest, and absolutely within
 // 2^-33 of it below.  P * vscale, in units of 2^-14 times the largest V scale
-// met so far (a power of two), enters as two f16 terms (22 bits) for fp32
-// outputs; for bf16 outputs as one (rounded by 2^-11 at most, an eighth of the
-// output's own rounding, and differently for each token).  Sums, maxima and
-// partial outputs are fp32.
+// met so far (a power of two, 2^-112 or more), enters as two f16 terms (22 bits)
+// for fp32 outputs; for bf16 outputs as one (rounded by 2^-11 at most, an eighth of
+// the output's own rounding, and differently for each token).  Sums, maxima and
+// partial outputs are fp32; sums stay in those units until they are divided, so
+// that V may be as large as its outputs can be.
 #include <limits.h>
 
 #include <atomic>
@@ -71,13 +75,13 @@ constexpr int kMinTiles = 8;    // tiles of a part of a cut pair at least
 __host__ __device__ constexpr int whole_tiles(int teams) { return 2 * teams * kTeamWarps; }
 constexpr int kMergeTiles = 3;  // what a merge costs, in tiles per warp
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMinRef = 7.888609052210118e-31f;  // 2^-100
+constexpr float kMinRef = 1.925929944387236e-34f;  // 2^-112
 constexpr uint32_t kMaxRef = 0x7f000000u;          // 2^127, as bits
-// A logit passes the running maximum by 2^kRoom before the state is rescaled to a
-// new one, and P enters in units of 2^-kUnit: 2^(kRoom + kUnit) at most, twice that
-// for a V scale above 2^127, which f16 holds.
-constexpr float kRoom = 6.0f;
-constexpr int kUnit = 8;
+// P * vscale enters in units of 2^-kUnit times the reference: 2^14 at most, twice that
+// for a V scale above 2^127, which f16 holds.  (P up to 2^6, in units of 2^-8, would
+// spare most rescalings of the state: 28.3 -> 27.8 us for 16 heads of 64 channels,
+// for 6 bits less below the f16 range.)
+constexpr int kUnit = 14;
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -123,6 +127,10 @@ __device__ __forceinline__ float exp2_fast(float x) {  // 2 ulp; results under 2
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// 2^kUnit / ref, of a power of two from kMinRef to 2^127
+__device__ __forceinline__ float unit_over(float ref) {
+  return __uint_as_float((static_cast<uint32_t>(254 + kUnit) << 23) - __float_as_uint(ref));
 }
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -197,7 +205,7 @@ struct Team {
 //   time of a short part; with more pairs than CTAs, or pairs so uneven that CTAs
 //   are left idle, teams balance better.  Taken where every CTA has one part at
 //   most and the longest pair's, in tiles per warp, is not longer than the teams' by
-//   more than a merge.  32 requests x 4 heads x 4096 selected tokens: joint 29 us, teams
+//   more than a merge.  32 requests x 4 heads x 4096 selected tokens: joint 28 us, teams
 //   32; 24 uneven requests x 4 heads: 56 and 48; 64 x 4 heads x 4096: 54 and 49.
 struct Cut {
   int per, slots, whole;
@@ -317,7 +325,7 @@ __device__ __forceinline__ void store_out(const BlockArgs& a, int64_t at, float4
 
 // Joins the partial results of a pair into out / lse, every kTeamWarps warps of
 // the team those of every groups-th part, and then the groups.  The order goes by
-// the parts' numbers alone.  w: shared memory for G * (count + 2) floats and
+// the parts' numbers alone.  w: shared memory for G * (count + 1) floats and
 // groups - 1 results.  The first results are on their way while their weights are
 // found.
 template <int D, int NT>
@@ -328,9 +336,8 @@ __device__ void merge_pair(const KvView& kv, const BlockArgs& a, const Team& tea
   constexpr int U = 16 / NI;                   // results in flight
   const int G = kv.group, lane = team.rank & 31, warp = team.rank >> 5, threads = team.threads();
   const int groups = team.warps / kTeamWarps, grp = team.rank / kGroup, rank = team.rank - grp * kGroup;
-  float* norm = w + G * count;  // per head: 1 / sum of the weights
-  float* lses = norm + G;
-  float4* sums = reinterpret_cast<float4*>(w + (G * (count + 2) + 3) / 4 * 4);
+  float* lses = w + G * count;
+  float4* sums = reinterpret_cast<float4*>(w + (G * (count + 1) + 3) / 4 * 4);
   const float* ws_lse = a.ws_lse + static_cast<int64_t>(row0) * G;
   const float4* ws_o = reinterpret_cast<const float4*>(a.ws_o + static_cast<int64_t>(row0) * G * D);
   const int pieces = G * (D / 4);
@@ -359,10 +366,9 @@ __device__ void merge_pair(const KvView& kv, const BlockArgs& a, const Team& tea
       tot += e;
     }
     tot = warp_sum(tot);
-    if (lane == 0) {
-      norm[h] = tot == 0.0f ? 0.0f : 1.0f / tot;
-      lses[h] = tot == 0.0f ? -INFINITY : M + logf(tot);
-    }
+    const float norm = tot == 0.0f ? 0.0f : 1.0f / tot;
+    for (int i = lane; i < count; i += 32) w[i * G + h] *= norm;
+    if (lane == 0) lses[h] = tot == 0.0f ? -INFINITY : M + logf(tot);
   }
   team.sync();
   float4 acc[NI];
@@ -398,8 +404,7 @@ __device__ void merge_pair(const KvView& kv, const BlockArgs& a, const Team& tea
       const float4 v = sums[j * pieces + idx];
       acc[n] = make_float4(acc[n].x + v.x, acc[n].y + v.y, acc[n].z + v.z, acc[n].w + v.w);
     }
-    const float s = norm[idx / (D / 4)];
-    store_out(a, out_row * D + 4 * idx, make_float4(acc[n].x * s, acc[n].y * s, acc[n].z * s, acc[n].w * s));
+    store_out(a, out_row * D + 4 * idx, acc[n]);
   }
   if (a.lse && team.rank < G) a.lse[out_row + team.rank] = lses[team.rank];
 }
@@ -419,7 +424,7 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
   extern __shared__ __align__(1024) uint8_t ring[];
   __shared__ float s_ks[kWarps][kStages][kTile], s_vs[kWarps][kStages][kTile];
   __shared__ uint32_t s_live[kWarps][kStages];
-  __shared__ float s_m[kWarps][8 * NT], s_l[kWarps][8 * NT];
+  __shared__ float s_m[kWarps][8 * NT], s_l[kWarps][8 * NT], s_ref[kWarps];
   __shared__ Scratch s_scratch[kTeams];
   __shared__ Part s_parts[kTeams][kListed];
   __shared__ int s_last[kTeams], s_empty;
@@ -745,7 +750,7 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
           mn[nt][e] = fmaxf(m[nt][e], top * qs[nt][e]);
-          raised |= mn[nt][e] > m[nt][e] + kRoom;
+          raised |= mn[nt][e] > m[nt][e];
         }
       const uint32_t vmax = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(vs[lane])));
       const uint32_t vcap = max(__float_as_uint(vref), min((vmax + 0x7fffffu) & 0x7f800000u, kMaxRef));
@@ -768,7 +773,7 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
             }
           }
       }
-      const float unit = __uint_as_float((static_cast<uint32_t>(254 + kUnit) << 23) - __float_as_uint(vref));  // 2^kUnit / vref
+      const float unit = unit_over(vref);
 #pragma unroll
       for (int i = 0; i < 4; ++i) vr[i] *= unit;
 
@@ -830,6 +835,7 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
 
     // ---- the warps' states joined ----
     team.sync();  // every warp is done with its ring: the team's rings now hold the outputs
+    if (lane == 0) s_ref[warp] = vref;
     float* so = reinterpret_cast<float*>(ring + first_warp * (kStages * kStageBytes));  // [team warp][8 NT][D]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -844,35 +850,40 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
           s_m[warp][h] = m[nt][e];
           s_l[warp][h] = sum;
         }
-        const float back = vref * (1.0f / (1 << kUnit));
         float* dst = so + (team_warp * 8 * NT + h) * D + g * (D / 8);
 #pragma unroll
         for (int i = 0; i < D / 16; i += 2)
           *reinterpret_cast<float4*>(dst + 2 * i) =
-              make_float4(o[nt][i][e] * back, o[nt][i][2 + e] * back, o[nt][i + 1][e] * back, o[nt][i + 1][2 + e] * back);
+              make_float4(o[nt][i][e], o[nt][i][2 + e], o[nt][i + 1][e], o[nt][i + 1][2 + e]);
       }
     team.sync();
     const bool whole = part.count == 1;
     for (int idx = team.rank; idx < G * (D / 4); idx += team.threads()) {
       const int h = idx / (D / 4), d = (idx - h * (D / 4)) * 4;
-      float M = -INFINITY;
-      for (int w = 0; w < team.warps; ++w) M = fmaxf(M, s_m[first_warp + w][h]);
+      float M = -INFINITY, ref = kMinRef;
+      for (int w = 0; w < team.warps; ++w) {
+        M = fmaxf(M, s_m[first_warp + w][h]);
+        ref = fmaxf(ref, s_ref[first_warp + w]);
+      }
       if (M == -INFINITY) M = 0.0f;  // no token, or only logits that are not numbers
+      const float per = unit_over(ref);
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       float tot = 0.0f;
 #pragma unroll 4
       for (int w = 0; w < team.warps; ++w) {
         const float f = exp2f(s_m[first_warp + w][h] - M);
         const float4 v = *reinterpret_cast<const float4*>(so + (w * 8 * NT + h) * D + d);
+        const float fr = f * (s_ref[first_warp + w] * per);  // (the sums stay in units of the largest reference)
         tot = fmaf(s_l[first_warp + w][h], f, tot);
-        acc.x = fmaf(v.x, f, acc.x);
-        acc.y = fmaf(v.y, f, acc.y);
-        acc.z = fmaf(v.z, f, acc.z);
-        acc.w = fmaf(v.w, f, acc.w);
+        acc.x = fmaf(v.x, fr, acc.x);
+        acc.y = fmaf(v.y, fr, acc.y);
+        acc.z = fmaf(v.z, fr, acc.z);
+        acc.w = fmaf(v.w, fr, acc.w);
       }
       float lse = -INFINITY;
       if (tot != 0.0f) {
-        acc = make_float4(acc.x / tot, acc.y / tot, acc.z / tot, acc.w / tot);
+        const float n = 1.0f / (1 << 2 * kUnit) / tot;
+        acc = make_float4(acc.x * n * ref, acc.y * n * ref, acc.z * n * ref, acc.w * n * ref);
         lse = M * kLn2 + logf(tot);
       }
       if (whole) {

@@ -197,6 +197,27 @@ def test_v_scales_of_very_different_sizes(vscale):
     check_attention(c, q, sel, cnt, out, lse)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_v_scale_near_the_largest_float(d):
+    c = Cache([100, 64], 1, d, 64, seed=4, poison=False)
+    c.scales["v"][c.table[0, 0, 0]] = 1.75 * 2.0 ** 127
+    c.codes["v"][c.table[0, 0, 0]] = O.e4m3_encode(c.rng.uniform(-1, 1, (64, d)))
+    c.up()
+    q = query(c, 8)
+    sel, cnt = chosen(c, 2, None)
+    out, lse = attend(c, q, sel, cnt)
+    assert torch.isfinite(out).all()
+    check_attention(c, q, sel, cnt, out, lse)
+
+
+def test_v_scales_near_the_smallest():
+    c = Cache([700, 64, 2000], 1, 128, 16, seed=4, vscale=(-111, -108))
+    q = query(c, 8)
+    sel, cnt = chosen(c, max(c.nb), None)
+    out, lse = attend(c, q, sel, cnt)
+    check_attention(c, q, sel, cnt, out, lse)
+
+
 def test_pages_of_zeros_and_large_or_tiny_queries():
     c = Cache([300, 64], 1, 128, 16, seed=4, poison=False)
     for p in c.table[0, 0, 3:9]:  # as the append leaves a page of zeros
