@@ -430,18 +430,20 @@ __global__ __launch_bounds__(threads_of(UW), (KIND == HS_KV_F32 ? 384 : 512) / t
   const int B = kv.block;
   // request b has the slots from offsets[b] / B + 2 b on: enough for every block
   // its rows can touch, wherever in a block they begin
-  const int b = last_not_above(kv.batch, slot, lane, [&](int i) { return __ldg(a.offsets + i) / B + 2 * i; });
+  const int shift = (B & (B - 1)) == 0 ? 31 - __clz(B) : -1;
+  const auto blocks = [&](int rows) { return shift >= 0 ? rows >> shift : rows / B; };
+  const int b = last_not_above(kv.batch, slot, lane, [&](int i) { return blocks(__ldg(a.offsets + i)) + 2 * i; });
   const int o0 = __ldg(a.offsets + b), o1 = __ldg(a.offsets + b + 1);
   const int L = __ldg(kv.seq_lens + b);
   if (o0 < 0 || o1 < o0 || o1 > a.rows || o1 - o0 > max(L, 0)) {
     if (tid == 0) set_error(err, HS_EBIT_BLOCK_RANGE);
     return;
   }
-  const int n = o1 - o0, x = slot - (o0 / B + 2 * b);
+  const int n = o1 - o0, x = slot - (blocks(o0) + 2 * b);
   if (x < 0 || n == 0) return;
   const int first = L - n;  // cache position of the request's first new row
-  const int j = first / B + x;
-  if (j > (L - 1) / B) return;
+  const int j = blocks(first) + x;
+  if (j > blocks(L - 1)) return;
   const int64_t pair = static_cast<int64_t>(b) * kv.hkv + kvh;
   if (j >= kv.max_blocks) {
     if (tid == 0) set_error(err, HS_EBIT_BLOCK_RANGE);
