@@ -291,46 +291,80 @@ __device__ __forceinline__ void decode8(uint2 c, float s, float (&x)[8]) {
   }
 }
 
+// x / s for each x, rounded as IEEE division rounds it.  Where s is of ordinary size
+// after Markstein (IBM J. Res. Dev. 34, 1990): with r = 1 / s rounded, the remainder
+// of x r corrects it to the rounded quotient.  (Compared with division on the host
+// for every significand of s and the three x next to each border of a code's
+// neighbours, where a code could differ: 8 10^8 quotients, all the same.)  The
+// remainder is exact for |x| >= 2^-101; a smaller x has a quotient under 2^-40, which
+// no code shows.  Prompts of 8 / 8 heads 97 us, with divisions 117.
+__device__ __forceinline__ void divide8(float (&x)[8], float s) {
+  if (s >= 8.673617379884035e-19f && s <= 1.152921504606847e18f) {  // 2^-60, 2^60
+    const float r = 1.0f / s;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float q = x[c] * r;
+      x[c] = fmaf(fmaf(-q, s, x[c]), r, q);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) x[c] = x[c] / s;
+  }
+}
+
 // The grouped format: every 32-channel group its own scale (amax / 448).  A row's
 // TPR neighbouring threads call it together; `part` is their D / 32 words of
 // shared memory.  Stores the codes and scales and leaves in u, w what they stand
 // for.
-template <int D>
-__device__ __forceinline__ void store_grouped(void* pages, float* scales, int64_t row, int s, const Slot& t, bool live,
+template <int D, bool INTERLEAVED>
+__device__ __forceinline__ void store_grouped(void* pages, float* scales, int64_t row, int s, const Slot& t, int rotary, bool live,
                                               unsigned* part, float (&u)[8], float (&w)[8]) {
-  if (s < D / kQuantGroup) part[s] = 0u;
-  __syncwarp();
+  float ga = 0.0f, gb = 0.0f;  // the largest magnitudes of the vectors' groups
   if (live) {
-    float p = 0.0f, q = 0.0f;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      p = fmaxf(p, fabsf(u[c]));
-      q = fmaxf(q, fabsf(w[c]));
+      ga = fmaxf(ga, fabsf(u[c]));
+      gb = fmaxf(gb, fabsf(w[c]));
     }
-    atomicMax(&part[t.ca / kQuantGroup], __float_as_uint(p));  // a maximum: the order does not matter
-    atomicMax(&part[t.cb / kQuantGroup], __float_as_uint(q));
   }
-  __syncwarp();
-  if (live) {
-    const float ga = __uint_as_float(part[t.ca / kQuantGroup]), gb = __uint_as_float(part[t.cb / kQuantGroup]);
-    const float sa = ga > 0.0f ? ga / 448.0f : 1.0f, sb = gb > 0.0f ? gb / 448.0f : 1.0f;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {  // IEEE division, as the quantiser of whole rows does
-      u[c] = u[c] / sa;
-      w[c] = w[c] / sb;
+  const bool split = !INTERLEAVED && t.rotated;
+  const bool neighbours = INTERLEAVED || rotary % 64 == 0;
+  if (neighbours) {  // a group is two threads' vectors, or (split) one vector of four threads
+    if (!split) ga = gb = fmaxf(ga, gb);
+    ga = fmaxf(ga, __shfl_xor_sync(0xffffffffu, ga, 1));
+    gb = fmaxf(gb, __shfl_xor_sync(0xffffffffu, gb, 1));
+    if constexpr (!INTERLEAVED) {
+      const float a2 = __shfl_xor_sync(0xffffffffu, ga, 2), b2 = __shfl_xor_sync(0xffffffffu, gb, 2);
+      if (split) {
+        ga = fmaxf(ga, a2);
+        gb = fmaxf(gb, b2);
+      }
     }
-    uint8_t* dst = static_cast<uint8_t*>(pages) + row * D;
-    const uint2 cu = encode8(u, 1.0f), cw = encode8(w, 1.0f);
-    *reinterpret_cast<uint2*>(dst + t.ca) = cu;
-    *reinterpret_cast<uint2*>(dst + t.cb) = cw;
-    if (s < D / kQuantGroup) {
-      const float g = __uint_as_float(part[s]);
-      scales[row * (D / kQuantGroup) + s] = g > 0.0f ? g / 448.0f : 1.0f;
+  } else {
+    if (s < D / kQuantGroup) part[s] = 0u;
+    __syncwarp();
+    if (live) {
+      atomicMax(&part[t.ca / kQuantGroup], __float_as_uint(ga));  // a maximum: the order does not matter
+      atomicMax(&part[t.cb / kQuantGroup], __float_as_uint(gb));
     }
-    decode8(cu, sa, u);
-    decode8(cw, sb, w);
+    __syncwarp();
+    ga = __uint_as_float(part[t.ca / kQuantGroup]);
+    gb = __uint_as_float(part[t.cb / kQuantGroup]);
+    __syncwarp();
   }
-  __syncwarp();
+  if (!live) return;
+  const float sa = ga > 0.0f ? ga / 448.0f : 1.0f, sb = gb > 0.0f ? gb / 448.0f : 1.0f;
+  divide8(u, sa);  // as the quantiser of whole rows does
+  divide8(w, sb);
+  uint8_t* dst = static_cast<uint8_t*>(pages) + row * D;
+  const uint2 cu = encode8(u, 1.0f), cw = encode8(w, 1.0f);
+  *reinterpret_cast<uint2*>(dst + t.ca) = cu;
+  *reinterpret_cast<uint2*>(dst + t.cb) = cw;
+  // the thread with a group's first channel has its scale
+  if (t.ca % kQuantGroup == 0) scales[row * (D / kQuantGroup) + t.ca / kQuantGroup] = sa;
+  if (t.cb % kQuantGroup == 0) scales[row * (D / kQuantGroup) + t.cb / kQuantGroup] = sb;
+  decode8(cu, sa, u);
+  decode8(cw, sb, w);
 }
 
 // Stores a row of an f32 or bf16 cache and leaves in u, w what it holds.
@@ -518,7 +552,7 @@ __global__ __launch_bounds__(threads_of(UW), (KIND == HS_KV_F32 ? 384 : 512) / t
       const bool on = turned(r, xa[i], xb[i], u, w);
       any |= on;
       if constexpr (KIND == HS_KV_FP8E4M3_G32) {
-        store_grouped<D>(pages, scales, row0 + r, s, t, on, s_group[threadIdx.x / TPR], u, w);
+        store_grouped<D, INTERLEAVED>(pages, scales, row0 + r, s, t, a.rotary, on, s_group[threadIdx.x / TPR], u, w);
       } else if constexpr (KIND == HS_KV_FP8E4M3_BLOCK) {
         if (on && !box) amax = widen_any(amax, u, w);
       } else {
@@ -743,8 +777,8 @@ __global__ __launch_bounds__(kThreads) void append_one_kernel(KvView kv, AppendT
   const bool box = a.smin != nullptr;
 
   if constexpr (KIND == HS_KV_FP8E4M3_G32) {
-    store_grouped<D>(kp, ks, row, s, t, live_k, s_group[rs], ku, kw);
-    store_grouped<D>(vp, vs, row, s, t, live, s_group[rs], vu, vw);
+    store_grouped<D, INTERLEAVED>(kp, ks, row, s, t, a.rotary, live_k, s_group[rs], ku, kw);
+    store_grouped<D, INTERLEAVED>(vp, vs, row, s, t, a.rotary, live, s_group[rs], vu, vw);
   } else if constexpr (KIND == HS_KV_FP8E4M3_BLOCK) {
     float lo[16], hi[16];  // box of the earlier rows, channels 16 s and up, where their codes change
     // The page's scale, the codes and the earlier rows' codes where the scale

@@ -283,6 +283,27 @@ def test_channels_of_nothing_but_not_a_number(kind, n):
     assert torch.isfinite(w.smin[0, 0, n // 16]).all()
 
 
+@pytest.mark.parametrize("d,rotary,interleaved", [(128, 128, False), (128, 64, False), (128, 96, True), (64, 48, False), (64, 0, False)])
+@pytest.mark.parametrize("n", [1, 90])
+def test_grouped_codes_are_those_of_the_quantiser(d, rotary, interleaved, n):
+    """Bit for bit, for rows that are not rotated (V): ordinary ones, zeros, and groups of the smallest and largest sizes."""
+    w = World("fp8", d, 16, 4, 2, [0], [n], rotary, interleaved, seed=8, spread=4.0)
+    if n > 1:
+        w.vn[5] = 0
+        w.vn[6, :, :32] *= 1e-30
+        w.vn[7] *= 1e36
+        w.vn[8, 1] *= 1e-37
+        w.vn[9] = torch.exp2(torch.randint(-30, 30, w.vn[9].shape, device="cuda").float()).to(w.wide)
+    w.append()
+    codes, scales = O.quantize_e4m3_g32(w.vn.float().cpu().numpy().reshape(-1, d))
+    codes, scales = codes.reshape(n, w.hkv, d), scales.reshape(n, w.hkv, d // 32)
+    for t in range(n):
+        for h in range(w.hkv):
+            page = w.table[0, h, t // 16]
+            assert np.array_equal(w.g["v"][page, t % 16].cpu().numpy(), codes[t, h]), (t, h)
+            assert np.array_equal(w.gs["v"][page, t % 16].cpu().numpy(), scales[t, h]), (t, h)
+
+
 def test_query_in_place():
     w = World("bf16", 128, 16, 4, 2, [20, 0], [30, 3], 128, seed=6)
     w.append()
