@@ -16,15 +16,15 @@
 //
 // A thread holds 16 channels of a row as two vectors of 8 chosen so that both
 // members of every rotated pair are its own.  One launch either way:
-//   any number of rows per request: one to eight warps take a unit, one (touched
+//   any number of rows per request: one warp or four take a unit, one (touched
 //     block, kv head, K or V).  They own the page and its scale, so units exchange
-//     nothing; the rows of pages up to 128 tokens are read once and held, as read,
-//     while the scale is found (rotated twice: held rotated, their registers cost
-//     the occupancy that streams Q).  Other CTAs rotate Q: a warp takes 16 heads of a
+//     nothing; rows are held, as read, or read again while the scale is found
+//     (rotated twice: held rotated, their registers cost the occupancy that streams
+//     Q).  Other CTAs rotate Q: a warp takes 16 heads of a
 //     few consecutive rows, and reads a row's cos and sin once for the 16.
 //     Memory-bound: prompts of 16 requests of up to 4096 tokens, 32 / 4 heads of 128
-//     channels, block-scaled, 859 MB: 135 us, 0.95 of the copy rate; bf16 pages
-//     0.99; 8 query heads on 8 kv heads 0.46: there the K and V units'
+//     channels, block-scaled, 859 MB: 131 us, 0.98 of the copy rate; bf16 pages
+//     0.99; 8 query heads on 8 kv heads 0.53: there the K and V units'
 //     instructions bind (two rotations, minimum and maximum of every channel).
 //   one row per request: the D / 16 threads of a row take its K and V, so a warp
 //     holds several (request, kv head) pairs; the row's thread holds the channels
@@ -297,7 +297,7 @@ __device__ __forceinline__ void decode8(uint2 c, float s, float (&x)[8]) {
 // for every significand of s and the three x next to each border of a code's
 // neighbours, where a code could differ: 8 10^8 quotients, all the same.)  The
 // remainder is exact for |x| >= 2^-101; a smaller x has a quotient under 2^-40, which
-// no code shows.  Prompts of 8 / 8 heads 97 us, with divisions 117.
+// no code shows.  Prompts of 8 / 8 heads 95 us, with divisions 114 (before P = 2).
 __device__ __forceinline__ void divide8(float (&x)[8], float s) {
   if (s >= 8.673617379884035e-19f && s <= 1.152921504606847e18f) {  // 2^-60, 2^60
     const float r = 1.0f / s;
@@ -412,20 +412,31 @@ __device__ __forceinline__ uint4 rescaled(uint4 v, float f) {
 }
 
 // ---- any number of rows per request ----
-// A unit is one touched block of one kv head, K or V, taken by UW warps: as many
-// as let the page's rows be read in P = 4 passes (pages of more than 8 warps'
-// rows are taken in turns; with four warps for every page size, prompts into
-// 16-token bf16 pages took 179 us where one warp takes 140).  The rows of the
-// passes are read together and, block-scaled, held, as read, until the scale is
-// known.
-constexpr int P = 4;
-constexpr int threads_of(int unit_warps) { return unit_warps > 4 ? 32 * unit_warps : 128; }
+// A unit is one touched block of one kv head, K or V.  One warp takes it, or the
+// CTA's four: the page's rows are read in passes of 32 / (D / 16) rows a warp, P
+// passes at a time, and one warp takes pages of up to 4 passes.  (8 requests of up to
+// 4096 tokens, 8 kv heads, block-scaled: 4 passes, 16-token pages, by one warp 105 us,
+// by four 132; 8 passes, 32-token pages, by four warps 77, by two 99; and four warps
+// taking 128-token pages in turns 67, eight at once 76.)
+//
+// Block-scaled, the rows of one turn are held, as read, until the scale is known, and
+// those of more turns are read once more, from the caches.  P = 2 leaves registers for
+// 640 threads on an SM instead of 512: prompts of 16 requests 131 us, P = 4, all rows
+// of a page held, 134; 8 / 8 heads 70 and 79.  Where all units run at once that counts
+// for nothing and holding saves the second reading: a chunk of 2000 tokens 11.9 us,
+// P = 2 13.2.  Grouped e4m3: P = 2, 8 / 8 heads 71 us, P = 4 95.  bf16 and f32 have
+// registers enough for P = 4 (bf16 56 us at 640 threads, 60 at 512; f32 89 at 512, 97 at
+// 384).
+constexpr int threads_per_sm(int kind, int p) {
+  return kind == HS_KV_F32 || (kind == HS_KV_FP8E4M3_BLOCK && p == 4) ? 512 : 640;
+}
 
-template <int D, int KIND, bool INTERLEAVED, int UW>
-__global__ __launch_bounds__(threads_of(UW), (KIND == HS_KV_F32 ? 384 : 512) / threads_of(UW)) void append_rows_kernel(
+template <int D, int KIND, bool INTERLEAVED, int UW, int P>
+__global__ __launch_bounds__(kThreads, threads_per_sm(KIND, P) / kThreads) void append_rows_kernel(
     KvView kv, AppendTokensArgs a, int kv_units, uint64_t mix, int q_units, int q_rows, unsigned* err) {
   constexpr bool F32 = KIND == HS_KV_F32;
-  constexpr int kWarps = threads_of(UW) / 32, kUnits = kWarps / UW;  // of a CTA
+  static_assert(UW == 1 || UW == kWarps);
+  constexpr int kUnits = kWarps / UW;  // of a CTA
   constexpr int TPR = D / 16, RPP = UW * 32 / TPR;  // threads per row, rows per pass of a unit
   __shared__ float s_mn[kWarps][D], s_mx[kWarps][D];
   __shared__ float s_amax[kWarps];
@@ -452,10 +463,8 @@ __global__ __launch_bounds__(threads_of(UW), (KIND == HS_KV_F32 ? 384 : 512) / t
   const auto unit_sync = [&]() {
     if constexpr (UW == 1)
       __syncwarp();
-    else if constexpr (kUnits == 1)
-      __syncthreads();
     else
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + first_warp / UW), "n"(UW * 32) : "memory");
+      __syncthreads();
   };
   const int unit = cta * kUnits + first_warp / UW;
   if (unit >= kv_units) return;
@@ -870,18 +879,18 @@ __global__ __launch_bounds__(kThreads) void append_one_kernel(KvView kv, AppendT
   }
 }
 
-template <int D, int KIND, bool INTERLEAVED, int UW>
+template <int D, int KIND, bool INTERLEAVED, int UW, int P>
 cudaError_t launch_rows(const KvView& kv, const AppendTokensArgs& a, int sms, unsigned* err, cudaStream_t st) {
-  constexpr int kThreads = threads_of(UW), kWarps = kThreads / 32, kUnits = kWarps / UW;
+  constexpr int kUnits = kWarps / UW;
   const int64_t kv_units = kv_units_of(kv, a), kv_ctas = (kv_units + kUnits - 1) / kUnits;
   const int64_t q_units = q_units_of(kv, a), ctas = kv_ctas + (q_units + kWarps - 1) / kWarps;
   // K and V units that all run at once go first: they take longest (a chunk of
   // 2000 tokens 12.0 us, mixed evenly 14.4).  More than that are mixed evenly
   // with the Q units, which keep the memory busy while they look up and reduce
   // (prompts of 16 requests 135 us, K and V first 151).
-  const int64_t span = kv_ctas <= static_cast<int64_t>(sms) * (512 / kThreads) ? kv_ctas : ctas;
+  const int64_t span = kv_ctas <= static_cast<int64_t>(sms) * (threads_per_sm(KIND, P) / kThreads) ? kv_ctas : ctas;
   const uint64_t mix = ((static_cast<uint64_t>(kv_ctas) << 32) + span - 1) / span;
-  return launch_pdl(append_rows_kernel<D, KIND, INTERLEAVED, UW>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, st, kv, a,
+  return launch_pdl(append_rows_kernel<D, KIND, INTERLEAVED, UW, P>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, st, kv, a,
                     static_cast<int>(kv_units), mix, static_cast<int>(q_units), q_rows_of(kv, a), err);
 }
 
@@ -893,11 +902,15 @@ cudaError_t launch_i(const KvView& kv, const AppendTokensArgs& a, int sms, unsig
     return launch_pdl(append_one_kernel<D, KIND, INTERLEAVED>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, st, kv, a, kv_ctas,
                       err);
   }
-  constexpr int kWarpRows = P * 32 / (D / 16);  // rows of a page that a warp reads at once
-  if (kv.block <= kWarpRows) return launch_rows<D, KIND, INTERLEAVED, 1>(kv, a, sms, err, st);
-  if (kv.block <= 2 * kWarpRows) return launch_rows<D, KIND, INTERLEAVED, 2>(kv, a, sms, err, st);
-  if (kv.block <= 4 * kWarpRows) return launch_rows<D, KIND, INTERLEAVED, 4>(kv, a, sms, err, st);
-  return launch_rows<D, KIND, INTERLEAVED, 8>(kv, a, sms, err, st);
+  constexpr int kPass = 32 / (D / 16);  // rows of a page that a warp reads at a time
+  constexpr bool kBlock = KIND == HS_KV_FP8E4M3_BLOCK;
+  constexpr int P = kBlock || KIND == HS_KV_FP8E4M3_G32 ? 2 : 4;
+  if (kv.block <= 2 * kPass) return launch_rows<D, KIND, INTERLEAVED, 1, 2>(kv, a, sms, err, st);
+  if (kv.block <= 4 * kPass) return launch_rows<D, KIND, INTERLEAVED, 1, P>(kv, a, sms, err, st);
+  if constexpr (kBlock)
+    if (kv.block > P * kWarps * kPass && kv_units_of(kv, a) <= static_cast<int64_t>(sms) * (threads_per_sm(KIND, 4) / kThreads))
+      return launch_rows<D, KIND, INTERLEAVED, kWarps, 4>(kv, a, sms, err, st);
+  return launch_rows<D, KIND, INTERLEAVED, kWarps, P>(kv, a, sms, err, st);
 }
 
 template <int D, int KIND>

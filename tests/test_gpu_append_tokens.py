@@ -227,6 +227,11 @@ CASES = {
     "no_rotation": ("fp8_block", 128, 64, 4, 4, [30], [50], 0, False, False, 0),
     "many_requests": ("bf16", 64, 16, 2, 1, [i % 37 for i in range(90)], [i % 5 for i in range(90)], 64, False, False, 11),
     "many_single_rows": ("fp8_block", 64, 16, 2, 1, [i for i in range(70)], [1] * 70, 64, False, True, 2),
+    "many_prompts": ("fp8_block", 128, 64, 4, 4, [i % 70 for i in range(45)], [7 * i % 90 for i in range(45)], 128, False, False, 0),
+    "many_prompts_d64": ("fp8_block", 64, 100, 4, 4, [i % 70 for i in range(45)], [7 * i % 120 for i in range(45)], 64, False, False, 0),
+    "prompts_block_16": ("fp8_block", 128, 16, 4, 2, [0, 5, 16], [40, 30, 9], 128, False, False, 0),
+    "prompts_block_32": ("fp8_block", 128, 32, 4, 2, [0, 5, 33], [70, 30, 9], 128, True, False, 0),
+    "prompts_g32_256": ("fp8", 64, 256, 4, 2, [0, 5], [300, 30], 64, False, False, 0),
     "no_new_rows": ("fp8_block", 64, 16, 2, 1, [5, 0], [0, 0], 64, False, False, 3),
 }
 
@@ -376,6 +381,27 @@ def test_values_that_are_not_finite_and_pages_of_zeros():
     hs.hs_append_tokens(shape, kv, hs.append_params(), x[3:], x[3:])
     assert float(vs[1]) == power_scale(float(x[3].abs().max())) and (v[1, :4] == 0).all() and (v[1, 4] != 0).any()
     assert hs.hs_get_device_error() == (hs.HS_OK, 0)
+
+
+@pytest.mark.parametrize("d,block,batch", [(128, 16, 2), (128, 64, 2), (128, 64, 45), (64, 32, 3), (64, 256, 2), (128, 5, 2)])
+def test_infinities_in_pages_of_any_size(d, block, batch):
+    """The scale goes by the page's finite values, whether its rows are held or read once more."""
+    new = [1 + (37 * i + 90) % 130 for i in range(batch)]
+    w = World("fp8_block", d, block, 4, 4, [0] * batch, new, d, seed=9)
+    rng = np.random.default_rng(9)
+    for row in rng.choice(w.rows, max(3, w.rows // 40), replace=False):
+        w.vn[row, rng.integers(4), rng.integers(d)] = float("inf") if row % 2 else float("-inf")
+    w.append(q=False)
+    assert w.hs.hs_get_device_error() == (w.hs.HS_OK, 0)
+    v, codes, scales = w.vn.float().cpu().numpy(), w.g["v"].cpu().numpy(), w.gs["v"].cpu().numpy()
+    for b in range(batch):
+        o = int(w.offsets[b])
+        for j in range(-(-new[b] // block)):
+            for h in range(4):
+                x = v[o + j * block:min(o + (j + 1) * block, o + new[b]), h]
+                page = w.table[b, h, j]
+                assert scales[page] == power_scale(float(np.abs(x[np.isfinite(x)]).max()))
+                assert np.array_equal(codes[page, :len(x)], O.e4m3_encode(x / scales[page]))
 
 
 def test_bad_pages_lengths_offsets_and_positions_are_reported_and_skipped():
