@@ -199,10 +199,10 @@ int64_t kv_units_of(const KvView& kv, const AppendTokensArgs& a) {
   return (a.rows / kv.block + 2 * static_cast<int64_t>(kv.batch)) * kv.hkv * 2;
 }
 // Rows a warp rotates 16 heads of: more than one only where there are warps
-// enough without that (prompts of 16 requests: 4 rows 135 us, one 139; a chunk of
-// 2000 tokens: 13.2 and 11.9).
+// enough without that (8000 tokens of 32 heads: 4 rows 38.0 us, one 39.3; 2000 tokens
+// 13.1 and 11.9).
 int q_rows_of(const KvView& kv, const AppendTokensArgs& a) {
-  return a.offsets && a.rows * ceil_div(kv.hq, kQHeads) >= 32768 ? 4 : 1;
+  return a.offsets && a.rows * ceil_div(kv.hq, kQHeads) >= 8000 ? 4 : 1;
 }
 int64_t q_units_of(const KvView& kv, const AppendTokensArgs& a) {
   const int n = q_rows_of(kv, a);
@@ -884,11 +884,11 @@ cudaError_t launch_rows(const KvView& kv, const AppendTokensArgs& a, int sms, un
   constexpr int kUnits = kWarps / UW;
   const int64_t kv_units = kv_units_of(kv, a), kv_ctas = (kv_units + kUnits - 1) / kUnits;
   const int64_t q_units = q_units_of(kv, a), ctas = kv_ctas + (q_units + kWarps - 1) / kWarps;
-  // K and V units that all run at once go first: they take longest (a chunk of
-  // 2000 tokens 12.0 us, mixed evenly 14.4).  More than that are mixed evenly
-  // with the Q units, which keep the memory busy while they look up and reduce
-  // (prompts of 16 requests 135 us, K and V first 151).
-  const int64_t span = kv_ctas <= static_cast<int64_t>(sms) * (threads_per_sm(KIND, P) / kThreads) ? kv_ctas : ctas;
+  // K and V units go first where two rounds of them at most fill the GPU: they take
+  // longest (a chunk of 2000 tokens 11.9 us, mixed evenly 14.4; 3000 tokens 15.8 and
+  // 19.2).  More than that are mixed evenly with the Q units, which keep the memory
+  // busy while they look up and reduce (12000 tokens 53.8, K and V first 58.0).
+  const int64_t span = kv_ctas <= 2 * static_cast<int64_t>(sms) * (threads_per_sm(KIND, P) / kThreads) ? kv_ctas : ctas;
   const uint64_t mix = ((static_cast<uint64_t>(kv_ctas) << 32) + span - 1) / span;
   return launch_pdl(append_rows_kernel<D, KIND, INTERLEAVED, UW, P>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, st, kv, a,
                     static_cast<int>(kv_units), mix, static_cast<int>(q_units), q_rows_of(kv, a), err);

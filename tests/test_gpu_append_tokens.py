@@ -232,6 +232,8 @@ CASES = {
     "prompts_block_16": ("fp8_block", 128, 16, 4, 2, [0, 5, 16], [40, 30, 9], 128, False, False, 0),
     "prompts_block_32": ("fp8_block", 128, 32, 4, 2, [0, 5, 33], [70, 30, 9], 128, True, False, 0),
     "prompts_g32_256": ("fp8", 64, 256, 4, 2, [0, 5], [300, 30], 64, False, False, 0),
+    "long_prompts": ("bf16", 64, 64, 2, 1, [0, 100, 3, 9], [4001, 4102, 77, 1], 64, False, False, 5),
+    "long_prompts_block": ("fp8_block", 64, 32, 32, 2, [5, 0, 7], [2000, 2, 2099], 32, True, True, 3),
     "no_new_rows": ("fp8_block", 64, 16, 2, 1, [5, 0], [0, 0], 64, False, False, 3),
 }
 
