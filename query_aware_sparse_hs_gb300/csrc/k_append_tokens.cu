@@ -20,8 +20,8 @@
 //     block, kv head, K or V).  They own the page and its scale, so units exchange
 //     nothing; rows are held, as read, or read again while the scale is found
 //     (rotated twice: held rotated, their registers cost the occupancy that streams
-//     Q).  Other CTAs rotate Q: a warp takes 16 heads of a
-//     few consecutive rows, and reads a row's cos and sin once for the 16.
+//     Q).  Other CTAs rotate Q: a warp takes 16 heads of a few consecutive rows, and
+//     reads a row's cos and sin once for the 16.
 //     Memory-bound: prompts of 16 requests of up to 4096 tokens, 32 / 4 heads of 128
 //     channels, block-scaled, 859 MB: 131 us, 0.98 of the copy rate; bf16 pages
 //     0.99; 8 query heads on 8 kv heads 0.53: there the K and V units'
