@@ -32,10 +32,11 @@
 // has bank conflicts.
 //
 // What bounds it: memory, for long work (16 requests x 4 heads x 131072 tokens, 2.15
-// GB: 318 us, 1.0 of the copy rate; 64 channels 0.83).  Before it streams, a part
+// GB: 315 to 327 us from one GPU to another, 0.98 to 1.02 of the copy rate; 64
+// channels 0.80).  Before it streams, a part
 // waits for a chain of lookups (counts, selection, pages, rows: 4 us), after it
 // for the join of its warps and, where pairs are cut, the merge (2 and 2 us): 32
-// requests x 4096 selected tokens, 134 MB, no pair cut: 28 us, 0.71.  (Asking the L2
+// requests x 4096 selected tokens, 134 MB, no pair cut: 28.8 us, 0.70.  (Asking the L2
 // ahead for selections and pages did not shorten the chain.)  With 16 query heads
 // and 64 channels a 32-token tile takes an SM about 240 cycles whatever the number
 // of warps: instructions, some 440 a tile.  (Codes converted by shifts on the
@@ -46,9 +47,11 @@
 // Precision: q times a power of two per head (largest entry into [128, 256)) is
 // exact in f16 for entries within 2^-21 of the largest, and absolutely within
 // 2^-33 of it below.  P * vscale, in units of 2^-14 times the largest V scale
-// met so far (a power of two, 2^-112 or more), enters as two f16 terms (22 bits)
-// for fp32 outputs; for bf16 outputs as one (rounded by 2^-11 at most, an eighth of
-// the output's own rounding, and differently for each token).  Sums, maxima and
+// met so far (a power of two, 2^-112 or more), enters as two f16 terms (22 bits;
+// less where the product is under 2^-14 of the units, by 2^-25 of them at most).  One
+// term, for bf16 outputs, would save 2 to 3% with up to 8 heads (nothing where memory
+// binds), 8% with 16 heads of 64 channels and 20% of 128 (37.8 us for 47.0), and moves
+// bf16 outputs by 6 10^-4 of their norm.  Sums, maxima and
 // partial outputs are fp32; sums stay in those units until they are divided, so
 // that V may be as large as its outputs can be.
 #include <limits.h>
@@ -414,7 +417,7 @@ constexpr int ring_bytes() {
   return teams_of(D) * kTeamWarps * kStages * 2 * kTile * D;
 }
 
-template <int D, int NT, bool F32>
+template <int D, int NT>
 __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_kernel(KvView kv, BlockArgs a, unsigned* err) {
   constexpr int kTeams = teams_of(D), kWarps = kTeams * kTeamWarps;
   constexpr int kStageBytes = 2 * kTile * D;
@@ -794,10 +797,8 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
             }
             const uint32_t hi = pack_half2(p[0], p[1]);
             ph[nt][i] = transpose8x8(hi);
-            if constexpr (F32) {
-              const float2 back = unpack_half2(hi);
-              pl[nt][i] = transpose8x8(pack_half2(p[0] - back.x, p[1] - back.y));
-            }
+            const float2 back = unpack_half2(hi);
+            pl[nt][i] = transpose8x8(pack_half2(p[0] - back.x, p[1] - back.y));
           }
         const int t0 = 16 * st + token_of<D>(2 * c4), t1 = 16 * st + token_of<D>(2 * c4 + 1);
         constexpr int kWords = D / 32;  // words of a lane's channels: D / 8 of them
@@ -825,7 +826,7 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma(o[nt][i], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-            if constexpr (F32) mma(o[nt][i], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+            mma(o[nt][i], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
           }
         }
       }
@@ -931,9 +932,9 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32) void attn_block_merg
   if (s_pair.count > 1) merge_pair<D, NT>(kv, a, team, pair, s_pair.row, s_pair.count, weights);
 }
 
-template <int D, int NT, bool F32>
-cudaError_t launch_o(const KvView& kv, const BlockArgs& b, int ctas, unsigned* err, cudaStream_t st) {
-  auto kern = attn_block_kernel<D, NT, F32>;
+template <int D, int NT>
+cudaError_t launch_n(const KvView& kv, const BlockArgs& b, int ctas, unsigned* err, cudaStream_t st) {
+  auto kern = attn_block_kernel<D, NT>;
   // the attribute stays with the device: asked for once
   static std::atomic<uint64_t> allowed{0};
   int dev = 0;
@@ -950,11 +951,6 @@ cudaError_t launch_o(const KvView& kv, const BlockArgs& b, int ctas, unsigned* e
   auto merge = attn_block_merge_kernel<D, NT>;
   if ((e = allow_dynamic_smem(merge, smem)) != cudaSuccess) return e;
   return launch_pdl(merge, dim3(kv.batch * kv.hkv), dim3(teams_of(D) * kTeamWarps * 32), smem, st, kv, b, ctas);
-}
-
-template <int D, int NT>
-cudaError_t launch_n(const KvView& kv, const BlockArgs& b, int ctas, unsigned* err, cudaStream_t st) {
-  return b.out_f32 ? launch_o<D, NT, true>(kv, b, ctas, err, st) : launch_o<D, NT, false>(kv, b, ctas, err, st);
 }
 
 }  // namespace

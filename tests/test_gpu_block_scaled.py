@@ -163,6 +163,18 @@ def test_attention_matches_the_definition(name, form):
     check_attention(c, q, sel, cnt, out, lse, simt=simt)
 
 
+@pytest.mark.parametrize("group,d", [(8, 128), (16, 128), (2, 64), (16, 64)])
+def test_bf16_outputs_are_the_fp32_outputs_rounded(group, d):
+    """The output's type decides its last rounding and nothing before it."""
+    c = Cache([3000, 100, 700], 2, d, 64, seed=12)
+    q = query(c, 2 * group)
+    sel, cnt = chosen(c, max(c.nb), None)
+    for counters in (True, False):
+        wide, lw = attend(c, q, sel, cnt, counters=counters)
+        out, lse = attend(c, q, sel, cnt, f32=False, counters=counters)
+        assert torch.equal(out, wide.to(torch.bfloat16)) and torch.equal(lse, lw)
+
+
 def test_results_do_not_depend_on_the_arrival_order_or_the_number_of_ctas():
     c = Cache([9000, 100, 5000], 2, 128, 64, seed=3)
     q = query(c, 16)
