@@ -311,6 +311,59 @@ def test_grouped_codes_are_those_of_the_quantiser(d, rotary, interleaved, n):
             assert np.array_equal(w.gs["v"][page, t % 16].cpu().numpy(), scales[t, h]), (t, h)
 
 
+@pytest.mark.parametrize("d,rotary,interleaved", [(128, 128, False), (128, 96, True), (64, 0, False)])
+@pytest.mark.parametrize("n", [1, 90])
+def test_grouped_codes_keep_the_sign_of_zero(d, rotary, interleaved, n):
+    """-0 among other values, groups of nothing but -0, negative values too small for a code: bit for bit the quantiser's
+    codes (0x80), by the append of many rows and of one, as by the one-token call."""
+    from query_aware_sparse_hs_gb300 import hs
+    w = World("fp8", d, 16, 4, 2, [0], [n], rotary, interleaved, seed=8)
+    w.vn[:, :, ::3] = -0.0
+    w.vn[:, :, 1::6] = 0.0
+    w.vn[:, 0, :32] = -0.0
+    w.vn[:, 1, 33] = -2.0 ** -130
+    w.append()
+    codes = torch.empty((n * w.hkv, d), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((n * w.hkv, d // 32), device="cuda")
+    hs.hs_quantize_e4m3_g32(w.vn.contiguous(), codes, scales)
+    assert (codes.view(n, w.hkv, d)[:, :, 0] == 0x80).all()
+    t = torch.arange(n, device="cuda")
+    page = w.gt[0, :, t // 16].T.long()  # [n, hkv]
+    assert torch.equal(w.g["v"][page, (t % 16)[:, None]], codes.view(n, w.hkv, d))
+    assert torch.equal(w.gs["v"][page, (t % 16)[:, None]], scales.view(n, w.hkv, -1))
+    # the last token again by the one-token call: the same bytes
+    before = w.g["v"].clone()
+    hs.hs_append_token(w.shape, w.kv, w.vn[n - 1:].contiguous(), w.vn[n - 1:].contiguous(), w.smin, w.smax)
+    assert torch.equal(before, w.g["v"])
+
+
+def test_grouped_codes_of_every_quotient_of_two_bf16_significands():
+    """Every significand of a group's largest value against every one of the others and 24 exponents, either sign: the
+    quotients that the append corrects instead of dividing give the quantiser's codes, bit for bit."""
+    from query_aware_sparse_hs_gb300 import hs
+    d, block = 64, 256
+    top = 1 + torch.arange(128, dtype=torch.float64) / 128
+    x = (top[None, :] * torch.exp2(-1.0 - torch.arange(24, dtype=torch.float64))[:, None]).flatten()  # below every top
+    x = torch.cat([x, -x, x[:(31 - 2 * len(x) % 31) % 31]]).view(-1, 31)
+    g = torch.cat([top[:, None, None].expand(128, len(x), 1), x[None].expand(128, -1, -1)], 2).reshape(-1, d)
+    for unit in (1.0, 2.0 ** -40, 2.0 ** 70):  # scales inside the corrected range, and past it
+        v = (g * unit).to(torch.bfloat16)
+        assert torch.equal(v.double(), g * unit)
+        v = v.cuda()
+        n = len(v)
+        pages = torch.zeros((-(-n // block), block, d), dtype=torch.uint8, device="cuda")
+        k, ks = torch.zeros_like(pages), torch.zeros(pages.shape[:2] + (2,), device="cuda")
+        vs = torch.zeros_like(ks)
+        table = torch.arange(len(pages), dtype=torch.int32, device="cuda").view(1, 1, -1)
+        lens, off = torch.tensor([n], dtype=torch.int32, device="cuda"), torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        kv = hs.paged_kv(k, pages, table, lens, ks, vs)
+        hs.hs_append_tokens(hs.attn_shape(1, 1, d, block, "fp8"), kv, hs.append_params(new_offsets=off), v[:, None], v[:, None])
+        codes, scales = torch.empty((n, d), dtype=torch.uint8, device="cuda"), torch.empty((n, 2), device="cuda")
+        hs.hs_quantize_e4m3_g32(v, codes, scales)
+        for got_c, got_s in ((pages, vs), (k, ks)):
+            assert torch.equal(got_c.view(-1, d)[:n], codes) and torch.equal(got_s.view(-1, 2)[:n], scales)
+
+
 def test_query_in_place():
     w = World("bf16", 128, 16, 4, 2, [20, 0], [30, 3], 128, seed=6)
     w.append()
