@@ -357,10 +357,12 @@ typedef struct hs_append_params {
  *                matter.
  *   smin, smax   the summaries, or both NULL.
  * Without new_offsets a request of seq_lens 0 has no new token.  A request with
- * more new rows than tokens, or offsets that do not ascend within [0, rows], set
- * HS_EBIT_BLOCK_RANGE and leave the request's cache as it was; so does a block index >= max_blocks, for that block.  A page id outside [0,
- * num_pages) sets HS_EBIT_PAGE_RANGE and skips the block; a position outside
- * [0, table_rows) sets HS_EBIT_POSITION and leaves the row's K and Q unwritten.
+ * more new rows than tokens, or with offsets that do not ascend within [0, rows],
+ * sets HS_EBIT_BLOCK_RANGE and its cache stays as it was (offsets that descend may
+ * leave other requests' rows unwritten too); a block index >= max_blocks does so
+ * for that block.  A page id outside [0, num_pages) sets HS_EBIT_PAGE_RANGE and
+ * skips the block; a position outside [0, table_rows) sets HS_EBIT_POSITION and
+ * leaves the row's K and Q unwritten.
  * Two requests must not share a page that the call writes to. */
 HS_API hs_status hs_append_tokens(const hs_attn_shape* shape, const hs_paged_kv* kv, const hs_append_params* params,
                                   int64_t rows, const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,

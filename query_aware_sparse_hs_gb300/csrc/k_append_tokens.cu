@@ -214,7 +214,7 @@ __device__ __forceinline__ bool place_of_row(const KvView& kv, const AppendToken
   int64_t behind = 1;  // tokens from this row's to the end of its request
   if (a.offsets) {
     const int64_t o0 = __ldg(a.offsets + b), o1 = __ldg(a.offsets + b + 1);
-    // behind the last request, or offsets that the K and V units report
+    // behind the last request, or offsets that are reported by the K and V units
     if (row < o0 || row >= o1 || o1 > a.rows || o1 - o0 > __ldg(kv.seq_lens + b)) return false;
     behind = o1 - row;
   }
@@ -472,6 +472,14 @@ __global__ __launch_bounds__(kThreads, threads_per_sm(KIND, P) / kThreads) void 
   const bool is_k = (unit & 1) == 0;
   const int slot = (unit >> 1) / kv.hkv, kvh = (unit >> 1) - slot * kv.hkv;
   const int B = kv.block;
+  const auto bad = [&](int o0, int o1, int L) { return o0 < 0 || o1 < o0 || o1 > a.rows || o1 - o0 > max(L, 0); };
+  // The search below finds every request with rows only where the offsets ascend, so
+  // each request is checked apart from it, by as many of the last units (there are four
+  // or more for each request, and the last ones have spare slots).
+  const int checked = kv_units - 1 - unit;
+  if (tid == 0 && checked < kv.batch &&
+      bad(__ldg(a.offsets + checked), __ldg(a.offsets + checked + 1), __ldg(kv.seq_lens + checked)))
+    set_error(err, HS_EBIT_BLOCK_RANGE);
   // request b has the slots from offsets[b] / B + 2 b on: enough for every block
   // its rows can touch, wherever in a block they begin
   const int shift = (B & (B - 1)) == 0 ? 31 - __clz(B) : -1;
@@ -479,10 +487,7 @@ __global__ __launch_bounds__(kThreads, threads_per_sm(KIND, P) / kThreads) void 
   const int b = last_not_above(kv.batch, slot, lane, [&](int i) { return blocks(__ldg(a.offsets + i)) + 2 * i; });
   const int o0 = __ldg(a.offsets + b), o1 = __ldg(a.offsets + b + 1);
   const int L = __ldg(kv.seq_lens + b);
-  if (o0 < 0 || o1 < o0 || o1 > a.rows || o1 - o0 > max(L, 0)) {
-    if (tid == 0) set_error(err, HS_EBIT_BLOCK_RANGE);
-    return;
-  }
+  if (bad(o0, o1, L)) return;
   const int n = o1 - o0, x = slot - (blocks(o0) + 2 * b);
   if (x < 0 || n == 0) return;
   const int first = L - n;  // cache position of the request's first new row
@@ -938,7 +943,7 @@ bool append_tokens_fits(const KvView& kv, const AppendTokensArgs& a) {
 
 cudaError_t launch_append_tokens(const KvView& kv, const AppendTokensArgs& a, int sms, unsigned* err,
                                  cudaStream_t st) {
-  if (kv.batch == 0 || a.rows == 0) return cudaSuccess;
+  if (kv.batch == 0 || (a.rows == 0 && !a.offsets)) return cudaSuccess;  // (offsets are checked for no rows too)
   return kv.head_dim == 128 ? launch_d<128>(kv, a, sms, err, st) : launch_d<64>(kv, a, sms, err, st);
 }
 

@@ -504,6 +504,58 @@ def test_bad_pages_lengths_offsets_and_positions_are_reported_and_skipped():
         hs.hs_get_device_error()
 
 
+OFFSETS = {
+    # block, earlier tokens, rows of each request, offsets given instead
+    "descend": (16, [20, 0, 5], [30, 20, 3], [0, 40, 20, 53]),
+    "past_the_rows": (16, [20, 0, 5], [30, 20, 3], [0, 30, 50, 4000]),
+    "negative": (16, [20, 0, 5], [30, 20, 3], [-5, 30, 50, 53]),
+    "all_descend": (16, [20, 0, 5], [30, 20, 3], [7, 3, 1, 0]),
+    "one_hidden_by_the_others": (16, [20, 0, 57], [30, 20, 3], [0, 32, 0, 53]),  # two blocks back: the next request's slots
+    "one_hidden_64": (64, [20, 0, 170], [150, 20, 3], [0, 128, 0, 173]),
+    "one_hidden_blocks_of_one": (1, [3, 0, 5], [5, 2, 4], [0, 5, 3, 9]),
+    "extremes": (16, [20, 0, 5], [30, 20, 3], [-2 ** 31, 2 ** 31 - 1, -2 ** 31, 53]),
+    "many": (16, [i % 37 for i in range(90)], [2 + i % 5 for i in range(90)], {41: 0}),
+    "many_last": (16, [i % 37 for i in range(90)], [2 + i % 5 for i in range(90)], {90: 100000}),
+}
+
+
+@pytest.mark.parametrize("name", list(OFFSETS))
+@pytest.mark.parametrize("kind", ["fp8_block", "bf16"])
+def test_every_request_whose_offsets_do_not_ascend_is_reported(name, kind):
+    """The error bit, whatever the other requests' offsets are; the bad requests' pages, scales and summaries stay as they
+    were, the others are written (but for those that a descent hides)."""
+    block, old, new, given = OFFSETS[name]
+    w = World(kind, 64, block, 4, 2, old, new, 64, pad=2, seed=9)
+    hs, n = w.hs, len(new)
+    o = w.offsets.tolist()
+    o = [given.get(i, x) for i, x in enumerate(o)] if isinstance(given, dict) else given
+    w.params._keep[1].copy_(torch.tensor(o, dtype=torch.int32))
+    bad = [o[b] < 0 or o[b + 1] < o[b] or o[b + 1] > w.rows or o[b + 1] - o[b] > w.lens[b] for b in range(n)]
+    keep = {x: w.g[x].clone() for x in "kv"}, {x: None if w.gs[x] is None else w.gs[x].clone() for x in "kv"}, w.smin.clone()
+    assert any(bad)
+    w.append()
+    assert hs.hs_get_device_error() == (hs.HS_ERR_OUT_OF_RANGE, hs.HS_EBIT_BLOCK_RANGE)
+    for b in range(n):
+        pages = torch.from_numpy(w.table[b][w.table[b] >= 0]).long().cuda()
+        for x in "kv":
+            same = torch.equal(w.g[x][pages].view(torch.uint8), keep[0][x][pages].view(torch.uint8))
+            assert same or not bad[b], (b, x)
+            assert not same or bad[b] or o[b] == o[b + 1] or name == "many", (b, x)
+            if bad[b] and w.gs[x] is not None:
+                assert torch.equal(w.gs[x][pages], keep[1][x][pages])
+        if bad[b]:
+            assert torch.equal(w.smin[b], keep[2][b])
+
+
+def test_offsets_are_checked_where_there_are_no_rows():
+    w = World("bf16", 64, 16, 4, 2, [5, 20], [0, 0], 64, seed=2)
+    keep = w.g["k"].clone()
+    w.params._keep[1].copy_(torch.tensor([0, 0, 5], dtype=torch.int32))
+    w.append()
+    assert w.hs.hs_get_device_error() == (w.hs.HS_ERR_OUT_OF_RANGE, w.hs.HS_EBIT_BLOCK_RANGE)
+    assert torch.equal(keep, w.g["k"])
+
+
 def test_other_streams_and_graphs():
     a, b = (World(*CASES["prompts_block"], seed=4) for _ in range(2))
     a.append()
