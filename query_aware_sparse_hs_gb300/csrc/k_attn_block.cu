@@ -521,8 +521,8 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
     const auto window_end = [&](uint32_t u, uint32_t e) {  // first token past the window's whole tiles
       return u + ((e + 32) * Bu - u) / kTile * kTile;
     };
-    const auto load_sel = [&](uint32_t u, uint32_t e) {  // INT_MIN: no such entry
-      return u < u_stop && e + lane < static_cast<uint32_t>(cnt) ? __ldg(sel + e + lane) : INT_MIN;
+    const auto load_sel = [&](uint32_t u, uint32_t e) {  // INT_MIN: no such entry (one that is INT_MIN is out of range anyway)
+      return u < u_stop && e + lane < static_cast<uint32_t>(cnt) ? max(__ldg(sel + e + lane), INT_MIN + 1) : INT_MIN;
     };
     const auto load_page = [&](int j, int& page, int& lim) {  // lim: valid rows of the page
       page = lim = 0;

@@ -316,6 +316,23 @@ def test_bad_selections_and_pages_are_reported_and_skipped():
         assert torch.equal(out3[1], good[1])
 
 
+@pytest.mark.parametrize("entry", [-2 ** 31, -2 ** 31 + 1, -1, 2 ** 31 - 1])
+def test_every_entry_outside_the_request_is_reported(entry):
+    from query_aware_sparse_hs_gb300 import hs
+    for algo in ("auto", "simt"):
+        c = Cache([1000, 100], 1, 128, 16, seed=7)
+        q = query(c, 8)
+        sel, cnt = chosen(c, max(c.nb), None)
+        bad = sel.copy()
+        bad[0, 0, 40] = entry
+        out, lse = attend(c, q, bad, cnt, algo=algo)
+        assert hs.hs_get_device_error() == (hs.HS_ERR_OUT_OF_RANGE, hs.HS_EBIT_BLOCK_RANGE)
+        part, less = sel.copy(), cnt.copy()
+        part[0, 0, :62] = np.delete(sel[0, 0], 40)
+        less[0, 0] = 62
+        check_attention(c, q, part, less, out, lse, simt=algo == "simt")
+
+
 def test_a_block_selected_twice_counts_twice():
     c = Cache([500], 1, 128, 16, seed=7)
     q = query(c, 8)
