@@ -44,11 +44,13 @@
 // cycle: 29.4 us where it takes 28.6; 64 tokens at a time: long runs 5% faster, 30.1
 // for 27.7 us where a warp has few tiles.)
 //
-// Precision: q times a power of two per head (largest entry into [128, 256)) is
-// exact in f16 for entries within 2^-21 of the largest, and absolutely within
-// 2^-33 of it below.  P * vscale, in units of 2^-14 times the largest V scale
-// met so far (a power of two, 2^-112 or more), enters as two f16 terms (22 bits;
-// less where the product is under 2^-14 of the units, by 2^-25 of them at most).  One
+// Precision: q times a power of two per head (largest entry into [256, 512)) is
+// exact in f16 for entries within 2^-25 of the largest (eight bits down to 2^-24), and
+// absolutely within 2^-33 of it below (half of 2^-24 in 256).  The power is 2^127 at
+// most: a head whose largest entry is under 2^-118 is exact, as bf16 ends at 2^-133.
+// P * vscale, in units of 2^-14 times the largest V scale met so far (a power of two,
+// 2^-112 or more), enters as two f16 terms: 22 bits, and absolutely within 2^-25 of
+// the units where it is under an eighth of them.  One
 // term, for bf16 outputs, would save 2 to 3% with up to 8 heads (nothing where memory
 // binds), 8% with 16 heads of 64 channels and 20% of 128 (37.8 us for 47.0), and moves
 // bf16 outputs by 6 10^-4 of their norm.  Sums, maxima and
@@ -642,8 +644,8 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      float f = 1.0f;  // 2^(7 - exponent of amax)
-      if (amax > 0.0f && amax < INFINITY) f = __uint_as_float(static_cast<uint32_t>(min(254, 261 - static_cast<int>(__float_as_uint(amax) >> 23))) << 23);
+      float f = 1.0f;  // 2^(8 - exponent of amax), 2^127 at most
+      if (amax > 0.0f && amax < INFINITY) f = __uint_as_float(static_cast<uint32_t>(min(254, 262 - static_cast<int>(__float_as_uint(amax) >> 23))) << 23);
       const float fs = a.scale < 0.0f ? -f : f;  // the factors of the logits are not negative
 #pragma unroll
       for (int k = 0; k < kChunks; ++k)

@@ -230,6 +230,45 @@ def test_v_scales_near_the_smallest():
     check_attention(c, q, sel, cnt, out, lse)
 
 
+@pytest.mark.parametrize("d,group", [(128, 8), (64, 16)])
+@pytest.mark.parametrize("top", [1.0, 1.9921875, 2.0 ** 100, 2.0 ** -100, 2.0 ** -117])
+def test_small_entries_of_a_query_are_held_to_2_33_of_the_largest(d, group, top):
+    """One token, so that lse is its logit: the query's largest entry meets a zero of K, a small one the largest code."""
+    c = Cache([1], 1, d, 16, seed=1, poison=False)
+    c.codes["k"][c.table[0, 0, 0], 0] = 0
+    c.codes["k"][c.table[0, 0, 0], 0, 1] = 0x7E  # 448
+    c.scales["k"][:] = 2.0 ** 24
+    c.up()
+    sel, cnt = chosen(c, 1, None)
+    q = torch.zeros((1, group, d), dtype=torch.float64)
+    q[:, :, 0] = top
+    for h in range(group):
+        q[:, h, 1] = top * 2.0 ** -(24 + h) * 1.5
+    q = q.to(torch.bfloat16).cuda()
+    out, lse = attend(c, q, sel, cnt, scale=1.0 / top)
+    qn = q.double().cpu().numpy()[0]
+    want = qn[:, 1] * 448 * 2.0 ** 24 / top
+    # half a step of f16's smallest numbers; the products are exact, then four roundings of fp32
+    err = np.where(qn[:, 1] >= 2.0 ** -25 * top, 0.0, 2.0 ** -33 * 448 * 2.0 ** 24) + 8 * U * np.abs(want)
+    assert (np.abs(lse[0].double().cpu().numpy() - want) <= err).all()
+
+
+def test_queries_at_the_end_of_bf16_are_exact():
+    c = Cache([1], 1, 64, 16, seed=1, poison=False)
+    c.codes["k"][c.table[0, 0, 0], 0] = 0
+    c.codes["k"][c.table[0, 0, 0], 0, 1] = 0x7E
+    c.scales["k"][:] = 2.0 ** 90
+    c.up()
+    sel, cnt = chosen(c, 1, None)
+    for top in (2.0 ** -119, 1.9921875 * 2.0 ** -119, 2.0 ** -126, 2.0 ** -133):
+        q = torch.zeros((1, 8, 64), dtype=torch.float64)
+        q[:, :, 0], q[:, :, 1] = top, 2.0 ** -133
+        q = q.to(torch.bfloat16).cuda()
+        out, lse = attend(c, q, sel, cnt, scale=2.0 ** 36)
+        want = float(q[0, 0, 1].double()) * 448 * 2.0 ** 126
+        assert want == 3.5 and (lse - want).abs().max() <= 8 * U * want
+
+
 def test_pages_of_zeros_and_large_or_tiny_queries():
     c = Cache([300, 64], 1, 128, 16, seed=4, poison=False)
     for p in c.table[0, 0, 3:9]:  # as the append leaves a page of zeros
