@@ -2,6 +2,9 @@
 the binding's own checks of shapes and types.  CPU only: the addresses are never followed."""
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -132,3 +135,24 @@ def test_the_binding_checks_shapes_and_types():
         hs.hs_append_tokens(shape, kv, hs.append_params(new_offsets=off[:3]), k, k)
     with pytest.raises(ValueError):  # fewer positions than rows
         hs.hs_append_tokens(shape, kv, hs.append_params(new_offsets=off, positions=off), k, k)
+
+
+def test_the_binding_loads_on_a_torch_without_cuda():
+    """Such a torch lacks the names that the short ways to the current device and stream take."""
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+from query_aware_sparse_hs_gb300 import hs
+shape, kv = hs.attn_shape(8, 2, 64, 16, "bf16"), hs.PagedKV()
+kv.batch = 3
+rows = torch.zeros((3, 2, 64), dtype=torch.bfloat16)
+try:
+    hs.hs_append_tokens(shape, kv, hs.append_params(), rows, rows)
+except ValueError as e:
+    print("refused:", e)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "on the current device" in r.stdout, r.stderr
