@@ -167,7 +167,7 @@ def _check(status: int, where: str):
 
 
 def _ptr(t) -> int | None:
-    if t is None or t.__class__ is int:  # None, or an address already
+    if t is None or isinstance(t, int):  # None, or an address already
         return t
     if not t.is_contiguous():
         raise ValueError("tensor arguments must be contiguous")

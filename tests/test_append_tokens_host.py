@@ -156,3 +156,13 @@ except ValueError as e:
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "on the current device" in r.stdout, r.stderr
+
+
+def test_addresses_may_be_of_a_subclass_of_int():
+    from query_aware_sparse_hs_gb300 import hs
+
+    class Address(int):
+        pass
+
+    assert hs.select_params(0, 0, 1, 1, 0.5, Address(P)).score_history == P
+    assert hs.attn_params(0.1, split_counters=Address(P)).split_counters == P
