@@ -55,6 +55,7 @@ class SelectParams(ctypes.Structure):
 class AppendParams(ctypes.Structure):
     _fields_ = [("new_offsets", c_void_p), ("positions", c_void_p), ("cos_sin", c_void_p),
                 ("table_rows", c_int32), ("rotary_dim", c_int32), ("interleaved", c_int32)]
+    _requests = _rows = None  # what append_params knows of its tensors; of addresses nothing is known
 
 
 class AttnParams(ctypes.Structure):

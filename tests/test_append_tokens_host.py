@@ -166,3 +166,16 @@ def test_addresses_may_be_of_a_subclass_of_int():
 
     assert hs.select_params(0, 0, 1, 1, 0.5, Address(P)).score_history == P
     assert hs.attn_params(0.1, split_counters=Address(P)).split_counters == P
+
+
+def test_params_filled_in_by_hand_are_taken():
+    """With addresses in them, as the structures of the other calls: nothing but what the library checks."""
+    from query_aware_sparse_hs_gb300 import hs
+    shape, kv = hs.attn_shape(8, 2, 64, 16, "bf16"), hs.PagedKV()
+    kv.batch = 3
+    rows = torch.zeros((3, 2, 64), dtype=torch.bfloat16)
+    p = hs.AppendParams()
+    p.new_offsets, p.table_rows = P, 0
+    with pytest.raises(ValueError, match="on the current device"):  # the rows are not on a GPU
+        hs.hs_append_tokens(shape, kv, p, rows, rows)
+    assert p._requests is None and p._rows is None
