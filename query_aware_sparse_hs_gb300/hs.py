@@ -55,7 +55,7 @@ class SelectParams(ctypes.Structure):
 class AppendParams(ctypes.Structure):
     _fields_ = [("new_offsets", c_void_p), ("positions", c_void_p), ("cos_sin", c_void_p),
                 ("table_rows", c_int32), ("rotary_dim", c_int32), ("interleaved", c_int32)]
-    _requests = _rows = None  # what append_params knows of its tensors; of addresses nothing is known
+    _requests = _rows = _device = None  # what append_params knows of its tensors; of addresses nothing is known
 
 
 class AttnParams(ctypes.Structure):
@@ -267,11 +267,15 @@ def append_params(cos_sin=None, interleaved=False, new_offsets=None, positions=N
     for t, dt in ((cos_sin, torch.float32), (new_offsets, torch.int32), (positions, torch.int32)):
         if t is not None and t.dtype != dt:
             raise ValueError(f"expected {dt}, got {t.dtype}")
+    devices = {t.get_device() for t in (cos_sin, new_offsets, positions) if t is not None}
+    if len(devices) > 1:
+        raise ValueError("cos_sin, new_offsets and positions must be on one device")
     p = AppendParams(_ptr(new_offsets), _ptr(positions), _ptr(cos_sin),
                      0 if cos_sin is None else int(cos_sin.shape[0]), int(rotary_dim), 1 if interleaved else 0)
     p._keep = (cos_sin, new_offsets, positions)
     p._requests = None if new_offsets is None else new_offsets.numel() - 1
     p._rows = None if positions is None else positions.numel()
+    p._device = devices.pop() if devices else None
     return p
 
 
@@ -312,6 +316,8 @@ def hs_append_tokens(shape, kv, params, new_k, new_v, q=None, q_out=None, smin=N
         raise ValueError("new_offsets must have batch + 1 entries")
     if params._rows is not None and params._rows < rows:
         raise ValueError("positions must have an entry for every row")
+    if params._device is not None and params._device != device:
+        raise ValueError("cos_sin, new_offsets and positions must be on the current device")
     st = _append_tokens(_byref(shape), _byref(kv), _byref(params), rows, qp, qs, op, os_, kp, ks, vp, vs, _ptr(smin),
                         _ptr(smax), _raw_stream(device) if stream is None else _stream(stream))
     if st:

@@ -556,6 +556,18 @@ def test_offsets_are_checked_where_there_are_no_rows():
     assert torch.equal(keep, w.g["k"])
 
 
+def test_tables_that_are_not_on_the_gpu_are_refused():
+    w = World("bf16", 64, 16, 4, 2, [5, 20], [3, 4], 64, positions=True, seed=2)
+    cos_sin, off, pos = w.params._keep[0], w.params._keep[1], w.params._keep[2]
+    keep = w.g["k"].clone()
+    with pytest.raises(ValueError):
+        w.hs.append_params(cos_sin, new_offsets=off.cpu(), positions=pos)
+    for p in (w.hs.append_params(cos_sin.cpu(), new_offsets=off.cpu()), w.hs.append_params(new_offsets=off.cpu())):
+        with pytest.raises(ValueError, match="on the current device"):
+            w.hs.hs_append_tokens(w.shape, w.kv, p, w.kn, w.vn)
+    assert torch.equal(keep, w.g["k"])
+
+
 def test_other_streams_and_graphs():
     a, b = (World(*CASES["prompts_block"], seed=4) for _ in range(2))
     a.append()
