@@ -2,6 +2,9 @@
 decode steps on it, against plain 64-bit loops.  GPU only."""
 
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -451,6 +454,64 @@ def test_two_calls_at_once_with_their_own_workspaces():
         torch.cuda.synchronize()
         for (o, l), (wo, wl) in zip(got, want):
             assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+SECOND_CONTEXT = """
+import ctypes, math
+import numpy as np
+from query_aware_sparse_hs_gb300 import hs
+cu = ctypes.CDLL("libcuda.so.1")
+
+def ok(status):
+    assert status == 0, status
+
+def on_gpu(a):
+    p = ctypes.c_uint64()
+    ok(cu.cuMemAlloc_v2(ctypes.byref(p), ctypes.c_size_t(a.nbytes)))
+    ok(cu.cuMemcpyHtoD_v2(p, a.ctypes.data_as(ctypes.c_void_p), ctypes.c_size_t(a.nbytes)))
+    return p.value
+
+def attend(d, group):
+    shape, p = hs.attn_shape(group, 1, d, 64, "fp8_block"), hs.attn_params(0.1, True)
+    kv = hs.PagedKV()
+    kv.k_pages, kv.v_pages = on_gpu(np.zeros((2, 64, d), np.uint8)), on_gpu(np.full((2, 64, d), 0x38, np.uint8))
+    kv.k_scales = kv.v_scales = on_gpu(np.ones(2, np.float32))
+    kv.page_table, kv.seq_lens = on_gpu(np.array([0, 1], np.int32)), on_gpu(np.array([100], np.int32))
+    kv.batch, kv.max_blocks, kv.num_pages = 1, 2, 2
+    need = hs.hs_workspace_bytes(shape, 1, 2, p)
+    out, lse = np.zeros((group, d), np.float32), np.zeros(group, np.float32)
+    go, gl = on_gpu(out), on_gpu(lse)
+    r = ctypes.byref
+    status = hs.library().hs_sparse_paged_decode_attn(
+        r(shape), r(kv), on_gpu(np.zeros((group, d), np.uint16)), on_gpu(np.array([0, 1], np.int32)),
+        on_gpu(np.array([2], np.int32)), 2, r(p), go, gl, on_gpu(np.zeros(need, np.uint8)), need, None)
+    assert status == hs.HS_OK, status
+    ok(cu.cuCtxSynchronize())
+    ok(cu.cuMemcpyDtoH_v2(out.ctypes.data_as(ctypes.c_void_p), ctypes.c_uint64(go), ctypes.c_size_t(out.nbytes)))
+    ok(cu.cuMemcpyDtoH_v2(lse.ctypes.data_as(ctypes.c_void_p), ctypes.c_uint64(gl), ctypes.c_size_t(lse.nbytes)))
+    assert (out == 1).all() and np.abs(lse - math.log(100)).max() < 1e-5  # 4 roundings of a number under 8
+
+ok(cu.cuInit(0))
+dev, ctx = ctypes.c_int(), ctypes.c_void_p()
+ok(cu.cuDeviceGet(ctypes.byref(dev), 0))
+ok(cu.cuDevicePrimaryCtxRetain(ctypes.byref(ctx), dev))
+ok(cu.cuCtxSetCurrent(ctx))
+for shape in ((128, 8), (64, 16)):
+    attend(*shape)
+other = ctypes.c_void_p()
+ok(cu.cuCtxCreate_v2(ctypes.byref(other), 0, dev))
+for shape in ((128, 8), (64, 16)):
+    attend(*shape)
+ok(cu.cuCtxDestroy_v2(other))
+print("both contexts")
+"""
+
+
+def test_a_second_context_on_the_device():
+    """What a launch needs set, once for the device, holds in a context made later."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", SECOND_CONTEXT], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "both contexts" in r.stdout, r.stderr
 
 
 def test_pages_past_4_gib_of_the_pool():
