@@ -504,6 +504,110 @@ def test_bad_pages_lengths_offsets_and_positions_are_reported_and_skipped():
         hs.hs_get_device_error()
 
 
+ONE_ROW = {
+    # as CASES, one new token per request and no offsets: kind, d, block, hq, hkv, earlier tokens, rotary, interleaved, positions
+    "f32": ("f32", 64, 16, 8, 2, [0, 5, 16, 31], 64, False, True),
+    "f32_partial": ("f32", 128, 16, 4, 4, [0, 15, 47], 96, False, False),
+    "f32_pairs": ("f32", 128, 5, 2, 1, [4, 5, 6], 128, True, False),
+    "f32_unrotated": ("f32", 64, 16, 2, 2, [3, 0], 0, False, False),
+    "bf16_positions": ("bf16", 128, 64, 32, 4, [0, 63, 64, 1], 128, False, True),
+    "bf16_pairs": ("bf16", 64, 32, 6, 6, [0, 33], 48, True, True),
+    "bf16_one_head": ("bf16", 64, 16, 1, 1, [9], 16, False, False),
+    "g32_positions": ("fp8", 128, 16, 8, 8, [0, 16, 17], 128, False, True),
+    "g32_partial": ("fp8", 128, 16, 4, 2, [3, 20], 48, False, False),
+    "g32_pairs": ("fp8", 128, 48, 2, 2, [47, 48], 96, True, False),
+    "block_positions": ("fp8_block", 128, 64, 32, 4, [0, 63, 64, 130, 1], 128, False, True),
+    "block_partial": ("fp8_block", 128, 256, 4, 2, [255, 256, 100], 32, False, False),
+    "block_pairs": ("fp8_block", 64, 16, 16, 1, [5, 16, 0], 64, True, True),
+    "block_pairs_d128": ("fp8_block", 128, 5, 2, 2, [3, 4, 5, 44], 96, True, False),
+    "block_of_one": ("fp8_block", 64, 1, 2, 1, [0, 3], 64, False, False),
+    "block_unrotated": ("fp8_block", 128, 48, 4, 4, [30, 0], 0, False, False),
+}
+
+
+def one_row_world(name, grow=0, **kw):
+    kind, d, block, hq, hkv, old, rotary, interleaved, positions = ONE_ROW[name]
+    w = World(kind, d, block, hq, hkv, old, [1] * len(old), rotary, interleaved, positions, seed=len(name), **kw)
+    assert w.offsets is None
+    if grow:
+        w.kn *= 2.0 ** grow
+        w.vn *= 2.0 ** grow
+        w.qkv[:, hq:] *= 2.0 ** grow
+    return w
+
+
+@pytest.mark.parametrize("grow", [0, 7, -12])
+@pytest.mark.parametrize("name", list(ONE_ROW))
+def test_one_row_per_request_matches_the_definition(name, grow):
+    """Rows of the size of the earlier ones, larger (a page's scale has to grow: the earlier codes and their summary are
+    taken anew, whichever channels the rotation gave a thread) and smaller."""
+    w = one_row_world(name, grow)
+    before = {x: None if w.gs[x] is None else w.gs[x].clone() for x in "kv"}
+    w.append()
+    check(w)
+    check_summaries(w)
+    if grow > 0 and w.kind == "fp8_block":
+        last = [w.table[b, :, n // w.block] for b, n in enumerate(w.old) if n % w.block]
+        if last:
+            pages = torch.from_numpy(np.concatenate(last)).long().cuda()
+            assert (w.gs["k"][pages] > before["k"][pages]).all() and (w.gs["v"][pages] > before["v"][pages]).all()
+    keep = [t.clone() for t in (w.g["k"], w.g["v"], w.q_out, w.smin, w.smax)]
+    w.append()
+    for a, b in zip(keep, (w.g["k"], w.g["v"], w.q_out, w.smin, w.smax)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16_positions", "g32_positions", "block_positions", "block_pairs"])
+def test_one_row_per_request_reports_and_skips_what_is_out_of_range(name):
+    def of(w, b):  # what request b's append may write
+        pages = torch.from_numpy(w.table[b][w.table[b] >= 0]).long().cuda()
+        return [t[pages] for t in (w.g["k"], w.g["v"])] + [w.smin[b], w.smax[b]] + [t[pages] for t in (w.gs["k"], w.gs["v"]) if t is not None]
+
+    def same(a, b):
+        return all(torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8)) for x, y in zip(a, b))
+
+    good = one_row_world(name)
+    good.append()
+    hs, last = good.hs, len(good.new) - 1
+
+    def others(w):  # the other requests are as in the good call
+        assert all(same(of(w, b), of(good, b)) and torch.equal(w.q_out[b], good.q_out[b]) for b in range(last + 1) if b != 1)
+
+    # no token: nothing is written for the request, and nothing is wrong with that
+    w = one_row_world(name)
+    was = of(w, 1)
+    w.gl[1] = 0
+    w.append()
+    assert hs.hs_get_device_error() == (hs.HS_OK, 0)
+    assert same(of(w, 1), was) and (w.q_out[1] == SENTINEL).all()
+    others(w)
+    # no page, a page past the pool, a block past the table: Q needs none of them
+    for change, bit in (("gt", hs.HS_EBIT_PAGE_RANGE), ("pool", hs.HS_EBIT_PAGE_RANGE), ("gl", hs.HS_EBIT_BLOCK_RANGE)):
+        w = one_row_world(name)
+        was, j = of(w, 1), w.old[1] // w.block
+        if change == "gl":
+            w.gl[1] = w.mb * w.block + 1
+            w.params = hs.append_params(w.params._keep[0], w.interleaved, None, torch.zeros(last + 1, dtype=torch.int32, device="cuda"))
+        else:
+            w.gt[1, :, j] = -1 if change == "gt" else w.pages
+        w.append()
+        assert hs.hs_get_device_error() == (hs.HS_ERR_OUT_OF_RANGE, bit), change
+        assert same(of(w, 1), was)
+        if change != "gl":
+            others(w)
+    # a position without angles: K, its summary and scale and Q stay, V is written
+    for bad in (-1, w.cos_sin.shape[0], 2 ** 31 - 1):
+        w = one_row_world(name)
+        was = of(w, 1)
+        w.params._keep[2][1] = bad
+        w.append()
+        assert hs.hs_get_device_error() == (hs.HS_ERR_OUT_OF_RANGE, hs.HS_EBIT_POSITION)
+        now, want = of(w, 1), of(good, 1)
+        assert same([now[0]] + now[2:5], [was[0]] + was[2:5])
+        assert same([now[1]] + now[5:], [want[1]] + want[5:]) and (w.q_out[1] == SENTINEL).all()
+        others(w)
+
+
 OFFSETS = {
     # block, earlier tokens, rows of each request, offsets given instead
     "descend": (16, [20, 0, 5], [30, 20, 3], [0, 40, 20, 53]),
