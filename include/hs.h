@@ -152,12 +152,15 @@ typedef struct hs_select_params {
 /* Attention options.  scale multiplies q.k (usually 1/sqrt(head_dim)).
  * blocks_per_split: selected blocks handled by one CTA before the LSE merge;
  * 0 = chosen by the library from the SMs the call may use.  algo: 0 =
- * automatic, 1 = CUDA-core kernel (every dtype), 2 = tensor-core (tcgen05)
- * kernel (bf16 and e4m3 only; HS_ERR_UNSUPPORTED otherwise).  The e4m3
- * tensor-core kernel forms each V value, code times scale, in f16 (as it does
- * the products with P), so it needs |code * scale| <= 65504 (a V scale up to
- * 146 for codes up to 448); beyond that its output is not finite.  The
- * CUDA-core kernel forms them in fp32.  max_ctas: 0 =
+ * automatic, 1 = CUDA-core kernel (every dtype), 2 = tensor-core kernel: tcgen05
+ * for bf16 and e4m3 with grouped scales (head_dim 128 and the block sizes above;
+ * at most 8 query heads per kv head for e4m3), warp-level products for e4m3 with a
+ * scale per page; HS_ERR_UNSUPPORTED where there is none.  The tensor-core kernel
+ * of e4m3 with grouped scales forms each V value, code times scale, in f16 (as it
+ * does the products with P), so it needs |code * scale| <= 65504 (a V scale up to
+ * 146 for codes up to 448); beyond that its output is not finite.  The CUDA-core
+ * kernel forms them in fp32; with a scale per page the tensor-core kernel does not
+ * form them and has no such bound.  max_ctas: 0 =
  * the tensor-core kernel runs one CTA on every SM; n > 0 = at most n CTAs (and
  * the automatic split for n SMs), leaving the other SMs to work launched
  * beside it, such as hs_swapin_copy.  Each of its CTAs takes a whole SM's
@@ -198,7 +201,11 @@ typedef struct hs_select_params {
  * counts, whatever blocks_per_split and these flags say, and needs no more
  * workspace for more requests; it waits for nothing but its own copies, so
  * wait_limit_ns does not concern it; max_ctas as above; without split_counters
- * it merges in a second launch.  Pools of 2^32 token rows, and selections of 2^31
+ * it merges in a second launch.  It holds a query's entries exactly within 2^-25
+ * of the head's largest, and absolutely within 2^-33 of that below; a token's
+ * probability times its V scale to 22 bits, or absolutely within 2^-38 of the
+ * largest V scale of the selection (of 2^-112 at least); everything else in fp32.
+ * A bf16 output is the fp32 output rounded.  Pools of 2^32 token rows, and selections of 2^31
  * tokens or (over all requests and kv heads) 2^36, are not supported.
  * Calls that may overlap on the GPU (other streams, graphs replayed side by side)
  * need a workspace and split_counters each. */
@@ -276,9 +283,10 @@ HS_API int32_t hs_attn_geometry(const hs_attn_shape* shape, int32_t batch, int32
 /* Per-block key summaries, [KVS] §5 Quest: for every request b, kv head kvh and
  * block j with first_block <= j < N_b, smin/smax[b][kvh][j][d] = min/max over
  * the block's valid tokens t in [jB, min((j+1)B, L_b)) of K[t][d].  e4m3 K is
- * dequantised (code * scale in fp32; with a scale per page the min and max are
- * taken over the codes and then scaled, which is the same) first and the results rounded outward to
- * bf16 (min toward -inf, max toward +inf).  Other entries are not written.
+ * dequantised first (code * scale in fp32; with a scale per page the min and max
+ * are taken over the codes and then scaled, which is the same) and the results
+ * rounded outward to bf16 (min toward -inf, max toward +inf).  Other entries are
+ * not written.
  * Reading a page id outside [0, num_pages) sets HS_EBIT_PAGE_RANGE and skips
  * that block. */
 HS_API hs_status hs_build_block_summaries(const hs_attn_shape* shape, const hs_paged_kv* kv,
@@ -344,7 +352,8 @@ typedef struct hs_append_params {
  * scale when that is at least s; else it takes s, the codes of the earlier rows
  * are multiplied by old/new (exact but for values under the smallest e4m3
  * step, when the old scale is a power of two) and its summary is taken anew.
- * Values are stored nearest-even; infinities as +-448 s, NaN as the NaN code.
+ * Values are stored nearest-even (where the caller's s is no power of two, of the
+ * value times 1/s rounded); infinities as +-448 s, NaN as the NaN code.
  *   q, q_out     [rows][Hq][D], rows q_stride, q_out_stride elements apart; both
  *                NULL: no Q.  q_out may be q itself (same stride), else they do
  *                not overlap.

@@ -23,14 +23,19 @@
 //     Q).  Other CTAs rotate Q: a warp takes 16 heads of a few consecutive rows, and
 //     reads a row's cos and sin once for the 16.
 //     Memory-bound: prompts of 16 requests of up to 4096 tokens, 32 / 4 heads of 128
-//     channels, block-scaled, 859 MB: 131 us, 0.98 of the copy rate; bf16 pages
-//     0.99; 8 query heads on 8 kv heads 0.53: there the K and V units'
-//     instructions bind (two rotations, minimum and maximum of every channel).
+//     channels, block-scaled, 859 MB: 131 us, 0.98 of the copy rate; 8 prompts in bf16
+//     pages 1.00; with 8 query heads on 8 kv heads 0.78, and 0.54 for both e4m3 kinds
+//     (68 us): there the K and V units' instructions count (two rotations, minimum and
+//     maximum of every channel: 46 M, 0.58 of the issue slots, the 20 warps of an SM
+//     waiting for their loads in between).
 //   one row per request: the D / 16 threads of a row take its K and V, so a warp
 //     holds several (request, kv head) pairs; the row's thread holds the channels
 //     of the summary too, and nothing is exchanged but the row's largest value.
 //     Latency-bound: seq_lens, page table, then everything else at once; 256
-//     requests x 4 kv heads 3.3 us.
+//     requests x 4 kv heads 3.3 us, block-scaled 3.5.  A page whose scale grows has its
+//     earlier rows rewritten by the D / 16 threads alone, K and then V: where the pages
+//     of all 256 requests grow at once 10 us with 16-token pages, 30 with 64, 118 with
+//     256.
 #include <float.h>
 
 #include "hs_internal.h"
@@ -193,7 +198,7 @@ __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const Angle
   }
 }
 
-// CTAs for the touched blocks: with offsets, request b's blocks have the slots
+// Units for the touched blocks: with offsets, request b's blocks have the slots
 // from offsets[b] / B + 2 b on.
 int64_t kv_units_of(const KvView& kv, const AppendTokensArgs& a) {
   return (a.rows / kv.block + 2 * static_cast<int64_t>(kv.batch)) * kv.hkv * 2;
@@ -280,8 +285,7 @@ __device__ void rotate_q(const KvView& kv, const AppendTokensArgs& a, int h0, in
   }
 }
 
-// 16 codes of a row, as both formats of e4m3 store them: the encoded values and
-// (box) the values they stand for.
+// What 8 codes stand for at scale s.
 __device__ __forceinline__ void decode8(uint2 c, float s, float (&x)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -424,10 +428,10 @@ __device__ __forceinline__ uint4 rescaled(uint4 v, float f) {
 // those of more turns are read once more, from the caches.  P = 2 leaves registers for
 // 640 threads on an SM instead of 512: prompts of 16 requests 131 us, P = 4, all rows
 // of a page held, 134; 8 / 8 heads 70 and 79.  Where all units run at once that counts
-// for nothing and holding saves the second reading: a chunk of 2000 tokens 11.9 us,
-// P = 2 13.2.  Grouped e4m3: P = 2, 8 / 8 heads 71 us, P = 4 95.  bf16 and f32 have
-// registers enough for P = 4 (bf16 56 us at 640 threads, 60 at 512; f32 89 at 512, 97 at
-// 384).
+// for nothing and holding saves the second reading: a chunk of 2000 tokens 12.2 us,
+// P = 2 13.2.  Grouped e4m3: P = 2, 8 / 8 heads 71 us, P = 4 95.  bf16 and f32 take P = 4:
+// bf16 at 640 threads, whose 96 registers spill 112 bytes (188 where one warp takes a
+// page), 56 us, at 512 without spills 60; f32 at 512 (up to 36 bytes) 89, at 384 97.
 constexpr int threads_per_sm(int kind, int p) {
   return kind == HS_KV_F32 || (kind == HS_KV_FP8E4M3_BLOCK && p == 4) ? 512 : 640;
 }

@@ -23,8 +23,10 @@
 //   O^T[channel][head] += V^T . P^T: 16 channels by 8 heads over 16 tokens.
 // (tcgen05 would take K's codes as they are, but P and V through shared and tensor
 // memory: that chain, not the products, bounds the kernel of grouped scales at
-// half the copy rate; here the matrix pipe is 6% busy, and its e4m3 form of this
-// instruction, which converts inside, was slower by an eighth.)
+// half the copy rate; here the matrix pipe is 23% busy, for uneven requests and for 16
+// heads of 64 channels alike, and its e4m3 form of this instruction, which converts
+// inside, was slower by an eighth.  A form whose V codes and P enter the 8-bit products
+// of tcgen05 as they are has not been built.)
 // Order of the contracted channels and of the output's channels is free, so a
 // lane's operands are whole 16-byte pieces of a row as it lies in memory; V's
 // transposition is one byte permutation per two operands.  Rows lie in shared
@@ -38,11 +40,13 @@
 // for the join of its warps and, where pairs are cut, the merge (2 and 2 us): 32
 // requests x 4096 selected tokens, 134 MB, no pair cut: 28.8 us, 0.70.  (Asking the L2
 // ahead for selections and pages did not shorten the chain.)  With 16 query heads
-// and 64 channels a 32-token tile takes an SM about 240 cycles whatever the number
-// of warps: instructions, some 440 a tile.  (Codes converted by shifts on the
-// integer pipe instead of the converting instruction, which retires 17 pairs a
-// cycle: 29.4 us where it takes 28.6; 64 tokens at a time: long runs 5% faster, 30.1
-// for 27.7 us where a warp has few tiles.)
+// and 64 channels (12 requests x 2 heads, 75 MB: 31.0 us, 0.36) a 32-token tile takes an
+// SM about 260 cycles whatever the number of warps, and about half of the call is
+// start, join and merge of parts of ten tiles a warp.  (Codes converted by shifts on
+// the integer pipe instead of the converting instruction, which retires 17 pairs a
+// cycle: 3% slower; 64 tokens at a time: long runs 5% faster, 8% slower where a warp has
+// few tiles.)  16 heads of 128 channels: 16 requests x 4 heads x 65536 tokens 228 us,
+// 0.71; 255 registers, 56 bytes spilled.
 //
 // Precision: q times a power of two per head (largest entry into [256, 512)) is
 // exact in f16 for entries within 2^-25 of the largest (eight bits down to 2^-24), and
@@ -68,15 +72,16 @@ namespace {
 constexpr int kTeamWarps = 4;
 // Teams of a CTA, and with them the warps of an SM (one CTA on each): as many as
 // the registers (128 channels: up to 255 a thread, 64 channels: 168) and the
-// rings of tiles allow.  64 channels, 32 x 4 heads x 65536 tokens: 12 warps 195 us, 8
-// warps 222, 16 warps (128 registers) 192 but slower for short requests.
+// rings of tiles allow.  64 channels, 32 x 4 heads x 65536 tokens, with one term of P:
+// 12 warps 195 us, 8 warps 222, 16 warps (128 registers) 192 but slower for short
+// requests; with two terms 12 warps 202.
 __host__ __device__ constexpr int teams_of(int head_dim) { return head_dim == 128 ? 2 : 3; }
 constexpr int kMaxWarps = 3 * kTeamWarps;
 constexpr int kTile = 32;       // tokens a warp handles at a time
 constexpr int kStages = 3;      // tiles in a warp's ring
 constexpr int kMinTiles = 8;    // tiles of a part of a cut pair at least
 // Pairs of up to so many tiles are not cut: two for each warp of a CTA (4 pairs of
-// 1000 tokens, 128 channels, 32 tiles: 9.6 us cut, 11.0 whole; 16 tiles: 8.2 whole).
+// 1000 tokens, 128 channels, 32 tiles: 9.6 us cut, 11.0 whole; 16 tiles: 8.4 whole).
 __host__ __device__ constexpr int whole_tiles(int teams) { return 2 * teams * kTeamWarps; }
 constexpr int kMergeTiles = 3;  // what a merge costs, in tiles per warp
 constexpr float kLog2e = 1.4426950408889634f;
@@ -84,8 +89,8 @@ constexpr float kMinRef = 1.925929944387236e-34f;  // 2^-112
 constexpr uint32_t kMaxRef = 0x7f000000u;          // 2^127, as bits
 // P * vscale enters in units of 2^-kUnit times the reference: 2^14 at most, twice that
 // for a V scale above 2^127, which f16 holds.  (P up to 2^6, in units of 2^-8, would
-// spare most rescalings of the state: 28.3 -> 27.8 us for 16 heads of 64 channels,
-// for 6 bits less below the f16 range.)
+// spare most rescalings of the state, 2% for 16 heads of 64 channels, for 6 bits less
+// below the f16 range.)
 constexpr int kUnit = 14;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -175,8 +180,8 @@ struct BlockArgs {
   float scale;
 };
 
-// Tiles of pair p's selection.
-__device__ __forceinline__ int pair_count(const KvView& kv, const BlockArgs& a, int64_t p) {
+// Selected blocks of pair p, and tiles of so many.
+__device__ __forceinline__ int pair_count(const BlockArgs& a, int64_t p) {
   const int c = __ldg(a.sel_count + p);
   return min(max(c, 0), a.capacity);
 }
@@ -210,8 +215,9 @@ struct Team {
 //   time of a short part; with more pairs than CTAs, or pairs so uneven that CTAs
 //   are left idle, teams balance better.  Taken where every CTA has one part at
 //   most and the longest pair's, in tiles per warp, is not longer than the teams' by
-//   more than a merge.  32 requests x 4 heads x 4096 selected tokens: joint 28 us, teams
-//   32; 24 uneven requests x 4 heads: 56 and 48; 64 x 4 heads x 4096: 54 and 49.
+//   more than a merge.  With one term of P, 32 requests x 4 heads x 4096 selected tokens:
+//   joint 28 us, teams 32; 24 uneven requests x 4 heads: 56 and 48; 64 x 4 heads x 4096:
+//   54 and 49.
 struct Cut {
   int per, slots, whole;
   bool joint;
@@ -251,7 +257,7 @@ __device__ Cut choose_cut(const KvView& kv, const BlockArgs& a, int ctas, int te
   const int p0 = min(pairs, cta.rank * mine_n), p1 = min(pairs, p0 + mine_n);
   int total = 0, longest = 0;  // tiles
   for (int p = p0; p < p1; ++p) {
-    const int c = pair_count(kv, a, p), n = tiles_of(kv, c);
+    const int c = pair_count(a, p), n = tiles_of(kv, c);
     seen(p, c);
     total += n;
     longest = max(longest, n);
@@ -289,7 +295,7 @@ __device__ int number_parts(const KvView& kv, const BlockArgs& a, const Cut& cut
   const int p0 = min(pairs, team.rank * mine_n), p1 = min(pairs, p0 + mine_n);
   int64_t mine = 0;  // parts, and rows of the workspace in the upper half
   for (int p = p0; p < p1; ++p) {
-    const int k = parts_of(tiles_of(kv, pair_count(kv, a, p)), cut.per, cut.whole);
+    const int k = parts_of(tiles_of(kv, pair_count(a, p)), cut.per, cut.whole);
     mine += k + (k > 1 ? static_cast<int64_t>(k) << 32 : 0);
   }
   int64_t at = mine;
@@ -308,7 +314,7 @@ __device__ int number_parts(const KvView& kv, const BlockArgs& a, const Cut& cut
   }
   for (int p = p0; p < p1; ++p) {
     Pairs n;
-    n.count = parts_of(tiles_of(kv, pair_count(kv, a, p)), cut.per, cut.whole);
+    n.count = parts_of(tiles_of(kv, pair_count(a, p)), cut.per, cut.whole);
     n.part = static_cast<int>(at & 0xffffffff);
     n.row = static_cast<int>(at >> 32);
     each(p, n);
@@ -451,7 +457,7 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
   });
   if (s_empty) {  // nothing selected: out = 0, lse = -inf
     for (int p = blockIdx.x; p < pairs; p += ctas) {
-      if (pair_count(kv, a, p) > 0) continue;
+      if (pair_count(a, p) > 0) continue;
       const int64_t b = p / kv.hkv, row = b * kv.hq + static_cast<int64_t>(p - b * kv.hkv) * G;
       for (int i = tid; i < G * D / 4; i += kWarps * 32)
         store_out(a, row * D + 4 * i, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
@@ -486,7 +492,7 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
     // ---- the part: seg_tiles tiles of `pair` from seg0 on ----
     const Part part = s_parts[tm][n_part - listed];
     const int pair = part.pair;
-    const int cnt = pair_count(kv, a, pair);
+    const int cnt = pair_count(a, pair);
     const int pair_tiles = tiles_of(kv, cnt), each = pair_tiles / part.count, more = pair_tiles - each * part.count;
     const int seg0 = part.index * each + min(part.index, more), seg_tiles = each + (part.index < more ? 1 : 0);
     const int ws_row = (part.row + part.index) * G;
