@@ -364,6 +364,15 @@ def test_grouped_codes_of_every_quotient_of_two_bf16_significands():
             assert torch.equal(got_c.view(-1, d)[:n], codes) and torch.equal(got_s.view(-1, 2)[:n], scales)
 
 
+@pytest.mark.parametrize("kind,new", [("fp8_block", [i % 5 for i in range(2500)]), ("bf16", [0] * 2499 + [70]), ("fp8", [1] * 2500),
+                                      ("fp8_block", [1] * 2500), ("f32", [0, 1] * 1250)])
+def test_thousands_of_requests(kind, new):
+    w = World(kind, 64, 16, 2, 1, [i % 37 for i in range(2500)], new, 32, seed=11)
+    w.append()
+    check(w)
+    check_summaries(w)
+
+
 def test_query_in_place():
     w = World("bf16", 128, 16, 4, 2, [20, 0], [30, 3], 128, seed=6)
     w.append()

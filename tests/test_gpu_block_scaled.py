@@ -440,6 +440,29 @@ def test_captured_and_replayed_with_other_lengths_and_on_another_stream():
     assert torch.equal(again, out)
 
 
+@pytest.mark.parametrize("long", [1, 3000])
+def test_thousands_of_requests(long):
+    """More pairs than threads of a CTA, hundreds of them empty, one long or none."""
+    lens = [(3 * i) % 41 for i in range(2500)]
+    lens[1777] = long
+    c = Cache(lens, 1, 64, 16, seed=13)
+    q = query(c, 2)
+    sel, cnt = chosen(c, max(c.nb), None)
+    for counters in (True, False):
+        out, lse = attend(c, q, sel, cnt, counters=counters)
+        check_attention(c, q, sel, cnt, out, lse)
+    from query_aware_sparse_hs_gb300 import hs
+    lo = torch.full((2500, 1, c.mb, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    hi = lo.clone()
+    hs.hs_build_block_summaries(hs.attn_shape(2, 1, 64, 16, "fp8_block"), c.kv, 0, lo, hi)
+    lo, hi = lo.double().cpu().numpy(), hi.double().cpu().numpy()
+    for b, n in enumerate(c.nb):
+        assert (lo[b, 0, n:] == 9).all() and (hi[b, 0, n:] == 9).all()
+        for j in range(n):
+            x = c.rows("k", b, 0, [j]).astype(np.float32)
+            assert np.array_equal(lo[b, 0, j], O.bf16_round_down(x.min(0))) and np.array_equal(hi[b, 0, j], O.bf16_round_up(x.max(0)))
+
+
 def test_two_calls_at_once_with_their_own_workspaces():
     a, b = Cache([5000, 70], 2, 128, 16, seed=9), Cache([20, 9000, 3], 1, 64, 64, seed=10)
     qa, qb = query(a, 16), query(b, 16)
