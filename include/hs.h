@@ -205,7 +205,8 @@ typedef struct hs_select_params {
  * of the head's largest, and absolutely within 2^-33 of that below; a token's
  * probability times its V scale to 22 bits, or absolutely within 2^-38 of the
  * largest V scale of the selection (of 2^-112 at least); everything else in fp32.
- * A bf16 output is the fp32 output rounded.  Pools of 2^32 token rows, and selections of 2^31
+ * K scales up to 2^100 cannot overflow a logit of ordinary size.  A bf16 output is
+ * the fp32 output rounded.  Pools of 2^32 token rows, and selections of 2^31
  * tokens or (over all requests and kv heads) 2^36, are not supported.
  * Calls that may overlap on the GPU (other streams, graphs replayed side by side)
  * need a workspace and split_counters each. */

@@ -660,7 +660,8 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
           qf[nt][4 * k + w][0] = pack_half2(x[k][4 * w] * fs, x[k][4 * w + 1] * fs);
           qf[nt][4 * k + w][1] = pack_half2(x[k][4 * w + 2] * fs, x[k][4 * w + 3] * fs);
         }
-      const float s = fmaxf(fabsf(a.scale) * kLog2e / f, 1e-37f);  // (times -inf is -inf, for a scale of 0 too)
+      // (times -inf is -inf, for a scale of 0 too: 2^-149, and no logit passes 2^127)
+      const float s = fmaxf(fabsf(a.scale) * kLog2e / f, __uint_as_float(1u));
       qs[nt][0] = __shfl_sync(0xffffffffu, s, 8 * c4);
       qs[nt][1] = __shfl_sync(0xffffffffu, s, 8 * c4 + 4);
     }

@@ -272,6 +272,37 @@ def test_queries_at_the_end_of_bf16_are_exact():
         assert want == 3.5 and (lse - want).abs().max() <= 8 * U * want
 
 
+@pytest.mark.parametrize("q0,kscale", [(2.0 ** -118, 2.0 ** 100), (2.0 ** -126, 2.0 ** 100), (2.0 ** -100, 2.0 ** 90), (2.0 ** 110, 2.0 ** -117)])
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 12, -1.0, 0.0])
+def test_logits_of_tiny_queries_and_large_k_scales(q0, kscale, scale):
+    """The factor of the logits is very small where the query is, whatever the K scale makes of it."""
+    c = Cache([2], 1, 64, 16, seed=1, poison=False)
+    page = c.table[0, 0, 0]
+    c.codes["k"][page, :2] = 0
+    c.codes["k"][page, 0, 0], c.codes["k"][page, 1, 0] = 0x7E, 0xFE  # 448, -448
+    c.scales["k"][:] = kscale
+    c.up()
+    sel, cnt = chosen(c, 1, None)
+    q = torch.zeros((1, 8, 64), dtype=torch.float64)
+    q[:, :, 0] = q0
+    q = q.to(torch.bfloat16).cuda()
+    out, lse = attend(c, q, sel, cnt, scale=scale)
+    logit = q0 * 448 * kscale * abs(scale)
+    want = logit + math.log1p(math.exp(-2 * logit))
+    # the factor may lie under fp32's normal numbers: half of 2^-149 times the largest product of codes and scale
+    tiny = 2.0 ** -149 * 448 * 512 * kscale
+    assert (lse - want).abs().max() <= 8 * U * (abs(want) + 1) + 2 * tiny, (lse[0, 0], want)
+
+
+@pytest.mark.parametrize("kscale,f", [((99, 100), -104), ((-117, -116), 110)])
+def test_k_scales_at_the_ends_of_their_range(kscale, f):
+    c = Cache([700, 64, 33], 1, 128, 16, seed=4, kscale=kscale)
+    q = query(c, 8) * 2.0 ** f
+    sel, cnt = chosen(c, max(c.nb), None)
+    out, lse = attend(c, q, sel, cnt, scale=2.0 ** -4)
+    check_attention(c, q, sel, cnt, out, lse, scale=2.0 ** -4)
+
+
 def test_pages_of_zeros_and_large_or_tiny_queries():
     c = Cache([300, 64], 1, 128, 16, seed=4, poison=False)
     for p in c.table[0, 0, 3:9]:  # as the append leaves a page of zeros
