@@ -71,6 +71,13 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t two) {
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
+// Four e4m3 codes (low byte first) to two pairs of f16, exactly.
+__device__ __forceinline__ void e4m3x4_to_halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
 // fp32 score -> unsigned key whose integer order is the float order (-0 and +0
 // are one key); NaN is mapped below every number (key 0).
 __device__ __forceinline__ uint32_t score_key(float s) {

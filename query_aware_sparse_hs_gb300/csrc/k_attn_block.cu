@@ -127,12 +127,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-// four e4m3 codes to two pairs of f16, exactly
-__device__ __forceinline__ void halves_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
 __device__ __forceinline__ float exp2_fast(float x) {  // 2 ulp; results under 2^-126 are 0
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -721,8 +715,8 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
 #pragma unroll
           for (int st = 0; st < 2; ++st) {
             uint32_t a0, a1, a2, a3;
-            halves_of(wa[st][w], a0, a2);
-            halves_of(wb[st][w], a1, a3);
+            e4m3x4_to_halves(wa[st][w], a0, a2);
+            e4m3x4_to_halves(wb[st][w], a1, a3);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma(s[st][nt], a0, a1, a2, a3, qf[nt][4 * k + w][0], qf[nt][4 * k + w][1]);
           }
@@ -830,8 +824,8 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
           const uint32_t pick = (i & 1) ? 0x7362u : 0x5140u;  // (byte of token 2k, byte of token 2k + 1) twice
           const uint32_t y0 = __byte_perm(x[0][i >> 1], x[1][i >> 1], pick), y1 = __byte_perm(x[2][i >> 1], x[3][i >> 1], pick);
           uint32_t a0, a1, a2, a3;
-          halves_of(y0, a0, a1);
-          halves_of(y1, a2, a3);
+          e4m3x4_to_halves(y0, a0, a1);
+          e4m3x4_to_halves(y1, a2, a3);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma(o[nt][i], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);

@@ -201,9 +201,7 @@ cudaError_t launch_k(const KvView& kv, int first_block, int nblocks, void* smin,
 // channels, 770 MB: 128 us, 0.90 of the copy rate (the common kernel above: 400).
 __device__ __forceinline__ void codes_to_half2(uint32_t w, __half2& a, __half2& b) {
   uint32_t x, y;
-  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
-      : "=r"(x), "=r"(y)
-      : "r"(w));
+  e4m3x4_to_halves(w, x, y);
   a = *reinterpret_cast<__half2*>(&x);
   b = *reinterpret_cast<__half2*>(&y);
 }
