@@ -35,11 +35,11 @@
 //
 // What bounds it: memory, for long work (16 requests x 4 heads x 131072 tokens, 2.15
 // GB: 315 to 327 us from one GPU to another, 0.98 to 1.02 of the copy rate; 64
-// channels 0.80).  Before it streams, a part
-// waits for a chain of lookups (counts, selection, pages, rows: 4 us), after it
-// for the join of its warps and, where pairs are cut, the merge (2 and 2 us): 32
-// requests x 4096 selected tokens, 134 MB, no pair cut: 28.8 us, 0.70.  (Asking the L2
-// ahead for selections and pages did not shorten the chain.)  With 16 query heads
+// channels 0.80).  Before it streams, a part waits for a chain of lookups (counts,
+// selection, pages, rows: 4 us), after it for the join of its warps and, where pairs
+// are cut, the merge (2 and 2 us): 32 requests x 4096 selected tokens, 134 MB, no pair
+// cut: 28.8 us, 0.70.  (Asking the L2 ahead for selections and pages did not shorten
+// the chain.)  With 16 query heads
 // and 64 channels (12 requests x 2 heads, 75 MB: 31.0 us, 0.36) a 32-token tile takes an
 // SM about 260 cycles whatever the number of warps, and about half of the call is
 // start, join and merge of parts of ten tiles a warp.  (Codes converted by shifts on
@@ -54,12 +54,11 @@
 // most: a head whose largest entry is under 2^-118 is exact, as bf16 ends at 2^-133.
 // P * vscale, in units of 2^-14 times the largest V scale met so far (a power of two,
 // 2^-112 or more), enters as two f16 terms: 22 bits, and absolutely within 2^-25 of
-// the units where it is under an eighth of them.  One
-// term, for bf16 outputs, would save 2 to 3% with up to 8 heads (nothing where memory
-// binds), 8% with 16 heads of 64 channels and 20% of 128 (37.8 us for 47.0), and moves
-// bf16 outputs by 6 10^-4 of their norm.  Sums, maxima and
-// partial outputs are fp32; sums stay in those units until they are divided, so
-// that V may be as large as its outputs can be.
+// the units where it is under an eighth of them.  One term, for bf16 outputs, would
+// save 2 to 3% with up to 8 heads (nothing where memory binds), 8% with 16 heads of 64
+// channels and 20% of 128 (37.8 us for 47.0), and moves bf16 outputs by 6 10^-4 of
+// their norm.  Sums, maxima and partial outputs are fp32; sums stay in those units
+// until they are divided, so that V may be as large as its outputs can be.
 #include <limits.h>
 
 #include <atomic>
