@@ -1,12 +1,13 @@
 /*
  * hs.h - C ABI of a GB300 (sm_103a) library for one decode step of query-aware
  * block-sparse attention over a paged KV cache, with a HiSparse-style hot
- * device buffer, and for filling that cache (prompts and tokens, rotated by
- * position on the way).
+ * device buffer, for filling that cache (prompts and tokens, rotated by
+ * position on the way), and for cutting it down to the tokens that attention
+ * looks at.
  *
  * The operations follow these pages:
  *   [KVS] "KV 稀疏化" (KV-cache sparsity wiki): §2 attention sink + sliding
- *         window, §5 Quest (per-block min/max summary, coarse filter of the
+ *         window, heavy hitters by accumulated attention, §5 Quest (per-block min/max summary, coarse filter of the
  *         query against the summaries, top-k blocks, full attention on the
  *         chosen blocks only), §7 HiSparse (hot device buffer, host inactive KV,
  *         swap-in kernel that detects misses, updates the page table and brings
@@ -36,10 +37,13 @@
  *   B = block_size tokens per block (= per page), D = head_dim,
  *   Hq / Hkv query / kv heads, g = Hq / Hkv query heads per kv head,
  *   N_b = ceil(seq_lens[b] / B) blocks of request b.
- *   k_pages, v_pages  [num_pages][B][D]   f32 | bf16 | e4m3 (one byte)
+ *   k_pages, v_pages  [num_pages][B][D]   f32 | bf16 | e4m3 (one byte); 4-bit:
+ *                     [num_pages][B][D/2] bytes, channel 2i in the low half
  *   k_scales,v_scales [num_pages][B][D/32] f32 (e4m3 with grouped scales),
  *                     [num_pages] f32 (e4m3 with a scale per page: positive,
- *                     finite numbers), else NULL
+ *                     finite numbers), [num_pages][B][2][D/32] bf16 (4-bit: a
+ *                     row's scales, then its centres; 16-byte aligned, passed
+ *                     as float pointers), else NULL
  *   page_table        [batch][Hkv][max_blocks] int32: physical page of block j
  *                     of (b, kvh); only entries j < N_b are read.
  *   seq_lens          [batch] int32 tokens of each request, including the
@@ -95,10 +99,16 @@ typedef enum hs_kv_dtype {
   HS_KV_BF16 = 1,        /* bf16 K/V, bf16 q, bf16 summaries */
   HS_KV_FP8E4M3_G32 = 2,  /* e4m3 K/V + one fp32 scale per 32 channels per token;
                              bf16 q; bf16 summaries rounded outward */
-  HS_KV_FP8E4M3_BLOCK = 3 /* e4m3 K/V + one fp32 scale per page (a block of
+  HS_KV_FP8E4M3_BLOCK = 3, /* e4m3 K/V + one fp32 scale per page (a block of
                              tokens of one kv head): k_scales, v_scales
                              [num_pages]; bf16 q; bf16 summaries rounded
                              outward.  1/9 fewer bytes than G32 */
+  HS_KV_INT4_G32 = 4       /* 4-bit codes c of -8 .. 7, stored as c + 8, and for
+                             every token and 32 channels a bf16 scale s and a
+                             bf16 centre z: a value is z + s c in fp32 ([FLL]
+                             §2.4, a scale and a zero point per group); bf16 q;
+                             bf16 summaries rounded outward.  5/16 of the bytes
+                             of bf16 */
 } hs_kv_dtype;
 
 /* Attention geometry.  head_dim in {64, 128}; num_q_heads / num_kv_heads in
@@ -116,8 +126,8 @@ typedef struct hs_attn_shape {
 typedef struct hs_paged_kv {
   const void* k_pages;
   const void* v_pages;
-  const float* k_scales; /* e4m3 only */
-  const float* v_scales; /* e4m3 only */
+  const float* k_scales; /* e4m3 and 4-bit only */
+  const float* v_scales; /* e4m3 and 4-bit only */
   const int32_t* page_table;
   const int32_t* seq_lens;
   int32_t batch;
@@ -209,7 +219,8 @@ typedef struct hs_select_params {
  * the fp32 output rounded.  Pools of 2^32 token rows, and selections of 2^31
  * tokens or (over all requests and kv heads) 2^36, are not supported.
  * Calls that may overlap on the GPU (other streams, graphs replayed side by side)
- * need a workspace and split_counters each. */
+ * need a workspace and split_counters each.
+ * A 4-bit cache (HS_KV_INT4_G32) runs on the CUDA-core kernel. */
 #define HS_ATTN_EARLY_SUMMARIES 1u
 #define HS_ATTN_RANGES 2u
 #define HS_ATTN_NO_RANGES 4u
@@ -236,7 +247,8 @@ typedef struct hs_attn_params {
  *   host_k, host_v        pinned, mapped host memory [batch][Hkv][max_blocks][B][D]
  *   host_k_scales, host_v_scales  pinned host [..][B][D/32] (e4m3 only)
  * Start state: page_table, slot_owner and last_used all -1.
- * Not for HS_KV_FP8E4M3_BLOCK: the swap-in calls answer HS_ERR_UNSUPPORTED. */
+ * Not for HS_KV_FP8E4M3_BLOCK and HS_KV_INT4_G32: the swap-in calls answer
+ * HS_ERR_UNSUPPORTED. */
 typedef struct hs_hot_buffer {
   int32_t* page_table;
   int32_t* slot_owner;
@@ -285,8 +297,8 @@ HS_API int32_t hs_attn_geometry(const hs_attn_shape* shape, int32_t batch, int32
  * block j with first_block <= j < N_b, smin/smax[b][kvh][j][d] = min/max over
  * the block's valid tokens t in [jB, min((j+1)B, L_b)) of K[t][d].  e4m3 K is
  * dequantised first (code * scale in fp32; with a scale per page the min and max
- * are taken over the codes and then scaled, which is the same) and the results
- * rounded outward to bf16 (min toward -inf, max toward +inf).  Other entries are
+ * are taken over the codes and then scaled, which is the same), 4-bit K likewise
+ * (z + s c in fp32), and the results rounded outward to bf16 (min toward -inf, max toward +inf).  Other entries are
  * not written.
  * Reading a page id outside [0, num_pages) sets HS_EBIT_PAGE_RANGE and skips
  * that block. */
@@ -306,8 +318,8 @@ HS_API hs_status hs_build_block_summaries(const hs_attn_shape* shape, const hs_p
  *   new_k, new_v  [batch][Hkv][D]  f32 for f32 K/V, bf16 otherwise; an e4m3
  *                 cache with grouped scales stores them quantised as
  *                 hs_quantize_e4m3_g32 does (codes into k_pages/v_pages, scales
- *                 into k_scales/v_scales), one with a scale per page as
- *                 hs_append_tokens does.
+ *                 into k_scales/v_scales), a 4-bit cache as hs_quantize_int4_g32
+ *                 does, one with a scale per page as hs_append_tokens does.
  *   The call WRITES through kv->k_pages, v_pages, k_scales and v_scales: they
  *   must point to writable device memory.
  * A block index >= max_blocks sets HS_EBIT_BLOCK_RANGE, a page id outside
@@ -344,7 +356,8 @@ typedef struct hs_append_params {
  * angle at the row's position, a' = a cos t - b sin t, b' = b cos t + a sin t in
  * fp32: for K before it is stored, for Q into q_out; V is stored as it is.
  * Stored as the cache holds it: f32; bf16, rounded once; e4m3 with grouped
- * scales as hs_quantize_e4m3_g32 does; e4m3 with a scale per page (below).  The
+ * scales as hs_quantize_e4m3_g32 does; 4-bit as hs_quantize_int4_g32 does; e4m3
+ * with a scale per page (below).  The
  * summaries of the touched blocks ([KVS] §5) are widened to the new tokens
  * (started afresh where the block's row 0 is new), so that they equal what
  * hs_build_block_summaries computes, as with hs_append_token.
@@ -586,6 +599,81 @@ HS_API hs_status hs_merge_attn_partials(const hs_attn_shape* shape, int32_t batc
 HS_API hs_status hs_quantize_e4m3_g32(const void* src, int32_t src_is_fp32, int64_t rows,
                                int32_t head_dim, uint8_t* codes, float* scales,
                                hs_stream_t stream);
+
+/* The 4-bit format of K or V rows ([FLL] §2.4, a scale and a zero point per
+ * group; §3.2, groups of 32): for each row and each 32-channel group with values
+ * between lo and hi,
+ *   z = bf16((7 lo + 8 hi) / 15),  s = max((hi - z) / 7, (z - lo) / 8) rounded up to
+ *   bf16,  c = (x - z) / s rounded to nearest (even), within -8 .. 7,
+ * in fp32, so that z + s c is within s / 2 of x (and fp32's rounding).  Values beyond
+ * +-2^126, infinities among them, are held as +-2^126; a group with a NaN gets a NaN
+ * scale and reads as NaN; a group whose s would be under 2^-116 gets s = 0 and reads
+ * as z.
+ *   src      [rows][head_dim] f32 (src_is_fp32) or bf16, 16-byte aligned
+ *   codes    [rows][head_dim / 2] bytes, c + 8, channel 2i in the low half of byte i
+ *   scales   [rows][2][head_dim / 32] bf16: the s's, then the z's
+ * codes and scales 4-byte aligned at least.  head_dim: 64, 128 or 256. */
+HS_API hs_status hs_quantize_int4_g32(const void* src, int32_t src_is_fp32, int64_t rows, int32_t head_dim,
+                                      uint8_t* codes, void* scales, hs_stream_t stream);
+
+/* The values of 4-bit rows: dst [rows][head_dim], z + s c in fp32, f32
+ * (dst_is_fp32) or rounded to bf16, 16-byte aligned. */
+HS_API hs_status hs_dequantize_int4_g32(const uint8_t* codes, const void* scales, int64_t rows, int32_t head_dim,
+                                        void* dst, int32_t dst_is_fp32, hs_stream_t stream);
+
+/* Attention weights accumulated per token, for the eviction below ([KVS] §2, heavy
+ * hitters): for every (b, kvh) and every valid token t of the blocks in
+ * sel[b][kvh][0 .. sel_count),
+ *   weights[b][kvh][t] += sum over the group's heads h of
+ *                         e^(scale (q[b][h] . K[t]) - lse[b][h])
+ * with lse as the attention over the same selection left it, so that each head adds 1
+ * in all; a head whose lse is -inf adds nothing.  Every kind of cache; reads K only
+ * (kv->v_pages and v_scales may be NULL).
+ *   lse      [batch][Hq] f32;  weights [batch][Hkv][max_blocks * B] f32, the token's
+ *            place in its request last; read and written, start it at 0.
+ * Sums are fp32.  A block selected twice is added twice.  Entries of tokens that are
+ * not selected stay as they are.  Selections larger than capacity, blocks outside the
+ * request and pages outside the pool are reported and skipped as in the attention. */
+HS_API hs_status hs_accumulate_attn_weights(const hs_attn_shape* shape, const hs_paged_kv* kv, const void* q,
+                                            const float* lse, const int32_t* sel, const int32_t* sel_count,
+                                            int32_t capacity, float scale, float* weights, hs_stream_t stream);
+
+/* Which tokens hs_evict_tokens keeps of each (request, kv head): at most `budget`
+ * (at least 1), the first sink_tokens and the last recent_tokens among them
+ * (sink_tokens + recent_tokens <= budget). */
+typedef struct hs_evict_params {
+  int32_t budget;
+  int32_t sink_tokens;
+  int32_t recent_tokens;
+} hs_evict_params;
+
+/* Eviction by accumulated attention weight ([KVS] §2, H2O: the heavy hitters and the
+ * recent tokens stay): of every (b, kvh) with more than budget tokens the sink, the
+ * recent tokens and the heaviest of the others stay (equal weights: the lower token;
+ * NaN weights last), of one with fewer all of them.  Their rows (K, V and scales, bit
+ * for bit) are gathered, in order, into the first places of request b in another cache:
+ *   dst          the cache that is written: its page table has pages for
+ *                ceil(min(seq_lens[b], budget) / B) blocks of each (b, kvh), budget <=
+ *                dst->max_blocks * B, dst->batch = kv->batch.  dst->seq_lens is WRITTEN:
+ *                min(seq_lens[b], budget); it may be kv->seq_lens itself.  The pools may
+ *                be the same one, but no page that is written may be one that a request
+ *                of kv uses, or be used twice.  (A copy and not a move in place: pages
+ *                of kv may be shared between requests, and stay as they were.)
+ *   weights      [batch][Hkv][kv->max_blocks * B] f32
+ *   dst_weights  nullable [batch][Hkv][dst->max_blocks * B] f32: the kept tokens'
+ *                weights in their new places; not weights itself
+ *   kept         [batch][Hkv][budget] int32: the kept tokens' old places, ascending,
+ *                -1 behind them
+ * Rows, weights and table entries of dst behind the new length stay as they were.  The
+ * summaries of dst are hs_build_block_summaries'; K keeps the positions it was rotated
+ * by, so new tokens go on with theirs (hs_append_params.positions).  A request longer
+ * than max_blocks * B sets HS_EBIT_BLOCK_RANGE and counts as that long; a page id
+ * outside its pool sets HS_EBIT_PAGE_RANGE and that token's row is not written.
+ * Not for HS_KV_FP8E4M3_BLOCK (rows of one page share their scale):
+ * HS_ERR_UNSUPPORTED. */
+HS_API hs_status hs_evict_tokens(const hs_attn_shape* shape, const hs_paged_kv* kv, const hs_paged_kv* dst,
+                                 const hs_evict_params* params, const float* weights, float* dst_weights,
+                                 int32_t* kept, hs_stream_t stream);
 
 /* Same computation, arguments and results as hs_sparse_paged_decode_attn, for
  * callers that cannot allocate device memory.  (The pages have no counterpart

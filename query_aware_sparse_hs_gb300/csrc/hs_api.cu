@@ -52,7 +52,7 @@ hs_status check_shape(const hs_attn_shape* s) {
   if (g != 1 && g != 2 && g != 4 && g != 8 && g != 16) return HS_ERR_UNSUPPORTED;
   if (s->head_dim != 64 && s->head_dim != 128) return HS_ERR_UNSUPPORTED;
   if (s->block_size < 1 || s->block_size > 256) return HS_ERR_UNSUPPORTED;
-  if (s->kv_dtype < HS_KV_F32 || s->kv_dtype > HS_KV_FP8E4M3_BLOCK) return HS_ERR_INVALID_ARG;
+  if (s->kv_dtype < HS_KV_F32 || s->kv_dtype > HS_KV_INT4_G32) return HS_ERR_INVALID_ARG;
   return HS_OK;
 }
 
@@ -63,6 +63,8 @@ hs_status check_kv(const hs_attn_shape* s, const hs_paged_kv* kv, bool need_v) {
   if (need_v && !kv->v_pages) return HS_ERR_INVALID_ARG;
   if (s->kv_dtype >= HS_KV_FP8E4M3_G32 &&
       (!kv->k_scales || !aligned(kv->k_scales, 4) || (need_v && (!kv->v_scales || !aligned(kv->v_scales, 4)))))
+    return HS_ERR_INVALID_ARG;
+  if (s->kv_dtype == HS_KV_INT4_G32 && (!aligned(kv->k_scales, 16) || (need_v && !aligned(kv->v_scales, 16))))
     return HS_ERR_INVALID_ARG;
   if (kv->batch < 0 || kv->max_blocks < 1 || kv->num_pages < 0 || kv->num_pages > INT32_MAX)
     return HS_ERR_INVALID_ARG;
@@ -647,7 +649,8 @@ static hs_status hot_view(const hs_attn_shape* shape, const hs_hot_buffer* hb, H
   if (!hb->page_table || !hb->slot_owner || !hb->last_used || !hb->k_slots || !hb->v_slots ||
       !hb->host_k || !hb->host_v)
     return HS_ERR_INVALID_ARG;
-  if (shape->kv_dtype == HS_KV_FP8E4M3_BLOCK) return HS_ERR_UNSUPPORTED;  // no copy of a page's scale
+  if (shape->kv_dtype == HS_KV_FP8E4M3_BLOCK || shape->kv_dtype == HS_KV_INT4_G32)
+    return HS_ERR_UNSUPPORTED;  // no copy of their scales
   const bool fp8 = shape->kv_dtype == HS_KV_FP8E4M3_G32;
   if (fp8 && (!hb->k_slot_scales || !hb->v_slot_scales || !hb->host_k_scales || !hb->host_v_scales))
     return HS_ERR_INVALID_ARG;
@@ -812,6 +815,69 @@ hs_status hs_quantize_e4m3_g32(const void* src, int32_t src_is_fp32, int64_t row
   if (st != HS_OK) return st;
   return from_cuda(launch_quantize(src, src_is_fp32 != 0, rows, head_dim, codes, scales,
                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+static hs_status check_int4_rows(const void* values, int64_t rows, int32_t head_dim, const uint8_t* codes, const void* scales) {
+  if (rows < 0 || (rows > 0 && (!values || !codes || !scales))) return HS_ERR_INVALID_ARG;
+  if (!aligned(values, 16) || !aligned(codes, 4) || !aligned(scales, 4)) return HS_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return HS_ERR_UNSUPPORTED;
+  if (rows / 8 >= INT32_MAX) return HS_ERR_UNSUPPORTED;
+  return HS_OK;
+}
+
+hs_status hs_quantize_int4_g32(const void* src, int32_t src_is_fp32, int64_t rows, int32_t head_dim, uint8_t* codes,
+                               void* scales, hs_stream_t stream) {
+  hs_status st = check_int4_rows(src, rows, head_dim, codes, scales);
+  if (st != HS_OK) return st;
+  return from_cuda(launch_quantize_int4(src, src_is_fp32 != 0, rows, head_dim, codes, scales,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+hs_status hs_dequantize_int4_g32(const uint8_t* codes, const void* scales, int64_t rows, int32_t head_dim, void* dst,
+                                 int32_t dst_is_fp32, hs_stream_t stream) {
+  hs_status st = check_int4_rows(dst, rows, head_dim, codes, scales);
+  if (st != HS_OK) return st;
+  return from_cuda(launch_dequantize_int4(codes, scales, rows, head_dim, dst, dst_is_fp32 != 0,
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+hs_status hs_accumulate_attn_weights(const hs_attn_shape* shape, const hs_paged_kv* kv, const void* q, const float* lse,
+                                     const int32_t* sel, const int32_t* sel_count, int32_t capacity, float scale,
+                                     float* weights, hs_stream_t stream) {
+  hs_status st = check_shape(shape);
+  if (st != HS_OK) return st;
+  if ((st = check_kv(shape, kv, false)) != HS_OK) return st;
+  if (!q || !lse || !sel || !sel_count || !weights || capacity < 1) return HS_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(lse, 4) || !aligned(sel, 4) || !aligned(sel_count, 4) || !aligned(weights, 4))
+    return HS_ERR_INVALID_ARG;
+  const WeightsArgs a{q, lse, sel, sel_count, capacity, scale, weights};
+  const KvView v = make_view(shape, kv);
+  if (!weights_fits(v, a)) return HS_ERR_UNSUPPORTED;
+  Device d;
+  if ((st = current_device(&d)) != HS_OK) return st;
+  return from_cuda(launch_weights(v, a, d.sms, d.err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+hs_status hs_evict_tokens(const hs_attn_shape* shape, const hs_paged_kv* kv, const hs_paged_kv* dst,
+                          const hs_evict_params* params, const float* weights, float* dst_weights, int32_t* kept,
+                          hs_stream_t stream) {
+  hs_status st = check_shape(shape);
+  if (st != HS_OK) return st;
+  if ((st = check_kv(shape, kv, true)) != HS_OK) return st;
+  if ((st = check_kv(shape, dst, true)) != HS_OK) return st;
+  if (!params || !weights || !kept || dst->batch != kv->batch) return HS_ERR_INVALID_ARG;
+  if (!aligned(weights, 4) || !aligned(dst_weights, 4) || !aligned(kept, 4) || weights == dst_weights) return HS_ERR_INVALID_ARG;
+  if (params->budget < 1 || params->sink_tokens < 0 || params->recent_tokens < 0 ||
+      static_cast<int64_t>(params->sink_tokens) + params->recent_tokens > params->budget)
+    return HS_ERR_INVALID_ARG;
+  if (params->budget > static_cast<int64_t>(dst->max_blocks) * shape->block_size) return HS_ERR_INVALID_ARG;
+  if (shape->kv_dtype == HS_KV_FP8E4M3_BLOCK) return HS_ERR_UNSUPPORTED;
+  const EvictArgs a{weights, dst_weights, kept, params->budget, params->sink_tokens, params->recent_tokens};
+  const KvView v = make_view(shape, kv), to = make_view(shape, dst);
+  if (evict_ctas(v, params->budget) > INT32_MAX) return HS_ERR_UNSUPPORTED;
+  Device d;
+  if ((st = current_device(&d)) != HS_OK) return st;
+  return from_cuda(launch_evict(v, to, a, d.err, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 hs_status hs_get_device_error(hs_stream_t stream, uint32_t* bits_opt) {

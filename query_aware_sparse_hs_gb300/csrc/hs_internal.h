@@ -148,6 +148,32 @@ struct MissAttnArgs {
 cudaError_t launch_swapin_copy(const HotView& hb, const int32_t* miss_sel, const int32_t* miss_count,
                                int capacity, int ctas, const MissAttnArgs* attn, hs_swap_stats* stats, unsigned* err,
                                cudaStream_t st);
+// Weights of the step's attention added up per token.
+struct WeightsArgs {
+  const void* q;
+  const float* lse;
+  const int32_t* sel;
+  const int32_t* sel_count;
+  int32_t capacity;
+  float scale;
+  float* weights;  // [batch][Hkv][max_blocks][B]
+};
+bool weights_fits(const KvView& kv, const WeightsArgs& a);
+cudaError_t launch_weights(const KvView& kv, const WeightsArgs& a, int sms, unsigned* err, cudaStream_t st);
+// The heaviest tokens of every (request, kv head) gathered into dst's pages.
+struct EvictArgs {
+  const float* weights;  // [batch][Hkv][max_blocks][B]
+  float* dst_weights;    // nullable, with dst's max_blocks
+  int32_t* kept;         // [batch][Hkv][budget]
+  int32_t budget, sink, recent;
+};
+int64_t evict_ctas(const KvView& kv, int budget);  // of its largest launch
+cudaError_t launch_evict(const KvView& kv, const KvView& dst, const EvictArgs& a, unsigned* err, cudaStream_t st);
+// The 4-bit format of rows and back; scales [rows][2][head_dim / 32] bf16.
+cudaError_t launch_quantize_int4(const void* src, bool src_f32, int64_t rows, int head_dim, uint8_t* codes, void* scales,
+                                 cudaStream_t st);
+cudaError_t launch_dequantize_int4(const uint8_t* codes, const void* scales, int64_t rows, int head_dim, void* dst, bool dst_f32,
+                                   cudaStream_t st);
 cudaError_t launch_quantize(const void* src, bool src_f32, int64_t rows, int head_dim,
                             uint8_t* codes, float* scales, cudaStream_t st);
 

@@ -1,0 +1,104 @@
+// The 4-bit cache format: for every row and 32 channels a bf16 scale s, a bf16
+// centre z and codes c of -8 .. 7, stored as c + 8, channel 2i in the low half of
+// byte i.  A value is z + s c, in fp32.
+//
+// Of a group's values between lo and hi: z = (7 lo + 8 hi) / 15 rounded to bf16, so
+// that c = -8 is lo and c = 7 is hi; s = max((hi - z) / 7, (z - lo) / 8) rounded up
+// to bf16, so that every value has a code within s / 2 although z was rounded.  (A
+// centre instead of a minimum: the codes' products are sums of both signs, which
+// stay as small as the attention's result over long contexts, where sums of codes
+// 0 .. 15 would have to cancel against the minimum's.)  bf16 for both: a centre of
+// bf16 values of any size, and a group of equal values is held exactly.
+#pragma once
+
+#include "hs_common.cuh"
+
+namespace hs {
+namespace int4 {
+
+constexpr float kMost = 8.507059173023462e37f;        // 2^126: values beyond it are held as it
+constexpr float kLeastScale = 1.2037062152420224e-35f;  // 2^-116: smaller ranges are held as their centre
+constexpr float kRound = 12582920.0f;                 // 1.5 2^23 + 8: adding it leaves round(c) + 8 in the low bits
+
+__host__ __device__ constexpr int row_bytes(int head_dim) { return head_dim / 2; }
+// scales and centres of a row, in 16-bit words
+__host__ __device__ constexpr int record(int head_dim) { return 2 * (head_dim / kQuantGroup); }
+
+// Least and largest of a group's values, and whether one is not a number (held as
+// an infinite hi, which no other value leaves).
+struct Range {
+  float lo, hi;
+  __device__ __forceinline__ void clear() {
+    lo = INFINITY;
+    hi = -INFINITY;
+  }
+  __device__ __forceinline__ void add(float x) {
+    const float y = fminf(fmaxf(x, -kMost), kMost);  // NaN: -2^126, but then the group's scale is NaN
+    lo = fminf(lo, y);
+    hi = fmaxf(hi, x == x ? y : INFINITY);
+  }
+  __device__ __forceinline__ void join(const Range& o) {
+    lo = fminf(lo, o.lo);
+    hi = fmaxf(hi, o.hi);
+  }
+  __device__ __forceinline__ void join_lane(int mask) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, mask));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, mask));
+  }
+};
+
+struct Scale {
+  float s, z, inv;  // inv: 1 / s, 0 for a scale of 0
+};
+__device__ __forceinline__ Scale scale_of(const Range& r) {
+  Scale q;
+  const bool nan = r.hi == INFINITY;
+  const float lo = nan ? 0.0f : r.lo, hi = nan ? 0.0f : r.hi;
+  // (one rounding of the sum, so that a centre next to zero keeps its precision)
+  q.z = __bfloat162float(__float2bfloat16_rn(fmaf(lo, 7.0f / 16.0f, hi * 0.5f) * (16.0f / 15.0f)));
+  q.s = __bfloat162float(__float2bfloat16_ru(fmaxf((hi - q.z) / 7.0f, (q.z - lo) / 8.0f)));
+  if (!(q.s >= kLeastScale)) q.s = 0.0f;
+  q.inv = q.s > 0.0f ? 1.0f / q.s : 0.0f;
+  if (nan) q.s = __uint_as_float(0x7fc00000u);  // every value of the group reads as NaN
+  return q;
+}
+__device__ __forceinline__ uint16_t bf16_bits(float exact) { return static_cast<uint16_t>(__float_as_uint(exact) >> 16); }
+
+// Codes of 8 neighbouring channels.  The quotient is corrected by its remainder
+// (Markstein, IBM J. Res. Dev. 34, 1990), so that it rounds as the division does: bf16
+// values lie halfway between two codes often enough (times 1 / s alone, 2 of 1000 codes
+// of random bf16 values differed from the definition's).
+__device__ __forceinline__ uint32_t encode8(const float (&x)[8], const Scale& q) {
+  uint32_t w = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float t = fminf(fmaxf(x[i], -kMost), kMost) - q.z, a = t * q.inv;
+    const float c = fminf(fmaxf(fmaf(fmaf(-a, q.s, t), q.inv, a), -8.0f), 7.0f);
+    w |= (__float_as_uint(c + kRound) & 15u) << (4 * i);
+  }
+  return w;
+}
+// The codes of 8 neighbouring channels as numbers, exactly.
+__device__ __forceinline__ void codes8(uint32_t w, float (&c)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = __uint_as_float(((w >> (4 * i)) & 15u) | 0x4b000000u) - 8388616.0f;  // 2^23 + 8
+}
+__device__ __forceinline__ void decode8(uint32_t w, float s, float z, float (&x)[8]) {
+  codes8(w, x);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = fmaf(s, x[i], z);
+}
+
+// Scale and centre of group g of a row.
+__device__ __forceinline__ float2 load_scale(const void* scales, int64_t row, int head_dim, int g) {
+  const unsigned short* p = reinterpret_cast<const unsigned short*>(scales) + row * record(head_dim);
+  return make_float2(bf16_bits_to_float(__ldg(p + g)), bf16_bits_to_float(__ldg(p + head_dim / kQuantGroup + g)));
+}
+__device__ __forceinline__ void store_scale(void* scales, int64_t row, int head_dim, int g, const Scale& q) {
+  uint16_t* p = static_cast<uint16_t*>(scales) + row * record(head_dim);
+  p[g] = bf16_bits(q.s);
+  p[head_dim / kQuantGroup + g] = bf16_bits(q.z);
+}
+
+}  // namespace int4
+}  // namespace hs

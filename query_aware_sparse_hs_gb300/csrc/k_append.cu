@@ -147,7 +147,8 @@ cudaError_t launch_c(const KvView& kv, const void* new_k, const void* new_v, voi
 cudaError_t launch_append(const KvView& kv, const void* new_k, const void* new_v, void* smin, void* smax,
                           unsigned* err, cudaStream_t st) {
   if (kv.batch == 0) return cudaSuccess;
-  if (kv.kv_dtype == HS_KV_FP8E4M3_BLOCK) {  // the scale of a page concerns all its rows
+  // (the scale of a page concerns all its rows; 4-bit rows are stored there only)
+  if (kv.kv_dtype == HS_KV_FP8E4M3_BLOCK || kv.kv_dtype == HS_KV_INT4_G32) {
     AppendTokensArgs a{};
     a.k = new_k;
     a.v = new_v;

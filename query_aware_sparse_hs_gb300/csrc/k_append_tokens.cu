@@ -39,6 +39,7 @@
 #include <float.h>
 
 #include "hs_internal.h"
+#include "int4.cuh"
 
 namespace hs {
 namespace {
@@ -372,6 +373,76 @@ __device__ __forceinline__ void store_grouped(void* pages, float* scales, int64_
   decode8(cw, sb, w);
 }
 
+// fp32 -> unsigned whose order is the float order, and back (no NaN).
+__device__ __forceinline__ unsigned ordered(float x) {
+  const unsigned u = __float_as_uint(x);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(unsigned k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
+
+// The 4-bit format: every 32-channel group its own scale and centre.  Called as
+// store_grouped is; `part` are 2 D / 32 words.
+template <int D, bool INTERLEAVED>
+__device__ __forceinline__ void store_int4(void* pages, float* scales, int64_t row, int s, const Slot& t, int rotary, bool live,
+                                           unsigned* part, float (&u)[8], float (&w)[8]) {
+  constexpr int kGroups = D / kQuantGroup;
+  int4::Range ra, rb;  // of the vectors' groups
+  ra.clear();
+  rb.clear();
+  if (live) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      ra.add(u[c]);
+      rb.add(w[c]);
+    }
+  }
+  const bool split = !INTERLEAVED && t.rotated;
+  const bool neighbours = INTERLEAVED || rotary % 64 == 0;
+  if (neighbours) {  // a group is two threads' vectors, or (split) one vector of four threads
+    if (!split) {
+      ra.join(rb);
+      rb = ra;
+    }
+    ra.join_lane(1);
+    rb.join_lane(1);
+    if constexpr (!INTERLEAVED) {
+      int4::Range a2 = ra, b2 = rb;
+      a2.join_lane(2);
+      b2.join_lane(2);
+      if (split) {
+        ra = a2;
+        rb = b2;
+      }
+    }
+  } else {
+    for (int i = s; i < 2 * kGroups; i += D / 16) part[i] = 0u;
+    __syncwarp();
+    if (live) {  // maxima: the order does not matter
+      atomicMax(&part[t.ca / kQuantGroup], ordered(ra.hi));
+      atomicMax(&part[kGroups + t.ca / kQuantGroup], ordered(-ra.lo));
+      atomicMax(&part[t.cb / kQuantGroup], ordered(rb.hi));
+      atomicMax(&part[kGroups + t.cb / kQuantGroup], ordered(-rb.lo));
+    }
+    __syncwarp();
+    ra.hi = unordered(part[t.ca / kQuantGroup]);
+    ra.lo = -unordered(part[kGroups + t.ca / kQuantGroup]);
+    rb.hi = unordered(part[t.cb / kQuantGroup]);
+    rb.lo = -unordered(part[kGroups + t.cb / kQuantGroup]);
+    __syncwarp();
+  }
+  if (!live) return;
+  const int4::Scale qa = int4::scale_of(ra), qb = int4::scale_of(rb);
+  uint8_t* dst = static_cast<uint8_t*>(pages) + row * int4::row_bytes(D);
+  const uint32_t cu = int4::encode8(u, qa), cw = int4::encode8(w, qb);
+  *reinterpret_cast<uint32_t*>(dst + t.ca / 2) = cu;
+  *reinterpret_cast<uint32_t*>(dst + t.cb / 2) = cw;
+  // the thread with a group's first channel has its scale
+  if (t.ca % kQuantGroup == 0) int4::store_scale(scales, row, D, t.ca / kQuantGroup, qa);
+  if (t.cb % kQuantGroup == 0) int4::store_scale(scales, row, D, t.cb / kQuantGroup, qb);
+  int4::decode8(cu, qa.s, qa.z, u);
+  int4::decode8(cw, qb.s, qb.z, w);
+}
+
 // Stores a row of an f32 or bf16 cache and leaves in u, w what it holds.
 template <int D, int KIND>
 __device__ __forceinline__ void store_plain(void* pages, int64_t row, const Slot& t, float (&u)[8], float (&w)[8]) {
@@ -446,7 +517,7 @@ __global__ __launch_bounds__(kThreads, threads_per_sm(KIND, P) / kThreads) void 
   __shared__ float s_mn[kWarps][D], s_mx[kWarps][D];
   __shared__ float s_amax[kWarps];
   __shared__ int s_any[kWarps];
-  __shared__ unsigned s_group[kWarps * 32 / TPR][D / kQuantGroup];
+  __shared__ unsigned s_group[kWarps * 32 / TPR][2 * (D / kQuantGroup)];
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -572,6 +643,8 @@ __global__ __launch_bounds__(kThreads, threads_per_sm(KIND, P) / kThreads) void 
       any |= on;
       if constexpr (KIND == HS_KV_FP8E4M3_G32) {
         store_grouped<D, INTERLEAVED>(pages, scales, row0 + r, s, t, a.rotary, on, s_group[threadIdx.x / TPR], u, w);
+      } else if constexpr (KIND == HS_KV_INT4_G32) {
+        store_int4<D, INTERLEAVED>(pages, scales, row0 + r, s, t, a.rotary, on, s_group[threadIdx.x / TPR], u, w);
       } else if constexpr (KIND == HS_KV_FP8E4M3_BLOCK) {
         if (on && !box) amax = widen_any(amax, u, w);
       } else {
@@ -736,7 +809,7 @@ template <int D, int KIND, bool INTERLEAVED>
 __global__ __launch_bounds__(kThreads) void append_one_kernel(KvView kv, AppendTokensArgs a, int kv_ctas, unsigned* err) {
   constexpr bool F32 = KIND == HS_KV_F32;
   constexpr int TPR = D / 16, RPC = kThreads / TPR;  // threads per row, rows per CTA
-  __shared__ unsigned s_group[RPC][D / kQuantGroup];
+  __shared__ unsigned s_group[RPC][2 * (D / kQuantGroup)];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -798,6 +871,9 @@ __global__ __launch_bounds__(kThreads) void append_one_kernel(KvView kv, AppendT
   if constexpr (KIND == HS_KV_FP8E4M3_G32) {
     store_grouped<D, INTERLEAVED>(kp, ks, row, s, t, a.rotary, live_k, s_group[rs], ku, kw);
     store_grouped<D, INTERLEAVED>(vp, vs, row, s, t, a.rotary, live, s_group[rs], vu, vw);
+  } else if constexpr (KIND == HS_KV_INT4_G32) {
+    store_int4<D, INTERLEAVED>(kp, ks, row, s, t, a.rotary, live_k, s_group[rs], ku, kw);
+    store_int4<D, INTERLEAVED>(vp, vs, row, s, t, a.rotary, live, s_group[rs], vu, vw);
   } else if constexpr (KIND == HS_KV_FP8E4M3_BLOCK) {
     float lo[16], hi[16];  // box of the earlier rows, channels 16 s and up, where their codes change
     // The page's scale, the codes and the earlier rows' codes where the scale
@@ -914,7 +990,7 @@ cudaError_t launch_i(const KvView& kv, const AppendTokensArgs& a, int sms, unsig
   }
   constexpr int kPass = 32 / (D / 16);  // rows of a page that a warp reads at a time
   constexpr bool kBlock = KIND == HS_KV_FP8E4M3_BLOCK;
-  constexpr int P = kBlock || KIND == HS_KV_FP8E4M3_G32 ? 2 : 4;
+  constexpr int P = kBlock || KIND == HS_KV_FP8E4M3_G32 || KIND == HS_KV_INT4_G32 ? 2 : 4;
   if (kv.block <= 2 * kPass) return launch_rows<D, KIND, INTERLEAVED, 1, 2>(kv, a, sms, err, st);
   if (kv.block <= 4 * kPass) return launch_rows<D, KIND, INTERLEAVED, 1, P>(kv, a, sms, err, st);
   if constexpr (kBlock)
@@ -934,6 +1010,7 @@ cudaError_t launch_d(const KvView& kv, const AppendTokensArgs& a, int sms, unsig
     case HS_KV_F32: return launch_k<D, HS_KV_F32>(kv, a, sms, err, st);
     case HS_KV_BF16: return launch_k<D, HS_KV_BF16>(kv, a, sms, err, st);
     case HS_KV_FP8E4M3_G32: return launch_k<D, HS_KV_FP8E4M3_G32>(kv, a, sms, err, st);
+    case HS_KV_INT4_G32: return launch_k<D, HS_KV_INT4_G32>(kv, a, sms, err, st);
     default: return launch_k<D, HS_KV_FP8E4M3_BLOCK>(kv, a, sms, err, st);
   }
 }

@@ -10,35 +10,12 @@
 // are combined in shared memory and written as one normalised partial
 // (o, lse) per query head and split.
 #include "hs_internal.h"
+#include "kv_row.cuh"
 
 namespace hs {
 namespace {
 
 constexpr int kWarps = 4;
-
-template <int C, int KIND>
-__device__ __forceinline__ void load_row(const void* pages, const float* scales, int page, int64_t row,
-                                         int D, int d0, float (&x)[C]) {
-  if constexpr (KIND == HS_KV_F32) {
-    const float* p = static_cast<const float*>(pages) + row * D + d0;
-#pragma unroll
-    for (int c = 0; c < C; ++c) x[c] = __ldg(p + c);
-  } else if constexpr (KIND == HS_KV_BF16) {
-    const uint16_t* p = static_cast<const uint16_t*>(pages) + row * D + d0;
-#pragma unroll
-    for (int c = 0; c < C; ++c) x[c] = bf16_bits_to_float(__ldg(reinterpret_cast<const unsigned short*>(p + c)));
-  } else {
-    const uint8_t* p = static_cast<const uint8_t*>(pages) + row * D + d0;
-    const float s = __ldg(KIND == HS_KV_FP8E4M3_BLOCK ? scales + page : scales + row * (D / kQuantGroup) + d0 / kQuantGroup);
-#pragma unroll
-    for (int c = 0; c < C; c += 2) {
-      const uint16_t two = static_cast<uint16_t>(__ldg(p + c)) | (static_cast<uint16_t>(__ldg(p + c + 1)) << 8);
-      float2 f = e4m3x2_to_float2(two);
-      x[c] = f.x * s;
-      x[c + 1] = f.y * s;
-    }
-  }
-}
 
 template <int C, int G, int KIND>
 __global__ __launch_bounds__(kWarps * 32) void attn_simt_kernel(KvView kv, AttnArgs a,
@@ -167,6 +144,7 @@ cudaError_t launch_c(const KvView& kv, const AttnArgs& a, unsigned* err, cudaStr
     case HS_KV_F32: return launch_g<C, HS_KV_F32>(kv, a, err, st);
     case HS_KV_BF16: return launch_g<C, HS_KV_BF16>(kv, a, err, st);
     case HS_KV_FP8E4M3_G32: return launch_g<C, HS_KV_FP8E4M3_G32>(kv, a, err, st);
+    case HS_KV_INT4_G32: return launch_g<C, HS_KV_INT4_G32>(kv, a, err, st);
     default: return launch_g<C, HS_KV_FP8E4M3_BLOCK>(kv, a, err, st);
   }
 }

@@ -3,6 +3,7 @@
 // consecutive channels of a row, so one warp load reads whole consecutive
 // rows.  HBM-bound: one pass over the K pages of the blocks asked for.
 #include "hs_internal.h"
+#include "int4.cuh"
 
 namespace hs {
 namespace {
@@ -186,6 +187,70 @@ cudaError_t launch_k(const KvView& kv, int first_block, int nblocks, void* smin,
   }
 }
 
+// A warp's equal run of the blocks of all requests and kv heads, end to end.  All 32
+// lanes call the constructor; `w` of `warps` warps.
+struct BlockRun {
+  const KvView& kv;
+  int first_block, req, n_req, j;  // the request, its blocks, the block
+  int64_t pair, g, g_end;
+
+  __device__ __forceinline__ int blocks_of(int b) const {
+    return max(min(ceil_div(max(__ldg(kv.seq_lens + b), 0), kv.block), kv.max_blocks) - first_block, 0);
+  }
+  __device__ __forceinline__ BlockRun(const KvView& view, int first, int64_t w, int64_t warps, int lane)
+      : kv(view), first_block(first), req(0), n_req(0), j(0), pair(0) {
+    const int batch = kv.batch, mine_n = (batch + 31) / 32, b0 = min(batch, lane * mine_n), b1 = min(batch, b0 + mine_n);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += blocks_of(b);
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const int64_t total = __shfl_sync(0xffffffffu, incl, 31) * kv.hkv;
+    const int64_t per = (total + warps - 1) / warps;
+    g = w * per;
+    g_end = min(total, g + per);
+    if (g >= g_end) return;
+    int64_t before = 0;  // blocks of the requests before req, all kv heads
+    const unsigned has = __ballot_sync(0xffffffffu, incl * kv.hkv > g);
+    const int owner = __ffs(has) - 1;
+    if (lane == owner) {
+      before = (incl - mine) * kv.hkv;
+      for (req = b0; req < b1 - 1; ++req) {
+        const int64_t n = static_cast<int64_t>(blocks_of(req)) * kv.hkv;
+        if (g < before + n) break;
+        before += n;
+      }
+    }
+    req = __shfl_sync(0xffffffffu, req, owner);
+    before = __shfl_sync(0xffffffffu, before, owner);
+    n_req = blocks_of(req);
+    pair = static_cast<int64_t>(req) * kv.hkv + (g - before) / n_req;
+    j = first_block + static_cast<int>((g - before) % n_req);
+  }
+  __device__ __forceinline__ bool more() const { return g < g_end; }
+  // Blocks from j on that are of the same pair and this run's, 32 at most.
+  __device__ __forceinline__ int count() const {
+    return static_cast<int>(min(static_cast<int64_t>(min(32, first_block + n_req - j)), g_end - g));
+  }
+  __device__ __forceinline__ void on(int n) {
+    g += n;
+    j += n;
+    if (j < first_block + n_req) return;
+    j = first_block;
+    ++pair;
+    if (pair == static_cast<int64_t>(req + 1) * kv.hkv && g < g_end) {
+      do {  // the next request with blocks: there is one before g_end
+        ++req;
+        n_req = blocks_of(req);
+      } while (n_req == 0);
+      pair = static_cast<int64_t>(req) * kv.hkv;
+    }
+  }
+};
+
 // ---- e4m3 with one scale per page ----
 // The scale is the same for the whole block, so min and max are taken over the
 // codes, as f16 pairs (which hold every e4m3 number), and only the two results
@@ -224,49 +289,14 @@ __global__ __launch_bounds__(kWarps * 32, block_ctas(kRows)) void summaries_bloc
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int rs = lane / (D / 4), d0 = lane % (D / 4) * 4;
-  const int B = kv.block, batch = kv.batch;
-  const auto blocks_of = [&](int b) { return max(min(ceil_div(max(__ldg(kv.seq_lens + b), 0), B), kv.max_blocks) - first_block, 0); };
-
-  // ---- this warp's run [g, g_end) of all blocks, and where it begins ----
-  const int mine_n = (batch + 31) / 32, b0 = min(batch, lane * mine_n), b1 = min(batch, b0 + mine_n);
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += blocks_of(b);
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  const int64_t total = __shfl_sync(0xffffffffu, incl, 31) * kv.hkv;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps, w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int64_t per = (total + warps - 1) / warps;
-  int64_t g = w * per;
-  const int64_t g_end = min(total, g + per);
-  if (g >= g_end) return;
-  int req = 0;
-  int64_t before = 0;  // blocks of the requests before req, all kv heads
-  {
-    const unsigned has = __ballot_sync(0xffffffffu, incl * kv.hkv > g);
-    const int owner = __ffs(has) - 1;
-    if (lane == owner) {
-      before = (incl - mine) * kv.hkv;
-      for (req = b0; req < b1 - 1; ++req) {
-        const int64_t n = static_cast<int64_t>(blocks_of(req)) * kv.hkv;
-        if (g < before + n) break;
-        before += n;
-      }
-    }
-    req = __shfl_sync(0xffffffffu, req, owner);
-    before = __shfl_sync(0xffffffffu, before, owner);
-  }
-  int n_req = blocks_of(req);
-  int64_t pair = static_cast<int64_t>(req) * kv.hkv + (g - before) / n_req;
-  int j = first_block + static_cast<int>((g - before) % n_req);
-
-  while (g < g_end) {
+  const int B = kv.block;
+  BlockRun run(kv, first_block, static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5),
+               static_cast<int64_t>(gridDim.x) * kWarps, lane);
+  while (run.more()) {
     // ---- up to 32 blocks of one pair ----
-    const int n = static_cast<int>(min(static_cast<int64_t>(min(32, first_block + n_req - j)), g_end - g));
-    const int L = __ldg(kv.seq_lens + req);
+    const int n = run.count(), j = run.j;
+    const int64_t pair = run.pair;
+    const int L = __ldg(kv.seq_lens + run.req);
     int my_page = -1;
     float my_scale = 0.0f;
     if (lane < n) {
@@ -341,20 +371,7 @@ __global__ __launch_bounds__(kWarps * 32, block_ctas(kRows)) void summaries_bloc
         mx[0] = mx[1] = __half2half2(__ushort_as_half(0xfc00));
       }
     }
-    // ---- on ----
-    g += n;
-    j += n;
-    if (j == first_block + n_req) {
-      j = first_block;
-      ++pair;
-      if (pair == static_cast<int64_t>(req + 1) * kv.hkv && g < g_end) {
-        do {  // the next request with blocks: there is one before g_end
-          ++req;
-          n_req = blocks_of(req);
-        } while (n_req == 0);
-        pair = static_cast<int64_t>(req) * kv.hkv;
-      }
-    }
+    run.on(n);
   }
 }
 
@@ -376,6 +393,99 @@ cudaError_t launch_block(const KvView& kv, int first_block, int nblocks, void* s
                                    : launch_block_rows<D, 16>(kv, first_block, nblocks, smin, smax, err, sms, st);
 }
 
+// ---- 4-bit codes ----
+// Every row has scales and centres of its own, so each value is formed in fp32
+// (z + s c) before it is compared.  A lane owns 8 neighbouring channels, a warp a
+// run of blocks; the row slots of a warp are joined at a block's end.
+template <int D>
+__global__ __launch_bounds__(kWarps * 32) void summaries_int4_kernel(KvView kv, int first_block, void* smin, void* smax,
+                                                                     unsigned* err) {
+  constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes of a row, rows of one warp load
+  constexpr int kRows = 4;                    // loads in flight
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int rs = lane / LPR, d0 = lane % LPR * 8;
+  const int B = kv.block;
+  BlockRun run(kv, first_block, static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5),
+               static_cast<int64_t>(gridDim.x) * kWarps, lane);
+  while (run.more()) {
+    const int n = run.count(), j = run.j;
+    const int64_t pair = run.pair;
+    const int L = __ldg(kv.seq_lens + run.req);
+    int my_page = -1;
+    if (lane < n) {
+      my_page = __ldg(kv.page_table + pair * kv.max_blocks + j + lane);
+      if (my_page < 0 || my_page >= kv.num_pages) {
+        set_error(err, HS_EBIT_PAGE_RANGE);
+        my_page = -1;
+      }
+    }
+    for (unsigned left = __ballot_sync(0xffffffffu, my_page >= 0); left; left &= left - 1) {
+      const int i = __ffs(left) - 1;
+      const int64_t row0 = static_cast<int64_t>(__shfl_sync(0xffffffffu, my_page, i)) * B;
+      const int valid = min(B, L - (j + i) * B);
+      float mn[8], mx[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        mn[c] = INFINITY;
+        mx[c] = -INFINITY;
+      }
+      for (int t0 = 0; t0 < valid; t0 += kRows * RPL) {
+        uint32_t raw[kRows];
+        float2 q[kRows];
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {  // clamp: a repeated valid row changes nothing
+          const int64_t row = row0 + min(t0 + u * RPL + rs, valid - 1);
+          raw[u] = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(kv.k_pages) + row * int4::row_bytes(D) + d0 / 2));
+          q[u] = int4::load_scale(kv.k_scales, row, D, d0 / kQuantGroup);
+        }
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+          float x[8];
+          int4::decode8(raw[u], q[u].x, q[u].y, x);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            mn[c] = fminf(mn[c], x[c]);
+            mx[c] = fmaxf(mx[c], x[c]);
+          }
+        }
+      }
+#pragma unroll
+      for (int off = LPR; off < 32; off <<= 1)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          mn[c] = fminf(mn[c], __shfl_xor_sync(0xffffffffu, mn[c], off));
+          mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], off));
+        }
+      if (rs == 0) {
+        const int64_t o = (pair * kv.max_blocks + j + i) * D + d0;
+        __nv_bfloat162 lo[4], hi[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {  // outward: the stored box still contains every dequantised key
+          lo[c].x = __float2bfloat16_rd(mn[2 * c]);
+          lo[c].y = __float2bfloat16_rd(mn[2 * c + 1]);
+          hi[c].x = __float2bfloat16_ru(mx[2 * c]);
+          hi[c].y = __float2bfloat16_ru(mx[2 * c + 1]);
+        }
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(smin) + o) = *reinterpret_cast<const uint4*>(lo);
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(smax) + o) = *reinterpret_cast<const uint4*>(hi);
+      }
+    }
+    run.on(n);
+  }
+}
+
+template <int D>
+cudaError_t launch_int4(const KvView& kv, int first_block, int nblocks, void* smin, void* smax, unsigned* err, int sms,
+                        cudaStream_t st) {
+  // a warp for each block at most
+  const int64_t most = (static_cast<int64_t>(kv.batch) * kv.hkv * nblocks + kWarps - 1) / kWarps;
+  const int resident = sms * 4;
+  const unsigned grid = static_cast<unsigned>(most < resident ? most : resident);
+  return launch_pdl(summaries_int4_kernel<D>, dim3(grid), dim3(kWarps * 32), 0, st, kv, first_block, smin, smax, err);
+}
+
 template <int D>
 cudaError_t launch_d(const KvView& kv, int first_block, int nblocks, void* smin, void* smax,
                      unsigned* err, int sms, cudaStream_t st) {
@@ -383,6 +493,7 @@ cudaError_t launch_d(const KvView& kv, int first_block, int nblocks, void* smin,
     case HS_KV_F32: return launch_k<D, HS_KV_F32>(kv, first_block, nblocks, smin, smax, err, sms, st);
     case HS_KV_BF16: return launch_k<D, HS_KV_BF16>(kv, first_block, nblocks, smin, smax, err, sms, st);
     case HS_KV_FP8E4M3_G32: return launch_k<D, HS_KV_FP8E4M3_G32>(kv, first_block, nblocks, smin, smax, err, sms, st);
+    case HS_KV_INT4_G32: return launch_int4<D>(kv, first_block, nblocks, smin, smax, err, sms, st);
     default: return launch_block<D>(kv, first_block, nblocks, smin, smax, err, sms, st);
   }
 }

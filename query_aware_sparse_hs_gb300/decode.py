@@ -13,8 +13,9 @@ import torch
 from . import hs
 
 _SUMMARY_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8": torch.bfloat16,
-                  "fp8_block": torch.bfloat16}
-_Q_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8": torch.bfloat16, "fp8_block": torch.bfloat16}
+                  "fp8_block": torch.bfloat16, "int4": torch.bfloat16}
+_Q_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8": torch.bfloat16, "fp8_block": torch.bfloat16,
+            "int4": torch.bfloat16}
 
 
 class SparseDecode:
@@ -137,6 +138,24 @@ class SparseDecode:
         hs.hs_score_select_attend(self.shape, kv, q, self.smin, self.smax, self.sel_params, self.sel,
                                   self.sel_count, self.scores if keep_scores else None, self.attn_params,
                                   self.out, self.lse, self.workspace, stream)
+
+    def accumulate_weights(self, kv: hs.PagedKV, q: torch.Tensor, weights: torch.Tensor, stream=None, selection=None):
+        """Adds what the step's queries looked at to ``weights`` ([batch][Hkv][max_blocks * B] f32), after the step's
+        attention left ``lse`` (``selection`` as in attend())."""
+        src = self if selection is None else selection
+        if src.capacity != self.capacity:
+            raise ValueError("a reused selection must have the same capacity")
+        hs.hs_accumulate_attn_weights(self.shape, kv, q, self.lse, src.sel, src.sel_count, self.capacity,
+                                      self.attn_params.scale, weights, stream)
+
+    def evict(self, kv: hs.PagedKV, dst: hs.PagedKV, params: hs.EvictParams, weights: torch.Tensor,
+              dst_weights: torch.Tensor | None, kept: torch.Tensor, stream=None):
+        """Gathers the heaviest tokens of every (request, kv head) into the pages of ``dst`` and builds their summaries,
+        so that the next step goes on with ``dst`` (its seq_lens is written)."""
+        if dst.max_blocks != self.max_blocks:
+            raise ValueError("dst must have this decoder's max_blocks")
+        hs.hs_evict_tokens(self.shape, kv, dst, params, weights, dst_weights, kept, stream)
+        self.build_summaries(dst, 0, stream)
 
     def swap_in(self, hb: hs.HotBuffer, step: int, stats=None, stream=None):
         hs.hs_swapin_misses(self.shape, hb, self.sel, self.sel_count, self.capacity, step, stats, stream)

@@ -26,7 +26,7 @@ HS_ATTN_RANGES = 2
 HS_ATTN_NO_RANGES = 4
 HS_EBIT_PAGE_RANGE, HS_EBIT_CAPACITY, HS_EBIT_TIMEOUT, HS_EBIT_BLOCK_RANGE = 0x1, 0x2, 0x4, 0x8
 HS_EBIT_POSITION = 0x10
-KV_DTYPES = {"f32": 0, "bf16": 1, "fp8": 2, "fp8_block": 3}
+KV_DTYPES = {"f32": 0, "bf16": 1, "fp8": 2, "fp8_block": 3, "int4": 4}
 ALGO = {"auto": 0, "simt": 1, "tcgen05": 2}
 
 
@@ -70,6 +70,10 @@ class HotBuffer(ctypes.Structure):
                 ("v_slot_scales", c_void_p), ("host_k", c_void_p), ("host_v", c_void_p),
                 ("host_k_scales", c_void_p), ("host_v_scales", c_void_p), ("batch", c_int32),
                 ("max_blocks", c_int32), ("slots_per_stream", c_int32)]
+
+
+class EvictParams(ctypes.Structure):
+    _fields_ = [("budget", c_int32), ("sink_tokens", c_int32), ("recent_tokens", c_int32)]
 
 
 class SwapStats(ctypes.Structure):
@@ -130,6 +134,12 @@ SYMBOLS = {
                                          c_int32, c_void_p, c_void_p]),
     "hs_quantize_e4m3_g32": (c_int32, [c_void_p, c_int32, c_int64, c_int32, c_void_p, c_void_p,
                                        c_void_p]),
+    "hs_quantize_int4_g32": (c_int32, [c_void_p, c_int32, c_int64, c_int32, c_void_p, c_void_p, c_void_p]),
+    "hs_dequantize_int4_g32": (c_int32, [c_void_p, c_void_p, c_int64, c_int32, c_void_p, c_int32, c_void_p]),
+    "hs_accumulate_attn_weights": (c_int32, [POINTER(AttnShape), POINTER(PagedKV), c_void_p, c_void_p, c_void_p,
+                                             c_void_p, c_int32, c_float, c_void_p, c_void_p]),
+    "hs_evict_tokens": (c_int32, [POINTER(AttnShape), POINTER(PagedKV), POINTER(PagedKV), POINTER(EvictParams),
+                                  c_void_p, c_void_p, c_void_p, c_void_p]),
     "hs_get_device_error": (c_int32, [c_void_p, POINTER(c_uint32)]),
     "hs_get_device_error_detail": (c_int32, [c_void_p, POINTER(c_uint32), POINTER(c_uint32)]),
 }
@@ -196,7 +206,8 @@ def attn_shape(num_q_heads, num_kv_heads, head_dim, block_size, kv_dtype) -> Att
 
 
 def paged_kv(k_pages, v_pages, page_table, seq_lens, k_scales=None, v_scales=None) -> PagedKV:
-    """Describe a paged cache: pages [num_pages][B][D], page_table [batch][Hkv][max_blocks]."""
+    """Describe a paged cache: pages [num_pages][B][D] (4-bit: [num_pages][B][D/2] bytes), page_table
+    [batch][Hkv][max_blocks], scales as hs.h lays them out (4-bit: [num_pages][B][2][D/32] bf16)."""
     kv = PagedKV(_ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales), _ptr(page_table),
                  _ptr(seq_lens), int(page_table.shape[0]), int(page_table.shape[-1]),
                  int(k_pages.shape[0]))
@@ -472,6 +483,69 @@ def hs_quantize_e4m3_g32(src, codes, scales, stream=None):
     _check(_lib.hs_quantize_e4m3_g32(_ptr(src), 1 if src.dtype == torch.float32 else 0, rows, D,
                                      _ptr(codes), _ptr(scales), _stream(stream)),
            "hs_quantize_e4m3_g32")
+
+
+def _int4_rows(values, codes, scales, what):
+    """Rows and head_dim of [rows][D] values, [rows][D/2] codes and [rows][2][D/32] scales (leading dimensions alike)."""
+    D = values.shape[-1]
+    rows = values.numel() // D if D else 0
+    if values.dtype not in (_F32, _BF16) or codes.dtype != torch.uint8 or scales.dtype != _BF16:
+        raise ValueError(f"{what}: values f32 or bf16, codes uint8, scales bf16")
+    if codes.numel() * 2 != rows * D or scales.numel() * 16 != rows * D or codes.shape[-1] * 2 != D:
+        raise ValueError(f"{what}: [rows][{D}] values go with [rows][{D // 2}] codes and [rows][2][{D // 32}] scales")
+    if not values.get_device() == codes.get_device() == scales.get_device():
+        raise ValueError(f"{what}: values, codes and scales must be on one device")
+    return rows, D
+
+
+def hs_quantize_int4_g32(src, codes, scales, stream=None):
+    """src [rows][D] f32 or bf16 -> codes [rows][D/2] uint8, scales [rows][2][D/32] bf16 (scales, then centres)."""
+    rows, D = _int4_rows(src, codes, scales, "hs_quantize_int4_g32")
+    _check(_lib.hs_quantize_int4_g32(_ptr(src), 1 if src.dtype == _F32 else 0, rows, D, _ptr(codes), _ptr(scales),
+                                     _stream(stream)),
+           "hs_quantize_int4_g32")
+
+
+def hs_dequantize_int4_g32(codes, scales, out, stream=None):
+    """codes [rows][D/2] uint8, scales [rows][2][D/32] bf16 -> out [rows][D] f32 or bf16 (pages as they are: any
+    leading dimensions)."""
+    rows, D = _int4_rows(out, codes, scales, "hs_dequantize_int4_g32")
+    _check(_lib.hs_dequantize_int4_g32(_ptr(codes), _ptr(scales), rows, D, _ptr(out), 1 if out.dtype == _F32 else 0,
+                                       _stream(stream)),
+           "hs_dequantize_int4_g32")
+
+
+def hs_accumulate_attn_weights(shape, kv, q, lse, sel, sel_count, capacity, scale, weights, stream=None):
+    """weights [batch][Hkv][max_blocks * B] f32 += the group's softmax weights of every token of the selected blocks,
+    lse [batch][Hq] f32 as the attention over the same selection left it."""
+    if lse.dtype != _F32 or weights.dtype != _F32 or weights.numel() != kv.batch * shape.num_kv_heads * kv.max_blocks * shape.block_size:
+        raise ValueError("lse and weights must be f32, weights [batch][Hkv][max_blocks * B]")
+    _check(_lib.hs_accumulate_attn_weights(ctypes.byref(shape), ctypes.byref(kv), _ptr(q), _ptr(lse), _ptr(sel),
+                                           _ptr(sel_count), int(capacity), float(scale), _ptr(weights),
+                                           _stream(stream)),
+           "hs_accumulate_attn_weights")
+
+
+def evict_params(budget, sink_tokens=0, recent_tokens=0) -> EvictParams:
+    """Tokens that hs_evict_tokens keeps of each (request, kv head), the first sink_tokens and the last recent_tokens
+    among them."""
+    return EvictParams(int(budget), int(sink_tokens), int(recent_tokens))
+
+
+def hs_evict_tokens(shape, kv, dst, params, weights, dst_weights, kept, stream=None):
+    """The heaviest tokens of every (request, kv head) gathered into the pages of ``dst`` (a paged_kv whose seq_lens is
+    written).  weights [batch][Hkv][max_blocks * B] f32, dst_weights the same for dst (or None), kept
+    [batch][Hkv][budget] int32."""
+    pairs = kv.batch * shape.num_kv_heads
+    if weights.dtype != _F32 or weights.numel() != pairs * kv.max_blocks * shape.block_size:
+        raise ValueError("weights must be f32 [batch][Hkv][max_blocks * B]")
+    if dst_weights is not None and (dst_weights.dtype != _F32 or dst_weights.numel() != pairs * dst.max_blocks * shape.block_size):
+        raise ValueError("dst_weights must be f32 [batch][Hkv][max_blocks of dst * B]")
+    if kept.dtype != torch.int32 or kept.numel() != pairs * params.budget:
+        raise ValueError("kept must be int32 [batch][Hkv][budget]")
+    _check(_lib.hs_evict_tokens(ctypes.byref(shape), ctypes.byref(kv), ctypes.byref(dst), ctypes.byref(params),
+                                _ptr(weights), _ptr(dst_weights), _ptr(kept), _stream(stream)),
+           "hs_evict_tokens")
 
 
 def hs_get_device_error(stream=None) -> tuple[int, int]:

@@ -1,0 +1,127 @@
+"""Refusals of the 4-bit cache, the accumulated weights and the eviction, before anything is launched.  CPU only."""
+
+import ctypes
+
+import pytest
+import torch
+
+P = 0x10000  # an aligned address that nothing reads
+
+
+def kv(hs, batch=2, mb=8, pages=16, **more):
+    k = hs.PagedKV()
+    k.k_pages = k.v_pages = k.k_scales = k.v_scales = k.page_table = k.seq_lens = P
+    k.batch, k.max_blocks, k.num_pages = batch, mb, pages
+    for name, value in more.items():
+        setattr(k, name, value)
+    return k
+
+
+def ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+@pytest.fixture
+def hs():
+    from query_aware_sparse_hs_gb300 import hs
+    return hs
+
+
+def test_quantise_and_dequantise(hs):
+    lib = hs.library()
+    for call in (lambda s, r, d, c, z: lib.hs_quantize_int4_g32(s, 0, r, d, c, z, None),
+                 lambda s, r, d, c, z: lib.hs_dequantize_int4_g32(c, z, r, d, s, 0, None)):
+        assert call(None, 4, 128, P, P) == hs.HS_ERR_INVALID_ARG
+        assert call(P, 4, 128, None, P) == hs.HS_ERR_INVALID_ARG
+        assert call(P, 4, 128, P, None) == hs.HS_ERR_INVALID_ARG
+        assert call(P, -1, 128, P, P) == hs.HS_ERR_INVALID_ARG
+        assert call(P + 8, 4, 128, P, P) == hs.HS_ERR_INVALID_ARG
+        assert call(P, 4, 128, P + 2, P) == hs.HS_ERR_INVALID_ARG
+        assert call(P, 4, 128, P, P + 2) == hs.HS_ERR_INVALID_ARG
+        assert call(P, 4, 96, P, P) == hs.HS_ERR_UNSUPPORTED
+        assert call(P, 1 << 40, 128, P, P) == hs.HS_ERR_UNSUPPORTED
+    x = torch.zeros((4, 128))
+    c, s = torch.zeros((4, 64), dtype=torch.uint8), torch.zeros((4, 2, 4), dtype=torch.bfloat16)
+    for bad in ((x.half(), c, s), (x, c.int(), s), (x, c, s.float()), (x, c[:3], s), (x, c, s[:3]), (x, c.view(8, 32), s)):
+        with pytest.raises(ValueError):
+            hs.hs_quantize_int4_g32(*bad)
+        with pytest.raises(ValueError):
+            hs.hs_dequantize_int4_g32(bad[1], bad[2], bad[0])
+    with pytest.raises(ValueError):
+        hs.hs_quantize_int4_g32(x.t().contiguous().t(), c, s)
+
+
+def test_a_4_bit_cache(hs):
+    lib = hs.library()
+    shape = hs.attn_shape(16, 2, 128, 64, "int4")
+    for bad in (kv(hs, k_scales=None), kv(hs, k_scales=P + 8), kv(hs, k_pages=P + 8), kv(hs, num_pages=-1)):
+        assert lib.hs_build_block_summaries(ref(shape), ref(bad), 0, P, P, None) == hs.HS_ERR_INVALID_ARG
+    for bad in (kv(hs, v_scales=None), kv(hs, v_scales=P + 4), kv(hs, v_pages=None)):
+        assert lib.hs_append_token(ref(shape), ref(bad), P, P, P, P, None) == hs.HS_ERR_INVALID_ARG
+        params = hs.attn_params(0.1)
+        assert lib.hs_sparse_paged_decode_attn(ref(shape), ref(bad), P, P, P, 4, ref(params), P, None, P, 1 << 30,
+                                               None) == hs.HS_ERR_INVALID_ARG
+    # no host pool of 4-bit pages
+    hb = hs.HotBuffer()
+    for f in ("page_table", "slot_owner", "last_used", "k_slots", "v_slots", "host_k", "host_v", "k_slot_scales", "v_slot_scales",
+              "host_k_scales", "host_v_scales"):
+        setattr(hb, f, P)
+    hb.batch, hb.max_blocks, hb.slots_per_stream = 2, 8, 4
+    assert lib.hs_swapin_misses(ref(shape), ref(hb), P, P, 4, 0, None, None) == hs.HS_ERR_UNSUPPORTED
+    assert lib.hs_swapin_copy(ref(shape), ref(hb), P, P, 4, 0, None, None) == hs.HS_ERR_UNSUPPORTED
+    assert hs.hs_workspace_bytes(shape, 2, 4, hs.attn_params(0.1)) > 0
+    past = hs.AttnShape(16, 2, 128, 64, 5)
+    assert lib.hs_build_block_summaries(ref(past), ref(kv(hs)), 0, P, P, None) == hs.HS_ERR_INVALID_ARG
+
+
+def test_accumulated_weights(hs):
+    lib = hs.library()
+    shape = hs.attn_shape(16, 2, 128, 64, "bf16")
+
+    def call(s=shape, c=None, q=P, lse=P, sel=P, cnt=P, cap=4, w=P):
+        return lib.hs_accumulate_attn_weights(ref(s), ref(kv(hs) if c is None else c), q, lse, sel, cnt, cap, 0.1, w, None)
+
+    for bad in ({"q": None}, {"lse": None}, {"sel": None}, {"cnt": None}, {"w": None}, {"cap": 0}, {"q": P + 8}, {"lse": P + 2},
+                {"sel": P + 1}, {"cnt": P + 2}, {"w": P + 2}, {"c": kv(hs, k_pages=None)}, {"c": kv(hs, batch=-1)}, {"s": None}):
+        assert call(**bad) == hs.HS_ERR_INVALID_ARG, bad
+    assert call(s=hs.attn_shape(16, 2, 96, 64, "bf16")) == hs.HS_ERR_UNSUPPORTED
+    assert call(c=kv(hs, batch=1 << 30)) == hs.HS_ERR_UNSUPPORTED
+    k = kv(hs)
+    lse, w = torch.zeros((2, 16)), torch.zeros((2, 2, 8 * 64))
+    q, sel, cnt = torch.zeros((2, 16, 128), dtype=torch.bfloat16), torch.zeros((2, 2, 4), dtype=torch.int32), torch.zeros((2, 2), dtype=torch.int32)
+    for bad in ((lse.half(), w), (lse, w.half()), (lse, w[:, :, 1:])):
+        with pytest.raises(ValueError):
+            hs.hs_accumulate_attn_weights(shape, k, q, bad[0], sel, cnt, 4, 0.1, bad[1])
+
+
+def test_eviction(hs):
+    lib = hs.library()
+    shape = hs.attn_shape(16, 2, 128, 64, "bf16")
+
+    def call(s=shape, c=None, d=None, p=(100, 4, 32), w=P, dw=P + 64, kept=P):
+        params = None if p is None else hs.evict_params(*p)
+        return lib.hs_evict_tokens(ref(s), ref(kv(hs) if c is None else c), ref(kv(hs) if d is None else d), ref(params), w, dw, kept, None)
+
+    for bad in ({"p": None}, {"w": None}, {"kept": None}, {"dw": P}, {"w": P + 2}, {"dw": P + 66}, {"kept": P + 1}, {"p": (0, 0, 0)},
+                {"p": (-1, 0, 0)}, {"p": (100, -1, 0)}, {"p": (100, 0, -1)}, {"p": (100, 60, 41)}, {"p": (8 * 64 + 1, 0, 0)},
+                {"p": (100, 2147483647, 2147483647)}, {"d": kv(hs, batch=3)}, {"c": kv(hs, v_pages=None)}, {"d": kv(hs, k_pages=None)},
+                {"d": kv(hs, v_pages=P + 4)}, {"s": None}):
+        assert call(**bad) == hs.HS_ERR_INVALID_ARG, bad
+    assert call(s=hs.attn_shape(16, 2, 128, 64, "fp8_block")) == hs.HS_ERR_UNSUPPORTED
+    big = dict(batch=1 << 20, mb=1 << 20)
+    assert call(c=kv(hs, **big), d=kv(hs, **big), p=(1 << 25, 0, 0)) == hs.HS_ERR_UNSUPPORTED
+    k = kv(hs)
+    w, kept = torch.zeros((2, 2, 8 * 64)), torch.zeros((2, 2, 100), dtype=torch.int32)
+    p = hs.evict_params(100)
+    for bad in ((w.double(), w.clone(), kept), (w[:, :1], w.clone(), kept), (w, w[:, :1].clone(), kept), (w, w.half(), kept),
+                (w, None, kept.long()), (w, None, kept[:, :, 1:])):
+        with pytest.raises(ValueError):
+            hs.hs_evict_tokens(shape, k, k, p, *bad)
+
+
+def test_the_driver_refuses_a_cache_of_another_length(hs, monkeypatch):
+    from query_aware_sparse_hs_gb300.decode import SparseDecode
+    dec = SparseDecode.__new__(SparseDecode)
+    dec.max_blocks = 9
+    with pytest.raises(ValueError):
+        dec.evict(kv(hs), kv(hs), hs.evict_params(10), None, None, None)
