@@ -1,0 +1,510 @@
+// What the attention kernels that cut their work by the actual counts share: the parts
+// of every (request, kv head)'s selection and the teams of warps that take them, the
+// lookup of a run's rows, the merge of a pair's partial results.  Everything is in an
+// anonymous namespace of its includer.
+#pragma once
+
+#include <limits.h>
+
+#include "hs_internal.h"
+
+namespace hs {
+namespace {
+namespace parts {
+
+constexpr int kTeamWarps = 4;
+constexpr int kMaxWarps = 4 * kTeamWarps;
+constexpr int kTile = 32;       // tokens a warp handles at a time
+constexpr int kMinTiles = 8;    // tiles of a part of a cut pair at least
+// Pairs of up to so many tiles are not cut: two for each warp of a CTA (4 pairs of
+// 1000 tokens, 128 channels, 32 tiles: 9.6 us cut, 11.0 whole; 16 tiles: 8.4 whole).
+__host__ __device__ constexpr int whole_tiles(int teams) { return 2 * teams * kTeamWarps; }
+constexpr int kMergeTiles = 3;  // what a merge costs, in tiles per warp
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMinRef = 1.925929944387236e-34f;  // 2^-112
+constexpr uint32_t kMaxRef = 0x7f000000u;          // 2^127, as bits
+// P * vscale enters in units of 2^-kUnit times the reference: 2^14 at most, twice that
+// for a V scale above 2^127, which f16 holds.  (P up to 2^6, in units of 2^-8, would
+// spare most rescalings of the state, 2% for 16 heads of 64 channels, for 6 bits less
+// below the f16 range.)
+constexpr int kUnit = 14;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 bytes to shared memory
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// the same; zeros, and nothing read, unless `live`
+__device__ __forceinline__ void copy16_if(uint32_t dst, const void* src, bool live) {
+  const int n = live ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool live) {
+  const int n = live ? 4 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float exp2_fast(float x) {  // 2 ulp; results under 2^-126 are 0
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 2^kUnit / ref, of a power of two from kMinRef to 2^127
+__device__ __forceinline__ float unit_over(float ref) {
+  return __uint_as_float((static_cast<uint32_t>(254 + kUnit) << 23) - __float_as_uint(ref));
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_half2(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
+
+struct PartArgs {
+  const void* q;
+  const int32_t* sel;
+  const int32_t* sel_count;
+  void* out;
+  float* lse;
+  float* ws_o;
+  float* ws_lse;
+  uint32_t* counters;  // nullable
+  int32_t capacity;
+  int32_t out_f32;
+  float scale;
+};
+
+// Selected blocks of pair p, and tiles of so many.
+__device__ __forceinline__ int pair_count(const PartArgs& a, int64_t p) {
+  const int c = __ldg(a.sel_count + p);
+  return min(max(c, 0), a.capacity);
+}
+__device__ __forceinline__ int tiles_of(const KvView& kv, int count) {  // (the host saw that all of them fit)
+  return static_cast<int>((static_cast<uint32_t>(count) * kv.block + kTile - 1) / kTile);
+}
+
+// Warps that take parts together.  bar: 0 for the whole CTA, else the number of
+// the hardware barrier.
+struct Team {
+  int rank, warps, bar;  // the thread's number in the team, the team's warps
+  __device__ __forceinline__ int threads() const { return warps * 32; }
+  __device__ __forceinline__ void sync() const {
+    if (bar == 0)
+      __syncthreads();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(kTeamWarps * 32) : "memory");
+  }
+};
+
+// Every pair is cut into equal parts of at most `per` tiles; the parts of all
+// pairs are numbered through and dealt to the slots in turn.  A slot is a team
+// of kTeamWarps warps, or (joint) all warps of a CTA.  With
+// per = total / max(slots - pairs, slots / 2) there are no more parts than slots
+// where the pairs leave room for that (sum of ceil(n / per) <= total / per +
+// pairs), and a long pair among many short ones is still spread over half the
+// slots.  Short pairs are not cut: they have nothing to merge.  A pair that is cut
+// has a row of the workspace for each part: at most 2 total / per <= 2 slots rows
+// in all.
+//   Joint parts halve (64 channels: third) the parts, and so the merges, and the
+//   time of a short part; with more pairs than CTAs, or pairs so uneven that CTAs
+//   are left idle, teams balance better.  Taken where every CTA has one part at
+//   most and the longest pair's, in tiles per warp, is not longer than the teams' by
+//   more than a merge.  With one term of P, 32 requests x 4 heads x 4096 selected tokens:
+//   joint 28 us, teams 32; 24 uneven requests x 4 heads: 56 and 48; 64 x 4 heads x 4096:
+//   54 and 49.
+struct Cut {
+  int per, slots, whole;
+  bool joint;
+};
+struct Part {
+  int pair;
+  int index, count;  // which of the pair's parts
+  int row;           // workspace row of the pair's first part
+};
+struct Pairs {  // one pair's numbers
+  int part, count, row;  // its first part, how many, workspace row of the first
+};
+constexpr int kListed = 32;  // parts a team notes at a time
+
+__device__ __forceinline__ int parts_of(int tiles, int per, int whole) {
+  return tiles <= whole ? (tiles > 0 ? 1 : 0) : (tiles + per - 1) / per;
+}
+__device__ __forceinline__ int part_of(int tiles, int per) {  // the longest part of a pair that is cut
+  const int k = max((tiles + per - 1) / per, 1);
+  return (tiles + k - 1) / k;
+}
+__device__ __forceinline__ int per_of(int total, int pairs, int slots) {
+  return max((total - 1) / max(max(slots - pairs, slots / 2), 1) + 1, kMinTiles);
+}
+
+struct Scratch {
+  int64_t sums[kMaxWarps];
+  int tiles[kMaxWarps], longest[kMaxWarps];
+};
+
+// The cut for this call's counts, by all threads of a CTA (`cta`).  seen(p, count)
+// sees every pair once, in one of the threads.
+template <typename F>
+__device__ Cut choose_cut(const KvView& kv, const PartArgs& a, int ctas, int teams, const Team& cta, Scratch& sc, F&& seen) {
+  const int warp = cta.rank >> 5, lane = cta.rank & 31;
+  const int pairs = kv.batch * kv.hkv, mine_n = (pairs + cta.threads() - 1) / cta.threads();
+  const int p0 = min(pairs, cta.rank * mine_n), p1 = min(pairs, p0 + mine_n);
+  int total = 0, longest = 0;  // tiles
+  for (int p = p0; p < p1; ++p) {
+    const int c = pair_count(a, p), n = tiles_of(kv, c);
+    seen(p, c);
+    total += n;
+    longest = max(longest, n);
+  }
+  total = __reduce_add_sync(0xffffffffu, total);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 0) {
+    sc.tiles[warp] = total;
+    sc.longest[warp] = longest;
+  }
+  cta.sync();
+  total = longest = 0;
+  for (int w = 0; w < cta.warps; ++w) {
+    total += sc.tiles[w];
+    longest = max(longest, sc.longest[w]);
+  }
+  const int per_joint = per_of(total, pairs, ctas), per_team = per_of(total, pairs, ctas * teams);
+  Cut cut;
+  cut.whole = whole_tiles(teams);
+  // no more joint parts than CTAs: the pairs leave room for the cuts, or none is cut
+  const bool one_each = pairs <= ctas / 2 || (pairs <= ctas && longest <= max(per_joint, cut.whole));
+  const int joint = part_of(longest, per_joint), team = part_of(longest, per_team);
+  cut.joint = one_each && joint <= (team / kTeamWarps + kMergeTiles) * kTeamWarps * teams;
+  cut.slots = cut.joint ? ctas : ctas * teams;
+  cut.per = cut.joint ? per_joint : per_team;
+  return cut;
+}
+
+// each(p, numbers) sees every pair once, in one of the team's threads; the team
+// meets before the number of parts is returned.
+template <typename F>
+__device__ int number_parts(const KvView& kv, const PartArgs& a, const Cut& cut, const Team& team, Scratch& sc, F&& each) {
+  const int warp = team.rank >> 5, lane = team.rank & 31;
+  const int pairs = kv.batch * kv.hkv, mine_n = (pairs + team.threads() - 1) / team.threads();
+  const int p0 = min(pairs, team.rank * mine_n), p1 = min(pairs, p0 + mine_n);
+  int64_t mine = 0;  // parts, and rows of the workspace in the upper half
+  for (int p = p0; p < p1; ++p) {
+    const int k = parts_of(tiles_of(kv, pair_count(a, p)), cut.per, cut.whole);
+    mine += k + (k > 1 ? static_cast<int64_t>(k) << 32 : 0);
+  }
+  int64_t at = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += v;
+  }
+  if (lane == 31) sc.sums[warp] = at;
+  at -= mine;
+  team.sync();
+  int64_t all = 0;
+  for (int w = 0; w < team.warps; ++w) {
+    if (w == warp) at += all;
+    all += sc.sums[w];
+  }
+  for (int p = p0; p < p1; ++p) {
+    Pairs n;
+    n.count = parts_of(tiles_of(kv, pair_count(a, p)), cut.per, cut.whole);
+    n.part = static_cast<int>(at & 0xffffffff);
+    n.row = static_cast<int>(at >> 32);
+    each(p, n);
+    at += n.count + (n.count > 1 ? static_cast<int64_t>(n.count) << 32 : 0);
+  }
+  team.sync();
+  return static_cast<int>(all & 0xffffffff);
+}
+
+__device__ __forceinline__ void store_out(const PartArgs& a, int64_t at, float4 v) {
+  if (a.out_f32) {
+    reinterpret_cast<float4*>(a.out)[at / 4] = v;
+  } else {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
+    reinterpret_cast<uint2*>(a.out)[at / 4] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  }
+}
+
+// Joins the partial results of a pair into out / lse, every kTeamWarps warps of
+// the team those of every groups-th part, and then the groups.  The order goes by
+// the parts' numbers alone.  w: shared memory for G * (count + 1) floats and
+// groups - 1 results.  The first results are on their way while their weights are
+// found.
+template <int D, int NT>
+__device__ void merge_pair(const KvView& kv, const PartArgs& a, const Team& team, int64_t pair, int row0, int count,
+                           float* w) {
+  constexpr int kGroup = kTeamWarps * 32;
+  constexpr int NI = NT * 8 * D / 4 / kGroup;  // 16-byte pieces of a result per thread, at most
+  constexpr int U = 16 / NI;                   // results in flight
+  const int G = kv.group, lane = team.rank & 31, warp = team.rank >> 5, threads = team.threads();
+  const int groups = team.warps / kTeamWarps, grp = team.rank / kGroup, rank = team.rank - grp * kGroup;
+  float* lses = w + G * count;
+  float4* sums = reinterpret_cast<float4*>(w + (G * (count + 1) + 3) / 4 * 4);
+  const float* ws_lse = a.ws_lse + static_cast<int64_t>(row0) * G;
+  const float4* ws_o = reinterpret_cast<const float4*>(a.ws_o + static_cast<int64_t>(row0) * G * D);
+  const int pieces = G * (D / 4);
+  float4 got[U][NI];
+  const auto load = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+#pragma unroll
+      for (int n = 0; n < NI; ++n) {
+        const int i = i0 + k * groups, idx = rank + n * kGroup;
+        got[k][n] = i < count && idx < pieces ? __ldcg(ws_o + static_cast<int64_t>(i) * pieces + idx)
+                                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+  };
+  load(grp);
+  for (int i = team.rank; i < G * count; i += threads) w[i] = __ldcg(ws_lse + i);
+  team.sync();
+  for (int h = warp; h < G; h += team.warps) {
+    float M = -INFINITY, tot = 0.0f;
+    for (int i = lane; i < count; i += 32) M = fmaxf(M, w[i * G + h]);
+    M = warp_max(M);
+    if (M == -INFINITY) M = 0.0f;  // no token, or only results that are not numbers: those stay so
+    for (int i = lane; i < count; i += 32) {
+      const float e = expf(w[i * G + h] - M);
+      w[i * G + h] = e;
+      tot += e;
+    }
+    tot = warp_sum(tot);
+    const float norm = tot == 0.0f ? 0.0f : 1.0f / tot;
+    for (int i = lane; i < count; i += 32) w[i * G + h] *= norm;
+    if (lane == 0) lses[h] = tot == 0.0f ? -INFINITY : M + logf(tot);
+  }
+  team.sync();
+  float4 acc[NI];
+#pragma unroll
+  for (int n = 0; n < NI; ++n) acc[n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int i0 = grp; i0 < count;) {
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+#pragma unroll
+      for (int n = 0; n < NI; ++n) {
+        const int i = i0 + k * groups, idx = rank + n * kGroup;
+        const float e = i < count && idx < pieces ? w[i * G + idx / (D / 4)] : 0.0f;
+        acc[n].x = fmaf(e, got[k][n].x, acc[n].x);
+        acc[n].y = fmaf(e, got[k][n].y, acc[n].y);
+        acc[n].z = fmaf(e, got[k][n].z, acc[n].z);
+        acc[n].w = fmaf(e, got[k][n].w, acc[n].w);
+      }
+    i0 += U * groups;
+    if (i0 < count) load(i0);
+  }
+  if (groups > 1) {
+#pragma unroll
+    for (int n = 0; n < NI; ++n)
+      if (grp > 0 && rank + n * kGroup < pieces) sums[(grp - 1) * pieces + rank + n * kGroup] = acc[n];
+    team.sync();
+  }
+  const int64_t b = pair / kv.hkv, out_row = b * kv.hq + (pair - b * kv.hkv) * G;
+#pragma unroll
+  for (int n = 0; n < NI; ++n) {
+    const int idx = rank + n * kGroup;
+    if (grp > 0 || idx >= pieces) continue;
+    for (int j = 0; j < groups - 1; ++j) {
+      const float4 v = sums[j * pieces + idx];
+      acc[n] = make_float4(acc[n].x + v.x, acc[n].y + v.y, acc[n].z + v.z, acc[n].w + v.w);
+    }
+    store_out(a, out_row * D + 4 * idx, acc[n]);
+  }
+  if (a.lse && team.rank < G) a.lse[out_row + team.rank] = lses[team.rank];
+}
+
+// Pairs that nothing is selected of: out = 0, lse = -inf.  CTAs share them.
+template <int D>
+__device__ void answer_empty(const KvView& kv, const PartArgs& a, int tid, int threads) {
+  const int G = kv.group;
+  for (int p = blockIdx.x; p < kv.batch * kv.hkv; p += gridDim.x) {
+    if (pair_count(a, p) > 0) continue;
+    const int64_t b = p / kv.hkv, row = b * kv.hq + static_cast<int64_t>(p - b * kv.hkv) * G;
+    for (int i = tid; i < G * D / 4; i += threads) store_out(a, row * D + 4 * i, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+    if (a.lse && tid < G) a.lse[row + tid] = -INFINITY;
+  }
+}
+
+// The states of a team's warps joined: running maxima, sums and references in s_m, s_l
+// and s_ref by the team's warps, outputs in `so` ([warp][8 NT][D], in units of
+// 2^-kUnit of the warp's reference).  A part that is a whole pair goes to out / lse,
+// another to its row of the workspace, and the team that arrives last merges the pair.
+template <int D, int NT>
+__device__ void finish_part(const KvView& kv, const PartArgs& a, const Team& team, const Part& part, const float (*s_m)[8 * NT],
+                            const float (*s_l)[8 * NT], const float* s_ref, float* so, int* last) {
+  const int G = kv.group, b = part.pair / kv.hkv, ws_row = (part.row + part.index) * G;
+  const bool whole = part.count == 1;
+  for (int idx = team.rank; idx < G * (D / 4); idx += team.threads()) {
+    const int h = idx / (D / 4), d = (idx - h * (D / 4)) * 4;
+    float M = -INFINITY, ref = kMinRef;
+    for (int w = 0; w < team.warps; ++w) {
+      M = fmaxf(M, s_m[w][h]);
+      ref = fmaxf(ref, s_ref[w]);
+    }
+    if (M == -INFINITY) M = 0.0f;  // no token, or only logits that are not numbers
+    const float per = unit_over(ref);
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float tot = 0.0f;
+#pragma unroll 4
+    for (int w = 0; w < team.warps; ++w) {
+      const float f = exp2f(s_m[w][h] - M);
+      const float4 v = *reinterpret_cast<const float4*>(so + (w * 8 * NT + h) * D + d);
+      const float fr = f * (s_ref[w] * per);  // (the sums stay in units of the largest reference)
+      tot = fmaf(s_l[w][h], f, tot);
+      acc.x = fmaf(v.x, fr, acc.x);
+      acc.y = fmaf(v.y, fr, acc.y);
+      acc.z = fmaf(v.z, fr, acc.z);
+      acc.w = fmaf(v.w, fr, acc.w);
+    }
+    float lse = -INFINITY;
+    if (tot != 0.0f) {
+      const float n = 1.0f / (1 << 2 * kUnit) / tot;
+      acc = make_float4(acc.x * n * ref, acc.y * n * ref, acc.z * n * ref, acc.w * n * ref);
+      lse = M * kLn2 + logf(tot);
+    }
+    if (whole) {
+      const int64_t row = static_cast<int64_t>(b) * kv.hq + (part.pair - b * kv.hkv) * G + h;
+      store_out(a, row * D + d, acc);
+      if (d == 0 && a.lse) a.lse[row] = lse;
+    } else {
+      *reinterpret_cast<float4*>(a.ws_o + static_cast<int64_t>(ws_row + h) * D + d) = acc;
+      if (d == 0) a.ws_lse[ws_row + h] = lse;
+    }
+  }
+  if (!whole && a.counters) {
+    team.sync();
+    if (team.rank == 0) {
+      // releases what the team wrote before the barrier, acquires what the others released
+      uint32_t there;
+      asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(there) : "l"(a.counters + part.pair) : "memory");
+      *last = there == static_cast<uint32_t>(part.count - 1);
+      if (*last) a.counters[part.pair] = 0u;
+    }
+    team.sync();
+    if (*last) merge_pair<D, NT>(kv, a, team, part.pair, part.row, part.count, so);
+  }
+}
+
+// The merge as a launch of its own, for callers without split counters.  CTA =
+// pair; as many warps as merge in place, so that the results are the same.
+template <int D, int NT, int TEAMS>
+__global__ __launch_bounds__(TEAMS * kTeamWarps * 32) void merge_parts_kernel(KvView kv, PartArgs a, int ctas) {
+  extern __shared__ __align__(16) float weights[];
+  __shared__ Scratch s_scratch;
+  __shared__ Pairs s_pair;
+  pdl_trigger();
+  pdl_wait();
+  const int pair = blockIdx.x, tid = threadIdx.x;
+  const Team cta{tid, TEAMS * kTeamWarps, 0};
+  const Cut cut = choose_cut(kv, a, ctas, TEAMS, cta, s_scratch, [](int, int) {});
+  if (!cut.joint && tid >= kTeamWarps * 32) return;
+  const Team team = cut.joint ? cta : Team{tid, kTeamWarps, 1};
+  number_parts(kv, a, cut, team, s_scratch, [&](int p, const Pairs& n) {
+    if (p == pair) s_pair = n;
+  });
+  if (s_pair.count > 1) merge_pair<D, NT>(kv, a, team, pair, s_pair.row, s_pair.count, weights);
+}
+
+// The rows of a run of 32-token tiles of a pair's selection, lane = token: which row of
+// the pool it is, tile by tile.  Selected blocks are looked up 32 at a time, one to a
+// lane, the pages one window ahead of the rows and the selection two, so that neither
+// load is waited for.  A window holds the entries from that of its first tile on; a
+// tile that does not fit opens the next.  All 32 lanes call everything.
+struct TileRows {
+  const int32_t* sel;
+  const int32_t* table;
+  unsigned* err;
+  int64_t num_pages;
+  uint32_t B, u, u_stop, e_base, e1, e2, w_end, w_end1, w_end2;
+  int cnt, nb, L, lane, page, lim, page1, lim1, j2, ei, er, step_i, step_r;
+
+  __device__ __forceinline__ uint32_t window_end(uint32_t from, uint32_t e) const {  // past the window's whole tiles
+    return from + ((e + 32) * B - from) / kTile * kTile;
+  }
+  __device__ __forceinline__ int load_sel(uint32_t from, uint32_t e) const {  // INT_MIN: no such entry (one that is so is out of range anyway)
+    return from < u_stop && e + lane < static_cast<uint32_t>(cnt) ? max(__ldg(sel + e + lane), INT_MIN + 1) : INT_MIN;
+  }
+  __device__ __forceinline__ void load_page(int j, int& pg, int& rows) const {  // rows: valid rows of the page
+    pg = rows = 0;
+    if (j == INT_MIN) return;
+    if (j < 0 || j >= nb) {
+      set_error(err, HS_EBIT_BLOCK_RANGE);
+      return;
+    }
+    pg = __ldg(table + j);
+    if (pg < 0 || pg >= num_pages) {
+      set_error(err, HS_EBIT_PAGE_RANGE);
+      pg = 0;
+      return;
+    }
+    rows = min(static_cast<int>(B), L - j * static_cast<int>(B));
+  }
+  // Tiles [run0, run0 + tiles) of the first `count` selected blocks; L tokens in the request.
+  __device__ __forceinline__ void start(const KvView& kv, const int32_t* selection, const int32_t* pages, int count, int tokens,
+                                        int run0, int tiles, int this_lane, unsigned* error) {
+    sel = selection;
+    table = pages;
+    err = error;
+    num_pages = kv.num_pages;
+    B = kv.block;
+    cnt = count;
+    L = tokens;
+    lane = this_lane;
+    nb = min(ceil_div(max(L, 0), kv.block), kv.max_blocks);
+    u = static_cast<uint32_t>(run0) * kTile;
+    u_stop = u + static_cast<uint32_t>(tiles) * kTile;
+    e_base = u / B;
+    const int j0 = load_sel(u, e_base);
+    w_end = window_end(u, e_base);
+    e1 = w_end / B;
+    const int j1 = load_sel(w_end, e1);
+    w_end1 = window_end(w_end, e1);
+    e2 = w_end1 / B;
+    j2 = load_sel(w_end1, e2);
+    w_end2 = window_end(w_end1, e2);
+    load_page(j0, page, lim);
+    load_page(j1, page1, lim1);
+    ei = static_cast<int>((u + lane) / B);
+    er = static_cast<int>(u + lane - ei * B);
+    step_i = kTile / static_cast<int>(B);
+    step_r = kTile - step_i * static_cast<int>(B);
+  }
+  // The lane's row of the next tile (0 where there is none), and its place in the
+  // request; false: no such token.
+  __device__ __forceinline__ bool next(uint32_t& row) {
+    if (u >= w_end) {
+      e_base = e1;
+      w_end = w_end1;
+      page = page1;
+      lim = lim1;
+      e1 = e2;
+      w_end1 = w_end2;
+      load_page(j2, page1, lim1);
+      e2 = w_end2 / B;
+      j2 = load_sel(w_end2, e2);
+      w_end2 = window_end(w_end2, e2);
+    }
+    const int pg = __shfl_sync(0xffffffffu, page, ei - static_cast<int>(e_base));
+    const bool ok = er < __shfl_sync(0xffffffffu, lim, ei - static_cast<int>(e_base));
+    row = ok ? static_cast<uint32_t>(pg) * B + er : 0u;
+    u += kTile;
+    ei += step_i;
+    er += step_r;
+    if (er >= static_cast<int>(B)) {
+      er -= B;
+      ++ei;
+    }
+    return ok;
+  }
+};
+
+}  // namespace parts
+}  // namespace
+}  // namespace hs

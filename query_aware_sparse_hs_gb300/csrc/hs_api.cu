@@ -171,11 +171,16 @@ size_t workspace_for(const hs_attn_shape* s, int batch, int splits) {
   return (bytes + 255) & ~static_cast<size_t>(255);
 }
 
-// The same for the kernel of block-scaled e4m3, which cuts the work by the
-// actual counts.
-size_t block_workspace(const hs_attn_shape* s, int ctas) {
-  const size_t rows = static_cast<size_t>(block_attn_rows(ctas, s->head_dim)) * (s->num_q_heads / s->num_kv_heads);
-  return (rows * (s->head_dim + 1) * sizeof(float) + 255) & ~static_cast<size_t>(255);
+// The kinds whose tensor-core kernels cut the work by the actual counts, and the rows
+// of partial results that they may write.
+bool cut_by_counts(int kv_dtype) { return kv_dtype == HS_KV_FP8E4M3_BLOCK || kv_dtype == HS_KV_INT4_G32; }
+size_t counts_rows(const hs_attn_shape* s, int ctas) {
+  const int group = s->num_q_heads / s->num_kv_heads;
+  return static_cast<size_t>(s->kv_dtype == HS_KV_INT4_G32 ? int4_attn_rows(ctas, s->head_dim, group) : block_attn_rows(ctas, s->head_dim)) *
+         group;
+}
+size_t counts_workspace(const hs_attn_shape* s, int ctas) {
+  return (counts_rows(s, ctas) * (s->head_dim + 1) * sizeof(float) + 255) & ~static_cast<size_t>(255);
 }
 
 // Partial workspace an attention call may need: the larger of the uniform
@@ -188,7 +193,7 @@ size_t attn_workspace_need(const hs_attn_shape* s, int batch, int capacity, cons
   AttnArgs t;
   split_geometry(s, batch, capacity, p, ctas, &bps, &splits, &t);
   size_t tc = workspace_for(s, batch, splits);
-  if (s->kv_dtype == HS_KV_FP8E4M3_BLOCK) tc = block_workspace(s, ctas);
+  if (cut_by_counts(s->kv_dtype)) tc = counts_workspace(s, ctas);
   return uniform > tc ? uniform : tc;
 }
 
@@ -276,7 +281,7 @@ hs_status prepare_attn(const hs_attn_shape* shape, const hs_paged_kv* kv, const 
   const int ctas = attn_ctas(d.sms, params);
   if (params->algo == 1) {
     *use_tc = false;
-  } else if (shape->kv_dtype == HS_KV_FP8E4M3_BLOCK) {
+  } else if (cut_by_counts(shape->kv_dtype)) {
     *use_tc = true;
   } else if (params->algo == 2) {
     if (!attn_tc_supported(v)) return HS_ERR_UNSUPPORTED;
@@ -285,7 +290,7 @@ hs_status prepare_attn(const hs_attn_shape* shape, const hs_paged_kv* kv, const 
     *use_tc = attn_tc_supported(v);
   }
   AttnArgs& a = *out_args;
-  const bool by_counts = *use_tc && shape->kv_dtype == HS_KV_FP8E4M3_BLOCK;
+  const bool by_counts = *use_tc && cut_by_counts(shape->kv_dtype);
   if (by_counts && (static_cast<int64_t>(kv->batch) * shape->num_kv_heads > INT32_MAX ||
                  kv->num_pages * shape->block_size > UINT32_MAX ||  // rows are numbered in 32 bits
                  static_cast<int64_t>(capacity) * shape->block_size > INT32_MAX ||
@@ -293,7 +298,7 @@ hs_status prepare_attn(const hs_attn_shape* shape, const hs_paged_kv* kv, const 
                  (static_cast<int64_t>(capacity) * shape->block_size / 32 + 1) * kv->batch * shape->num_kv_heads > INT32_MAX))
     return HS_ERR_UNSUPPORTED;
   split_geometry(shape, kv->batch, capacity, params, ctas, &a.blocks_per_split, &a.splits, *use_tc ? &a : nullptr);
-  const size_t need = by_counts ? block_workspace(shape, ctas) : workspace_for(shape, kv->batch, a.splits);
+  const size_t need = by_counts ? counts_workspace(shape, ctas) : workspace_for(shape, kv->batch, a.splits);
   if (need > 0 && (!workspace || ws_bytes < need || !aligned(workspace, 16))) return HS_ERR_WORKSPACE;
   a.sms = ctas;
   if (params->split_counters && !aligned(params->split_counters, 4)) return HS_ERR_INVALID_ARG;
@@ -309,7 +314,7 @@ hs_status prepare_attn(const hs_attn_shape* shape, const hs_paged_kv* kv, const 
   a.out = out;
   a.lse = lse_opt;
   a.ws_o = static_cast<float*>(workspace);
-  a.ws_lse = a.ws_o + (by_counts ? static_cast<size_t>(block_attn_rows(ctas, v.head_dim)) * v.group
+  a.ws_lse = a.ws_o + (by_counts ? counts_rows(shape, ctas)
                               : static_cast<size_t>(kv->batch) * shape->num_q_heads * a.splits) *
                           shape->head_dim;
   return HS_OK;
@@ -317,6 +322,7 @@ hs_status prepare_attn(const hs_attn_shape* shape, const hs_paged_kv* kv, const 
 
 // The attention's launches, the merge of its splits among them.
 hs_status run_attn(const KvView& v, AttnArgs& a, bool use_tc, unsigned* err, cudaStream_t s) {
+  if (use_tc && v.kv_dtype == HS_KV_INT4_G32) return from_cuda(launch_int4_attn(v, a, err, s));
   if (use_tc && v.kv_dtype == HS_KV_FP8E4M3_BLOCK) return from_cuda(launch_block_attn(v, a, err, s));
   const cudaError_t e = use_tc ? launch_attn_tc(v, a, err, s) : launch_attn_simt(v, a, err, s);
   if (e != cudaSuccess) return HS_ERR_CUDA;
@@ -352,7 +358,7 @@ int32_t hs_attn_geometry(const hs_attn_shape* shape, int32_t batch, int32_t capa
                          const hs_attn_params* params, int32_t* splits, int32_t* chunks_per_cta) {
   if (check_shape(shape) != HS_OK || batch < 0 || capacity < 1 || !params || !splits || !chunks_per_cta) return -1;
   if (params->blocks_per_split < 0 || params->max_ctas < 0) return -1;
-  if (shape->kv_dtype == HS_KV_FP8E4M3_BLOCK) {  // cut on the device, by the counts
+  if (cut_by_counts(shape->kv_dtype)) {  // cut on the device, by the counts
     *splits = *chunks_per_cta = 0;
     return 0;
   }

@@ -100,6 +100,9 @@ bool attn_tc_supported(const KvView& kv);
 // a.counters, else in a second launch.
 int block_attn_rows(int ctas, int head_dim);
 cudaError_t launch_block_attn(const KvView& kv, const AttnArgs& a, unsigned* err, cudaStream_t st);
+// The same for 4-bit caches.
+int int4_attn_rows(int ctas, int head_dim, int group);
+cudaError_t launch_int4_attn(const KvView& kv, const AttnArgs& a, unsigned* err, cudaStream_t st);
 // Bound scoring, selection and tensor-core attention in one cluster launch
 // (bf16, head_dim 128, g <= 8, every pair in one wave of at most 8 CTAs).
 bool score_select_attn_supported(const KvView& kv, const AttnArgs& a, int sms);
