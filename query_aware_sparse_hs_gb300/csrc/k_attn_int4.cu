@@ -20,15 +20,15 @@
 // masking 4 bits out of either half of it gives two numbers n = c + 8:
 //   K: as they stand, bf16 numbers below the normal ones, n 2^-133 and 16 n 2^-133, which
 //     the matrix units multiply exactly (q times a power of two brings the products back
-//     to size, its odd channels by 1/16); the sum starts at -8 sum q.
-//   V: with the exponent of 2^10 set, f16 1024 + n and 1024 + 16 n; one two-wide
-//     subtraction makes them c and 16 c.  (They are sums over the whole context, so n
+//     to size, its odd channels by 1/16); -8 sum q goes with the scale.
+//   V: likewise f16 numbers, n 2^-24 and 16 n 2^-24; one two-wide subtraction makes
+//     them c 2^-24 and 16 c 2^-24, exactly.  (They are sums over the whole context, so n
 //     itself would have to cancel against 8: a flat softmax over 60000 tokens would lose
 //     its digits.)  V's transposition is ldmatrix's: its 16-bit units are 4 codes of a
 //     token.
-// The centres' products are instructions of their own: for K the row's centres times
-// sum q as three bf16 terms, for V two bf16 terms of P times the record of scales and
-// centres as it lies in memory.
+// What scales and centres are multiplied by without the codes, -8 sum q and sum q for K,
+// P for V, goes with the record as it lies in memory, in instructions of its own: three
+// bf16 terms of the sums, two of P.
 //
 // Precision: q is exact (bf16, times a power of two, which takes entries up to 2^90), S
 // and all sums fp32.  P times s, in units of 2^-14 of the reference (the largest power of
@@ -82,14 +82,14 @@ __device__ __forceinline__ void load4_trans(uint32_t at, uint32_t (&r)[4]) {
                : "r"(at)
                : "memory");
 }
-// d = a b + c
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
-                                         float c0, float c2) {
+// d = a b
+__device__ __forceinline__ void mma_bf16_0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%11,%11};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c2));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
+// d += a b
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -108,7 +108,30 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 __device__ __forceinline__ float lower(uint32_t two) { return __uint_as_float(two << 16); }        // of two bf16
 __device__ __forceinline__ float upper(uint32_t two) { return __uint_as_float(two & 0xffff0000u); }
-// n (or 16 n) of two of V's codes, as f16 with 2^10 added -> c (or 16 c)
+// Two fp32 numbers at a time.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+// n 2^-24 (or 16 times that) of two of V's codes, as f16 -> c 2^-24
 __device__ __forceinline__ uint32_t centred(uint32_t two, uint32_t minus) {
   const __half2 x = __hadd2(*reinterpret_cast<const __half2*>(&two), *reinterpret_cast<const __half2*>(&minus));
   return *reinterpret_cast<const uint32_t*>(&x);
@@ -167,6 +190,11 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
   const uint8_t* v_recs = reinterpret_cast<const uint8_t*>(kv.v_scales);
   // what it reads: row lane % 8 of matrix lane / 8
   const int mat = lane >> 3, mr = lane & 7;
+  // (every 8th row is permuted alike)
+  const uint32_t k_at = D == 128 ? piece_at<D>(mr, mat) : piece_at<D>(8 * (mat >> 1) + mr, mat & 1);
+  uint32_t v_at[kGroups / 2];
+#pragma unroll
+  for (int k = 0; k < kGroups; k += 2) v_at[k / 2] = At::kV + piece_at<D>(8 * (mat & 1) + mr, k + (mat >> 1));
 
   const int my_parts = (all_parts - slot + cut.slots - 1) / cut.slots;
   for (int n_part = 0; n_part < my_parts; ++n_part) {
@@ -211,13 +239,23 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
       const bool ok = rows.next(row);
       const uint32_t live = __ballot_sync(0xffffffffu, ok);
       const uint32_t dst = ring_addr + stage_in * At::kBytes;
+      const uint32_t my = dst + piece_at<D>(lane / kPieces, lane % kPieces);  // (the same for every kRowsPer-th row)
+      if (live == 0xffffffffu) {
 #pragma unroll
-      for (int i = 0; i < kTile / kRowsPer; ++i) {
-        const int r = i * kRowsPer + lane / kPieces;
-        const uint64_t at = static_cast<uint64_t>(__shfl_sync(0xffffffffu, row, r)) * At::kRow;
-        const bool there = (live >> r) & 1u;
-        copy16_if(dst + piece_at<D>(r, lane % kPieces), k_piece + at, there);
-        copy16_if(dst + At::kV + piece_at<D>(r, lane % kPieces), v_piece + at, there);
+        for (int i = 0; i < kTile / kRowsPer; ++i) {
+          const uint64_t at = static_cast<uint64_t>(__shfl_sync(0xffffffffu, row, i * kRowsPer + lane / kPieces)) * At::kRow;
+          copy16(my + i * (kRowsPer * At::kRow), k_piece + at);
+          copy16(my + i * (kRowsPer * At::kRow) + At::kV, v_piece + at);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kTile / kRowsPer; ++i) {
+          const int r = i * kRowsPer + lane / kPieces;
+          const uint64_t at = static_cast<uint64_t>(__shfl_sync(0xffffffffu, row, r)) * At::kRow;
+          const bool there = (live >> r) & 1u;
+          copy16_if(my + i * (kRowsPer * At::kRow), k_piece + at, there);
+          copy16_if(my + i * (kRowsPer * At::kRow) + At::kV, v_piece + at, there);
+        }
       }
       const uint64_t rec = static_cast<uint64_t>(row) * (D / 8);
       if constexpr (D == 128) {
@@ -242,8 +280,7 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
 
     // ---- the query, as first operands ----
     uint32_t qa[NT][kGroups][4];  // even channels 0 4 and 2 6 of a lane's 8, then the odd ones by 1/16
-    float q8[NT][kGroups];        // what the sum starts at
-    uint32_t xa[NT][2];           // the groups' sums as three bf16 terms, k = term * groups + group
+    uint32_t xa[NT][3];           // three bf16 terms of what scale or centre word c4 of a record is multiplied by
     float f[NT];                  // from S times the scale to a logit (log2 units)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -268,44 +305,37 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
       const int e = min(max(227 - static_cast<int>(__float_as_uint(amax) >> 23), 10), 127);
       const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
       f[nt] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(133 - e + 127) << 23);
-      float t[3][kGroups];  // sum q times the logits' factor, in three terms
 #pragma unroll
       for (int k = 0; k < kGroups; ++k) {
         qa[nt][k][0] = pack_bf16(x[k][0] * up, x[k][4] * up);
         qa[nt][k][1] = pack_bf16(x[k][2] * up, x[k][6] * up);
         qa[nt][k][2] = pack_bf16(x[k][1] * up * 0.0625f, x[k][5] * up * 0.0625f);
         qa[nt][k][3] = pack_bf16(x[k][3] * up * 0.0625f, x[k][7] * up * 0.0625f);
-        q8[nt][k] = -sum[k] * __uint_as_float(static_cast<uint32_t>(e - 130 + 127) << 23);  // -8 2^-133 sum q 2^e
-        float rest = sum[k] * (a.scale * kLog2e);
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          t[i][k] = __bfloat162float(__float2bfloat16_rn(rest));
-          rest -= t[i][k];
-        }
       }
-      // k = 2 c4, 2 c4 + 1 and 8 more: (D = 128) terms 0 and 1 of the groups, then term 2;
-      // (D = 64) the three terms, then nothing
-      if constexpr (D == 128) {
-        const int i = c4 >> 1;
-        const float u0 = c4 & 1 ? t[i][2] : t[i][0], u1 = c4 & 1 ? t[i][3] : t[i][1];
-        const float w0 = c4 & 1 ? t[2][2] : t[2][0], w1 = c4 & 1 ? t[2][3] : t[2][1];
-        xa[nt][0] = pack_bf16(u0, u1);
-        xa[nt][1] = c4 < 2 ? pack_bf16(w0, w1) : 0u;
-      } else {
-        const float u0 = c4 == 0 ? t[0][0] : c4 == 1 ? t[1][0] : t[2][0], u1 = c4 == 0 ? t[0][1] : c4 == 1 ? t[1][1] : t[2][1];
-        xa[nt][0] = c4 < 3 ? pack_bf16(u0, u1) : 0u;
-        xa[nt][1] = 0u;
+      // a record's words: scales of groups 0 1 (and 2 3), then the centres; -8 sum q for
+      // a scale, sum q for a centre
+      constexpr int kWords = kGroups / 2;  // of scales
+      const int pair = c4 & (kWords - 1);
+      const float by = a.scale * kLog2e * (c4 < kWords ? -8.0f : c4 < 2 * kWords ? 1.0f : 0.0f);
+      float r0 = (pair ? sum[kGroups - 2] : sum[0]) * by, r1 = (pair ? sum[kGroups - 1] : sum[1]) * by;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        xa[nt][i] = pack_bf16(r0, r1);
+        r0 -= lower(xa[nt][i]);
+        r1 -= upper(xa[nt][i]);
       }
     }
 
-    float m[NT], l[NT], base[NT];  // base: the maximum, 0 as long as there is none
+    float2 l[NT];
+    float m[NT], base[NT];         // base: the maximum, 0 as long as there is none
     float o[kGroups][4][4];        // rows g and g + 8 (up to 8 heads: P's second term), channels 32 k + 4 (2 c4 + e) + i
     float oz[4];                   // the centres' sums: column kGroups + k of the record
     float vref = kMinRef;          // power of two, not below the V scales and centres / 8 met
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt] = -INFINITY;
-      base[nt] = l[nt] = 0.0f;
+      base[nt] = 0.0f;
+      l[nt] = both(0.0f);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -331,60 +361,55 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
       const uint32_t live = s_live[warp][stage];
 
       // ---- logits (log2 units) of 8 tokens at a time ----
-      float x[NT][4][2];  // tokens 8 i + 2 c4, 8 i + 2 c4 + 1 of head g (and g + 8)
+      float2 x[NT][4];    // tokens 8 i + 2 c4, 8 i + 2 c4 + 1 of head g (and g + 8)
       uint32_t kw[4];     // codes of the 8 tokens' four groups, or of 16 tokens' two
+      uint32_t kr[4];     // the records, 8 tokens each
+      load4(st_addr + At::kRec + 16 * lane, kr);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (D == 128)
-          load4(st_addr + piece_at<D>(8 * i + mr, mat), kw);
+          load4(st_addr + k_at + i * (8 * At::kRow), kw);
         else if (i % 2 == 0)
-          load4(st_addr + piece_at<D>(8 * i + 8 * (mat >> 1) + mr, mat & 1), kw);
+          load4(st_addr + k_at + i * (8 * At::kRow), kw);
         float s[kGroups][4], sz[4];
 #pragma unroll
         for (int k = 0; k < kGroups; ++k) {
           const uint32_t v = kw[D == 128 ? k : 2 * (i % 2) + k], v8 = v >> 8;
-          mma_bf16(s[k], qa[0][k][0], qa[NT - 1][k][0], qa[0][k][1], qa[NT - 1][k][1], v & 0x000f000fu, v8 & 0x000f000fu, q8[0][k],
-                   q8[NT - 1][k]);
+          mma_bf16_0(s[k], qa[0][k][0], qa[NT - 1][k][0], qa[0][k][1], qa[NT - 1][k][1], v & 0x000f000fu, v8 & 0x000f000fu);
           mma_bf16(s[k], qa[0][k][2], qa[NT - 1][k][2], qa[0][k][3], qa[NT - 1][k][3], v & 0x00f000f0u, v8 & 0x00f000f0u);
         }
-        const uint8_t* rec = st + At::kRec + 128 * i;
-        const uint32_t z = *reinterpret_cast<const uint32_t*>(rec + 16 * g + (D == 128 ? 8 + 4 * (c4 & 1) : 4));
-        mma_bf16(sz, xa[0][0], xa[NT - 1][0], xa[0][1], xa[NT - 1][1], z, z, 0.0f, 0.0f);
+        mma_bf16_0(sz, xa[0][0], xa[NT - 1][0], xa[0][1], xa[NT - 1][1], kr[i], kr[i]);
+        mma_bf16(sz, xa[0][2], xa[NT - 1][2], 0u, 0u, kr[i], kr[i]);
+        const uint8_t* rec = st + At::kRec + 32 * c4 + 128 * i;
+        // the scales of tokens 8 i + 2 c4 and + 1
+        const uint2 r0 = *reinterpret_cast<const uint2*>(rec), r1 = *reinterpret_cast<const uint2*>(rec + 16);
+        float2 sc[4];
+        sc[0] = make_float2(lower(r0.x), lower(r1.x));
+        sc[1] = make_float2(upper(r0.x), upper(r1.x));
+        sc[2] = make_float2(lower(r0.y), lower(r1.y));
+        sc[3] = make_float2(upper(r0.y), upper(r1.y));
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float sc[kGroups];
-          const uint2 two = *reinterpret_cast<const uint2*>(rec + 16 * (2 * c4 + e));
-          sc[0] = lower(two.x);
-          sc[1] = upper(two.x);
-          if constexpr (D == 128) {
-            sc[2] = lower(two.y);
-            sc[3] = upper(two.y);
-          }
+        for (int nt = 0; nt < NT; ++nt) {
+          float2 sum = mul2(make_float2(s[0][2 * nt], s[0][2 * nt + 1]), sc[0]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float sum = s[0][2 * nt + e] * sc[0];
-#pragma unroll
-            for (int k = 1; k < kGroups; ++k) sum = fmaf(s[k][2 * nt + e], sc[k], sum);
-            x[nt][i][e] = fmaf(sum, f[nt], sz[2 * nt + e]);
-          }
+          for (int k = 1; k < kGroups; ++k) sum = fma2(make_float2(s[k][2 * nt], s[k][2 * nt + 1]), sc[k], sum);
+          x[nt][i] = fma2(sum, both(f[nt]), make_float2(sz[2 * nt], sz[2 * nt + 1]));
         }
       }
       if (live != 0xffffffffu) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (!((live >> (8 * i + 2 * c4 + e)) & 1u)) {
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) x[nt][i][e] = -INFINITY;
-            }
+          for (int nt = 0; nt < NT; ++nt) {
+            if (!((live >> (8 * i + 2 * c4)) & 1u)) x[nt][i].x = -INFINITY;
+            if (!((live >> (8 * i + 2 * c4 + 1)) & 1u)) x[nt][i].y = -INFINITY;
+          }
       }
       bool raised = false;
       float mn[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float top = fmaxf(fmaxf(fmaxf(x[nt][0][0], x[nt][0][1]), fmaxf(x[nt][1][0], x[nt][1][1])),
-                          fmaxf(fmaxf(x[nt][2][0], x[nt][2][1]), fmaxf(x[nt][3][0], x[nt][3][1])));
+        float top = fmaxf(fmaxf(fmaxf(x[nt][0].x, x[nt][0].y), fmaxf(x[nt][1].x, x[nt][1].y)),
+                          fmaxf(fmaxf(x[nt][2].x, x[nt][2].y), fmaxf(x[nt][3].x, x[nt][3].y)));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         mn[nt] = fmaxf(m[nt], top);
@@ -406,7 +431,7 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float was = m[nt] == -INFINITY ? 0.0f : exp2f(m[nt] - mn[nt]);
-          l[nt] *= was;
+          l[nt] = mul2(l[nt], both(was));
           m[nt] = mn[nt];
           base[nt] = mn[nt] == -INFINITY ? 0.0f : mn[nt];
           by[nt] = was * down;
@@ -428,43 +453,39 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
       load4_trans(st_addr + At::kRecV + 16 * lane, zr);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float p[NT][4];  // tokens 16 j + 2 c4, + 1, + 8, + 9
+        float2 p[NT][2];  // tokens 16 j + 2 c4 and + 1, 8 more
         uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float y = exp2_fast(x[nt][2 * j + (i >> 1)][i & 1] - base[nt]);
-            l[nt] += y;
-            p[nt][i] = y * unit;
-          }
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            hi[nt][i] = pack_bf16(p[nt][2 * i], p[nt][2 * i + 1]);
-            lo[nt][i] = pack_bf16(p[nt][2 * i] - lower(hi[nt][i]), p[nt][2 * i + 1] - upper(hi[nt][i]));
+            const float2 y = add2(x[nt][2 * j + i], both(-base[nt]));
+            p[nt][i] = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+            l[nt] = add2(l[nt], p[nt][i]);
+            p[nt][i] = mul2(p[nt][i], both(unit));
+            hi[nt][i] = pack_bf16(p[nt][i].x, p[nt][i].y);
+            lo[nt][i] = pack_bf16(p[nt][i].x - lower(hi[nt][i]), p[nt][i].y - upper(hi[nt][i]));
           }
-        }
         if constexpr (NT == 1) {
           mma_bf16(oz, hi[0][0], lo[0][0], hi[0][1], lo[0][1], zr[2 * j], zr[2 * j + 1]);
         } else {
           mma_bf16(oz, hi[0][0], hi[NT - 1][0], hi[0][1], hi[NT - 1][1], zr[2 * j], zr[2 * j + 1]);
           mma_bf16(oz, lo[0][0], lo[NT - 1][0], lo[0][1], lo[NT - 1][1], zr[2 * j], zr[2 * j + 1]);
         }
-        float sc[4][kGroups];  // the tokens' scales
+        float2 sc[2][4];  // the tokens' scales
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint2 two = *reinterpret_cast<const uint2*>(st + At::kRecV + 16 * (16 * j + 8 * (i >> 1) + 2 * c4 + (i & 1)));
-          sc[i][0] = lower(two.x);
-          sc[i][1] = upper(two.x);
-          if constexpr (D == 128) {
-            sc[i][2] = lower(two.y);
-            sc[i][3] = upper(two.y);
-          }
+        for (int i = 0; i < 2; ++i) {
+          const uint8_t* rec = st + At::kRecV + 32 * c4 + 16 * (16 * j + 8 * i);
+          const uint2 r0 = *reinterpret_cast<const uint2*>(rec), r1 = *reinterpret_cast<const uint2*>(rec + 16);
+          sc[i][0] = make_float2(lower(r0.x), lower(r1.x));
+          sc[i][1] = make_float2(upper(r0.x), upper(r1.x));
+          sc[i][2] = make_float2(lower(r0.y), lower(r1.y));
+          sc[i][3] = make_float2(upper(r0.y), upper(r1.y));
         }
 #pragma unroll
         for (int k2 = 0; k2 < kGroups; k2 += 2) {
           uint32_t w[4];  // tokens 16 j .. + 7 and + 8 .. + 15 of groups k2 and k2 + 1
-          load4_trans(st_addr + At::kV + piece_at<D>(16 * j + 8 * (mat & 1) + mr, k2 + (mat >> 1)), w);
+          load4_trans(st_addr + v_at[k2 / 2] + j * (16 * At::kRow), w);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int k = k2 + h;
@@ -472,18 +493,18 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const float y0 = p[nt][2 * i] * sc[2 * i][k], y1 = p[nt][2 * i + 1] * sc[2 * i + 1][k];
-                hi[nt][i] = pack_half2(y0, y1);
-                const float2 back = unpack_half2(hi[nt][i]);
-                lo[nt][i] = pack_half2(y0 - back.x, y1 - back.y);
+                const float2 y = mul2(p[nt][i], sc[i][k]);
+                hi[nt][i] = pack_half2(y.x, y.y);
+                const float2 rest = fma2(unpack_half2(hi[nt][i]), both(-1.0f), y);
+                lo[nt][i] = pack_half2(rest.x, rest.y);
               }
             const uint32_t w0 = w[2 * h], w1 = w[2 * h + 1];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t mask = i & 1 ? 0x00f000f0u : 0x000f000fu;
-              const uint32_t minus = i & 1 ? 0xe480e480u : 0xe408e408u;  // -1152, -1032
-              const uint32_t b0 = centred(((i < 2 ? w0 : w0 >> 8) & mask) | 0x64006400u, minus);
-              const uint32_t b1 = centred(((i < 2 ? w1 : w1 >> 8) & mask) | 0x64006400u, minus);
+              const uint32_t minus = i & 1 ? 0x80808080u : 0x80088008u;  // -8 times 2^-20, 2^-24
+              const uint32_t b0 = centred((i < 2 ? w0 : w0 >> 8) & mask, minus);
+              const uint32_t b1 = centred((i < 2 ? w1 : w1 >> 8) & mask, minus);
               if constexpr (NT == 1) {
                 mma_f16(o[k][i], hi[0][0], lo[0][0], hi[0][1], lo[0][1], b0, b1);
               } else {
@@ -504,7 +525,7 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
     float* so = reinterpret_cast<float*>(ring + first_warp * (kStages * At::kBytes));  // [team warp][8 NT][D]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float sum = l[nt];
+      float sum = l[nt].x + l[nt].y;
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       const int h = nt * 8 + g;
@@ -522,7 +543,7 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
           float y[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            y[i] = fmaf(NT == 1 ? o[k][i][e] + o[k][i][2 + e] : o[k][i][2 * nt + e], i & 1 ? 0.0625f : 1.0f, z);
+            y[i] = fmaf(NT == 1 ? o[k][i][e] + o[k][i][2 + e] : o[k][i][2 * nt + e], i & 1 ? 1048576.0f : 16777216.0f, z);
           *reinterpret_cast<float4*>(so + (team_warp * 8 * NT + h) * D + 32 * k + 4 * (2 * c4 + e)) = make_float4(y[0], y[1], y[2], y[3]);
         }
       }
