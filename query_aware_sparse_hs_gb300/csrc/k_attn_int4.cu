@@ -13,8 +13,11 @@
 //     because every token's group has its own scale;
 //   O[head][channel] += P . C  f16, over 16 tokens.
 // Heads as rows: S lies in a lane's registers as P is wanted, so nothing is exchanged
-// between lanes but the maxima.  Up to 8 heads leave half of the rows; P's second term
-// goes there, which makes the two terms one instruction.
+// between lanes but the maxima.  Up to 8 heads leave half of the rows: P's second term
+// goes there, which makes the two terms one instruction, and the q of the odd channels,
+// so that an operand is four registers of its own (an instruction for even channels
+// gives the first half of the rows, one for odd channels the second; with q in both
+// halves the copies of registers cost 5%).
 //
 // Codes become operands without a conversion.  A lane loads 8 of them as a word;
 // masking 4 bits out of either half of it gives two numbers n = c + 8:
@@ -372,14 +375,24 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
         else if (i % 2 == 0)
           load4(st_addr + k_at + i * (8 * At::kRow), kw);
         float s[kGroups][4], sz[4];
+        float odd[kGroups][4];
 #pragma unroll
         for (int k = 0; k < kGroups; ++k) {
           const uint32_t v = kw[D == 128 ? k : 2 * (i % 2) + k], v8 = v >> 8;
-          mma_bf16_0(s[k], qa[0][k][0], qa[NT - 1][k][0], qa[0][k][1], qa[NT - 1][k][1], v & 0x000f000fu, v8 & 0x000f000fu);
-          mma_bf16(s[k], qa[0][k][2], qa[NT - 1][k][2], qa[0][k][3], qa[NT - 1][k][3], v & 0x00f000f0u, v8 & 0x00f000f0u);
+          if constexpr (NT == 1) {
+            mma_bf16_0(s[k], qa[0][k][0], qa[0][k][2], qa[0][k][1], qa[0][k][3], v & 0x000f000fu, v8 & 0x000f000fu);
+            mma_bf16_0(odd[k], qa[0][k][0], qa[0][k][2], qa[0][k][1], qa[0][k][3], v & 0x00f000f0u, v8 & 0x00f000f0u);
+          } else {
+            mma_bf16_0(s[k], qa[0][k][0], qa[NT - 1][k][0], qa[0][k][1], qa[NT - 1][k][1], v & 0x000f000fu, v8 & 0x000f000fu);
+            mma_bf16(s[k], qa[0][k][2], qa[NT - 1][k][2], qa[0][k][3], qa[NT - 1][k][3], v & 0x00f000f0u, v8 & 0x00f000f0u);
+          }
         }
-        mma_bf16_0(sz, xa[0][0], xa[NT - 1][0], xa[0][1], xa[NT - 1][1], kr[i], kr[i]);
-        mma_bf16(sz, xa[0][2], xa[NT - 1][2], 0u, 0u, kr[i], kr[i]);
+        if constexpr (NT == 1) {
+          mma_bf16_0(sz, xa[0][0], xa[0][2], xa[0][1], 0u, kr[i], kr[i]);
+        } else {
+          mma_bf16_0(sz, xa[0][0], xa[NT - 1][0], xa[0][1], xa[NT - 1][1], kr[i], kr[i]);
+          mma_bf16(sz, xa[0][2], xa[NT - 1][2], 0u, 0u, kr[i], kr[i]);
+        }
         const uint8_t* rec = st + At::kRec + 32 * c4 + 128 * i;
         // the scales of tokens 8 i + 2 c4 and + 1
         const uint2 r0 = *reinterpret_cast<const uint2*>(rec), r1 = *reinterpret_cast<const uint2*>(rec + 16);
@@ -390,10 +403,15 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
         sc[3] = make_float2(upper(r0.y), upper(r1.y));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float2 sum = mul2(make_float2(s[0][2 * nt], s[0][2 * nt + 1]), sc[0]);
+          const auto of = [&](int k) {
+            const float2 even = make_float2(s[k][2 * nt], s[k][2 * nt + 1]);
+            return NT == 1 ? add2(even, make_float2(odd[k][2], odd[k][3])) : even;
+          };
+          const float2 affine = make_float2(sz[2 * nt], sz[2 * nt + 1]);
+          float2 sum = mul2(of(0), sc[0]);
 #pragma unroll
-          for (int k = 1; k < kGroups; ++k) sum = fma2(make_float2(s[k][2 * nt], s[k][2 * nt + 1]), sc[k], sum);
-          x[nt][i] = fma2(sum, both(f[nt]), make_float2(sz[2 * nt], sz[2 * nt + 1]));
+          for (int k = 1; k < kGroups; ++k) sum = fma2(of(k), sc[k], sum);
+          x[nt][i] = fma2(sum, both(f[nt]), NT == 1 ? add2(affine, make_float2(sz[2], sz[3])) : affine);
         }
       }
       if (live != 0xffffffffu) {
