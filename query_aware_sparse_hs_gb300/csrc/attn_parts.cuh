@@ -66,6 +66,72 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 }
 __device__ __forceinline__ float2 unpack_half2(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
 
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool live) {
+  const int n = live ? 8 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void load4(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void load4_trans(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+// d = a b
+__device__ __forceinline__ void mma_bf16_0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+// d += a b
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float lower(uint32_t two) { return __uint_as_float(two << 16); }        // of two bf16
+__device__ __forceinline__ float upper(uint32_t two) { return __uint_as_float(two & 0xffff0000u); }
+// Two fp32 numbers at a time.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 struct PartArgs {
   const void* q;
   const int32_t* sel;
@@ -423,7 +489,7 @@ struct TileRows {
   unsigned* err;
   int64_t num_pages;
   uint32_t B, u, u_stop, e_base, e1, e2, w_end, w_end1, w_end2;
-  int cnt, nb, L, lane, page, lim, page1, lim1, j2, ei, er, step_i, step_r;
+  int cnt, nb, L, lane, page, lim, page1, lim1, j0, j1, j2, ei, er, step_i, step_r;
 
   __device__ __forceinline__ uint32_t window_end(uint32_t from, uint32_t e) const {  // past the window's whole tiles
     return from + ((e + 32) * B - from) / kTile * kTile;
@@ -461,10 +527,10 @@ struct TileRows {
     u = static_cast<uint32_t>(run0) * kTile;
     u_stop = u + static_cast<uint32_t>(tiles) * kTile;
     e_base = u / B;
-    const int j0 = load_sel(u, e_base);
+    j0 = load_sel(u, e_base);
     w_end = window_end(u, e_base);
     e1 = w_end / B;
-    const int j1 = load_sel(w_end, e1);
+    j1 = load_sel(w_end, e1);
     w_end1 = window_end(w_end, e1);
     e2 = w_end1 / B;
     j2 = load_sel(w_end1, e2);
@@ -476,21 +542,29 @@ struct TileRows {
     step_i = kTile / static_cast<int>(B);
     step_r = kTile - step_i * static_cast<int>(B);
   }
-  // The lane's row of the next tile (0 where there is none), and its place in the
-  // request; false: no such token.
+  // The lane's row of the next tile (0 where there is none); false: no such token.
   __device__ __forceinline__ bool next(uint32_t& row) {
+    int place;
+    return next_at<false>(row, place);
+  }
+  // With its place in the request.
+  template <bool PLACE>
+  __device__ __forceinline__ bool next_at(uint32_t& row, int& place) {
     if (u >= w_end) {
       e_base = e1;
       w_end = w_end1;
       page = page1;
       lim = lim1;
+      if constexpr (PLACE) j0 = j1;
       e1 = e2;
       w_end1 = w_end2;
       load_page(j2, page1, lim1);
+      if constexpr (PLACE) j1 = j2;
       e2 = w_end2 / B;
       j2 = load_sel(w_end2, e2);
       w_end2 = window_end(w_end2, e2);
     }
+    if constexpr (PLACE) place = static_cast<int>(static_cast<uint32_t>(__shfl_sync(0xffffffffu, j0, ei - static_cast<int>(e_base))) * B) + er;
     const int pg = __shfl_sync(0xffffffffu, page, ei - static_cast<int>(e_base));
     const bool ok = er < __shfl_sync(0xffffffffu, lim, ei - static_cast<int>(e_base));
     row = ok ? static_cast<uint32_t>(pg) * B + er : 0u;
