@@ -883,7 +883,7 @@ hs_status hs_evict_tokens(const hs_attn_shape* shape, const hs_paged_kv* kv, con
   if (evict_ctas(v, params->budget) > INT32_MAX) return HS_ERR_UNSUPPORTED;
   Device d;
   if ((st = current_device(&d)) != HS_OK) return st;
-  return from_cuda(launch_evict(v, to, a, d.err, reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_evict(v, to, a, d.sms, d.err, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 hs_status hs_get_device_error(hs_stream_t stream, uint32_t* bits_opt) {

@@ -171,7 +171,7 @@ struct EvictArgs {
   int32_t budget, sink, recent;
 };
 int64_t evict_ctas(const KvView& kv, int budget);  // of its largest launch
-cudaError_t launch_evict(const KvView& kv, const KvView& dst, const EvictArgs& a, unsigned* err, cudaStream_t st);
+cudaError_t launch_evict(const KvView& kv, const KvView& dst, const EvictArgs& a, int sms, unsigned* err, cudaStream_t st);
 // The 4-bit format of rows and back; scales [rows][2][head_dim / 32] bf16.
 cudaError_t launch_quantize_int4(const void* src, bool src_f32, int64_t rows, int head_dim, uint8_t* codes, void* scales,
                                  cudaStream_t st);

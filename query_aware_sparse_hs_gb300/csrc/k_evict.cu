@@ -5,14 +5,20 @@
 //   evict_select_kernel  which tokens: the weight of the last that stays by a radix
 //                        search, then their indices in ascending order (kept)
 //   evict_gather_kernel  their rows, scales and weights to the new pages
+#include <cooperative_groups.h>
+
 #include "hs_internal.h"
+
+namespace cg = cooperative_groups;
 
 namespace hs {
 namespace {
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 256;
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kHeld = 16;             // keys of a thread that stay in registers
+constexpr int kMostCtas = 8;          // of a cluster
+constexpr int kBins = 2048;           // 11 bits of a key: 11, 11 and 10 are all of it
 
 __device__ __forceinline__ uint32_t weight_key(float w) {  // NaN last, -0 as 0
   if (isnan(w)) return 0u;
@@ -20,65 +26,113 @@ __device__ __forceinline__ uint32_t weight_key(float w) {  // NaN last, -0 as 0
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// CTA = (request, kv head).
-__global__ __launch_bounds__(kSelThreads) void evict_select_kernel(KvView kv, EvictArgs a, unsigned* err) {
-  __shared__ uint32_t s_hist[kBins];
-  __shared__ uint32_t s_found[2];  // digit, keys above it
-  __shared__ int s_above[kSelWarps], s_same[kSelWarps];
+// Cluster = (request, kv head).  The tokens that are chosen from are cut into a run for
+// each warp of the cluster's CTAs, whose keys stay in registers, 16 to a thread (more are
+// read again from the caches).  The key of the last token that stays is found from
+// histograms of 11 bits at a time, which every CTA sums over the cluster through
+// distributed shared memory; a bin that is taken whole ends the search.
+// Latency-bound: a few barriers of the cluster, over 2 x 4 heads of 3000 tokens and
+// 16 x 4 of 32768 alike.
+__global__ __launch_bounds__(kThreads) void evict_select_kernel(KvView kv, EvictArgs a, int ctas, unsigned* err) {
+  __shared__ uint32_t s_hist[3][kBins];  // one for each digit
+  __shared__ uint32_t s_sums[2][kWarps];
+  __shared__ uint32_t s_found[3][2];     // digit, keys above it, keys in it
+  __shared__ uint32_t s_size[3];
+  __shared__ int s_above[kWarps], s_same[kWarps], s_counts[2];
+  const cg::cluster_group cluster = cg::this_cluster();
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t pair = blockIdx.x;
+  const int64_t pair = blockIdx.x / ctas;
+  const int rank = static_cast<int>(blockIdx.x - pair * ctas);
   const int b = static_cast<int>(pair / kv.hkv);
   const int64_t most = static_cast<int64_t>(kv.max_blocks) * kv.block;
   int L = max(__ldg(kv.seq_lens + b), 0);
   if (L > most) {
-    if (tid == 0) set_error(err, HS_EBIT_BLOCK_RANGE);
+    if (tid == 0 && rank == 0) set_error(err, HS_EBIT_BLOCK_RANGE);
     L = static_cast<int>(most);
   }
   int32_t* kept = a.kept + pair * a.budget;
-  if (L <= a.budget) {
-    for (int i = tid; i < a.budget; i += kSelThreads) kept[i] = i < L ? i : -1;
+  const int all = ctas * kThreads, me = rank * kThreads + tid;
+  if (L <= a.budget) {  // (the same for the whole cluster)
+    for (int i = me; i < a.budget; i += all) kept[i] = i < L ? i : -1;
     return;
   }
-  const float* w = a.weights + pair * most;
   const int first = a.sink, last = L - a.recent;  // the tokens that are chosen from
   const int need = a.budget - a.sink - a.recent;
-  for (int i = tid; i < a.sink; i += kSelThreads) kept[i] = i;
-  for (int i = tid; i < a.recent; i += kSelThreads) kept[a.budget - a.recent + i] = last + i;
+  for (int i = me; i < a.sink; i += all) kept[i] = i;
+  for (int i = me; i < a.recent; i += all) kept[a.budget - a.recent + i] = last + i;
   if (need == 0) return;
-  // ---- the key of the last that stays, and how many of the same key do ----
+  const float* w = a.weights + pair * most;
+  // this warp's run, lane i every 32nd token of it
+  const int turns = ((last - first + ctas * kWarps - 1) / (ctas * kWarps) + 31) / 32;
+  const int64_t run0 = first + static_cast<int64_t>(rank * kWarps + warp) * turns * 32;
+  const int t0 = static_cast<int>(min(static_cast<int64_t>(last), run0)), n = min(turns * 32, last - t0);
+  uint32_t held[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) held[i] = 32 * i + lane < n ? weight_key(__ldg(w + t0 + 32 * i + lane)) : 0u;
+  // each(turn, key, there) over the run
+  const auto over = [&](auto&& each) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (32 * i < n) each(i, held[i], 32 * i + lane < n);
+    for (int i = kHeld; 32 * i < n; ++i) {
+      const bool there = 32 * i + lane < n;
+      each(i, there ? weight_key(__ldg(w + t0 + 32 * i + lane)) : 0u, there);
+    }
+  };
+  for (int i = tid; i < 3 * kBins; i += kThreads) (&s_hist[0][0])[i] = 0u;
+  __syncthreads();
+  // ---- the key of the last that stays: its digits, and how many of that key do ----
   uint32_t prefix = 0u, mask = 0u;
-  int rank = need;  // among the keys that share the prefix
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0u;
+  int rest = need;  // of the keys that share the digits so far
+#pragma unroll
+  for (int digit = 0; digit < 3; ++digit) {
+    const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
+    const uint32_t field = digit == 2 ? 1023u : 2047u;
+    over([&](int, uint32_t k, bool there) {
+      if (there && (k & mask) == prefix) atomicAdd(&s_hist[digit][(k >> shift) & field], 1u);
+    });
+    cluster.sync();
+    // bins 2047 - 2 tid and 2046 - 2 tid of the cluster, from the largest down
+    uint32_t h[2] = {0u, 0u};
+    for (int c = 0; c < ctas; ++c) {
+      const uint2 two = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&s_hist[digit][0], c) + kBins - 2 - 2 * tid);
+      h[0] += two.y;
+      h[1] += two.x;
+    }
+    uint32_t incl = h[0] + h[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_sums[digit & 1][warp] = incl;
     __syncthreads();
-    for (int t = first + tid; t < last; t += kSelThreads) {
-      const uint32_t k = weight_key(__ldg(w + t));
-      if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & 255u], 1u);
+    uint32_t before = lane < warp ? s_sums[digit & 1][lane] : 0u;
+    before = __reduce_add_sync(0xffffffffu, before);
+    uint32_t above = before + incl - h[0] - h[1];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (above < static_cast<uint32_t>(rest) && static_cast<uint32_t>(rest) <= above + h[i]) {
+        s_found[digit][0] = kBins - 1 - 2 * tid - i;
+        s_found[digit][1] = above;
+        s_size[digit] = h[i];
+      }
+      above += h[i];
     }
     __syncthreads();
-    if (tid == 0) {
-      uint32_t above = 0u;
-      int d = 255;
-      while (d > 0 && above + s_hist[d] < static_cast<uint32_t>(rank)) above += s_hist[d--];
-      s_found[0] = d;
-      s_found[1] = above;
-    }
-    __syncthreads();
-    prefix |= s_found[0] << shift;
-    mask |= 255u << shift;
-    rank -= static_cast<int>(s_found[1]);
+    prefix |= s_found[digit][0] << shift;
+    mask |= field << shift;
+    rest -= static_cast<int>(s_found[digit][1]);
+    if (s_size[digit] == static_cast<uint32_t>(rest)) break;  // all keys with these digits stay
   }
-  // ---- their indices: a warp takes a run of the tokens ----
-  const int run = ((last - first + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
-  const int t0 = min(last, first + warp * run), t1 = min(last, t0 + run);
+  // ---- the indices in order: keys whose digits are above, and the first `rest` of the same ----
   int above = 0, same = 0;
-  for (int t = t0 + lane; t < t1; t += 32) {
-    const uint32_t k = weight_key(__ldg(w + t));
-    above += k > prefix;
-    same += k == prefix;
-  }
+  over([&](int, uint32_t k, bool there) {
+    above += there && (k & mask) > prefix;
+    same += there && (k & mask) == prefix;
+  });
   above = __reduce_add_sync(0xffffffffu, above);
   same = __reduce_add_sync(0xffffffffu, same);
   if (lane == 0) {
@@ -86,26 +140,37 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(KvView kv, Ev
     s_same[warp] = same;
   }
   __syncthreads();
-  above = same = 0;
-  for (int i = 0; i < warp; ++i) {
-    above += s_above[i];
-    same += s_same[i];
+  const int wa = s_above[lane], ws = s_same[lane];
+  above = __reduce_add_sync(0xffffffffu, lane < warp ? wa : 0);  // of the warps before
+  same = __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0);
+  if (warp == 0) {
+    const int ca = __reduce_add_sync(0xffffffffu, wa), cs = __reduce_add_sync(0xffffffffu, ws);
+    if (lane == 0) {
+      s_counts[0] = ca;
+      s_counts[1] = cs;
+    }
   }
-  for (int t = t0; t < t1; t += 32) {
-    const uint32_t k = t + lane < t1 ? weight_key(__ldg(w + t + lane)) : 0u;
-    const bool is_above = t + lane < t1 && k > prefix, is_same = t + lane < t1 && k == prefix;
+  cluster.sync();
+  for (int c = 0; c < rank; ++c) {
+    const int* counts = cluster.map_shared_rank(s_counts, c);
+    above += counts[0];
+    same += counts[1];
+  }
+  over([&](int i, uint32_t k, bool there) {
+    const bool is_above = there && (k & mask) > prefix, is_same = there && (k & mask) == prefix;
     const unsigned ma = __ballot_sync(0xffffffffu, is_above), ms = __ballot_sync(0xffffffffu, is_same);
     const unsigned lower = (1u << lane) - 1u;
     const int same_here = same + __popc(ms & lower), above_here = above + __popc(ma & lower);
-    // of the equal ones the first `rank` stay
-    if (is_above || (is_same && same_here < rank)) kept[a.sink + above_here + min(same_here, rank)] = t + lane;
+    if (is_above || (is_same && same_here < rest)) kept[a.sink + above_here + min(same_here, rest)] = t0 + 32 * i + lane;
     above += __popc(ma);
     same += __popc(ms);
-  }
+  });
+  cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
 constexpr int kRows = 32;  // rows of a CTA
 constexpr int kGatherThreads = 128;
+constexpr int kFlight = 4;  // pieces of a thread on their way
 
 // CTA = kRows places of a (request, kv head)'s new pages.  row_bytes, scale_bytes: of a
 // row of K (or V).
@@ -143,15 +208,24 @@ __global__ __launch_bounds__(kGatherThreads) void evict_gather_kernel(KvView kv,
     s_to[tid] = to;
   }
   __syncthreads();
-  const int pieces = row_bytes / 16, each = pieces * 2;
-  for (int n = tid; n < kRows * each; n += kGatherThreads) {
-    const int r = n / each, x = n - r * each;
-    const bool v = x >= pieces;
-    const int at = (v ? x - pieces : x) * 16;
-    if (s_from[r] < 0) continue;
-    const char* src = static_cast<const char*>(v ? kv.v_pages : kv.k_pages) + s_from[r] * row_bytes + at;
-    char* to = static_cast<char*>(const_cast<void*>(v ? dst.v_pages : dst.k_pages)) + s_to[r] * row_bytes + at;
-    *reinterpret_cast<uint4*>(to) = __ldg(reinterpret_cast<const uint4*>(src));
+  const int pieces = row_bytes / 16, each = pieces * 2;  // (a power of two)
+  const int shift = 31 - __clz(each);
+  for (int n0 = tid; n0 < kRows * each; n0 += kFlight * kGatherThreads) {
+    uint4 x[kFlight];
+    char* to[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const int n = n0 + u * kGatherThreads, r = n >> shift, c = n - (r << shift);
+      to[u] = nullptr;
+      if (n >= kRows * each || s_from[r] < 0) continue;
+      const bool v = c >= pieces;
+      const int at = (v ? c - pieces : c) * 16;
+      x[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(v ? kv.v_pages : kv.k_pages) + s_from[r] * row_bytes + at));
+      to[u] = static_cast<char*>(const_cast<void*>(v ? dst.v_pages : dst.k_pages)) + s_to[r] * row_bytes + at;
+    }
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u)
+      if (to[u]) *reinterpret_cast<uint4*>(to[u]) = x[u];
   }
   const int words = scale_bytes / 4;
   for (int n = tid; n < kRows * words * 2; n += kGatherThreads) {
@@ -165,15 +239,36 @@ __global__ __launch_bounds__(kGatherThreads) void evict_gather_kernel(KvView kv,
   }
 }
 
+cudaError_t launch_select(const KvView& kv, const EvictArgs& a, int sms, unsigned* err, cudaStream_t st) {
+  const int64_t pairs = static_cast<int64_t>(kv.batch) * kv.hkv, tokens = static_cast<int64_t>(kv.max_blocks) * kv.block;
+  // as many CTAs to a pair as keep its longest request's keys in registers, four to a
+  // thread where there is room, and as all pairs leave room for at once (one on an SM)
+  int ctas = 1;
+  while (ctas < kMostCtas && tokens > static_cast<int64_t>(ctas) * kThreads * 4 && pairs * 2 * ctas <= sms) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(pairs * ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel, kv, a, ctas, err);
+}
+
 }  // namespace
 
 int64_t evict_ctas(const KvView& kv, int budget) {
   return static_cast<int64_t>(kv.batch) * kv.hkv * ceil_div(budget, kRows);
 }
 
-cudaError_t launch_evict(const KvView& kv, const KvView& dst, const EvictArgs& a, unsigned* err, cudaStream_t st) {
+cudaError_t launch_evict(const KvView& kv, const KvView& dst, const EvictArgs& a, int sms, unsigned* err, cudaStream_t st) {
   if (kv.batch == 0) return cudaSuccess;
-  cudaError_t e = launch_pdl(evict_select_kernel, dim3(kv.batch * kv.hkv), dim3(kSelThreads), 0, st, kv, a, err);
+  cudaError_t e = launch_select(kv, a, sms, err, st);
   if (e != cudaSuccess) return e;
   const int elem2 = kv.kv_dtype == HS_KV_F32 ? 8 : kv.kv_dtype == HS_KV_BF16 ? 4 : kv.kv_dtype == HS_KV_INT4_G32 ? 1 : 2;
   const int scale_bytes = kv.kv_dtype >= HS_KV_FP8E4M3_G32 ? kv.head_dim / kQuantGroup * 4 : 0;
