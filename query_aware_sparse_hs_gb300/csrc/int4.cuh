@@ -18,7 +18,7 @@ namespace int4 {
 
 constexpr float kMost = 8.507059173023462e37f;        // 2^126: values beyond it are held as it
 constexpr float kLeastScale = 1.2037062152420224e-35f;  // 2^-116: smaller ranges are held as their centre
-constexpr float kRound = 12582920.0f;                 // 1.5 2^23 + 8: adding it leaves round(c) + 8 in the low bits
+constexpr float kRound = 12582920.0f;  // 1.5 2^23 + 8: c plus it is, as bits, round(c) + 8 more than 0x4b400000
 
 __host__ __device__ constexpr int row_bytes(int head_dim) { return head_dim / 2; }
 // scales and centres of a row, in 16-bit words
@@ -28,15 +28,6 @@ __host__ __device__ constexpr int record(int head_dim) { return 2 * (head_dim / 
 // an infinite hi, which no other value leaves).
 struct Range {
   float lo, hi;
-  __device__ __forceinline__ void clear() {
-    lo = INFINITY;
-    hi = -INFINITY;
-  }
-  __device__ __forceinline__ void add(float x) {
-    const float y = fminf(fmaxf(x, -kMost), kMost);  // NaN: -2^126, but then the group's scale is NaN
-    lo = fminf(lo, y);
-    hi = fmaxf(hi, x == x ? y : INFINITY);
-  }
   __device__ __forceinline__ void join(const Range& o) {
     lo = fminf(lo, o.lo);
     hi = fmaxf(hi, o.hi);
@@ -46,6 +37,29 @@ struct Range {
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, mask));
   }
 };
+__device__ __forceinline__ Range no_values() { return Range{INFINITY, -INFINITY}; }
+// Of 8 values, of which those beyond 2^126 become it.
+__device__ __forceinline__ Range range_of(float (&x)[8]) {
+  Range r = no_values();
+  float odd = 0.0f;  // 0 times a value is 0 unless that is infinite or not a number
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    r.lo = fminf(r.lo, x[i]);
+    r.hi = fmaxf(r.hi, x[i]);
+    odd = fmaf(x[i], 0.0f, odd);
+  }
+  if (!(odd == 0.0f && r.hi <= kMost && r.lo >= -kMost)) {
+    r = no_values();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool nan = isnan(x[i]);
+      x[i] = fminf(fmaxf(x[i], -kMost), kMost);
+      r.lo = fminf(r.lo, x[i]);
+      r.hi = fmaxf(r.hi, nan ? INFINITY : x[i]);
+    }
+  }
+  return r;
+}
 
 struct Scale {
   float s, z, inv;  // inv: 1 / s, 0 for a scale of 0
@@ -69,12 +83,12 @@ __device__ __forceinline__ uint16_t bf16_bits(float exact) { return static_cast<
 // values lie halfway between two codes often enough (times 1 / s alone, 2 of 1000 codes
 // of random bf16 values differed from the definition's).
 __device__ __forceinline__ uint32_t encode8(const float (&x)[8], const Scale& q) {
-  uint32_t w = 0u;
+  uint32_t w = 0u - 0x3f400000u;  // what the upper bits of 8 terms of kRound add up to
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float t = fminf(fmaxf(x[i], -kMost), kMost) - q.z, a = t * q.inv;
-    const float c = fminf(fmaxf(fmaf(fmaf(-a, q.s, t), q.inv, a), -8.0f), 7.0f);
-    w |= (__float_as_uint(c + kRound) & 15u) << (4 * i);
+    const float t = x[i] - q.z, a = t * q.inv;
+    const float c = fmaf(fmaf(-a, q.s, t), q.inv, a);  // from -8 to 7 by the choice of z and s
+    w += __float_as_uint(c + kRound) << (4 * i);
   }
   return w;
 }

@@ -386,15 +386,10 @@ template <int D, bool INTERLEAVED>
 __device__ __forceinline__ void store_int4(void* pages, float* scales, int64_t row, int s, const Slot& t, int rotary, bool live,
                                            unsigned* part, float (&u)[8], float (&w)[8]) {
   constexpr int kGroups = D / kQuantGroup;
-  int4::Range ra, rb;  // of the vectors' groups
-  ra.clear();
-  rb.clear();
+  int4::Range ra = int4::no_values(), rb = ra;  // of the vectors' groups
   if (live) {
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      ra.add(u[c]);
-      rb.add(w[c]);
-    }
+    ra = int4::range_of(u);
+    rb = int4::range_of(w);
   }
   const bool split = !INTERLEAVED && t.rotated;
   const bool neighbours = INTERLEAVED || rotary % 64 == 0;

@@ -395,24 +395,95 @@ cudaError_t launch_block(const KvView& kv, int first_block, int nblocks, void* s
 
 // ---- 4-bit codes ----
 // Every row has scales and centres of its own, so each value is formed in fp32
-// (z + s c) before it is compared.  A lane owns 8 neighbouring channels, a warp a
-// run of blocks; the row slots of a warp are joined at a block's end.
+// (z + s c) before it is compared.  A lane owns 8 neighbouring channels, which are of
+// one group, a warp a run of blocks; a block's row slots are joined by halving the
+// channels.  A code becomes a number by masking its bits where they are (8 ors and masks,
+// one shift: 2^23 + 16^i n), one addition and one fused multiply of two at a time, its
+// scale being s / 16^i.
+// What bounds it: instructions, two thirds of them comparisons, masks and shifts, whose
+// pipe is busy for 0.65 of the time.  32 requests x 4 heads of 4K to 64K tokens, 128
+// channels: 152 us with 64-token pages (0.41 of the copy rate), 175 with 16-token pages
+// (0.45).  (16 channels to a lane: 148 and 190 us; additions and multiplies one at a time
+// 155 and 177; rows loaded into registers instead of the ring 162 and 201.)
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy8_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma_pair(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+// 2^23 + n 16^i: the code's bits where they are, below the exponent of 2^23 (`magic`, in
+// a register).
+template <uint32_t MASK>
+__device__ __forceinline__ float number(uint32_t v, uint32_t magic) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(v), "n"(MASK), "r"(magic));  // (v & MASK) | magic
+  return __uint_as_float(d);
+}
+// 8 channels of a row as they lie in memory.
+struct Codes8 {
+  uint32_t w;
+  uint32_t s, z;  // in the low half
+  // What they stand for.
+  __device__ __forceinline__ void get(float (&x)[8], uint32_t magic) const {
+    const float f = __uint_as_float(s << 16), c = __uint_as_float(z << 16);
+    const float f1 = f * 0.0625f, f2 = f * 0.00390625f, f3 = f * 0.000244140625f, f4 = f * 0.0000152587890625f;
+    constexpr float k = 8388608.0f;  // 2^23
+    const float2 centre = make_float2(c, c);
+    const uint32_t lo = w, up = w >> 20;
+    const float2 a = add_pair(make_float2(number<0xfu>(lo, magic), number<0xf0u>(lo, magic)), make_float2(-k - 8.0f, -k - 128.0f));
+    const float2 b = add_pair(make_float2(number<0xf00u>(lo, magic), number<0xf000u>(lo, magic)), make_float2(-k - 2048.0f, -k - 32768.0f));
+    const float2 d = add_pair(make_float2(number<0xf0000u>(lo, magic), number<0xfu>(up, magic)), make_float2(-k - 524288.0f, -k - 8.0f));
+    const float2 e = add_pair(make_float2(number<0xf0u>(up, magic), number<0xf00u>(up, magic)), make_float2(-k - 128.0f, -k - 2048.0f));
+    const float2 va = fma_pair(a, make_float2(f, f1), centre), vb = fma_pair(b, make_float2(f2, f3), centre);
+    const float2 vd = fma_pair(d, make_float2(f4, f), centre), ve = fma_pair(e, make_float2(f1, f2), centre);
+    x[0] = va.x; x[1] = va.y; x[2] = vb.x; x[3] = vb.y;
+    x[4] = vd.x; x[5] = vd.y; x[6] = ve.x; x[7] = ve.y;
+  }
+};
+
+// A warp's rows go through its ring in shared memory in units of up to 16 rows of a
+// block, kUnits - 1 of them on their way.
+constexpr int kUnitRows = 16, kUnits = 6;
 template <int D>
-__global__ __launch_bounds__(kWarps * 32) void summaries_int4_kernel(KvView kv, int first_block, void* smin, void* smax,
-                                                                     unsigned* err) {
-  constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes of a row, rows of one warp load
-  constexpr int kRows = 4;                    // loads in flight
+struct Unit {
+  static constexpr int kCodes = kUnitRows * int4::row_bytes(D), kBytes = kCodes + kUnitRows * int4::record(D) * 2;
+};
+
+template <int D>
+__global__ __launch_bounds__(kWarps * 32, 3) void summaries_int4_kernel(KvView kv, int first_block, void* smin, void* smax,
+                                                                        unsigned* err) {
+  constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes of a row, rows of a warp at a time
+  constexpr int kRecord = int4::record(D) * 2;
+  extern __shared__ __align__(128) uint8_t ring[];
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rs = lane / LPR, d0 = lane % LPR * 8;
   const int B = kv.block;
-  BlockRun run(kv, first_block, static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5),
-               static_cast<int64_t>(gridDim.x) * kWarps, lane);
+  uint8_t* mine = ring + warp * (kUnits * Unit<D>::kBytes);
+  const uint32_t mine_addr = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+  BlockRun run(kv, first_block, static_cast<int64_t>(blockIdx.x) * kWarps + warp, static_cast<int64_t>(gridDim.x) * kWarps, lane);
+  uint32_t magic = 0x4b000000u;
+  asm volatile("" : "+r"(magic));  // (a register: the mask is the instruction's constant)
   while (run.more()) {
+    // ---- up to 32 blocks of one pair ----
     const int n = run.count(), j = run.j;
     const int64_t pair = run.pair;
-    const int L = __ldg(kv.seq_lens + run.req);
+    const int tail = __ldg(kv.seq_lens + run.req) - j * B;  // tokens from the first of the blocks on
     int my_page = -1;
     if (lane < n) {
       my_page = __ldg(kv.page_table + pair * kv.max_blocks + j + lane);
@@ -421,57 +492,125 @@ __global__ __launch_bounds__(kWarps * 32) void summaries_int4_kernel(KvView kv, 
         my_page = -1;
       }
     }
-    for (unsigned left = __ballot_sync(0xffffffffu, my_page >= 0); left; left &= left - 1) {
-      const int i = __ffs(left) - 1;
-      const int64_t row0 = static_cast<int64_t>(__shfl_sync(0xffffffffu, my_page, i)) * B;
-      const int valid = min(B, L - (j + i) * B);
-      float mn[8], mx[8];
+    // a place in the blocks that are there: block i (32: past them), row t
+    struct Place {
+      int i, t;
+      unsigned left;  // blocks from i on
+      __device__ __forceinline__ void block() { i = left ? __ffs(left) - 1 : 32; }
+      __device__ __forceinline__ bool next(int valid) {  // true: the block ends
+        t += kUnitRows;
+        if (t < valid) return false;
+        t = 0;
+        left &= left - 1;
+        block();
+        return true;
+      }
+    };
+    Place in{0, 0, __ballot_sync(0xffffffffu, my_page >= 0)};
+    in.block();
+    Place out = in;
+    const auto valid_of = [&](int i) { return min(B, tail - i * B); };
+    int unit_in = 0, unit_out = 0;
+    const auto issue = [&]() {  // the next unit's rows, which lie together
+      if (in.i < 32) {
+        const int64_t row = static_cast<int64_t>(__shfl_sync(0xffffffffu, my_page, in.i)) * B + in.t;
+        const int valid = valid_of(in.i), bytes = min(valid - in.t, kUnitRows);
+        const uint8_t* codes = static_cast<const uint8_t*>(kv.k_pages) + row * int4::row_bytes(D);
+        const uint8_t* recs = reinterpret_cast<const uint8_t*>(kv.k_scales) + row * kRecord;
+        const uint32_t to = mine_addr + unit_in * Unit<D>::kBytes;
+#pragma unroll
+        for (int x = 0; x < Unit<D>::kCodes; x += 512)
+          if (x + lane * 16 < bytes * int4::row_bytes(D)) copy16_async(to + x + lane * 16, codes + x + lane * 16);
+        if (lane * kRecord < kUnitRows * kRecord && lane < bytes) {
+          if constexpr (kRecord == 16)
+            copy16_async(to + Unit<D>::kCodes + lane * 16, recs + lane * 16);
+          else
+            copy8_async(to + Unit<D>::kCodes + lane * 8, recs + lane * 8);
+        }
+        in.next(valid);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      unit_in = unit_in + 1 == kUnits ? 0 : unit_in + 1;
+    };
+#pragma unroll
+    for (int u = 0; u < kUnits - 1; ++u) issue();
+    float mn[8], mx[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      mn[c] = INFINITY;
+      mx[c] = -INFINITY;
+    }
+    while (out.i < 32) {
+      __syncwarp();  // the unit about to be filled has been read by every lane
+      issue();
+      asm volatile("cp.async.wait_group %0;" ::"n"(kUnits - 1) : "memory");
+      __syncwarp();
+      const uint8_t* unit = mine + unit_out * Unit<D>::kBytes;
+      unit_out = unit_out + 1 == kUnits ? 0 : unit_out + 1;
+      const int valid = valid_of(out.i), rows = min(valid - out.t, kUnitRows);
+      const auto get = [&](int t, float (&x)[8]) {
+        const int r = min(t + rs, rows - 1);  // (a repeated row changes nothing)
+        Codes8 c;
+        c.w = *reinterpret_cast<const uint32_t*>(unit + r * int4::row_bytes(D) + d0 / 2);
+        const uint16_t* rec = reinterpret_cast<const uint16_t*>(unit + Unit<D>::kCodes + r * kRecord) + d0 / kQuantGroup;
+        c.s = rec[0];
+        c.z = rec[D / kQuantGroup];
+        c.get(x, magic);
+      };
+#pragma unroll
+      for (int t = 0; t < kUnitRows; t += 2 * RPL) {
+        if (t > 0 && t >= rows) break;
+        float x[8], y[8];
+        get(t, x);
+        get(t + RPL, y);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          mn[c] = fminf(mn[c], fminf(x[c], y[c]));
+          mx[c] = fmaxf(mx[c], fmaxf(x[c], y[c]));
+        }
+      }
+      const int now = out.i;
+      if (!out.next(valid)) continue;
+      // the row slots joined: a lane keeps half of its channels each time
+      int at = d0;
+#pragma unroll
+      for (int off = LPR, w = 4; off < 32; off <<= 1, w >>= 1) {
+        const bool upper = lane & off;
+#pragma unroll
+        for (int c = 0; c < w; ++c) {
+          const float a = upper ? mn[c + w] : mn[c], b = upper ? mx[c + w] : mx[c];
+          const float oa = __shfl_xor_sync(0xffffffffu, upper ? mn[c] : mn[c + w], off);
+          const float ob = __shfl_xor_sync(0xffffffffu, upper ? mx[c] : mx[c + w], off);
+          mn[c] = fminf(a, oa);
+          mx[c] = fmaxf(b, ob);
+        }
+        at += upper ? w : 0;
+      }
+      constexpr int kKept = 8 / RPL;
+      const int64_t o = (pair * kv.max_blocks + j + now) * D + at;
+      __nv_bfloat162 lo[kKept / 2], hi[kKept / 2];
+#pragma unroll
+      for (int c = 0; c < kKept / 2; ++c) {  // outward: the stored box still contains every dequantised key
+        lo[c].x = __float2bfloat16_rd(mn[2 * c]);
+        lo[c].y = __float2bfloat16_rd(mn[2 * c + 1]);
+        hi[c].x = __float2bfloat16_ru(mx[2 * c]);
+        hi[c].y = __float2bfloat16_ru(mx[2 * c + 1]);
+      }
+      if constexpr (kKept == 4) {
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(smin) + o) = *reinterpret_cast<const uint2*>(lo);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(smax) + o) = *reinterpret_cast<const uint2*>(hi);
+      } else {
+        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(smin) + o) = *reinterpret_cast<const uint32_t*>(lo);
+        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(smax) + o) = *reinterpret_cast<const uint32_t*>(hi);
+      }
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         mn[c] = INFINITY;
         mx[c] = -INFINITY;
       }
-      for (int t0 = 0; t0 < valid; t0 += kRows * RPL) {
-        uint32_t raw[kRows];
-        float2 q[kRows];
-#pragma unroll
-        for (int u = 0; u < kRows; ++u) {  // clamp: a repeated valid row changes nothing
-          const int64_t row = row0 + min(t0 + u * RPL + rs, valid - 1);
-          raw[u] = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(kv.k_pages) + row * int4::row_bytes(D) + d0 / 2));
-          q[u] = int4::load_scale(kv.k_scales, row, D, d0 / kQuantGroup);
-        }
-#pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-          float x[8];
-          int4::decode8(raw[u], q[u].x, q[u].y, x);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            mn[c] = fminf(mn[c], x[c]);
-            mx[c] = fmaxf(mx[c], x[c]);
-          }
-        }
-      }
-#pragma unroll
-      for (int off = LPR; off < 32; off <<= 1)
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          mn[c] = fminf(mn[c], __shfl_xor_sync(0xffffffffu, mn[c], off));
-          mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], off));
-        }
-      if (rs == 0) {
-        const int64_t o = (pair * kv.max_blocks + j + i) * D + d0;
-        __nv_bfloat162 lo[4], hi[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {  // outward: the stored box still contains every dequantised key
-          lo[c].x = __float2bfloat16_rd(mn[2 * c]);
-          lo[c].y = __float2bfloat16_rd(mn[2 * c + 1]);
-          hi[c].x = __float2bfloat16_ru(mx[2 * c]);
-          hi[c].y = __float2bfloat16_ru(mx[2 * c + 1]);
-        }
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(smin) + o) = *reinterpret_cast<const uint4*>(lo);
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(smax) + o) = *reinterpret_cast<const uint4*>(hi);
-      }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
     run.on(n);
   }
 }
@@ -481,9 +620,11 @@ cudaError_t launch_int4(const KvView& kv, int first_block, int nblocks, void* sm
                         cudaStream_t st) {
   // a warp for each block at most
   const int64_t most = (static_cast<int64_t>(kv.batch) * kv.hkv * nblocks + kWarps - 1) / kWarps;
-  const int resident = sms * 4;
+  const int resident = sms * 3;
   const unsigned grid = static_cast<unsigned>(most < resident ? most : resident);
-  return launch_pdl(summaries_int4_kernel<D>, dim3(grid), dim3(kWarps * 32), 0, st, kv, first_block, smin, smax, err);
+  constexpr size_t smem = static_cast<size_t>(kWarps) * kUnits * Unit<D>::kBytes;
+  if (cudaError_t e = allow_dynamic_smem(summaries_int4_kernel<D>, smem); e != cudaSuccess) return e;
+  return launch_pdl(summaries_int4_kernel<D>, dim3(grid), dim3(kWarps * 32), smem, st, kv, first_block, smin, smax, err);
 }
 
 template <int D>
