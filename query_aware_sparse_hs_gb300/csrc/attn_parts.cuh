@@ -483,64 +483,58 @@ __global__ __launch_bounds__(TEAMS * kTeamWarps * 32) void merge_parts_kernel(Kv
 // lane, the pages one window ahead of the rows and the selection two, so that neither
 // load is waited for.  A window holds the entries from that of its first tile on; a
 // tile that does not fit opens the next.  All 32 lanes call everything.
+// `Args` has sel and capacity.  (What a window that opens needs, and little else does, is
+// worked out again then: registers are short where this is used.)
+template <typename Args>
 struct TileRows {
-  const int32_t* sel;
-  const int32_t* table;
+  const KvView& kv;
+  const Args& a;
   unsigned* err;
-  int64_t num_pages;
-  uint32_t B, u, u_stop, e_base, e1, e2, w_end, w_end1, w_end2;
-  int cnt, nb, L, lane, page, lim, page1, lim1, j0, j1, j2, ei, er, step_i, step_r;
+  int64_t pair;
+  uint32_t u, u_stop, w_end, e_base;  // the next tile's first token, the run's end, the window's end and first entry
+  int lane, cnt, L, page, lim, page1, lim1, j0, j1, j2, ei, er, step_i, step_r;
 
   __device__ __forceinline__ uint32_t window_end(uint32_t from, uint32_t e) const {  // past the window's whole tiles
-    return from + ((e + 32) * B - from) / kTile * kTile;
+    return from + ((e + 32) * kv.block - from) / kTile * kTile;
   }
   __device__ __forceinline__ int load_sel(uint32_t from, uint32_t e) const {  // INT_MIN: no such entry (one that is so is out of range anyway)
-    return from < u_stop && e + lane < static_cast<uint32_t>(cnt) ? max(__ldg(sel + e + lane), INT_MIN + 1) : INT_MIN;
+    return from < u_stop && e + lane < static_cast<uint32_t>(cnt) ? max(__ldg(a.sel + pair * a.capacity + e + lane), INT_MIN + 1) : INT_MIN;
   }
   __device__ __forceinline__ void load_page(int j, int& pg, int& rows) const {  // rows: valid rows of the page
     pg = rows = 0;
     if (j == INT_MIN) return;
-    if (j < 0 || j >= nb) {
+    if (j < 0 || j >= min(ceil_div(max(L, 0), kv.block), kv.max_blocks)) {
       set_error(err, HS_EBIT_BLOCK_RANGE);
       return;
     }
-    pg = __ldg(table + j);
-    if (pg < 0 || pg >= num_pages) {
+    pg = __ldg(kv.page_table + pair * kv.max_blocks + j);
+    if (pg < 0 || pg >= kv.num_pages) {
       set_error(err, HS_EBIT_PAGE_RANGE);
       pg = 0;
       return;
     }
-    rows = min(static_cast<int>(B), L - j * static_cast<int>(B));
+    rows = min(kv.block, L - j * kv.block);
   }
-  // Tiles [run0, run0 + tiles) of the first `count` selected blocks; L tokens in the request.
-  __device__ __forceinline__ void start(const KvView& kv, const int32_t* selection, const int32_t* pages, int count, int tokens,
-                                        int run0, int tiles, int this_lane, unsigned* error) {
-    sel = selection;
-    table = pages;
-    err = error;
-    num_pages = kv.num_pages;
-    B = kv.block;
-    cnt = count;
-    L = tokens;
-    lane = this_lane;
-    nb = min(ceil_div(max(L, 0), kv.block), kv.max_blocks);
+  // Tiles [run0, run0 + tiles) of the first `count` selected blocks; `tokens` in the request.
+  __device__ __forceinline__ TileRows(const KvView& view, const Args& args, int this_pair, int count, int tokens, int run0, int tiles,
+                                      int this_lane, unsigned* error)
+      : kv(view), a(args), err(error), pair(this_pair), lane(this_lane), cnt(count), L(tokens) {
+    const uint32_t B = kv.block;
     u = static_cast<uint32_t>(run0) * kTile;
     u_stop = u + static_cast<uint32_t>(tiles) * kTile;
     e_base = u / B;
     j0 = load_sel(u, e_base);
     w_end = window_end(u, e_base);
-    e1 = w_end / B;
+    const uint32_t e1 = w_end / B;
     j1 = load_sel(w_end, e1);
-    w_end1 = window_end(w_end, e1);
-    e2 = w_end1 / B;
-    j2 = load_sel(w_end1, e2);
-    w_end2 = window_end(w_end1, e2);
+    const uint32_t w_end1 = window_end(w_end, e1);
+    j2 = load_sel(w_end1, w_end1 / B);
     load_page(j0, page, lim);
     load_page(j1, page1, lim1);
     ei = static_cast<int>((u + lane) / B);
     er = static_cast<int>(u + lane - ei * B);
-    step_i = kTile / static_cast<int>(B);
-    step_r = kTile - step_i * static_cast<int>(B);
+    step_i = kTile / kv.block;
+    step_r = kTile - step_i * kv.block;
   }
   // The lane's row of the next tile (0 where there is none); false: no such token.
   __device__ __forceinline__ bool next(uint32_t& row) {
@@ -550,29 +544,28 @@ struct TileRows {
   // With its place in the request.
   template <bool PLACE>
   __device__ __forceinline__ bool next_at(uint32_t& row, int& place) {
-    if (u >= w_end) {
-      e_base = e1;
-      w_end = w_end1;
+    if (u >= w_end) {  // the next window, whose pages are here; the pages of the one after it, whose entries are
+      const uint32_t B = kv.block;
+      e_base = w_end / B;
+      w_end = window_end(w_end, e_base);
       page = page1;
       lim = lim1;
       if constexpr (PLACE) j0 = j1;
-      e1 = e2;
-      w_end1 = w_end2;
       load_page(j2, page1, lim1);
       if constexpr (PLACE) j1 = j2;
-      e2 = w_end2 / B;
-      j2 = load_sel(w_end2, e2);
-      w_end2 = window_end(w_end2, e2);
+      const uint32_t w_end1 = window_end(w_end, w_end / B);
+      j2 = load_sel(w_end1, w_end1 / B);
     }
-    if constexpr (PLACE) place = static_cast<int>(static_cast<uint32_t>(__shfl_sync(0xffffffffu, j0, ei - static_cast<int>(e_base))) * B) + er;
-    const int pg = __shfl_sync(0xffffffffu, page, ei - static_cast<int>(e_base));
-    const bool ok = er < __shfl_sync(0xffffffffu, lim, ei - static_cast<int>(e_base));
-    row = ok ? static_cast<uint32_t>(pg) * B + er : 0u;
+    const int e = ei - static_cast<int>(e_base);
+    if constexpr (PLACE) place = static_cast<int>(static_cast<uint32_t>(__shfl_sync(0xffffffffu, j0, e)) * static_cast<uint32_t>(kv.block)) + er;
+    const int pg = __shfl_sync(0xffffffffu, page, e);
+    const bool ok = er < __shfl_sync(0xffffffffu, lim, e);
+    row = ok ? static_cast<uint32_t>(pg) * static_cast<uint32_t>(kv.block) + er : 0u;
     u += kTile;
     ei += step_i;
     er += step_r;
-    if (er >= static_cast<int>(B)) {
-      er -= B;
+    if (er >= kv.block) {
+      er -= kv.block;
       ++ei;
     }
     return ok;

@@ -34,7 +34,7 @@
 // bf16 terms of the sums, two of P.
 //
 // Precision: q is exact (bf16, times a power of two, which takes entries up to 2^90), S
-// and all sums fp32.  P times s, in units of 2^-14 of the reference (the largest power of
+// and all sums fp32.  P times s, in units of 2^-13 of the reference (the largest power of
 // two met of s and z / 8), as two f16 terms: 22 bits, absolutely 2^-25 of the units; P
 // times z as two bf16 terms, 16 bits.
 #include <limits.h>
@@ -50,6 +50,12 @@ namespace {
 using namespace parts;
 
 constexpr int kStages = 3;  // tiles in a warp's ring
+// Logits may pass the running maximum by so much (log2 units) before the state is
+// rescaled, which takes 68 products: with runs of a hundred tiles every fourth tile
+// raises a maximum, one of twenty by more than this.  P times s is in units of 2^-13 of
+// the reference then, 2^15 at most.
+constexpr float kMargin = 2.0f;
+constexpr int kUnit4 = 13;
 __host__ __device__ constexpr int teams_of(int, int nt) { return nt == 1 ? 3 : 2; }
 
 template <int D>
@@ -146,7 +152,6 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
     const int pair_tiles = tiles_of(kv, cnt), each = pair_tiles / part.count, more = pair_tiles - each * part.count;
     const int seg0 = part.index * each + min(part.index, more), seg_tiles = each + (part.index < more ? 1 : 0);
     const int b = part.pair / kv.hkv, kvh = part.pair - b * kv.hkv;
-    const int L = kv.seq_lens[b];
     // the query's loads go out ahead of the rows'
     uint4 q_raw[NT][kGroups];
 #pragma unroll
@@ -161,9 +166,7 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
     // The warp's tiles: a run of the part.
     const int run0 = seg0 + seg_tiles * team_warp / team.warps;
     const int tiles = seg0 + seg_tiles * (team_warp + 1) / team.warps - run0;
-    TileRows rows;
-    rows.start(kv, a.sel + static_cast<int64_t>(part.pair) * a.capacity, kv.page_table + static_cast<int64_t>(part.pair) * kv.max_blocks, cnt,
-               L, run0, tiles, lane, err);
+    TileRows<PartArgs> rows(kv, a, part.pair, cnt, kv.seq_lens[b], run0, tiles, lane, err);
     if constexpr (D == 64) {  // the empty halves of the records
 #pragma unroll
       for (int i = 0; i < kStages; ++i) {
@@ -366,7 +369,7 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         mn[nt] = fmaxf(m[nt], top);
-        raised |= mn[nt] > m[nt];
+        raised |= mn[nt] > m[nt] + kMargin;
       }
       uint32_t vmax;
       {
@@ -399,7 +402,7 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
             for (int i = 0; i < 4; ++i) o[k][i][e] *= y;
         }
       }
-      const float unit = unit_over(vref);
+      const float unit = unit_over(vref) * (1.0f / (1 << (kUnit - kUnit4)));
 
       // ---- P, and O += P C, 16 tokens at a time ----
       uint32_t zr[4];  // records: scales in the first columns, centres behind them
@@ -496,7 +499,7 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
           float y[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            y[i] = fmaf(NT == 1 ? o[k][i][e] + o[k][i][2 + e] : o[k][i][2 * nt + e], i & 1 ? 1048576.0f : 16777216.0f, z);
+            y[i] = fmaf(NT == 1 ? o[k][i][e] + o[k][i][2 + e] : o[k][i][2 * nt + e], i & 1 ? 1048576.0f : 16777216.0f, z) * static_cast<float>(1 << (kUnit - kUnit4));
           *reinterpret_cast<float4*>(so + (team_warp * 8 * NT + h) * D + 32 * k + 4 * (2 * c4 + e)) = make_float4(y[0], y[1], y[2], y[3]);
         }
       }

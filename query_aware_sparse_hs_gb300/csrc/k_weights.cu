@@ -121,9 +121,7 @@ __global__ __launch_bounds__(Row<D, KIND>::kWarps * 32, 1) void weights_kernel(K
     const int cnt = blocks_of(a, run.pair);
     const int tiles = run.here(kv, cnt);
     const int b = run.pair / kv.hkv, kvh = run.pair - b * kv.hkv;
-    TileRows rows;
-    rows.start(kv, a.sel + static_cast<int64_t>(run.pair) * a.capacity, kv.page_table + static_cast<int64_t>(run.pair) * kv.max_blocks, cnt,
-               __ldg(kv.seq_lens + b), run.first, tiles, lane, err);
+    TileRows<WeightsArgs> rows(kv, a, run.pair, cnt, __ldg(kv.seq_lens + b), run.first, tiles, lane, err);
     float* out = a.weights + static_cast<int64_t>(run.pair) * kv.max_blocks * kv.block;
     int stage_in = 0, place_in[kStages];
 #pragma unroll
@@ -382,9 +380,7 @@ __global__ __launch_bounds__(kWarpsF32 * 32) void weights_f32_kernel(KvView kv, 
   while (run.left > 0) {
     const int cnt = blocks_of(a, run.pair), tiles = run.here(kv, cnt);
     const int b = run.pair / kv.hkv, kvh = run.pair - b * kv.hkv;
-    TileRows rows;
-    rows.start(kv, a.sel + static_cast<int64_t>(run.pair) * a.capacity, kv.page_table + static_cast<int64_t>(run.pair) * kv.max_blocks, cnt,
-               __ldg(kv.seq_lens + b), run.first, tiles, lane, err);
+    TileRows<WeightsArgs> rows(kv, a, run.pair, cnt, __ldg(kv.seq_lens + b), run.first, tiles, lane, err);
     float* out = a.weights + static_cast<int64_t>(run.pair) * kv.max_blocks * kv.block;
     const int64_t head0 = static_cast<int64_t>(b) * kv.hq + kvh * kv.group;
     for (int n = 0; n < tiles; ++n) {

@@ -110,8 +110,9 @@ def check_attention(c, q, sel, cnt, out, lse, scale=None):
     """Against the definition.  Bounds: a logit is the sum, in fp32, of D exact products of a query's entry and a code of
     0 .. 15, less 8 times the entries' sum, times a scale, and of the centre's product (three terms of 8 bits: 2^-24), so it
     is off by (D + 20) U of the magnitudes' sum, a code counting as 24 scales.  A probability times a V scale enters as two
-    f16 terms (2^-21, and absolutely 2^-39 of the largest V scale met, times a code of 8), times a centre as two bf16 terms
-    (2^-16); an output is a sum of T such terms, and one rounding to its type."""
+    f16 terms (2^-21, and absolutely half of f16's smallest step 2^-24 in units of 2^-13 of a reference under twice the
+    largest scale or eighth of a centre met, so 2^-37 of that, times a code of 8), times a centre as two bf16 terms (2^-16);
+    an output is a sum of T such terms, and one rounding to its type."""
     scale = c.d ** -0.5 if scale is None else scale
     qn, group = q.double().cpu().numpy(), q.shape[1] // c.hkv
     half = 0.0 if out.dtype == torch.float32 else 2.0 ** -8
@@ -125,7 +126,8 @@ def check_attention(c, q, sel, cnt, out, lse, scale=None):
             if T:
                 ks = np.concatenate([np.repeat(c.scales["k"][c.table[b, h, j], :min(c.block, c.lens[b] - j * c.block), 0], 32, -1)
                                      for j in blocks])
-                vs = max(np.max(c.scales["v"][c.table[b, h, j], :min(c.block, c.lens[b] - j * c.block), 0]) for j in blocks)
+                vs = max(np.max(np.abs(c.scales["v"][c.table[b, h, j], :min(c.block, c.lens[b] - j * c.block)]) * [[1.0], [0.125]])
+                         for j in blocks)
             for i in range(h * group, (h + 1) * group):
                 if T == 0:
                     assert (got[b, i] == 0).all() and gl[b, i] == -np.inf
@@ -140,6 +142,6 @@ def check_attention(c, q, sel, cnt, out, lse, scale=None):
                 wz = (p[:, None] * Z).sum(0) / p.sum()
                 wc = (p[:, None] * (np.abs(V) + Z)).sum(0) / p.sum()  # |s c| at most
                 rel = 2 * math.expm1(ds) + (T + 60) * U
-                tiny = 8 * 2.0 ** -38 * vs * T / p.sum()
+                tiny = 8 * 2.0 ** -37 * vs * T / p.sum()
                 bound = half * np.abs(want) + (1 + half) * ((rel + 2.0 ** -20) * wc + (rel + 2.0 ** -16) * wz + tiny)
                 assert (np.abs(got[b, i] - want) <= bound).all(), (b, i, np.abs(got[b, i] - want).max(), bound.min())
