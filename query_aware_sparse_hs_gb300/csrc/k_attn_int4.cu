@@ -126,10 +126,10 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
 
   uint8_t* my_ring = ring + warp * (kStages * At::kBytes);
   const uint32_t ring_addr = smem_addr(my_ring);
-  // what a lane copies: piece lane % kPieces of row lane / kPieces of kRowsPer; the
-  // record of row `lane`
-  const uint8_t* k_piece = static_cast<const uint8_t*>(kv.k_pages) + 16 * (lane % kPieces);
-  const uint8_t* v_piece = static_cast<const uint8_t*>(kv.v_pages) + 16 * (lane % kPieces);
+  // what a lane copies: 16 bytes of a row's codes (kPieces lanes to a row), and the record of row `lane`
+  const bool together = (kv.block & 31) == 0;  // tiles lie within a page
+  const uint8_t* k_codes = static_cast<const uint8_t*>(kv.k_pages) + 16 * lane;
+  const uint8_t* v_codes = static_cast<const uint8_t*>(kv.v_pages) + 16 * lane;
   const uint8_t* k_recs = reinterpret_cast<const uint8_t*>(kv.k_scales);
   const uint8_t* v_recs = reinterpret_cast<const uint8_t*>(kv.v_scales);
   // what it reads: row lane % 8 of matrix lane / 8
@@ -181,30 +181,39 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
       const uint32_t live = __ballot_sync(0xffffffffu, ok);
       const uint32_t dst = ring_addr + stage_in * At::kBytes;
       const uint32_t my = dst + piece_at<D>(lane / kPieces, lane % kPieces);  // (the same for every kRowsPer-th row)
-      if (live == 0xffffffffu) {
+      if (live == 0xffffffffu && together) {  // 32 rows that lie together: one address and constants
+        const uint64_t first = __shfl_sync(0xffffffffu, row, 0);
+        const uint8_t* k = k_codes + first * At::kRow;
+        const uint8_t* v = v_codes + first * At::kRow;
 #pragma unroll
         for (int i = 0; i < kTile / kRowsPer; ++i) {
-          const uint64_t at = static_cast<uint64_t>(__shfl_sync(0xffffffffu, row, i * kRowsPer + lane / kPieces)) * At::kRow;
-          copy16(my + i * (kRowsPer * At::kRow), k_piece + at);
-          copy16(my + i * (kRowsPer * At::kRow) + At::kV, v_piece + at);
+          copy16(my + i * (kRowsPer * At::kRow), k + i * (kRowsPer * At::kRow));
+          copy16(my + i * (kRowsPer * At::kRow) + At::kV, v + i * (kRowsPer * At::kRow));
+        }
+        if constexpr (D == 128) {
+          copy16(dst + At::kRec + lane * 16, k_recs + static_cast<uint64_t>(row) * 16);
+          copy16(dst + At::kRecV + lane * 16, v_recs + static_cast<uint64_t>(row) * 16);
+        } else {
+          copy8(dst + At::kRec + lane * 16, k_recs + static_cast<uint64_t>(row) * 8, true);
+          copy8(dst + At::kRecV + lane * 16, v_recs + static_cast<uint64_t>(row) * 8, true);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < kTile / kRowsPer; ++i) {
           const int r = i * kRowsPer + lane / kPieces;
-          const uint64_t at = static_cast<uint64_t>(__shfl_sync(0xffffffffu, row, r)) * At::kRow;
+          const uint64_t at = static_cast<uint64_t>(__shfl_sync(0xffffffffu, row, r)) * At::kRow + 16 * (lane % kPieces);
           const bool there = (live >> r) & 1u;
-          copy16_if(my + i * (kRowsPer * At::kRow), k_piece + at, there);
-          copy16_if(my + i * (kRowsPer * At::kRow) + At::kV, v_piece + at, there);
+          copy16_if(my + i * (kRowsPer * At::kRow), static_cast<const uint8_t*>(kv.k_pages) + at, there);
+          copy16_if(my + i * (kRowsPer * At::kRow) + At::kV, static_cast<const uint8_t*>(kv.v_pages) + at, there);
         }
-      }
-      const uint64_t rec = static_cast<uint64_t>(row) * (D / 8);
-      if constexpr (D == 128) {
-        copy16_if(dst + At::kRec + lane * 16, k_recs + rec, ok);
-        copy16_if(dst + At::kRecV + lane * 16, v_recs + rec, ok);
-      } else {
-        copy8(dst + At::kRec + lane * 16, k_recs + rec, ok);
-        copy8(dst + At::kRecV + lane * 16, v_recs + rec, ok);
+        const uint64_t rec = static_cast<uint64_t>(row) * (D / 8);
+        if constexpr (D == 128) {
+          copy16_if(dst + At::kRec + lane * 16, k_recs + rec, ok);
+          copy16_if(dst + At::kRecV + lane * 16, v_recs + rec, ok);
+        } else {
+          copy8(dst + At::kRec + lane * 16, k_recs + rec, ok);
+          copy8(dst + At::kRecV + lane * 16, v_recs + rec, ok);
+        }
       }
       if (lane == 0) s_live[warp][stage_in] = live;
       stage_in = stage_in + 1 == kStages ? 0 : stage_in + 1;
