@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "../../include/hs.h"
@@ -141,6 +142,19 @@ cudaError_t allow_dynamic_smem(void (*kern)(KArgs...), size_t dynamic) {
   if (e != cudaSuccess) return e;
   if (dynamic + fa.sharedSizeBytes <= 48 * 1024) return cudaSuccess;
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(dynamic));
+}
+
+// The same, asked for once a device: the runtime keeps it for contexts made later, and
+// over a reset, as a test does (asking every time took 1.2 us of host time a call).
+template <typename... KArgs>
+cudaError_t allow_dynamic_smem_once(std::atomic<uint64_t>& allowed, void (*kern)(KArgs...), size_t dynamic) {
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (allowed.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  if (cudaError_t e = allow_dynamic_smem(kern, dynamic); e != cudaSuccess) return e;
+  allowed.fetch_or(bit, std::memory_order_relaxed);
+  return cudaSuccess;
 }
 
 template <typename... KArgs, typename... Args>

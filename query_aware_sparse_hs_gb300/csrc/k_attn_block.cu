@@ -61,8 +61,6 @@
 // until they are divided, so that V may be as large as its outputs can be.
 #include <limits.h>
 
-#include <atomic>
-
 #include "attn_parts.cuh"
 
 namespace hs {
@@ -556,16 +554,8 @@ __global__ __launch_bounds__(teams_of(D) * kTeamWarps * 32, 1) void attn_block_k
 template <int D, int NT>
 cudaError_t launch_n(const KvView& kv, const PartArgs& b, int ctas, unsigned* err, cudaStream_t st) {
   auto kern = attn_block_kernel<D, NT>;
-  // asked for once a device: the runtime keeps it for contexts made later, and over a
-  // reset, as a test does (asking every time took 1.2 us of host time a call)
   static std::atomic<uint64_t> allowed{0};
-  int dev = 0;
-  if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
-  const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (!(allowed.load(std::memory_order_relaxed) & bit)) {
-    if (cudaError_t e = allow_dynamic_smem(kern, ring_bytes<D>()); e != cudaSuccess) return e;
-    allowed.fetch_or(bit, std::memory_order_relaxed);
-  }
+  if (cudaError_t e = allow_dynamic_smem_once(allowed, kern, ring_bytes<D>()); e != cudaSuccess) return e;
   cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(teams_of(D) * kTeamWarps * 32), ring_bytes<D>(), st, kv, b, err);
   if (e != cudaSuccess || b.counters) return e;
   const size_t smem = (static_cast<size_t>(ctas * teams_of(D) + 2) * kv.group + 4 +

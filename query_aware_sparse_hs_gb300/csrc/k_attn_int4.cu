@@ -39,8 +39,6 @@
 // times z as two bf16 terms, 16 bits.
 #include <limits.h>
 
-#include <atomic>
-
 #include "attn_parts.cuh"
 #include "int4.cuh"
 
@@ -523,15 +521,8 @@ template <int D, int NT>
 cudaError_t launch_n(const KvView& kv, const PartArgs& b, int ctas, unsigned* err, cudaStream_t st) {
   constexpr int kTeams = teams_of(D, NT);
   auto kern = attn_int4_kernel<D, NT>;
-  // asked for once a device, as for the block-scaled kernel
   static std::atomic<uint64_t> allowed{0};
-  int dev = 0;
-  if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
-  const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (!(allowed.load(std::memory_order_relaxed) & bit)) {
-    if (cudaError_t e = allow_dynamic_smem(kern, ring_bytes<D, NT>()); e != cudaSuccess) return e;
-    allowed.fetch_or(bit, std::memory_order_relaxed);
-  }
+  if (cudaError_t e = allow_dynamic_smem_once(allowed, kern, ring_bytes<D, NT>()); e != cudaSuccess) return e;
   cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(kTeams * kTeamWarps * 32), (ring_bytes<D, NT>()), st, kv, b, err);
   if (e != cudaSuccess || b.counters) return e;
   const size_t smem = (static_cast<size_t>(ctas * kTeams + 2) * kv.group + 4 + static_cast<size_t>(kTeams - 1) * kv.group * D) * sizeof(float);

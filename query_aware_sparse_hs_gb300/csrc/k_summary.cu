@@ -623,7 +623,8 @@ cudaError_t launch_int4(const KvView& kv, int first_block, int nblocks, void* sm
   const int resident = sms * 3;
   const unsigned grid = static_cast<unsigned>(most < resident ? most : resident);
   constexpr size_t smem = static_cast<size_t>(kWarps) * kUnits * Unit<D>::kBytes;
-  if (cudaError_t e = allow_dynamic_smem(summaries_int4_kernel<D>, smem); e != cudaSuccess) return e;
+  static std::atomic<uint64_t> allowed{0};
+  if (cudaError_t e = allow_dynamic_smem_once(allowed, summaries_int4_kernel<D>, smem); e != cudaSuccess) return e;
   return launch_pdl(summaries_int4_kernel<D>, dim3(grid), dim3(kWarps * 32), smem, st, kv, first_block, smin, smax, err);
 }
 

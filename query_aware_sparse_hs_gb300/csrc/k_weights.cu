@@ -438,7 +438,8 @@ cudaError_t launch_n(const KvView& kv, const WeightsArgs& a, int sms, unsigned* 
   using R = Row<D, KIND>;
   constexpr size_t smem = static_cast<size_t>(R::kWarps) * kStages * R::kStage;
   auto kern = weights_kernel<D, KIND, NT>;
-  if (cudaError_t e = allow_dynamic_smem(kern, smem); e != cudaSuccess) return e;
+  static std::atomic<uint64_t> allowed{0};
+  if (cudaError_t e = allow_dynamic_smem_once(allowed, kern, smem); e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(sms), dim3(R::kWarps * 32), smem, st, kv, a, err);
 }
 

@@ -485,45 +485,66 @@ def hs_quantize_e4m3_g32(src, codes, scales, stream=None):
            "hs_quantize_e4m3_g32")
 
 
+_U8, _I32 = torch.uint8, torch.int32
+_quantize_int4, _dequantize_int4 = _lib.hs_quantize_int4_g32, _lib.hs_dequantize_int4_g32
+_accumulate, _evict = _lib.hs_accumulate_attn_weights, _lib.hs_evict_tokens
+
+
+def _here(what, *tensors):
+    """The current device, which contiguous CUDA tensors (None: not given) must be on."""
+    device = _current_device() if tensors[0].is_cuda else -2
+    for t in tensors:
+        if t is not None and (t.get_device() != device or not t.is_contiguous()):
+            raise ValueError(f"{what}: tensors must be contiguous and on the current CUDA device")
+    return device
+
+
 def _int4_rows(values, codes, scales, what):
-    """Rows and head_dim of [rows][D] values, [rows][D/2] codes and [rows][2][D/32] scales (leading dimensions alike)."""
-    D = values.shape[-1]
-    rows = values.numel() // D if D else 0
-    if values.dtype not in (_F32, _BF16) or codes.dtype != torch.uint8 or scales.dtype != _BF16:
-        raise ValueError(f"{what}: values f32 or bf16, codes uint8, scales bf16")
-    if codes.numel() * 2 != rows * D or scales.numel() * 16 != rows * D or codes.shape[-1] * 2 != D:
-        raise ValueError(f"{what}: [rows][{D}] values go with [rows][{D // 2}] codes and [rows][2][{D // 32}] scales")
-    if not values.get_device() == codes.get_device() == scales.get_device():
-        raise ValueError(f"{what}: values, codes and scales must be on one device")
-    return rows, D
+    """Rows, head_dim, whether f32, and device of [rows][D] values, [rows][D/2] codes and [rows][2][D/32] scales
+    (leading dimensions alike)."""
+    d, n, dtype = values.shape[-1], values.numel(), values.dtype
+    if (codes.numel() * 2 != n or scales.numel() * 16 != n or codes.shape[-1] * 2 != d or codes.dtype is not _U8
+            or scales.dtype is not _BF16 or (dtype is not _BF16 and dtype is not _F32)):
+        raise ValueError(f"{what}: [rows][D] values of f32 or bf16 go with [rows][D/2] uint8 codes and [rows][2][D/32] "
+                         "bf16 scales")
+    return n // d if d else 0, d, 0 if dtype is _BF16 else 1, _here(what, values, codes, scales)
 
 
 def hs_quantize_int4_g32(src, codes, scales, stream=None):
     """src [rows][D] f32 or bf16 -> codes [rows][D/2] uint8, scales [rows][2][D/32] bf16 (scales, then centres)."""
-    rows, D = _int4_rows(src, codes, scales, "hs_quantize_int4_g32")
-    _check(_lib.hs_quantize_int4_g32(_ptr(src), 1 if src.dtype == _F32 else 0, rows, D, _ptr(codes), _ptr(scales),
-                                     _stream(stream)),
-           "hs_quantize_int4_g32")
+    rows, d, f32, device = _int4_rows(src, codes, scales, "hs_quantize_int4_g32")
+    st = _quantize_int4(src.data_ptr(), f32, rows, d, codes.data_ptr(), scales.data_ptr(),
+                        _raw_stream(device) if stream is None else _stream(stream))
+    if st:
+        raise HSError(st, "hs_quantize_int4_g32")
 
 
 def hs_dequantize_int4_g32(codes, scales, out, stream=None):
     """codes [rows][D/2] uint8, scales [rows][2][D/32] bf16 -> out [rows][D] f32 or bf16 (pages as they are: any
     leading dimensions)."""
-    rows, D = _int4_rows(out, codes, scales, "hs_dequantize_int4_g32")
-    _check(_lib.hs_dequantize_int4_g32(_ptr(codes), _ptr(scales), rows, D, _ptr(out), 1 if out.dtype == _F32 else 0,
-                                       _stream(stream)),
-           "hs_dequantize_int4_g32")
+    rows, d, f32, device = _int4_rows(out, codes, scales, "hs_dequantize_int4_g32")
+    st = _dequantize_int4(codes.data_ptr(), scales.data_ptr(), rows, d, out.data_ptr(), f32,
+                          _raw_stream(device) if stream is None else _stream(stream))
+    if st:
+        raise HSError(st, "hs_dequantize_int4_g32")
 
 
 def hs_accumulate_attn_weights(shape, kv, q, lse, sel, sel_count, capacity, scale, weights, stream=None):
     """weights [batch][Hkv][max_blocks * B] f32 += the group's softmax weights of every token of the selected blocks,
     lse [batch][Hq] f32 as the attention over the same selection left it."""
-    if lse.dtype != _F32 or weights.dtype != _F32 or weights.numel() != kv.batch * shape.num_kv_heads * kv.max_blocks * shape.block_size:
-        raise ValueError("lse and weights must be f32, weights [batch][Hkv][max_blocks * B]")
-    _check(_lib.hs_accumulate_attn_weights(ctypes.byref(shape), ctypes.byref(kv), _ptr(q), _ptr(lse), _ptr(sel),
-                                           _ptr(sel_count), int(capacity), float(scale), _ptr(weights),
-                                           _stream(stream)),
-           "hs_accumulate_attn_weights")
+    heads, pairs = kv.batch * shape.num_q_heads, kv.batch * shape.num_kv_heads
+    if (lse.dtype is not _F32 or weights.dtype is not _F32 or sel.dtype is not _I32 or sel_count.dtype is not _I32
+            or q.dtype is not (_BF16 if shape.kv_dtype else _F32) or q.numel() != heads * shape.head_dim
+            or lse.numel() != heads or sel.numel() != pairs * capacity or sel_count.numel() != pairs
+            or weights.numel() != pairs * kv.max_blocks * shape.block_size):
+        raise ValueError("hs_accumulate_attn_weights: q [batch][Hq][D], lse [batch][Hq] f32, sel [batch][Hkv][capacity] "
+                         "and sel_count [batch][Hkv] int32, weights [batch][Hkv][max_blocks * B] f32")
+    device = _here("hs_accumulate_attn_weights", q, lse, sel, sel_count, weights)
+    st = _accumulate(_byref(shape), _byref(kv), q.data_ptr(), lse.data_ptr(), sel.data_ptr(), sel_count.data_ptr(),
+                     int(capacity), float(scale), weights.data_ptr(),
+                     _raw_stream(device) if stream is None else _stream(stream))
+    if st:
+        raise HSError(st, "hs_accumulate_attn_weights")
 
 
 def evict_params(budget, sink_tokens=0, recent_tokens=0) -> EvictParams:
@@ -536,16 +557,19 @@ def hs_evict_tokens(shape, kv, dst, params, weights, dst_weights, kept, stream=N
     """The heaviest tokens of every (request, kv head) gathered into the pages of ``dst`` (a paged_kv whose seq_lens is
     written).  weights [batch][Hkv][max_blocks * B] f32, dst_weights the same for dst (or None), kept
     [batch][Hkv][budget] int32."""
-    pairs = kv.batch * shape.num_kv_heads
-    if weights.dtype != _F32 or weights.numel() != pairs * kv.max_blocks * shape.block_size:
-        raise ValueError("weights must be f32 [batch][Hkv][max_blocks * B]")
-    if dst_weights is not None and (dst_weights.dtype != _F32 or dst_weights.numel() != pairs * dst.max_blocks * shape.block_size):
-        raise ValueError("dst_weights must be f32 [batch][Hkv][max_blocks of dst * B]")
-    if kept.dtype != torch.int32 or kept.numel() != pairs * params.budget:
-        raise ValueError("kept must be int32 [batch][Hkv][budget]")
-    _check(_lib.hs_evict_tokens(ctypes.byref(shape), ctypes.byref(kv), ctypes.byref(dst), ctypes.byref(params),
-                                _ptr(weights), _ptr(dst_weights), _ptr(kept), _stream(stream)),
-           "hs_evict_tokens")
+    pairs, block = kv.batch * shape.num_kv_heads, shape.block_size
+    if weights.dtype is not _F32 or weights.numel() != pairs * kv.max_blocks * block:
+        raise ValueError("hs_evict_tokens: weights must be f32 [batch][Hkv][max_blocks * B]")
+    if dst_weights is not None and (dst_weights.dtype is not _F32 or dst_weights.numel() != pairs * dst.max_blocks * block):
+        raise ValueError("hs_evict_tokens: dst_weights must be f32 [batch][Hkv][max_blocks of dst * B]")
+    if kept.dtype is not _I32 or kept.numel() != pairs * params.budget:
+        raise ValueError("hs_evict_tokens: kept must be int32 [batch][Hkv][budget]")
+    device = _here("hs_evict_tokens", weights, kept, dst_weights)
+    st = _evict(_byref(shape), _byref(kv), _byref(dst), _byref(params), weights.data_ptr(),
+                None if dst_weights is None else dst_weights.data_ptr(), kept.data_ptr(),
+                _raw_stream(device) if stream is None else _stream(stream))
+    if st:
+        raise HSError(st, "hs_evict_tokens")
 
 
 def hs_get_device_error(stream=None) -> tuple[int, int]:

@@ -47,8 +47,10 @@ def test_quantise_and_dequantise(hs):
             hs.hs_quantize_int4_g32(*bad)
         with pytest.raises(ValueError):
             hs.hs_dequantize_int4_g32(bad[1], bad[2], bad[0])
-    with pytest.raises(ValueError):
-        hs.hs_quantize_int4_g32(x.t().contiguous().t(), c, s)
+    with pytest.raises(ValueError, match="current CUDA device"):  # right, but on the host
+        hs.hs_quantize_int4_g32(x, c, s)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        hs.hs_dequantize_int4_g32(c, s, x)
 
 
 def test_a_4_bit_cache(hs):
@@ -89,9 +91,13 @@ def test_accumulated_weights(hs):
     k = kv(hs)
     lse, w = torch.zeros((2, 16)), torch.zeros((2, 2, 8 * 64))
     q, sel, cnt = torch.zeros((2, 16, 128), dtype=torch.bfloat16), torch.zeros((2, 2, 4), dtype=torch.int32), torch.zeros((2, 2), dtype=torch.int32)
-    for bad in ((lse.half(), w), (lse, w.half()), (lse, w[:, :, 1:])):
-        with pytest.raises(ValueError):
-            hs.hs_accumulate_attn_weights(shape, k, q, bad[0], sel, cnt, 4, 0.1, bad[1])
+    for bad in ((q, lse.half(), sel, cnt, w), (q, lse, sel, cnt, w.half()), (q, lse, sel, cnt, w[:, :, 1:]), (q.float(), lse, sel, cnt, w),
+                (q[:1], lse, sel, cnt, w), (q, lse[:1], sel, cnt, w), (q, lse, sel.long(), cnt, w), (q, lse, sel[:, :, :3], cnt, w),
+                (q, lse, sel, cnt[:1], w), (q, lse, sel, cnt.float(), w)):
+        with pytest.raises(ValueError, match="lse"):
+            hs.hs_accumulate_attn_weights(shape, k, *bad[:4], 4, 0.1, bad[4])
+    with pytest.raises(ValueError, match="current CUDA device"):
+        hs.hs_accumulate_attn_weights(shape, k, q, lse, sel, cnt, 4, 0.1, w)
 
 
 def test_eviction(hs):
@@ -115,8 +121,10 @@ def test_eviction(hs):
     p = hs.evict_params(100)
     for bad in ((w.double(), w.clone(), kept), (w[:, :1], w.clone(), kept), (w, w[:, :1].clone(), kept), (w, w.half(), kept),
                 (w, None, kept.long()), (w, None, kept[:, :, 1:])):
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match="must be"):
             hs.hs_evict_tokens(shape, k, k, p, *bad)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        hs.hs_evict_tokens(shape, k, k, p, w, w.clone(), kept)
 
 
 def test_the_driver_refuses_a_cache_of_another_length(hs, monkeypatch):
