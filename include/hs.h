@@ -165,7 +165,7 @@ typedef struct hs_select_params {
  * automatic, 1 = CUDA-core kernel (every dtype), 2 = tensor-core kernel: tcgen05
  * for bf16 and e4m3 with grouped scales (head_dim 128 and the block sizes above;
  * at most 8 query heads per kv head for e4m3), warp-level products for e4m3 with a
- * scale per page; HS_ERR_UNSUPPORTED where there is none.  The tensor-core kernel
+ * scale per page and for 4-bit caches; HS_ERR_UNSUPPORTED where there is none.  The tensor-core kernel
  * of e4m3 with grouped scales forms each V value, code times scale, in f16 (as it
  * does the products with P), so it needs |code * scale| <= 65504 (a V scale up to
  * 146 for codes up to 448); beyond that its output is not finite.  The CUDA-core
@@ -220,7 +220,12 @@ typedef struct hs_select_params {
  * tokens or (over all requests and kv heads) 2^36, are not supported.
  * Calls that may overlap on the GPU (other streams, graphs replayed side by side)
  * need a workspace and split_counters each.
- * A 4-bit cache (HS_KV_INT4_G32) runs on the CUDA-core kernel. */
+ * A 4-bit cache (HS_KV_INT4_G32) likewise has a tensor-core kernel of its own for every
+ * block_size, with the same rules of cutting, workspace, max_ctas and limits.  It holds
+ * queries exactly (entries up to 2^90), a token's probability times its V scale to 22
+ * bits, or absolutely within 2^-37 of the largest V scale, or eighth of a centre, of the
+ * selection (of 2^-112 at least), times its V centre to 16 bits; everything else in
+ * fp32.  Scales and centres up to 2^126. */
 #define HS_ATTN_EARLY_SUMMARIES 1u
 #define HS_ATTN_RANGES 2u
 #define HS_ATTN_NO_RANGES 4u
@@ -289,7 +294,8 @@ HS_API size_t hs_workspace_bytes(const hs_attn_shape* shape, int32_t batch, int3
  * per pair instead).  Returns 0, or -1 on invalid input (outputs untouched).
  * Without a device it assumes 148 SMs, as hs_workspace_bytes does.  The
  * CUDA-core kernel always uses equal splits.  Both are 0 for a cache with a
- * scale per page, whose kernel divides by the counts it finds on the device. */
+ * scale per page and for a 4-bit one, whose kernels divide by the counts they find on
+ * the device. */
 HS_API int32_t hs_attn_geometry(const hs_attn_shape* shape, int32_t batch, int32_t capacity,
                                 const hs_attn_params* params, int32_t* splits, int32_t* chunks_per_cta);
 
@@ -633,7 +639,9 @@ HS_API hs_status hs_dequantize_int4_g32(const uint8_t* codes, const void* scales
  *            place in its request last; read and written, start it at 0.
  * Sums are fp32.  A block selected twice is added twice.  Entries of tokens that are
  * not selected stay as they are.  Selections larger than capacity, blocks outside the
- * request and pages outside the pool are reported and skipped as in the attention. */
+ * request and pages outside the pool are reported and skipped as in the attention.
+ * Pools of 2^32 token rows, and selections of 2^31 tokens or (over all requests and kv
+ * heads) 2^36, are not supported. */
 HS_API hs_status hs_accumulate_attn_weights(const hs_attn_shape* shape, const hs_paged_kv* kv, const void* q,
                                             const float* lse, const int32_t* sel, const int32_t* sel_count,
                                             int32_t capacity, float scale, float* weights, hs_stream_t stream);

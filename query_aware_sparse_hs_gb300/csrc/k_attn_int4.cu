@@ -33,6 +33,15 @@
 // P for V, goes with the record as it lies in memory, in instructions of its own: three
 // bf16 terms of the sums, two of P.
 //
+// What bounds it: the matrix, integer and fp32 pipes in turn (30%, 45% and 25% busy;
+// 866 instructions for 32 tokens of 128 channels, 8 heads, a third of them V's codes and
+// P times s, 2.2 of 4 issued a cycle): 16 requests x 4 heads x 131072 tokens, 1.34 GB, 318
+// us, 0.62 of the copy rate; 64 channels 218 us for half of that (0.45).  32 requests x
+// 4096 selected tokens: 32.0 us, of which the chain of lookups before the stream and
+// the join behind it are 8; 12 uneven requests of 16 heads, 64 channels: 32.5.  8 warps an
+// SM instead of 12: 442 us; 16 for 64 channels: no faster; fp32 sums one at a time instead
+// of in pairs: 322; two stages instead of three: 315; without the copies 0.85 of the time.
+//
 // Precision: q is exact (bf16, times a power of two, which takes entries up to 2^90), S
 // and all sums fp32.  P times s, in units of 2^-13 of the reference (the largest power of
 // two met of s and z / 8), as two f16 terms: 22 bits, absolutely 2^-25 of the units; P
@@ -54,7 +63,10 @@ constexpr int kStages = 3;  // tiles in a warp's ring
 // the reference then, 2^15 at most.
 constexpr float kMargin = 2.0f;
 constexpr int kUnit4 = 13;
-__host__ __device__ constexpr int teams_of(int, int nt) { return nt == 1 ? 3 : 2; }
+// Teams of a CTA (one CTA to an SM), as many as the registers allow without spilling much:
+// 16 heads of 64 channels, 16 x 4 heads x 65536 tokens, 139 us with 12 warps, 166 with 8;
+// of 128 channels 258 with 8 warps, 279 with 12.
+__host__ __device__ constexpr int teams_of(int head_dim, int nt) { return head_dim == 64 || nt == 1 ? 3 : 2; }
 
 template <int D>
 struct Stage {  // byte offsets in a stage of the ring

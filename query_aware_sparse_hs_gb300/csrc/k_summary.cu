@@ -514,14 +514,14 @@ __global__ __launch_bounds__(kWarps * 32, 3) void summaries_int4_kernel(KvView k
     const auto issue = [&]() {  // the next unit's rows, which lie together
       if (in.i < 32) {
         const int64_t row = static_cast<int64_t>(__shfl_sync(0xffffffffu, my_page, in.i)) * B + in.t;
-        const int valid = valid_of(in.i), bytes = min(valid - in.t, kUnitRows);
+        const int valid = valid_of(in.i), rows = min(valid - in.t, kUnitRows);
         const uint8_t* codes = static_cast<const uint8_t*>(kv.k_pages) + row * int4::row_bytes(D);
         const uint8_t* recs = reinterpret_cast<const uint8_t*>(kv.k_scales) + row * kRecord;
         const uint32_t to = mine_addr + unit_in * Unit<D>::kBytes;
 #pragma unroll
         for (int x = 0; x < Unit<D>::kCodes; x += 512)
-          if (x + lane * 16 < bytes * int4::row_bytes(D)) copy16_async(to + x + lane * 16, codes + x + lane * 16);
-        if (lane * kRecord < kUnitRows * kRecord && lane < bytes) {
+          if (x + lane * 16 < rows * int4::row_bytes(D)) copy16_async(to + x + lane * 16, codes + x + lane * 16);
+        if (lane < rows) {
           if constexpr (kRecord == 16)
             copy16_async(to + Unit<D>::kCodes + lane * 16, recs + lane * 16);
           else

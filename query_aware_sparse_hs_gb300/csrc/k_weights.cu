@@ -14,6 +14,12 @@
 // 4-bit codes as bf16 numbers below the normal ones, as in the attention.  Scales of
 // groups of channels are applied to the groups' partial sums.  f32 caches: on the CUDA
 // cores, as fp32 products are wanted.
+//
+// What bounds it: memory for bf16 (16 requests x 4 heads x 16384 tokens, 277 MB: 45.9 us,
+// 0.89 of the copy rate); instructions beside it for the others (4-bit, 32 requests, 185
+// MB: 35.6 us, 0.77; e4m3 0.73 to 0.75); the CUDA cores for f32 (0.32).  A short call, 4
+// requests of up to 3000 tokens, takes 4.3 us: the launch, the counts and one chain of
+// lookups.
 #include <limits.h>
 
 #include "attn_parts.cuh"
@@ -464,7 +470,8 @@ cudaError_t launch_d(const KvView& kv, const WeightsArgs& a, int sms, unsigned* 
 bool weights_fits(const KvView& kv, const WeightsArgs& a) {
   const int64_t pairs = static_cast<int64_t>(kv.batch) * kv.hkv, tokens = static_cast<int64_t>(a.capacity) * kv.block;
   return pairs <= INT32_MAX && kv.num_pages * kv.block <= UINT32_MAX && tokens <= INT32_MAX &&  // rows and places are 32-bit
-         static_cast<int64_t>(kv.max_blocks) * kv.block <= INT32_MAX;
+         static_cast<int64_t>(kv.max_blocks) * kv.block <= INT32_MAX &&
+         (tokens / kTile + 1) * pairs <= INT32_MAX;  // tiles
 }
 
 cudaError_t launch_weights(const KvView& kv, const WeightsArgs& a, int sms, unsigned* err, cudaStream_t st) {

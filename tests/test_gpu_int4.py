@@ -451,6 +451,34 @@ def test_captured_and_on_another_stream():
         assert torch.equal(out, again) and torch.equal(lse, la)
 
 
+def test_two_calls_at_once_and_the_call_without_a_workspace():
+    """Two streams, a workspace and counters each, many times over; and the library's own scratch."""
+    from query_aware_sparse_hs_gb300 import hs
+    shape = hs.attn_shape(16, 2, 128, 64, "int4")
+    jobs = []
+    for seed in (1, 2):
+        c = Cache([9000, 700, 3000], 2, 128, 64, seed=seed)
+        q = query(c, 16, seed=seed)
+        sel, cnt = chosen(c, max(c.nb), None)
+        want = attend(c, q, sel, cnt)
+        ctr = torch.zeros(6, dtype=torch.int32, device="cuda")
+        p = hs.attn_params(128 ** -0.5, True, split_counters=ctr)
+        ws = torch.empty(hs.hs_workspace_bytes(shape, 3, sel.shape[2], p), dtype=torch.uint8, device="cuda")
+        jobs.append((c, q, torch.from_numpy(sel).cuda(), torch.from_numpy(cnt).cuda(), p, ws, torch.zeros_like(want[0]),
+                     torch.zeros_like(want[1]), want, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, q, sel, cnt, p, ws, out, lse, _, stream in jobs:
+            hs.hs_sparse_paged_decode_attn(shape, c.kv, q, sel, cnt, sel.shape[2], p, out, lse, ws, stream=stream)
+    torch.cuda.synchronize()
+    for c, q, sel, cnt, p, ws, out, lse, want, _ in jobs:
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        out.fill_(float("nan"))
+        hs.hs_sparse_paged_decode_attn_noalloc(shape, c.kv, q, sel, cnt, sel.shape[2], p, out, lse)
+        assert torch.equal(out, want[0])
+    ok()
+
+
 # ---- summaries -----------------------------------------------------------------------------------------------------------
 
 
