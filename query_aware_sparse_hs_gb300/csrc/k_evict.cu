@@ -34,7 +34,8 @@ __device__ __forceinline__ uint32_t weight_key(float w) {  // NaN last, -0 as 0
 // Latency-bound, by the barriers of the cluster and what lies between them: with a budget
 // of 64, so that little is gathered, both launches take 11 us for 3000 tokens, 19 for
 // 16 x 4 heads of up to 32768.  (A byte at a time with the digit found by one thread, a
-// CTA to a pair: 26 and 43 for this launch alone.)
+// CTA to a pair: 26 and 43 for this launch alone; the keys of the first digit's bin listed
+// for the other two: no change.)
 __global__ __launch_bounds__(kThreads) void evict_select_kernel(KvView kv, EvictArgs a, int ctas, unsigned* err) {
   __shared__ uint32_t s_hist[3][kBins];  // one for each digit
   __shared__ uint32_t s_sums[2][kWarps];
@@ -170,15 +171,15 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(KvView kv, Evict
   cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
-constexpr int kRows = 32;  // rows of a CTA
-constexpr int kGatherThreads = 128;
+constexpr int kRows = 64;  // rows of a CTA
+constexpr int kGatherThreads = 256;
 constexpr int kFlight = 4;  // pieces of a thread on their way
 
 // CTA = kRows places of a (request, kv head)'s new pages.  row_bytes, scale_bytes: of a
 // row of K (or V).  Memory-bound: 16 x 4 heads, 4096 rows each of 512 bytes of K and V,
-// 268 MB: 41 us, the copy rate.
+// 268 MB: 41 us, the copy rate; rows of 128 and 64 bytes, scattered, half of it.
 __global__ __launch_bounds__(kGatherThreads) void evict_gather_kernel(KvView kv, KvView dst, EvictArgs a, int chunks, int row_bytes,
-                                                                      int scale_bytes, unsigned* err) {
+                                                                      int scale_bytes, int scale_unit, unsigned* err) {
   __shared__ int64_t s_from[kRows], s_to[kRows];  // rows of the pools, -1: none
   pdl_trigger();
   pdl_wait();
@@ -230,16 +231,26 @@ __global__ __launch_bounds__(kGatherThreads) void evict_gather_kernel(KvView kv,
     for (int u = 0; u < kFlight; ++u)
       if (to[u]) *reinterpret_cast<uint4*>(to[u]) = x[u];
   }
-  const int words = scale_bytes / 4;
-  for (int n = tid; n < kRows * words * 2; n += kGatherThreads) {
-    const int r = n / (words * 2), x = n - r * words * 2;
-    const bool v = x >= words;
-    const int at = v ? x - words : x;
-    if (s_from[r] < 0) continue;
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(v ? kv.v_scales : kv.k_scales) + s_from[r] * words + at;
-    uint32_t* to = reinterpret_cast<uint32_t*>(const_cast<float*>(v ? dst.v_scales : dst.k_scales)) + s_to[r] * words + at;
-    *to = __ldg(src);
-  }
+  // scales, by the widest units that their rows and addresses allow
+  const auto copy_scales = [&](auto unit) {
+    using Unit = decltype(unit);
+    const int n_row = scale_bytes / static_cast<int>(sizeof(Unit));
+    for (int n = tid; n < kRows * n_row * 2; n += kGatherThreads) {
+      const int r = n / (n_row * 2), x = n - r * n_row * 2;
+      const bool v = x >= n_row;
+      const int at = v ? x - n_row : x;
+      if (s_from[r] < 0) continue;
+      const Unit* src = reinterpret_cast<const Unit*>(v ? kv.v_scales : kv.k_scales) + s_from[r] * n_row + at;
+      Unit* to = reinterpret_cast<Unit*>(const_cast<float*>(v ? dst.v_scales : dst.k_scales)) + s_to[r] * n_row + at;
+      *to = __ldg(src);
+    }
+  };
+  if (scale_unit == 16)
+    copy_scales(uint4{});
+  else if (scale_unit == 8)
+    copy_scales(uint2{});
+  else if (scale_unit == 4)
+    copy_scales(uint32_t{});
 }
 
 cudaError_t launch_select(const KvView& kv, const EvictArgs& a, int sms, unsigned* err, cudaStream_t st) {
@@ -275,8 +286,11 @@ cudaError_t launch_evict(const KvView& kv, const KvView& dst, const EvictArgs& a
   if (e != cudaSuccess) return e;
   const int elem2 = kv.kv_dtype == HS_KV_F32 ? 8 : kv.kv_dtype == HS_KV_BF16 ? 4 : kv.kv_dtype == HS_KV_INT4_G32 ? 1 : 2;
   const int scale_bytes = kv.kv_dtype >= HS_KV_FP8E4M3_G32 ? kv.head_dim / kQuantGroup * 4 : 0;
+  const uintptr_t bases = reinterpret_cast<uintptr_t>(kv.k_scales) | reinterpret_cast<uintptr_t>(kv.v_scales) |
+                          reinterpret_cast<uintptr_t>(dst.k_scales) | reinterpret_cast<uintptr_t>(dst.v_scales);
+  const int scale_unit = scale_bytes == 0 ? 0 : bases % scale_bytes == 0 ? scale_bytes : 4;
   return launch_pdl(evict_gather_kernel, dim3(static_cast<unsigned>(evict_ctas(kv, a.budget))), dim3(kGatherThreads), 0, st, kv, dst, a,
-                    ceil_div(a.budget, kRows), kv.head_dim * elem2 / 2, scale_bytes, err);
+                    ceil_div(a.budget, kRows), kv.head_dim * elem2 / 2, scale_bytes, scale_unit, err);
 }
 
 }  // namespace hs
