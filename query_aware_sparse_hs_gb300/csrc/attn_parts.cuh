@@ -108,6 +108,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 __device__ __forceinline__ float lower(uint32_t two) { return __uint_as_float(two << 16); }        // of two bf16
 __device__ __forceinline__ float upper(uint32_t two) { return __uint_as_float(two & 0xffff0000u); }
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
 // Two fp32 numbers at a time.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;
@@ -131,6 +136,56 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// A head's query for products with 4-bit codes, 8 channels (32 k + 8 c4 .. + 7) of every
+// group k to a lane, the head's four lanes together.
+template <int GROUPS>
+struct Int4Query {
+  uint32_t q[GROUPS][4];  // bf16 times 2^e: channels 0 4, 2 6 of the 8; by 1/16, as their codes are 16 times as large, 1 5, 3 7
+  uint32_t terms[3];      // what word c4 of a record is multiplied by, in three bf16 terms: -8 sum q for a scale, sum q for a centre
+  float factor;           // from the products with codes n 2^-133 to a logit (log2 units)
+
+  __device__ __forceinline__ Int4Query(const uint4 (&raw)[GROUPS], float scale, int c4) {
+    float amax = 0.0f, sum[GROUPS], x[GROUPS][8];
+#pragma unroll
+    for (int k = 0; k < GROUPS; ++k) {
+      const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+      sum[k] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[k][2 * i] = lower(w[i]);
+        x[k][2 * i + 1] = upper(w[i]);
+        amax = fmaxf(amax, fmaxf(fabsf(x[k][2 * i]), fabsf(x[k][2 * i + 1])));
+        sum[k] += x[k][2 * i] + x[k][2 * i + 1];
+      }
+      sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
+      sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    // the largest entry in [2^100, 2^101) where e is from 10 to 127
+    const int e = min(max(227 - static_cast<int>(__float_as_uint(amax) >> 23), 10), 127);
+    const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+    factor = scale * kLog2e * __uint_as_float(static_cast<uint32_t>(133 - e + 127) << 23);
+#pragma unroll
+    for (int k = 0; k < GROUPS; ++k) {
+      q[k][0] = pack_bf16(x[k][0] * up, x[k][4] * up);
+      q[k][1] = pack_bf16(x[k][2] * up, x[k][6] * up);
+      q[k][2] = pack_bf16(x[k][1] * up * 0.0625f, x[k][5] * up * 0.0625f);
+      q[k][3] = pack_bf16(x[k][3] * up * 0.0625f, x[k][7] * up * 0.0625f);
+    }
+    constexpr int kWords = GROUPS / 2;  // a record's words of scales; then those of centres
+    const int pair = c4 & (kWords - 1);
+    const float by = scale * kLog2e * (c4 < kWords ? -8.0f : c4 < 2 * kWords ? 1.0f : 0.0f);
+    float r0 = (pair ? sum[GROUPS - 2] : sum[0]) * by, r1 = (pair ? sum[GROUPS - 1] : sum[1]) * by;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      terms[i] = pack_bf16(r0, r1);
+      r0 -= lower(terms[i]);
+      r1 -= upper(terms[i]);
+    }
+  }
+};
 
 struct PartArgs {
   const void* q;

@@ -48,6 +48,8 @@
 // times z as two bf16 terms, 16 bits.
 #include <limits.h>
 
+#include <type_traits>
+
 #include "attn_parts.cuh"
 #include "int4.cuh"
 
@@ -91,11 +93,440 @@ __device__ __forceinline__ uint32_t centred(uint32_t two, uint32_t minus) {
   return *reinterpret_cast<const uint32_t*>(&x);
 }
 
+// The largest V scale, or eighth of a centre, of a tile's records, as bits (NaN: 0).
+template <int D>
+__device__ __forceinline__ uint32_t largest_of(const uint8_t* records, int lane) {
+  const uint4 r = *reinterpret_cast<const uint4*>(records + 16 * lane);
+  const auto wide = [](uint32_t p, uint32_t q) { return fmaxf(fmaxf(fabsf(lower(p)), fabsf(upper(p))), fmaxf(fabsf(lower(q)), fabsf(upper(q)))); };
+  const float top = D == 128 ? fmaxf(wide(r.x, r.y), 0.125f * wide(r.z, r.w)) : fmaxf(wide(r.x, r.x), 0.125f * wide(r.y, r.y));
+  return __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(top, 0.0f)));
+}
+// The scales of a record and the next one's, by group.
+__device__ __forceinline__ void scale_pairs(const uint8_t* record, float2 (&sc)[4]) {
+  const uint2 r0 = *reinterpret_cast<const uint2*>(record), r1 = *reinterpret_cast<const uint2*>(record + 16);
+  sc[0] = make_float2(lower(r0.x), lower(r1.x));
+  sc[1] = make_float2(upper(r0.x), upper(r1.x));
+  sc[2] = make_float2(lower(r0.y), lower(r1.y));
+  sc[3] = make_float2(upper(r0.y), upper(r1.y));
+}
+// Two f16 terms of two numbers.
+__device__ __forceinline__ void two_terms(float2 y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_half2(y.x, y.y);
+  const float2 rest = fma2(unpack_half2(hi), both(-1.0f), y);
+  lo = pack_half2(rest.x, rest.y);
+}
+// Codes i (of the four in each half) of two tokens' 16 bits, centred, times 2^-24 (odd i: 2^-20).
+__device__ __forceinline__ uint32_t centred_code(uint32_t w, int i) {
+  return centred((i < 2 ? w : w >> 8) & (i & 1 ? 0x00f000f0u : 0x000f000fu), i & 1 ? 0x80808080u : 0x80088008u);
+}
+
+// Up to 8 heads: tokens as rows, heads on the instruction's narrow side.
+//   S[token][head] = C . Q^T,  O^T[channel][head] += C^T . P^T
+// P is transposed between the two, 16 bits at a time.  (Heads as rows, half of them empty
+// or taken by P's second term, need no transposition, but twice the registers of O and
+// more instructions: HEADSUS.)
+template <int D>
+struct TokensInRows {
+  using At = Stage<D>;
+  static constexpr int kHeads = 8, kGroups = D / kQuantGroup;
+  const int lane, g, c4;
+  uint32_t k_at[kGroups / 2], v_at[kGroups / 2], z_at;  // what the lane reads of a tile
+  uint32_t qb[kGroups][4], xb[3];
+  float2 f;                 // of heads 2 c4 and + 1, as all that follows
+  float2 l, m, base;        // base: the maximum, 0 as long as there is none
+  float o[kGroups][2][4];   // channels 32 k + 4 g + 2 i and + 1 (rows g and g + 8; odd ones 16 times too large)
+  float oz[2][4];           // row g: what column g of the records adds up to, over the first 16 tokens of each tile; row g + 8 of
+                            // the second: over the others
+  float vref;               // power of two, not below the V scales and centres / 8 met
+
+  __device__ __forceinline__ TokensInRows(const KvView& kv, const PartArgs& a, int64_t head0, int this_lane)
+      : lane(this_lane), g(this_lane >> 2), c4(this_lane & 3), vref(kMinRef) {
+    const int mat = lane >> 3, mr = lane & 7;
+#pragma unroll
+    for (int k = 0; k < kGroups; k += 2) {
+      k_at[k / 2] = piece_at<D>(8 * (mat & 1) + mr, k + (mat >> 1));
+      v_at[k / 2] = At::kV + k_at[k / 2];
+    }
+    z_at = At::kRecV + 16 * (8 * (mat >> 1) + 16 * (mat & 1) + mr);  // tokens 0, 16, 8 and 24 on
+    uint4 raw[kGroups];
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k)
+      raw[k] = g < kv.group ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (head0 + g) * D + 32 * k + 8 * c4))
+                            : make_uint4(0u, 0u, 0u, 0u);
+    const Int4Query<kGroups> q(raw, a.scale, c4);
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qb[k][i] = q.q[k][i];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) xb[i] = q.terms[i];
+    f = make_float2(__shfl_sync(0xffffffffu, q.factor, 8 * c4), __shfl_sync(0xffffffffu, q.factor, 8 * c4 + 4));
+    l = base = both(0.0f);
+    m = both(-INFINITY);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      oz[0][e] = oz[1][e] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) o[k][0][e] = o[k][1][e] = 0.0f;
+    }
+  }
+
+  __device__ __forceinline__ void tile(const uint8_t* st, uint32_t st_addr, uint32_t live) {
+    // ---- logits (log2 units), 16 tokens at a time ----
+    float2 x[2][2];  // tokens 16 j + 8 e + g
+    uint32_t kr[4];  // the records, 8 tokens each
+    load4(st_addr + At::kRec + 16 * lane, kr);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float s[kGroups][4], add[4];
+#pragma unroll
+      for (int k2 = 0; k2 < kGroups; k2 += 2) {
+        uint32_t w[4];  // rows g and g + 8 of group k2, then of the next
+        load4(st_addr + k_at[k2 / 2] + j * (16 * At::kRow), w);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = k2 + h;
+          const uint32_t u = w[2 * h], v = w[2 * h + 1], u8 = u >> 8, v8 = v >> 8;
+          mma_bf16_0(s[k], u & 0x000f000fu, v & 0x000f000fu, u8 & 0x000f000fu, v8 & 0x000f000fu, qb[k][0], qb[k][1]);
+          mma_bf16(s[k], u & 0x00f000f0u, v & 0x00f000f0u, u8 & 0x00f000f0u, v8 & 0x00f000f0u, qb[k][2], qb[k][3]);
+        }
+      }
+      mma_bf16_0(add, kr[2 * j], kr[2 * j + 1], kr[2 * j], kr[2 * j + 1], xb[0], xb[1]);
+      mma_bf16(add, kr[2 * j], kr[2 * j + 1], 0u, 0u, xb[2], 0u);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint2 two = *reinterpret_cast<const uint2*>(st + At::kRec + 16 * (16 * j + 8 * e + g));
+        const float sc[4] = {lower(two.x), upper(two.x), lower(two.y), upper(two.y)};
+        float2 sum = make_float2(s[0][2 * e] * sc[0], s[0][2 * e + 1] * sc[0]);
+#pragma unroll
+        for (int k = 1; k < kGroups; ++k) {
+          sum.x = fmaf(s[k][2 * e], sc[k], sum.x);
+          sum.y = fmaf(s[k][2 * e + 1], sc[k], sum.y);
+        }
+        x[j][e] = fma2(sum, f, make_float2(add[2 * e], add[2 * e + 1]));
+      }
+    }
+    if (live != 0xffffffffu) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (!((live >> (8 * i + g)) & 1u)) x[i >> 1][i & 1] = both(-INFINITY);
+    }
+    float2 mn = make_float2(fmaxf(fmaxf(x[0][0].x, x[0][1].x), fmaxf(x[1][0].x, x[1][1].x)),
+                            fmaxf(fmaxf(x[0][0].y, x[0][1].y), fmaxf(x[1][0].y, x[1][1].y)));
+#pragma unroll
+    for (int i = 4; i < 32; i <<= 1) {
+      mn.x = fmaxf(mn.x, __shfl_xor_sync(0xffffffffu, mn.x, i));
+      mn.y = fmaxf(mn.y, __shfl_xor_sync(0xffffffffu, mn.y, i));
+    }
+    mn.x = fmaxf(mn.x, m.x);
+    mn.y = fmaxf(mn.y, m.y);
+    const bool raised = mn.x > m.x + kMargin || mn.y > m.y + kMargin;
+    const uint32_t vmax = largest_of<D>(st + At::kRecV, lane);
+    const uint32_t vcap = max(__float_as_uint(vref), min((vmax + 0x7fffffu) & 0x7f800000u, kMaxRef));
+    if (__any_sync(0xffffffffu, raised) || vcap != __float_as_uint(vref)) {
+      const float vnew = __uint_as_float(vcap), down = vref / vnew;
+      vref = vnew;
+      const float2 was = make_float2(m.x == -INFINITY ? 0.0f : exp2f(m.x - mn.x), m.y == -INFINITY ? 0.0f : exp2f(m.y - mn.y));
+      l = mul2(l, was);
+      m = mn;
+      base = make_float2(mn.x == -INFINITY ? 0.0f : mn.x, mn.y == -INFINITY ? 0.0f : mn.y);
+      const float2 by = mul2(was, both(down));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float y = e & 1 ? by.y : by.x;
+        oz[0][e] *= y;
+        oz[1][e] *= y;
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+          o[k][0][e] *= y;
+          o[k][1][e] *= y;
+        }
+      }
+    }
+    const float unit = unit_over(vref) * (1.0f / (1 << (kUnit - kUnit4)));
+
+    // ---- P, and O^T += C^T P^T, 16 tokens at a time ----
+    uint32_t zr[4];  // the records' columns: scales, then centres
+    load4_trans(st_addr + z_at, zr);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float2 p[2];  // of head g: tokens 16 j + 8 e + 2 c4 and + 1
+      uint32_t hi[2], lo[2];
+      float2 sc[2][4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float2 y = add2(x[j][e], make_float2(-base.x, -base.y));
+        const float2 w = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+        l = add2(l, w);
+        const float2 in = mul2(w, both(unit));
+        const uint32_t a = __float_as_uint(in.x), b = __float_as_uint(in.y);
+        const uint32_t up = transpose8x8(__byte_perm(a, b, 0x7632)), down = transpose8x8(__byte_perm(a, b, 0x5410));
+        p[e] = make_float2(__uint_as_float(__byte_perm(down, up, 0x5410)), __uint_as_float(__byte_perm(down, up, 0x7632)));
+        hi[e] = pack_bf16(p[e].x, p[e].y);
+        lo[e] = pack_bf16(p[e].x - lower(hi[e]), p[e].y - upper(hi[e]));
+        scale_pairs(st + At::kRecV + 32 * c4 + 16 * (16 * j + 8 * e), sc[e]);
+      }
+      mma_bf16(oz[j], zr[0], zr[1], zr[2], zr[3], hi[0], hi[1]);
+      mma_bf16(oz[j], zr[0], zr[1], zr[2], zr[3], lo[0], lo[1]);
+#pragma unroll
+      for (int k2 = 0; k2 < kGroups; k2 += 2) {
+        uint32_t w[4];  // tokens 16 j .. + 7 and + 8 .. + 15 of groups k2 and k2 + 1
+        load4_trans(st_addr + v_at[k2 / 2] + j * (16 * At::kRow), w);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = k2 + h;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) two_terms(mul2(p[e], sc[e][k]), hi[e], lo[e]);
+          const uint32_t w0 = w[2 * h], w1 = w[2 * h + 1];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t a0 = centred_code(w0, 2 * i), a1 = centred_code(w0, 2 * i + 1);
+            const uint32_t a2 = centred_code(w1, 2 * i), a3 = centred_code(w1, 2 * i + 1);
+            mma_f16(o[k][i], a0, a1, a2, a3, hi[0], hi[1]);
+            mma_f16(o[k][i], a0, a1, a2, a3, lo[0], lo[1]);
+          }
+        }
+      }
+    }
+  }
+
+  // The warp's state: outputs in units of 2^-kUnit of the reference.
+  __device__ __forceinline__ void state(float* so, float* s_m, float* s_l, float* s_ref) const {
+    float2 sum = l;
+#pragma unroll
+    for (int i = 4; i < 32; i <<= 1) {
+      sum.x += __shfl_xor_sync(0xffffffffu, sum.x, i);
+      sum.y += __shfl_xor_sync(0xffffffffu, sum.y, i);
+    }
+    if (lane == 0) *s_ref = vref;
+    if (g == 0) {
+      s_m[2 * c4] = m.x;
+      s_m[2 * c4 + 1] = m.y;
+      s_l[2 * c4] = sum.x;
+      s_l[2 * c4 + 1] = sum.y;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float col = oz[0][e] + oz[1][2 + e];
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {
+        const float z = __shfl_sync(0xffffffffu, col, 4 * (kGroups + k) + c4);  // centre k is column kGroups + k
+        constexpr float kBack = static_cast<float>(1 << (kUnit - kUnit4));
+        *reinterpret_cast<float4*>(so + (2 * c4 + e) * D + 32 * k + 4 * g) =
+            make_float4(fmaf(o[k][0][e], 16777216.0f, z) * kBack, fmaf(o[k][0][2 + e], 1048576.0f, z) * kBack,
+                        fmaf(o[k][1][e], 16777216.0f, z) * kBack, fmaf(o[k][1][2 + e], 1048576.0f, z) * kBack);
+      }
+    }
+  }
+};
+
+// 16 heads: heads as rows.
+//   S[head][token] = Q . C^T,  O[head][channel] += P . C
+// S lies in a lane's registers as P is wanted, and nothing but the maxima is exchanged
+// between lanes.
+template <int D>
+struct HeadsInRows {
+  using At = Stage<D>;
+  static constexpr int kHeads = 16, kGroups = D / kQuantGroup;
+  const int lane, g, c4;
+  uint32_t k_at, v_at[kGroups / 2];  // what the lane reads of a tile
+  uint32_t qa[2][kGroups][4], xa[2][3];
+  float f[2];                // of heads g and g + 8, as all that follows
+  float2 l[2];
+  float m[2], base[2];       // base: the maximum, 0 as long as there is none
+  float o[kGroups][4][4];    // channels 32 k + 4 (2 c4 + e) + i (odd i 16 times too large)
+  float oz[4];               // what columns 2 c4 and + 1 of the records add up to
+  float vref;                // power of two, not below the V scales and centres / 8 met
+
+  __device__ __forceinline__ HeadsInRows(const KvView& kv, const PartArgs& a, int64_t head0, int this_lane)
+      : lane(this_lane), g(this_lane >> 2), c4(this_lane & 3), vref(kMinRef) {
+    const int mat = lane >> 3, mr = lane & 7;
+    k_at = D == 128 ? piece_at<D>(mr, mat) : piece_at<D>(8 * (mat >> 1) + mr, mat & 1);  // (every 8th row is permuted alike)
+#pragma unroll
+    for (int k = 0; k < kGroups; k += 2) v_at[k / 2] = At::kV + piece_at<D>(8 * (mat & 1) + mr, k + (mat >> 1));
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      uint4 raw[kGroups];
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k)
+        raw[k] = nt * 8 + g < kv.group ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                                             (head0 + nt * 8 + g) * D + 32 * k + 8 * c4))
+                                       : make_uint4(0u, 0u, 0u, 0u);
+      const Int4Query<kGroups> q(raw, a.scale, c4);
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qa[nt][k][i] = q.q[k][i];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) xa[nt][i] = q.terms[i];
+      f[nt] = q.factor;
+      l[nt] = both(0.0f);
+      m[nt] = -INFINITY;
+      base[nt] = 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      oz[e] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[k][i][e] = 0.0f;
+    }
+  }
+
+  __device__ __forceinline__ void tile(const uint8_t* st, uint32_t st_addr, uint32_t live) {
+    // ---- logits (log2 units) of 8 tokens at a time ----
+    float2 x[2][4];  // tokens 8 i + 2 c4, 8 i + 2 c4 + 1
+    uint32_t kw[4];  // codes of the 8 tokens' four groups, or of 16 tokens' two
+    uint32_t kr[4];  // the records, 8 tokens each
+    load4(st_addr + At::kRec + 16 * lane, kr);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (D == 128 || i % 2 == 0) load4(st_addr + k_at + i * (8 * At::kRow), kw);
+      float s[kGroups][4], sz[4];
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {
+        const uint32_t v = kw[D == 128 ? k : 2 * (i % 2) + k], v8 = v >> 8;
+        mma_bf16_0(s[k], qa[0][k][0], qa[1][k][0], qa[0][k][1], qa[1][k][1], v & 0x000f000fu, v8 & 0x000f000fu);
+        mma_bf16(s[k], qa[0][k][2], qa[1][k][2], qa[0][k][3], qa[1][k][3], v & 0x00f000f0u, v8 & 0x00f000f0u);
+      }
+      mma_bf16_0(sz, xa[0][0], xa[1][0], xa[0][1], xa[1][1], kr[i], kr[i]);
+      mma_bf16(sz, xa[0][2], xa[1][2], 0u, 0u, kr[i], kr[i]);
+      float2 sc[4];
+      scale_pairs(st + At::kRec + 32 * c4 + 128 * i, sc);
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        float2 sum = mul2(make_float2(s[0][2 * nt], s[0][2 * nt + 1]), sc[0]);
+#pragma unroll
+        for (int k = 1; k < kGroups; ++k) sum = fma2(make_float2(s[k][2 * nt], s[k][2 * nt + 1]), sc[k], sum);
+        x[nt][i] = fma2(sum, both(f[nt]), make_float2(sz[2 * nt], sz[2 * nt + 1]));
+      }
+    }
+    if (live != 0xffffffffu) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          if (!((live >> (8 * i + 2 * c4)) & 1u)) x[nt][i].x = -INFINITY;
+          if (!((live >> (8 * i + 2 * c4 + 1)) & 1u)) x[nt][i].y = -INFINITY;
+        }
+    }
+    bool raised = false;
+    float mn[2];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      float top = fmaxf(fmaxf(fmaxf(x[nt][0].x, x[nt][0].y), fmaxf(x[nt][1].x, x[nt][1].y)),
+                        fmaxf(fmaxf(x[nt][2].x, x[nt][2].y), fmaxf(x[nt][3].x, x[nt][3].y)));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      mn[nt] = fmaxf(m[nt], top);
+      raised |= mn[nt] > m[nt] + kMargin;
+    }
+    const uint32_t vmax = largest_of<D>(st + At::kRecV, lane);
+    const uint32_t vcap = max(__float_as_uint(vref), min((vmax + 0x7fffffu) & 0x7f800000u, kMaxRef));
+    if (__any_sync(0xffffffffu, raised) || vcap != __float_as_uint(vref)) {
+      const float vnew = __uint_as_float(vcap), down = vref / vnew;
+      vref = vnew;
+      float by[2];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        const float was = m[nt] == -INFINITY ? 0.0f : exp2f(m[nt] - mn[nt]);
+        l[nt] = mul2(l[nt], both(was));
+        m[nt] = mn[nt];
+        base[nt] = mn[nt] == -INFINITY ? 0.0f : mn[nt];
+        by[nt] = was * down;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        oz[e] *= by[e >> 1];
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[k][i][e] *= by[e >> 1];
+      }
+    }
+    const float unit = unit_over(vref) * (1.0f / (1 << (kUnit - kUnit4)));
+
+    // ---- P, and O += P C, 16 tokens at a time ----
+    uint32_t zr[4];  // the records' columns: scales, then centres
+    load4_trans(st_addr + At::kRecV + 16 * lane, zr);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float2 p[2][2];  // tokens 16 j + 2 c4 and + 1, 8 more
+      uint32_t hi[2][2], lo[2][2];
+      float2 sc[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          const float2 y = add2(x[nt][2 * j + i], both(-base[nt]));
+          p[nt][i] = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+          l[nt] = add2(l[nt], p[nt][i]);
+          p[nt][i] = mul2(p[nt][i], both(unit));
+          hi[nt][i] = pack_bf16(p[nt][i].x, p[nt][i].y);
+          lo[nt][i] = pack_bf16(p[nt][i].x - lower(hi[nt][i]), p[nt][i].y - upper(hi[nt][i]));
+        }
+        scale_pairs(st + At::kRecV + 32 * c4 + 16 * (16 * j + 8 * i), sc[i]);
+      }
+      mma_bf16(oz, hi[0][0], hi[1][0], hi[0][1], hi[1][1], zr[2 * j], zr[2 * j + 1]);
+      mma_bf16(oz, lo[0][0], lo[1][0], lo[0][1], lo[1][1], zr[2 * j], zr[2 * j + 1]);
+#pragma unroll
+      for (int k2 = 0; k2 < kGroups; k2 += 2) {
+        uint32_t w[4];  // tokens 16 j .. + 7 and + 8 .. + 15 of groups k2 and k2 + 1
+        load4_trans(st_addr + v_at[k2 / 2] + j * (16 * At::kRow), w);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = k2 + h;
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) two_terms(mul2(p[nt][i], sc[i][k]), hi[nt][i], lo[nt][i]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t b0 = centred_code(w[2 * h], i), b1 = centred_code(w[2 * h + 1], i);
+            mma_f16(o[k][i], hi[0][0], hi[1][0], hi[0][1], hi[1][1], b0, b1);
+            mma_f16(o[k][i], lo[0][0], lo[1][0], lo[0][1], lo[1][1], b0, b1);
+          }
+        }
+      }
+    }
+  }
+
+  // The warp's state: outputs in units of 2^-kUnit of the reference.
+  __device__ __forceinline__ void state(float* so, float* s_m, float* s_l, float* s_ref) const {
+    if (lane == 0) *s_ref = vref;
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      float sum = l[nt].x + l[nt].y;
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const int h = nt * 8 + g;
+      if (c4 == 0) {
+        s_m[h] = m[nt];
+        s_l[h] = sum;
+      }
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {
+        // centre k is column kGroups + k: lane (kGroups + k) / 2 of the head's four
+        const float z = __shfl_sync(0xffffffffu, k & 1 ? oz[2 * nt + 1] : oz[2 * nt], (lane & ~3) | ((kGroups + k) >> 1));
+        constexpr float kBack = static_cast<float>(1 << (kUnit - kUnit4));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int at = 2 * nt + e;
+          *reinterpret_cast<float4*>(so + h * D + 32 * k + 4 * (2 * c4 + e)) =
+              make_float4(fmaf(o[k][0][at], 16777216.0f, z) * kBack, fmaf(o[k][1][at], 1048576.0f, z) * kBack,
+                          fmaf(o[k][2][at], 16777216.0f, z) * kBack, fmaf(o[k][3][at], 1048576.0f, z) * kBack);
+        }
+      }
+    }
+  }
+};
+
 template <int D, int NT>
 __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int4_kernel(KvView kv, PartArgs a, unsigned* err) {
   constexpr int kTeams = teams_of(D, NT), kWarps = kTeams * kTeamWarps;
   using At = Stage<D>;
-  constexpr int kGroups = D / kQuantGroup;
+  using Math = std::conditional_t<NT == 1, TokensInRows<D>, HeadsInRows<D>>;
   constexpr int kPieces = At::kRow / 16;  // 16-byte pieces of a row, a group of channels each
   constexpr int kRowsPer = 32 / kPieces;  // rows one copy instruction of a warp covers
   extern __shared__ __align__(1024) uint8_t ring[];
@@ -109,8 +540,6 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) s_empty = 0;
   __syncthreads();
-  const int g = lane >> 2, c4 = lane & 3;
-  const int G = kv.group;
   const int ctas = gridDim.x;
 
   const Team cta{tid, kWarps, 0};
@@ -142,13 +571,6 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
   const uint8_t* v_codes = static_cast<const uint8_t*>(kv.v_pages) + 16 * lane;
   const uint8_t* k_recs = reinterpret_cast<const uint8_t*>(kv.k_scales);
   const uint8_t* v_recs = reinterpret_cast<const uint8_t*>(kv.v_scales);
-  // what it reads: row lane % 8 of matrix lane / 8
-  const int mat = lane >> 3, mr = lane & 7;
-  // (every 8th row is permuted alike)
-  const uint32_t k_at = D == 128 ? piece_at<D>(mr, mat) : piece_at<D>(8 * (mat >> 1) + mr, mat & 1);
-  uint32_t v_at[kGroups / 2];
-#pragma unroll
-  for (int k = 0; k < kGroups; k += 2) v_at[k / 2] = At::kV + piece_at<D>(8 * (mat & 1) + mr, k + (mat >> 1));
 
   const int my_parts = (all_parts - slot + cut.slots - 1) / cut.slots;
   for (int n_part = 0; n_part < my_parts; ++n_part) {
@@ -162,17 +584,6 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
     const int pair_tiles = tiles_of(kv, cnt), each = pair_tiles / part.count, more = pair_tiles - each * part.count;
     const int seg0 = part.index * each + min(part.index, more), seg_tiles = each + (part.index < more ? 1 : 0);
     const int b = part.pair / kv.hkv, kvh = part.pair - b * kv.hkv;
-    // the query's loads go out ahead of the rows'
-    uint4 q_raw[NT][kGroups];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int k = 0; k < kGroups; ++k) {
-        q_raw[nt][k] = make_uint4(0u, 0u, 0u, 0u);
-        if (nt * 8 + g < G)
-          q_raw[nt][k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                                              (static_cast<int64_t>(b) * kv.hq + kvh * G + nt * 8 + g) * D + 32 * k + 8 * c4));
-      }
     // The warp's tiles: a run of the part.
     const int run0 = seg0 + seg_tiles * team_warp / team.warps;
     const int tiles = seg0 + seg_tiles * (team_warp + 1) / team.warps - run0;
@@ -238,74 +649,7 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
       copies_commit();
     }
 
-    // ---- the query, as first operands ----
-    uint32_t qa[NT][kGroups][4];  // even channels 0 4 and 2 6 of a lane's 8, then the odd ones by 1/16
-    uint32_t xa[NT][3];           // three bf16 terms of what scale or centre word c4 of a record is multiplied by
-    float f[NT];                  // from S times the scale to a logit (log2 units)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float amax = 0.0f, sum[kGroups], x[kGroups][8];
-#pragma unroll
-      for (int k = 0; k < kGroups; ++k) {
-        const uint32_t w[4] = {q_raw[nt][k].x, q_raw[nt][k].y, q_raw[nt][k].z, q_raw[nt][k].w};
-        sum[k] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[k][2 * i] = lower(w[i]);
-          x[k][2 * i + 1] = upper(w[i]);
-          amax = fmaxf(amax, fmaxf(fabsf(x[k][2 * i]), fabsf(x[k][2 * i + 1])));
-          sum[k] += x[k][2 * i] + x[k][2 * i + 1];
-        }
-        sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
-        sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
-      }
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // times 2^e, the largest entry in [2^100, 2^101) where e is from 10 to 127
-      const int e = min(max(227 - static_cast<int>(__float_as_uint(amax) >> 23), 10), 127);
-      const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-      f[nt] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(133 - e + 127) << 23);
-#pragma unroll
-      for (int k = 0; k < kGroups; ++k) {
-        qa[nt][k][0] = pack_bf16(x[k][0] * up, x[k][4] * up);
-        qa[nt][k][1] = pack_bf16(x[k][2] * up, x[k][6] * up);
-        qa[nt][k][2] = pack_bf16(x[k][1] * up * 0.0625f, x[k][5] * up * 0.0625f);
-        qa[nt][k][3] = pack_bf16(x[k][3] * up * 0.0625f, x[k][7] * up * 0.0625f);
-      }
-      // a record's words: scales of groups 0 1 (and 2 3), then the centres; -8 sum q for
-      // a scale, sum q for a centre
-      constexpr int kWords = kGroups / 2;  // of scales
-      const int pair = c4 & (kWords - 1);
-      const float by = a.scale * kLog2e * (c4 < kWords ? -8.0f : c4 < 2 * kWords ? 1.0f : 0.0f);
-      float r0 = (pair ? sum[kGroups - 2] : sum[0]) * by, r1 = (pair ? sum[kGroups - 1] : sum[1]) * by;
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        xa[nt][i] = pack_bf16(r0, r1);
-        r0 -= lower(xa[nt][i]);
-        r1 -= upper(xa[nt][i]);
-      }
-    }
-
-    float2 l[NT];
-    float m[NT], base[NT];         // base: the maximum, 0 as long as there is none
-    float o[kGroups][4][4];        // rows g and g + 8 (up to 8 heads: P's second term), channels 32 k + 4 (2 c4 + e) + i
-    float oz[4];                   // the centres' sums: column kGroups + k of the record
-    float vref = kMinRef;          // power of two, not below the V scales and centres / 8 met
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      m[nt] = -INFINITY;
-      base[nt] = 0.0f;
-      l[nt] = both(0.0f);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      oz[e] = 0.0f;
-#pragma unroll
-      for (int k = 0; k < kGroups; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[k][i][e] = 0.0f;
-    }
-
+    Math math(kv, a, static_cast<int64_t>(b) * kv.hq + kvh * kv.group, lane);
     int stage = 0;
     for (int n = 0; n < tiles; ++n) {
       __syncwarp();  // the stage about to be filled has been read by every lane
@@ -316,213 +660,15 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
       copies_commit();
       copies_wait<kStages - 1>();
       __syncwarp();
-      const uint8_t* st = my_ring + stage * At::kBytes;
-      const uint32_t st_addr = ring_addr + stage * At::kBytes;
-      const uint32_t live = s_live[warp][stage];
-
-      // ---- logits (log2 units) of 8 tokens at a time ----
-      float2 x[NT][4];    // tokens 8 i + 2 c4, 8 i + 2 c4 + 1 of head g (and g + 8)
-      uint32_t kw[4];     // codes of the 8 tokens' four groups, or of 16 tokens' two
-      uint32_t kr[4];     // the records, 8 tokens each
-      load4(st_addr + At::kRec + 16 * lane, kr);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (D == 128)
-          load4(st_addr + k_at + i * (8 * At::kRow), kw);
-        else if (i % 2 == 0)
-          load4(st_addr + k_at + i * (8 * At::kRow), kw);
-        float s[kGroups][4], sz[4];
-        float odd[kGroups][4];
-#pragma unroll
-        for (int k = 0; k < kGroups; ++k) {
-          const uint32_t v = kw[D == 128 ? k : 2 * (i % 2) + k], v8 = v >> 8;
-          if constexpr (NT == 1) {
-            mma_bf16_0(s[k], qa[0][k][0], qa[0][k][2], qa[0][k][1], qa[0][k][3], v & 0x000f000fu, v8 & 0x000f000fu);
-            mma_bf16_0(odd[k], qa[0][k][0], qa[0][k][2], qa[0][k][1], qa[0][k][3], v & 0x00f000f0u, v8 & 0x00f000f0u);
-          } else {
-            mma_bf16_0(s[k], qa[0][k][0], qa[NT - 1][k][0], qa[0][k][1], qa[NT - 1][k][1], v & 0x000f000fu, v8 & 0x000f000fu);
-            mma_bf16(s[k], qa[0][k][2], qa[NT - 1][k][2], qa[0][k][3], qa[NT - 1][k][3], v & 0x00f000f0u, v8 & 0x00f000f0u);
-          }
-        }
-        if constexpr (NT == 1) {
-          mma_bf16_0(sz, xa[0][0], xa[0][2], xa[0][1], 0u, kr[i], kr[i]);
-        } else {
-          mma_bf16_0(sz, xa[0][0], xa[NT - 1][0], xa[0][1], xa[NT - 1][1], kr[i], kr[i]);
-          mma_bf16(sz, xa[0][2], xa[NT - 1][2], 0u, 0u, kr[i], kr[i]);
-        }
-        const uint8_t* rec = st + At::kRec + 32 * c4 + 128 * i;
-        // the scales of tokens 8 i + 2 c4 and + 1
-        const uint2 r0 = *reinterpret_cast<const uint2*>(rec), r1 = *reinterpret_cast<const uint2*>(rec + 16);
-        float2 sc[4];
-        sc[0] = make_float2(lower(r0.x), lower(r1.x));
-        sc[1] = make_float2(upper(r0.x), upper(r1.x));
-        sc[2] = make_float2(lower(r0.y), lower(r1.y));
-        sc[3] = make_float2(upper(r0.y), upper(r1.y));
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const auto of = [&](int k) {
-            const float2 even = make_float2(s[k][2 * nt], s[k][2 * nt + 1]);
-            return NT == 1 ? add2(even, make_float2(odd[k][2], odd[k][3])) : even;
-          };
-          const float2 affine = make_float2(sz[2 * nt], sz[2 * nt + 1]);
-          float2 sum = mul2(of(0), sc[0]);
-#pragma unroll
-          for (int k = 1; k < kGroups; ++k) sum = fma2(of(k), sc[k], sum);
-          x[nt][i] = fma2(sum, both(f[nt]), NT == 1 ? add2(affine, make_float2(sz[2], sz[3])) : affine);
-        }
-      }
-      if (live != 0xffffffffu) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          for (int nt = 0; nt < NT; ++nt) {
-            if (!((live >> (8 * i + 2 * c4)) & 1u)) x[nt][i].x = -INFINITY;
-            if (!((live >> (8 * i + 2 * c4 + 1)) & 1u)) x[nt][i].y = -INFINITY;
-          }
-      }
-      bool raised = false;
-      float mn[NT];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float top = fmaxf(fmaxf(fmaxf(x[nt][0].x, x[nt][0].y), fmaxf(x[nt][1].x, x[nt][1].y)),
-                          fmaxf(fmaxf(x[nt][2].x, x[nt][2].y), fmaxf(x[nt][3].x, x[nt][3].y)));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        mn[nt] = fmaxf(m[nt], top);
-        raised |= mn[nt] > m[nt] + kMargin;
-      }
-      uint32_t vmax;
-      {
-        const uint4 r = *reinterpret_cast<const uint4*>(st + At::kRecV + 16 * lane);
-        const auto wide = [](uint32_t p, uint32_t q) { return fmaxf(fmaxf(fabsf(lower(p)), fabsf(upper(p))), fmaxf(fabsf(lower(q)), fabsf(upper(q)))); };
-        const float top = D == 128 ? fmaxf(wide(r.x, r.y), 0.125f * wide(r.z, r.w)) : fmaxf(wide(r.x, r.x), 0.125f * wide(r.y, r.y));
-        vmax = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(top, 0.0f)));  // (NaN: 0)
-      }
-      const uint32_t vcap = max(__float_as_uint(vref), min((vmax + 0x7fffffu) & 0x7f800000u, kMaxRef));
-      if (__any_sync(0xffffffffu, raised) || vcap != __float_as_uint(vref)) {
-        const float vnew = __uint_as_float(vcap);
-        const float down = vref / vnew;
-        vref = vnew;
-        float by[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float was = m[nt] == -INFINITY ? 0.0f : exp2f(m[nt] - mn[nt]);
-          l[nt] = mul2(l[nt], both(was));
-          m[nt] = mn[nt];
-          base[nt] = mn[nt] == -INFINITY ? 0.0f : mn[nt];
-          by[nt] = was * down;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float y = by[(e >> 1) * (NT - 1)];
-          oz[e] *= y;
-#pragma unroll
-          for (int k = 0; k < kGroups; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[k][i][e] *= y;
-        }
-      }
-      const float unit = unit_over(vref) * (1.0f / (1 << (kUnit - kUnit4)));
-
-      // ---- P, and O += P C, 16 tokens at a time ----
-      uint32_t zr[4];  // records: scales in the first columns, centres behind them
-      load4_trans(st_addr + At::kRecV + 16 * lane, zr);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float2 p[NT][2];  // tokens 16 j + 2 c4 and + 1, 8 more
-        uint32_t hi[NT][2], lo[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float2 y = add2(x[nt][2 * j + i], both(-base[nt]));
-            p[nt][i] = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-            l[nt] = add2(l[nt], p[nt][i]);
-            p[nt][i] = mul2(p[nt][i], both(unit));
-            hi[nt][i] = pack_bf16(p[nt][i].x, p[nt][i].y);
-            lo[nt][i] = pack_bf16(p[nt][i].x - lower(hi[nt][i]), p[nt][i].y - upper(hi[nt][i]));
-          }
-        if constexpr (NT == 1) {
-          mma_bf16(oz, hi[0][0], lo[0][0], hi[0][1], lo[0][1], zr[2 * j], zr[2 * j + 1]);
-        } else {
-          mma_bf16(oz, hi[0][0], hi[NT - 1][0], hi[0][1], hi[NT - 1][1], zr[2 * j], zr[2 * j + 1]);
-          mma_bf16(oz, lo[0][0], lo[NT - 1][0], lo[0][1], lo[NT - 1][1], zr[2 * j], zr[2 * j + 1]);
-        }
-        float2 sc[2][4];  // the tokens' scales
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint8_t* rec = st + At::kRecV + 32 * c4 + 16 * (16 * j + 8 * i);
-          const uint2 r0 = *reinterpret_cast<const uint2*>(rec), r1 = *reinterpret_cast<const uint2*>(rec + 16);
-          sc[i][0] = make_float2(lower(r0.x), lower(r1.x));
-          sc[i][1] = make_float2(upper(r0.x), upper(r1.x));
-          sc[i][2] = make_float2(lower(r0.y), lower(r1.y));
-          sc[i][3] = make_float2(upper(r0.y), upper(r1.y));
-        }
-#pragma unroll
-        for (int k2 = 0; k2 < kGroups; k2 += 2) {
-          uint32_t w[4];  // tokens 16 j .. + 7 and + 8 .. + 15 of groups k2 and k2 + 1
-          load4_trans(st_addr + v_at[k2 / 2] + j * (16 * At::kRow), w);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int k = k2 + h;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const float2 y = mul2(p[nt][i], sc[i][k]);
-                hi[nt][i] = pack_half2(y.x, y.y);
-                const float2 rest = fma2(unpack_half2(hi[nt][i]), both(-1.0f), y);
-                lo[nt][i] = pack_half2(rest.x, rest.y);
-              }
-            const uint32_t w0 = w[2 * h], w1 = w[2 * h + 1];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t mask = i & 1 ? 0x00f000f0u : 0x000f000fu;
-              const uint32_t minus = i & 1 ? 0x80808080u : 0x80088008u;  // -8 times 2^-20, 2^-24
-              const uint32_t b0 = centred((i < 2 ? w0 : w0 >> 8) & mask, minus);
-              const uint32_t b1 = centred((i < 2 ? w1 : w1 >> 8) & mask, minus);
-              if constexpr (NT == 1) {
-                mma_f16(o[k][i], hi[0][0], lo[0][0], hi[0][1], lo[0][1], b0, b1);
-              } else {
-                mma_f16(o[k][i], hi[0][0], hi[NT - 1][0], hi[0][1], hi[NT - 1][1], b0, b1);
-                mma_f16(o[k][i], lo[0][0], lo[NT - 1][0], lo[0][1], lo[NT - 1][1], b0, b1);
-              }
-            }
-          }
-        }
-      }
+      math.tile(my_ring + stage * At::kBytes, ring_addr + stage * At::kBytes, s_live[warp][stage]);
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     copies_wait<0>();
 
     // ---- the warps' states joined ----
     team.sync();  // every warp is done with its ring: the team's rings now hold the outputs
-    if (lane == 0) s_ref[warp] = vref;
-    float* so = reinterpret_cast<float*>(ring + first_warp * (kStages * At::kBytes));  // [team warp][8 NT][D]
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float sum = l[nt].x + l[nt].y;
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      const int h = nt * 8 + g;
-      if (c4 == 0) {
-        s_m[warp][h] = m[nt];
-        s_l[warp][h] = sum;
-      }
-      // centre k is column kGroups + k: lane (kGroups + k) / 2 of the head's four
-      const float z0 = NT == 1 ? oz[0] + oz[2] : oz[2 * nt], z1 = NT == 1 ? oz[1] + oz[3] : oz[2 * nt + 1];
-#pragma unroll
-      for (int k = 0; k < kGroups; ++k) {
-        const float z = __shfl_sync(0xffffffffu, k & 1 ? z1 : z0, (lane & ~3) | ((kGroups + k) >> 1));
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float y[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            y[i] = fmaf(NT == 1 ? o[k][i][e] + o[k][i][2 + e] : o[k][i][2 * nt + e], i & 1 ? 1048576.0f : 16777216.0f, z) * static_cast<float>(1 << (kUnit - kUnit4));
-          *reinterpret_cast<float4*>(so + (team_warp * 8 * NT + h) * D + 32 * k + 4 * (2 * c4 + e)) = make_float4(y[0], y[1], y[2], y[3]);
-        }
-      }
-    }
+    float* so = reinterpret_cast<float*>(ring + first_warp * (kStages * At::kBytes));  // [team warp][heads][D]
+    math.state(so + team_warp * Math::kHeads * D, s_m[warp], s_l[warp], &s_ref[warp]);
     team.sync();
     finish_part<D, NT>(kv, a, team, part, s_m + first_warp, s_l + first_warp, s_ref + first_warp, so, &s_last[tm]);
     team.sync();  // the rings and s_m are free again

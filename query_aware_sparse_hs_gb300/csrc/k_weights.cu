@@ -184,44 +184,18 @@ __global__ __launch_bounds__(Row<D, KIND>::kWarps * 32, 1) void weights_kernel(K
           for (int h = 0; h < 2; ++h)
             qb[nt][i][h] = head ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * i + 8 * h + 2 * c4)) : 0u;
       } else if constexpr (KIND == HS_KV_INT4_G32) {  // channels 32 k + 8 c4 .. + 7
-        float amax = 0.0f, sum[kGroups], x[kGroups][8];
-#pragma unroll
-        for (int k = 0; k < kGroups; ++k) {
-          const uint4 v = head ? __ldg(reinterpret_cast<const uint4*>(src + 32 * k + 8 * c4)) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          sum[k] = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[k][2 * i] = lower(w[i]);
-            x[k][2 * i + 1] = upper(w[i]);
-            amax = fmaxf(amax, fmaxf(fabsf(x[k][2 * i]), fabsf(x[k][2 * i + 1])));
-            sum[k] += x[k][2 * i] + x[k][2 * i + 1];
-          }
-          sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
-          sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const int e = min(max(227 - static_cast<int>(__float_as_uint(amax) >> 23), 10), 127);
-        const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+        uint4 raw[kGroups];
 #pragma unroll
         for (int k = 0; k < kGroups; ++k)
+          raw[k] = head ? __ldg(reinterpret_cast<const uint4*>(src + 32 * k + 8 * c4)) : make_uint4(0u, 0u, 0u, 0u);
+        const Int4Query<kGroups> mine(raw, a.scale, c4);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {  // (odd channels by 1/16)
-            qb[nt][2 * k][h] = pack_bf16(x[k][2 * h] * up, x[k][2 * h + 4] * up);
-            qb[nt][2 * k + 1][h] = pack_bf16(x[k][2 * h + 1] * up * 0.0625f, x[k][2 * h + 5] * up * 0.0625f);
-          }
-        constexpr int kWords = kGroups / 2;
-        const int two = c4 & (kWords - 1);
-        const float by = factor * (c4 < kWords ? -8.0f : c4 < 2 * kWords ? 1.0f : 0.0f);
-        float r0 = (two ? sum[kGroups - 2] : sum[0]) * by, r1 = (two ? sum[kGroups - 1] : sum[1]) * by;
+        for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          xb[nt][i] = pack_bf16(r0, r1);
-          r0 -= lower(xb[nt][i]);
-          r1 -= upper(xb[nt][i]);
-        }
-        factor *= __uint_as_float(static_cast<uint32_t>(133 - e + 127) << 23);
+          for (int h = 0; h < 2; ++h) qb[nt][i][h] = mine.q[i / 2][2 * (i % 2) + h];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) xb[nt][i] = mine.terms[i];
+        factor = mine.factor;
       } else {  // channels 16 i + 4 c4 .. + 3
         uint2 v[kSteps];
         float amax = 0.0f;
