@@ -8,16 +8,10 @@
 // (attn_parts.cuh): a warp takes a run of 32-token tiles through its own ring in shared
 // memory, filled by asynchronous copies.
 //
-// Products on the warp-level matrix instruction m16n8k16, rows of A = query heads:
-//   S[head][token] = Q . C^T   bf16, a group of 32 channels (two instructions) at a time,
-//     because every token's group has its own scale;
-//   O[head][channel] += P . C  f16, over 16 tokens.
-// Heads as rows: S lies in a lane's registers as P is wanted, so nothing is exchanged
-// between lanes but the maxima.  Up to 8 heads leave half of the rows: P's second term
-// goes there, which makes the two terms one instruction, and the q of the odd channels,
-// so that an operand is four registers of its own (an instruction for even channels
-// gives the first half of the rows, one for odd channels the second; with q in both
-// halves the copies of registers cost 5%).
+// Products on the warp-level matrix instruction m16n8k16: q and codes in bf16, a group of
+// 32 channels (two instructions) at a time, because every token's group has its own scale;
+// P times scales and codes in f16, over 16 tokens.  Up to 8 heads are the instruction's
+// narrow side, 16 its rows.
 //
 // Codes become operands without a conversion.  A lane loads 8 of them as a word;
 // masking 4 bits out of either half of it gives two numbers n = c + 8:
@@ -33,14 +27,13 @@
 // P for V, goes with the record as it lies in memory, in instructions of its own: three
 // bf16 terms of the sums, two of P.
 //
-// What bounds it: the matrix, integer and fp32 pipes in turn (30%, 45% and 25% busy;
-// 866 instructions for 32 tokens of 128 channels, 8 heads, a third of them V's codes and
-// P times s, 2.2 of 4 issued a cycle): 16 requests x 4 heads x 131072 tokens, 1.34 GB, 318
-// us, 0.62 of the copy rate; 64 channels 218 us for half of that (0.45).  32 requests x
-// 4096 selected tokens: 32.0 us, of which the chain of lookups before the stream and
-// the join behind it are 8; 12 uneven requests of 16 heads, 64 channels: 32.5.  8 warps an
-// SM instead of 12: 442 us; 16 for 64 channels: no faster; fp32 sums one at a time instead
-// of in pairs: 322; two stages instead of three: 315; without the copies 0.85 of the time.
+// What bounds it: the matrix, integer and fp32 pipes in turn, none of them busy half of
+// the time, with instructions waiting for each other in between: 16 requests x 4 heads x
+// 131072 tokens, 1.34 GB, 280 us, 0.71 of the copy rate; 64 channels 206 us for half of
+// that (0.48); 16 heads 254 us for half (0.39).  32 requests x 4096 selected tokens: 30.0
+// us, of which the chain of lookups before the stream and the join behind it are 8; 12
+// uneven requests of 16 heads, 64 channels: 33.9.  (Heads as rows for up to 8 heads, with
+// half of the rows empty or taken by P's second term and O in twice the registers: 318.)
 //
 // Precision: q is exact (bf16, times a power of two, which takes entries up to 2^90), S
 // and all sums fp32.  P times s, in units of 2^-13 of the reference (the largest power of
@@ -58,7 +51,9 @@ namespace {
 
 using namespace parts;
 
-constexpr int kStages = 3;  // tiles in a warp's ring
+// Tiles in a warp's ring: 128 channels, two 280 us, three 282 (16 requests x 4 heads x
+// 131072 tokens); 64 channels 210 and 206.
+__host__ __device__ constexpr int stages_of(int head_dim) { return head_dim == 128 ? 2 : 3; }
 // Logits may pass the running maximum by so much (log2 units) before the state is
 // rescaled, which takes 68 products: with runs of a hundred tiles every fourth tile
 // raises a maximum, one of twenty by more than this.  P times s is in units of 2^-13 of
@@ -77,7 +72,7 @@ struct Stage {  // byte offsets in a stage of the ring
 };
 template <int D, int NT>
 constexpr int ring_bytes() {
-  return teams_of(D, NT) * kTeamWarps * kStages * Stage<D>::kBytes;
+  return teams_of(D, NT) * kTeamWarps * stages_of(D) * Stage<D>::kBytes;
 }
 
 // Where 16-byte piece c (a group of channels) of row r of a tile lies: the reads of 8
@@ -122,9 +117,7 @@ __device__ __forceinline__ uint32_t centred_code(uint32_t w, int i) {
 
 // Up to 8 heads: tokens as rows, heads on the instruction's narrow side.
 //   S[token][head] = C . Q^T,  O^T[channel][head] += C^T . P^T
-// P is transposed between the two, 16 bits at a time.  (Heads as rows, half of them empty
-// or taken by P's second term, need no transposition, but twice the registers of O and
-// more instructions: HEADSUS.)
+// P is transposed between the two, 16 bits at a time.
 template <int D>
 struct TokensInRows {
   using At = Stage<D>;
@@ -526,7 +519,11 @@ template <int D, int NT>
 __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int4_kernel(KvView kv, PartArgs a, unsigned* err) {
   constexpr int kTeams = teams_of(D, NT), kWarps = kTeams * kTeamWarps;
   using At = Stage<D>;
+  constexpr int kStages = stages_of(D);
   using Math = std::conditional_t<NT == 1, TokensInRows<D>, HeadsInRows<D>>;
+  // a team's rings hold the outputs of its warps, and the weights of a pair's parts where it merges them
+  constexpr int kRings = kTeamWarps * kStages * At::kBytes, kMostCtas = 160;
+  static_assert(kTeamWarps * 8 * NT * D * 4 <= kRings && 8 * NT * (kMostCtas * kTeams + 2) * 4 + 16 <= kRings);
   constexpr int kPieces = At::kRow / 16;  // 16-byte pieces of a row, a group of channels each
   constexpr int kRowsPer = 32 / kPieces;  // rows one copy instruction of a warp covers
   extern __shared__ __align__(1024) uint8_t ring[];
