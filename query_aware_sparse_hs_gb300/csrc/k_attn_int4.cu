@@ -55,8 +55,8 @@ using namespace parts;
 // 131072 tokens); 64 channels 210 and 206.
 __host__ __device__ constexpr int stages_of(int head_dim) { return head_dim == 128 ? 2 : 3; }
 // Logits may pass the running maximum by so much (log2 units) before the state is
-// rescaled, which takes 68 products: with runs of a hundred tiles every fourth tile
-// raises a maximum, one of twenty by more than this.  P times s is in units of 2^-13 of
+// rescaled, which takes 40 products for up to 8 heads of 128 channels, 68 for 16: with
+// runs of a hundred tiles every fourth tile raises a maximum, one of twenty by more than this.  P times s is in units of 2^-13 of
 // the reference then, 2^15 at most.
 constexpr float kMargin = 2.0f;
 constexpr int kUnit4 = 13;

@@ -15,9 +15,9 @@
 // groups of channels are applied to the groups' partial sums.  f32 caches: on the CUDA
 // cores, as fp32 products are wanted.
 //
-// What bounds it: memory for bf16 (16 requests x 4 heads x 16384 tokens, 277 MB: 45.9 us,
-// 0.89 of the copy rate); instructions beside it for the others (4-bit, 32 requests, 185
-// MB: 35.6 us, 0.77; e4m3 0.73 to 0.75); the CUDA cores for f32 (0.32).  A short call, 4
+// What bounds it: memory for bf16 (16 requests x 4 heads x 16384 tokens, 277 MB: 46.3 us,
+// 0.88 of the copy rate); instructions beside it for the others (4-bit, 32 requests, 185
+// MB: 34.5 us, 0.79; e4m3 0.73 to 0.75); the CUDA cores for f32 (0.33).  A short call, 4
 // requests of up to 3000 tokens, takes 4.3 us: the launch, the counts and one chain of
 // lookups.
 #include <limits.h>
@@ -325,7 +325,8 @@ __global__ __launch_bounds__(Row<D, KIND>::kWarps * 32, 1) void weights_kernel(K
             float2 plus = minus[nt];
             if constexpr (KIND == HS_KV_INT4_G32) plus = add2(plus, make_float2(add[nt][2 * e], add[nt][2 * e + 1]));
             x = fma2(x, f[nt], plus);
-            sum += exp2_fast(x.x) + exp2_fast(x.y);
+            // (of no head, or an empty one: 0 times an infinite K is not a number)
+            sum += (minus[nt].x == -INFINITY ? 0.0f : exp2_fast(x.x)) + (minus[nt].y == -INFINITY ? 0.0f : exp2_fast(x.y));
           }
           sums[2 * mt + e] = sum;
         }

@@ -193,6 +193,39 @@ def test_weights_of_any_order_twice_selected_negative_scales_and_empty_heads(kin
         assert torch.equal(got, first)
 
 
+@pytest.mark.parametrize("group", [1, 4, 16])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "fp8"])
+def test_weights_of_tokens_infinitely_far_off(kind, group):
+    """A logit of -inf is a weight of 0, whatever the product's places without a head make of an infinite K."""
+    from query_aware_sparse_hs_gb300 import hs
+    c = Cache(kind, [70, 200], 1, 128, 16)
+    q = queries(c, group)
+    q[:, :, 32:64] = -q[:, :, 32:64].abs()
+    far = {0: [3, 69], 1: [0, 31, 150]}
+    sel, cnt = selection(c, None)
+    lse = lse_of(c, q, group, sel, cnt, 0.09)  # (of other keys: any will do)
+    start = torch.zeros((2, 1, c.mb * 16), device="cuda")
+
+    def run():
+        got = start.clone()
+        hs.hs_accumulate_attn_weights(c.shape(group), c.kv, q, lse, torch.from_numpy(sel).cuda(), torch.from_numpy(cnt).cuda(),
+                                      sel.shape[2], 0.09, got)
+        assert hs.hs_get_device_error() == (hs.HS_OK, 0)
+        return got
+
+    want = run()
+    for b, tokens in far.items():
+        for t in tokens:
+            p = int(c.table[b, 0, t // 16])
+            if kind == "fp8":
+                c.x["k"][p, t % 16, 32:64] = 0x38  # 1.0
+                c.sc["k"][p, t % 16, 1] = float("inf")
+            else:
+                c.x["k"][p, t % 16, 40] = float("inf")
+            want[b, 0, t] = 0.0
+    assert torch.equal(run(), want)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_weights_report_what_is_out_of_range(kind):
     from query_aware_sparse_hs_gb300 import hs
