@@ -401,10 +401,11 @@ cudaError_t launch_block(const KvView& kv, int first_block, int nblocks, void* s
 // one shift: 2^23 + 16^i n), one addition and one fused multiply of two at a time, its
 // scale being s / 16^i.
 // What bounds it: instructions, two thirds of them comparisons, masks and shifts, whose
-// pipe is busy for 0.65 of the time.  32 requests x 4 heads of 4K to 64K tokens, 128
-// channels: 152 us with 64-token pages (0.41 of the copy rate), 175 with 16-token pages
-// (0.45).  (16 channels to a lane: 148 and 190 us; additions and multiplies one at a time
-// 155 and 177; rows loaded into registers instead of the ring 162 and 201.)
+// pipe is busy for two thirds of the time.  32 requests x 4 heads of 4K to 64K tokens,
+// 128 channels: 138 us with 64-token pages (0.45 of the copy rate), 161 with 16-token pages
+// (0.49); full units without a clamp of the rows: 152 and 175 with it.  (Before that, 16
+// channels to a lane: 148 and 190 us; additions and multiplies one at a time 155 and 177;
+// rows loaded into registers instead of the ring 162 and 201.)
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -548,26 +549,28 @@ __global__ __launch_bounds__(kWarps * 32, 3) void summaries_int4_kernel(KvView k
       const uint8_t* unit = mine + unit_out * Unit<D>::kBytes;
       unit_out = unit_out + 1 == kUnits ? 0 : unit_out + 1;
       const int valid = valid_of(out.i), rows = min(valid - out.t, kUnitRows);
-      const auto get = [&](int t, float (&x)[8]) {
-        const int r = min(t + rs, rows - 1);  // (a repeated row changes nothing)
-        Codes8 c;
-        c.w = *reinterpret_cast<const uint32_t*>(unit + r * int4::row_bytes(D) + d0 / 2);
-        const uint16_t* rec = reinterpret_cast<const uint16_t*>(unit + Unit<D>::kCodes + r * kRecord) + d0 / kQuantGroup;
-        c.s = rec[0];
-        c.z = rec[D / kQuantGroup];
-        c.get(x, magic);
-      };
-#pragma unroll
-      for (int t = 0; t < kUnitRows; t += 2 * RPL) {
-        if (t > 0 && t >= rows) break;
+      const uint8_t* codes = unit + d0 / 2;
+      const uint16_t* recs = reinterpret_cast<const uint16_t*>(unit + Unit<D>::kCodes) + d0 / kQuantGroup;
+      const auto two = [&](int r0, int r1) {  // the lane's channels of two rows
         float x[8], y[8];
-        get(t, x);
-        get(t + RPL, y);
+        Codes8{*reinterpret_cast<const uint32_t*>(codes + r0 * int4::row_bytes(D)), recs[r0 * (kRecord / 2)],
+               recs[r0 * (kRecord / 2) + D / kQuantGroup]}.get(x, magic);
+        Codes8{*reinterpret_cast<const uint32_t*>(codes + r1 * int4::row_bytes(D)), recs[r1 * (kRecord / 2)],
+               recs[r1 * (kRecord / 2) + D / kQuantGroup]}.get(y, magic);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           mn[c] = fminf(mn[c], fminf(x[c], y[c]));
           mx[c] = fmaxf(mx[c], fmaxf(x[c], y[c]));
         }
+      };
+      if (rows == kUnitRows) {
+        codes += rs * int4::row_bytes(D);
+        recs += rs * (kRecord / 2);
+#pragma unroll
+        for (int t = 0; t < kUnitRows; t += 2 * RPL) two(t, t + RPL);
+      } else {
+#pragma unroll 1
+        for (int t = 0; t < rows; t += 2 * RPL) two(min(t + rs, rows - 1), min(t + RPL + rs, rows - 1));  // (a repeated row changes nothing)
       }
       const int now = out.i;
       if (!out.next(valid)) continue;
