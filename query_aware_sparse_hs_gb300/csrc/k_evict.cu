@@ -71,9 +71,13 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(KvView kv, Evict
   const int turns = ((last - first + ctas * kWarps - 1) / (ctas * kWarps) + 31) / 32;
   const int64_t run0 = first + static_cast<int64_t>(rank * kWarps + warp) * turns * 32;
   const int t0 = static_cast<int>(min(static_cast<int64_t>(last), run0)), n = min(turns * 32, last - t0);
+  // (loads behind conditions would wait for each other: places past the run read its last)
+  float raw[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) raw[i] = __ldg(w + min(t0 + 32 * i + lane, last - 1));
   uint32_t held[kHeld];
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) held[i] = 32 * i + lane < n ? weight_key(__ldg(w + t0 + 32 * i + lane)) : 0u;
+  for (int i = 0; i < kHeld; ++i) held[i] = weight_key(raw[i]);
   // each(turn, key, there) over the run
   const auto over = [&](auto&& each) {
 #pragma unroll
@@ -89,6 +93,7 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(KvView kv, Evict
   // ---- the key of the last that stays: its digits, and how many of that key do ----
   uint32_t prefix = 0u, mask = 0u;
   int rest = need;  // of the keys that share the digits so far
+  bool all_stay = false;  // all of them
 #pragma unroll
   for (int digit = 0; digit < 3; ++digit) {
     const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
@@ -128,13 +133,16 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(KvView kv, Evict
     prefix |= s_found[digit][0] << shift;
     mask |= field << shift;
     rest -= static_cast<int>(s_found[digit][1]);
-    if (s_size[digit] == static_cast<uint32_t>(rest)) break;  // all keys with these digits stay
+    all_stay = s_size[digit] == static_cast<uint32_t>(rest);
+    if (all_stay) break;
   }
-  // ---- the indices in order: keys whose digits are above, and the first `rest` of the same ----
+  // ---- the indices in order: keys from `from` on, and, but where all stay, the first
+  // `rest` whose digits are the same (no key has the largest digits: no overflow) ----
+  const uint32_t from = all_stay ? prefix : (prefix | ~mask) + 1u;
   int above = 0, same = 0;
   over([&](int, uint32_t k, bool there) {
-    above += there && (k & mask) > prefix;
-    same += there && (k & mask) == prefix;
+    above += there && k >= from;
+    same += there && !all_stay && (k & mask) == prefix;
   });
   above = __reduce_add_sync(0xffffffffu, above);
   same = __reduce_add_sync(0xffffffffu, same);
@@ -159,15 +167,25 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(KvView kv, Evict
     above += counts[0];
     same += counts[1];
   }
-  over([&](int i, uint32_t k, bool there) {
-    const bool is_above = there && (k & mask) > prefix, is_same = there && (k & mask) == prefix;
-    const unsigned ma = __ballot_sync(0xffffffffu, is_above), ms = __ballot_sync(0xffffffffu, is_same);
-    const unsigned lower = (1u << lane) - 1u;
-    const int same_here = same + __popc(ms & lower), above_here = above + __popc(ma & lower);
-    if (is_above || (is_same && same_here < rest)) kept[a.sink + above_here + min(same_here, rest)] = t0 + 32 * i + lane;
-    above += __popc(ma);
-    same += __popc(ms);
-  });
+  const unsigned lower = (1u << lane) - 1u;
+  int32_t* mine = kept + a.sink;
+  if (all_stay) {
+    over([&](int i, uint32_t k, bool there) {
+      const bool stays = there && k >= from;
+      const unsigned m = __ballot_sync(0xffffffffu, stays);
+      if (stays) mine[above + __popc(m & lower)] = t0 + 32 * i + lane;
+      above += __popc(m);
+    });
+  } else {
+    over([&](int i, uint32_t k, bool there) {
+      const bool is_above = there && k >= from, is_same = there && (k & mask) == prefix;
+      const unsigned ma = __ballot_sync(0xffffffffu, is_above), ms = __ballot_sync(0xffffffffu, is_same);
+      const int same_here = same + __popc(ms & lower), above_here = above + __popc(ma & lower);
+      if (is_above || (is_same && same_here < rest)) mine[above_here + min(same_here, rest)] = t0 + 32 * i + lane;
+      above += __popc(ma);
+      same += __popc(ms);
+    });
+  }
   cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
