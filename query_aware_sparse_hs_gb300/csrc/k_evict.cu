@@ -36,18 +36,25 @@ __device__ __forceinline__ uint32_t weight_key(float w) {  // NaN last, -0 as 0
 // 16 x 4 heads of up to 32768.  (A byte at a time with the digit found by one thread, a
 // CTA to a pair: 26 and 43 for this launch alone; the keys of the first digit's bin listed
 // for the other two: no change.)
-__global__ __launch_bounds__(kThreads) void evict_select_kernel(KvView kv, EvictArgs a, int ctas, unsigned* err) {
+template <int CTAS>
+__global__ __launch_bounds__(kThreads) void evict_select_kernel(KvView kv, EvictArgs a, unsigned* err) {
   __shared__ uint32_t s_hist[3][kBins];  // one for each digit
   __shared__ uint32_t s_sums[2][kWarps];
   __shared__ uint32_t s_found[3][2];     // digit, keys above it, keys in it
   __shared__ uint32_t s_size[3];
   __shared__ int s_above[kWarps], s_same[kWarps], s_counts[2];
   const cg::cluster_group cluster = cg::this_cluster();
+  const auto meet = [&]() {  // the pair's CTAs
+    if constexpr (CTAS == 1)
+      __syncthreads();
+    else
+      cluster.sync();
+  };
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t pair = blockIdx.x / ctas;
-  const int rank = static_cast<int>(blockIdx.x - pair * ctas);
+  const int64_t pair = blockIdx.x / CTAS;
+  const int rank = static_cast<int>(blockIdx.x % CTAS);
   const int b = static_cast<int>(pair / kv.hkv);
   const int64_t most = static_cast<int64_t>(kv.max_blocks) * kv.block;
   int L = max(__ldg(kv.seq_lens + b), 0);
@@ -56,7 +63,8 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(KvView kv, Evict
     L = static_cast<int>(most);
   }
   int32_t* kept = a.kept + pair * a.budget;
-  const int all = ctas * kThreads, me = rank * kThreads + tid;
+  constexpr int all = CTAS * kThreads;
+  const int me = rank * kThreads + tid;
   if (L <= a.budget) {  // (the same for the whole cluster)
     for (int i = me; i < a.budget; i += all) kept[i] = i < L ? i : -1;
     return;
@@ -68,7 +76,7 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(KvView kv, Evict
   if (need == 0) return;
   const float* w = a.weights + pair * most;
   // this warp's run, lane i every 32nd token of it
-  const int turns = ((last - first + ctas * kWarps - 1) / (ctas * kWarps) + 31) / 32;
+  const int turns = ((last - first + CTAS * kWarps - 1) / (CTAS * kWarps) + 31) / 32;
   const int64_t run0 = first + static_cast<int64_t>(rank * kWarps + warp) * turns * 32;
   const int t0 = static_cast<int>(min(static_cast<int64_t>(last), run0)), n = min(turns * 32, last - t0);
   // (loads behind conditions would wait for each other: places past the run read its last)
@@ -81,8 +89,10 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(KvView kv, Evict
   // each(turn, key, there) over the run
   const auto over = [&](auto&& each) {
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-      if (32 * i < n) each(i, held[i], 32 * i + lane < n);
+    for (int i = 0; i < kHeld; ++i) {
+      if (32 * i >= n) return;
+      each(i, held[i], 32 * i + lane < n);
+    }
     for (int i = kHeld; 32 * i < n; ++i) {
       const bool there = 32 * i + lane < n;
       each(i, there ? weight_key(__ldg(w + t0 + 32 * i + lane)) : 0u, there);
@@ -94,18 +104,19 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(KvView kv, Evict
   uint32_t prefix = 0u, mask = 0u;
   int rest = need;  // of the keys that share the digits so far
   bool all_stay = false;  // all of them
-#pragma unroll
+#pragma unroll 1
   for (int digit = 0; digit < 3; ++digit) {
     const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
     const uint32_t field = digit == 2 ? 1023u : 2047u;
     over([&](int, uint32_t k, bool there) {
       if (there && (k & mask) == prefix) atomicAdd(&s_hist[digit][(k >> shift) & field], 1u);
     });
-    cluster.sync();
+    meet();
     // bins 2047 - 2 tid and 2046 - 2 tid of the cluster, from the largest down
     uint32_t h[2] = {0u, 0u};
-    for (int c = 0; c < ctas; ++c) {
-      const uint2 two = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&s_hist[digit][0], c) + kBins - 2 - 2 * tid);
+#pragma unroll
+    for (int c = 0; c < CTAS; ++c) {
+      const uint2 two = CTAS == 1 ? *reinterpret_cast<const uint2*>(&s_hist[digit][kBins - 2 - 2 * tid]) : *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&s_hist[digit][0], c) + kBins - 2 - 2 * tid);
       h[0] += two.y;
       h[1] += two.x;
     }
@@ -161,7 +172,7 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(KvView kv, Evict
       s_counts[1] = cs;
     }
   }
-  cluster.sync();
+  meet();
   for (int c = 0; c < rank; ++c) {
     const int* counts = cluster.map_shared_rank(s_counts, c);
     above += counts[0];
@@ -186,7 +197,7 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(KvView kv, Evict
       same += __popc(ms);
     });
   }
-  cluster.sync();  // no CTA leaves while another reads its shared memory
+  if constexpr (CTAS > 1) cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
 constexpr int kRows = 64;  // rows of a CTA
@@ -271,25 +282,34 @@ __global__ __launch_bounds__(kGatherThreads) void evict_gather_kernel(KvView kv,
     copy_scales(uint32_t{});
 }
 
-cudaError_t launch_select(const KvView& kv, const EvictArgs& a, int sms, unsigned* err, cudaStream_t st) {
-  const int64_t pairs = static_cast<int64_t>(kv.batch) * kv.hkv, tokens = static_cast<int64_t>(kv.max_blocks) * kv.block;
-  // as many CTAs to a pair as keep its longest request's keys in registers, four to a
-  // thread where there is room, and as all pairs leave room for at once (one on an SM)
-  int ctas = 1;
-  while (ctas < kMostCtas && tokens > static_cast<int64_t>(ctas) * kThreads * 4 && pairs * 2 * ctas <= sms) ctas *= 2;
+template <int CTAS>
+cudaError_t launch_select_by(const KvView& kv, const EvictArgs& a, unsigned* err, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(pairs * ctas));
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(kv.batch) * kv.hkv * CTAS));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.x = CTAS;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel, kv, a, ctas, err);
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<CTAS>, kv, a, err);
+}
+cudaError_t launch_select(const KvView& kv, const EvictArgs& a, int sms, unsigned* err, cudaStream_t st) {
+  const int64_t pairs = static_cast<int64_t>(kv.batch) * kv.hkv, tokens = static_cast<int64_t>(kv.max_blocks) * kv.block;
+  // as many CTAs to a pair as keep its longest request's keys in registers, four to a
+  // thread where there is room, and as all pairs leave room for at once (one on an SM)
+  int ctas = 1;
+  while (ctas < kMostCtas && tokens > static_cast<int64_t>(ctas) * kThreads * 4 && pairs * 2 * ctas <= sms) ctas *= 2;
+  switch (ctas) {
+    case 1: return launch_select_by<1>(kv, a, err, st);
+    case 2: return launch_select_by<2>(kv, a, err, st);
+    case 4: return launch_select_by<4>(kv, a, err, st);
+    default: return launch_select_by<kMostCtas>(kv, a, err, st);
+  }
 }
 
 }  // namespace
