@@ -31,9 +31,9 @@ __device__ __forceinline__ uint32_t weight_key(float w) {  // NaN last, -0 as 0
 // read again from the caches).  The key of the last token that stays is found from
 // histograms of 11 bits at a time, which every CTA sums over the cluster through
 // distributed shared memory; a bin that is taken whole ends the search.
-// Latency-bound, by the barriers of the cluster and what lies between them: with a budget
-// of 64, so that little is gathered, both launches take 11 us for 3000 tokens, 19 for
-// 16 x 4 heads of up to 32768.  (A byte at a time with the digit found by one thread, a
+// Latency-bound, by two loads that follow one another, the barriers of the cluster (0.6 us
+// each) and what lies between them: with a budget of 64, so that little is gathered, both
+// launches take 9 us for 3000 tokens, 16 for 16 x 4 heads of up to 32768.  (A byte at a time with the digit found by one thread, a
 // CTA to a pair: 26 and 43 for this launch alone; the keys of the first digit's bin listed
 // for the other two: no change.)
 template <int CTAS>
