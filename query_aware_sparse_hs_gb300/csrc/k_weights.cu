@@ -17,7 +17,7 @@
 //
 // What bounds it: memory for bf16 (16 requests x 4 heads x 16384 tokens, 277 MB: 46.3 us,
 // 0.88 of the copy rate); instructions beside it for the others (4-bit, 32 requests, 185
-// MB: 34.5 us, 0.79; e4m3 0.73 to 0.75); the CUDA cores for f32 (0.33).  A short call, 4
+// MB: 34.5 us, 0.79; e4m3 0.73 to 0.75); the CUDA cores for f32 (0.60).  A short call, 4
 // requests of up to 3000 tokens, takes 4.3 us: the launch, the counts and one chain of
 // lookups.
 #include <limits.h>
@@ -348,67 +348,90 @@ __global__ __launch_bounds__(Row<D, KIND>::kWarps * 32, 1) void weights_kernel(K
   }
 }
 
-// f32: 8 lanes take a token, 4 D / 32 channels each, the heads in turn.
+// f32: 8 lanes take a token, 4 D / 32 channels each, four tokens and four heads at a time.
+// The lanes' parts of a logit are joined by halving the heads, so that two lanes form its
+// exponential and not eight.  16 requests x 4 heads x 16384 tokens, 546 MB: 134 us, 0.60 of
+// the copy rate, bound by the loads of the query and the shuffles (16 heads 230, 1 head 95);
+// one head and two tokens at a time, every lane with the whole logit: 242.  (Two tokens at
+// a time, 16 or 24 warps an SM: 143 and 146.)
 constexpr int kWarpsF32 = 8;
 template <int D>
-__global__ __launch_bounds__(kWarpsF32 * 32) void weights_f32_kernel(KvView kv, WeightsArgs a, unsigned* err) {
+__global__ __launch_bounds__(kWarpsF32 * 32, 2) void weights_f32_kernel(KvView kv, WeightsArgs a, unsigned* err) {
   constexpr int C = D / 32;  // 16-byte pieces of a lane, 8 lanes apart
+  constexpr int kTokens = 4, kHeads = 4;
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 7;
+  const bool upper = lane & 4, odd = lane & 2;
+  const int my_head = (upper ? 2 : 0) + (odd ? 1 : 0);  // of four
   report_counts(kv, a, err);
   TileRun run(kv, a, static_cast<int64_t>(warp) * gridDim.x + blockIdx.x, static_cast<int64_t>(gridDim.x) * kWarpsF32, lane);
   while (run.left > 0) {
     const int cnt = blocks_of(a, run.pair), tiles = run.here(kv, cnt);
-    const int b = run.pair / kv.hkv, kvh = run.pair - b * kv.hkv;
+    const int b = run.pair / kv.hkv, kvh = run.pair - b * kv.hkv, G = kv.group;
     TileRows<WeightsArgs> rows(kv, a, run.pair, cnt, __ldg(kv.seq_lens + b), run.first, tiles, lane, err);
     float* out = a.weights + static_cast<int64_t>(run.pair) * kv.max_blocks * kv.block;
-    const int64_t head0 = static_cast<int64_t>(b) * kv.hq + kvh * kv.group;
+    const int64_t head0 = static_cast<int64_t>(b) * kv.hq + kvh * G;
+    const float4* q0 = reinterpret_cast<const float4*>(a.q) + head0 * (D / 4) + c;
     for (int n = 0; n < tiles; ++n) {
       uint32_t row;
       int place;
       const bool ok = rows.template next_at<true>(row, place);
-      if (!ok) place = -1;
-      const uint32_t live = __ballot_sync(0xffffffffu, ok);
-      float sum = 0.0f;  // of token `lane`
+      if (__ballot_sync(0xffffffffu, ok) == 0u) continue;  // (there is a row 0 else, read where a token is not there)
+      float sum = 0.0f;                                    // of token `lane`
 #pragma unroll 1
-      for (int i0 = 0; i0 < 8; i0 += 2) {  // tokens 4 i0 .. 4 i0 + 7, two to a lane
-        float4 x[2][C];
+      for (int t0 = 0; t0 < kTile; t0 += 4 * kTokens) {
+        float4 x[kTokens][C];  // of token t0 + 4 t + lane / 8
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int t = 4 * (i0 + h) + (lane >> 3);
-          const uint32_t r = __shfl_sync(0xffffffffu, row, t);
+        for (int t = 0; t < kTokens; ++t) {
+          const uint32_t r = __shfl_sync(0xffffffffu, row, t0 + 4 * t + (lane >> 3));
           const float4* src = reinterpret_cast<const float4*>(kv.k_pages) + static_cast<uint64_t>(r) * (D / 4) + c;
 #pragma unroll
-          for (int k = 0; k < C; ++k) x[h][k] = (live >> t) & 1u ? __ldg(src + 8 * k) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int k = 0; k < C; ++k) x[t][k] = __ldg(src + 8 * k);
         }
-        float all[2] = {0.0f, 0.0f};
-        for (int h = 0; h < kv.group; ++h) {
-          const float4* q = reinterpret_cast<const float4*>(a.q) + (head0 + h) * (D / 4) + c;
-          float dot[2] = {0.0f, 0.0f};
+        float all[kTokens] = {};
+#pragma unroll 1
+        for (int h0 = 0; h0 < G; h0 += kHeads) {
+          float dot[kHeads][kTokens];
 #pragma unroll
-          for (int k = 0; k < C; ++k) {
-            const float4 y = __ldg(q + 8 * k);
+          for (int h = 0; h < kHeads; ++h) {
+            const float4* q = q0 + min(h0 + h, G - 1) * (D / 4);
+            float2 two[kTokens];
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-              dot[t] = fmaf(x[t][k].x, y.x, fmaf(x[t][k].y, y.y, fmaf(x[t][k].z, y.z, fmaf(x[t][k].w, y.w, dot[t]))));
+            for (int t = 0; t < kTokens; ++t) two[t] = both(0.0f);
+#pragma unroll
+            for (int k = 0; k < C; ++k) {
+              const float4 y = __ldg(q + 8 * k);
+#pragma unroll
+              for (int t = 0; t < kTokens; ++t) {
+                two[t] = fma2(make_float2(x[t][k].x, x[t][k].y), make_float2(y.x, y.y), two[t]);
+                two[t] = fma2(make_float2(x[t][k].z, x[t][k].w), make_float2(y.z, y.w), two[t]);
+              }
+            }
+#pragma unroll
+            for (int t = 0; t < kTokens; ++t) dot[h][t] = two[t].x + two[t].y;
           }
-          const float lse = __ldg(a.lse + head0 + h);
+          const float lse = h0 + my_head < G ? __ldg(a.lse + head0 + h0 + my_head) : -INFINITY;
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            dot[t] += __shfl_xor_sync(0xffffffffu, dot[t], 1);
-            dot[t] += __shfl_xor_sync(0xffffffffu, dot[t], 2);
-            dot[t] += __shfl_xor_sync(0xffffffffu, dot[t], 4);
-            if (lse != -INFINITY) all[t] += expf(fmaf(dot[t], a.scale, -lse));
+          for (int t = 0; t < kTokens; ++t) {
+            float u = upper ? dot[2][t] : dot[0][t], v = upper ? dot[3][t] : dot[1][t];
+            u += __shfl_xor_sync(0xffffffffu, upper ? dot[0][t] : dot[2][t], 4);
+            v += __shfl_xor_sync(0xffffffffu, upper ? dot[1][t] : dot[3][t], 4);
+            float z = odd ? v : u;
+            z += __shfl_xor_sync(0xffffffffu, odd ? u : v, 2);
+            z += __shfl_xor_sync(0xffffffffu, z, 1);
+            if (lse != -INFINITY) all[t] += expf(fmaf(z, a.scale, -lse));
           }
         }
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < kTokens; ++t) {
+          all[t] += __shfl_xor_sync(0xffffffffu, all[t], 2);
+          all[t] += __shfl_xor_sync(0xffffffffu, all[t], 4);
           const float v = __shfl_sync(0xffffffffu, all[t], 8 * (lane & 3));
-          if (lane >> 2 == i0 + t) sum = v;
+          if (lane >> 2 == t0 / 4 + t) sum = v;
         }
       }
-      if (place >= 0) atomicAdd(out + place, sum);
+      if (ok) atomicAdd(out + place, sum);
     }
     run.on(kv, a, tiles);
   }
@@ -432,7 +455,7 @@ cudaError_t launch_k(const KvView& kv, const WeightsArgs& a, int sms, unsigned* 
 template <int D>
 cudaError_t launch_d(const KvView& kv, const WeightsArgs& a, int sms, unsigned* err, cudaStream_t st) {
   switch (kv.kv_dtype) {
-    case HS_KV_F32: return launch_pdl(weights_f32_kernel<D>, dim3(4 * sms), dim3(kWarpsF32 * 32), 0, st, kv, a, err);
+    case HS_KV_F32: return launch_pdl(weights_f32_kernel<D>, dim3(2 * sms), dim3(kWarpsF32 * 32), 0, st, kv, a, err);
     case HS_KV_BF16: return launch_k<D, HS_KV_BF16>(kv, a, sms, err, st);
     case HS_KV_FP8E4M3_G32: return launch_k<D, HS_KV_FP8E4M3_G32>(kv, a, sms, err, st);
     case HS_KV_INT4_G32: return launch_k<D, HS_KV_INT4_G32>(kv, a, sms, err, st);
