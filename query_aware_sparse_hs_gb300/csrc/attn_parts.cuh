@@ -315,8 +315,9 @@ __device__ int number_parts(const KvView& kv, const PartArgs& a, const Cut& cut,
   const int pairs = kv.batch * kv.hkv, mine_n = (pairs + team.threads() - 1) / team.threads();
   const int p0 = min(pairs, team.rank * mine_n), p1 = min(pairs, p0 + mine_n);
   int64_t mine = 0;  // parts, and rows of the workspace in the upper half
+  int k = 0;
   for (int p = p0; p < p1; ++p) {
-    const int k = parts_of(tiles_of(kv, pair_count(a, p)), cut.per, cut.whole);
+    k = parts_of(tiles_of(kv, pair_count(a, p)), cut.per, cut.whole);
     mine += k + (k > 1 ? static_cast<int64_t>(k) << 32 : 0);
   }
   int64_t at = mine;
@@ -335,7 +336,7 @@ __device__ int number_parts(const KvView& kv, const PartArgs& a, const Cut& cut,
   }
   for (int p = p0; p < p1; ++p) {
     Pairs n;
-    n.count = parts_of(tiles_of(kv, pair_count(a, p)), cut.per, cut.whole);
+    n.count = mine_n == 1 ? k : parts_of(tiles_of(kv, pair_count(a, p)), cut.per, cut.whole);
     n.part = static_cast<int>(at & 0xffffffff);
     n.row = static_cast<int>(at >> 32);
     each(p, n);

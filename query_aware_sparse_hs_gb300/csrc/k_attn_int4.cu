@@ -30,9 +30,10 @@
 // What bounds it: the matrix, integer and fp32 pipes in turn, none of them busy half of
 // the time, with instructions waiting for each other in between: 16 requests x 4 heads x
 // 131072 tokens, 1.34 GB, 280 us, 0.71 of the copy rate; 64 channels 206 us for half of
-// that (0.48); 16 heads 254 us for half (0.39).  32 requests x 4096 selected tokens: 30.0
-// us, of which the chain of lookups before the stream and the join behind it are 8; 12
-// uneven requests of 16 heads, 64 channels: 33.9.  (Heads as rows for up to 8 heads, with
+// that (0.48); 16 heads 255 us for half (0.39).  32 requests x 4096 selected tokens: 29.0
+// us, of which the chain of lookups before the stream and the join behind it are 7 (with
+// the query asked for behind the first pages, and a slot's part found by divisions, 30.0); 12
+// uneven requests of 16 heads, 64 channels: 32.6.  (Heads as rows for up to 8 heads, with
 // half of the rows empty or taken by P's second term and O in twice the registers: 318.)
 //
 // Precision: q is exact (bf16, times a power of two, which takes entries up to 2^90), S
@@ -132,7 +133,19 @@ struct TokensInRows {
                             // the second: over the others
   float vref;               // power of two, not below the V scales and centres / 8 met
 
-  __device__ __forceinline__ TokensInRows(const KvView& kv, const PartArgs& a, int64_t head0, int this_lane)
+  // The query's channels of the lane: asked for before the lookups of the first rows.
+  struct Query {
+    uint4 raw[kGroups];
+    __device__ __forceinline__ Query(const KvView& kv, const PartArgs& a, int64_t head0, int lane) {
+      const int g = lane >> 2, c4 = lane & 3;
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k)
+        raw[k] = g < kv.group ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (head0 + g) * D + 32 * k + 8 * c4))
+                              : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+
+  __device__ __forceinline__ TokensInRows(const Query& query, float scale, int this_lane)
       : lane(this_lane), g(this_lane >> 2), c4(this_lane & 3), vref(kMinRef) {
     const int mat = lane >> 3, mr = lane & 7;
 #pragma unroll
@@ -141,12 +154,7 @@ struct TokensInRows {
       v_at[k / 2] = At::kV + k_at[k / 2];
     }
     z_at = At::kRecV + 16 * (8 * (mat >> 1) + 16 * (mat & 1) + mr);  // tokens 0, 16, 8 and 24 on
-    uint4 raw[kGroups];
-#pragma unroll
-    for (int k = 0; k < kGroups; ++k)
-      raw[k] = g < kv.group ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (head0 + g) * D + 32 * k + 8 * c4))
-                            : make_uint4(0u, 0u, 0u, 0u);
-    const Int4Query<kGroups> q(raw, a.scale, c4);
+    const Int4Query<kGroups> q(query.raw, scale, c4);
 #pragma unroll
     for (int k = 0; k < kGroups; ++k)
 #pragma unroll
@@ -331,7 +339,21 @@ struct HeadsInRows {
   float oz[4];               // what columns 2 c4 and + 1 of the records add up to
   float vref;                // power of two, not below the V scales and centres / 8 met
 
-  __device__ __forceinline__ HeadsInRows(const KvView& kv, const PartArgs& a, int64_t head0, int this_lane)
+  struct Query {  // as above, of heads g and g + 8
+    uint4 raw[2][kGroups];
+    __device__ __forceinline__ Query(const KvView& kv, const PartArgs& a, int64_t head0, int lane) {
+      const int g = lane >> 2, c4 = lane & 3;
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k)
+          raw[nt][k] = nt * 8 + g < kv.group ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                                                   (head0 + nt * 8 + g) * D + 32 * k + 8 * c4))
+                                             : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+
+  __device__ __forceinline__ HeadsInRows(const Query& query, float scale, int this_lane)
       : lane(this_lane), g(this_lane >> 2), c4(this_lane & 3), vref(kMinRef) {
     const int mat = lane >> 3, mr = lane & 7;
     k_at = D == 128 ? piece_at<D>(mr, mat) : piece_at<D>(8 * (mat >> 1) + mr, mat & 1);  // (every 8th row is permuted alike)
@@ -339,13 +361,7 @@ struct HeadsInRows {
     for (int k = 0; k < kGroups; k += 2) v_at[k / 2] = At::kV + piece_at<D>(8 * (mat & 1) + mr, k + (mat >> 1));
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
-      uint4 raw[kGroups];
-#pragma unroll
-      for (int k = 0; k < kGroups; ++k)
-        raw[k] = nt * 8 + g < kv.group ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                                                             (head0 + nt * 8 + g) * D + 32 * k + 8 * c4))
-                                       : make_uint4(0u, 0u, 0u, 0u);
-      const Int4Query<kGroups> q(raw, a.scale, c4);
+      const Int4Query<kGroups> q(query.raw[nt], scale, c4);
 #pragma unroll
       for (int k = 0; k < kGroups; ++k)
 #pragma unroll
@@ -553,6 +569,10 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
   int listed = 0;                           // parts of this team noted so far
   const auto note = [&](int p, const Pairs& n) {
     // this team's parts among the pair's, the next kListed of them
+    if (n.part + n.count <= cut.slots) {  // no slot has two: without the divisions
+      if (slot >= n.part && slot < n.part + n.count && listed == 0) s_parts[tm][0] = Part{p, slot - n.part, n.count, n.row};
+      return;
+    }
     for (int j = n.part + (slot + cut.slots - n.part % cut.slots) % cut.slots; j < n.part + n.count; j += cut.slots) {
       const int at = j / cut.slots - listed;
       if (at >= 0 && at < kListed) s_parts[tm][at] = Part{p, j - n.part, n.count, n.row};
@@ -584,6 +604,7 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
     // The warp's tiles: a run of the part.
     const int run0 = seg0 + seg_tiles * team_warp / team.warps;
     const int tiles = seg0 + seg_tiles * (team_warp + 1) / team.warps - run0;
+    const typename Math::Query query(kv, a, static_cast<int64_t>(b) * kv.hq + kvh * kv.group, lane);
     TileRows<PartArgs> rows(kv, a, part.pair, cnt, kv.seq_lens[b], run0, tiles, lane, err);
     if constexpr (D == 64) {  // the empty halves of the records
 #pragma unroll
@@ -646,7 +667,7 @@ __global__ __launch_bounds__(teams_of(D, NT) * kTeamWarps * 32, 1) void attn_int
       copies_commit();
     }
 
-    Math math(kv, a, static_cast<int64_t>(b) * kv.hq + kvh * kv.group, lane);
+    Math math(query, a.scale, lane);
     int stage = 0;
     for (int n = 0; n < tiles; ++n) {
       __syncwarp();  // the stage about to be filled has been read by every lane
