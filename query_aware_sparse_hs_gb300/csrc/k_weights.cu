@@ -17,7 +17,7 @@
 //
 // What bounds it: memory for bf16 (16 requests x 4 heads x 16384 tokens, 277 MB: 46.3 us,
 // 0.88 of the copy rate); instructions beside it for the others (4-bit, 32 requests, 185
-// MB: 34.5 us, 0.79; e4m3 0.73 to 0.75); the CUDA cores for f32 (0.60).  A short call, 4
+// MB: 34.5 us, 0.79; e4m3 0.73 to 0.75); the CUDA cores for f32 (0.72).  A short call, 4
 // requests of up to 3000 tokens, takes 4.3 us: the launch, the counts and one chain of
 // lookups.
 #include <limits.h>
@@ -350,29 +350,34 @@ __global__ __launch_bounds__(Row<D, KIND>::kWarps * 32, 1) void weights_kernel(K
 
 // f32: 8 lanes take a token, 4 D / 32 channels each, four tokens and four heads at a time.
 // The lanes' parts of a logit are joined by halving the heads, so that two lanes form its
-// exponential and not eight.  16 requests x 4 heads x 16384 tokens, 546 MB: 134 us, 0.60 of
-// the copy rate, bound by the loads of the query and the shuffles (16 heads 230, 1 head 95);
-// one head and two tokens at a time, every lane with the whole logit: 242.  (Two tokens at
-// a time, 16 or 24 warps an SM: 143 and 146.)
-constexpr int kWarpsF32 = 8;
+// exponential and not eight.  16 requests x 4 heads x 16384 tokens, 546 MB: 112 us, 0.72 of
+// the copy rate (1 head 91, 16 heads 178, bound by the reads of the query and the
+// shuffles).  (One head and two tokens at a time, every lane with the whole logit: 242; the
+// query not in shared memory 122, and with 16 warps, which spill, 134; two tokens at a time
+// 143; the next tile's rows prefetched into the L2 149.)
+__host__ __device__ constexpr int warps_f32(int head_dim) { return head_dim == 128 ? 6 : 8; }  // two CTAs to an SM, without spilling
 template <int D>
-__global__ __launch_bounds__(kWarpsF32 * 32, 2) void weights_f32_kernel(KvView kv, WeightsArgs a, unsigned* err) {
+__global__ __launch_bounds__(warps_f32(D) * 32, 2) void weights_f32_kernel(KvView kv, WeightsArgs a, unsigned* err) {
   constexpr int C = D / 32;  // 16-byte pieces of a lane, 8 lanes apart
-  constexpr int kTokens = 4, kHeads = 4;
+  constexpr int kTokens = 4, kHeads = 4, kWarps = warps_f32(D);
+  __shared__ float4 s_q[kWarps][16 * D / 4];  // the pair's query
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 7;
   const bool upper = lane & 4, odd = lane & 2;
   const int my_head = (upper ? 2 : 0) + (odd ? 1 : 0);  // of four
   report_counts(kv, a, err);
-  TileRun run(kv, a, static_cast<int64_t>(warp) * gridDim.x + blockIdx.x, static_cast<int64_t>(gridDim.x) * kWarpsF32, lane);
+  TileRun run(kv, a, static_cast<int64_t>(warp) * gridDim.x + blockIdx.x, static_cast<int64_t>(gridDim.x) * kWarps, lane);
   while (run.left > 0) {
     const int cnt = blocks_of(a, run.pair), tiles = run.here(kv, cnt);
     const int b = run.pair / kv.hkv, kvh = run.pair - b * kv.hkv, G = kv.group;
     TileRows<WeightsArgs> rows(kv, a, run.pair, cnt, __ldg(kv.seq_lens + b), run.first, tiles, lane, err);
     float* out = a.weights + static_cast<int64_t>(run.pair) * kv.max_blocks * kv.block;
     const int64_t head0 = static_cast<int64_t>(b) * kv.hq + kvh * G;
-    const float4* q0 = reinterpret_cast<const float4*>(a.q) + head0 * (D / 4) + c;
+    __syncwarp();
+    for (int i = lane; i < G * (D / 4); i += 32) s_q[warp][i] = __ldg(reinterpret_cast<const float4*>(a.q) + head0 * (D / 4) + i);
+    __syncwarp();
+    const float4* q0 = s_q[warp] + c;
     for (int n = 0; n < tiles; ++n) {
       uint32_t row;
       int place;
@@ -401,7 +406,7 @@ __global__ __launch_bounds__(kWarpsF32 * 32, 2) void weights_f32_kernel(KvView k
             for (int t = 0; t < kTokens; ++t) two[t] = both(0.0f);
 #pragma unroll
             for (int k = 0; k < C; ++k) {
-              const float4 y = __ldg(q + 8 * k);
+              const float4 y = q[8 * k];
 #pragma unroll
               for (int t = 0; t < kTokens; ++t) {
                 two[t] = fma2(make_float2(x[t][k].x, x[t][k].y), make_float2(y.x, y.y), two[t]);
@@ -455,7 +460,7 @@ cudaError_t launch_k(const KvView& kv, const WeightsArgs& a, int sms, unsigned* 
 template <int D>
 cudaError_t launch_d(const KvView& kv, const WeightsArgs& a, int sms, unsigned* err, cudaStream_t st) {
   switch (kv.kv_dtype) {
-    case HS_KV_F32: return launch_pdl(weights_f32_kernel<D>, dim3(2 * sms), dim3(kWarpsF32 * 32), 0, st, kv, a, err);
+    case HS_KV_F32: return launch_pdl(weights_f32_kernel<D>, dim3(2 * sms), dim3(warps_f32(D) * 32), 0, st, kv, a, err);
     case HS_KV_BF16: return launch_k<D, HS_KV_BF16>(kv, a, sms, err, st);
     case HS_KV_FP8E4M3_G32: return launch_k<D, HS_KV_FP8E4M3_G32>(kv, a, sms, err, st);
     case HS_KV_INT4_G32: return launch_k<D, HS_KV_INT4_G32>(kv, a, sms, err, st);
