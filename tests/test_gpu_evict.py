@@ -355,6 +355,9 @@ EVICTS = {
     "long": ([70001, 20000], 1, 64, 64, 5000, 4, 500),
     "many_requests": ([1 + 7 * i % 190 for i in range(200)], 2, 64, 16, 50, 2, 9),
     "nothing_at_all": ([0, 0], 1, 128, 16, 10, 2, 2),
+    "two_ctas_to_a_pair": ([6000, 4097, 5], 2, 64, 64, 1000, 4, 100),
+    "four_ctas_to_a_pair": ([12000, 300], 1, 64, 64, 2000, 0, 1),
+    "longer_than_the_registers": ([20000] + [3 + i for i in range(76)], 1, 64, 64, 700, 4, 33),
 }
 
 
@@ -373,9 +376,10 @@ def test_the_heaviest_tokens_are_gathered(kind, name):
     assert torch.equal(c.gl.cpu(), torch.tensor(lens, dtype=torch.int32))
 
 
-def test_ties_nan_infinities_and_zeros_of_the_weights():
+@pytest.mark.parametrize("n, more", [(900, 0), (7000, 0), (33000, 0), (17000, 80)])  # CTAs to a pair: 1, 2, 8; 1, past its registers
+def test_ties_nan_infinities_and_zeros_of_the_weights(n, more):
     from query_aware_sparse_hs_gb300 import hs
-    c = Cache("bf16", [900, 900, 900, 900, 900], 1, 64, 16, seed=5)
+    c = Cache("bf16", [n] * 5 + [7] * more, 1, 64, 16, seed=5)
     w = weights_for(c)
     w[0] = 0.5                                  # all alike: the lower ones stay
     w[1, 0, ::2] = -0.0
@@ -383,9 +387,9 @@ def test_ties_nan_infinities_and_zeros_of_the_weights():
     w[2, 0, 100:850] = float("nan")             # last of all
     w[3, 0, 500:700], w[3, 0, 300:400] = float("inf"), float("-inf")
     w[4, 0, :] = -torch.rand(w.shape[2], generator=torch.Generator().manual_seed(1)).cuda()
-    for budget, sink, recent in ((300, 4, 64), (64, 0, 0), (899, 1, 1)):
+    for budget, sink, recent in ((300, 4, 64), (64, 0, 0), (n - 1, 1, 1)):
         d = destination(c, budget)
-        kept = torch.zeros((5, 1, budget), dtype=torch.int32, device="cuda")
+        kept = torch.zeros((5 + more, 1, budget), dtype=torch.int32, device="cuda")
         hs.hs_evict_tokens(c.shape(1), c.kv, d["kv"], hs.evict_params(budget, sink, recent), w, d["w"], kept)
         check_evicted(c, d, w, budget, sink, recent, kept)
 
