@@ -16,6 +16,29 @@
 namespace hs {
 namespace int4 {
 
+// Two fp32 numbers at a time.
+__device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul_pair(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma_pair(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
 constexpr float kMost = 8.507059173023462e37f;        // 2^126: values beyond it are held as it
 constexpr float kLeastScale = 1.2037062152420224e-35f;  // 2^-116: smaller ranges are held as their centre
 constexpr float kRound = 12582920.0f;  // 1.5 2^23 + 8: c plus it is, as bits, round(c) + 8 more than 0x4b400000
@@ -70,7 +93,10 @@ __device__ __forceinline__ Scale scale_of(const Range& r) {
   const float lo = nan ? 0.0f : r.lo, hi = nan ? 0.0f : r.hi;
   // (one rounding of the sum, so that a centre next to zero keeps its precision)
   q.z = __bfloat162float(__float2bfloat16_rn(fmaf(lo, 7.0f / 16.0f, hi * 0.5f) * (16.0f / 15.0f)));
-  q.s = __bfloat162float(__float2bfloat16_ru(fmaxf((hi - q.z) / 7.0f, (q.z - lo) / 8.0f)));
+  // a seventh, by a quotient corrected by its remainder (as in encode8; a range that is too
+  // small for it to be exact becomes 0)
+  const float above = hi - q.z, seventh = above * (1.0f / 7.0f);
+  q.s = __bfloat162float(__float2bfloat16_ru(fmaxf(fmaf(fmaf(-seventh, 7.0f, above), 1.0f / 7.0f, seventh), (q.z - lo) * 0.125f)));
   if (!(q.s >= kLeastScale)) q.s = 0.0f;
   q.inv = q.s > 0.0f ? 1.0f / q.s : 0.0f;
   if (nan) q.s = __uint_as_float(0x7fc00000u);  // every value of the group reads as NaN
@@ -84,23 +110,25 @@ __device__ __forceinline__ uint16_t bf16_bits(float exact) { return static_cast<
 // of random bf16 values differed from the definition's).
 __device__ __forceinline__ uint32_t encode8(const float (&x)[8], const Scale& q) {
   uint32_t w = 0u - 0x3f400000u;  // what the upper bits of 8 terms of kRound add up to
+  const float2 less = make_float2(-q.z, -q.z), inv = make_float2(q.inv, q.inv), by = make_float2(-q.s, -q.s), round = make_float2(kRound, kRound);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = x[i] - q.z, a = t * q.inv;
-    const float c = fmaf(fmaf(-a, q.s, t), q.inv, a);  // from -8 to 7 by the choice of z and s
-    w += __float_as_uint(c + kRound) << (4 * i);
+  for (int i = 0; i < 8; i += 2) {
+    const float2 t = add_pair(make_float2(x[i], x[i + 1]), less), a = mul_pair(t, inv);
+    const float2 c = add_pair(fma_pair(fma_pair(a, by, t), inv, a), round);  // from -8 to 7 by the choice of z and s
+    w += __float_as_uint(c.x) << (4 * i);
+    w += __float_as_uint(c.y) << (4 * i + 4);
   }
   return w;
 }
-// The codes of 8 neighbouring channels as numbers, exactly.
-__device__ __forceinline__ void codes8(uint32_t w, float (&c)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = __uint_as_float(((w >> (4 * i)) & 15u) | 0x4b000000u) - 8388616.0f;  // 2^23 + 8
-}
 __device__ __forceinline__ void decode8(uint32_t w, float s, float z, float (&x)[8]) {
-  codes8(w, x);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = fmaf(s, x[i], z);
+  for (int i = 0; i < 8; i += 2) {
+    const float a = __uint_as_float(((w >> (4 * i)) & 15u) | 0x4b000000u), b = __uint_as_float(((w >> (4 * i + 4)) & 15u) | 0x4b000000u);
+    const float2 c = add_pair(make_float2(a, b), make_float2(-8388616.0f, -8388616.0f));  // 2^23 + 8: the codes, exactly
+    const float2 v = fma_pair(make_float2(s, s), c, make_float2(z, z));
+    x[i] = v.x;
+    x[i + 1] = v.y;
+  }
 }
 
 // Scale and centre of group g of a row.

@@ -50,9 +50,9 @@ cudaError_t launch_c(const void* src, bool f32, int64_t rows, uint8_t* codes, fl
 
 // The 4-bit format (int4.cuh): a thread takes 8 neighbouring channels, so that a
 // group is 4 threads and every access of a warp is one run of memory.  4 million rows of
-// 128 bf16 values: read back in 231 us, 0.86 of the copy rate (four vectors to a thread
-// 225, but 8192 rows 2.2 us for 1.8); quantised in 317 us, 0.62, bound by instructions
-// (14 a value).
+// 128 bf16 values: read back in 230 us, 0.86 of the copy rate (four vectors to a thread
+// 225, but 8192 rows 2.2 us for 1.8); quantised in 260 us, 0.76, bound by instructions
+// (with values one at a time and a division by 7: 317).
 constexpr int kThreads4 = 256;
 
 constexpr int kFlight = 2;  // vectors of a thread, kThreads4 apart, both loaded before one is used

@@ -412,20 +412,6 @@ __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
 __device__ __forceinline__ void copy8_async(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 fma_pair(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
 // 2^23 + n 16^i: the code's bits where they are, below the exponent of 2^23 (`magic`, in
 // a register).
 template <uint32_t MASK>
@@ -445,12 +431,12 @@ struct Codes8 {
     constexpr float k = 8388608.0f;  // 2^23
     const float2 centre = make_float2(c, c);
     const uint32_t lo = w, up = w >> 20;
-    const float2 a = add_pair(make_float2(number<0xfu>(lo, magic), number<0xf0u>(lo, magic)), make_float2(-k - 8.0f, -k - 128.0f));
-    const float2 b = add_pair(make_float2(number<0xf00u>(lo, magic), number<0xf000u>(lo, magic)), make_float2(-k - 2048.0f, -k - 32768.0f));
-    const float2 d = add_pair(make_float2(number<0xf0000u>(lo, magic), number<0xfu>(up, magic)), make_float2(-k - 524288.0f, -k - 8.0f));
-    const float2 e = add_pair(make_float2(number<0xf0u>(up, magic), number<0xf00u>(up, magic)), make_float2(-k - 128.0f, -k - 2048.0f));
-    const float2 va = fma_pair(a, make_float2(f, f1), centre), vb = fma_pair(b, make_float2(f2, f3), centre);
-    const float2 vd = fma_pair(d, make_float2(f4, f), centre), ve = fma_pair(e, make_float2(f1, f2), centre);
+    const float2 a = int4::add_pair(make_float2(number<0xfu>(lo, magic), number<0xf0u>(lo, magic)), make_float2(-k - 8.0f, -k - 128.0f));
+    const float2 b = int4::add_pair(make_float2(number<0xf00u>(lo, magic), number<0xf000u>(lo, magic)), make_float2(-k - 2048.0f, -k - 32768.0f));
+    const float2 d = int4::add_pair(make_float2(number<0xf0000u>(lo, magic), number<0xfu>(up, magic)), make_float2(-k - 524288.0f, -k - 8.0f));
+    const float2 e = int4::add_pair(make_float2(number<0xf0u>(up, magic), number<0xf00u>(up, magic)), make_float2(-k - 128.0f, -k - 2048.0f));
+    const float2 va = int4::fma_pair(a, make_float2(f, f1), centre), vb = int4::fma_pair(b, make_float2(f2, f3), centre);
+    const float2 vd = int4::fma_pair(d, make_float2(f4, f), centre), ve = int4::fma_pair(e, make_float2(f1, f2), centre);
     x[0] = va.x; x[1] = va.y; x[2] = vb.x; x[3] = vb.y;
     x[4] = vd.x; x[5] = vd.y; x[6] = ve.x; x[7] = ve.y;
   }
