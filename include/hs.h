@@ -304,7 +304,8 @@ HS_API int32_t hs_attn_geometry(const hs_attn_shape* shape, int32_t batch, int32
  * the block's valid tokens t in [jB, min((j+1)B, L_b)) of K[t][d].  e4m3 K is
  * dequantised first (code * scale in fp32; with a scale per page the min and max
  * are taken over the codes and then scaled, which is the same), 4-bit K likewise
- * (z + s c in fp32), and the results rounded outward to bf16 (min toward -inf, max toward +inf).  Other entries are
+ * (z + s c in fp32; scales of 2^-116 at least, or 0, as the quantiser makes them), and the
+ * results rounded outward to bf16 (min toward -inf, max toward +inf).  Other entries are
  * not written.
  * Reading a page id outside [0, num_pages) sets HS_EBIT_PAGE_RANGE and skips
  * that block. */
