@@ -30,7 +30,7 @@
 // What bounds it: the matrix, integer and fp32 pipes in turn, none of them busy half of
 // the time, with instructions waiting for each other in between: 16 requests x 4 heads x
 // 131072 tokens, 1.34 GB, 280 us, 0.71 of the copy rate; 64 channels 206 us for half of
-// that (0.48); 16 heads 255 us for half (0.39).  32 requests x 4096 selected tokens: 29.0
+// that (0.48); 16 heads 253 us for half (0.39).  32 requests x 4096 selected tokens: 29.0
 // us, of which the chain of lookups before the stream and the join behind it are 7 (with
 // the query asked for behind the first pages, and a slot's part found by divisions, 30.0); 12
 // uneven requests of 16 heads, 64 channels: 32.6.  (Heads as rows for up to 8 heads, with
@@ -62,7 +62,7 @@ __host__ __device__ constexpr int stages_of(int head_dim) { return head_dim == 1
 constexpr float kMargin = 2.0f;
 constexpr int kUnit4 = 13;
 // Teams of a CTA (one CTA to an SM), as many as the registers allow without spilling much:
-// 16 heads of 64 channels, 16 x 4 heads x 65536 tokens, 139 us with 12 warps, 166 with 8;
+// 16 heads of 64 channels, 16 x 4 heads x 65536 tokens, 139 us (135 by now) with 12 warps, 166 with 8;
 // of 128 channels 258 with 8 warps, 279 with 12.
 __host__ __device__ constexpr int teams_of(int head_dim, int nt) { return head_dim == 64 || nt == 1 ? 3 : 2; }
 
@@ -108,7 +108,7 @@ __device__ __forceinline__ void scale_pairs(const uint8_t* record, float2 (&sc)[
 // Two f16 terms of two numbers.
 __device__ __forceinline__ void two_terms(float2 y, uint32_t& hi, uint32_t& lo) {
   hi = pack_half2(y.x, y.y);
-  const float2 rest = fma2(unpack_half2(hi), both(-1.0f), y);
+  const float2 rest = less_f16(y, hi);
   lo = pack_half2(rest.x, rest.y);
 }
 // Codes i (of the four in each half) of two tokens' 16 bits, centred, times 2^-24 (odd i: 2^-20).
@@ -264,7 +264,8 @@ struct TokensInRows {
         const uint32_t up = transpose8x8(__byte_perm(a, b, 0x7632)), down = transpose8x8(__byte_perm(a, b, 0x5410));
         p[e] = make_float2(__uint_as_float(__byte_perm(down, up, 0x5410)), __uint_as_float(__byte_perm(down, up, 0x7632)));
         hi[e] = pack_bf16(p[e].x, p[e].y);
-        lo[e] = pack_bf16(p[e].x - lower(hi[e]), p[e].y - upper(hi[e]));
+        const float2 rest = less_bf16(p[e], hi[e]);
+        lo[e] = pack_bf16(rest.x, rest.y);
         scale_pairs(st + At::kRecV + 32 * c4 + 16 * (16 * j + 8 * e), sc[e]);
       }
       mma_bf16(oz[j], zr[0], zr[1], zr[2], zr[3], hi[0], hi[1]);
@@ -473,7 +474,8 @@ struct HeadsInRows {
           l[nt] = add2(l[nt], p[nt][i]);
           p[nt][i] = mul2(p[nt][i], both(unit));
           hi[nt][i] = pack_bf16(p[nt][i].x, p[nt][i].y);
-          lo[nt][i] = pack_bf16(p[nt][i].x - lower(hi[nt][i]), p[nt][i].y - upper(hi[nt][i]));
+          const float2 rest = less_bf16(p[nt][i], hi[nt][i]);
+          lo[nt][i] = pack_bf16(rest.x, rest.y);
         }
         scale_pairs(st + At::kRecV + 32 * c4 + 16 * (16 * j + 8 * i), sc[i]);
       }
