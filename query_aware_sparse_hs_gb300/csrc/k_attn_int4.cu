@@ -30,10 +30,10 @@
 // What bounds it: the matrix, integer and fp32 pipes in turn, none of them busy half of
 // the time, with instructions waiting for each other in between: 16 requests x 4 heads x
 // 131072 tokens, 1.34 GB, 280 us, 0.71 of the copy rate; 64 channels 206 us for half of
-// that (0.48); 16 heads 253 us for half (0.39).  32 requests x 4096 selected tokens: 29.0
+// that (0.48); 16 heads 254 us for half (0.39).  32 requests x 4096 selected tokens: 29.0
 // us, of which the chain of lookups before the stream and the join behind it are 7 (with
 // the query asked for behind the first pages, and a slot's part found by divisions, 30.0); 12
-// uneven requests of 16 heads, 64 channels: 32.6.  (Heads as rows for up to 8 heads, with
+// uneven requests of 16 heads, 64 channels: 32.0.  (Heads as rows for up to 8 heads, with
 // half of the rows empty or taken by P's second term and O in twice the registers: 318.)
 //
 // Precision: q is exact (bf16, times a power of two, which takes entries up to 2^90), S
@@ -105,10 +105,11 @@ __device__ __forceinline__ void scale_pairs(const uint8_t* record, float2 (&sc)[
   sc[2] = make_float2(lower(r0.y), lower(r1.y));
   sc[3] = make_float2(upper(r0.y), upper(r1.y));
 }
-// Two f16 terms of two numbers.
+// Two f16 terms of two numbers.  MIXED: the first leaves them without being widened.
+template <bool MIXED>
 __device__ __forceinline__ void two_terms(float2 y, uint32_t& hi, uint32_t& lo) {
   hi = pack_half2(y.x, y.y);
-  const float2 rest = less_f16(y, hi);
+  const float2 rest = MIXED ? less_f16(y, hi) : fma2(unpack_half2(hi), both(-1.0f), y);
   lo = pack_half2(rest.x, rest.y);
 }
 // Codes i (of the four in each half) of two tokens' 16 bits, centred, times 2^-24 (odd i: 2^-20).
@@ -264,8 +265,7 @@ struct TokensInRows {
         const uint32_t up = transpose8x8(__byte_perm(a, b, 0x7632)), down = transpose8x8(__byte_perm(a, b, 0x5410));
         p[e] = make_float2(__uint_as_float(__byte_perm(down, up, 0x5410)), __uint_as_float(__byte_perm(down, up, 0x7632)));
         hi[e] = pack_bf16(p[e].x, p[e].y);
-        const float2 rest = less_bf16(p[e], hi[e]);
-        lo[e] = pack_bf16(rest.x, rest.y);
+        lo[e] = pack_bf16(p[e].x - lower(hi[e]), p[e].y - upper(hi[e]));
         scale_pairs(st + At::kRecV + 32 * c4 + 16 * (16 * j + 8 * e), sc[e]);
       }
       mma_bf16(oz[j], zr[0], zr[1], zr[2], zr[3], hi[0], hi[1]);
@@ -278,7 +278,7 @@ struct TokensInRows {
         for (int h = 0; h < 2; ++h) {
           const int k = k2 + h;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) two_terms(mul2(p[e], sc[e][k]), hi[e], lo[e]);
+          for (int e = 0; e < 2; ++e) two_terms<false>(mul2(p[e], sc[e][k]), hi[e], lo[e]);
           const uint32_t w0 = w[2 * h], w1 = w[2 * h + 1];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -491,7 +491,7 @@ struct HeadsInRows {
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) two_terms(mul2(p[nt][i], sc[i][k]), hi[nt][i], lo[nt][i]);
+            for (int i = 0; i < 2; ++i) two_terms<true>(mul2(p[nt][i], sc[i][k]), hi[nt][i], lo[nt][i]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t b0 = centred_code(w[2 * h], i), b1 = centred_code(w[2 * h + 1], i);
