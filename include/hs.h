@@ -39,11 +39,11 @@
  *   N_b = ceil(seq_lens[b] / B) blocks of request b.
  *   k_pages, v_pages  [num_pages][B][D]   f32 | bf16 | e4m3 (one byte); 4-bit:
  *                     [num_pages][B][D/2] bytes, channel 2i in the low half
- *   k_scales,v_scales [num_pages][B][D/32] f32 (e4m3 with grouped scales),
- *                     [num_pages] f32 (e4m3 with a scale per page: positive,
- *                     finite numbers), [num_pages][B][2][D/32] bf16 (4-bit: a
- *                     row's scales, then its centres; 16-byte aligned, passed
- *                     as float pointers), else NULL
+ *   k_scales,v_scales [num_pages][B][D/32] f32 (e4m3 with grouped scales, 4-byte
+ *                     aligned), [num_pages] f32 (e4m3 with a scale per page:
+ *                     positive, finite numbers), [num_pages][B][2][D/32] bf16
+ *                     (4-bit: a row's scales, then its centres; 16-byte
+ *                     aligned, passed as float pointers), else NULL
  *   page_table        [batch][Hkv][max_blocks] int32: physical page of block j
  *                     of (b, kvh); only entries j < N_b are read.
  *   seq_lens          [batch] int32 tokens of each request, including the

@@ -563,3 +563,40 @@ def test_decode_accumulate_evict_and_decode_again():
     weights = after
     for _ in range(4):
         step(e)
+
+
+# ---- scales that start where an element may ---------------------------------------------------------------------------------
+
+
+def off_by_words(t, words=1):
+    """The same tensor, its first element `words` elements behind a 16-byte boundary."""
+    flat = torch.zeros(t.numel() + words, dtype=t.dtype, device=t.device)
+    got = flat[words:].view(t.shape)
+    got.copy_(t)
+    assert got.data_ptr() % 16 == words * t.element_size()
+    return got
+
+
+@pytest.mark.parametrize("words", [1, 2, 3])
+@pytest.mark.parametrize("d", [64, 128])
+def test_weights_of_grouped_scales_at_any_element(d, words):
+    """A row's scales are copied whole where they lie at multiples of their size, else one by one: the same results."""
+    from query_aware_sparse_hs_gb300 import hs
+    c = Cache("fp8", [900, 31, 0, 2000], 2, d, 16, seed=4)
+    q = queries(c, 8)
+    sel, cnt = selection(c, 40, shuffle=True)
+    lse = lse_of(c, q, 8, sel, cnt, d ** -0.5)
+    start = torch.rand((4, 2, c.mb * 16), generator=torch.Generator().manual_seed(3)).cuda()
+
+    def run():
+        got = start.clone()
+        hs.hs_accumulate_attn_weights(c.shape(8), c.kv, q, lse, torch.from_numpy(sel).cuda(), torch.from_numpy(cnt).cuda(),
+                                      sel.shape[2], d ** -0.5, got)
+        assert hs.hs_get_device_error() == (hs.HS_OK, 0)
+        return got
+
+    want = run()
+    check_weights(c, q, 8, lse, sel, cnt, d ** -0.5, start, want)
+    c.sc["k"] = off_by_words(c.sc["k"], words)
+    c.up()
+    assert torch.equal(run(), want)
