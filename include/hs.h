@@ -164,8 +164,9 @@ typedef struct hs_select_params {
  * 0 = chosen by the library from the SMs the call may use.  algo: 0 =
  * automatic, 1 = CUDA-core kernel (every dtype), 2 = tensor-core kernel: tcgen05
  * for bf16 and e4m3 with grouped scales (head_dim 128 and the block sizes above;
- * at most 8 query heads per kv head for e4m3), warp-level products for e4m3 with a
- * scale per page and for 4-bit caches; HS_ERR_UNSUPPORTED where there is none.  The tensor-core kernel
+ * at most 8 query heads per kv head and scales that are 16-byte aligned for e4m3),
+ * warp-level products for e4m3 with a scale per page and for 4-bit caches;
+ * HS_ERR_UNSUPPORTED where there is none.  The tensor-core kernel
  * of e4m3 with grouped scales forms each V value, code times scale, in f16 (as it
  * does the products with P), so it needs |code * scale| <= 65504 (a V scale up to
  * 146 for codes up to 448); beyond that its output is not finite.  The CUDA-core

@@ -2170,6 +2170,8 @@ bool attn_tc_supported(const KvView& kv) {
     if (kv.group > 16) return false;
   } else if (kv.kv_dtype == HS_KV_FP8E4M3_G32) {
     if (kv.group > 8 || !kv.k_scales || !kv.v_scales) return false;
+    // a page's scales are copied by cp.async.bulk, which needs 16-byte addresses
+    if ((reinterpret_cast<uintptr_t>(kv.k_scales) | reinterpret_cast<uintptr_t>(kv.v_scales)) % 16 != 0) return false;
   } else {
     return false;
   }

@@ -481,3 +481,35 @@ def test_fp8_summaries_every_code_small_and_large_scales():
             lo, hi = O.stored_summaries(*O.block_summaries(K, B), "fp8")
             assert np.array_equal(smin[b, kvh, :nb], lo.astype(np.float32)), (b, kvh)
             assert np.array_equal(smax[b, kvh, :nb], hi.astype(np.float32)), (b, kvh)
+
+
+@pytest.mark.parametrize("which", ["k", "v", "kv"])
+def test_grouped_scales_at_any_element(which):
+    """The tensor-core kernel copies a token's scales as 16 bytes: where they do not start at a multiple of that, the library's
+    choice is the CUDA-core kernel, and the tensor-core one is refused."""
+    from _parity import Case
+    from query_aware_sparse_hs_gb300 import hs
+    w = CASES["fp8_tail"]
+    c = Case(w, make_inputs(w))
+    dec = c.decoder(out_is_fp32=True, algo="simt")
+    dec.build_summaries(c.kv)
+    dec.select_attend(c.kv, c.q)
+    _err_clear()
+    moved = {}
+    for i, t in (("k", c.k_scales), ("v", c.v_scales)):
+        moved[i] = t
+        if i in which:
+            moved[i] = torch.zeros(t.numel() + 1, device="cuda")[1:].view(t.shape)
+            moved[i].copy_(t)
+            assert moved[i].data_ptr() % 16 == 4
+    kv = hs.paged_kv(c.k_pages, c.v_pages, c.page_table, c.seq_lens, moved["k"], moved["v"])
+    auto = c.decoder(out_is_fp32=True)
+    auto.build_summaries(kv)
+    auto.select_attend(kv, c.q)
+    _err_clear()
+    assert torch.equal(auto.smin, dec.smin) and torch.equal(auto.smax, dec.smax) and torch.equal(auto.sel, dec.sel)
+    assert torch.equal(auto.out, dec.out) and torch.equal(auto.lse, dec.lse)
+    only = c.decoder(out_is_fp32=True, algo="tcgen05")
+    with pytest.raises(hs.HSError) as e:
+        only.attend(kv, c.q, selection=auto)
+    assert e.value.status == hs.HS_ERR_UNSUPPORTED
