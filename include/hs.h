@@ -679,8 +679,8 @@ typedef struct hs_evict_params {
  * by, so new tokens go on with theirs (hs_append_params.positions).  A request longer
  * than max_blocks * B sets HS_EBIT_BLOCK_RANGE and counts as that long; a page id
  * outside its pool sets HS_EBIT_PAGE_RANGE and that token's row is not written.
- * Not for HS_KV_FP8E4M3_BLOCK (rows of one page share their scale):
- * HS_ERR_UNSUPPORTED. */
+ * Not for HS_KV_FP8E4M3_BLOCK (rows of one page share their scale), nor where
+ * kv->max_blocks * B or budget is 2^31 - 2^14 or more: HS_ERR_UNSUPPORTED. */
 HS_API hs_status hs_evict_tokens(const hs_attn_shape* shape, const hs_paged_kv* kv, const hs_paged_kv* dst,
                                  const hs_evict_params* params, const float* weights, float* dst_weights,
                                  int32_t* kept, hs_stream_t stream);

@@ -878,6 +878,9 @@ hs_status hs_evict_tokens(const hs_attn_shape* shape, const hs_paged_kv* kv, con
     return HS_ERR_INVALID_ARG;
   if (params->budget > static_cast<int64_t>(dst->max_blocks) * shape->block_size) return HS_ERR_INVALID_ARG;
   if (shape->kv_dtype == HS_KV_FP8E4M3_BLOCK) return HS_ERR_UNSUPPORTED;
+  // (the kernels count places in 32 bits, a turn of all threads past the last)
+  constexpr int64_t kMost = (int64_t(1) << 31) - (1 << 14);
+  if (static_cast<int64_t>(kv->max_blocks) * shape->block_size >= kMost || params->budget >= kMost) return HS_ERR_UNSUPPORTED;
   const EvictArgs a{weights, dst_weights, kept, params->budget, params->sink_tokens, params->recent_tokens};
   const KvView v = make_view(shape, kv), to = make_view(shape, dst);
   if (evict_ctas(v, params->budget) > INT32_MAX) return HS_ERR_UNSUPPORTED;

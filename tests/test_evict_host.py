@@ -133,3 +133,21 @@ def test_the_driver_refuses_a_cache_of_another_length(hs, monkeypatch):
     dec.max_blocks = 9
     with pytest.raises(ValueError):
         dec.evict(kv(hs), kv(hs), hs.evict_params(10), None, None, None)
+
+
+def test_eviction_of_requests_whose_places_pass_31_bits(hs):
+    """Places are counted in 32 bits, some thousands past the last one: a table of 2^31 - 2^14 places or more is refused, and so
+    is such a budget."""
+    lib = hs.library()
+    most = 2 ** 31 - 2 ** 14
+
+    def call(places, budget, room, block):
+        shape = hs.attn_shape(8, 1, 64, block, "int4")
+        c, d = kv(hs, batch=1, mb=places // block), kv(hs, batch=1, mb=room // block)
+        return lib.hs_evict_tokens(ref(shape), ref(c), ref(d), ref(hs.evict_params(budget)), P, None, P, None)
+
+    for block in (1, 64, 256):
+        assert call(most, 4096, 4096, block) == hs.HS_ERR_UNSUPPORTED
+        assert call(2 ** 31 - block, 4096, 4096, block) == hs.HS_ERR_UNSUPPORTED
+        assert call(65536, most, 2 ** 31 - block, block) == hs.HS_ERR_UNSUPPORTED
+        assert call(65536, 2 ** 31 - 256, 2 ** 31 - block, block) == hs.HS_ERR_UNSUPPORTED
