@@ -676,7 +676,9 @@ typedef struct hs_evict_params {
  *                -1 behind them
  * Rows, weights and table entries of dst behind the new length stay as they were.  The
  * summaries of dst are hs_build_block_summaries'; K keeps the positions it was rotated
- * by, so new tokens go on with theirs (hs_append_params.positions).  A request longer
+ * by, so new tokens go on with theirs (hs_append_params.positions).  A selection over kv
+ * is none over dst, and a smoothed score (hs_select_params.score_history) of a request
+ * that was cut is that of other tokens: the caller sets it to NaN.  A request longer
  * than max_blocks * B sets HS_EBIT_BLOCK_RANGE and counts as that long; a page id
  * outside its pool sets HS_EBIT_PAGE_RANGE and that token's row is not written.
  * Not for HS_KV_FP8E4M3_BLOCK (rows of one page share their scale), nor where

@@ -6,6 +6,7 @@ a step itself allocates nothing, so it can be captured in a CUDA graph.
 
 from __future__ import annotations
 
+import contextlib
 import math
 
 import torch
@@ -151,11 +152,25 @@ class SparseDecode:
     def evict(self, kv: hs.PagedKV, dst: hs.PagedKV, params: hs.EvictParams, weights: torch.Tensor,
               dst_weights: torch.Tensor | None, kept: torch.Tensor, stream=None):
         """Gathers the heaviest tokens of every (request, kv head) into the pages of ``dst`` and builds their summaries,
-        so that the next step goes on with ``dst`` (its seq_lens is written)."""
+        so that the next step goes on with ``dst`` (its seq_lens is written).  The smoothed scores of requests that fill
+        the budget are forgotten, as their blocks hold other tokens than before.  (A selection made before, which a
+        step may reuse, is one of ``kv``'s blocks.  With early_summaries some other kernel comes before the next step.)"""
         if dst.max_blocks != self.max_blocks:
             raise ValueError("dst must have this decoder's max_blocks")
         hs.hs_evict_tokens(self.shape, kv, dst, params, weights, dst_weights, kept, stream)
         self.build_summaries(dst, 0, stream)
+        if self.score_history is not None:
+            with self._on(stream):
+                full = kept.view(kv.batch, self.shape.num_kv_heads, -1)[:, :, -1:] >= 0
+                self.score_history[:kv.batch].masked_fill_(full, float("nan"))
+
+    def _on(self, stream):
+        """torch's work on ``stream`` (as the calls take it) meanwhile."""
+        if stream is None:
+            return contextlib.nullcontext()
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.sel.device)
+        return torch.cuda.stream(stream)
 
     def swap_in(self, hb: hs.HotBuffer, step: int, stats=None, stream=None):
         hs.hs_swapin_misses(self.shape, hb, self.sel, self.sel_count, self.capacity, step, stats, stream)

@@ -151,3 +151,32 @@ def test_eviction_of_requests_whose_places_pass_31_bits(hs):
         assert call(2 ** 31 - block, 4096, 4096, block) == hs.HS_ERR_UNSUPPORTED
         assert call(65536, most, 2 ** 31 - block, block) == hs.HS_ERR_UNSUPPORTED
         assert call(65536, 2 ** 31 - 256, 2 ** 31 - block, block) == hs.HS_ERR_UNSUPPORTED
+
+
+def driver(monkeypatch, hs, **more):
+    """A decoder without device buffers, the library's calls noted and not made."""
+    from query_aware_sparse_hs_gb300 import decode
+    calls = []
+    monkeypatch.setattr(decode.hs, "hs_evict_tokens", lambda *a: calls.append("evict"))
+    monkeypatch.setattr(decode.hs, "hs_build_block_summaries", lambda *a: calls.append("summaries"))
+    dec = decode.SparseDecode.__new__(decode.SparseDecode)
+    dec.shape, dec.batch, dec.max_blocks, dec.smin, dec.smax = hs.attn_shape(8, 2, 128, 16, "int4"), 3, 4, None, None
+    for name, value in more.items():
+        setattr(dec, name, value)
+    return dec, calls
+
+
+def test_the_driver_forgets_the_scores_of_requests_that_were_cut(hs, monkeypatch):
+    """Blocks of a cut request hold other tokens: their smoothed scores are not those of the new ones.  A request shorter than
+    the budget keeps its blocks and their scores."""
+    history = torch.arange(24.0).view(3, 2, 4) + 1
+    before = history.clone()
+    dec, calls = driver(monkeypatch, hs, score_history=history)
+    kept = torch.tensor([[0, 1, 2, 3, 4], [0, 1, 2, -1, -1], [0, 7, 8, 30, 31]], dtype=torch.int32)[:, None, :].repeat(1, 2, 1)
+    c = kv(hs, batch=3, mb=4)
+    dec.evict(c, c, hs.evict_params(5, 1, 1), None, None, kept)
+    assert calls == ["evict", "summaries"]
+    assert dec.score_history is history and history[0].isnan().all() and history[2].isnan().all()
+    assert torch.equal(history[1], before[1])
+    dec.score_history = None  # no smoothing
+    dec.evict(c, c, hs.evict_params(5, 1, 1), None, None, kept)

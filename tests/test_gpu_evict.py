@@ -600,3 +600,43 @@ def test_weights_of_grouped_scales_at_any_element(d, words):
     c.sc["k"] = off_by_words(c.sc["k"], words)
     c.up()
     assert torch.equal(run(), want)
+
+
+@pytest.mark.parametrize("kind,block", [("bf16", 16), ("int4", 64)])
+@pytest.mark.parametrize("on", ["current", "stream", "handle"])
+def test_selection_after_an_eviction_with_smoothed_scores(kind, block, on):
+    """The first selection over the cut cache is a new decoder's for the requests that were cut, and goes on from its history
+    for the one that was not."""
+    from query_aware_sparse_hs_gb300 import hs
+    from query_aware_sparse_hs_gb300.decode import SparseDecode
+    c = Cache(kind, [3000, 250, 2000], 2, 128, block, seed=3)
+    e = destination(c, 1024, mb=c.mb)
+
+    def decoder():
+        return SparseDecode(num_q_heads=8, num_kv_heads=2, head_dim=128, block_size=block, kv_dtype=kind, batch=3, max_blocks=c.mb,
+                            sink_tokens=4, window_tokens=32, k_scored=6, score_smoothing=0.6, out_is_fp32=True)
+    dec, fresh, uncut = decoder(), decoder(), decoder()
+    for d in (dec, uncut):
+        d.build_summaries(c.kv)
+        for i in range(3):
+            d.step(c.kv, queries(c, 4, seed=20 + i))
+    w = weights_for(c)
+    kept = torch.zeros((3, 2, 1024), dtype=torch.int32, device="cuda")
+    side = None if on == "current" else torch.cuda.Stream()
+    stream = side.cuda_stream if on == "handle" else side
+    torch.cuda.synchronize()
+    dec.evict(c.kv, e["kv"], hs.evict_params(1024, 4, 32), w, None, kept, stream)
+    if side is not None:
+        torch.cuda.current_stream().wait_stream(side)
+    fresh.build_summaries(e["kv"])
+    q = queries(c, 4, seed=40)
+    dec.step(e["kv"], q)
+    fresh.step(e["kv"], q)
+    uncut.step(c.kv, q)
+    assert hs.hs_get_device_error() == (hs.HS_OK, 0)
+    for b, other in ((0, fresh), (1, uncut), (2, fresh)):
+        n = -(-min(c.lens[b], 1024) // block)
+        assert torch.equal(dec.sel[b], other.sel[b]), b
+        assert other is uncut or torch.equal(dec.out[b], other.out[b]), b  # (over the old cache the work may be cut elsewhere)
+        assert torch.equal(dec.score_history[b, :, :n], other.score_history[b, :, :n]), b
+    assert dec.score_history[[0, 2], :, -(-1024 // block):].isnan().all()
