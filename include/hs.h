@@ -674,7 +674,8 @@ typedef struct hs_evict_params {
  *                weights in their new places; not weights itself
  *   kept         [batch][Hkv][budget] int32: the kept tokens' old places, ascending,
  *                -1 behind them
- * Rows, weights and table entries of dst behind the new length stay as they were.  The
+ * Rows, weights and table entries of dst behind the new length stay as they were
+ * (weights that go on being accumulated are set to 0 there by the caller).  The
  * summaries of dst are hs_build_block_summaries'; K keeps the positions it was rotated
  * by, so new tokens go on with theirs (hs_append_params.positions).  A selection over kv
  * is none over dst, and a smoothed score (hs_select_params.score_history) of a request

@@ -153,16 +153,23 @@ class SparseDecode:
               dst_weights: torch.Tensor | None, kept: torch.Tensor, stream=None):
         """Gathers the heaviest tokens of every (request, kv head) into the pages of ``dst`` and builds their summaries,
         so that the next step goes on with ``dst`` (its seq_lens is written).  The smoothed scores of requests that fill
-        the budget are forgotten, as their blocks hold other tokens than before.  (A selection made before, which a
-        step may reuse, is one of ``kv``'s blocks.  With early_summaries some other kernel comes before the next step.)"""
+        the budget are forgotten, as their blocks hold other tokens than before, and ``dst_weights`` are 0 behind the
+        kept tokens', where those of new ones start.  (A selection made before, which a step may reuse, is one of
+        ``kv``'s blocks.  With early_summaries some other kernel comes before the next step.)"""
         if dst.max_blocks != self.max_blocks:
             raise ValueError("dst must have this decoder's max_blocks")
         hs.hs_evict_tokens(self.shape, kv, dst, params, weights, dst_weights, kept, stream)
         self.build_summaries(dst, 0, stream)
-        if self.score_history is not None:
-            with self._on(stream):
-                full = kept.view(kv.batch, self.shape.num_kv_heads, -1)[:, :, -1:] >= 0
-                self.score_history[:kv.batch].masked_fill_(full, float("nan"))
+        if self.score_history is None and dst_weights is None:
+            return
+        places = kept.view(kv.batch, self.shape.num_kv_heads, -1)
+        with self._on(stream):
+            if dst_weights is not None:
+                new = dst_weights.view(kv.batch, self.shape.num_kv_heads, -1)
+                new[:, :, :places.shape[2]].masked_fill_(places < 0, 0.0)
+                new[:, :, places.shape[2]:].zero_()
+            if self.score_history is not None:
+                self.score_history[:kv.batch].masked_fill_(places[:, :, -1:] >= 0, float("nan"))
 
     def _on(self, stream):
         """torch's work on ``stream`` (as the calls take it) meanwhile."""

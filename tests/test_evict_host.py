@@ -180,3 +180,17 @@ def test_the_driver_forgets_the_scores_of_requests_that_were_cut(hs, monkeypatch
     assert torch.equal(history[1], before[1])
     dec.score_history = None  # no smoothing
     dec.evict(c, c, hs.evict_params(5, 1, 1), None, None, kept)
+
+
+def test_the_driver_starts_the_weights_of_tokens_to_come_at_0(hs, monkeypatch):
+    """Two weight buffers that take turns: the one written now still holds what was there two cuts ago, behind the new length."""
+    dec, _ = driver(monkeypatch, hs, score_history=None)
+    kept = torch.tensor([[0, 1, 2, 3, 4], [0, 1, 2, -1, -1], [-1] * 5], dtype=torch.int32)[:, None, :].repeat(1, 2, 1)
+    w = torch.rand(3, 2, 64) + 1
+    want = w.clone()
+    for b, n in enumerate((5, 3, 0)):
+        want[b, :, n:] = 0.0
+    c = kv(hs, batch=3, mb=4)
+    dec.evict(c, c, hs.evict_params(5), None, w, kept)
+    assert torch.equal(w, want)
+    dec.evict(c, c, hs.evict_params(5), None, None, kept)  # none wanted

@@ -640,3 +640,36 @@ def test_selection_after_an_eviction_with_smoothed_scores(kind, block, on):
         assert other is uncut or torch.equal(dec.out[b], other.out[b]), b  # (over the old cache the work may be cut elsewhere)
         assert torch.equal(dec.score_history[b, :, :n], other.score_history[b, :, :n]), b
     assert dec.score_history[[0, 2], :, -(-1024 // block):].isnan().all()
+
+
+def test_weights_that_take_turns_between_two_buffers():
+    """Accumulate, cut, accumulate, cut back into the first buffer, whose old weights lie behind the new lengths: tokens that
+    come then start at 0."""
+    from query_aware_sparse_hs_gb300 import hs
+    from query_aware_sparse_hs_gb300.decode import SparseDecode
+    c = Cache("bf16", [900, 150, 40], 2, 64, 16, seed=3)
+    dec = SparseDecode(num_q_heads=8, num_kv_heads=2, head_dim=64, block_size=16, kv_dtype="bf16", batch=3, max_blocks=c.mb,
+                       sink_tokens=4, window_tokens=32, k_scored=90)
+    bufs = [torch.zeros((3, 2, c.mb * 16), device="cuda"), torch.full((3, 2, c.mb * 16), 5.0, device="cuda")]
+    now = c
+    for i, budget in enumerate((200, 100)):
+        dec.build_summaries(now.kv)
+        q = queries(now, 4, seed=i)
+        dec.step(now.kv, q)
+        dec.accumulate_weights(now.kv, q, bufs[0])
+        d = destination(now, budget, mb=c.mb)
+        kept = torch.zeros((3, 2, budget), dtype=torch.int32, device="cuda")
+        dec.evict(now.kv, d["kv"], hs.evict_params(budget, 4, 32), bufs[0], bufs[1], kept)
+        assert hs.hs_get_device_error() == (hs.HS_OK, 0)
+        lens = [min(n, budget) for n in now.lens]
+        for b, n in enumerate(lens):
+            for h in range(2):
+                t = kept_of(bufs[0][b, h].cpu().numpy(), now.lens[b], budget, 4, 32)
+                assert torch.equal(bufs[1][b, h, :n], bufs[0][b, h, torch.from_numpy(t).cuda()])
+                assert (bufs[1][b, h, n:] == 0).all(), (i, b, h)
+        nxt = Cache.__new__(Cache)
+        nxt.kind, nxt.hkv, nxt.d, nxt.block, nxt.mb, nxt.rng = "bf16", 2, 64, 16, c.mb, c.rng
+        nxt.x, nxt.sc, nxt.table, nxt.gt, nxt.gl, nxt.lens = d["x"], d["sc"], d["table"], d["gt"], d["lens"], lens
+        nxt.up()
+        now = nxt
+        bufs.reverse()
