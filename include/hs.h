@@ -224,9 +224,10 @@ typedef struct hs_select_params {
  * A 4-bit cache (HS_KV_INT4_G32) likewise has a tensor-core kernel of its own for every
  * block_size, with the same rules of cutting, workspace, max_ctas and limits.  It holds
  * queries exactly (entries up to 2^90), a token's probability times its V scale to 22
- * bits, or absolutely within 2^-37 of the largest V scale, or eighth of a centre, of the
- * selection (of 2^-112 at least), times its V centre to 16 bits; everything else in
- * fp32.  Scales and centres up to 2^126. */
+ * bits, or absolutely within 2^-36 of the largest V scale, or eighth of a centre, of the
+ * selection (of 2^-112 at least), and the probability that its V centre is multiplied by
+ * to 16 bits, or absolutely within 2^-146 of that largest (2^-46 where that is 2^100, 2^-20
+ * at 2^126); everything else in fp32.  Scales and centres up to 2^126. */
 #define HS_ATTN_EARLY_SUMMARIES 1u
 #define HS_ATTN_RANGES 2u
 #define HS_ATTN_NO_RANGES 4u

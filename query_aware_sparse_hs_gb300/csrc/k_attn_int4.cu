@@ -39,7 +39,10 @@
 // Precision: q is exact (bf16, times a power of two, which takes entries up to 2^90), S
 // and all sums fp32.  P times s, in units of 2^-13 of the reference (the largest power of
 // two met of s and z / 8), as two f16 terms: 22 bits, absolutely 2^-25 of the units; P
-// times z as two bf16 terms, 16 bits.
+// that z is multiplied by, in the same units, as two bf16 terms: 16 bits, absolutely 2^-134
+// of the units, bf16's smallest step halved.  (With a reference of 2^126 that is 2^-21 of
+// P: 12000 tokens on one CTA, most of 2^-8 and 2^-10, all of one centre, 2.3e-5 off; with
+// one of 2^20 3.3e-6.)
 #include <limits.h>
 
 #include <type_traits>

@@ -541,3 +541,33 @@ def test_a_decode_step_is_its_calls_in_order(hkv, group, d, block):
         check_attention(c, q, dec.sel.cpu().numpy(), dec.sel_count.cpu().numpy(), dec.out, dec.lse)
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("top", [126, 118, 110, 100, 20])
+@pytest.mark.parametrize("group,d", [(8, 128), (16, 64)])
+@pytest.mark.parametrize("max_ctas", [0, 1])
+def test_large_centres_under_many_small_probabilities(group, d, top, max_ctas):
+    """Every token has the same centres, and codes of 0: the output is the centres, whatever the probabilities are.  They enter
+    to 16 bits, or absolutely within 2^-146 of the largest V scale, 2^top, times as many as there are over their sum; the sums
+    are off by a rounding for each token.  (Every 500th token has 1, the others 2^-8.0 or 2^-9.6.)"""
+    T = 12000
+    c = Cache([T], 1, d, 64, seed=9)
+    c.scales["k"][:, :, 0], c.scales["k"][:, :, 1] = 1.6015625, 0.0
+    codes = c.rng.integers(9, 11, T + 32).astype(np.uint8)  # of channel 0: c + 8
+    codes[7::500] = 15
+    c.codes["k"][:] = c.codes["v"][:] = 0x88
+    c.codes["k"][c.table[0, 0, :c.nb[0]], :, 0] = 0x80 | codes.reshape(-1, 64)
+    z = bf16((1 + c.rng.random(d // 32)) * 2.0 ** (top - 1) * c.rng.choice([-1.0, 1.0], d // 32))
+    c.scales["v"][:, :, 0], c.scales["v"][:, :, 1] = 2.0 ** top, z
+    c.up()
+    q = torch.zeros((1, group, d), dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 1.0
+    sel, cnt = chosen(c, max(c.nb), None)
+    out, lse = attend(c, q, sel, cnt, scale=float(np.log(2)), max_ctas=max_ctas)
+    ok()
+    s = (codes[:T] - 8.0) * 1.6015625  # logits, in log2 units
+    total = np.exp2(s - s.max()).sum()
+    bound = 2.0 ** -16 + (T + 60) * U + 2.0 ** (top - 146) * T / total
+    off = np.abs(out[0].double().cpu().numpy() / np.repeat(z, 32) - 1.0).max()
+    assert off <= bound, (off, bound)
+    assert np.abs(lse.cpu().numpy() - (s.max() + np.log2(total)) * np.log(2)).max() < 1e-3
