@@ -673,3 +673,111 @@ def test_weights_that_take_turns_between_two_buffers():
         nxt.up()
         now = nxt
         bufs.reverse()
+
+
+def nobody_is_written(c, d, budget):
+    """Scales of rows that no request has still hold their fill (the rows themselves: check_evicted)."""
+    for k in "kv":
+        free = torch.ones(d["x"][k].shape[:2], dtype=torch.bool)
+        for b, L in enumerate(c.lens):
+            i = np.arange(min(L, budget))
+            for h in range(c.hkv):
+                free[d["table"][b, h, i // c.block], i % c.block] = False
+        assert free.any() and (d["sc"][k].float()[free.cuda()] == 9).all()
+
+
+@pytest.mark.parametrize("src,dst", [(0, 0), (1, 0), (0, 1), (2, 2), (3, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_grouped_scales_at_any_element_are_gathered(d, src, dst):
+    """Scales that start `src` and `dst` elements behind a boundary: by 16 or 8 bytes where all of them allow it, else by 4."""
+    from query_aware_sparse_hs_gb300 import hs
+    c = Cache("fp8", [900, 100, 3], 2, d, 16, seed=5)
+    w = weights_for(c)
+    e = destination(c, 130)
+    for k, other in (("k", 0), ("v", 1)):
+        c.sc[k] = off_by_words(c.sc[k], src)
+        e["sc"][k] = off_by_words(e["sc"][k], (dst + other) % 4 if dst == 1 else dst)
+    c.up()
+    e["kv"] = hs.paged_kv(e["x"]["k"], e["x"]["v"], e["gt"], e["lens"], e["sc"]["k"], e["sc"]["v"])
+    kept = torch.full((3, 2, 130), 77, dtype=torch.int32, device="cuda")
+    hs.hs_evict_tokens(c.shape(2), c.kv, e["kv"], hs.evict_params(130, 4, 32), w, e["w"], kept)
+    assert hs.hs_get_device_error() == (hs.HS_OK, 0)
+    check_evicted(c, e, w, 130, 4, 32, kept)
+    nobody_is_written(c, e, 130)
+
+
+@pytest.mark.parametrize("kind", ["int4", "fp8"])
+@pytest.mark.parametrize("d,block", [(64, 16), (128, 16), (128, 5)])
+def test_scales_and_centres_are_gathered_within_one_pool(kind, d, block):
+    """Source and destination pages of one pool: codes, scales and centres arrive bit for bit, everything else stays."""
+    from query_aware_sparse_hs_gb300 import hs
+    budget = 200
+    nb = [-(-min(L, budget) // block) for L in (700, 90, 300)]
+    c = Cache(kind, [700, 90, 300], 2, d, block, seed=5, spare=2 * sum(nb) + 7)
+    free = list(np.setdiff1d(np.arange(c.x["k"].shape[0]), c.table[c.table >= 0]))
+    table = np.full((3, 2, max(nb)), -1, np.int32)
+    for b in range(3):
+        for h in range(2):
+            table[b, h, :nb[b]] = [free.pop() for _ in range(nb[b])]
+    w = weights_for(c)
+    want = {k: (c.x[k].clone().view(torch.uint8), c.sc[k].clone().view(torch.uint8)) for k in "kv"}
+    lens = torch.zeros(3, dtype=torch.int32, device="cuda")
+    dst = hs.paged_kv(c.x["k"], c.x["v"], torch.from_numpy(table).cuda(), lens, c.sc["k"], c.sc["v"])
+    kept = torch.zeros((3, 2, budget), dtype=torch.int32, device="cuda")
+    hs.hs_evict_tokens(c.shape(2), c.kv, dst, hs.evict_params(budget, 4, 32), w, None, kept)
+    assert hs.hs_get_device_error() == (hs.HS_OK, 0) and lens.tolist() == [200, 90, 200]
+    for b, L in enumerate(c.lens):
+        for h in range(2):
+            t = kept_of(w[b, h].cpu().numpy(), L, budget, 4, 32)
+            i = np.arange(len(t))
+            src = torch.from_numpy(c.table[b, h, t // block].astype(np.int64)).cuda(), torch.from_numpy(t % block).cuda()
+            to = torch.from_numpy(table[b, h, i // block].astype(np.int64)).cuda(), torch.from_numpy(i % block).cuda()
+            for k in "kv":
+                for x in want[k]:
+                    x[to] = x[src]
+    for k in "kv":
+        assert torch.equal(c.x[k].view(torch.uint8), want[k][0]) and torch.equal(c.sc[k].view(torch.uint8), want[k][1])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_weights_and_eviction_of_pools_past_four_gib(kind):
+    """Rows, and for eviction the rows they go to, beyond 2^32 bytes of their pool: the same as from a small one."""
+    from query_aware_sparse_hs_gb300 import hs
+    c = Cache(kind, [700, 130], 2, 128, 64, seed=5)
+    q = queries(c, 8)
+    sel, cnt = selection(c, None)
+    lse = lse_of(c, q, 8, sel, cnt, 128 ** -0.5)
+    d = destination(c, 300)
+    w = weights_for(c)
+    total = (1 << 32) // (64 * 128 * c.x["k"].element_size()) + 200
+    far = np.random.default_rng(1).permutation(np.arange(total - 190, total))
+    pages, more = c.x["k"].shape[0], d["x"]["k"].shape[0]
+
+    def pool(x, at):
+        if x is None:
+            return None
+        big = torch.full((total,) + x.shape[1:], 9, dtype=x.dtype, device="cuda")
+        big[torch.from_numpy(at).cuda()] = x
+        return big
+
+    def moved(table, at):
+        return torch.from_numpy(np.where(table >= 0, at[np.maximum(table, 0)], -1).astype(np.int32)).cuda()
+
+    x, sc = {k: pool(c.x[k], far[:pages]) for k in "kv"}, {k: pool(c.sc[k], far[:pages]) for k in "kv"}
+    src = hs.paged_kv(x["k"], x["v"], moved(c.table, far[:pages]), c.gl, sc["k"], sc["v"])
+    at = far[pages:pages + more]
+    to = hs.paged_kv(x["k"], x["v"], moved(d["table"], at), d["lens"], sc["k"], sc["v"])
+    got = [torch.zeros((2, 2, c.mb * 64), device="cuda") for _ in range(2)]
+    for kv, g in zip((c.kv, src), got):
+        hs.hs_accumulate_attn_weights(c.shape(8), kv, q, lse, torch.from_numpy(sel).cuda(), torch.from_numpy(cnt).cuda(), sel.shape[2],
+                                      128 ** -0.5, g)
+    check_weights(c, q, 8, lse, sel, cnt, 128 ** -0.5, torch.zeros_like(got[0]), got[0])
+    assert torch.equal(got[0], got[1])
+    kept = torch.zeros((2, 2, 300), dtype=torch.int32, device="cuda")
+    hs.hs_evict_tokens(c.shape(8), src, to, hs.evict_params(300, 4, 32), w, d["w"], kept)
+    assert hs.hs_get_device_error() == (hs.HS_OK, 0)
+    for k in "kv":
+        d["x"][k] = x[k][torch.from_numpy(at).cuda()]
+        if sc[k] is not None:
+            d["sc"][k] = sc[k][torch.from_numpy(at).cuda()]
+    check_evicted(c, d, w, 300, 4, 32, kept)
