@@ -162,12 +162,13 @@ class SparseDecode:
         self.build_summaries(dst, 0, stream)
         if self.score_history is None and dst_weights is None:
             return
-        places = kept.view(kv.batch, self.shape.num_kv_heads, -1)
+        pairs = (kv.batch, self.shape.num_kv_heads)
+        places = kept.view(*pairs, params.budget)
         with self._on(stream):
             if dst_weights is not None:
-                new = dst_weights.view(kv.batch, self.shape.num_kv_heads, -1)
-                new[:, :, :places.shape[2]].masked_fill_(places < 0, 0.0)
-                new[:, :, places.shape[2]:].zero_()
+                new = dst_weights.view(*pairs, dst.max_blocks * self.shape.block_size)
+                new[:, :, :params.budget].masked_fill_(places < 0, 0.0)
+                new[:, :, params.budget:].zero_()
             if self.score_history is not None:
                 self.score_history[:kv.batch].masked_fill_(places[:, :, -1:] >= 0, float("nan"))
 

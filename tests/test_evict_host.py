@@ -194,3 +194,10 @@ def test_the_driver_starts_the_weights_of_tokens_to_come_at_0(hs, monkeypatch):
     dec.evict(c, c, hs.evict_params(5), None, w, kept)
     assert torch.equal(w, want)
     dec.evict(c, c, hs.evict_params(5), None, None, kept)  # none wanted
+
+
+def test_the_driver_with_a_batch_of_none(hs, monkeypatch):
+    dec, calls = driver(monkeypatch, hs, score_history=torch.ones(3, 2, 4))
+    c = kv(hs, batch=0, mb=4)
+    dec.evict(c, c, hs.evict_params(5), None, torch.ones(0, 2, 64), torch.zeros((0, 2, 5), dtype=torch.int32))
+    assert calls == ["evict", "summaries"] and (dec.score_history == 1).all()
