@@ -17,7 +17,7 @@
 //
 // What bounds it: memory for bf16 (16 requests x 4 heads x 16384 tokens, 277 MB: 46.3 us,
 // 0.88 of the copy rate); instructions beside it for the others (4-bit, 32 requests, 185
-// MB: 34.5 us, 0.79; e4m3 0.73 to 0.75); the CUDA cores for f32 (0.72).  A short call, 4
+// MB: 34.5 us, 0.79; e4m3 0.73 to 0.77); the CUDA cores for f32 (0.72).  A short call, 4
 // requests of up to 3000 tokens, takes 4.3 us: the launch, the counts and one chain of
 // lookups.
 #include <limits.h>
@@ -100,8 +100,7 @@ __device__ __forceinline__ void report_counts(const KvView& kv, const WeightsArg
     if (__ldg(a.sel_count + p) > a.capacity) set_error(err, HS_EBIT_CAPACITY);
 }
 
-// APART: a row's scales do not start at a multiple of their size, and are copied one by one.
-template <int D, int KIND, int NT, bool APART>
+template <int D, int KIND, int NT>
 __global__ __launch_bounds__(Row<D, KIND>::kWarps * 32, 1) void weights_kernel(KvView kv, WeightsArgs a, unsigned* err) {
   using R = Row<D, KIND>;
   constexpr int kWarps = R::kWarps, kBytes = R::kBytes, kRowsPer = 32 / R::kPieces;
@@ -148,7 +147,9 @@ __global__ __launch_bounds__(Row<D, KIND>::kWarps * 32, 1) void weights_kernel(K
         const uint32_t to = dst + (kRowsPer % 8 == 0 ? my_at + i * (kRowsPer * kBytes) : piece_at<kBytes>(r, lane % R::kPieces));
         copy16_if(to, piece + at, (live >> r) & 1u);
       }
-      if constexpr (APART) {
+      if constexpr (KIND == HS_KV_FP8E4M3_G32) {
+        // one by one, as they may start at any element, and no slower (16 requests x 4 heads x
+        // 16384 tokens 30.5 us, by 16 bytes 31.1; 32 x 8 x 32768 of 64 channels 108, by 8 bytes 111)
 #pragma unroll
         for (int i = 0; i < R::kRecord; i += 4)
           copy4(dst + kTile * kBytes + lane * 16 + i, records + static_cast<uint64_t>(row) * R::kRecord + i, ok);
@@ -447,28 +448,19 @@ __global__ __launch_bounds__(warps_f32(D) * 32, 2) void weights_f32_kernel(KvVie
   }
 }
 
-template <int D, int KIND, int NT, bool APART>
+template <int D, int KIND, int NT>
 cudaError_t launch_n(const KvView& kv, const WeightsArgs& a, int sms, unsigned* err, cudaStream_t st) {
   using R = Row<D, KIND>;
   constexpr size_t smem = static_cast<size_t>(R::kWarps) * kStages * R::kStage;
-  auto kern = weights_kernel<D, KIND, NT, APART>;
+  auto kern = weights_kernel<D, KIND, NT>;
   static std::atomic<uint64_t> allowed{0};
   if (cudaError_t e = allow_dynamic_smem_once(allowed, kern, smem); e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(sms), dim3(R::kWarps * 32), smem, st, kv, a, err);
 }
 
-template <int D, int KIND, bool APART = false>
+template <int D, int KIND>
 cudaError_t launch_k(const KvView& kv, const WeightsArgs& a, int sms, unsigned* err, cudaStream_t st) {
-  return kv.group <= 8 ? launch_n<D, KIND, 1, APART>(kv, a, sms, err, st) : launch_n<D, KIND, 2, APART>(kv, a, sms, err, st);
-}
-
-// Scales of grouped e4m3 may start at any number (the host asks the other kinds' to be aligned).  A kernel
-// of its own for those that do: asking in the kernel took 32.2 us for 30.8 (16 requests x 4 heads x 16384 tokens).
-template <int D>
-cudaError_t launch_fp8(const KvView& kv, const WeightsArgs& a, int sms, unsigned* err, cudaStream_t st) {
-  return reinterpret_cast<uintptr_t>(kv.k_scales) % Row<D, HS_KV_FP8E4M3_G32>::kRecord == 0
-             ? launch_k<D, HS_KV_FP8E4M3_G32>(kv, a, sms, err, st)
-             : launch_k<D, HS_KV_FP8E4M3_G32, true>(kv, a, sms, err, st);
+  return kv.group <= 8 ? launch_n<D, KIND, 1>(kv, a, sms, err, st) : launch_n<D, KIND, 2>(kv, a, sms, err, st);
 }
 
 template <int D>
@@ -476,7 +468,7 @@ cudaError_t launch_d(const KvView& kv, const WeightsArgs& a, int sms, unsigned* 
   switch (kv.kv_dtype) {
     case HS_KV_F32: return launch_pdl(weights_f32_kernel<D>, dim3(2 * sms), dim3(warps_f32(D) * 32), 0, st, kv, a, err);
     case HS_KV_BF16: return launch_k<D, HS_KV_BF16>(kv, a, sms, err, st);
-    case HS_KV_FP8E4M3_G32: return launch_fp8<D>(kv, a, sms, err, st);
+    case HS_KV_FP8E4M3_G32: return launch_k<D, HS_KV_FP8E4M3_G32>(kv, a, sms, err, st);
     case HS_KV_INT4_G32: return launch_k<D, HS_KV_INT4_G32>(kv, a, sms, err, st);
     default: return launch_k<D, HS_KV_FP8E4M3_BLOCK>(kv, a, sms, err, st);
   }

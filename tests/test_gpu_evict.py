@@ -580,7 +580,7 @@ def off_by_words(t, words=1):
 @pytest.mark.parametrize("words", [1, 2, 3])
 @pytest.mark.parametrize("d", [64, 128])
 def test_weights_of_grouped_scales_at_any_element(d, words):
-    """A row's scales are copied whole where they lie at multiples of their size, else one by one: the same results."""
+    """Wherever they start, the results are the same."""
     from query_aware_sparse_hs_gb300 import hs
     c = Cache("fp8", [900, 31, 0, 2000], 2, d, 16, seed=4)
     q = queries(c, 8)
