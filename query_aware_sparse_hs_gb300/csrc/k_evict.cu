@@ -33,9 +33,11 @@ __device__ __forceinline__ uint32_t weight_key(float w) {  // NaN last, -0 as 0
 // distributed shared memory; a bin that is taken whole ends the search.
 // Latency-bound, by two loads that follow one another, the barriers of the cluster (0.6 us
 // each) and what lies between them: with a budget of 64, so that little is gathered, both
-// launches take 9 us for 3000 tokens, 16 for 16 x 4 heads of up to 32768.  (A byte at a time with the digit found by one thread, a
-// CTA to a pair: 26 and 43 for this launch alone; the keys of the first digit's bin listed
-// for the other two: no change.)
+// launches take 9 us for 3000 tokens, 16 for 16 x 4 heads of up to 32768.  Keys past the
+// registers cost a load each in every pass, one behind the other: 78 us for 16 x 4 heads of
+// 131072.  (A byte at a time with the digit found by one thread, a CTA to a pair: 26 and 43
+// for this launch alone; the keys of the first digit's bin listed for the other two: no
+// change.)
 template <int CTAS>
 __global__ __launch_bounds__(kThreads) void evict_select_kernel(KvView kv, EvictArgs a, unsigned* err) {
   __shared__ uint32_t s_hist[3][kBins];  // one for each digit
