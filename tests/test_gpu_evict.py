@@ -781,3 +781,48 @@ def test_weights_and_eviction_of_pools_past_four_gib(kind):
         if sc[k] is not None:
             d["sc"][k] = sc[k][torch.from_numpy(at).cuda()]
     check_evicted(c, d, w, 300, 4, 32, kept)
+
+
+def test_the_driver_captured_and_on_the_default_stream_by_its_handle():
+    """A captured evict() clears the weights and the smoothed scores at every replay; handle 0 is the default stream."""
+    from query_aware_sparse_hs_gb300 import hs
+    from query_aware_sparse_hs_gb300.decode import SparseDecode
+    c = Cache("int4", [900, 150], 2, 64, 16, seed=3)
+    dec = SparseDecode(num_q_heads=8, num_kv_heads=2, head_dim=64, block_size=16, kv_dtype="int4", batch=2, max_blocks=c.mb,
+                       sink_tokens=4, window_tokens=32, k_scored=9, score_smoothing=0.5)
+    d = destination(c, 200, mb=c.mb)
+    kept = torch.zeros((2, 2, 200), dtype=torch.int32, device="cuda")
+    w = weights_for(c)
+
+    def evict(stream=None):
+        dec.evict(c.kv, d["kv"], hs.evict_params(200, 4, 32), w, d["w"], kept, stream)
+
+    def before(seed):
+        w.copy_(weights_for(c, seed))
+        d["w"].fill_(7.0)
+        dec.score_history.copy_(torch.rand(dec.score_history.shape))
+        return dec.score_history.clone()
+
+    def after(old):
+        torch.cuda.synchronize()
+        assert hs.hs_get_device_error() == (hs.HS_OK, 0)
+        assert dec.score_history[0].isnan().all() and torch.equal(dec.score_history[1], old[1])
+        for b, n in enumerate((200, 150)):
+            assert (d["w"][b, :, n:] == 0).all()
+            for h in range(2):
+                t = kept_of(w[b, h].cpu().numpy(), c.lens[b], 200, 4, 32)
+                assert torch.equal(d["w"][b, h, :n], w[b, h, torch.from_numpy(t).cuda()])
+
+    old = before(1)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        evict(0)
+    after(old)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        evict()
+    for seed in (2, 3):
+        old = before(seed)
+        graph.replay()
+        after(old)
