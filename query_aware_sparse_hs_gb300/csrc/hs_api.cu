@@ -271,7 +271,7 @@ hs_status prepare_attn(const hs_attn_shape* shape, const hs_paged_kv* kv, const 
   hs_status st = check_kv(shape, kv, true);
   if (st != HS_OK) return st;
   if (!q || !sel || !sel_count || !out || !params || capacity < 1) return HS_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(sel, 4) || !aligned(sel_count, 4))
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(sel, 4) || !aligned(sel_count, 4) || !aligned(lse_opt, 4))
     return HS_ERR_INVALID_ARG;
   if (params->algo < 0 || params->algo > 2 || params->blocks_per_split < 0 || params->max_ctas < 0)
     return HS_ERR_INVALID_ARG;

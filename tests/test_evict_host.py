@@ -201,3 +201,12 @@ def test_the_driver_with_a_batch_of_none(hs, monkeypatch):
     c = kv(hs, batch=0, mb=4)
     dec.evict(c, c, hs.evict_params(5), None, torch.ones(0, 2, 64), torch.zeros((0, 2, 5), dtype=torch.int32))
     assert calls == ["evict", "summaries"] and (dec.score_history == 1).all()
+
+
+def test_attention_whose_lse_is_no_float_address(hs):
+    lib, params = hs.library(), hs.attn_params(0.1)
+    for kind in ("int4", "bf16", "fp8", "fp8_block", "f32"):
+        shape = hs.attn_shape(16, 2, 128, 64, kind)
+        for off in (1, 2, 3):
+            assert lib.hs_sparse_paged_decode_attn(ref(shape), ref(kv(hs)), P, P, P, 4, ref(params), P, P + off, P, 1 << 30,
+                                                   None) == hs.HS_ERR_INVALID_ARG
